@@ -530,6 +530,135 @@ rdkv_status rdkv_allocate_at_levels(const rdkv_shape* seg, int32_t per_head, con
                                     float* sigma_chan, float* g_chan, uint8_t* bits_chan, void* plan, void* ws,
                                     size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- 4-bit cache, quantised as it is written
+ * No counterpart in the paper: a cache for the tokens that no prefill
+ * statistics exist for (new tokens, or whole prompts when the prefill's
+ * attention is not scored).  Every row is quantised on its own when it is
+ * written, by the quantiser of the TriZone pack: per KV head and group of 32
+ * channels of one token, K and V alike,
+ *   zero = fp16(min), scale = fp16(fl32(max - min) / 15),
+ *   code = clamp(rint((x - zero) / scale), 0, 15)   (IEEE fp32, ties to even; scale 0: code 0)
+ * and stands for x^ = fl32(zero + scale * code).  Values past +-65504
+ * (infinities too) are held as +-65504; a NaN takes no part in min and max
+ * and gets code 0.
+ *
+ * Layout.  Pages of RDKV_Q4_PAGE_TOKENS tokens of one sequence, each with all
+ * KV heads: pages [n_pages][h_kv][rdkv_q4_page_bytes(head_dim)], position p of
+ * sequence b is slot p % 64 of page page_table[b * page_stride + p / 64].  With
+ * NG = head_dim / 32 groups, the 80 * head_dim bytes of a (page, head) are
+ *   K codes   uint32 [64 tokens][4 q][NG]: word q of a token and group holds its channels 8q .. 8q+7,
+ *             element e at bit 16 (e mod 2) + 4 (e / 2);
+ *   K scales  fp16 [32 token pairs][NG][2 tokens];
+ *   K zeros   fp16 [64 tokens][NG];
+ *   V codes   uint32 [32 token pairs][8 g][NG]: channels 4g .. 4g+3 of the group at bits 0, 4, 8, 12 for
+ *             the even token and 16 above for the odd one;
+ *   V scales, V zeros  fp16 [32 token pairs][NG][2 tokens].
+ * `bounds` (may be NULL: no rdkv_q4_select) is fp16 [n_pages][h_kv][2][head_dim]:
+ * the smallest and the largest value fp16(x^) of each K channel over the
+ * page's tokens (all the tokens written since the page's slot 0 was).
+ *
+ * `lens` [batch] (int32, device) is the number of tokens each sequence holds,
+ * kept by the caller: raise it BEFORE rdkv_q4_write, which writes the last rows
+ * of each sequence, and call rdkv_q4_attn with the same values.  A slot without
+ * a sequence has length 0.  Nothing in these calls changes it, so captured
+ * graphs replay with whatever it then holds.
+ *
+ * Entries of `page_table` that no held token needs are not read, and may be
+ * anything.  Pages may be shared between sequences (a common prefix) as long as
+ * no call writes them.
+ * `status` is one device int32, zero before the first call: a call that finds
+ * RDKV_ERR_INVALID_ARG (a page outside [0, n_pages), row counts or positions
+ * that do not fit), RDKV_ERR_CAPACITY (a length past 64 * page_stride) or
+ * RDKV_ERR_TIMEOUT (a bounded wait) on the device leaves out what it concerns
+ * and raises *status to that code; rdkv_q4_status reads and clears it.
+ *
+ * Supported: head_dim 64 or 128, 1 <= h_q / h_kv <= 8, rows and queries in
+ * RDKV_F16, RDKV_F32 or RDKV_BF16 (the other calls of this library take no
+ * RDKV_BF16).  pages and bounds 16-byte aligned. */
+enum { RDKV_BF16 = 2 };
+#define RDKV_Q4_PAGE_TOKENS 64
+/* Most query tokens of a sequence in one rdkv_q4_attn or rdkv_q4_select. */
+#define RDKV_Q4_MAX_QUERIES 64
+typedef struct rdkv_q4_cache {
+  int32_t batch, h_kv, head_dim;
+  int32_t n_pages;            /* pages of the pool */
+  int32_t page_stride;        /* page-table entries of a sequence */
+  uint8_t* pages;
+  uint16_t* bounds;           /* or NULL */
+  const int32_t* page_table;  /* [batch][page_stride] */
+  const int32_t* lens;        /* [batch] */
+  int32_t* status;            /* [1] */
+} rdkv_q4_cache;
+
+/* Bytes of one (page, KV head): 80 * head_dim; 0 for an unsupported head_dim. */
+size_t rdkv_q4_page_bytes(int32_t head_dim);
+
+/* Writes new rows k, v [rows][h_kv][head_dim] in `dtype`, consecutive rows
+ * row_stride elements apart (>= h_kv * head_dim).  Sequence b's rows are
+ * [row_start[b], row_start[b + 1]) (int32 [batch + 1], device), at most
+ * max_rows of them, or, with row_start NULL, max_rows rows each, sequence after
+ * sequence.  They are its LAST tokens: row i of n goes to position
+ * lens[b] - n + i.  With row_start, a sequence with more than max_rows rows or
+ * more rows than lens[b] gets none written (RDKV_ERR_INVALID_ARG in *status);
+ * with row_start NULL a sequence of length 0 is an empty slot: its rows are
+ * skipped.  Rows past row_start[batch] are not read.  k, v 16-byte aligned, row_stride a
+ * multiple of 16 bytes. */
+rdkv_status rdkv_q4_write(const rdkv_q4_cache* cache, int32_t dtype, const void* k, const void* v, int64_t row_stride,
+                          const int32_t* row_start, int32_t max_rows, void* stream);
+
+/* Reads rows back, x^ rounded to `dtype` (fp16 saturates at +-65504): k, v as for rdkv_q4_write,
+ * row i of sequence b from position first[b] + i (int32 [batch], device; NULL:
+ * 0).  Rows at positions past lens[b] are left as they were, and so are rows
+ * of k, v that belong to no sequence. */
+rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, void* v, int64_t row_stride,
+                         const int32_t* row_start, const int32_t* first, int32_t max_rows, void* stream);
+
+/* Attention of the n_q (1 .. RDKV_Q4_MAX_QUERIES) newest tokens of every
+ * sequence over its cache: query token i of sequence b sees positions
+ * [0, lens[b] - n_q + i + 1), and for query head h (KV head h / G)
+ *   out = sum_t softmax_t(q . k^_t / sqrt(head_dim)) v^_t,
+ *   lse = ln sum_t exp(q . k^_t / sqrt(head_dim))
+ * (no position seen: out 0, lse -inf).  q [batch][n_q][h_q][head_dim] in
+ * `dtype`, consecutive tokens q_stride elements apart (16-byte aligned,
+ * q_stride a multiple of 16 bytes); out [batch][n_q][h_q][head_dim] dense in
+ * out_dtype, which is dtype or RDKV_F32 (fp32 outputs are computed to fp32
+ * accuracy, the others to their type's); lse [batch][n_q][h_q] fp32 or NULL.
+ * fp32 out and lse join other caches' attention through rdkv_merge_attn.
+ *
+ * sel NULL: every position.  Else sel [batch][n_q][h_kv][n_sel] (int32, device;
+ * rdkv_q4_select's output, or the caller's own choice): query token i's heads of
+ * KV head j see only the positions that also lie in one of those pages (indices
+ * into the sequence's pages, position / 64; entries < 0 or past its last page
+ * are left out; an index must not occur twice).
+ *
+ * ws: rdkv_q4_attn_workspace_bytes bytes, 16-byte aligned, zero-filled before its first use; every
+ * call leaves its counters at zero again, so calls of any shape that need no
+ * more bytes may follow one another on it.  Calls that may run at the same time
+ * (two streams, two captured graphs) need one each. */
+size_t rdkv_q4_attn_workspace_bytes(const rdkv_q4_cache* cache, int32_t h_q, int32_t n_q);
+rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
+                         int32_t n_q, const int32_t* sel, int32_t n_sel, void* out, int32_t out_dtype, float* lse,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* Chooses n_keep pages for every (sequence, query token, KV head): sel
+ * [batch][n_q][h_kv][n_keep] int32, ascending, -1 behind the last.  Of the P
+ * pages that hold a position the query token sees, all when P <= n_keep; else
+ * the first n_first, the last n_last and the best others by
+ *   score(page) = max over the G query heads of sum_c max(q_c lo_c, q_c hi_c),
+ * lo and hi the page's `bounds`: no logit of the page's keys (up to the bounds'
+ * fp16 rounding) is larger than score / sqrt(head_dim).  Equal scores: the lower
+ * page first; the order is that of sums carried to twice fp32's precision.
+ * q, q_stride, h_q, n_q as for rdkv_q4_attn; 0 <= n_first, 0 <= n_last,
+ * n_first + n_last <= n_keep, 1 <= n_keep; cache->bounds not NULL; ws as for
+ * rdkv_q4_attn, sized by rdkv_q4_select_workspace_bytes. */
+size_t rdkv_q4_select_workspace_bytes(const rdkv_q4_cache* cache, int32_t h_q, int32_t n_q);
+rdkv_status rdkv_q4_select(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
+                           int32_t n_q, int32_t n_keep, int32_t n_first, int32_t n_last, int32_t* sel, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Reads *status and clears it.  SYNCHRONISES `stream`. */
+rdkv_status rdkv_q4_status(const rdkv_q4_cache* cache, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,126 @@
+// Shared parts of the 4-bit paged cache (rdkv_q4_* in include/rdkv.h): the page layout, the rows' types
+// and the host checks.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace rdkv {
+namespace q4 {
+
+constexpr int kPage = RDKV_Q4_PAGE_TOKENS;
+constexpr int kGroup = 32;             // channels that share a scale and a zero
+constexpr float kHalfMax = 65504.0f;
+
+// Byte offsets inside one (page, KV head); the K half (codes, scales, zeros) comes first, so that each
+// half is one bulk copy.
+template <int D>
+struct Layout {
+  static constexpr int NG = D / kGroup;
+  static constexpr int kCodes = kPage * D / 2, kMeta = kPage * NG * 2;
+  static constexpr int kKCodes = 0, kKScales = kCodes, kKZeros = kCodes + kMeta;
+  static constexpr int kHalf = kCodes + 2 * kMeta;  // bytes of the K half and of the V half: 40 D
+  static constexpr int kVCodes = kHalf, kVScales = kHalf + kCodes, kVZeros = kHalf + kCodes + kMeta;
+  static constexpr int kBytes = 2 * kHalf;
+};
+
+// What a kernel reads of the cache.
+struct View {
+  int batch, h_kv, n_pages, page_stride;
+  uint8_t* pages;
+  __half* bounds;
+  const int32_t* page_table;
+  const int32_t* lens;
+  int32_t* status;
+};
+
+inline View view_of(const rdkv_q4_cache* c) {
+  return View{c->batch,  c->h_kv, c->n_pages, c->page_stride, c->pages, reinterpret_cast<__half*>(c->bounds), c->page_table, c->lens,
+              c->status};
+}
+
+__device__ __forceinline__ void raise(const View& v, int code) { atomicMax(v.status, code); }
+
+// Tokens that sequence b holds, cut to what its page table can hold.
+__device__ __forceinline__ int held_tokens(const View& v, int b) {
+  const int n = __ldg(v.lens + b);
+  return max(0, (int)min((int64_t)n, (int64_t)v.page_stride * kPage));
+}
+
+// ---------------------------------------------------------------- rows of the model's types
+template <typename T>
+struct Eight;  // eight consecutive channels
+template <>
+struct Eight<__half> {
+  static __device__ __forceinline__ void load(const __half* p, float (&x)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h[i]);
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ void store(__half* p, const float (&x)[8]) {
+    uint4 u;
+    __half2* h = reinterpret_cast<__half2*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[i] = __floats2half2_rn(fminf(fmaxf(x[2 * i], -kHalfMax), kHalfMax), fminf(fmaxf(x[2 * i + 1], -kHalfMax), kHalfMax));
+    *reinterpret_cast<uint4*>(p) = u;
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
+    uint4 u;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = u;
+  }
+};
+template <>
+struct Eight<float> {
+  static __device__ __forceinline__ void load(const float* p, float (&x)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+
+// One value in a type that is named at run time (outputs of the merges, where the rows are few).
+__device__ __forceinline__ void store_as(void* p, int64_t i, int dtype, float x) {
+  if (dtype == RDKV_F32) static_cast<float*>(p)[i] = x;
+  else if (dtype == RDKV_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
+  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+}
+__device__ __forceinline__ float load_q(const void* p, int64_t i, int dtype) {
+  if (dtype == RDKV_F32) return static_cast<const float*>(p)[i];
+  if (dtype == RDKV_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// ---------------------------------------------------------------- host checks
+inline int size_of(int32_t dtype) { return dtype == RDKV_F32 ? 4 : 2; }
+rdkv_status check_cache(const rdkv_q4_cache* c);
+rdkv_status check_rows(const rdkv_q4_cache* c, int32_t dtype, const void* k, const void* v, int64_t row_stride,
+                       int32_t max_rows);
+rdkv_status check_queries(const rdkv_q4_cache* c, int32_t h_q, int32_t n_q);
+rdkv_status check_q(const rdkv_q4_cache* c, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q, int32_t n_q);
+
+}  // namespace q4
+}  // namespace rdkv

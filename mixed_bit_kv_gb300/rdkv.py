@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "librdkv.so")
 
 RDKV_OK, RDKV_ERR_INVALID_ARG, RDKV_ERR_UNSUPPORTED, RDKV_ERR_CAPACITY = 0, 1, 2, 3
 RDKV_ERR_CUDA, RDKV_ERR_TIMEOUT, RDKV_ERR_WORKSPACE = 4, 5, 6
-RDKV_F16, RDKV_F32 = 0, 1
+RDKV_F16, RDKV_F32, RDKV_BF16 = 0, 1, 2  # RDKV_BF16: the 4-bit cache's calls only
 RDKV_ALLOC_POOLED, RDKV_ALLOC_PER_HEAD, RDKV_ALLOC_TOPK, RDKV_ALLOC_THRESHOLD = 0, 1, 2, 3
 
 EXPORTED = (
@@ -32,6 +32,8 @@ EXPORTED = (
     "rdkv_decode_multi_status", "rdkv_zone_bounds", "rdkv_decode_timeout_selftest", "rdkv_workspace_bytes",
     "rdkv_decode_ragged_workspace_bytes", "rdkv_decode_ragged", "rdkv_decode_ragged_status",
     "rdkv_allocate_pack_workspace_bytes", "rdkv_allocate_pack",
+    "rdkv_q4_page_bytes", "rdkv_q4_write", "rdkv_q4_read", "rdkv_q4_attn_workspace_bytes", "rdkv_q4_attn",
+    "rdkv_q4_select_workspace_bytes", "rdkv_q4_select", "rdkv_q4_status",
 )
 RDKV_CALL_SCORE, RDKV_CALL_ALLOCATE, RDKV_CALL_DECODE = 0, 1, 2
 
@@ -63,9 +65,16 @@ class CacheStruct(ctypes.Structure):
                 ("sizes", Sizes), ("zone_c_pages", ctypes.c_void_p), ("zone_c_page_stride", ctypes.c_int32),
                 ("zone_a_pages", ctypes.c_void_p), ("zone_b_pages", ctypes.c_void_p)]
 
+
+class Q4CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "h_kv", "head_dim", "n_pages", "page_stride")] + [
+        (n, ctypes.c_void_p) for n in ("pages", "bounds", "page_table", "lens", "status")]
+
 PAGE_ROWS = 16  # RDKV_ZONE_C_PAGE_ROWS
 A_PAGE_BYTES = 65536  # RDKV_ZONE_A_PAGE_BYTES
 B_PAGE_ROWS = 16  # RDKV_ZONE_B_PAGE_ROWS
+Q4_PAGE_TOKENS = 64  # RDKV_Q4_PAGE_TOKENS
+Q4_MAX_QUERIES = 64  # RDKV_Q4_MAX_QUERIES
 
 
 HEAD_PLAN_DTYPE = [("n_v", "<i4", 4), ("tiles", "<i4", 4), ("n_k", "<i4", 5), ("k_words", "<i4", 4),
@@ -132,6 +141,16 @@ def lib():
             "rdkv_allocate_pack_workspace_bytes": (ctypes.c_size_t, [sp, ctypes.c_int32]),
             "rdkv_allocate_pack": (ctypes.c_int, [cp, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float,
                                                   _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+            "rdkv_q4_page_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+            "rdkv_q4_write": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_int64, _P, ctypes.c_int32, _P]),
+            "rdkv_q4_read": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_int32, _P]),
+            "rdkv_q4_attn_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32]),
+            "rdkv_q4_attn": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P,
+                                            ctypes.c_int32, _P, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P]),
+            "rdkv_q4_select_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32]),
+            "rdkv_q4_select": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64] + [ctypes.c_int32] * 5
+                               + [_P, _P, ctypes.c_size_t, _P]),
+            "rdkv_q4_status": (ctypes.c_int, [_P, _P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -736,3 +755,236 @@ class Compressor:
         self.cache.sizes = sizes
         self.cache.c.sizes = sizes
         return self.cache
+
+
+# ---------------------------------------------------------------- 4-bit cache, quantised as it is written
+_Q4_DTYPES = {torch.float16: RDKV_F16, torch.float32: RDKV_F32, torch.bfloat16: RDKV_BF16}
+
+
+def _q4_require(ok, msg):
+    if not ok:
+        raise RDKVError(RDKV_ERR_INVALID_ARG, msg)
+
+
+class Q4Cache:
+    """A 4-bit cache of `batch` sequences (slots) of up to max_tokens tokens: its pages, page table,
+    lengths and the C struct that points at them.
+
+    The buffers are allocated unless given: pages uint8 [n_pages, h_kv, 80 * head_dim], bounds fp16
+    [n_pages, h_kv, 2, head_dim] (False: none, no rdkv_q4_select), page_table int32 [batch, stride] and
+    lens int32 [batch]; caches may share pages and bounds (a pool) under their own tables.  Without a
+    table every sequence gets its own run of pages.  lens is the caller's: raise it before
+    rdkv_q4_write, which writes the last rows of each sequence."""
+
+    def __init__(self, batch, h_kv, head_dim, max_tokens, device, pages=None, bounds=None, page_table=None, lens=None):
+        _q4_require(batch >= 1 and h_kv >= 1 and max_tokens >= 1, "batch, h_kv and max_tokens must be positive")
+        page_bytes = lib().rdkv_q4_page_bytes(head_dim)
+        if page_bytes == 0:
+            raise RDKVError(RDKV_ERR_UNSUPPORTED, f"head_dim {head_dim} not in (64, 128)")
+        stride = -(-max_tokens // Q4_PAGE_TOKENS)
+        self.batch, self.h_kv, self.head_dim = batch, h_kv, head_dim
+        if pages is None:
+            pages = torch.zeros(batch * stride, h_kv, page_bytes, dtype=torch.uint8, device=device)
+        self.device, n_pages = pages.device, pages.shape[0]
+        _q4_require(self.device.type == "cuda", "the cache lives on a GPU")
+        if bounds is None:
+            bounds = torch.zeros(n_pages, h_kv, 2, head_dim, dtype=torch.float16, device=self.device)
+        if page_table is None:
+            _q4_require(n_pages >= batch * stride, f"{n_pages} pages for {batch} sequences of {stride}: give a page_table")
+            page_table = torch.arange(batch * stride, dtype=torch.int32, device=self.device).view(batch, stride)
+        if lens is None:
+            lens = torch.zeros(batch, dtype=torch.int32, device=self.device)
+        self.pages, self.bounds, self.page_table, self.lens = pages, bounds if bounds is not False else None, page_table, lens
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        for name, t, dtype, shape in (("pages", pages, torch.uint8, (n_pages, h_kv, page_bytes)),
+                                      ("bounds", self.bounds, torch.float16, (n_pages, h_kv, 2, head_dim)),
+                                      ("page_table", page_table, torch.int32, (batch, page_table.shape[-1])),
+                                      ("lens", lens, torch.int32, (batch,))):
+            if t is not None:
+                _q4_require(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous() and t.device == self.device,
+                            f"{name} must be a dense {dtype} {list(shape)} on {self.device}")
+        _q4_require(page_table.shape[1] >= 1 and n_pages >= 1, "a cache needs pages")
+        self.c = Q4CacheStruct(batch, h_kv, head_dim, n_pages, page_table.shape[1], pages.data_ptr(),
+                               None if self.bounds is None else self.bounds.data_ptr(), page_table.data_ptr(),
+                               lens.data_ptr(), self.status.data_ptr())
+        self._ref = ctypes.addressof(self.c)
+        self._ws = {}
+
+    def workspace(self, kind, h_q, n_q):
+        """The zero-filled workspace of rdkv_q4_attn ("attn") or rdkv_q4_select ("select") calls on the current
+        stream.  While a graph is being captured: one of that call's own, cleared in the graph (two captured
+        graphs may run at once)."""
+        nb = self._ws.get((kind, h_q, n_q))
+        if nb is None:
+            fn = lib().rdkv_q4_attn_workspace_bytes if kind == "attn" else lib().rdkv_q4_select_workspace_bytes
+            nb = fn(self._ref, h_q, n_q)
+            if nb == 0:
+                raise RDKVError(RDKV_ERR_INVALID_ARG, lib().rdkv_last_error_string().decode())
+            self._ws[kind, h_q, n_q] = nb
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(nb, dtype=torch.uint8, device=self.device)
+        key = kind, torch.cuda.current_stream().cuda_stream
+        ws = self._ws.get(key)
+        if ws is None or ws.numel() < nb:
+            ws = self._ws[key] = torch.zeros(nb, dtype=torch.uint8, device=self.device)
+        return ws
+
+
+def _q4_on(cache, stream, call, *args):
+    """call(cache, *args, stream pointer) with `stream` (default: the device's current one) and the cache's
+    device current, so that what the call allocates belongs to that stream."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return call(cache, *args, stream.cuda_stream)
+    if cache.device.index == torch.cuda.current_device():
+        return call(cache, *args, torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(cache.device):
+        return call(cache, *args, torch.cuda.current_stream().cuda_stream)
+
+
+def _q4_index(cache, t, n, name):
+    _q4_require(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n and t.device == cache.device),
+                f"{name} must be a dense int32 tensor of {n} on {cache.device}")
+    return None if t is None else t.data_ptr()
+
+
+def _q4_rows(cache, k, v, row_start, max_rows):
+    """(dtype code, row stride, max_rows) of rows k, v [rows, h_kv, D] or [batch, n, h_kv, D]."""
+    _q4_require(k.shape == v.shape and k.dtype == v.dtype and k.dtype in _Q4_DTYPES and k.dim() in (3, 4)
+                and k.shape[-2:] == (cache.h_kv, cache.head_dim) and k.device == v.device == cache.device,
+                f"k and v must be rows [.., {cache.h_kv}, {cache.head_dim}] of one type on {cache.device}")
+    if k.dim() == 4:
+        _q4_require(row_start is None and k.shape[0] == cache.batch, "[batch, n, h_kv, D] rows take no row_start")
+        n = k.shape[1]
+        _q4_require(n <= 1 or k.shape[0] == 1 or (k.stride(0) == n * k.stride(1) and v.stride(0) == n * v.stride(1)),
+                    "the sequences' rows must follow one another")
+        _q4_require(max_rows is None or max_rows == n, f"max_rows {max_rows} for {n} rows a sequence")
+        stride = k.stride(1) if n > 1 else k.stride(0)
+        other = v.stride(1) if n > 1 else v.stride(0)
+        max_rows = n
+    else:
+        n, stride, other = k.shape[0], k.stride(0), v.stride(0)
+        if row_start is None:
+            max_rows = n // cache.batch if max_rows is None else max_rows
+            _q4_require(max_rows * cache.batch == n, f"{n} rows for {cache.batch} sequences: give row_start")
+        else:
+            max_rows = n if max_rows is None else max_rows
+    if k.numel() == 0:
+        return _Q4_DTYPES[k.dtype], cache.h_kv * cache.head_dim, 0
+    if k.shape[0] == 1 and (k.dim() == 3 or n == 1):  # one row in all: its stride says nothing
+        stride = other = cache.h_kv * cache.head_dim
+    _q4_require(stride == other and k.stride(-1) == v.stride(-1) == 1
+                and (cache.h_kv == 1 or k.stride(-2) == v.stride(-2) == cache.head_dim),
+                "k and v need dense heads and the same distance between rows")
+    return _Q4_DTYPES[k.dtype], stride, int(max_rows)
+
+
+def rdkv_q4_write(cache, k, v, row_start=None, max_rows=None, stream=None):
+    """Quantises rows k, v into the cache: [batch, n, h_kv, D], the last n tokens of every sequence, or
+    [rows, h_kv, D] with row_start int32 [batch + 1] (sequence b's rows, at most max_rows of them).
+    cache.lens must already count them."""
+    _q4_on(cache, stream, _q4_write, k, v, row_start, max_rows)
+
+
+def _q4_write(cache, k, v, row_start, max_rows, s):
+    start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
+    code, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
+    _check(lib().rdkv_q4_write(cache._ref, code, k.data_ptr(), v.data_ptr(), stride, start, n, s))
+
+
+def rdkv_q4_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype=torch.float16, out=None, stream=None):
+    """Rows back as (k, v): max_rows of every sequence from position first (int32 [batch], default 0), as
+    [batch, max_rows, h_kv, D], or with row_start (int32 [batch + 1]) as [n_rows, h_kv, D].  `out`: a pair
+    of tensors to fill instead of new ones.  Rows past a sequence's length are not written."""
+    return _q4_on(cache, stream, _q4_read, max_rows, row_start, first, n_rows, dtype, out)
+
+
+def _q4_read(cache, max_rows, row_start, first, n_rows, dtype, out, s):
+    start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
+    at = _q4_index(cache, first, cache.batch, "first")
+    if out is None:
+        _q4_require(dtype in _Q4_DTYPES, f"dtype {dtype}")
+        if row_start is None:
+            shape = (cache.batch, max_rows, cache.h_kv, cache.head_dim)
+        else:
+            _q4_require(n_rows is not None, "row_start needs n_rows, the rows of the outputs")
+            shape = (n_rows, cache.h_kv, cache.head_dim)
+        out = torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device)
+    k, v = out
+    code, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
+    _check(lib().rdkv_q4_read(cache._ref, code, k.data_ptr(), v.data_ptr(), stride, start, at, n, s))
+    return k, v
+
+
+def _q4_queries(cache, q):
+    """(dtype code, h_q, n_q, token stride) of queries [batch, n_q, h_q, D] or [batch, h_q, D]."""
+    _q4_require(q.dtype in _Q4_DTYPES and q.dim() in (3, 4) and q.shape[0] == cache.batch
+                and q.shape[-1] == cache.head_dim and q.device == cache.device and q.numel() > 0,
+                f"queries must be [{cache.batch}, n_q, h_q, {cache.head_dim}] on {cache.device}")
+    n_q, h_q = (q.shape[1] if q.dim() == 4 else 1), q.shape[-2]
+    if q.is_contiguous():
+        return _Q4_DTYPES[q.dtype], h_q, n_q, h_q * cache.head_dim
+    stride = q.stride(1) if n_q > 1 else q.stride(0) if cache.batch > 1 else h_q * cache.head_dim
+    _q4_require(q.stride(-1) == 1 and (h_q == 1 or q.stride(-2) == cache.head_dim)
+                and (cache.batch == 1 or q.stride(0) == n_q * stride), "queries need dense heads and evenly spaced tokens")
+    return _Q4_DTYPES[q.dtype], h_q, n_q, stride
+
+
+def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None, stream=None):
+    """Attention of the newest tokens' queries q [batch, n_q, h_q, D] (or [batch, h_q, D]) over the cache:
+    (out in q's shape and out_dtype, lse fp32 without D).  sel: pages int32 [batch, n_q, h_kv, n_sel] (or
+    without n_q) to attend instead of all.  out_dtype: q's type (default) or torch.float32."""
+    return _q4_on(cache, stream, _q4_attn, q, sel, out, lse, out_dtype, ws)
+
+
+def _q4_attn(cache, q, sel, out, lse, out_dtype, ws, s):
+    code, h_q, n_q, stride = _q4_queries(cache, q)
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    else:
+        _q4_require(out.shape == q.shape and out.is_contiguous() and out.device == cache.device
+                    and out_dtype in (None, out.dtype), "out must be dense and in q's shape")
+    _q4_require(out.dtype in (q.dtype, torch.float32), "out must be in q's type or fp32")
+    if lse is None:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    else:
+        _q4_require(lse.shape == q.shape[:-1] and lse.dtype == torch.float32 and lse.is_contiguous()
+                    and lse.device == cache.device, "lse must be dense fp32 in q's shape without its last size")
+    n_sel, sel_ptr = 0, None
+    if sel is not None:
+        n_sel = sel.shape[-1]
+        sel_ptr = _q4_index(cache, sel, cache.batch * n_q * cache.h_kv * n_sel, "sel")
+    if ws is None:
+        ws = cache.workspace("attn", h_q, n_q)
+    _check(lib().rdkv_q4_attn(cache._ref, code, q.data_ptr(), stride, h_q, n_q, sel_ptr, n_sel, out.data_ptr(),
+                              _Q4_DTYPES[out.dtype], lse.data_ptr(), ws.data_ptr(), ws.numel(), s))
+    return out, lse
+
+
+def rdkv_q4_select(cache, q, n_keep, n_first=1, n_last=1, out=None, ws=None, stream=None):
+    """Pages for rdkv_q4_attn's `sel`: int32 [batch, n_q, h_kv, n_keep] (without n_q for q [batch, h_q, D]),
+    ascending, -1 behind the last: the first n_first, the last n_last and the best others."""
+    return _q4_on(cache, stream, _q4_select, q, n_keep, n_first, n_last, out, ws)
+
+
+def _q4_select(cache, q, n_keep, n_first, n_last, out, ws, s):
+    code, h_q, n_q, stride = _q4_queries(cache, q)
+    _q4_require(cache.bounds is not None, "the cache keeps no bounds")
+    _q4_require(n_keep >= 1, f"n_keep {n_keep}")
+    shape = (*q.shape[:-2], cache.h_kv, n_keep)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int32, device=q.device)
+    else:
+        _q4_require(out.shape == shape and out.dtype == torch.int32 and out.is_contiguous()
+                    and out.device == cache.device, f"out must be a dense int32 {list(shape)}")
+    if ws is None:
+        ws = cache.workspace("select", h_q, n_q)
+    _check(lib().rdkv_q4_select(cache._ref, code, q.data_ptr(), stride, h_q, n_q, n_keep, n_first, n_last,
+                                out.data_ptr(), ws.data_ptr(), ws.numel(), s))
+    return out
+
+
+def rdkv_q4_status(cache, stream=None):
+    """What the calls on this cache reported on the device since the last read (RDKV_OK: nothing);
+    synchronises the stream."""
+    return _q4_on(cache, stream, lambda c, s: lib().rdkv_q4_status(c._ref, s))

@@ -870,3 +870,83 @@ def allocate_at_levels(g_tok, w_chan, k, lam_v, lam_k):
     g_chan = np.asarray(w_chan, np.float32) * sig_c.astype(np.float32)
     bits_chan = widths_at(breakpoints(g_chan), lam_k).astype(np.uint8).reshape(g_chan.shape)
     return dict(bits_tok=bits_tok, sigma_chan=sig_c.astype(np.float32), g_chan=g_chan, bits_chan=bits_chan)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit cache, quantised as it is written (no counterpart in the paper).  Every
+# row on its own, K and V alike, per KV head and group of 32 channels, by the
+# quantiser of the zones at 4 bits; pages of 64 tokens of one sequence; the
+# attention over it; and the selection of pages by a bound of their logits.
+# ---------------------------------------------------------------------------
+Q4_PAGE = 64
+F16_MAX = 65504.0
+
+
+def q4_quantize(x):
+    """Codes uint8 [..., D], scale and zero fp16 [..., D / 32] of rows x [..., D]: ``quantize_groups`` at 4
+    bits of the values cut to +-65504; a NaN takes no part in min and max and gets code 0."""
+    x = np.clip(np.asarray(x, np.float32), -F16_MAX, F16_MAX)
+    g = x.reshape(*x.shape[:-1], x.shape[-1] // GROUP, GROUP)
+    nan = np.isnan(g)
+    low = np.where(nan, np.inf, g).min(axis=-1, keepdims=True)
+    low = np.where(np.isinf(low), 0.0, low).astype(np.float32)
+    codes, scale, zero = quantize_groups(np.where(nan, low, g), 4)
+    return np.where(nan, 0, codes).astype(np.uint8).reshape(x.shape), scale, zero
+
+
+def q4_values(codes, scale, zero):
+    """The values the codes stand for: fl32(zero + scale code), float64."""
+    c = codes.reshape(*codes.shape[:-1], codes.shape[-1] // GROUP, GROUP).astype(np.float64)
+    x = zero.astype(np.float64)[..., None] + scale.astype(np.float64)[..., None] * c
+    return x.astype(np.float32).astype(np.float64).reshape(codes.shape)
+
+
+def q4_page_bytes(k, v, page=None, slots=range(Q4_PAGE)):
+    """Bytes uint8 [80 D] of one (page, head) holding the rows k, v [len(slots), D] at `slots`, the others
+    as they are in `page` (default: zero)."""
+    D = k.shape[-1]
+    ng, half, meta = D // GROUP, 40 * D, 4 * D
+    out = np.zeros(80 * D, np.uint8) if page is None else page.copy()
+    h16, w32 = out.view(np.uint16), out.view(np.uint32)
+    for side, x in ((0, k), (1, v)):
+        codes, scale, zero = q4_quantize(x)
+        base = side * half
+        for i, s in enumerate(slots):
+            for grp in range(ng):
+                pair = ((s // 2) * ng + grp) * 2 + s % 2
+                h16[(base + 32 * D) // 2 + pair] = scale[i, grp].view(np.uint16)
+                h16[(base + 32 * D + meta) // 2 + (pair if side else s * ng + grp)] = zero[i, grp].view(np.uint16)
+                c = codes[i, 32 * grp:32 * grp + 32].astype(np.uint32)
+                if side == 0:
+                    for q in range(4):
+                        word = sum(int(c[8 * q + e]) << bit_offset(e, 4) for e in range(8))
+                        w32[(s * 4 + q) * ng + grp] = word
+                else:
+                    for g in range(8):
+                        word = sum(int(c[4 * g + j]) << (4 * j) for j in range(4))
+                        h16[(base // 4 + (s // 2 * 8 + g) * ng + grp) * 2 + s % 2] = word
+    return out
+
+
+def q4_bounds(k_values):
+    """Smallest and largest fp16 value of each channel over a page's rows: fp16 [2, D]."""
+    x = np.clip(k_values, -F16_MAX, F16_MAX).astype(np.float16)
+    return np.stack([x.min(axis=0), x.max(axis=0)])
+
+
+def q4_scores(q, bounds):
+    """Scores of pages for one group's queries q [G, D] and the pages' bounds [P, 2, D]: float64 [P], the
+    largest over the group's heads of sum_c max(q_c lo_c, q_c hi_c)."""
+    q64, e = _f64(q)[:, None, :], _f64(bounds)
+    return np.maximum(q64 * e[None, :, 0], q64 * e[None, :, 1]).sum(axis=-1).max(axis=0)
+
+
+def q4_select(scores, n_keep, n_first, n_last):
+    """Kept pages, ascending: all when they fit, else the first, the last and the best others (equal
+    scores: the lower page)."""
+    P = len(scores)
+    if P <= n_keep:
+        return list(range(P))
+    forced = set(range(n_first)) | set(range(P - n_last, P))
+    rest = sorted((p for p in range(P) if p not in forced), key=lambda p: (-scores[p], p))
+    return sorted(forced | set(rest[:n_keep - len(forced)]))
