@@ -1,4 +1,23 @@
 // Attention over the 4-bit paged cache (rdkv_q4_attn).
+//
+//   logits  s_t = (q . k^_t) / sqrt(D),  k^ = zero + scale code per group of 32 channels, so
+//           q . k^_t = sum_grp scale_t,grp (sum_c q_c code_t,c) + sum_grp zero_t,grp (sum_c q_c)
+//   out     = sum_t p_t v^_t / sum_t p_t,  p_t = 2^(s_t log2 e - ref), the values by the same split
+//
+// Work.  A unit is (sequence, chunk of query tokens, KV head): up to 8 NT query rows, NT = 1 or 2, that
+// share the unit's keys; an item is one page (64 tokens) of a unit.  The items of all units, one after
+// another, are dealt evenly to the warps of the grid (one block an SM): each warp takes a run of items
+// and works alone, copying page halves (K, then V) into its own ring with bulk copies.  Units that end
+// inside a warp's run are written by it; the pieces of the others are joined per block in shared memory
+// and, where a unit spans blocks, by the last of its blocks through the workspace.
+//
+// Products: mma.sync, queries on M and tokens on N for the logits, channels on M and queries on N for the
+// values.  A code at bit p < 8 of a half word is the fp16 subnormal code 2^(p - 24), so one AND makes two
+// codes an operand register; the units are undone in fp32.  Each group's logits accumulate on their own
+// and take the token's scale in fp32; the zeros' part is one more product, of the queries' group sums
+// (fp16 high part and remainder).  The weights are multiplied by the values' scales in fp32 and rounded
+// to fp16 once; for fp32 outputs (PREC) they keep a remainder too, and the queries a low part in the
+// rows 8 .. 15 of the same product.
 #include "q4.cuh"
 
 namespace rdkv {
@@ -10,81 +29,737 @@ struct AttnArgs {
   void* out;
   float* lse;
   const int32_t* sel;
+  float* heads;      // [grid * NW] partials: pieces of units that end inside a warp's run
+  float* parts;      // [grid * 2] partials: a block's part of a unit that began before it, of one that goes on
+  int32_t* tickets;  // [units] blocks that have written their part
   int64_t q_stride;
-  int dtype, out_dtype, n_q, G, n_sel;
+  int dtype, out_dtype, n_q, G, n_sel, chunk, n_chunks;  // chunk: query tokens of a unit
 };
 
-// One block per (sequence, query token, KV head): page after page, the logits of the group's heads by
-// a dot product a (token, head), then the running softmax and the values, a channel a thread.
-template <int D>
-__global__ void __launch_bounds__(128) attn_kernel(AttnArgs a) {
+constexpr long long kWaitCycles = 4000000000LL;  // a bounded wait, about two seconds
+constexpr int kInfo = 32;                        // items whose places a warp knows ahead
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  if (try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!try_wait(bar, parity))
+    if (clock64() - t0 > kWaitCycles) return false;
+  return true;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+// the remainders of two values past their fp16 parts
+__device__ __forceinline__ uint32_t rest2(float lo, float hi, uint32_t w) {
+  const float2 f = unpack2(w);
+  return pack2(lo - f.x, hi - f.y);
+}
+template <int NG>
+__device__ __forceinline__ void lds_groups(const uint8_t* p, uint32_t (&w)[NG]) {
+  if constexpr (NG == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+}
+// Four codes pairs of a word: at bits 0 and 16 (2^-24), 4 and 20 (2^-20), and the same of the upper bytes.
+struct Pairs {
+  uint32_t a, b, c, d;
+};
+__device__ __forceinline__ Pairs code_pairs(uint32_t w) {
+  const uint32_t u = w >> 8;
+  return Pairs{w & 0x000f000fu, w & 0x00f000f0u, u & 0x000f000fu, u & 0x00f000f0u};
+}
+
+// A piece of a unit: ROWS x D sums and each row's reference (base 2) and sum of weights.
+template <int D, int NT>
+struct Partial {
+  static constexpr int kRows = 8 * NT, kFloats = kRows * (D + 2);
+};
+
+// Items of (sequence, chunk) bc in each of its KV heads, and the keys that its last query token sees.
+__device__ __forceinline__ int seen_by(const AttnArgs& a, int b, int chunk) {
+  return held_tokens(a.c, b) - a.n_q + min((chunk + 1) * a.chunk, a.n_q);
+}
+__device__ __forceinline__ int items_of(const AttnArgs& a, int bc) {
+  const int seen = seen_by(a, bc / a.n_chunks, bc % a.n_chunks);
+  return seen <= 0 ? 0 : a.sel ? a.n_sel : ceil_div(seen, kPage);
+}
+
+// Four channels of one query row of a unit into out; nothing for rows past the unit's last.
+__device__ __forceinline__ void put4(const AttnArgs& a, int unit, int row, int D, int ch, float4 o) {
+  const int h = unit % a.c.h_kv, bc = unit / a.c.h_kv, t = bc % a.n_chunks * a.chunk + row / a.G;
+  const int64_t at = ((((int64_t)(bc / a.n_chunks) * a.n_q + t) * a.c.h_kv + h) * a.G + row % a.G) * D + ch;
+  if (a.out_dtype == RDKV_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
+  } else {
+    uint2 w;
+    if (a.out_dtype == RDKV_F16) {
+      w = make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
+      w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = w;
+  }
+}
+__device__ __forceinline__ void put_lse(const AttnArgs& a, int unit, int row, float m, float l) {
+  if (!a.lse) return;
+  const int h = unit % a.c.h_kv, bc = unit / a.c.h_kv, t = bc % a.n_chunks * a.chunk + row / a.G;
+  a.lse[(((int64_t)(bc / a.n_chunks) * a.n_q + t) * a.c.h_kv + h) * a.G + row % a.G] =
+      l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+__device__ __forceinline__ int rows_of(const AttnArgs& a, int unit) {
+  const int first = unit / a.c.h_kv % a.n_chunks * a.chunk;
+  return min(a.chunk, a.n_q - first) * a.G;
+}
+
+// One warp's running state over the pages of one unit.
+template <int D, int NT, bool PREC>
+struct Warp {
+  static constexpr int NG = D / kGroup, kQ = NT == 2 || PREC ? 2 : 1;
   using L = Layout<D>;
-  constexpr int NG = L::NG;
-  __shared__ float q_s[8][D], p_s[8][kPage], k_s[kPage][D + 1], m_s[8], l_s[8], f_s[8];
-  const int h = blockIdx.x % a.c.h_kv, bt = blockIdx.x / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q, tid = threadIdx.x;
-  const int held = held_tokens(a.c, b), seen = held - a.n_q + t + 1;
-  const int64_t qrow = ((int64_t)b * a.n_q + t) * a.q_stride + (int64_t)h * a.G * D;
-  for (int i = tid; i < a.G * D; i += 128) q_s[i / D][i % D] = load_q(a.q, qrow + i, a.dtype);
-  if (tid < 8) m_s[tid] = -INFINITY, l_s[tid] = 0.0f;
-  float o[8] = {};
-  const int n_pages = seen > 0 ? ceil_div(seen, kPage) : 0, n = a.sel ? a.n_sel : n_pages;
-  const int32_t* sel = a.sel ? a.sel + ((int64_t)bt * a.c.h_kv + h) * a.n_sel : nullptr;
-  for (int i = 0; i < n; ++i) {
-    const int lp = sel ? sel[i] : i;
-    if (lp < 0 || lp >= n_pages) continue;
-    const int phys = a.c.page_table[(int64_t)b * a.c.page_stride + lp];
-    if (phys < 0 || phys >= a.c.n_pages) {
-      if (tid == 0) raise(a.c, RDKV_ERR_INVALID_ARG);
-      continue;
-    }
-    const uint8_t* page = a.c.pages + ((int64_t)phys * a.c.h_kv + h) * L::kBytes;
-    const int live = min(kPage, seen - lp * kPage);
-    __syncthreads();
-    for (int j = tid; j < kPage * D; j += 128) {
-      const int s = j / D, c = j % D, grp = c / 32, e = c % 8, q = c % 32 / 8;
-      const uint32_t w = reinterpret_cast<const uint32_t*>(page + L::kKCodes)[(s * 4 + q) * NG + grp];
-      const uint32_t code = (w >> (16 * (e & 1) + 4 * (e >> 1))) & 15u;
-      k_s[s][c] = fmaf(__half2float(reinterpret_cast<const __half*>(page + L::kKScales)[(s / 2 * NG + grp) * 2 + s % 2]),
-                       (float)code, __half2float(reinterpret_cast<const __half*>(page + L::kKZeros)[s * NG + grp]));
-    }
-    __syncthreads();
-    for (int j = tid; j < a.G * kPage; j += 128) {
-      const int g = j / kPage, s = j % kPage;
-      float x = 0.0f;
-      for (int c = 0; c < D; ++c) x = fmaf(q_s[g][c], k_s[s][c], x);
-      p_s[g][s] = s < live ? x * rsqrtf((float)D) : -INFINITY;
-    }
-    __syncthreads();
-    if (tid < a.G) {
-      float m = m_s[tid];
-      for (int s = 0; s < live; ++s) m = fmaxf(m, p_s[tid][s]);
-      const float f = expf(m_s[tid] - m);
-      float l = l_s[tid] * f;
-      for (int s = 0; s < kPage; ++s) {
-        const float p = s < live ? expf(p_s[tid][s] - m) : 0.0f;
-        p_s[tid][s] = p;
-        l += p;
+  uint32_t q[kQ][NG][4];  // A registers: rows g, and rows g + 8 (second half of the chunk, or the low parts)
+  uint32_t qz[NT];        // A registers of the zeros' product
+  float scale[NT];        // 2^(15 - s): a row's logits are held times 2^(s - 15)
+  float ref[NT], l[NT];   // the running maximum (base 2) and this lane's share of the sum
+  float o[NT][NG][2][4], oz[NT][4];
+  int off;                // weights are held times 2^off
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, int unit, int g, int qd) {
+    const int h = unit % a.c.h_kv, bc = unit / a.c.h_kv, b = bc / a.n_chunks, t0 = bc % a.n_chunks * a.chunk;
+    const int rows = rows_of(a, unit);
+    constexpr float kK = 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = g + 8 * n;
+      float x[NG][8], top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+      if (row < rows) {
+        const int64_t at = ((int64_t)b * a.n_q + t0 + row / a.G) * a.q_stride + ((int64_t)h * a.G + row % a.G) * D + 8 * qd;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          if (a.dtype == RDKV_F16) Eight<__half>::load(static_cast<const __half*>(a.q) + at + 32 * i, x[i]);
+          else if (a.dtype == RDKV_BF16) Eight<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(a.q) + at + 32 * i, x[i]);
+          else Eight<float>::load(static_cast<const float*>(a.q) + at + 32 * i, x[i]);
+        }
       }
-      m_s[tid] = m, l_s[tid] = l, f_s[tid] = f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the row times 2^s, its largest value in [2^14, 2^15): what fp16 drops is 2^-25 against that
+      const int e2 = (int)(__float_as_uint(top) >> 23) - 127;
+      const int s = top > 0.0f ? max(-96, min(111, 14 - e2)) : 0;
+      const float up = __uint_as_float((uint32_t)(s + 127) << 23);
+      scale[n] = __uint_as_float((uint32_t)(15 - s + 127) << 23);
+      float sum[NG];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        sum[i] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] *= up, sum[i] += x[i][e];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // pairs 1 and 3 meet codes that stand for sixteen times as much
+          const float f = j & 1 ? 0.0625f : 1.0f, y0 = x[i][2 * j] * f, y1 = x[i][2 * j + 1] * f;
+          q[n][i][j] = pack2(y0, y1);
+          if constexpr (PREC) q[1][i][j] = rest2(y0, y1, q[0][i][j]);
+        }
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+        sum[i] *= kK / 32768.0f;
+      }
+      // k slots 0 .. NG - 1: the sums' fp16 parts, the next NG: the remainders
+      uint32_t hi[NG / 2], lo[NG / 2];
+#pragma unroll
+      for (int i = 0; i < NG / 2; ++i) {
+        hi[i] = pack2(sum[2 * i], sum[2 * i + 1]);
+        lo[i] = rest2(sum[2 * i], sum[2 * i + 1], hi[i]);
+      }
+      if constexpr (NG == 4) qz[n] = qd == 0 ? hi[0] : qd == 1 ? hi[1] : qd == 2 ? lo[0] : lo[1];
+      else qz[n] = qd == 0 ? hi[0] : qd == 1 ? lo[0] : 0u;
+      ref[n] = -INFINITY;
+      l[n] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[n][i][j / 4][j % 4] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) oz[n][j] = 0.0f;
     }
-    __syncthreads();
-    if (tid < D) {
-      const int c = tid, grp = c / 32, g8 = c % 32 / 4, j4 = c % 4;
-      for (int g = 0; g < a.G; ++g) o[g] *= f_s[g];
-      for (int s = 0; s < live; ++s) {
-        const int m = (s / 2 * NG + grp) * 2 + s % 2;
-        const uint32_t w = reinterpret_cast<const uint16_t*>(page + L::kVCodes)[((s / 2 * 8 + g8) * NG + grp) * 2 + s % 2];
-        const float x = fmaf(__half2float(reinterpret_cast<const __half*>(page + L::kVScales)[m]), (float)((w >> (4 * j4)) & 15u),
-                             __half2float(reinterpret_cast<const __half*>(page + L::kVZeros)[m]));
-        for (int g = 0; g < a.G; ++g) o[g] = fmaf(p_s[g][s], x, o[g]);
+    off = 11;
+  }
+
+  // Logits of the page's 64 keys for this lane's rows: u[n][tile][token 2 qd + i of the tile's eight].
+  __device__ __forceinline__ void logits(const uint8_t* k, int g, int qd, float (&u)[NT][8][2]) const {
+    constexpr float kK = 512.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      uint32_t w[NG], sw[NG];
+      lds_groups<NG>(k + L::kKCodes + ((8 * t + g) * 4 + qd) * NG * 4, w);
+      lds_groups<NG>(k + L::kKScales + (4 * t + qd) * NG * 4, sw);
+      const uint32_t zw = reinterpret_cast<const uint32_t*>(k + L::kKZeros)[(8 * t + g) * (NG / 2) + (NG == 4 ? qd & 1 : 0)];
+      float z[4] = {}, s[NT][2] = {};
+      mma8(z, qz[0], NT == 2 ? qz[NT - 1] : 0u, zw);
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const Pairs p = code_pairs(w[i]);
+        float c[4] = {};
+        mma16(c, q[0][i][0], kQ == 2 ? q[kQ - 1][i][0] : 0u, q[0][i][1], kQ == 2 ? q[kQ - 1][i][1] : 0u, p.a, p.b);
+        mma16(c, q[0][i][2], kQ == 2 ? q[kQ - 1][i][2] : 0u, q[0][i][3], kQ == 2 ? q[kQ - 1][i][3] : 0u, p.c, p.d);
+        const float2 f = unpack2(sw[i]);
+        if constexpr (PREC) c[0] += c[2], c[1] += c[3];
+        s[0][0] = fmaf(f.x, c[0], s[0][0]);
+        s[0][1] = fmaf(f.y, c[1], s[0][1]);
+        if constexpr (NT == 2) {
+          s[1][0] = fmaf(f.x, c[2], s[1][0]);
+          s[1][1] = fmaf(f.y, c[3], s[1][1]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        u[n][t][0] = fmaf(s[n][0], kK, z[2 * n]);
+        u[n][t][1] = fmaf(s[n][1], kK, z[2 * n + 1]);
       }
     }
   }
+
+  // Sums and weights times 2^d, d this lane's rows' own.
+  __device__ __forceinline__ void rescale(int n, float f, int qd) {
+    l[n] *= f;
+    // columns 2 qd and 2 qd + 1 of the sums are rows that lanes 8 qd and 8 qd + 4 keep
+    const float f0 = __shfl_sync(0xffffffffu, f, 8 * qd), f1 = __shfl_sync(0xffffffffu, f, 8 * qd + 4);
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        o[n][i][m][0] *= f0, o[n][i][m][1] *= f1, o[n][i][m][2] *= f0, o[n][i][m][3] *= f1;
+    oz[n][0] *= f0, oz[n][1] *= f1, oz[n][2] *= f0, oz[n][3] *= f1;
+  }
+
+  // Raises a row's reference when a logit passes it by more than 4, so that weights stay at most 2^4.
+  __device__ __forceinline__ void raise_refs(const float (&u)[NT][8][2], int qd) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float m = fmaxf(u[n][0][0], u[n][0][1]);
+#pragma unroll
+      for (int t = 1; t < 8; ++t) m = fmaxf(m, fmaxf(u[n][t][0], u[n][t][1]));
+      m *= scale[n];
+      if (__any_sync(0xffffffffu, m > ref[n] + 4.0f)) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = fmaxf(m, ref[n]);
+        const float f = ref[n] == -INFINITY ? 0.0f : ex2(ref[n] - m);
+        ref[n] = m;
+        rescale(n, f, qd);
+      }
+    }
+  }
+
+  // The page's values.  live: the page's tokens that hold anything; kTail: fewer than all, so that what
+  // the others hold (arbitrary bits) is replaced by zero.
+  template <bool kTail>
+  __device__ __forceinline__ void values(const uint8_t* k, int g, int qd, int live, const float (&u)[NT][8][2]) {
+    const int lane = 4 * g + qd;
+    uint32_t sw[NG];
+    {  // The weights' exponent follows the largest scale met, so that weight times scale stays in fp16's
+       // range: with the weight at most 2^(4 + off) and the scale below 2^(e + 1), the product is below
+       // 2^13, and off <= 11 keeps the weight itself in range.
+      lds_groups<NG>(k + L::kVScales + lane * NG * 4, sw);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        uint32_t w = sw[i];
+        if (kTail) w &= (2 * lane < live ? 0xffffu : 0u) | (2 * lane + 1 < live ? 0xffff0000u : 0u);
+        top = __vmaxu2(top, w);
+      }
+      top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+      const int now = min(off, 8 - ((int)(top >> 10) - 15));
+      if (now < off) {
+        const float f = __uint_as_float((uint32_t)(now - off + 127) << 23);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) rescale(n, f, qd);
+        off = now;
+      }
+    }
+    float r[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) r[n] = (float)off - (ref[n] == -INFINITY ? 0.0f : ref[n]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {  // 16 tokens
+      float p[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        p[n][0] = ex2(fmaf(u[n][2 * t][0], scale[n], r[n]));
+        p[n][1] = ex2(fmaf(u[n][2 * t][1], scale[n], r[n]));
+        p[n][2] = ex2(fmaf(u[n][2 * t + 1][0], scale[n], r[n]));
+        p[n][3] = ex2(fmaf(u[n][2 * t + 1][1], scale[n], r[n]));
+        l[n] += (p[n][0] + p[n][1]) + (p[n][2] + p[n][3]);
+      }
+      const int p0 = 8 * t + qd, p1 = p0 + 4;  // this lane's token pairs
+      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+      if (kTail) {
+        keep0 = (2 * p0 < live ? 0xffffu : 0u) | (2 * p0 + 1 < live ? 0xffff0000u : 0u);
+        keep1 = (2 * p1 < live ? 0xffffu : 0u) | (2 * p1 + 1 < live ? 0xffff0000u : 0u);
+      }
+      const uint32_t* zs = reinterpret_cast<const uint32_t*>(k + L::kVZeros);
+      const uint32_t z0 = g < NG ? zs[p0 * NG + g] & keep0 : 0u, z1 = g < NG ? zs[p1 * NG + g] & keep1 : 0u;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t b0 = pack2(p[n][0], p[n][1]), b1 = pack2(p[n][2], p[n][3]);
+        mma16(oz[n], z0, 0u, z1, 0u, b0, b1);
+        if constexpr (PREC) mma16(oz[n], z0, 0u, z1, 0u, rest2(p[n][0], p[n][1], b0), rest2(p[n][2], p[n][3], b1));
+      }
+      uint32_t w0[NG], w1[NG], s0[NG], s1[NG];
+      lds_groups<NG>(k + L::kVCodes + (p0 * 8 + g) * NG * 4, w0);
+      lds_groups<NG>(k + L::kVCodes + (p1 * 8 + g) * NG * 4, w1);
+      lds_groups<NG>(k + L::kVScales + p0 * NG * 4, s0);
+      lds_groups<NG>(k + L::kVScales + p1 * NG * 4, s1);
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const Pairs x = code_pairs(w0[i]), y = code_pairs(w1[i]);
+        const float2 f0 = unpack2(s0[i] & keep0), f1 = unpack2(s1[i] & keep1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float e0 = p[n][0] * f0.x, e1 = p[n][1] * f0.y, e2 = p[n][2] * f1.x, e3 = p[n][3] * f1.y;
+          const uint32_t b0 = pack2(e0, e1), b1 = pack2(e2, e3);
+          mma16(o[n][i][0], x.a, x.b, y.a, y.b, b0, b1);
+          mma16(o[n][i][1], x.c, x.d, y.c, y.d, b0, b1);
+          if constexpr (PREC) {
+            const uint32_t c0 = rest2(e0, e1, b0), c1 = rest2(e2, e3, b1);
+            mma16(o[n][i][0], x.a, x.b, y.a, y.b, c0, c1);
+            mma16(o[n][i][1], x.c, x.d, y.c, y.d, c0, c1);
+          }
+        }
+      }
+    }
+  }
+
+  // The unit's sums: put(row, first channel, four sums) for every row and channel of this lane, then
+  // stat(row, reference, sum) once a row.
+  template <class Put, class Stat>
+  __device__ __forceinline__ void finish(int g, int qd, Put put, Stat stat) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float sum = l[n];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const float m = ref[n] == -INFINITY ? -INFINITY : ref[n] - (float)off;
+      // the sums' columns are rows of lanes 8 qd and 8 qd + 4
+      const float l0 = __shfl_sync(0xffffffffu, sum, 8 * qd), l1 = __shfl_sync(0xffffffffu, sum, 8 * qd + 4);
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const float z0 = __shfl_sync(0xffffffffu, oz[n][0], 4 * i + qd), z1 = __shfl_sync(0xffffffffu, oz[n][1], 4 * i + qd);
+        const float(&c)[2][4] = o[n][i];
+        constexpr float a = 16777216.0f, b = 1048576.0f;  // the codes' units
+        put(8 * n + 2 * qd, 32 * i + 4 * g, l0,
+            make_float4(fmaf(c[0][0], a, z0), fmaf(c[0][2], b, z0), fmaf(c[1][0], a, z0), fmaf(c[1][2], b, z0)));
+        put(8 * n + 2 * qd + 1, 32 * i + 4 * g, l1,
+            make_float4(fmaf(c[0][1], a, z1), fmaf(c[0][3], b, z1), fmaf(c[1][1], a, z1), fmaf(c[1][3], b, z1)));
+      }
+      if (qd == 0) stat(8 * n + g, m, sum);
+    }
+  }
+};
+
+// What a block knows of a piece it joins.
+struct Piece {
+  int64_t base;  // the unit's first item
+  int unit, items;
+};
+
+template <int D, int NT, bool PREC, int NW, int NS>
+struct Smem {
+  static constexpr int kRing = NS * Layout<D>::kHalf;
+  static_assert(Partial<D, NT>::kFloats * 4 <= kRing, "a warp's piece goes into its ring");
+  static_assert(2 * NW <= 32, "a lane a piece");
+  static constexpr size_t kBars = (size_t)NW * kRing, kInfoAt = kBars + 8 * NW * NS, kBytes = kInfoAt + 16 * NW * kInfo;
+};
+
+template <int D, int NT, bool PREC, int NW, int NS>
+__global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
+  using L = Layout<D>;
+  using P = Partial<D, NT>;
+  using S = Smem<D, NT, PREC, NW, NS>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Piece piece_s[2 * NW];
+  __shared__ uint32_t valid_s, start_s, end_s;
+  __shared__ unsigned long long total_s;
+  __shared__ int last_s[2];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, qd = lane % 4, H = a.c.h_kv;
+  uint8_t* ring = smem + (size_t)warp * S::kRing;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * NS;
+  int4* info = reinterpret_cast<int4*>(smem + S::kInfoAt) + warp * kInfo;
+  const int BC = a.c.batch * a.n_chunks;
+  if (tid == 0) total_s = 0, valid_s = start_s = end_s = 0;
+  if (lane < NS) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bars + lane)) : "memory");
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncthreads();
-  const int64_t row = (int64_t)bt * a.c.h_kv * a.G + (int64_t)h * a.G;
-  if (tid < D)
-    for (int g = 0; g < a.G; ++g) store_as(a.out, (row + g) * D + tid, a.out_dtype, l_s[g] > 0.0f ? o[g] / l_s[g] : 0.0f);
-  if (a.lse && tid < a.G) a.lse[row + tid] = l_s[tid] > 0.0f ? m_s[tid] + logf(l_s[tid]) : -INFINITY;
+  {
+    int64_t n = 0;
+    for (int i = tid; i < BC; i += 32 * NW) {
+      n += items_of(a, i);
+      if (blockIdx.x == 0 && i % a.n_chunks == 0) {
+        const int len = __ldg(a.c.lens + i / a.n_chunks);
+        if (len < 0) raise(a.c, RDKV_ERR_INVALID_ARG);
+        if ((int64_t)len > (int64_t)a.c.page_stride * kPage) raise(a.c, RDKV_ERR_CAPACITY);
+      }
+    }
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0 && n) atomicAdd(&total_s, (unsigned long long)n);
+  }
+  // units without a key: nothing else writes their rows
+  for (int bc = blockIdx.x; bc < BC; bc += gridDim.x) {
+    if (items_of(a, bc) > 0) continue;
+    for (int h = 0; h < H; ++h) {
+      const int unit = bc * H + h, rows = rows_of(a, unit);
+      for (int i = tid; i < rows * (D / 4); i += 32 * NW) put4(a, unit, i / (D / 4), D, i % (D / 4) * 4, make_float4(0, 0, 0, 0));
+      if (tid < rows) put_lse(a, unit, tid, 0.0f, 0.0f);
+    }
+  }
+  __syncthreads();
+  const int64_t total = (int64_t)total_s * H;
+  // a block for as many items as it has warps: few items stay in few blocks, whose joins are cheap
+  const int64_t nb = min((int64_t)gridDim.x, ceil_div64(total, NW));
+  if (blockIdx.x >= nb) return;
+  const int64_t nw = nb * NW, me = (int64_t)blockIdx.x * NW + warp;
+  const int64_t w0 = me * total / nw, w1 = (me + 1) * total / nw;
+  const int n_items = (int)min(w1 - w0, (int64_t)INT32_MAX);
+
+  // ---- where the run begins
+  int bc = 0, h = 0, p = 0, cnt = 0;  // the next item to look up
+  {
+    int64_t before = 0;
+    for (int i0 = 0; i0 < BC && n_items > 0; i0 += 32) {
+      const int c = i0 + lane < BC ? items_of(a, i0 + lane) : 0;
+      int64_t in = (int64_t)c * H;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + in > w0);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        cnt = __shfl_sync(0xffffffffu, c, l);
+        const int64_t rem = w0 - before - (__shfl_sync(0xffffffffu, in, l) - (int64_t)cnt * H);
+        bc = i0 + l, h = (int)(rem / cnt), p = (int)(rem % cnt);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, in, 31);
+    }
+  }
+  // The next n items' places, one a lane: physical page (-1: nothing to copy), logical page, unit, and
+  // whether the item is its unit's first or last.
+  int known = 0;
+  auto look_up = [&](int n) {
+    const int i = known + lane;
+    int4 e = make_int4(-1, 0, 0, 0);
+    int b1 = bc, h1 = h, p1 = p + lane, c1 = cnt;
+    const bool mine = lane < n && i < n_items;
+    if (mine) {
+      while (p1 >= c1) {
+        p1 -= c1;
+        if (++h1 == H) {
+          h1 = 0;
+          do c1 = items_of(a, ++b1);
+          while (c1 == 0);
+        }
+      }
+      const int unit = b1 * H + h1, b = b1 / a.n_chunks;
+      int lp = p1;
+      if (a.sel) {
+        lp = __ldg(a.sel + (int64_t)unit * a.n_sel + p1);
+        if (lp < 0 || (int64_t)lp * kPage >= seen_by(a, b, b1 % a.n_chunks)) lp = -1;
+      }
+      if (lp >= 0) {
+        e.x = __ldg(a.c.page_table + (int64_t)b * a.c.page_stride + lp);
+        if (e.x < 0 || e.x >= a.c.n_pages) {
+          raise(a.c, RDKV_ERR_INVALID_ARG);
+          e.x = -1;
+        }
+      }
+      e.y = lp, e.z = unit, e.w = (p1 == 0 ? 1 : 0) | (p1 == c1 - 1 ? 2 : 0);
+      info[i % kInfo] = e;
+    }
+    // from the last lane's item the next begins one further; only items that exist are passed on
+    const int from = min(n, n_items - known) - 1;
+    if (from >= 0) {
+      bc = __shfl_sync(0xffffffffu, b1, from), h = __shfl_sync(0xffffffffu, h1, from);
+      p = __shfl_sync(0xffffffffu, p1, from) + 1, cnt = __shfl_sync(0xffffffffu, c1, from);
+      known += from + 1;
+    }
+    __syncwarp();
+  };
+  look_up(kInfo);
+  // Copies half x (K, then V of item x / 2) into stage x % NS.
+  auto issue = [&](int x) {
+    const int i = x / 2;
+    if (i >= n_items) return;
+    if (i >= known) look_up(kInfo / 2);
+    if (lane == 0) {
+      const int4 e = info[i % kInfo];
+      uint64_t* bar = bars + x % NS;
+      if (e.x < 0) {
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+      } else {
+        const uint8_t* src = a.c.pages + ((int64_t)e.x * H + e.z % H) * L::kBytes + (x & 1) * L::kHalf;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(L::kHalf) : "memory");
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         smem_u32(ring + x % NS * L::kHalf)),
+                     "l"(src), "r"(L::kHalf), "r"(smem_u32(bar))
+                     : "memory");
+      }
+    }
+    __syncwarp();
+  };
+  for (int x = 0; x < NS; ++x) issue(x);
+
+  // ---- the run
+  Warp<D, NT, PREC> w;
+  bool in_unit = false, began = false, ok = true;
+  int held = 0, x = 0;  // held: tokens of the unit's sequence
+  int low[NT];          // keys that this lane's rows see
+  for (int i = 0; i < n_items && ok; ++i) {
+    const int4 e = info[i % kInfo];
+    if (!in_unit) {
+      in_unit = true, began = e.w & 1;
+      w.begin(a, e.z, g, qd);
+      const int bc1 = e.z / H;
+      held = held_tokens(a.c, bc1 / a.n_chunks);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        low[n] = held - a.n_q + min(bc1 % a.n_chunks * a.chunk + (g + 8 * n) / a.G, a.n_q - 1) + 1;
+    }
+    float u[NT][8][2];
+    const int t0 = e.y * kPage;
+    ok = wait_for(bars + x % NS, (x / NS) & 1);
+    if (ok && e.x >= 0) {
+      w.logits(ring + x % NS * L::kHalf, g, qd, u);
+      bool cut = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) cut |= t0 + kPage > low[n];
+      if (__any_sync(0xffffffffu, cut)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (t0 + 8 * t + 2 * qd + j >= low[n]) u[n][t][j] = -INFINITY;
+      }
+      w.raise_refs(u, qd);
+    }
+    __syncwarp();
+    if (ok) issue(x + NS);
+    ++x;
+    ok = ok && wait_for(bars + x % NS, (x / NS) & 1);
+    if (ok && e.x >= 0) {
+      const uint8_t* v = ring + x % NS * L::kHalf - L::kHalf;  // the layout's V offsets count from the K half
+      const int live = held - t0;
+      if (live < kPage) w.template values<true>(v, g, qd, live, u);
+      else w.template values<false>(v, g, qd, kPage, u);
+    }
+    __syncwarp();
+    if (ok) issue(x + NS);
+    ++x;
+    if ((e.w & 2) || i == n_items - 1) {  // the unit, or the run, ends
+      const int rows = rows_of(a, e.z);
+      if (began && (e.w & 2)) {
+        w.finish(
+            g, qd,
+            [&](int row, int ch, float l, float4 o) {
+              if (row >= rows) return;
+              const float f = l > 0.0f ? 1.0f / l : 0.0f;
+              put4(a, e.z, row, D, ch, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+            },
+            [&](int row, float m, float l) {
+              if (row < rows) put_lse(a, e.z, row, m, l);
+            });
+      } else {
+        // a unit that ends here lies first in the run: copies are under way, its piece goes to global memory
+        float* dst = e.w & 2 ? a.heads + me * P::kFloats : reinterpret_cast<float*>(ring);
+        w.finish(
+            g, qd, [&](int row, int ch, float, float4 o) { *reinterpret_cast<float4*>(dst + row * D + ch) = o; },
+            [&](int row, float m, float l) { dst[P::kRows * D + row] = m, dst[P::kRows * (D + 1) + row] = l; });
+        if (lane == 0) {
+          const int at = 2 * warp + (e.w & 2 ? 0 : 1);
+          const int items = items_of(a, e.z / H);
+          // the item's place in its unit: the last one, or what the lookup of a later item would hold
+          int64_t base = w0 + i - (items - 1);
+          if (!(e.w & 2)) base = w1 - p;  // the lookup stands one past the run's last item
+          piece_s[at] = Piece{base, e.z, items};
+          atomicOr(&valid_s, 1u << at);
+          if (began) atomicOr(&start_s, 1u << at);
+          if (e.w & 2) atomicOr(&end_s, 1u << at);
+        }
+      }
+      in_unit = false;
+    }
+  }
+  if (!ok) {  // a wait ran out: report it, and let the copies under way land (again with a limit)
+    if (lane == 0) raise(a.c, RDKV_ERR_TIMEOUT);
+    for (int y = x; y < min(x + NS, 2 * n_items); ++y) wait_for(bars + y % NS, (y / NS) & 1);
+  }
+  __syncthreads();
+
+  // ---- joining the block's pieces: runs of pieces of one unit, a run begins at a piece that holds its
+  // unit's first item, or at the block's first piece
+  const uint32_t valid = valid_s, ends = end_s;
+  const uint32_t begins = start_s, starts = begins | (valid & (0u - valid));
+  const int n_runs = __popc(starts);
+  auto src_of = [&](int e) -> const float* {
+    return e & 1 ? reinterpret_cast<const float*>(smem + (size_t)(e / 2) * S::kRing)
+                 : a.heads + ((int64_t)blockIdx.x * NW + e / 2) * P::kFloats;
+  };
+  int open_unit[2] = {-1, -1};  // runs that are a part of their unit: one that began before the block, one that goes on
+  int open_n[2] = {0, 0}, open_first[2] = {0, 0};
+  auto block_of = [&](int64_t item) { return (int)(((item + 1) * nb - 1) / total); };
+  {
+    uint32_t left = starts;
+    for (int r = 0; r < n_runs; ++r) {
+      const int s = __ffs(left) - 1;
+      left &= left - 1;
+      const uint32_t members = valid & ~((1u << s) - 1u) & (left ? (1u << (__ffs(left) - 1)) - 1u : 0xffffffffu);
+      const bool whole = (begins >> s & 1) && (ends & members);
+      const Piece pc = piece_s[s];
+      const int slot = begins >> s & 1, rows = rows_of(a, pc.unit);
+      float* part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * P::kFloats;
+      for (int idx = tid; idx < rows * (D / 4); idx += 32 * NW) {
+        const int row = idx / (D / 4), ch = idx % (D / 4) * 4;
+        float M = -INFINITY;
+        for (uint32_t m = members; m; m &= m - 1) M = fmaxf(M, src_of(__ffs(m) - 1)[P::kRows * D + row]);
+        float4 o = make_float4(0, 0, 0, 0);
+        float l = 0.0f;
+        for (uint32_t m = members; m; m &= m - 1) {
+          const float* src = src_of(__ffs(m) - 1);
+          const float f = M == -INFINITY ? 0.0f : ex2(src[P::kRows * D + row] - M);
+          const float4 y = *reinterpret_cast<const float4*>(src + row * D + ch);
+          o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+          l = fmaf(f, src[P::kRows * (D + 1) + row], l);
+        }
+        if (whole) {
+          const float f = l > 0.0f ? 1.0f / l : 0.0f;
+          put4(a, pc.unit, row, D, ch, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+          if (ch == 0) put_lse(a, pc.unit, row, M, l);
+        } else {
+          *reinterpret_cast<float4*>(part + row * D + ch) = o;
+          if (ch == 0) part[P::kRows * D + row] = M, part[P::kRows * (D + 1) + row] = l;
+        }
+      }
+      if (!whole) {
+        open_unit[slot] = pc.unit;
+        open_first[slot] = block_of(pc.base);
+        open_n[slot] = block_of(pc.base + pc.items - 1) - open_first[slot] + 1;
+      }
+    }
+  }
+  // ---- joining the blocks' parts: the last block of a unit to arrive does it
+  __syncthreads();
+  if (tid < 2 && open_unit[tid] >= 0) {
+    __threadfence();
+    int32_t* t = a.tickets + open_unit[tid];
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(t) : "memory");
+    last_s[tid] = before == open_n[tid] - 1;
+    if (last_s[tid]) *t = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  for (int slot = 0; slot < 2; ++slot) {
+    const int unit = slot ? open_unit[1] : open_unit[0], n = slot ? open_n[1] : open_n[0], first = slot ? open_first[1] : open_first[0];
+    if (unit < 0 || !last_s[slot]) continue;
+    const int rows = rows_of(a, unit);
+    for (int idx = tid; idx < rows * (D / 4); idx += 32 * NW) {
+      const int row = idx / (D / 4), ch = idx % (D / 4) * 4;
+      // the unit's first block wrote it as the unit that goes on, the others as the one that began before
+      auto part = [&](int i) { return a.parts + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * P::kFloats; };
+      float M = -INFINITY;
+      for (int i = 0; i < n; ++i) M = fmaxf(M, __ldcg(part(i) + P::kRows * D + row));
+      float4 o = make_float4(0, 0, 0, 0);
+      float l = 0.0f;
+      for (int i = 0; i < n; ++i) {
+        const float* src = part(i);
+        const float f = M == -INFINITY ? 0.0f : ex2(__ldcg(src + P::kRows * D + row) - M);
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src + row * D + ch));
+        o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+        l = fmaf(f, __ldcg(src + P::kRows * (D + 1) + row), l);
+      }
+      const float f = l > 0.0f ? 1.0f / l : 0.0f;
+      put4(a, unit, row, D, ch, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+      if (ch == 0) put_lse(a, unit, row, M, l);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- launch
+// The workspace has the same places for every shape, so that calls of any shape may follow one another:
+// pieces of the largest variant, then the tickets.
+constexpr int kMaxWarps = 12;
+
+struct Geometry {
+  int chunk, n_chunks, nt, grid;
+  size_t parts_at, tickets_at, bytes;
+};
+
+static Geometry geometry(const rdkv_q4_cache* c, int h_q, int n_q, bool prec, bool own_pages) {
+  Geometry o;
+  const int G = h_q / c->h_kv;
+  // Query tokens that share one pass over the keys: as many as fit in 16 rows (8 for fp32 outputs, whose
+  // other 8 rows hold the queries' low parts); one when every query token has its own pages
+  o.chunk = own_pages ? 1 : std::min(n_q, std::max(1, (prec ? 8 : 16) / G));
+  o.n_chunks = ceil_div(n_q, o.chunk);
+  o.nt = o.chunk * G > 8 ? 2 : 1;
+  o.grid = num_sms();
+  const int64_t tickets = (int64_t)c->batch * n_q * c->h_kv, part = 4LL * Partial<128, 2>::kFloats;
+  o.parts_at = (size_t)align_up((int64_t)o.grid * kMaxWarps * part, 256);
+  o.tickets_at = o.parts_at + (size_t)align_up(2LL * o.grid * part, 256);
+  o.bytes = o.tickets_at + (size_t)align_up(4 * tickets, 256);
+  return o;
+}
+
+template <int D, int NT, bool PREC, int NW, int NS>
+static rdkv_status launch(const AttnArgs& a, int grid, cudaStream_t cs) {
+  using S = Smem<D, NT, PREC, NW, NS>;
+  static_assert(NW <= kMaxWarps, "the workspace counts with kMaxWarps");
+  auto kernel = attn_kernel<D, NT, PREC, NW, NS>;
+  RDKV_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes), "4-bit cache attention");
+  kernel<<<grid, 32 * NW, S::kBytes, cs>>>(a);
+  RDKV_CHECK_LAUNCH("4-bit cache attention");
+  return RDKV_OK;
 }
 
 }  // namespace q4
@@ -94,7 +769,8 @@ using namespace rdkv;
 using namespace rdkv::q4;
 
 extern "C" size_t rdkv_q4_attn_workspace_bytes(const rdkv_q4_cache* cache, int32_t h_q, int32_t n_q) {
-  return check_queries(cache, h_q, n_q) == RDKV_OK ? 256 : 0;
+  if (check_queries(cache, h_q, n_q) != RDKV_OK) return 0;
+  return geometry(cache, h_q, n_q, false, false).bytes;
 }
 
 extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
@@ -106,13 +782,21 @@ extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, c
   RDKV_REQUIRE((uintptr_t)out % 16 == 0, RDKV_ERR_INVALID_ARG, "out must be 16-byte aligned");
   RDKV_REQUIRE(out_dtype == dtype || out_dtype == RDKV_F32, RDKV_ERR_UNSUPPORTED, "out_dtype %d for dtype %d", out_dtype, dtype);
   RDKV_REQUIRE(!sel || n_sel >= 1, RDKV_ERR_INVALID_ARG, "n_sel %d", n_sel);
-  const size_t need = rdkv_q4_attn_workspace_bytes(cache, h_q, n_q);
-  RDKV_REQUIRE(ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= need, RDKV_ERR_WORKSPACE, "attention workspace too small (%zu < %zu) or unaligned",
-               ws_bytes, need);
-  AttnArgs a{view_of(cache), q, out, lse, sel, q_stride, dtype, out_dtype, n_q, h_q / cache->h_kv, n_sel};
-  const unsigned blocks = (unsigned)((int64_t)cache->batch * n_q * cache->h_kv);
-  if (cache->head_dim == 64) attn_kernel<64><<<blocks, 128, 0, (cudaStream_t)stream>>>(a);
-  else attn_kernel<128><<<blocks, 128, 0, (cudaStream_t)stream>>>(a);
-  RDKV_CHECK_LAUNCH("4-bit cache attention");
-  return RDKV_OK;
+  const bool prec = out_dtype == RDKV_F32;
+  const Geometry geo = geometry(cache, h_q, n_q, prec, sel != nullptr);
+  RDKV_REQUIRE(ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= geo.bytes, RDKV_ERR_WORKSPACE,
+               "attention workspace too small (%zu < %zu) or unaligned", ws_bytes, geo.bytes);
+  char* w = static_cast<char*>(ws);
+  const AttnArgs a{view_of(cache), q, out, lse, sel, reinterpret_cast<float*>(w), reinterpret_cast<float*>(w + geo.parts_at),
+                   reinterpret_cast<int32_t*>(w + geo.tickets_at), q_stride, dtype, out_dtype, n_q, h_q / cache->h_kv, n_sel,
+                   geo.chunk, geo.n_chunks};
+  cudaStream_t cs = (cudaStream_t)stream;
+  if (cache->head_dim == 128) {
+    if (prec) return launch<128, 1, true, 11, 4>(a, geo.grid, cs);
+    if (geo.nt == 2) return launch<128, 2, false, 8, 5>(a, geo.grid, cs);
+    return launch<128, 1, false, 12, 3>(a, geo.grid, cs);
+  }
+  if (prec) return launch<64, 1, true, 11, 8>(a, geo.grid, cs);
+  if (geo.nt == 2) return launch<64, 2, false, 8, 10>(a, geo.grid, cs);
+  return launch<64, 1, false, 12, 6>(a, geo.grid, cs);
 }
