@@ -4,6 +4,8 @@
 
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "common.cuh"
 
 namespace rdkv {

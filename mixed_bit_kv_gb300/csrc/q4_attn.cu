@@ -7,7 +7,7 @@
 // Work.  A unit is (sequence, chunk of query tokens, KV head): up to 8 NT query rows, NT = 1 or 2, that
 // share the unit's keys; an item is one page (64 tokens) of a unit.  The items of all units, one after
 // another, are dealt evenly to the warps of the grid (one block an SM): each warp takes a run of items
-// and works alone, copying page halves (K, then V) into its own ring with bulk copies.  Units that end
+// and works alone, copying pages into its own ring with bulk copies.  Units that end
 // inside a warp's run are written by it; the pieces of the others are joined per block in shared memory
 // and, where a unit spans blocks, by the last of its blocks through the workspace.
 //
@@ -15,9 +15,9 @@
 // values.  A code at bit p < 8 of a half word is the fp16 subnormal code 2^(p - 24), so one AND makes two
 // codes an operand register; the units are undone in fp32.  Each group's logits accumulate on their own
 // and take the token's scale in fp32; the zeros' part is one more product, of the queries' group sums
-// (fp16 high part and remainder).  The weights are multiplied by the values' scales in fp32 and rounded
-// to fp16 once; for fp32 outputs (PREC) they keep a remainder too, and the queries a low part in the
-// rows 8 .. 15 of the same product.
+// (fp16 high part and remainder).  A weight times its values' scale is rounded to fp16 once; for fp32
+// outputs (PREC) the product keeps a remainder too, and the queries a low part in the rows 8 .. 15 of
+// the same product.
 #include "q4.cuh"
 
 namespace rdkv {
@@ -65,10 +65,32 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(b0));
+// the same on a zero accumulator
+__device__ __forceinline__ void mma16z(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma8z(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
+}
+// two fp32 products and sums in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)), "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -114,10 +136,20 @@ __device__ __forceinline__ int items_of(const AttnArgs& a, int bc) {
   return seen <= 0 ? 0 : a.sel ? a.n_sel : ceil_div(seen, kPage);
 }
 
-// Four channels of one query row of a unit into out; nothing for rows past the unit's last.
-__device__ __forceinline__ void put4(const AttnArgs& a, int unit, int row, int D, int ch, float4 o) {
-  const int h = unit % a.c.h_kv, bc = unit / a.c.h_kv, t = bc % a.n_chunks * a.chunk + row / a.G;
-  const int64_t at = ((((int64_t)(bc / a.n_chunks) * a.n_q + t) * a.c.h_kv + h) * a.G + row % a.G) * D + ch;
+// What a unit's index stands for.
+struct Unit {
+  int b, t0, h, rows;  // sequence, first query token, KV head, query rows
+};
+__device__ __forceinline__ Unit unit_at(const AttnArgs& a, int unit) {
+  const int bc = unit / a.c.h_kv, b = bc / a.n_chunks, t0 = (bc - b * a.n_chunks) * a.chunk;
+  return Unit{b, t0, unit - bc * a.c.h_kv, min(a.chunk, a.n_q - t0) * a.G};
+}
+// Output row (and place in lse) of a unit's query row.
+__device__ __forceinline__ int64_t row_at(const AttnArgs& a, const Unit& u, int row) {
+  const int t = row / a.G;
+  return (((int64_t)u.b * a.n_q + u.t0 + t) * a.c.h_kv + u.h) * a.G + (row - t * a.G);
+}
+__device__ __forceinline__ void put4(const AttnArgs& a, int64_t at, float4 o) {
   if (a.out_dtype == RDKV_F32) {
     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
   } else {
@@ -131,15 +163,8 @@ __device__ __forceinline__ void put4(const AttnArgs& a, int unit, int row, int D
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = w;
   }
 }
-__device__ __forceinline__ void put_lse(const AttnArgs& a, int unit, int row, float m, float l) {
-  if (!a.lse) return;
-  const int h = unit % a.c.h_kv, bc = unit / a.c.h_kv, t = bc % a.n_chunks * a.chunk + row / a.G;
-  a.lse[(((int64_t)(bc / a.n_chunks) * a.n_q + t) * a.c.h_kv + h) * a.G + row % a.G] =
-      l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-}
-__device__ __forceinline__ int rows_of(const AttnArgs& a, int unit) {
-  const int first = unit / a.c.h_kv % a.n_chunks * a.chunk;
-  return min(a.chunk, a.n_q - first) * a.G;
+__device__ __forceinline__ void put_lse(const AttnArgs& a, int64_t row, float m, float l) {
+  if (a.lse) a.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // One warp's running state over the pages of one unit.
@@ -154,27 +179,33 @@ struct Warp {
   float o[NT][NG][2][4], oz[NT][4];
   int off;                // weights are held times 2^off
 
-  __device__ __forceinline__ void begin(const AttnArgs& a, int unit, int g, int qd) {
-    const int h = unit % a.c.h_kv, bc = unit / a.c.h_kv, b = bc / a.n_chunks, t0 = bc % a.n_chunks * a.chunk;
-    const int rows = rows_of(a, unit);
-    constexpr float kK = 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+  // This lane's channels of the unit's query rows (rows past the last: zero).
+  __device__ __forceinline__ static void fetch(const AttnArgs& a, const Unit& un, int g, int qd, float (&x)[NT][NG][8]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int row = g + 8 * n;
-      float x[NG][8], top = 0.0f;
 #pragma unroll
       for (int i = 0; i < NG; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
-      if (row < rows) {
-        const int64_t at = ((int64_t)b * a.n_q + t0 + row / a.G) * a.q_stride + ((int64_t)h * a.G + row % a.G) * D + 8 * qd;
+        for (int e = 0; e < 8; ++e) x[n][i][e] = 0.0f;
+      if (row < un.rows) {
+        const int64_t at = ((int64_t)un.b * a.n_q + un.t0 + row / a.G) * a.q_stride + ((int64_t)un.h * a.G + row % a.G) * D + 8 * qd;
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          if (a.dtype == RDKV_F16) Eight<__half>::load(static_cast<const __half*>(a.q) + at + 32 * i, x[i]);
-          else if (a.dtype == RDKV_BF16) Eight<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(a.q) + at + 32 * i, x[i]);
-          else Eight<float>::load(static_cast<const float*>(a.q) + at + 32 * i, x[i]);
+          if (a.dtype == RDKV_F16) Eight<__half>::load(static_cast<const __half*>(a.q) + at + 32 * i, x[n][i]);
+          else if (a.dtype == RDKV_BF16) Eight<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(a.q) + at + 32 * i, x[n][i]);
+          else Eight<float>::load(static_cast<const float*>(a.q) + at + 32 * i, x[n][i]);
         }
       }
+    }
+  }
+
+  __device__ __forceinline__ void begin(float (&rows)[NT][NG][8], int qd) {
+    constexpr float kK = 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float(&x)[NG][8] = rows[n];
+      float top = 0.0f;
 #pragma unroll
       for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -224,41 +255,7 @@ struct Warp {
     off = 11;
   }
 
-  // Logits of the page's 64 keys for this lane's rows: u[n][tile][token 2 qd + i of the tile's eight].
-  __device__ __forceinline__ void logits(const uint8_t* k, int g, int qd, float (&u)[NT][8][2]) const {
-    constexpr float kK = 512.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      uint32_t w[NG], sw[NG];
-      lds_groups<NG>(k + L::kKCodes + ((8 * t + g) * 4 + qd) * NG * 4, w);
-      lds_groups<NG>(k + L::kKScales + (4 * t + qd) * NG * 4, sw);
-      const uint32_t zw = reinterpret_cast<const uint32_t*>(k + L::kKZeros)[(8 * t + g) * (NG / 2) + (NG == 4 ? qd & 1 : 0)];
-      float z[4] = {}, s[NT][2] = {};
-      mma8(z, qz[0], NT == 2 ? qz[NT - 1] : 0u, zw);
-#pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const Pairs p = code_pairs(w[i]);
-        float c[4] = {};
-        mma16(c, q[0][i][0], kQ == 2 ? q[kQ - 1][i][0] : 0u, q[0][i][1], kQ == 2 ? q[kQ - 1][i][1] : 0u, p.a, p.b);
-        mma16(c, q[0][i][2], kQ == 2 ? q[kQ - 1][i][2] : 0u, q[0][i][3], kQ == 2 ? q[kQ - 1][i][3] : 0u, p.c, p.d);
-        const float2 f = unpack2(sw[i]);
-        if constexpr (PREC) c[0] += c[2], c[1] += c[3];
-        s[0][0] = fmaf(f.x, c[0], s[0][0]);
-        s[0][1] = fmaf(f.y, c[1], s[0][1]);
-        if constexpr (NT == 2) {
-          s[1][0] = fmaf(f.x, c[2], s[1][0]);
-          s[1][1] = fmaf(f.y, c[3], s[1][1]);
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        u[n][t][0] = fmaf(s[n][0], kK, z[2 * n]);
-        u[n][t][1] = fmaf(s[n][1], kK, z[2 * n + 1]);
-      }
-    }
-  }
-
-  // Sums and weights times 2^d, d this lane's rows' own.
+  // Row sums and weighted sums times f, each lane's row's own.
   __device__ __forceinline__ void rescale(int n, float f, int qd) {
     l[n] *= f;
     // columns 2 qd and 2 qd + 1 of the sums are rows that lanes 8 qd and 8 qd + 4 keep
@@ -271,44 +268,24 @@ struct Warp {
     oz[n][0] *= f0, oz[n][1] *= f1, oz[n][2] *= f0, oz[n][3] *= f1;
   }
 
-  // Raises a row's reference when a logit passes it by more than 4, so that weights stay at most 2^4.
-  __device__ __forceinline__ void raise_refs(const float (&u)[NT][8][2], int qd) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float m = fmaxf(u[n][0][0], u[n][0][1]);
-#pragma unroll
-      for (int t = 1; t < 8; ++t) m = fmaxf(m, fmaxf(u[n][t][0], u[n][t][1]));
-      m *= scale[n];
-      if (__any_sync(0xffffffffu, m > ref[n] + 4.0f)) {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        m = fmaxf(m, ref[n]);
-        const float f = ref[n] == -INFINITY ? 0.0f : ex2(ref[n] - m);
-        ref[n] = m;
-        rescale(n, f, qd);
-      }
-    }
-  }
-
-  // The page's values.  live: the page's tokens that hold anything; kTail: fewer than all, so that what
-  // the others hold (arbitrary bits) is replaced by zero.
+  // One page.  kTail: its last tokens may hold nothing (live of them do; what the others hold is arbitrary
+  // bits) or be hidden from some rows (row n of this lane sees low[n] of the page's tokens).
   template <bool kTail>
-  __device__ __forceinline__ void values(const uint8_t* k, int g, int qd, int live, const float (&u)[NT][8][2]) {
-    const int lane = 4 * g + qd;
-    uint32_t sw[NG];
-    {  // The weights' exponent follows the largest scale met, so that weight times scale stays in fp16's
-       // range: with the weight at most 2^(4 + off) and the scale below 2^(e + 1), the product is below
-       // 2^13, and off <= 11 keeps the weight itself in range.
+  __device__ __forceinline__ void page(const uint8_t* k, int g, int qd, int live, const int (&low)[NT]) {
+    constexpr float kK = 512.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+    {  // The weights' exponent follows the largest value scale met, so that weight times scale stays in
+       // fp16's range: with the weight at most 2^(4 + off) and the scale below 2^(e + 1), the product is
+       // below 2^13, and off <= 11 keeps the weight itself in range.
+      const int lane = 4 * g + qd;
+      uint32_t sw[NG], top = 0;
       lds_groups<NG>(k + L::kVScales + lane * NG * 4, sw);
-      uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        uint32_t w = sw[i];
-        if (kTail) w &= (2 * lane < live ? 0xffffu : 0u) | (2 * lane + 1 < live ? 0xffff0000u : 0u);
-        top = __vmaxu2(top, w);
+        if (kTail) sw[i] &= (2 * lane < live ? 0xffffu : 0u) | (2 * lane + 1 < live ? 0xffff0000u : 0u);
+        top = __vmaxu2(top, sw[i]);
       }
       top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-      const int now = min(off, 8 - ((int)(top >> 10) - 15));
+      const int now = min(off, 23 - (int)(top >> 10));
       if (now < off) {
         const float f = __uint_as_float((uint32_t)(now - off + 127) << 23);
 #pragma unroll
@@ -316,53 +293,111 @@ struct Warp {
         off = now;
       }
     }
-    float r[NT];
+    // 32 tokens a turn: enough independent products to hide their latency, and a body that stays in the
+    // instruction cache
+#pragma unroll 1
+    for (int t32 = 0; t32 < kPage; t32 += 32) {
+      float2 u[NT][4];  // logits (base 2, times 2^(s - 15)) of tokens t32 + 8 t + 2 qd + {0, 1}
 #pragma unroll
-    for (int n = 0; n < NT; ++n) r[n] = (float)off - (ref[n] == -INFINITY ? 0.0f : ref[n]);
+      for (int t = 0; t < 4; ++t) {
+        const int tok = t32 + 8 * t;
+        uint32_t w[NG], sw[NG];
+        lds_groups<NG>(k + L::kKCodes + ((tok + g) * 4 + qd) * NG * 4, w);
+        lds_groups<NG>(k + L::kKScales + (tok / 2 + qd) * NG * 4, sw);
+        const uint32_t zw = reinterpret_cast<const uint32_t*>(k + L::kKZeros)[(tok + g) * (NG / 2) + (NG == 4 ? qd & 1 : 0)];
+        float z[4];
+        mma8z(z, qz[0], NT == 2 ? qz[NT - 1] : 0u, zw);
+        float2 s[NT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {  // 16 tokens
-      float p[NT][4];
+        for (int n = 0; n < NT; ++n) s[n] = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        p[n][0] = ex2(fmaf(u[n][2 * t][0], scale[n], r[n]));
-        p[n][1] = ex2(fmaf(u[n][2 * t][1], scale[n], r[n]));
-        p[n][2] = ex2(fmaf(u[n][2 * t + 1][0], scale[n], r[n]));
-        p[n][3] = ex2(fmaf(u[n][2 * t + 1][1], scale[n], r[n]));
-        l[n] += (p[n][0] + p[n][1]) + (p[n][2] + p[n][3]);
-      }
-      const int p0 = 8 * t + qd, p1 = p0 + 4;  // this lane's token pairs
-      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-      if (kTail) {
-        keep0 = (2 * p0 < live ? 0xffffu : 0u) | (2 * p0 + 1 < live ? 0xffff0000u : 0u);
-        keep1 = (2 * p1 < live ? 0xffffu : 0u) | (2 * p1 + 1 < live ? 0xffff0000u : 0u);
-      }
-      const uint32_t* zs = reinterpret_cast<const uint32_t*>(k + L::kVZeros);
-      const uint32_t z0 = g < NG ? zs[p0 * NG + g] & keep0 : 0u, z1 = g < NG ? zs[p1 * NG + g] & keep1 : 0u;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint32_t b0 = pack2(p[n][0], p[n][1]), b1 = pack2(p[n][2], p[n][3]);
-        mma16(oz[n], z0, 0u, z1, 0u, b0, b1);
-        if constexpr (PREC) mma16(oz[n], z0, 0u, z1, 0u, rest2(p[n][0], p[n][1], b0), rest2(p[n][2], p[n][3], b1));
-      }
-      uint32_t w0[NG], w1[NG], s0[NG], s1[NG];
-      lds_groups<NG>(k + L::kVCodes + (p0 * 8 + g) * NG * 4, w0);
-      lds_groups<NG>(k + L::kVCodes + (p1 * 8 + g) * NG * 4, w1);
-      lds_groups<NG>(k + L::kVScales + p0 * NG * 4, s0);
-      lds_groups<NG>(k + L::kVScales + p1 * NG * 4, s1);
-#pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const Pairs x = code_pairs(w0[i]), y = code_pairs(w1[i]);
-        const float2 f0 = unpack2(s0[i] & keep0), f1 = unpack2(s1[i] & keep1);
+        for (int i = 0; i < NG; ++i) {
+          const Pairs p = code_pairs(w[i]);
+          float c[4];
+          mma16z(c, q[0][i][0], kQ == 2 ? q[kQ - 1][i][0] : 0u, q[0][i][1], kQ == 2 ? q[kQ - 1][i][1] : 0u, p.a, p.b);
+          mma16(c, q[0][i][2], kQ == 2 ? q[kQ - 1][i][2] : 0u, q[0][i][3], kQ == 2 ? q[kQ - 1][i][3] : 0u, p.c, p.d);
+          const float2 f = unpack2(sw[i]);
+          if constexpr (PREC) c[0] += c[2], c[1] += c[3];
+          s[0] = fma2(f, make_float2(c[0], c[1]), s[0]);
+          if constexpr (NT == 2) s[1] = fma2(f, make_float2(c[2], c[3]), s[1]);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float e0 = p[n][0] * f0.x, e1 = p[n][1] * f0.y, e2 = p[n][2] * f1.x, e3 = p[n][3] * f1.y;
-          const uint32_t b0 = pack2(e0, e1), b1 = pack2(e2, e3);
-          mma16(o[n][i][0], x.a, x.b, y.a, y.b, b0, b1);
-          mma16(o[n][i][1], x.c, x.d, y.c, y.d, b0, b1);
-          if constexpr (PREC) {
-            const uint32_t c0 = rest2(e0, e1, b0), c1 = rest2(e2, e3, b1);
-            mma16(o[n][i][0], x.a, x.b, y.a, y.b, c0, c1);
-            mma16(o[n][i][1], x.c, x.d, y.c, y.d, c0, c1);
+          u[n][t] = fma2(s[n], make_float2(kK, kK), make_float2(z[2 * n], z[2 * n + 1]));
+          if (kTail) {
+            if (tok + 2 * qd >= low[n]) u[n][t].x = -INFINITY;
+            if (tok + 2 * qd + 1 >= low[n]) u[n][t].y = -INFINITY;
+          }
+        }
+      }
+      // a row's reference rises when a logit passes it by more than 4, so that weights stay at most 2^4
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float m = fmaxf(u[n][0].x, u[n][0].y);
+#pragma unroll
+        for (int t = 1; t < 4; ++t) m = fmaxf(m, fmaxf(u[n][t].x, u[n][t].y));
+        m *= scale[n];
+        if (__any_sync(0xffffffffu, m > ref[n] + 4.0f)) {
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          m = fmaxf(m, ref[n]);
+          const float f = ref[n] == -INFINITY ? 0.0f : ex2(ref[n] - m);
+          ref[n] = m;
+          rescale(n, f, qd);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {  // 16 tokens
+        float p[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float r = (float)off - (ref[n] == -INFINITY ? 0.0f : ref[n]);
+          const float2 y0 = fma2(u[n][2 * t], make_float2(scale[n], scale[n]), make_float2(r, r));
+          const float2 y1 = fma2(u[n][2 * t + 1], make_float2(scale[n], scale[n]), make_float2(r, r));
+          p[n][0] = ex2(y0.x), p[n][1] = ex2(y0.y), p[n][2] = ex2(y1.x), p[n][3] = ex2(y1.y);
+          l[n] += (p[n][0] + p[n][1]) + (p[n][2] + p[n][3]);
+        }
+        const int p0 = t32 / 2 + 8 * t + qd, p1 = p0 + 4;  // this lane's token pairs
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (kTail) {
+          keep0 = (2 * p0 < live ? 0xffffu : 0u) | (2 * p0 + 1 < live ? 0xffff0000u : 0u);
+          keep1 = (2 * p1 < live ? 0xffffu : 0u) | (2 * p1 + 1 < live ? 0xffff0000u : 0u);
+        }
+        const uint32_t* zs = reinterpret_cast<const uint32_t*>(k + L::kVZeros);
+        const uint32_t z0 = g < NG ? zs[p0 * NG + g] & keep0 : 0u, z1 = g < NG ? zs[p1 * NG + g] & keep1 : 0u;
+        uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          hi[n][0] = pack2(p[n][0], p[n][1]), hi[n][1] = pack2(p[n][2], p[n][3]);
+          lo[n][0] = rest2(p[n][0], p[n][1], hi[n][0]), lo[n][1] = rest2(p[n][2], p[n][3], hi[n][1]);
+          mma16(oz[n], z0, 0u, z1, 0u, hi[n][0], hi[n][1]);
+          if constexpr (PREC) mma16(oz[n], z0, 0u, z1, 0u, lo[n][0], lo[n][1]);
+        }
+        uint32_t w0[NG], w1[NG], s0[NG], s1[NG];
+        lds_groups<NG>(k + L::kVCodes + (p0 * 8 + g) * NG * 4, w0);
+        lds_groups<NG>(k + L::kVCodes + (p1 * 8 + g) * NG * 4, w1);
+        lds_groups<NG>(k + L::kVScales + p0 * NG * 4, s0);
+        lds_groups<NG>(k + L::kVScales + p1 * NG * 4, s1);
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          const Pairs x = code_pairs(w0[i]), y = code_pairs(w1[i]);
+          if (kTail) s0[i] &= keep0, s1[i] &= keep1;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (PREC) {
+              const float2 f0 = unpack2(s0[i]), f1 = unpack2(s1[i]);
+              const float e0 = p[n][0] * f0.x, e1 = p[n][1] * f0.y, e2 = p[n][2] * f1.x, e3 = p[n][3] * f1.y;
+              const uint32_t b0 = pack2(e0, e1), b1 = pack2(e2, e3), c0 = rest2(e0, e1, b0), c1 = rest2(e2, e3, b1);
+              mma16(o[n][i][0], x.a, x.b, y.a, y.b, b0, b1);
+              mma16(o[n][i][1], x.c, x.d, y.c, y.d, b0, b1);
+              mma16(o[n][i][0], x.a, x.b, y.a, y.b, c0, c1);
+              mma16(o[n][i][1], x.c, x.d, y.c, y.d, c0, c1);
+            } else {
+              // weight times scale, rounded to fp16 once: the weight as an fp16 part and its remainder
+              const uint32_t b0 = hfma2(hi[n][0], s0[i], hmul2(lo[n][0], s0[i])), b1 = hfma2(hi[n][1], s1[i], hmul2(lo[n][1], s1[i]));
+              mma16(o[n][i][0], x.a, x.b, y.a, y.b, b0, b1);
+              mma16(o[n][i][1], x.c, x.d, y.c, y.d, b0, b1);
+            }
           }
         }
       }
@@ -402,12 +437,40 @@ struct Piece {
   int unit, items;
 };
 
+// Joins pieces of one query row: a lane's four channels of the sums and, in every lane, the row's reference
+// and sum.  n pieces, m_of(i), l_of(i) their statistics, y_of(i) this lane's channels.
+template <class M, class L, class Y>
+__device__ __forceinline__ void join_row(int n, int lane, M m_of, L l_of, Y y_of, float4& o, float& top, float& sum) {
+  top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, m_of(i));
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  o = make_float4(0, 0, 0, 0);
+  sum = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float f = 0.0f;
+    if (i0 + lane < n && top != -INFINITY) f = ex2(m_of(i0 + lane) - top);
+    if (i0 + lane < n) sum = fmaf(f, l_of(i0 + lane), sum);
+    const int k = min(32, n - i0);
+#pragma unroll 8
+    for (int i = 0; i < k; ++i) {
+      const float4 y = y_of(i0 + i);
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y), o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
+    }
+  }
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+}
+__device__ __forceinline__ float4 scaled(float4 o, float l) {
+  const float f = l > 0.0f ? 1.0f / l : 0.0f;
+  return make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+}
+
 template <int D, int NT, bool PREC, int NW, int NS>
 struct Smem {
-  static constexpr int kRing = NS * Layout<D>::kHalf;
+  static constexpr int kRing = NS * Layout<D>::kBytes;
   static_assert(Partial<D, NT>::kFloats * 4 <= kRing, "a warp's piece goes into its ring");
   static_assert(2 * NW <= 32, "a lane a piece");
-  static constexpr size_t kBars = (size_t)NW * kRing, kInfoAt = kBars + 8 * NW * NS, kBytes = kInfoAt + 16 * NW * kInfo;
+  static constexpr size_t kBars = (size_t)NW * kRing, kInfoAt = kBars + 16 * ((NW * NS + 1) / 2), kBytes = kInfoAt + 16 * NW * kInfo;
 };
 
 template <int D, int NT, bool PREC, int NW, int NS>
@@ -420,6 +483,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   __shared__ uint32_t valid_s, start_s, end_s;
   __shared__ unsigned long long total_s;
   __shared__ int last_s[2];
+  __shared__ uint8_t member_s[2 * NW];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, qd = lane % 4, H = a.c.h_kv;
   uint8_t* ring = smem + (size_t)warp * S::kRing;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * NS;
@@ -428,44 +492,50 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   if (tid == 0) total_s = 0, valid_s = start_s = end_s = 0;
   if (lane < NS) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bars + lane)) : "memory");
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  __syncthreads();
-  {
-    int64_t n = 0;
-    for (int i = tid; i < BC; i += 32 * NW) {
-      n += items_of(a, i);
-      if (blockIdx.x == 0 && i % a.n_chunks == 0) {
-        const int len = __ldg(a.c.lens + i / a.n_chunks);
-        if (len < 0) raise(a.c, RDKV_ERR_INVALID_ARG);
-        if ((int64_t)len > (int64_t)a.c.page_stride * kPage) raise(a.c, RDKV_ERR_CAPACITY);
-      }
+
+  // ---- the items of all units, and where this warp's run of them begins
+  if (blockIdx.x == 0)
+    for (int i = tid; i < a.c.batch; i += 32 * NW) {
+      const int len = __ldg(a.c.lens + i);
+      if (len < 0) raise(a.c, RDKV_ERR_INVALID_ARG);
+      if ((int64_t)len > (int64_t)a.c.page_stride * kPage) raise(a.c, RDKV_ERR_CAPACITY);
     }
+  const int c0 = lane < BC ? items_of(a, lane) : 0;  // of the first 32 (sequence, chunk) pairs
+  int64_t total;
+  if (BC <= 32) {
+    total = __reduce_add_sync(0xffffffffu, (unsigned)c0);  // 32 counts below 2^26
+    __syncthreads();
+  } else {
+    int64_t n = 0;
+    __syncthreads();
+    for (int i = tid; i < BC; i += 32 * NW) n += items_of(a, i);
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     if (lane == 0 && n) atomicAdd(&total_s, (unsigned long long)n);
+    __syncthreads();
+    total = (int64_t)total_s;
   }
+  total *= H;
   // units without a key: nothing else writes their rows
   for (int bc = blockIdx.x; bc < BC; bc += gridDim.x) {
     if (items_of(a, bc) > 0) continue;
     for (int h = 0; h < H; ++h) {
-      const int unit = bc * H + h, rows = rows_of(a, unit);
-      for (int i = tid; i < rows * (D / 4); i += 32 * NW) put4(a, unit, i / (D / 4), D, i % (D / 4) * 4, make_float4(0, 0, 0, 0));
-      if (tid < rows) put_lse(a, unit, tid, 0.0f, 0.0f);
+      const Unit un = unit_at(a, bc * H + h);
+      for (int i = tid; i < un.rows * (D / 4); i += 32 * NW)
+        put4(a, row_at(a, un, i / (D / 4)) * D + i % (D / 4) * 4, make_float4(0, 0, 0, 0));
+      if (tid < un.rows) put_lse(a, row_at(a, un, tid), 0.0f, 0.0f);
     }
   }
-  __syncthreads();
-  const int64_t total = (int64_t)total_s * H;
   // a block for as many items as it has warps: few items stay in few blocks, whose joins are cheap
   const int64_t nb = min((int64_t)gridDim.x, ceil_div64(total, NW));
   if (blockIdx.x >= nb) return;
   const int64_t nw = nb * NW, me = (int64_t)blockIdx.x * NW + warp;
   const int64_t w0 = me * total / nw, w1 = (me + 1) * total / nw;
   const int n_items = (int)min(w1 - w0, (int64_t)INT32_MAX);
-
-  // ---- where the run begins
   int bc = 0, h = 0, p = 0, cnt = 0;  // the next item to look up
   {
     int64_t before = 0;
     for (int i0 = 0; i0 < BC && n_items > 0; i0 += 32) {
-      const int c = i0 + lane < BC ? items_of(a, i0 + lane) : 0;
+      const int c = i0 == 0 ? c0 : i0 + lane < BC ? items_of(a, i0 + lane) : 0;
       int64_t in = (int64_t)c * H;
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, in, o);
@@ -475,8 +545,10 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       if (past) {
         const int l = __ffs(past) - 1;
         cnt = __shfl_sync(0xffffffffu, c, l);
-        const int64_t rem = w0 - before - (__shfl_sync(0xffffffffu, in, l) - (int64_t)cnt * H);
-        bc = i0 + l, h = (int)(rem / cnt), p = (int)(rem % cnt);
+        int64_t rem = w0 - before - (__shfl_sync(0xffffffffu, in, l) - (int64_t)cnt * H);
+        bc = i0 + l;
+        while (rem >= cnt) rem -= cnt, ++h;  // at most the heads
+        p = (int)rem;
         break;
       }
       before += __shfl_sync(0xffffffffu, in, 31);
@@ -489,8 +561,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     const int i = known + lane;
     int4 e = make_int4(-1, 0, 0, 0);
     int b1 = bc, h1 = h, p1 = p + lane, c1 = cnt;
-    const bool mine = lane < n && i < n_items;
-    if (mine) {
+    if (lane < n && i < n_items) {
       while (p1 >= c1) {
         p1 -= c1;
         if (++h1 == H) {
@@ -524,107 +595,99 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     }
     __syncwarp();
   };
-  look_up(kInfo);
-  // Copies half x (K, then V of item x / 2) into stage x % NS.
-  auto issue = [&](int x) {
-    const int i = x / 2;
-    if (i >= n_items) return;
+  // Copies item i's page into stage i % NS.
+  auto issue = [&](int i) {
     if (i >= known) look_up(kInfo / 2);
     if (lane == 0) {
       const int4 e = info[i % kInfo];
-      uint64_t* bar = bars + x % NS;
+      const uint32_t bar = smem_u32(bars + i % NS);
       if (e.x < 0) {
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
       } else {
-        const uint8_t* src = a.c.pages + ((int64_t)e.x * H + e.z % H) * L::kBytes + (x & 1) * L::kHalf;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(L::kHalf) : "memory");
+        const uint8_t* src = a.c.pages + ((int64_t)e.x * H + e.z % H) * L::kBytes;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(L::kBytes) : "memory");
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         smem_u32(ring + x % NS * L::kHalf)),
-                     "l"(src), "r"(L::kHalf), "r"(smem_u32(bar))
+                         smem_u32(ring + i % NS * L::kBytes)),
+                     "l"(src), "r"(L::kBytes), "r"(bar)
                      : "memory");
       }
     }
     __syncwarp();
   };
-  for (int x = 0; x < NS; ++x) issue(x);
 
   // ---- the run
   Warp<D, NT, PREC> w;
   bool in_unit = false, began = false, ok = true;
-  int held = 0, x = 0;  // held: tokens of the unit's sequence
-  int low[NT];          // keys that this lane's rows see
-  for (int i = 0; i < n_items && ok; ++i) {
+  int held = 0;  // tokens of the unit's sequence
+  int low[NT];   // keys that this lane's rows see
+  Unit un{0, 0, 0, 0};
+  int i = 0;
+  if (n_items > 0) {
+    look_up(kInfo);
+    // the first queries are asked for before the pages, behind which they would wait
+    float x[NT][Warp<D, NT, PREC>::NG][8];
+    un = unit_at(a, info[0].z);
+    w.fetch(a, un, g, qd, x);
+#pragma unroll 1
+    for (int j = 0; j < min(NS, n_items); ++j) issue(j);
+    w.begin(x, qd);
+    in_unit = true;
+  }
+#pragma unroll 1
+  for (; i < n_items; ++i) {
     const int4 e = info[i % kInfo];
     if (!in_unit) {
-      in_unit = true, began = e.w & 1;
-      w.begin(a, e.z, g, qd);
-      const int bc1 = e.z / H;
-      held = held_tokens(a.c, bc1 / a.n_chunks);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        low[n] = held - a.n_q + min(bc1 % a.n_chunks * a.chunk + (g + 8 * n) / a.G, a.n_q - 1) + 1;
+      float x[NT][Warp<D, NT, PREC>::NG][8];
+      un = unit_at(a, e.z);
+      w.fetch(a, un, g, qd, x);
+      w.begin(x, qd);
     }
-    float u[NT][8][2];
-    const int t0 = e.y * kPage;
-    ok = wait_for(bars + x % NS, (x / NS) & 1);
-    if (ok && e.x >= 0) {
-      w.logits(ring + x % NS * L::kHalf, g, qd, u);
+    if (!in_unit || i == 0) {
+      in_unit = true, began = e.w & 1;
+      held = held_tokens(a.c, un.b);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) low[n] = held - a.n_q + min(un.t0 + (g + 8 * n) / a.G, a.n_q - 1) + 1;
+    }
+    if (!wait_for(bars + i % NS, (i / NS) & 1)) {
+      ok = false;
+      break;
+    }
+    if (e.x >= 0) {
+      const uint8_t* page = ring + i % NS * L::kBytes;
+      int see[NT];
       bool cut = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) cut |= t0 + kPage > low[n];
-      if (__any_sync(0xffffffffu, cut)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (t0 + 8 * t + 2 * qd + j >= low[n]) u[n][t][j] = -INFINITY;
-      }
-      w.raise_refs(u, qd);
+      for (int n = 0; n < NT; ++n) see[n] = low[n] - e.y * kPage, cut |= see[n] < kPage;
+      if (__any_sync(0xffffffffu, cut)) w.template page<true>(page, g, qd, held - e.y * kPage, see);
+      else w.template page<false>(page, g, qd, kPage, see);
     }
     __syncwarp();
-    if (ok) issue(x + NS);
-    ++x;
-    ok = ok && wait_for(bars + x % NS, (x / NS) & 1);
-    if (ok && e.x >= 0) {
-      const uint8_t* v = ring + x % NS * L::kHalf - L::kHalf;  // the layout's V offsets count from the K half
-      const int live = held - t0;
-      if (live < kPage) w.template values<true>(v, g, qd, live, u);
-      else w.template values<false>(v, g, qd, kPage, u);
-    }
-    __syncwarp();
-    if (ok) issue(x + NS);
-    ++x;
+    if (i + NS < n_items) issue(i + NS);
     if ((e.w & 2) || i == n_items - 1) {  // the unit, or the run, ends
-      const int rows = rows_of(a, e.z);
-      if (began && (e.w & 2)) {
+      const bool ends = e.w & 2;
+      // a unit that ends here without having begun lies first in the run: copies are under way, its piece
+      // goes to global memory
+      float* dst = ends ? a.heads + me * P::kFloats : reinterpret_cast<float*>(ring);
+      if (began && ends) {
         w.finish(
             g, qd,
             [&](int row, int ch, float l, float4 o) {
-              if (row >= rows) return;
-              const float f = l > 0.0f ? 1.0f / l : 0.0f;
-              put4(a, e.z, row, D, ch, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+              if (row < un.rows) put4(a, row_at(a, un, row) * D + ch, scaled(o, l));
             },
             [&](int row, float m, float l) {
-              if (row < rows) put_lse(a, e.z, row, m, l);
+              if (row < un.rows) put_lse(a, row_at(a, un, row), m, l);
             });
       } else {
-        // a unit that ends here lies first in the run: copies are under way, its piece goes to global memory
-        float* dst = e.w & 2 ? a.heads + me * P::kFloats : reinterpret_cast<float*>(ring);
         w.finish(
             g, qd, [&](int row, int ch, float, float4 o) { *reinterpret_cast<float4*>(dst + row * D + ch) = o; },
             [&](int row, float m, float l) { dst[P::kRows * D + row] = m, dst[P::kRows * (D + 1) + row] = l; });
         if (lane == 0) {
-          const int at = 2 * warp + (e.w & 2 ? 0 : 1);
-          const int items = items_of(a, e.z / H);
-          // the item's place in its unit: the last one, or what the lookup of a later item would hold
-          int64_t base = w0 + i - (items - 1);
-          if (!(e.w & 2)) base = w1 - p;  // the lookup stands one past the run's last item
-          piece_s[at] = Piece{base, e.z, items};
+          const int at = 2 * warp + (ends ? 0 : 1), items = items_of(a, e.z / H);
+          // the unit's first item: this one is its last, or the lookup stands one past the run's last item
+          piece_s[at] = Piece{ends ? w0 + i - (items - 1) : w1 - p, e.z, items};
           atomicOr(&valid_s, 1u << at);
           if (began) atomicOr(&start_s, 1u << at);
-          if (e.w & 2) atomicOr(&end_s, 1u << at);
+          if (ends) atomicOr(&end_s, 1u << at);
         }
       }
       in_unit = false;
@@ -632,95 +695,85 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   }
   if (!ok) {  // a wait ran out: report it, and let the copies under way land (again with a limit)
     if (lane == 0) raise(a.c, RDKV_ERR_TIMEOUT);
-    for (int y = x; y < min(x + NS, 2 * n_items); ++y) wait_for(bars + y % NS, (y / NS) & 1);
+    for (int j = i; j < min(i + NS, n_items); ++j) wait_for(bars + j % NS, (j / NS) & 1);
   }
   __syncthreads();
 
   // ---- joining the block's pieces: runs of pieces of one unit, a run begins at a piece that holds its
-  // unit's first item, or at the block's first piece
-  const uint32_t valid = valid_s, ends = end_s;
-  const uint32_t begins = start_s, starts = begins | (valid & (0u - valid));
-  const int n_runs = __popc(starts);
-  auto src_of = [&](int e) -> const float* {
-    return e & 1 ? reinterpret_cast<const float*>(smem + (size_t)(e / 2) * S::kRing)
-                 : a.heads + ((int64_t)blockIdx.x * NW + e / 2) * P::kFloats;
-  };
+  // unit's first item, or at the block's first piece; a query row of a run a warp
+  const uint32_t valid = valid_s, ends = end_s, begins = start_s;
+  const uint32_t starts = begins | (valid & (0u - valid));
+  if (tid < 2 * NW && (valid >> tid & 1)) member_s[__popc(valid & ((1u << tid) - 1u))] = (uint8_t)tid;
+  __syncthreads();
   int open_unit[2] = {-1, -1};  // runs that are a part of their unit: one that began before the block, one that goes on
   int open_n[2] = {0, 0}, open_first[2] = {0, 0};
   auto block_of = [&](int64_t item) { return (int)(((item + 1) * nb - 1) / total); };
-  {
-    uint32_t left = starts;
-    for (int r = 0; r < n_runs; ++r) {
-      const int s = __ffs(left) - 1;
-      left &= left - 1;
-      const uint32_t members = valid & ~((1u << s) - 1u) & (left ? (1u << (__ffs(left) - 1)) - 1u : 0xffffffffu);
-      const bool whole = (begins >> s & 1) && (ends & members);
-      const Piece pc = piece_s[s];
-      const int slot = begins >> s & 1, rows = rows_of(a, pc.unit);
-      float* part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * P::kFloats;
-      for (int idx = tid; idx < rows * (D / 4); idx += 32 * NW) {
-        const int row = idx / (D / 4), ch = idx % (D / 4) * 4;
-        float M = -INFINITY;
-        for (uint32_t m = members; m; m &= m - 1) M = fmaxf(M, src_of(__ffs(m) - 1)[P::kRows * D + row]);
-        float4 o = make_float4(0, 0, 0, 0);
-        float l = 0.0f;
-        for (uint32_t m = members; m; m &= m - 1) {
-          const float* src = src_of(__ffs(m) - 1);
-          const float f = M == -INFINITY ? 0.0f : ex2(src[P::kRows * D + row] - M);
-          const float4 y = *reinterpret_cast<const float4*>(src + row * D + ch);
-          o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
-          l = fmaf(f, src[P::kRows * (D + 1) + row], l);
-        }
-        if (whole) {
-          const float f = l > 0.0f ? 1.0f / l : 0.0f;
-          put4(a, pc.unit, row, D, ch, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
-          if (ch == 0) put_lse(a, pc.unit, row, M, l);
-        } else {
-          *reinterpret_cast<float4*>(part + row * D + ch) = o;
-          if (ch == 0) part[P::kRows * D + row] = M, part[P::kRows * (D + 1) + row] = l;
-        }
+  int task = 0;
+  for (uint32_t left = starts; left; left &= left - 1) {
+    const int s = __ffs(left) - 1;
+    const uint32_t rest = left & (left - 1), members = valid & ~((1u << s) - 1u) & (rest ? (rest & (0u - rest)) - 1u : 0xffffffffu);
+    const bool whole = (begins >> s & 1) && (ends & members);
+    const Piece pc = piece_s[s];
+    const int slot = begins >> s & 1, n = __popc(members), first = __popc(valid & ((1u << s) - 1u));
+    const Unit ru = unit_at(a, pc.unit);
+    float* part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * P::kFloats;
+    auto src = [&](int j) -> const float* {
+      const int e = member_s[first + j];
+      return e & 1 ? reinterpret_cast<const float*>(smem + (size_t)(e / 2) * S::kRing)
+                   : a.heads + ((int64_t)blockIdx.x * NW + e / 2) * P::kFloats;
+    };
+    for (int row = 0; row < ru.rows; ++row) {
+      if (task++ % NW != warp) continue;
+      float4 o;
+      float m, l;
+      const int ch = 4 * lane % D;
+      join_row(
+          n, lane, [&](int j) { return src(j)[P::kRows * D + row]; }, [&](int j) { return src(j)[P::kRows * (D + 1) + row]; },
+          [&](int j) { return *reinterpret_cast<const float4*>(src(j) + row * D + ch); }, o, m, l);
+      if (whole) {
+        const int64_t at = row_at(a, ru, row);
+        if (4 * lane < D) put4(a, at * D + ch, scaled(o, l));
+        if (lane == 0) put_lse(a, at, m, l);
+      } else {
+        if (4 * lane < D) *reinterpret_cast<float4*>(part + row * D + ch) = o;
+        if (lane == 0) part[P::kRows * D + row] = m, part[P::kRows * (D + 1) + row] = l;
       }
-      if (!whole) {
-        open_unit[slot] = pc.unit;
-        open_first[slot] = block_of(pc.base);
-        open_n[slot] = block_of(pc.base + pc.items - 1) - open_first[slot] + 1;
-      }
+    }
+    if (!whole) {
+      open_unit[slot] = pc.unit;
+      open_first[slot] = block_of(pc.base);
+      open_n[slot] = block_of(pc.base + pc.items - 1) - open_first[slot] + 1;
     }
   }
   // ---- joining the blocks' parts: the last block of a unit to arrive does it
+  if (open_unit[0] < 0 && open_unit[1] < 0) return;
   __syncthreads();
   if (tid < 2 && open_unit[tid] >= 0) {
-    __threadfence();
     int32_t* t = a.tickets + open_unit[tid];
     int before;
     asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(t) : "memory");
     last_s[tid] = before == open_n[tid] - 1;
     if (last_s[tid]) *t = 0;
-    __threadfence();
   }
   __syncthreads();
+#pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
     const int unit = slot ? open_unit[1] : open_unit[0], n = slot ? open_n[1] : open_n[0], first = slot ? open_first[1] : open_first[0];
     if (unit < 0 || !last_s[slot]) continue;
-    const int rows = rows_of(a, unit);
-    for (int idx = tid; idx < rows * (D / 4); idx += 32 * NW) {
-      const int row = idx / (D / 4), ch = idx % (D / 4) * 4;
+    const Unit ru = unit_at(a, unit);
+    for (int row = warp; row < ru.rows; row += NW) {
       // the unit's first block wrote it as the unit that goes on, the others as the one that began before
-      auto part = [&](int i) { return a.parts + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * P::kFloats; };
-      float M = -INFINITY;
-      for (int i = 0; i < n; ++i) M = fmaxf(M, __ldcg(part(i) + P::kRows * D + row));
-      float4 o = make_float4(0, 0, 0, 0);
-      float l = 0.0f;
-      for (int i = 0; i < n; ++i) {
-        const float* src = part(i);
-        const float f = M == -INFINITY ? 0.0f : ex2(__ldcg(src + P::kRows * D + row) - M);
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(src + row * D + ch));
-        o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
-        l = fmaf(f, __ldcg(src + P::kRows * (D + 1) + row), l);
-      }
-      const float f = l > 0.0f ? 1.0f / l : 0.0f;
-      put4(a, unit, row, D, ch, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
-      if (ch == 0) put_lse(a, unit, row, M, l);
+      auto part = [&](int j) { return a.parts + ((int64_t)(first + j) * 2 + (j == 0 ? 1 : 0)) * P::kFloats; };
+      float4 o;
+      float m, l;
+      const int ch = 4 * lane % D;
+      join_row(
+          n, lane, [&](int j) { return __ldcg(part(j) + P::kRows * D + row); },
+          [&](int j) { return __ldcg(part(j) + P::kRows * (D + 1) + row); },
+          [&](int j) { return __ldcg(reinterpret_cast<const float4*>(part(j) + row * D + ch)); }, o, m, l);
+      const int64_t at = row_at(a, ru, row);
+      if (4 * lane < D) put4(a, at * D + ch, scaled(o, l));
+      if (lane == 0) put_lse(a, at, m, l);
     }
   }
 }
@@ -792,11 +845,11 @@ extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, c
                    geo.chunk, geo.n_chunks};
   cudaStream_t cs = (cudaStream_t)stream;
   if (cache->head_dim == 128) {
-    if (prec) return launch<128, 1, true, 11, 4>(a, geo.grid, cs);
-    if (geo.nt == 2) return launch<128, 2, false, 8, 5>(a, geo.grid, cs);
-    return launch<128, 1, false, 12, 3>(a, geo.grid, cs);
+    if (prec) return launch<128, 1, true, 11, 2>(a, geo.grid, cs);
+    if (geo.nt == 2) return launch<128, 2, false, 8, 2>(a, geo.grid, cs);
+    return launch<128, 1, false, 8, 2>(a, geo.grid, cs);
   }
-  if (prec) return launch<64, 1, true, 11, 8>(a, geo.grid, cs);
-  if (geo.nt == 2) return launch<64, 2, false, 8, 10>(a, geo.grid, cs);
-  return launch<64, 1, false, 12, 6>(a, geo.grid, cs);
+  if (prec) return launch<64, 1, true, 11, 4>(a, geo.grid, cs);
+  if (geo.nt == 2) return launch<64, 2, false, 8, 4>(a, geo.grid, cs);
+  return launch<64, 1, false, 8, 4>(a, geo.grid, cs);
 }

@@ -1,4 +1,13 @@
 // Page selection of the 4-bit paged cache (rdkv_q4_select).
+//
+//   score(page) = max over the G query heads of sum_c max(q_c lo_c, q_c hi_c)
+//               = max over heads of (max(q, 0) . hi + min(q, 0) . lo)
+//
+// Two kernels.  score_kernel takes the sums as tensor-core products (pages on M, the group's heads on N,
+// the 2 D bounds on K), each within eps of the exact sum; pick_kernel finds, per (sequence, query token, KV
+// head), an interval around the n-th best score, takes what lies above it by more than the error, and sums
+// only the few pages within the error again, to twice fp32's precision, so that the order next to the
+// border is the exact one.
 #include "q4.cuh"
 
 namespace rdkv {
@@ -8,77 +17,291 @@ struct SelectArgs {
   View c;
   const void* q;
   int32_t* sel;
-  double* score;  // [rows][page_stride]
+  float* score;  // [rows][page_stride]
+  float* error;  // [rows][tiles]: bound of a tile's scores' errors
+  int32_t* list;  // [rows][page_stride]: pages near the border
+  float2* value;  // [rows][page_stride]: their sums, high and low part
   int64_t q_stride;
-  int dtype, n_q, G, D, keep, first, last;
+  int dtype, n_q, G, keep, first, last, tiles;
 };
 
-// One block per (sequence, query token, KV head): the scores in 64 bits, then the best page again and
-// again until enough are kept.
-__global__ void __launch_bounds__(256) select_kernel(SelectArgs a) {
-  __shared__ double best_s[8];
-  __shared__ int arg_s[8], got_s;
-  const int h = blockIdx.x % a.c.h_kv, bt = blockIdx.x / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q, tid = threadIdx.x;
-  const int warp = tid / 32, lane = tid % 32;
-  const int seen = held_tokens(a.c, b) - a.n_q + t + 1, P = seen > 0 ? ceil_div(seen, kPage) : 0;
-  int32_t* sel = a.sel + (int64_t)blockIdx.x * a.keep;
-  if (P <= a.keep) {
-    for (int i = tid; i < a.keep; i += 256) sel[i] = i < P ? i : -1;
-    return;
-  }
-  double* score = a.score + (int64_t)blockIdx.x * a.c.page_stride;
-  const int64_t qrow = ((int64_t)b * a.n_q + t) * a.q_stride + (int64_t)h * a.G * a.D;
-  for (int p = warp; p < P; p += 8) {
-    const int phys = a.c.page_table[(int64_t)b * a.c.page_stride + p];
-    double best = -INFINITY;
-    if (phys < 0 || phys >= a.c.n_pages) {
-      if (lane == 0) raise(a.c, RDKV_ERR_INVALID_ARG);
-    } else {
-      const __half* e = a.c.bounds + ((int64_t)phys * a.c.h_kv + h) * 2 * a.D;
-      for (int g = 0; g < a.G; ++g) {
-        double s = 0;
-        for (int c = lane; c < a.D; c += 32) {
-          const double x = load_q(a.q, qrow + g * a.D + c, a.dtype);
-          s += x * (double)__half2float(e[x > 0 ? a.D + c : c]);
-        }
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        best = fmax(best, s);
+constexpr int kTilePages = 16;
+constexpr int kScoreWarps = 4;
+
+// Pages of row (b, t) that hold a key its query token sees.
+__device__ __forceinline__ int pages_seen(const SelectArgs& a, int b, int t) {
+  const int seen = held_tokens(a.c, b) - a.n_q + t + 1;
+  return seen > 0 ? ceil_div(seen, kPage) : 0;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_of(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+  const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// One warp a tile of 16 pages: every bound is read once, 16 bytes a lane and load, all in flight together.
+template <int D>
+__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(SelectArgs a) {
+  constexpr int NC = D / 32;
+  const int lane = threadIdx.x % 32, g = lane / 4, qd = lane % 4;
+  const int row = blockIdx.y, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
+  const int P = pages_seen(a, b, t);
+  if (P <= a.keep) return;  // every page is kept
+  const int n_tiles = ceil_div(P, kTilePages);
+  int tile = blockIdx.x * kScoreWarps + threadIdx.x / 32;
+  if (tile >= n_tiles) return;
+  // B: head g of the group, its channels 32 i + 8 qd .. + 7, positive and negative parts and magnitudes
+  uint32_t pos[NC][4], neg[NC][4], mag[NC][4];
+  float back;
+  {
+    float x[NC][8], top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+    if (g < a.G) {
+      const int64_t at = (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 8 * qd;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        if (a.dtype == RDKV_F16) Eight<__half>::load(static_cast<const __half*>(a.q) + at + 32 * i, x[i]);
+        else if (a.dtype == RDKV_BF16) Eight<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(a.q) + at + 32 * i, x[i]);
+        else Eight<float>::load(static_cast<const float*>(a.q) + at + 32 * i, x[i]);
       }
     }
-    if (p < a.first || p >= P - a.last) best = INFINITY;
-    if (lane == 0) score[p] = best;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // the head times 2^s, its largest value in [1, 2)
+    const int s = top > 0.0f ? max(-100, min(100, 127 - (int)(__float_as_uint(top) >> 23))) : 0;
+    const float up = __uint_as_float((uint32_t)(s + 127) << 23);
+    back = __uint_as_float((uint32_t)(127 - s) << 23);
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float y0 = x[i][2 * j] * up, y1 = x[i][2 * j + 1] * up;
+        pos[i][j] = half2_of(fmaxf(y0, 0.0f), fmaxf(y1, 0.0f));
+        neg[i][j] = half2_of(fminf(y0, 0.0f), fminf(y1, 0.0f));
+        // 2^-12 more: 2^-13 of the product then covers what fp16's subnormals drop (at most 2^-25 a channel)
+        mag[i][j] = half2_of(fabsf(y0) + 0.000244140625f, fabsf(y1) + 0.000244140625f);
+      }
+  }
+  // The products' error against the exact sum, relative to the sum of the magnitudes: at most 16 sums of 17
+  // terms, each cut 2^-22 below the largest: below 2^-13.8; the queries' own rounding is none for fp16
+  // and bf16, and 2^-11 for fp32.
+  const float rel = a.dtype == RDKV_F32 ? 0.0006103515625f + 0.0001220703125f : 0.0001220703125f;
+  const float back0 = __shfl_sync(0xffffffffu, back, 8 * qd), back1 = __shfl_sync(0xffffffffu, back, 8 * qd + 4);
+  for (; tile < n_tiles; tile += gridDim.x * kScoreWarps) {
+    uint4 lo[2][NC], hi[2][NC];
+    bool bad[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int p = min(tile * kTilePages + 8 * r + g, P - 1);
+      const int phys = __ldg(a.c.page_table + (int64_t)b * a.c.page_stride + p);
+      bad[r] = phys < 0 || phys >= a.c.n_pages;
+      if (bad[r] && qd == 0) raise(a.c, RDKV_ERR_INVALID_ARG);
+      const uint4* e = reinterpret_cast<const uint4*>(a.c.bounds + ((int64_t)(bad[r] ? 0 : phys) * a.c.h_kv + h) * 2 * D) + qd;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) lo[r][i] = __ldg(e + 4 * i), hi[r][i] = __ldg(e + D / 8 + 4 * i);
+    }
+    float s[4] = {}, m[4] = {};
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t l0[4] = {lo[0][i].x, lo[0][i].y, lo[0][i].z, lo[0][i].w}, l1[4] = {lo[1][i].x, lo[1][i].y, lo[1][i].z, lo[1][i].w};
+      const uint32_t h0[4] = {hi[0][i].x, hi[0][i].y, hi[0][i].z, hi[0][i].w}, h1[4] = {hi[1][i].x, hi[1][i].y, hi[1][i].z, hi[1][i].w};
+      uint32_t b0[4], b1[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        b0[j] = max2(l0[j] & 0x7fff7fffu, h0[j] & 0x7fff7fffu);
+        b1[j] = max2(l1[j] & 0x7fff7fffu, h1[j] & 0x7fff7fffu);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        mma_f16(s, h0[j], h1[j], h0[j + 1], h1[j + 1], pos[i][j], pos[i][j + 1]);
+        mma_f16(s, l0[j], l1[j], l0[j + 1], l1[j + 1], neg[i][j], neg[i][j + 1]);
+        mma_f16(m, b0[j], b1[j], b0[j + 1], b1[j + 1], mag[i][j], mag[i][j + 1]);
+      }
+    }
+    // rows g, g + 8 are pages, columns 2 qd, 2 qd + 1 heads
+    float err = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float x = -INFINITY;
+      if (2 * qd < a.G) x = s[2 * r] * back0, err = fmaxf(err, m[2 * r] * back0);
+      if (2 * qd + 1 < a.G) x = fmaxf(x, s[2 * r + 1] * back1), err = fmaxf(err, m[2 * r + 1] * back1);
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      const int p = tile * kTilePages + 8 * r + g;
+      if (qd == 0 && p < P)
+        a.score[(int64_t)row * a.c.page_stride + p] = bad[r] || !(x > -FLT_MAX) ? -FLT_MAX : fminf(x, FLT_MAX);
+    }
+    for (int d = 16; d; d >>= 1) err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, d));
+    if (lane == 0) a.error[(int64_t)row * a.tiles + tile] = err * rel;
+  }
+}
+
+// Sums of a high and a low part (about twice fp32's precision).
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return make_float2(s, (a - (s - t)) + (b - t));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  const float2 s = two_sum(a.x, b.x);
+  const float lo = s.y + (a.y + b.y), hi = s.x + lo;
+  return make_float2(hi, lo - (hi - s.x));
+}
+__device__ __forceinline__ bool above(float2 a, float2 b) { return a.x > b.x || (a.x == b.x && a.y > b.y); }
+
+constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
+constexpr int kPickShared = 12288;  // scores that are kept in shared memory (longer rows are read through L2)
+
+// Sum over the block, for every thread.
+__device__ __forceinline__ int3 block_sum(int3 v, int3* part) {
+  v.x = __reduce_add_sync(0xffffffffu, v.x), v.y = __reduce_add_sync(0xffffffffu, v.y), v.z = __reduce_add_sync(0xffffffffu, v.z);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+  __syncthreads();
+  const int3 w = part[threadIdx.x % kPickWarps];
+  const bool once = threadIdx.x % 32 < kPickWarps;
+  return make_int3(__reduce_add_sync(0xffffffffu, once ? w.x : 0), __reduce_add_sync(0xffffffffu, once ? w.y : 0),
+                   __reduce_add_sync(0xffffffffu, once ? w.z : 0));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a) {
+  extern __shared__ float score_s[];
+  __shared__ float part_f[kPickWarps][3];
+  __shared__ int3 part[kPickWarps];
+  __shared__ int list_n;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int row = blockIdx.x, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
+  const int P = pages_seen(a, b, t);
+  int32_t* sel = a.sel + (int64_t)row * a.keep;
+  if (P <= a.keep) {
+    for (int i = tid; i < a.keep; i += kPickThreads) sel[i] = i < P ? i : -1;
+    return;
+  }
+  float* score = a.score + (int64_t)row * a.c.page_stride;
+  const int lo_p = a.first, hi_p = P - a.last, want = a.keep - a.first - a.last;  // of hi_p - lo_p > want pages
+  float top = -INFINITY, low = INFINITY, eps = 0.0f;
+  const bool here = P <= kPickShared;
+  for (int p = tid; p < P; p += kPickThreads) {
+    const float s = __ldcg(score + p);
+    if (here) score_s[p] = s;
+    if (p >= lo_p && p < hi_p) top = fmaxf(top, s), low = fminf(low, s);
+  }
+  for (int i = tid; i < ceil_div(P, kTilePages); i += kPickThreads) eps = fmaxf(eps, __ldcg(a.error + (int64_t)row * a.tiles + i));
+  for (int d = 16; d; d >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
+    eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, d));
+  }
+  if (lane == 0) part_f[warp][0] = top, part_f[warp][1] = low, part_f[warp][2] = eps;
+  if (tid == 0) list_n = 0;
+  __syncthreads();
+  for (int w = 0; w < kPickWarps; ++w) top = fmaxf(top, part_f[w][0]), low = fminf(low, part_f[w][1]), eps = fmaxf(eps, part_f[w][2]);
+  if (!(eps <= FLT_MAX)) eps = FLT_MAX;
+  if (here) score = score_s;
+  if (want > 0) {
+    // [lo, hi) holds the want-th best score: at least `want` are >= lo, fewer are >= hi
+    float lo = low, hi = top < FLT_MAX ? nextafterf(top, INFINITY) : INFINITY;
+    for (int turn = 0; turn < 40; ++turn) {
+      const float m1 = 0.75f * lo + 0.25f * fminf(hi, FLT_MAX), m2 = 0.5f * lo + 0.5f * fminf(hi, FLT_MAX),
+                  m3 = 0.25f * lo + 0.75f * fminf(hi, FLT_MAX);
+      if (hi - lo <= eps || !(m2 > lo && m2 < hi)) break;
+      int3 n = make_int3(0, 0, 0);
+      for (int p = lo_p + tid; p < hi_p; p += kPickThreads) {
+        const float s = score[p];
+        n.x += s >= m1, n.y += s >= m2, n.z += s >= m3;
+      }
+      n = block_sum(n, part);
+      if (n.z >= want) lo = fmaxf(lo, m3);
+      else if (n.y >= want) lo = m2, hi = m3 > m2 ? m3 : hi;
+      else if (n.x >= want) lo = fmaxf(lo, m1), hi = m2;
+      else hi = m1 > lo ? m1 : m2;
+    }
+    // in: above the interval by more than twice the error; near: within it
+    const float sure = hi + 2.0f * eps, out = lo - 2.0f * eps;
+    int3 n = make_int3(0, 0, 0);
+    for (int p = lo_p + tid; p < hi_p; p += kPickThreads) {
+      const float s = score[p];
+      const bool in = s > sure, near = !in && s >= out;
+      n.x += in, n.y += near;
+      if (near) a.list[(int64_t)row * a.c.page_stride + atomicAdd(&list_n, 1)] = p;
+      score[p] = in ? INFINITY : near ? 0.0f : -INFINITY;
+    }
+    n = block_sum(n, part);
+    const int need = want - n.x, near = n.y;
+    const int32_t* list = a.list + (int64_t)row * a.c.page_stride;
+    if (near <= need) {
+      for (int i = tid; i < near; i += kPickThreads) score[list[i]] = INFINITY;
+    } else {
+      // their sums again, a page a warp
+      float2* value = a.value + (int64_t)row * a.c.page_stride;
+      for (int i = warp; i < near; i += kPickWarps) {
+        const int phys = __ldg(a.c.page_table + (int64_t)b * a.c.page_stride + list[i]);
+        float2 best = make_float2(-INFINITY, 0.0f);
+        if (phys >= 0 && phys < a.c.n_pages) {
+          const __half* e = a.c.bounds + ((int64_t)phys * a.c.h_kv + h) * 2 * D;
+          float l[D / 32], u[D / 32];
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) l[c] = __half2float(e[32 * c + lane]), u[c] = __half2float(e[D + 32 * c + lane]);
+#pragma unroll 1
+          for (int g = 0; g < a.G; ++g) {
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              const float x = load_q(a.q, (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 32 * c + lane, a.dtype);
+              const float y = x > 0.0f ? u[c] : l[c], p = x * y;
+              sum = add2(sum, make_float2(p, fmaf(x, y, -p)));
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+              sum = add2(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, d), __shfl_xor_sync(0xffffffffu, sum.y, d)));
+            if (above(sum, best)) best = sum;
+          }
+        }
+        if (lane == 0) value[i] = best;
+      }
+      __syncthreads();
+      for (int i = tid; i < near; i += kPickThreads) {
+        const float2 v = value[i];
+        const int p = list[i];
+        int before = 0;
+        for (int j = 0; j < near; ++j) before += above(value[j], v) || (!above(v, value[j]) && list[j] < p);
+        if (before < need) score[p] = INFINITY;
+      }
+    }
   }
   __syncthreads();
-  // the kept pages are marked by NaN, then listed in order
-  for (int n = 0; n < a.keep; ++n) {
-    double best = -INFINITY;
-    int arg = INT32_MAX;
-    for (int p = tid; p < P; p += 256) {
-      const double s = score[p];
-      if (s > best || (s == best && p < arg)) best = s, arg = p;
-    }
-    for (int o = 16; o; o >>= 1) {
-      const double s = __shfl_xor_sync(0xffffffffu, best, o);
-      const int p = __shfl_xor_sync(0xffffffffu, arg, o);
-      if (s > best || (s == best && p < arg)) best = s, arg = p;
-    }
-    if (lane == 0) best_s[warp] = best, arg_s[warp] = arg;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < 8; ++w)
-        if (best_s[w] > best || (best_s[w] == best && arg_s[w] < arg)) best = best_s[w], arg = arg_s[w];
-      if (arg < P) score[arg] = NAN;
-    }
-    __syncthreads();
+  // the kept pages in order: each thread its run of pages
+  const int per = ceil_div(P, kPickThreads), p0 = min(P, tid * per), p1 = min(P, p0 + per);
+  auto kept = [&](int p) { return p < lo_p || p >= hi_p || (want > 0 && score[p] == INFINITY); };
+  int n = 0;
+  for (int p = p0; p < p1; ++p) n += kept(p);
+  int at = n;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, at, d);
+    if (lane >= d) at += x;
   }
-  if (tid == 0) {
-    int n = 0;
-    for (int p = 0; p < P && n < a.keep; ++p)
-      if (isnan(score[p])) sel[n++] = p;
-    got_s = n;
-  }
+  if (lane == 31) part[warp].x = at;
   __syncthreads();
-  for (int i = got_s + tid; i < a.keep; i += 256) sel[i] = -1;
+  at -= n;
+  for (int w = 0; w < warp; ++w) at += part[w].x;
+  for (int p = p0; p < p1 && n > 0; ++p)
+    if (kept(p) && at < a.keep) sel[at++] = p;
 }
 
 }  // namespace q4
@@ -87,9 +310,27 @@ __global__ void __launch_bounds__(256) select_kernel(SelectArgs a) {
 using namespace rdkv;
 using namespace rdkv::q4;
 
+namespace {
+struct SelectGeometry {
+  int64_t rows;
+  int tiles;
+  size_t error_at, list_at, value_at, bytes;
+};
+SelectGeometry select_geometry(const rdkv_q4_cache* c, int n_q) {
+  SelectGeometry o;
+  o.rows = (int64_t)c->batch * n_q * c->h_kv;
+  o.tiles = ceil_div(c->page_stride, kTilePages);
+  const int64_t pages = o.rows * c->page_stride;
+  o.value_at = 0;
+  o.error_at = (size_t)align_up(8 * pages, 256);
+  o.list_at = o.error_at + (size_t)align_up(4 * o.rows * o.tiles, 256);
+  o.bytes = o.list_at + 2 * (size_t)align_up(4 * pages, 256);
+  return o;
+}
+}  // namespace
+
 extern "C" size_t rdkv_q4_select_workspace_bytes(const rdkv_q4_cache* cache, int32_t h_q, int32_t n_q) {
-  if (check_queries(cache, h_q, n_q) != RDKV_OK) return 0;
-  return (size_t)align_up((int64_t)cache->batch * n_q * cache->h_kv * cache->page_stride * 8, 256);
+  return check_queries(cache, h_q, n_q) == RDKV_OK ? select_geometry(cache, n_q).bytes : 0;
 }
 
 extern "C" rdkv_status rdkv_q4_select(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride,
@@ -100,12 +341,26 @@ extern "C" rdkv_status rdkv_q4_select(const rdkv_q4_cache* cache, int32_t dtype,
   RDKV_REQUIRE(cache->bounds && sel, RDKV_ERR_INVALID_ARG, "NULL bounds or selection");
   RDKV_REQUIRE(n_keep >= 1 && n_first >= 0 && n_last >= 0 && (int64_t)n_first + n_last <= n_keep, RDKV_ERR_INVALID_ARG,
                "n_keep=%d n_first=%d n_last=%d", n_keep, n_first, n_last);
-  const size_t need = rdkv_q4_select_workspace_bytes(cache, h_q, n_q);
-  RDKV_REQUIRE(ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= need, RDKV_ERR_WORKSPACE,
-               "selection workspace too small (%zu < %zu) or unaligned", ws_bytes, need);
-  SelectArgs a{view_of(cache), q, sel, static_cast<double*>(ws), q_stride, dtype, n_q, h_q / cache->h_kv, cache->head_dim,
-               n_keep, n_first, n_last};
-  select_kernel<<<(unsigned)((int64_t)cache->batch * n_q * cache->h_kv), 256, 0, (cudaStream_t)stream>>>(a);
-  RDKV_CHECK_LAUNCH("4-bit cache selection");
+  const SelectGeometry geo = select_geometry(cache, n_q);
+  RDKV_REQUIRE(geo.rows <= 65535, RDKV_ERR_UNSUPPORTED, "more than 65,535 (sequence, query token, KV head) rows");
+  RDKV_REQUIRE(ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= geo.bytes, RDKV_ERR_WORKSPACE,
+               "selection workspace too small (%zu < %zu) or unaligned", ws_bytes, geo.bytes);
+  char* w = static_cast<char*>(ws);
+  const SelectArgs a{view_of(cache), q, sel,
+                     reinterpret_cast<float*>(w + geo.list_at + align_up(4 * geo.rows * cache->page_stride, 256)),
+                     reinterpret_cast<float*>(w + geo.error_at), reinterpret_cast<int32_t*>(w + geo.list_at),
+                     reinterpret_cast<float2*>(w + geo.value_at), q_stride, dtype, n_q, h_q / cache->h_kv, n_keep, n_first, n_last,
+                     geo.tiles};
+  cudaStream_t cs = (cudaStream_t)stream;
+  // a tile a warp, as far as about four blocks an SM go; warps take further tiles in turn
+  const int64_t most = std::max<int64_t>(1, 8LL * num_sms() / geo.rows);
+  const dim3 grid((unsigned)std::min<int64_t>(ceil_div(geo.tiles, kScoreWarps), most), (unsigned)geo.rows);
+  const size_t smem = 4 * (size_t)std::min(cache->page_stride, kPickShared);
+  if (cache->head_dim == 128) score_kernel<128><<<grid, 32 * kScoreWarps, 0, cs>>>(a);
+  else score_kernel<64><<<grid, 32 * kScoreWarps, 0, cs>>>(a);
+  RDKV_CHECK_LAUNCH("4-bit cache page scores");
+  if (cache->head_dim == 128) pick_kernel<128><<<(unsigned)geo.rows, kPickThreads, smem, cs>>>(a);
+  else pick_kernel<64><<<(unsigned)geo.rows, kPickThreads, smem, cs>>>(a);
+  RDKV_CHECK_LAUNCH("4-bit cache page selection");
   return RDKV_OK;
 }
