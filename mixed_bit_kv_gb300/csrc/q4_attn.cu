@@ -16,8 +16,10 @@
 // codes an operand register; the units are undone in fp32.  Each group's logits accumulate on their own
 // and take the token's scale in fp32; the zeros' part is one more product, of the queries' group sums
 // (fp16 high part and remainder).  A weight times its values' scale is rounded to fp16 once; for fp32
-// outputs (PREC) the product keeps a remainder too, and the queries a low part in the rows 8 .. 15 of
-// the same product.
+// outputs (PREC) the product keeps a remainder too.  With one row set (NT = 1) the rows 8 .. 15 of the
+// logits' products hold the queries' low parts, which fp32 queries need.
+#include <atomic>
+
 #include "q4.cuh"
 
 namespace rdkv {
@@ -84,6 +86,11 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)), "l"(*reinterpret_cast<const uint64_t*>(&c)));
   return *reinterpret_cast<const float2*>(&d);
 }
+__device__ __forceinline__ float2 add2f(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&c));
   return *reinterpret_cast<const uint32_t*>(&d);
@@ -119,6 +126,18 @@ struct Pairs {
 __device__ __forceinline__ Pairs code_pairs(uint32_t w) {
   const uint32_t u = w >> 8;
   return Pairs{w & 0x000f000fu, w & 0x00f000f0u, u & 0x000f000fu, u & 0x00f000f0u};
+}
+
+// The same codes less eight, exactly: 1024 + code (and 1024 + 16 code) are the fp16 values of the code bits
+// under the exponent of 1024.
+__device__ __forceinline__ uint32_t minus(uint32_t w, uint32_t one) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&one));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ Pairs centred_pairs(uint32_t w) {
+  const Pairs p = code_pairs(w);
+  constexpr uint32_t k1024 = 0x64006400u, k1032 = 0x64086408u, k1152 = 0x64806480u;
+  return Pairs{minus(p.a | k1024, k1032), minus(p.b | k1024, k1152), minus(p.c | k1024, k1032), minus(p.d | k1024, k1152)};
 }
 
 // A piece of a unit: ROWS x D sums and each row's reference (base 2) and sum of weights.
@@ -170,14 +189,16 @@ __device__ __forceinline__ void put_lse(const AttnArgs& a, int64_t row, float m,
 // One warp's running state over the pages of one unit.
 template <int D, int NT, bool PREC>
 struct Warp {
-  static constexpr int NG = D / kGroup, kQ = NT == 2 || PREC ? 2 : 1;
+  static constexpr int NG = D / kGroup;
   using L = Layout<D>;
-  uint32_t q[kQ][NG][4];  // A registers: rows g, and rows g + 8 (second half of the chunk, or the low parts)
-  uint32_t qz[NT];        // A registers of the zeros' product
+  uint32_t q[2][NG][4];  // A registers: rows g, and rows g + 8 (the chunk's second half, or the low parts of the first)
+  uint32_t qz[2];        // A registers of the zeros' product
   float scale[NT];        // 2^(15 - s): a row's logits are held times 2^(s - 15)
   float ref[NT], l[NT];   // the running maximum (base 2) and this lane's share of the sum
-  float o[NT][NG][2][4], oz[NT][4];
-  int off;                // weights are held times 2^off
+  float o[NT][NG][2][4];
+  float oz[NT][PREC ? NG : 2];  // the zeros' part: by row g < NG = group and columns, or (PREC) this lane's row's, by group
+  int off;                      // weights are held times 2^off
+  static constexpr int kMaxOff = PREC ? 23 : 11;
 
   // This lane's channels of the unit's query rows (rows past the last: zero).
   __device__ __forceinline__ static void fetch(const AttnArgs& a, const Unit& un, int g, int qd, float (&x)[NT][NG][8]) {
@@ -228,7 +249,7 @@ struct Warp {
           // pairs 1 and 3 meet codes that stand for sixteen times as much
           const float f = j & 1 ? 0.0625f : 1.0f, y0 = x[i][2 * j] * f, y1 = x[i][2 * j + 1] * f;
           q[n][i][j] = pack2(y0, y1);
-          if constexpr (PREC) q[1][i][j] = rest2(y0, y1, q[0][i][j]);
+          if constexpr (NT == 1) q[1][i][j] = rest2(y0, y1, q[0][i][j]);
         }
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
@@ -241,6 +262,7 @@ struct Warp {
         hi[i] = pack2(sum[2 * i], sum[2 * i + 1]);
         lo[i] = rest2(sum[2 * i], sum[2 * i + 1], hi[i]);
       }
+      if constexpr (NT == 1) qz[1] = 0u;
       if constexpr (NG == 4) qz[n] = qd == 0 ? hi[0] : qd == 1 ? hi[1] : qd == 2 ? lo[0] : lo[1];
       else qz[n] = qd == 0 ? hi[0] : qd == 1 ? lo[0] : 0u;
       ref[n] = -INFINITY;
@@ -250,9 +272,9 @@ struct Warp {
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[n][i][j / 4][j % 4] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) oz[n][j] = 0.0f;
+      for (int j = 0; j < (PREC ? NG : 2); ++j) oz[n][j] = 0.0f;
     }
-    off = 11;
+    off = kMaxOff;
   }
 
   // Row sums and weighted sums times f, each lane's row's own.
@@ -265,7 +287,12 @@ struct Warp {
 #pragma unroll
       for (int m = 0; m < 2; ++m)
         o[n][i][m][0] *= f0, o[n][i][m][1] *= f1, o[n][i][m][2] *= f0, o[n][i][m][3] *= f1;
-    oz[n][0] *= f0, oz[n][1] *= f1, oz[n][2] *= f0, oz[n][3] *= f1;
+    if constexpr (PREC) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i) oz[n][i] *= f;
+    } else {
+      oz[n][0] *= f0, oz[n][1] *= f1;
+    }
   }
 
   // One page.  kTail: its last tokens may hold nothing (live of them do; what the others hold is arbitrary
@@ -275,7 +302,8 @@ struct Warp {
     constexpr float kK = 512.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
     {  // The weights' exponent follows the largest value scale met, so that weight times scale stays in
        // fp16's range: with the weight at most 2^(4 + off) and the scale below 2^(e + 1), the product is
-       // below 2^13, and off <= 11 keeps the weight itself in range.
+       // below 2^13, and off <= 11 keeps the weight itself in range.  (PREC: weights at most 2^off, products
+       // below 2^9.)
       const int lane = 4 * g + qd;
       uint32_t sw[NG], top = 0;
       lds_groups<NG>(k + L::kVScales + lane * NG * 4, sw);
@@ -306,7 +334,7 @@ struct Warp {
         lds_groups<NG>(k + L::kKScales + (tok / 2 + qd) * NG * 4, sw);
         const uint32_t zw = reinterpret_cast<const uint32_t*>(k + L::kKZeros)[(tok + g) * (NG / 2) + (NG == 4 ? qd & 1 : 0)];
         float z[4];
-        mma8z(z, qz[0], NT == 2 ? qz[NT - 1] : 0u, zw);
+        mma8z(z, qz[0], qz[1], zw);
         float2 s[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[n] = make_float2(0.0f, 0.0f);
@@ -314,8 +342,8 @@ struct Warp {
         for (int i = 0; i < NG; ++i) {
           const Pairs p = code_pairs(w[i]);
           float c[4];
-          mma16z(c, q[0][i][0], kQ == 2 ? q[kQ - 1][i][0] : 0u, q[0][i][1], kQ == 2 ? q[kQ - 1][i][1] : 0u, p.a, p.b);
-          mma16(c, q[0][i][2], kQ == 2 ? q[kQ - 1][i][2] : 0u, q[0][i][3], kQ == 2 ? q[kQ - 1][i][3] : 0u, p.c, p.d);
+          mma16z(c, q[0][i][0], q[1][i][0], q[0][i][1], q[1][i][1], p.a, p.b);
+          mma16(c, q[0][i][2], q[1][i][2], q[0][i][3], q[1][i][3], p.c, p.d);
           const float2 f = unpack2(sw[i]);
           if constexpr (PREC) c[0] += c[2], c[1] += c[3];
           s[0] = fma2(f, make_float2(c[0], c[1]), s[0]);
@@ -331,13 +359,14 @@ struct Warp {
         }
       }
       // a row's reference rises when a logit passes it by more than 4, so that weights stay at most 2^4
+      // (PREC: whenever one passes it)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float m = fmaxf(u[n][0].x, u[n][0].y);
 #pragma unroll
         for (int t = 1; t < 4; ++t) m = fmaxf(m, fmaxf(u[n][t].x, u[n][t].y));
         m *= scale[n];
-        if (__any_sync(0xffffffffu, m > ref[n] + 4.0f)) {
+        if (__any_sync(0xffffffffu, m > ref[n] + (PREC ? 0.0f : 4.0f))) {
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
           m = fmaxf(m, ref[n]);
@@ -346,60 +375,111 @@ struct Warp {
           rescale(n, f, qd);
         }
       }
+      // the weights, as fp16 parts and remainders, in the order of the values' products: 16 tokens a step
+      uint32_t hi[NT][2][2], lo[NT][2][2], s0[2][NG], s1[2][NG], w0[2][NG], w1[2][NG];
+      float p[NT][2][4], cz[NT][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {  // 16 tokens
-        float p[NT][4];
+      for (int t = 0; t < 2; ++t) {
+        const int p0 = t32 / 2 + 8 * t + qd, p1 = p0 + 4;  // this lane's token pairs
+        lds_groups<NG>(k + L::kVCodes + (p0 * 8 + g) * NG * 4, w0[t]);
+        lds_groups<NG>(k + L::kVCodes + (p1 * 8 + g) * NG * 4, w1[t]);
+        lds_groups<NG>(k + L::kVScales + p0 * NG * 4, s0[t]);
+        lds_groups<NG>(k + L::kVScales + p1 * NG * 4, s1[t]);
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (kTail) {
+          keep0 = (2 * p0 < live ? 0xffffu : 0u) | (2 * p0 + 1 < live ? 0xffff0000u : 0u);
+          keep1 = (2 * p1 < live ? 0xffffu : 0u) | (2 * p1 + 1 < live ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int i = 0; i < NG; ++i) s0[t][i] &= keep0, s1[t][i] &= keep1;
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float r = (float)off - (ref[n] == -INFINITY ? 0.0f : ref[n]);
           const float2 y0 = fma2(u[n][2 * t], make_float2(scale[n], scale[n]), make_float2(r, r));
           const float2 y1 = fma2(u[n][2 * t + 1], make_float2(scale[n], scale[n]), make_float2(r, r));
-          p[n][0] = ex2(y0.x), p[n][1] = ex2(y0.y), p[n][2] = ex2(y1.x), p[n][3] = ex2(y1.y);
-          l[n] += (p[n][0] + p[n][1]) + (p[n][2] + p[n][3]);
+          float(&x)[4] = p[n][t];
+          x[0] = ex2(y0.x), x[1] = ex2(y0.y), x[2] = ex2(y1.x), x[3] = ex2(y1.y);
+          l[n] += (x[0] + x[1]) + (x[2] + x[3]);
         }
-        const int p0 = t32 / 2 + 8 * t + qd, p1 = p0 + 4;  // this lane's token pairs
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if (kTail) {
-          keep0 = (2 * p0 < live ? 0xffffu : 0u) | (2 * p0 + 1 < live ? 0xffff0000u : 0u);
-          keep1 = (2 * p1 < live ? 0xffffu : 0u) | (2 * p1 + 1 < live ? 0xffff0000u : 0u);
-        }
-        const uint32_t* zs = reinterpret_cast<const uint32_t*>(k + L::kVZeros);
-        const uint32_t z0 = g < NG ? zs[p0 * NG + g] & keep0 : 0u, z1 = g < NG ? zs[p1 * NG + g] & keep1 : 0u;
-        uint32_t hi[NT][2], lo[NT][2];
+        if constexpr (PREC) {  // the values' middles (zero + 8 scale), in fp32
+          uint32_t z0[NG], z1[NG];
+          lds_groups<NG>(k + L::kVZeros + p0 * NG * 4, z0);
+          lds_groups<NG>(k + L::kVZeros + p1 * NG * 4, z1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          hi[n][0] = pack2(p[n][0], p[n][1]), hi[n][1] = pack2(p[n][2], p[n][3]);
-          lo[n][0] = rest2(p[n][0], p[n][1], hi[n][0]), lo[n][1] = rest2(p[n][2], p[n][3], hi[n][1]);
-          mma16(oz[n], z0, 0u, z1, 0u, hi[n][0], hi[n][1]);
-          if constexpr (PREC) mma16(oz[n], z0, 0u, z1, 0u, lo[n][0], lo[n][1]);
-        }
-        uint32_t w0[NG], w1[NG], s0[NG], s1[NG];
-        lds_groups<NG>(k + L::kVCodes + (p0 * 8 + g) * NG * 4, w0);
-        lds_groups<NG>(k + L::kVCodes + (p1 * 8 + g) * NG * 4, w1);
-        lds_groups<NG>(k + L::kVScales + p0 * NG * 4, s0);
-        lds_groups<NG>(k + L::kVScales + p1 * NG * 4, s1);
-#pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          const Pairs x = code_pairs(w0[i]), y = code_pairs(w1[i]);
-          if (kTail) s0[i] &= keep0, s1[i] &= keep1;
+          for (int i = 0; i < NG; ++i) {
+            const float2 a0 = unpack2(z0[i] & keep0), a1 = unpack2(z1[i] & keep1), f0 = unpack2(s0[t][i]), f1 = unpack2(s1[t][i]);
+            const float(&x)[4] = p[0][t];
+            oz[0][i] += (x[0] * fmaf(8.0f, f0.x, a0.x) + x[1] * fmaf(8.0f, f0.y, a0.y)) +
+                        (x[2] * fmaf(8.0f, f1.x, a1.x) + x[3] * fmaf(8.0f, f1.y, a1.y));
+          }
+        } else {  // one product; rows g >= NG of its operand are zero
+          const uint32_t* zs = reinterpret_cast<const uint32_t*>(k + L::kVZeros) + g % NG;
+          const uint32_t z0 = zs[p0 * NG] & (g < NG ? keep0 : 0u), z1 = zs[p1 * NG] & (g < NG ? keep1 : 0u);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
+            const float(&x)[4] = p[n][t];
+            hi[n][t][0] = pack2(x[0], x[1]), hi[n][t][1] = pack2(x[2], x[3]);
+            lo[n][t][0] = rest2(x[0], x[1], hi[n][t][0]), lo[n][t][1] = rest2(x[2], x[3], hi[n][t][1]);
+            if (t == 0) mma16z(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
+            else mma16(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
+          }
+        }
+      }
+      // The tensor core cuts what it adds to an accumulator (it does not round), which the difference of the
+      // two large sums would show: its accumulators start at zero every turn, and the sums over the turns are
+      // rounded fp32 additions.  PREC: codes less eight and the high parts on a grid of 1/4 (11 bits below
+      // 2^9) make every product and sum of theirs an exact integer of that grid.
+      if constexpr (!PREC) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) oz[n][0] += cz[n][0], oz[n][1] += cz[n][1];
+      }
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        float c[NT][2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const Pairs x = PREC ? centred_pairs(w0[t][i]) : code_pairs(w0[t][i]);
+          const Pairs y = PREC ? centred_pairs(w1[t][i]) : code_pairs(w1[t][i]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint32_t b0, b1;
             if constexpr (PREC) {
-              const float2 f0 = unpack2(s0[i]), f1 = unpack2(s1[i]);
-              const float e0 = p[n][0] * f0.x, e1 = p[n][1] * f0.y, e2 = p[n][2] * f1.x, e3 = p[n][3] * f1.y;
-              const uint32_t b0 = pack2(e0, e1), b1 = pack2(e2, e3), c0 = rest2(e0, e1, b0), c1 = rest2(e2, e3, b1);
-              mma16(o[n][i][0], x.a, x.b, y.a, y.b, b0, b1);
-              mma16(o[n][i][1], x.c, x.d, y.c, y.d, b0, b1);
-              mma16(o[n][i][0], x.a, x.b, y.a, y.b, c0, c1);
-              mma16(o[n][i][1], x.c, x.d, y.c, y.d, c0, c1);
+              const float2 f0 = unpack2(s0[t][i]), f1 = unpack2(s1[t][i]);
+              const float e0 = p[n][t][0] * f0.x, e1 = p[n][t][1] * f0.y, e2 = p[n][t][2] * f1.x, e3 = p[n][t][3] * f1.y;
+              constexpr float kGrid = 3145728.0f;  // 1.5 2^21: its last place is 1/4
+              b0 = pack2(__fadd_rn(__fadd_rn(e0, kGrid), -kGrid), __fadd_rn(__fadd_rn(e1, kGrid), -kGrid));
+              b1 = pack2(__fadd_rn(__fadd_rn(e2, kGrid), -kGrid), __fadd_rn(__fadd_rn(e3, kGrid), -kGrid));
+              const uint32_t c0 = rest2(e0, e1, b0), c1 = rest2(e2, e3, b1);
+              if (t == 0) {
+                mma16z(c[n][0], x.a, x.b, y.a, y.b, c0, c1);
+                mma16z(c[n][1], x.c, x.d, y.c, y.d, c0, c1);
+              } else {
+                mma16(c[n][0], x.a, x.b, y.a, y.b, c0, c1);
+                mma16(c[n][1], x.c, x.d, y.c, y.d, c0, c1);
+              }
             } else {
               // weight times scale, rounded to fp16 once: the weight as an fp16 part and its remainder
-              const uint32_t b0 = hfma2(hi[n][0], s0[i], hmul2(lo[n][0], s0[i])), b1 = hfma2(hi[n][1], s1[i], hmul2(lo[n][1], s1[i]));
-              mma16(o[n][i][0], x.a, x.b, y.a, y.b, b0, b1);
-              mma16(o[n][i][1], x.c, x.d, y.c, y.d, b0, b1);
+              b0 = hfma2(hi[n][t][0], s0[t][i], hmul2(lo[n][t][0], s0[t][i]));
+              b1 = hfma2(hi[n][t][1], s1[t][i], hmul2(lo[n][t][1], s1[t][i]));
+            }
+            if (t == 0 && !PREC) {
+              mma16z(c[n][0], x.a, x.b, y.a, y.b, b0, b1);
+              mma16z(c[n][1], x.c, x.d, y.c, y.d, b0, b1);
+            } else {
+              mma16(c[n][0], x.a, x.b, y.a, y.b, b0, b1);
+              mma16(c[n][1], x.c, x.d, y.c, y.d, b0, b1);
             }
           }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              const float2 y = add2f(make_float2(o[n][i][m][j], o[n][i][m][j + 1]), make_float2(c[n][m][j], c[n][m][j + 1]));
+              o[n][i][m][j] = y.x, o[n][i][m][j + 1] = y.y;
+            }
       }
     }
   }
@@ -418,9 +498,17 @@ struct Warp {
       const float l0 = __shfl_sync(0xffffffffu, sum, 8 * qd), l1 = __shfl_sync(0xffffffffu, sum, 8 * qd + 4);
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        const float z0 = __shfl_sync(0xffffffffu, oz[n][0], 4 * i + qd), z1 = __shfl_sync(0xffffffffu, oz[n][1], 4 * i + qd);
+        float z0, z1;
+        if constexpr (PREC) {
+          float z = oz[n][i];
+          z += __shfl_xor_sync(0xffffffffu, z, 1);
+          z += __shfl_xor_sync(0xffffffffu, z, 2);
+          z0 = __shfl_sync(0xffffffffu, z, 8 * qd), z1 = __shfl_sync(0xffffffffu, z, 8 * qd + 4);
+        } else {
+          z0 = __shfl_sync(0xffffffffu, oz[n][0], 4 * i + qd), z1 = __shfl_sync(0xffffffffu, oz[n][1], 4 * i + qd);
+        }
         const float(&c)[2][4] = o[n][i];
-        constexpr float a = 16777216.0f, b = 1048576.0f;  // the codes' units
+        constexpr float a = PREC ? 1.0f : 16777216.0f, b = a / 16.0f;  // the codes' units
         put(8 * n + 2 * qd, 32 * i + 4 * g, l0,
             make_float4(fmaf(c[0][0], a, z0), fmaf(c[0][2], b, z0), fmaf(c[1][0], a, z0), fmaf(c[1][2], b, z0)));
         put(8 * n + 2 * qd + 1, 32 * i + 4 * g, l1,
@@ -809,7 +897,15 @@ static rdkv_status launch(const AttnArgs& a, int grid, cudaStream_t cs) {
   using S = Smem<D, NT, PREC, NW, NS>;
   static_assert(NW <= kMaxWarps, "the workspace counts with kMaxWarps");
   auto kernel = attn_kernel<D, NT, PREC, NW, NS>;
-  RDKV_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes), "4-bit cache attention");
+  // once a device (of the first 64; the others pay for the call every time)
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  RDKV_TRY_CUDA(cudaGetDevice(&dev), "4-bit cache attention");
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    RDKV_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes), "4-bit cache attention");
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   kernel<<<grid, 32 * NW, S::kBytes, cs>>>(a);
   RDKV_CHECK_LAUNCH("4-bit cache attention");
   return RDKV_OK;
@@ -845,11 +941,11 @@ extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, c
                    geo.chunk, geo.n_chunks};
   cudaStream_t cs = (cudaStream_t)stream;
   if (cache->head_dim == 128) {
-    if (prec) return launch<128, 1, true, 11, 2>(a, geo.grid, cs);
+    if (prec) return launch<128, 1, true, 8, 2>(a, geo.grid, cs);
     if (geo.nt == 2) return launch<128, 2, false, 8, 2>(a, geo.grid, cs);
     return launch<128, 1, false, 8, 2>(a, geo.grid, cs);
   }
-  if (prec) return launch<64, 1, true, 11, 4>(a, geo.grid, cs);
+  if (prec) return launch<64, 1, true, 8, 4>(a, geo.grid, cs);
   if (geo.nt == 2) return launch<64, 2, false, 8, 4>(a, geo.grid, cs);
   return launch<64, 1, false, 8, 4>(a, geo.grid, cs);
 }

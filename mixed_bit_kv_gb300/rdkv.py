@@ -808,11 +808,12 @@ class Q4Cache:
                                None if self.bounds is None else self.bounds.data_ptr(), page_table.data_ptr(),
                                lens.data_ptr(), self.status.data_ptr())
         self._ref = ctypes.addressof(self.c)
-        self._ws = {}
+        self._index = self.device.index
+        self._ws, self._seen = {}, {}  # workspaces by stream; what the checks found for queries of a shape and type
 
-    def workspace(self, kind, h_q, n_q):
+    def workspace(self, kind, h_q, n_q, s):
         """The zero-filled workspace of rdkv_q4_attn ("attn") or rdkv_q4_select ("select") calls on the current
-        stream.  While a graph is being captured: one of that call's own, cleared in the graph (two captured
+        stream s.  While a graph is being captured: one of that call's own, cleared in the graph (two captured
         graphs may run at once)."""
         nb = self._ws.get((kind, h_q, n_q))
         if nb is None:
@@ -823,10 +824,9 @@ class Q4Cache:
             self._ws[kind, h_q, n_q] = nb
         if torch.cuda.is_current_stream_capturing():
             return torch.zeros(nb, dtype=torch.uint8, device=self.device)
-        key = kind, torch.cuda.current_stream().cuda_stream
-        ws = self._ws.get(key)
+        ws = self._ws.get((kind, s))
         if ws is None or ws.numel() < nb:
-            ws = self._ws[key] = torch.zeros(nb, dtype=torch.uint8, device=self.device)
+            ws = self._ws[kind, s] = torch.zeros(nb, dtype=torch.uint8, device=self.device)
         return ws
 
 
@@ -836,10 +836,10 @@ def _q4_on(cache, stream, call, *args):
     if stream is not None:
         with torch.cuda.stream(stream):
             return call(cache, *args, stream.cuda_stream)
-    if cache.device.index == torch.cuda.current_device():
-        return call(cache, *args, torch.cuda.current_stream().cuda_stream)
+    if cache._index == torch.cuda.current_device():
+        return call(cache, *args, torch._C._cuda_getCurrentRawStream(cache._index))
     with torch.cuda.device(cache.device):
-        return call(cache, *args, torch.cuda.current_stream().cuda_stream)
+        return call(cache, *args, torch._C._cuda_getCurrentRawStream(cache._index))
 
 
 def _q4_index(cache, t, n, name):
@@ -918,6 +918,14 @@ def _q4_read(cache, max_rows, row_start, first, n_rows, dtype, out, s):
 
 def _q4_queries(cache, q):
     """(dtype code, h_q, n_q, token stride) of queries [batch, n_q, h_q, D] or [batch, h_q, D]."""
+    key = q.shape, q.stride(), q.dtype, q.device
+    found = cache._seen.get(key)
+    if found is None:
+        found = cache._seen[key] = _q4_check_queries(cache, q)
+    return found
+
+
+def _q4_check_queries(cache, q):
     _q4_require(q.dtype in _Q4_DTYPES and q.dim() in (3, 4) and q.shape[0] == cache.batch
                 and q.shape[-1] == cache.head_dim and q.device == cache.device and q.numel() > 0,
                 f"queries must be [{cache.batch}, n_q, h_q, {cache.head_dim}] on {cache.device}")
@@ -939,14 +947,15 @@ def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None
 
 def _q4_attn(cache, q, sel, out, lse, out_dtype, ws, s):
     code, h_q, n_q, stride = _q4_queries(cache, q)
+    shape = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=cache.device)
     else:
-        _q4_require(out.shape == q.shape and out.is_contiguous() and out.device == cache.device
+        _q4_require(out.shape == shape and out.is_contiguous() and out.device == cache.device
                     and out_dtype in (None, out.dtype), "out must be dense and in q's shape")
     _q4_require(out.dtype in (q.dtype, torch.float32), "out must be in q's type or fp32")
     if lse is None:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=cache.device)
     else:
         _q4_require(lse.shape == q.shape[:-1] and lse.dtype == torch.float32 and lse.is_contiguous()
                     and lse.device == cache.device, "lse must be dense fp32 in q's shape without its last size")
@@ -955,7 +964,7 @@ def _q4_attn(cache, q, sel, out, lse, out_dtype, ws, s):
         n_sel = sel.shape[-1]
         sel_ptr = _q4_index(cache, sel, cache.batch * n_q * cache.h_kv * n_sel, "sel")
     if ws is None:
-        ws = cache.workspace("attn", h_q, n_q)
+        ws = cache.workspace("attn", h_q, n_q, s)
     _check(lib().rdkv_q4_attn(cache._ref, code, q.data_ptr(), stride, h_q, n_q, sel_ptr, n_sel, out.data_ptr(),
                               _Q4_DTYPES[out.dtype], lse.data_ptr(), ws.data_ptr(), ws.numel(), s))
     return out, lse
@@ -973,12 +982,12 @@ def _q4_select(cache, q, n_keep, n_first, n_last, out, ws, s):
     _q4_require(n_keep >= 1, f"n_keep {n_keep}")
     shape = (*q.shape[:-2], cache.h_kv, n_keep)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=q.device)
+        out = torch.empty(shape, dtype=torch.int32, device=cache.device)
     else:
         _q4_require(out.shape == shape and out.dtype == torch.int32 and out.is_contiguous()
                     and out.device == cache.device, f"out must be a dense int32 {list(shape)}")
     if ws is None:
-        ws = cache.workspace("select", h_q, n_q)
+        ws = cache.workspace("select", h_q, n_q, s)
     _check(lib().rdkv_q4_select(cache._ref, code, q.data_ptr(), stride, h_q, n_q, n_keep, n_first, n_last,
                                 out.data_ptr(), ws.data_ptr(), ws.numel(), s))
     return out

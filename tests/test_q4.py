@@ -191,6 +191,7 @@ def test_the_binding_refuses_wrong_tensors(L):
     assert rdkv._q4_rows(cache, flat[:5], flat[:5], flat, 4) == (0, 128, 4)
     with pytest.raises(rdkv.RDKVError):
         rdkv._q4_rows(cache, flat[:5], flat[:5], None, None)
+    cache._seen = {}
     q = torch.zeros(2, 3, 4, 64)
     assert rdkv._q4_queries(cache, q) == (1, 4, 3, 256)
     assert rdkv._q4_queries(cache, torch.zeros(2, 3, 8, 64)[:, :, 4:]) == (1, 4, 3, 512)
