@@ -155,6 +155,14 @@ __device__ __forceinline__ int items_of(const AttnArgs& a, int bc) {
   return seen <= 0 ? 0 : a.sel ? a.n_sel : ceil_div(seen, kPage);
 }
 
+// x / y for 0 <= x, 0 < y: 32 bits where they do (a 64-bit division takes some hundred instructions)
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+  return x / y;
+}
+// The first of n items that part i of `parts` equal ones takes.
+__device__ __forceinline__ int64_t share(int64_t i, int64_t n, int64_t parts) { return quotient(i * n, parts); }
+
 // What a unit's index stands for.
 struct Unit {
   int b, t0, h, rows;  // sequence, first query token, KV head, query rows
@@ -198,39 +206,55 @@ struct Warp {
   float o[NT][NG][2][4];
   float oz[NT][PREC ? NG : 2];  // the zeros' part: by row g < NG = group and columns, or (PREC) this lane's row's, by group
   int off;                      // weights are held times 2^off
+  static constexpr int kTurn = NT == 1 && !PREC ? 64 : 32;  // tokens whose products are under way together
   static constexpr int kMaxOff = PREC ? 23 : 11;
 
-  // This lane's channels of the unit's query rows (rows past the last: zero).
-  __device__ __forceinline__ static void fetch(const AttnArgs& a, const Unit& un, int g, int qd, float (&x)[NT][NG][8]) {
+  // This lane's channels of the unit's query rows, as they lie in memory (rows past the last: zero).  Kept
+  // apart from begin() so that copies can be issued while they are under way.
+  struct Rows {
+    uint4 w[NT][NG][2];
+  };
+  __device__ __forceinline__ static void fetch(const AttnArgs& a, const Unit& un, int g, int qd, Rows& r) {
+    const int size = a.dtype == RDKV_F32 ? 4 : 2;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int row = g + 8 * n;
+      const int row = g + 8 * n, t = row / a.G;
+      const bool real = row < un.rows;
+      const int64_t at = ((int64_t)un.b * a.n_q + un.t0 + t) * a.q_stride + ((int64_t)un.h * a.G + row - t * a.G) * D + 8 * qd;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + (real ? at * size : 0));
 #pragma unroll
-      for (int i = 0; i < NG; ++i)
+      for (int i = 0; i < NG; ++i) {
+        r.w[n][i][0] = real ? __ldg(src + 2 * i * size) : make_uint4(0, 0, 0, 0);
+        if (PREC) r.w[n][i][1] = real && size == 4 ? __ldg(src + 2 * i * size + 1) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  // (fp32 queries have fp32 outputs, so only PREC reads them)
+  __device__ __forceinline__ static void widen(int dtype, const uint4 (&w)[2], float (&x)[8]) {
+    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    if (PREC && dtype == RDKV_F32) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[n][i][e] = 0.0f;
-      if (row < un.rows) {
-        const int64_t at = ((int64_t)un.b * a.n_q + un.t0 + row / a.G) * a.q_stride + ((int64_t)un.h * a.G + row % a.G) * D + 8 * qd;
+      for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(v[e]);
+    } else {
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          if (a.dtype == RDKV_F16) Eight<__half>::load(static_cast<const __half*>(a.q) + at + 32 * i, x[n][i]);
-          else if (a.dtype == RDKV_BF16) Eight<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(a.q) + at + 32 * i, x[n][i]);
-          else Eight<float>::load(static_cast<const float*>(a.q) + at + 32 * i, x[n][i]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = dtype == RDKV_F16 ? unpack2(v[e]) : make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u));
+        x[2 * e] = f.x, x[2 * e + 1] = f.y;
       }
     }
   }
 
-  __device__ __forceinline__ void begin(float (&rows)[NT][NG][8], int qd) {
+  __device__ __forceinline__ void begin(int dtype, const Rows& rows, int qd) {
     constexpr float kK = 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float(&x)[NG][8] = rows[n];
-      float top = 0.0f;
+      float x[NG][8], top = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NG; ++i)
+      for (int i = 0; i < NG; ++i) {
+        widen(dtype, rows.w[n][i], x[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+      }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // the row times 2^s, its largest value in [2^14, 2^15): what fp16 drops is 2^-25 against that
@@ -324,10 +348,10 @@ struct Warp {
     // 32 tokens a turn: enough independent products to hide their latency, and a body that stays in the
     // instruction cache
 #pragma unroll 1
-    for (int t32 = 0; t32 < kPage; t32 += 32) {
-      float2 u[NT][4];  // logits (base 2, times 2^(s - 15)) of tokens t32 + 8 t + 2 qd + {0, 1}
+    for (int t32 = 0; t32 < kPage; t32 += kTurn) {
+      float2 u[NT][kTurn / 8];  // logits (base 2, times 2^(s - 15)) of tokens t32 + 8 t + 2 qd + {0, 1}
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < kTurn / 8; ++t) {
         const int tok = t32 + 8 * t;
         uint32_t w[NG], sw[NG];
         lds_groups<NG>(k + L::kKCodes + ((tok + g) * 4 + qd) * NG * 4, w);
@@ -364,7 +388,7 @@ struct Warp {
       for (int n = 0; n < NT; ++n) {
         float m = fmaxf(u[n][0].x, u[n][0].y);
 #pragma unroll
-        for (int t = 1; t < 4; ++t) m = fmaxf(m, fmaxf(u[n][t].x, u[n][t].y));
+        for (int t = 1; t < kTurn / 8; ++t) m = fmaxf(m, fmaxf(u[n][t].x, u[n][t].y));
         m *= scale[n];
         if (__any_sync(0xffffffffu, m > ref[n] + (PREC ? 0.0f : 4.0f))) {
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -376,10 +400,10 @@ struct Warp {
         }
       }
       // the weights, as fp16 parts and remainders, in the order of the values' products: 16 tokens a step
-      uint32_t hi[NT][2][2], lo[NT][2][2], s0[2][NG], s1[2][NG], w0[2][NG], w1[2][NG];
-      float p[NT][2][4], cz[NT][4];
+      uint32_t hi[NT][kTurn / 16][2], lo[NT][kTurn / 16][2], s0[kTurn / 16][NG], s1[kTurn / 16][NG], w0[kTurn / 16][NG], w1[kTurn / 16][NG];
+      float p[NT][kTurn / 16][4], cz[NT][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < kTurn / 16; ++t) {
         const int p0 = t32 / 2 + 8 * t + qd, p1 = p0 + 4;  // this lane's token pairs
         lds_groups<NG>(k + L::kVCodes + (p0 * 8 + g) * NG * 4, w0[t]);
         lds_groups<NG>(k + L::kVCodes + (p1 * 8 + g) * NG * 4, w1[t]);
@@ -437,7 +461,7 @@ struct Warp {
       for (int i = 0; i < NG; ++i) {
         float c[NT][2][4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < kTurn / 16; ++t) {
           const Pairs x = PREC ? centred_pairs(w0[t][i]) : code_pairs(w0[t][i]);
           const Pairs y = PREC ? centred_pairs(w1[t][i]) : code_pairs(w1[t][i]);
 #pragma unroll
@@ -526,27 +550,34 @@ struct Piece {
 };
 
 // Joins pieces of one query row: a lane's four channels of the sums and, in every lane, the row's reference
-// and sum.  n pieces, m_of(i), l_of(i) their statistics, y_of(i) this lane's channels.
+// and sum.  n pieces, m_of(i), l_of(i) their statistics, y_of(i) this lane's channels: the loads of up to 16
+// pieces are under way together.
 template <class M, class L, class Y>
 __device__ __forceinline__ void join_row(int n, int lane, M m_of, L l_of, Y y_of, float4& o, float& top, float& sum) {
-  top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, m_of(i));
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   o = make_float4(0, 0, 0, 0);
-  sum = 0.0f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float f = 0.0f;
-    if (i0 + lane < n && top != -INFINITY) f = ex2(m_of(i0 + lane) - top);
-    if (i0 + lane < n) sum = fmaf(f, l_of(i0 + lane), sum);
-    const int k = min(32, n - i0);
-#pragma unroll 8
-    for (int i = 0; i < k; ++i) {
-      const float4 y = y_of(i0 + i);
+  top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += 16) {
+    const bool mine = lane < 16 && i0 + lane < n;
+    const float m = mine ? m_of(i0 + lane) : -INFINITY, l = mine ? l_of(i0 + lane) : 0.0f;
+    float4 y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = i0 + i < n ? y_of(i0 + i) : make_float4(0, 0, 0, 0);
+    float now = m;
+    for (int d = 8; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+    now = fmaxf(top, __shfl_sync(0xffffffffu, now, 0));
+    const float back = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
+    top = now;
+    o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
+    float part = f * l;
+    for (int d = 8; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+    sum = fmaf(sum, back, __shfl_sync(0xffffffffu, part, 0));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
       const float w = __shfl_sync(0xffffffffu, f, i);
-      o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y), o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
+      o.x = fmaf(w, y[i].x, o.x), o.y = fmaf(w, y[i].y, o.y), o.z = fmaf(w, y[i].z, o.z), o.w = fmaf(w, y[i].w, o.w);
     }
   }
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
 }
 __device__ __forceinline__ float4 scaled(float4 o, float l) {
   const float f = l > 0.0f ? 1.0f / l : 0.0f;
@@ -570,7 +601,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   __shared__ Piece piece_s[2 * NW];
   __shared__ uint32_t valid_s, start_s, end_s;
   __shared__ unsigned long long total_s;
-  __shared__ int last_s[2];
+  __shared__ int last_s[2], first_s[2];
   __shared__ uint8_t member_s[2 * NW];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, qd = lane % 4, H = a.c.h_kv;
   uint8_t* ring = smem + (size_t)warp * S::kRing;
@@ -617,7 +648,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   const int64_t nb = min((int64_t)gridDim.x, ceil_div64(total, NW));
   if (blockIdx.x >= nb) return;
   const int64_t nw = nb * NW, me = (int64_t)blockIdx.x * NW + warp;
-  const int64_t w0 = me * total / nw, w1 = (me + 1) * total / nw;
+  const int64_t w0 = share(me, total, nw), w1 = share(me + 1, total, nw);
   const int n_items = (int)min(w1 - w0, (int64_t)INT32_MAX);
   int bc = 0, h = 0, p = 0, cnt = 0;  // the next item to look up
   {
@@ -642,8 +673,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       before += __shfl_sync(0xffffffffu, in, 31);
     }
   }
-  // The next n items' places, one a lane: physical page (-1: nothing to copy), logical page, unit, and
-  // whether the item is its unit's first or last.
+  // The next n items' places, one a lane: (physical page, head) (-1: nothing to copy), logical page, unit,
+  // and whether the item is its unit's first or last.
   int known = 0;
   auto look_up = [&](int n) {
     const int i = known + lane;
@@ -669,6 +700,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
         if (e.x < 0 || e.x >= a.c.n_pages) {
           raise(a.c, RDKV_ERR_INVALID_ARG);
           e.x = -1;
+        } else {
+          e.x = e.x * H + h1;
         }
       }
       e.y = lp, e.z = unit, e.w = (p1 == 0 ? 1 : 0) | (p1 == c1 - 1 ? 2 : 0);
@@ -692,7 +725,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       if (e.x < 0) {
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
       } else {
-        const uint8_t* src = a.c.pages + ((int64_t)e.x * H + e.z % H) * L::kBytes;
+        const uint8_t* src = a.c.pages + (int64_t)e.x * L::kBytes;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(L::kBytes) : "memory");
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                          smem_u32(ring + i % NS * L::kBytes)),
@@ -713,22 +746,22 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   if (n_items > 0) {
     look_up(kInfo);
     // the first queries are asked for before the pages, behind which they would wait
-    float x[NT][Warp<D, NT, PREC>::NG][8];
+    typename Warp<D, NT, PREC>::Rows x;
     un = unit_at(a, info[0].z);
     w.fetch(a, un, g, qd, x);
 #pragma unroll 1
     for (int j = 0; j < min(NS, n_items); ++j) issue(j);
-    w.begin(x, qd);
+    w.begin(a.dtype, x, qd);
     in_unit = true;
   }
 #pragma unroll 1
   for (; i < n_items; ++i) {
     const int4 e = info[i % kInfo];
     if (!in_unit) {
-      float x[NT][Warp<D, NT, PREC>::NG][8];
+      typename Warp<D, NT, PREC>::Rows x;
       un = unit_at(a, e.z);
       w.fetch(a, un, g, qd, x);
-      w.begin(x, qd);
+      w.begin(a.dtype, x, qd);
     }
     if (!in_unit || i == 0) {
       in_unit = true, began = e.w & 1;
@@ -793,9 +826,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   const uint32_t starts = begins | (valid & (0u - valid));
   if (tid < 2 * NW && (valid >> tid & 1)) member_s[__popc(valid & ((1u << tid) - 1u))] = (uint8_t)tid;
   __syncthreads();
-  int open_unit[2] = {-1, -1};  // runs that are a part of their unit: one that began before the block, one that goes on
-  int open_n[2] = {0, 0}, open_first[2] = {0, 0};
-  auto block_of = [&](int64_t item) { return (int)(((item + 1) * nb - 1) / total); };
+  int open[2] = {-1, -1};  // pieces of runs that are a part of their unit: one that began before the block, one that goes on
+  auto block_of = [&](int64_t item) { return (int)quotient((item + 1) * nb - 1, total); };
   int task = 0;
   for (uint32_t left = starts; left; left &= left - 1) {
     const int s = __ffs(left) - 1;
@@ -827,27 +859,28 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
         if (lane == 0) part[P::kRows * D + row] = m, part[P::kRows * (D + 1) + row] = l;
       }
     }
-    if (!whole) {
-      open_unit[slot] = pc.unit;
-      open_first[slot] = block_of(pc.base);
-      open_n[slot] = block_of(pc.base + pc.items - 1) - open_first[slot] + 1;
-    }
+    if (!whole) open[slot] = s;
   }
   // ---- joining the blocks' parts: the last block of a unit to arrive does it
-  if (open_unit[0] < 0 && open_unit[1] < 0) return;
+  if (open[0] < 0 && open[1] < 0) return;
   __syncthreads();
-  if (tid < 2 && open_unit[tid] >= 0) {
-    int32_t* t = a.tickets + open_unit[tid];
+  if (tid < 2 && open[tid] >= 0) {
+    const Piece pc = piece_s[open[tid]];
+    const int first = block_of(pc.base), n = block_of(pc.base + pc.items - 1) - first + 1;
+    int32_t* t = a.tickets + pc.unit;
     int before;
     asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(t) : "memory");
-    last_s[tid] = before == open_n[tid] - 1;
-    if (last_s[tid]) *t = 0;
+    const bool last = before == n - 1;
+    if (last) *t = 0;
+    last_s[tid] = last ? n : 0;
+    first_s[tid] = first;
   }
   __syncthreads();
 #pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
-    const int unit = slot ? open_unit[1] : open_unit[0], n = slot ? open_n[1] : open_n[0], first = slot ? open_first[1] : open_first[0];
-    if (unit < 0 || !last_s[slot]) continue;
+    const int e = slot ? open[1] : open[0];
+    if (e < 0 || last_s[slot] == 0) continue;
+    const int unit = piece_s[e].unit, n = last_s[slot], first = first_s[slot];
     const Unit ru = unit_at(a, unit);
     for (int row = warp; row < ru.rows; row += NW) {
       // the unit's first block wrote it as the unit that goes on, the others as the one that began before
