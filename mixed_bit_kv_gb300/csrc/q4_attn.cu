@@ -39,6 +39,7 @@ struct AttnArgs {
 };
 
 constexpr long long kWaitCycles = 4000000000LL;  // a bounded wait, about two seconds
+constexpr int kMinItems = 4;
 constexpr int kInfo = 32;                        // items whose places a warp knows ahead
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -156,12 +157,12 @@ __device__ __forceinline__ int items_of(const AttnArgs& a, int bc) {
 }
 
 // x / y for 0 <= x, 0 < y: 32 bits where they do (a 64-bit division takes some hundred instructions)
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
-  return x / y;
+__device__ __forceinline__ int quotient(int64_t x, int y) {
+  if ((x >> 32) == 0) return (int)((uint32_t)x / (uint32_t)y);
+  return (int)(x / y);
 }
 // The first of n items that part i of `parts` equal ones takes.
-__device__ __forceinline__ int64_t share(int64_t i, int64_t n, int64_t parts) { return quotient(i * n, parts); }
+__device__ __forceinline__ int share(int i, int n, int parts) { return quotient((int64_t)i * n, parts); }
 
 // What a unit's index stands for.
 struct Unit {
@@ -545,8 +546,7 @@ struct Warp {
 
 // What a block knows of a piece it joins.
 struct Piece {
-  int64_t base;  // the unit's first item
-  int unit, items;
+  int base, unit, items;  // the unit's first item, the unit, its items
 };
 
 // Joins pieces of one query row: a lane's four channels of the sums and, in every lane, the row's reference
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Piece piece_s[2 * NW];
   __shared__ uint32_t valid_s, start_s, end_s;
-  __shared__ unsigned long long total_s;
+  __shared__ int total_s;
   __shared__ int last_s[2], first_s[2];
   __shared__ uint8_t member_s[2 * NW];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, qd = lane % 4, H = a.c.h_kv;
@@ -611,6 +611,10 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   if (tid == 0) total_s = 0, valid_s = start_s = end_s = 0;
   if (lane < NS) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bars + lane)) : "memory");
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  // the kernel after this one may be set up beside it; nothing that the kernel before wrote is read until
+  // that one has ended
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- the items of all units, and where this warp's run of them begins
   if (blockIdx.x == 0)
@@ -620,18 +624,18 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       if ((int64_t)len > (int64_t)a.c.page_stride * kPage) raise(a.c, RDKV_ERR_CAPACITY);
     }
   const int c0 = lane < BC ? items_of(a, lane) : 0;  // of the first 32 (sequence, chunk) pairs
-  int64_t total;
+  int total;  // the host has made sure that all units' items fit
   if (BC <= 32) {
-    total = __reduce_add_sync(0xffffffffu, (unsigned)c0);  // 32 counts below 2^26
+    total = __reduce_add_sync(0xffffffffu, c0);
     __syncthreads();
   } else {
-    int64_t n = 0;
+    int n = 0;
     __syncthreads();
     for (int i = tid; i < BC; i += 32 * NW) n += items_of(a, i);
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (lane == 0 && n) atomicAdd(&total_s, (unsigned long long)n);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0 && n) atomicAdd(&total_s, n);
     __syncthreads();
-    total = (int64_t)total_s;
+    total = total_s;
   }
   total *= H;
   // units without a key: nothing else writes their rows
@@ -644,30 +648,30 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       if (tid < un.rows) put_lse(a, row_at(a, un, tid), 0.0f, 0.0f);
     }
   }
-  // a block for as many items as it has warps: few items stay in few blocks, whose joins are cheap
-  const int64_t nb = min((int64_t)gridDim.x, ceil_div64(total, NW));
-  if (blockIdx.x >= nb) return;
-  const int64_t nw = nb * NW, me = (int64_t)blockIdx.x * NW + warp;
-  const int64_t w0 = share(me, total, nw), w1 = share(me + 1, total, nw);
-  const int n_items = (int)min(w1 - w0, (int64_t)INT32_MAX);
+  // a block for every kMinItems items: few items stay in few blocks, whose joins are cheap
+  const int nb = min((int)gridDim.x, ceil_div(total, kMinItems));
+  if ((int)blockIdx.x >= nb) return;
+  const int nw = nb * NW, me = blockIdx.x * NW + warp;
+  const int w0 = share(me, total, nw), w1 = share(me + 1, total, nw), n_items = w1 - w0;
   int bc = 0, h = 0, p = 0, cnt = 0;  // the next item to look up
-  {
-    int64_t before = 0;
+  if (BC == 1) {
+    cnt = __shfl_sync(0xffffffffu, c0, 0);
+    h = w0 / cnt, p = w0 - h * cnt;
+  } else {
+    int before = 0;
     for (int i0 = 0; i0 < BC && n_items > 0; i0 += 32) {
       const int c = i0 == 0 ? c0 : i0 + lane < BC ? items_of(a, i0 + lane) : 0;
-      int64_t in = (int64_t)c * H;
+      int in = c * H;
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, in, o);
+        const int x = __shfl_up_sync(0xffffffffu, in, o);
         if (lane >= o) in += x;
       }
       const uint32_t past = __ballot_sync(0xffffffffu, before + in > w0);
       if (past) {
         const int l = __ffs(past) - 1;
         cnt = __shfl_sync(0xffffffffu, c, l);
-        int64_t rem = w0 - before - (__shfl_sync(0xffffffffu, in, l) - (int64_t)cnt * H);
-        bc = i0 + l;
-        while (rem >= cnt) rem -= cnt, ++h;  // at most the heads
-        p = (int)rem;
+        const int rem = w0 - before - (__shfl_sync(0xffffffffu, in, l) - cnt * H);
+        bc = i0 + l, h = rem / cnt, p = rem - h * cnt;
         break;
       }
       before += __shfl_sync(0xffffffffu, in, 31);
@@ -788,7 +792,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       const bool ends = e.w & 2;
       // a unit that ends here without having begun lies first in the run: copies are under way, its piece
       // goes to global memory
-      float* dst = ends ? a.heads + me * P::kFloats : reinterpret_cast<float*>(ring);
+      float* dst = ends ? a.heads + (int64_t)me * P::kFloats : reinterpret_cast<float*>(ring);
       if (began && ends) {
         w.finish(
             g, qd,
@@ -827,7 +831,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   if (tid < 2 * NW && (valid >> tid & 1)) member_s[__popc(valid & ((1u << tid) - 1u))] = (uint8_t)tid;
   __syncthreads();
   int open[2] = {-1, -1};  // pieces of runs that are a part of their unit: one that began before the block, one that goes on
-  auto block_of = [&](int64_t item) { return (int)quotient((item + 1) * nb - 1, total); };
+  auto block_of = [&](int64_t item) { return quotient((item + 1) * nb - 1, total); };
   int task = 0;
   for (uint32_t left = starts; left; left &= left - 1) {
     const int s = __ffs(left) - 1;
@@ -939,8 +943,8 @@ static rdkv_status launch(const AttnArgs& a, int grid, cudaStream_t cs) {
     RDKV_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes), "4-bit cache attention");
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  kernel<<<grid, 32 * NW, S::kBytes, cs>>>(a);
-  RDKV_CHECK_LAUNCH("4-bit cache attention");
+  RDKV_TRY_CUDA(launch_after(kernel, dim3(grid), 32 * NW, S::kBytes, cs, a), "4-bit cache attention");
+  count_launch();
   return RDKV_OK;
 }
 
@@ -964,6 +968,8 @@ extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, c
   RDKV_REQUIRE((uintptr_t)out % 16 == 0, RDKV_ERR_INVALID_ARG, "out must be 16-byte aligned");
   RDKV_REQUIRE(out_dtype == dtype || out_dtype == RDKV_F32, RDKV_ERR_UNSUPPORTED, "out_dtype %d for dtype %d", out_dtype, dtype);
   RDKV_REQUIRE(!sel || n_sel >= 1, RDKV_ERR_INVALID_ARG, "n_sel %d", n_sel);
+  RDKV_REQUIRE((int64_t)cache->batch * cache->h_kv * n_q * (sel ? n_sel : cache->page_stride) <= INT32_MAX, RDKV_ERR_UNSUPPORTED,
+               "more than 2^31 - 1 (sequence, query token, KV head, page) items");
   const bool prec = out_dtype == RDKV_F32;
   const Geometry geo = geometry(cache, h_q, n_q, prec, sel != nullptr);
   RDKV_REQUIRE(ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= geo.bytes, RDKV_ERR_WORKSPACE,
