@@ -121,136 +121,306 @@ __device__ __forceinline__ Run find_run(const View& v, const Rows& r, int b, int
   return o;
 }
 
-constexpr int kThreads = 256;
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)), "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 wide2(__half2 v) { return __half22float2(v); }
+__device__ __forceinline__ float2 wide2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+__device__ __forceinline__ __half2 halves_of(__half a, __half b) { return __halves2half2(a, b); }
+__device__ __forceinline__ __nv_bfloat162 halves_of(__nv_bfloat16 a, __nv_bfloat16 b) { return __halves2bfloat162(a, b); }
 
-// Codes of eight channels whose group of 32 is spread over four neighbouring lanes, with the group's
-// scale and zero (the quantiser of the pack, on values cut to the fp16 range; a NaN takes no part in
-// min and max and gets code 0).  xh: the values they stand for.
-struct Codes {
-  uint32_t c[8];
-  QParams p;
+// Eight channels of one row as they lie in memory, in two runs of four that are `gap` channels apart.
+template <typename T>
+struct Raw {
+  uint2 a, b;
 };
-__device__ __forceinline__ Codes quantise8(float (&x)[8], float (&xh)[8]) {
+template <>
+struct Raw<float> {
+  uint4 a, b;
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p, int gap) {
+  using W = decltype(Raw<T>::a);
+  return Raw<T>{__ldg(reinterpret_cast<const W*>(p)), __ldg(reinterpret_cast<const W*>(p + gap))};
+}
+__device__ __forceinline__ void widen(const Raw<__half>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.b.x, r.b.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.b.x, r.b.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+__device__ __forceinline__ void widen(const Raw<float>& r, float (&x)[8]) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+}
+
+// The smallest and the largest of eight values of four neighbouring lanes; a NaN takes no part (all NaN: not
+// smallest <= largest).
+__device__ __forceinline__ float2 extremes(const float (&x)[8]) {
   float mn = INFINITY, mx = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = x[i] > kHalfMax ? kHalfMax : x[i] < -kHalfMax ? -kHalfMax : x[i];
-    mn = fminf(mn, x[i]);
-    mx = fmaxf(mx, x[i]);
-  }
+  for (int i = 0; i < 8; ++i) mn = fminf(mn, x[i]), mx = fmaxf(mx, x[i]);
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
-  if (mn > mx) mn = mx = 0.0f;
+  return make_float2(mn, mx);
+}
+__device__ __forceinline__ float2 extremes_of(const Raw<float>& r, const float (&x)[8]) { return extremes(x); }
+// 16-bit types: pairs at a time, the largest as the smallest of the negatives
+template <typename T2>
+__device__ __forceinline__ float2 extremes16(const uint32_t (&w)[4], T2 all) {
+  auto as = [](uint32_t v) { return *reinterpret_cast<const T2*>(&v); };
+  T2 mn = __hmin2(__hmin2(as(w[0]), as(w[1])), __hmin2(as(w[2]), as(w[3])));
+  T2 mx = __hmax2(__hmax2(as(w[0]), as(w[1])), __hmax2(as(w[2]), as(w[3])));
+  T2 both = halves_of(__hmin(mn.x, mn.y), __hneg(__hmax(mx.x, mx.y)));
+  both = __hmin2(both, __shfl_xor_sync(0xffffffffu, both, 1));
+  both = __hmin2(both, __shfl_xor_sync(0xffffffffu, both, 2));
+  const float2 f = wide2(both);
+  return make_float2(f.x, -f.y);
+}
+__device__ __forceinline__ float2 extremes_of(const Raw<__half>& r, const float (&)[8]) {
+  return extremes16({r.a.x, r.a.y, r.b.x, r.b.y}, __half2());
+}
+__device__ __forceinline__ float2 extremes_of(const Raw<__nv_bfloat16>& r, const float (&)[8]) {
+  return extremes16({r.a.x, r.a.y, r.b.x, r.b.y}, __nv_bfloat162());
+}
+
+// Codes (as whole floats) of eight channels whose group of 32 is spread over four neighbouring lanes, with
+// the group's scale and zero (the quantiser of the pack, on values cut to the fp16 range; a NaN takes no
+// part in min and max and gets code 0).
+//   The fast way takes the quotients as products.  Range / 15 as range times fp32(1 / 15), within 2^-22 of the
+// quotient: the fp16 scale is the same unless the product lies within 8 units of its last place of the middle
+// of two fp16 values (or below fp16's normal range).  (x - zero) / scale as (x - zero) r, r within 2^-22 of
+// 1 / scale: with every quotient of the group in (-0.49, 15.49), rounding gives the same code unless the
+// product is within 2^-12 of a half-integer.  What fails a test, and groups that hold a NaN or values past
+// fp16's range, goes the exact way.
+struct Codes {
+  float c[8];
+  QParams p;
+};
+__device__ __noinline__ Codes quantise8_exact(float mn, float mx, float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+                                              float x7) {
+  const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
+  if (!(mn <= mx)) mn = mx = 0.0f;  // nothing but NaN
+  mn = fminf(fmaxf(mn, -kHalfMax), kHalfMax), mx = fminf(fmaxf(mx, -kHalfMax), kHalfMax);
   Codes r;
   r.p = qparams(mn, mx, 4);
-  const float rs = 1.0f / r.p.scale;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    r.c[i] = qcode_rcp(x[i], r.p.zero, r.p.scale, rs, 15.0f);
-    xh[i] = fmaf(r.p.scale, (float)r.c[i], r.p.zero);
+    const float y = x[i] > kHalfMax ? kHalfMax : x[i] < -kHalfMax ? -kHalfMax : x[i];
+    const float t = __fdiv_rn(y - r.p.zero, r.p.scale);
+    r.c[i] = r.p.scale == 0.0f ? 0.0f : fminf(fmaxf(rintf(t), 0.0f), 15.0f);  // a NaN: 0
   }
   return r;
 }
+template <typename T>
+__device__ __forceinline__ Codes quantise8(const Raw<T>& raw) {
+  float x[8];
+  widen(raw, x);
+  float2 ex = extremes_of(raw, x);
+  Codes r;
+  r.p.zero_h = half_bits(ex.x);
+  r.p.zero = __half2float(__ushort_as_half(r.p.zero_h));
+  const float step = (ex.y - ex.x) * 0.066666670143604279f;
+  r.p.scale_h = half_bits(step);
+  r.p.scale = __half2float(__ushort_as_half(r.p.scale_h));
+  const uint32_t below = (__float_as_uint(step) - 0xff8u) & 0x1fffu;  // 0 .. 16 next to the middle of two fp16 values
+  float rs;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(r.p.scale));
+  constexpr float kRound = 12582912.0f;  // 1.5 2^23: its last place is 1
+  const float2 zero = make_float2(-r.p.zero, -r.p.zero), rs2 = make_float2(rs, rs), up = make_float2(kRound, kRound),
+               down = make_float2(-kRound, -kRound);
+  float far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 d = add_f32x2(make_float2(x[i], x[i + 1]), zero);
+    const float2 c = add_f32x2(fma_f32x2(d, rs2, up), down);
+    const float2 e = fma_f32x2(d, rs2, make_float2(-c.x, -c.y));
+    r.c[i] = c.x, r.c[i + 1] = c.y;
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(far) : "f"(fabsf(e.x)), "f"(fabsf(e.y)));
+  }
+  // (far is NaN when a value is; the comparisons are false for NaN)
+  const bool fine = far <= 0.5f - 0.000244140625f && step >= 6.1035156e-5f && step < 8000.0f && below > 16u && (ex.x - r.p.zero) * rs > -0.49f &&
+                    (ex.y - r.p.zero) * rs < 15.49f && ex.x >= -kHalfMax && ex.y <= kHalfMax;
+  if (!fine) r = quantise8_exact(ex.x, ex.y, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
+  return r;
+}
+// Four codes in 16 bits, the first lowest.
+__device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d) {
+  return __float_as_uint(fmaf(d, 4096.0f, fmaf(c, 256.0f, fmaf(b, 16.0f, a))) + 8388608.0f);  // the low 16 bits
+}
+__device__ __forceinline__ uint32_t low_halves(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x5410); }
+// Two values in fp16, cut to its range.
+__device__ __forceinline__ __half2 cut_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return *reinterpret_cast<const __half2*>(&d);
+}
 
-// One block per (sequence, KV head, page that its rows touch).  Eight channels a thread: one K code
-// word, and the halves of two V code words.
-template <typename T, int D>
+// One block per (sequence, page that its rows touch, KV head), heads fastest: neighbouring blocks read
+// neighbouring memory.  A thread has eight channels of a token pair: of K eight in a row (a code word of each
+// token), of V the runs 4 q and 4 q + 16 (two words that hold both tokens), so that a warp's stores fill whole
+// sectors.  Every load of a thread's kSteps pairs is under way before the first is used.  kThreads, kSteps:
+// as few as the call's rows need (a decode step has one token a sequence).
+template <typename T, int D, int kThreads, int kSteps>
 __global__ void __launch_bounds__(kThreads) write_kernel(View v, Rows r, const T* __restrict__ k, const T* __restrict__ vv) {
   using L = Layout<D>;
-  constexpr int kLanes = D / 8, kSlots = kThreads / kLanes, NG = L::NG;
-  __shared__ __half lo_s[kSlots][D], hi_s[kSlots][D];
-  const int run = blockIdx.x % r.runs, u = blockIdx.x / r.runs, h = u % v.h_kv, b = u / v.h_kv;
+  constexpr int kLanes = D / 8, kPairs = kThreads / kLanes, kWarps = kThreads / 32, NG = L::NG;
+  __shared__ __half2 lo_s[kWarps][D / 2], hi_s[kWarps][D / 2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int h = blockIdx.x % v.h_kv, u = blockIdx.x / v.h_kv, run = u % r.runs, b = u / r.runs;
   const Run w = find_run<true>(v, r, b, run);
   if (w.page < 0) return;
   uint8_t* page = v.pages + ((int64_t)w.page * v.h_kv + h) * L::kBytes;
-  const int l = threadIdx.x % kLanes, g0 = threadIdx.x / kLanes, grp = l / 4, q = l % 4;
-  __half lo[8], hi[8];
+  const int l = threadIdx.x % kLanes, grp = l / 4, q = l % 4, first = w.s0 / 2 + threadIdx.x / kLanes;
+  __half2 lo[4], hi[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) lo[i] = __float2half(INFINITY), hi[i] = __float2half(-INFINITY);
-  for (int s0 = w.s0; s0 < w.s1; s0 += kSlots) {
-    const int s = s0 + g0;
-    const bool real = s < w.s1;
-    const int64_t at = (w.row + (real ? s - w.s0 : 0)) * r.stride + (int64_t)h * D + 8 * l;
-    float x[8], xh[8];
-    Eight<T>::load(k + at, x);
-    Codes c = quantise8(x, xh);
-    if (real) {
-      uint32_t word = 0;
+  for (int i = 0; i < 4; ++i) lo[i] = __float2half2_rn(INFINITY), hi[i] = __float2half2_rn(-INFINITY);
+  Raw<T> kr[kSteps][2], vr[kSteps][2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) word |= c.c[e] << bit_off(e, 4);
-      reinterpret_cast<uint32_t*>(page + L::kKCodes)[(s * 4 + q) * NG + grp] = word;
-      if (q == 0) {
-        reinterpret_cast<uint16_t*>(page + L::kKScales)[(s / 2 * NG + grp) * 2 + s % 2] = c.p.scale_h;
-        reinterpret_cast<uint16_t*>(page + L::kKZeros)[s * NG + grp] = c.p.zero_h;
-      }
+  for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const __half y = __float2half_rn(fminf(fmaxf(xh[i], -kHalfMax), kHalfMax));
-        lo[i] = __hmin(lo[i], y), hi[i] = __hmax(hi[i], y);
+    for (int j = 0; j < 2; ++j) {
+      // a token outside the run: the run's nearest, whose codes go nowhere
+      const int s = min(max(2 * (first + i * kPairs) + j, w.s0), w.s1 - 1);
+      const int64_t at = (w.row + s - w.s0) * r.stride + (int64_t)h * D + 32 * grp;
+      kr[i][j] = load_raw(k + at + 8 * q, 4);
+      vr[i][j] = load_raw(vv + at + 4 * q, 16);
+    }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int pair = first + i * kPairs, m = pair * NG + grp;
+    const bool in[2] = {2 * pair >= w.s0 && 2 * pair < w.s1, 2 * pair + 1 >= w.s0 && 2 * pair + 1 < w.s1};
+    if (!__any_sync(0xffffffffu, in[0] || in[1])) continue;
+    uint32_t word[2][2];
+    QParams pp[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const Codes c = quantise8(kr[i][j]);
+      pp[j] = c.p;
+      if (in[j]) {
+        reinterpret_cast<uint32_t*>(page + L::kKCodes)[((2 * pair + j) * 4 + q) * NG + grp] =
+            low_halves(nibbles(c.c[0], c.c[2], c.c[4], c.c[6]), nibbles(c.c[1], c.c[3], c.c[5], c.c[7]));
+        if (q == 0) reinterpret_cast<uint16_t*>(page + L::kKZeros)[(2 * pair + j) * NG + grp] = c.p.zero_h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = fma_f32x2(make_float2(c.p.scale, c.p.scale), make_float2(c.c[2 * e], c.c[2 * e + 1]), make_float2(c.p.zero, c.p.zero));
+          const __half2 z = cut_half2(y.x, y.y);
+          lo[e] = __hmin2(lo[e], z), hi[e] = __hmax2(hi[e], z);
+        }
       }
     }
-    Eight<T>::load(vv + at, x);
-    c = quantise8(x, xh);
-    if (real) {
+    auto store_pair = [&](int at, int index, uint32_t even, uint32_t odd) {
+      if (in[0] && in[1]) reinterpret_cast<uint32_t*>(page + at)[index] = low_halves(even, odd);
+      else if (in[0]) reinterpret_cast<uint16_t*>(page + at)[2 * index] = (uint16_t)even;
+      else if (in[1]) reinterpret_cast<uint16_t*>(page + at)[2 * index + 1] = (uint16_t)odd;
+    };
+    if (q == 0) store_pair(L::kKScales, m, pp[0].scale_h, pp[1].scale_h);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t half = c.c[4 * j] | c.c[4 * j + 1] << 4 | c.c[4 * j + 2] << 8 | c.c[4 * j + 3] << 12;
-        reinterpret_cast<uint16_t*>(page + L::kVCodes)[((s / 2 * 8 + 2 * q + j) * NG + grp) * 2 + s % 2] = (uint16_t)half;
-      }
-      if (q == 0) {
-        const int m = (s / 2 * NG + grp) * 2 + s % 2;
-        reinterpret_cast<uint16_t*>(page + L::kVScales)[m] = c.p.scale_h;
-        reinterpret_cast<uint16_t*>(page + L::kVZeros)[m] = c.p.zero_h;
-      }
+    for (int j = 0; j < 2; ++j) {
+      const Codes c = quantise8(vr[i][j]);
+      pp[j] = c.p;
+      word[j][0] = nibbles(c.c[0], c.c[1], c.c[2], c.c[3]), word[j][1] = nibbles(c.c[4], c.c[5], c.c[6], c.c[7]);
+    }
+    store_pair(L::kVCodes, (pair * 8 + q) * NG + grp, word[0][0], word[1][0]);
+    store_pair(L::kVCodes, (pair * 8 + q + 4) * NG + grp, word[0][1], word[1][1]);
+    if (q == 0) {
+      store_pair(L::kVScales, m, pp[0].scale_h, pp[1].scale_h);
+      store_pair(L::kVZeros, m, pp[0].zero_h, pp[1].zero_h);
     }
   }
   if (!v.bounds) return;
+  // the page's bounds: the pairs of a warp, the block's warps, and what the page held before
 #pragma unroll
-  for (int i = 0; i < 8; ++i) lo_s[g0][8 * l + i] = lo[i], hi_s[g0][8 * l + i] = hi[i];
+  for (int d = kLanes; d < 32; d <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo[e] = __hmin2(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
+      hi[e] = __hmax2(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
+    }
+  if (threadIdx.x % 32 < kLanes) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) lo_s[threadIdx.x / 32][4 * l + e] = lo[e], hi_s[threadIdx.x / 32][4 * l + e] = hi[e];
+  }
   __syncthreads();
-  const int c = threadIdx.x % D, side = threadIdx.x / D;
-  if (side >= 2) return;
-  __half* out = v.bounds + (((int64_t)w.page * v.h_kv + h) * 2 + side) * D + c;
-  __half m = side ? hi_s[0][c] : lo_s[0][c];
-  for (int g = 1; g < kSlots; ++g) m = side ? __hmax(m, hi_s[g][c]) : __hmin(m, lo_s[g][c]);
-  if (w.s0 > 0) m = side ? __hmax(m, *out) : __hmin(m, *out);
-  *out = m;
+  __half2* out = reinterpret_cast<__half2*>(v.bounds + ((int64_t)w.page * v.h_kv + h) * 2 * D);
+#pragma unroll
+  for (int c = threadIdx.x; c < D; c += kThreads) {
+    const int side = c / (D / 2), e = c % (D / 2);
+    __half2 m = side ? hi_s[0][e] : lo_s[0][e];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) m = side ? __hmax2(m, hi_s[i][e]) : __hmin2(m, lo_s[i][e]);
+    if (w.s0 > 0) m = side ? __hmax2(m, out[c]) : __hmin2(m, out[c]);
+    out[c] = m;
+  }
 }
 
-// The same blocks the other way: eight channels a thread.
-template <typename T, int D>
+__device__ __forceinline__ float value_of(uint32_t code, float scale, float zero) {
+  return fmaf(scale, __uint_as_float(code | 0x4b000000u) - 8388608.0f, zero);
+}
+
+// The same blocks the other way: eight channels in a row of a token pair a thread.
+template <typename T, int D, int kThreads, int kSteps>
 __global__ void __launch_bounds__(kThreads) read_kernel(View v, Rows r, T* __restrict__ k, T* __restrict__ vv) {
   using L = Layout<D>;
-  constexpr int kLanes = D / 8, kSlots = kThreads / kLanes, NG = L::NG;
-  const int run = blockIdx.x % r.runs, u = blockIdx.x / r.runs, h = u % v.h_kv, b = u / v.h_kv;
+  constexpr int kLanes = D / 8, kPairs = kThreads / kLanes, NG = L::NG;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int h = blockIdx.x % v.h_kv, u = blockIdx.x / v.h_kv, run = u % r.runs, b = u / r.runs;
   const Run w = find_run<false>(v, r, b, run);
   if (w.page < 0) return;
   const uint8_t* page = v.pages + ((int64_t)w.page * v.h_kv + h) * L::kBytes;
-  const int l = threadIdx.x % kLanes, grp = l / 4, q = l % 4;
-  for (int s = w.s0 + threadIdx.x / kLanes; s < w.s1; s += kSlots) {
-    const int64_t at = (w.row + s - w.s0) * r.stride + (int64_t)h * D + 8 * l;
-    const int m = (s / 2 * NG + grp) * 2 + s % 2;
-    float x[8];
-    const uint32_t word = reinterpret_cast<const uint32_t*>(page + L::kKCodes)[(s * 4 + q) * NG + grp];
-    float sc = __half2float(reinterpret_cast<const __half*>(page + L::kKScales)[m]);
-    float z = __half2float(reinterpret_cast<const __half*>(page + L::kKZeros)[s * NG + grp]);
+  const int l = threadIdx.x % kLanes, grp = l / 4, q = l % 4, first = w.s0 / 2 + threadIdx.x / kLanes;
+  auto word = [&](int at, int index) { return __ldg(reinterpret_cast<const uint32_t*>(page + at) + index); };
+  uint32_t kc[kSteps][2], vc[kSteps][2], ks[kSteps], vs[kSteps], vz[kSteps];
+  uint16_t kz[kSteps][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(sc, (float)((word >> bit_off(e, 4)) & 15u), z);
-    Eight<T>::store(k + at, x);
-    const uint16_t* codes = reinterpret_cast<const uint16_t*>(page + L::kVCodes);
-    sc = __half2float(reinterpret_cast<const __half*>(page + L::kVScales)[m]);
-    z = __half2float(reinterpret_cast<const __half*>(page + L::kVZeros)[m]);
+  for (int i = 0; i < kSteps; ++i) {
+    const int pair = min(first + i * kPairs, kPage / 2 - 1), m = pair * NG + grp;  // past the run: not used
+    ks[i] = word(L::kKScales, m), vs[i] = word(L::kVScales, m), vz[i] = word(L::kVZeros, m);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint32_t half = codes[((s / 2 * 8 + 2 * q + j) * NG + grp) * 2 + s % 2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[4 * j + i] = fmaf(sc, (float)((half >> (4 * i)) & 15u), z);
+      kc[i][j] = word(L::kKCodes, ((2 * pair + j) * 4 + q) * NG + grp);
+      vc[i][j] = word(L::kVCodes, (pair * 8 + 2 * q + j) * NG + grp);
+      kz[i][j] = __ldg(reinterpret_cast<const uint16_t*>(page + L::kKZeros) + (2 * pair + j) * NG + grp);
     }
-    Eight<T>::store(vv + at, x);
   }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int s = 2 * (first + i * kPairs) + j;
+      if (s < w.s0 || s >= w.s1) continue;
+      const int64_t at = (w.row + s - w.s0) * r.stride + (int64_t)h * D + 8 * l;
+      float x[8], sc = __half2float(__ushort_as_half((uint16_t)(ks[i] >> (16 * j)))), z = __half2float(__ushort_as_half(kz[i][j]));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = value_of((kc[i][j] >> bit_off(e, 4)) & 15u, sc, z);
+      Eight<T>::store(k + at, x);
+      sc = __half2float(__ushort_as_half((uint16_t)(vs[i] >> (16 * j)))), z = __half2float(__ushort_as_half((uint16_t)(vz[i] >> (16 * j))));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = value_of((vc[i][e / 4] >> (16 * j + 4 * (e % 4))) & 15u, sc, z);
+      Eight<T>::store(vv + at, x);
+    }
 }
 
 static rdkv_status grid_of(const rdkv_q4_cache* c, Rows* r, int64_t* blocks) {
@@ -271,15 +441,26 @@ extern "C" size_t rdkv_q4_page_bytes(int32_t head_dim) {
   return head_dim == 128 ? Layout<128>::kBytes : head_dim == 64 ? Layout<64>::kBytes : 0;
 }
 
-#define RDKV_Q4_ROWS_LAUNCH(kernel, ptr)                                                                         \
-  switch (dtype * 256 + cache->head_dim) {                                                                       \
-    case RDKV_F16 * 256 + 64: kernel<__half, 64><<<(unsigned)blocks, kThreads, 0, cs>>>(view, r, (ptr __half*)k, (ptr __half*)v); break;     \
-    case RDKV_F16 * 256 + 128: kernel<__half, 128><<<(unsigned)blocks, kThreads, 0, cs>>>(view, r, (ptr __half*)k, (ptr __half*)v); break;   \
-    case RDKV_F32 * 256 + 64: kernel<float, 64><<<(unsigned)blocks, kThreads, 0, cs>>>(view, r, (ptr float*)k, (ptr float*)v); break;        \
-    case RDKV_F32 * 256 + 128: kernel<float, 128><<<(unsigned)blocks, kThreads, 0, cs>>>(view, r, (ptr float*)k, (ptr float*)v); break;      \
-    case RDKV_BF16 * 256 + 64: kernel<__nv_bfloat16, 64><<<(unsigned)blocks, kThreads, 0, cs>>>(view, r, (ptr __nv_bfloat16*)k, (ptr __nv_bfloat16*)v); break; \
-    default: kernel<__nv_bfloat16, 128><<<(unsigned)blocks, kThreads, 0, cs>>>(view, r, (ptr __nv_bfloat16*)k, (ptr __nv_bfloat16*)v);       \
-  }
+namespace {
+// Threads and steps that cover the token pairs n rows can touch in a page.
+template <typename T, int D, int kThreads, int kSteps>
+constexpr bool covers(int n) {
+  return std::min(kPage / 2, n / 2 + 1) <= kThreads / (D / 8) * kSteps;
+}
+template <typename T, int D>
+cudaError_t launch_write(unsigned blocks, const View& view, const Rows& r, const void* k, const void* v, cudaStream_t cs) {
+  const T *kt = static_cast<const T*>(k), *vt = static_cast<const T*>(v);
+  if (covers<T, D, 32, 1>(r.max_rows)) return launch_after(write_kernel<T, D, 32, 1>, dim3(blocks), 32, 0, cs, view, r, kt, vt);
+  if (covers<T, D, 128, 1>(r.max_rows)) return launch_after(write_kernel<T, D, 128, 1>, dim3(blocks), 128, 0, cs, view, r, kt, vt);
+  return launch_after(write_kernel<T, D, 256, D / 64>, dim3(blocks), 256, 0, cs, view, r, kt, vt);
+}
+template <typename T, int D>
+cudaError_t launch_read(unsigned blocks, const View& view, const Rows& r, void* k, void* v, cudaStream_t cs) {
+  T *kt = static_cast<T*>(k), *vt = static_cast<T*>(v);
+  if (covers<T, D, 32, 1>(r.max_rows)) return launch_after(read_kernel<T, D, 32, 1>, dim3(blocks), 32, 0, cs, view, r, kt, vt);
+  return launch_after(read_kernel<T, D, 256, D / 64>, dim3(blocks), 256, 0, cs, view, r, kt, vt);
+}
+}  // namespace
 
 extern "C" rdkv_status rdkv_q4_write(const rdkv_q4_cache* cache, int32_t dtype, const void* k, const void* v,
                                      int64_t row_stride, const int32_t* row_start, int32_t max_rows, void* stream) {
@@ -292,8 +473,13 @@ extern "C" rdkv_status rdkv_q4_write(const rdkv_q4_cache* cache, int32_t dtype, 
   if (st != RDKV_OK) return st;
   cudaStream_t cs = (cudaStream_t)stream;
   const View view = view_of(cache);
-  RDKV_Q4_ROWS_LAUNCH(write_kernel, const)
-  RDKV_CHECK_LAUNCH("4-bit cache write");
+  const bool wide = cache->head_dim == 128;
+  cudaError_t e;
+  if (dtype == RDKV_F16) e = (wide ? launch_write<__half, 128> : launch_write<__half, 64>)((unsigned)blocks, view, r, k, v, cs);
+  else if (dtype == RDKV_F32) e = (wide ? launch_write<float, 128> : launch_write<float, 64>)((unsigned)blocks, view, r, k, v, cs);
+  else e = (wide ? launch_write<__nv_bfloat16, 128> : launch_write<__nv_bfloat16, 64>)((unsigned)blocks, view, r, k, v, cs);
+  RDKV_TRY_CUDA(e, "4-bit cache write");
+  count_launch();
   return RDKV_OK;
 }
 
@@ -308,8 +494,13 @@ extern "C" rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, v
   if (st != RDKV_OK) return st;
   cudaStream_t cs = (cudaStream_t)stream;
   const View view = view_of(cache);
-  RDKV_Q4_ROWS_LAUNCH(read_kernel, )
-  RDKV_CHECK_LAUNCH("4-bit cache read");
+  const bool wide = cache->head_dim == 128;
+  cudaError_t e;
+  if (dtype == RDKV_F16) e = (wide ? launch_read<__half, 128> : launch_read<__half, 64>)((unsigned)blocks, view, r, k, v, cs);
+  else if (dtype == RDKV_F32) e = (wide ? launch_read<float, 128> : launch_read<float, 64>)((unsigned)blocks, view, r, k, v, cs);
+  else e = (wide ? launch_read<__nv_bfloat16, 128> : launch_read<__nv_bfloat16, 64>)((unsigned)blocks, view, r, k, v, cs);
+  RDKV_TRY_CUDA(e, "4-bit cache read");
+  count_launch();
   return RDKV_OK;
 }
 

@@ -119,15 +119,15 @@ __device__ __forceinline__ float load_q(const void* p, int64_t i, int dtype) {
 // ---------------------------------------------------------------- launches
 // Launches a kernel that waits (griddepcontrol.wait) before it touches global memory, so that its blocks may
 // be set up while the kernel before it on the stream ends.
-template <class Kernel, class Args>
-inline cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args& args) {
+template <class Kernel, class... Args>
+inline cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // ---------------------------------------------------------------- host checks
