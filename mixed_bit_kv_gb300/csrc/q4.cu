@@ -1,5 +1,7 @@
 // The 4-bit paged cache: rows quantised as they are written (rdkv_q4_write) and read back
 // (rdkv_q4_read), and the host checks that every rdkv_q4_* call makes.
+#include <type_traits>
+
 #include "q4.cuh"
 #include "stages.cuh"
 
@@ -211,7 +213,7 @@ __device__ __forceinline__ float2 extremes_of(const Raw<__nv_bfloat16>& r, const
 // quotient: the fp16 scale is the same unless the product lies within 8 units of its last place of the middle
 // of two fp16 values (or below fp16's normal range).  (x - zero) / scale as (x - zero) r, r within 2^-22 of
 // 1 / scale: with every quotient of the group in (-0.49, 15.49), rounding gives the same code unless the
-// product is within 2^-12 of a half-integer.  What fails a test, and groups that hold a NaN or values past
+// product is within 2^-16 of a half-integer (the product and the quotient differ by less than 2^-18).  What fails a test, and groups that hold a NaN or values past
 // fp16's range, goes the exact way.
 struct Codes {
   float c[8];
@@ -232,6 +234,7 @@ __device__ __noinline__ Codes quantise8_exact(float mn, float mx, float x0, floa
   }
   return r;
 }
+__device__ __noinline__ float rounded_quotient(float d, float scale) { return fminf(fmaxf(rintf(__fdiv_rn(d, scale)), 0.0f), 15.0f); }
 template <typename T>
 __device__ __forceinline__ Codes quantise8(const Raw<T>& raw) {
   float x[8];
@@ -258,10 +261,22 @@ __device__ __forceinline__ Codes quantise8(const Raw<T>& raw) {
     r.c[i] = c.x, r.c[i + 1] = c.y;
     asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(far) : "f"(fabsf(e.x)), "f"(fabsf(e.y)));
   }
-  // (far is NaN when a value is; the comparisons are false for NaN)
-  const bool fine = far <= 0.5f - 0.000244140625f && step >= 6.1035156e-5f && step < 8000.0f && below > 16u && (ex.x - r.p.zero) * rs > -0.49f &&
-                    (ex.y - r.p.zero) * rs < 15.49f && ex.x >= -kHalfMax && ex.y <= kHalfMax;
-  if (!fine) r = quantise8_exact(ex.x, ex.y, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
+  // (the comparisons are false for NaN and infinities)
+  bool fine = (step >= 6.1035156e-5f) & (step < 8000.0f) & (below > 16u);
+  if constexpr (!std::is_same<T, __half>::value) {  // fp16 rows: zero is the smallest value itself, none is too large
+    fine &= ((ex.x - r.p.zero) * rs > -0.49f) & ((ex.y - r.p.zero) * rs < 15.49f) & (ex.x >= -kHalfMax) & (ex.y <= kHalfMax);
+  }
+  fine &= far == far;  // a NaN among the values
+  if (!fine) {
+    r = quantise8_exact(ex.x, ex.y, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
+  } else if (far > 0.5f - 0.0000152587890625f) {
+    // next to a half-integer: the quotient itself (fp16 rows meet exact ones in one of some ten warps)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = x[i] - r.p.zero;
+      if (fabsf(fmaf(d, rs, -r.c[i])) > 0.5f - 0.0000152587890625f) r.c[i] = rounded_quotient(d, r.p.scale);
+    }
+  }
   return r;
 }
 // Four codes in 16 bits, the first lowest.
@@ -282,7 +297,7 @@ __device__ __forceinline__ __half2 cut_half2(float lo, float hi) {
 // sectors.  Every load of a thread's kSteps pairs is under way before the first is used.  kThreads, kSteps:
 // as few as the call's rows need (a decode step has one token a sequence).
 template <typename T, int D, int kThreads, int kSteps>
-__global__ void __launch_bounds__(kThreads) write_kernel(View v, Rows r, const T* __restrict__ k, const T* __restrict__ vv) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) write_kernel(View v, Rows r, const T* __restrict__ k, const T* __restrict__ vv) {
   using L = Layout<D>;
   constexpr int kLanes = D / 8, kPairs = kThreads / kLanes, kWarps = kThreads / 32, NG = L::NG;
   __shared__ __half2 lo_s[kWarps][D / 2], hi_s[kWarps][D / 2];
@@ -307,48 +322,53 @@ __global__ void __launch_bounds__(kThreads) write_kernel(View v, Rows r, const T
       kr[i][j] = load_raw(k + at + 8 * q, 4);
       vr[i][j] = load_raw(vv + at + 4 * q, 16);
     }
+  auto pairs = [&](auto full) {
+    constexpr bool kFull = decltype(full)::value;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int pair = first + i * kPairs, m = pair * NG + grp;
-    const bool in[2] = {2 * pair >= w.s0 && 2 * pair < w.s1, 2 * pair + 1 >= w.s0 && 2 * pair + 1 < w.s1};
-    if (!__any_sync(0xffffffffu, in[0] || in[1])) continue;
-    uint32_t word[2][2];
-    QParams pp[2];
+    for (int i = 0; i < kSteps; ++i) {
+      const int pair = first + i * kPairs, m = pair * NG + grp;
+      const bool in[2] = {kFull || (2 * pair >= w.s0 && 2 * pair < w.s1), kFull || (2 * pair + 1 >= w.s0 && 2 * pair + 1 < w.s1)};
+      if (!kFull && !__any_sync(0xffffffffu, in[0] || in[1])) continue;
+      uint32_t word[2][2];
+      QParams pp[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const Codes c = quantise8(kr[i][j]);
-      pp[j] = c.p;
-      if (in[j]) {
-        reinterpret_cast<uint32_t*>(page + L::kKCodes)[((2 * pair + j) * 4 + q) * NG + grp] =
-            low_halves(nibbles(c.c[0], c.c[2], c.c[4], c.c[6]), nibbles(c.c[1], c.c[3], c.c[5], c.c[7]));
-        if (q == 0) reinterpret_cast<uint16_t*>(page + L::kKZeros)[(2 * pair + j) * NG + grp] = c.p.zero_h;
+      for (int j = 0; j < 2; ++j) {
+        const Codes c = quantise8(kr[i][j]);
+        pp[j] = c.p;
+        if (in[j]) {
+          reinterpret_cast<uint32_t*>(page + L::kKCodes)[((2 * pair + j) * 4 + q) * NG + grp] =
+              low_halves(nibbles(c.c[0], c.c[2], c.c[4], c.c[6]), nibbles(c.c[1], c.c[3], c.c[5], c.c[7]));
+          if (q == 0) reinterpret_cast<uint16_t*>(page + L::kKZeros)[(2 * pair + j) * NG + grp] = c.p.zero_h;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 y = fma_f32x2(make_float2(c.p.scale, c.p.scale), make_float2(c.c[2 * e], c.c[2 * e + 1]), make_float2(c.p.zero, c.p.zero));
-          const __half2 z = cut_half2(y.x, y.y);
-          lo[e] = __hmin2(lo[e], z), hi[e] = __hmax2(hi[e], z);
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = fma_f32x2(make_float2(c.p.scale, c.p.scale), make_float2(c.c[2 * e], c.c[2 * e + 1]), make_float2(c.p.zero, c.p.zero));
+            const __half2 z = cut_half2(y.x, y.y);
+            lo[e] = __hmin2(lo[e], z), hi[e] = __hmax2(hi[e], z);
+          }
         }
       }
-    }
-    auto store_pair = [&](int at, int index, uint32_t even, uint32_t odd) {
-      if (in[0] && in[1]) reinterpret_cast<uint32_t*>(page + at)[index] = low_halves(even, odd);
-      else if (in[0]) reinterpret_cast<uint16_t*>(page + at)[2 * index] = (uint16_t)even;
-      else if (in[1]) reinterpret_cast<uint16_t*>(page + at)[2 * index + 1] = (uint16_t)odd;
-    };
-    if (q == 0) store_pair(L::kKScales, m, pp[0].scale_h, pp[1].scale_h);
+      auto store_pair = [&](int at, int index, uint32_t even, uint32_t odd) {
+        if (in[0] && in[1]) reinterpret_cast<uint32_t*>(page + at)[index] = low_halves(even, odd);
+        else if (in[0]) reinterpret_cast<uint16_t*>(page + at)[2 * index] = (uint16_t)even;
+        else if (in[1]) reinterpret_cast<uint16_t*>(page + at)[2 * index + 1] = (uint16_t)odd;
+      };
+      if (q == 0) store_pair(L::kKScales, m, pp[0].scale_h, pp[1].scale_h);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const Codes c = quantise8(vr[i][j]);
-      pp[j] = c.p;
-      word[j][0] = nibbles(c.c[0], c.c[1], c.c[2], c.c[3]), word[j][1] = nibbles(c.c[4], c.c[5], c.c[6], c.c[7]);
+      for (int j = 0; j < 2; ++j) {
+        const Codes c = quantise8(vr[i][j]);
+        pp[j] = c.p;
+        word[j][0] = nibbles(c.c[0], c.c[1], c.c[2], c.c[3]), word[j][1] = nibbles(c.c[4], c.c[5], c.c[6], c.c[7]);
+      }
+      store_pair(L::kVCodes, (pair * 8 + q) * NG + grp, word[0][0], word[1][0]);
+      store_pair(L::kVCodes, (pair * 8 + q + 4) * NG + grp, word[0][1], word[1][1]);
+      if (q == 0) {
+        store_pair(L::kVScales, m, pp[0].scale_h, pp[1].scale_h);
+        store_pair(L::kVZeros, m, pp[0].zero_h, pp[1].zero_h);
+      }
     }
-    store_pair(L::kVCodes, (pair * 8 + q) * NG + grp, word[0][0], word[1][0]);
-    store_pair(L::kVCodes, (pair * 8 + q + 4) * NG + grp, word[0][1], word[1][1]);
-    if (q == 0) {
-      store_pair(L::kVScales, m, pp[0].scale_h, pp[1].scale_h);
-      store_pair(L::kVZeros, m, pp[0].zero_h, pp[1].zero_h);
-    }
-  }
+  };
+  if (w.s0 == 0 && w.s1 == kPage) pairs(std::true_type());
+  else pairs(std::false_type());
   if (!v.bounds) return;
   // the page's bounds: the pairs of a warp, the block's warps, and what the page held before
 #pragma unroll
