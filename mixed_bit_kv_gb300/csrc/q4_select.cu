@@ -52,6 +52,8 @@ __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
 template <int D>
 __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(SelectArgs a) {
   constexpr int NC = D / 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % 32, g = lane / 4, qd = lane % 4;
   const int row = blockIdx.y, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
   const int P = pages_seen(a, b, t);
@@ -185,6 +187,8 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a) {
   __shared__ float part_f[kPickWarps][3];
   __shared__ int3 part[kPickWarps];
   __shared__ int list_n;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int row = blockIdx.x, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
   const int P = pages_seen(a, b, t);
@@ -356,11 +360,11 @@ extern "C" rdkv_status rdkv_q4_select(const rdkv_q4_cache* cache, int32_t dtype,
   const int64_t most = std::max<int64_t>(1, 8LL * num_sms() / geo.rows);
   const dim3 grid((unsigned)std::min<int64_t>(ceil_div(geo.tiles, kScoreWarps), most), (unsigned)geo.rows);
   const size_t smem = 4 * (size_t)std::min(cache->page_stride, kPickShared);
-  if (cache->head_dim == 128) score_kernel<128><<<grid, 32 * kScoreWarps, 0, cs>>>(a);
-  else score_kernel<64><<<grid, 32 * kScoreWarps, 0, cs>>>(a);
-  RDKV_CHECK_LAUNCH("4-bit cache page scores");
-  if (cache->head_dim == 128) pick_kernel<128><<<(unsigned)geo.rows, kPickThreads, smem, cs>>>(a);
-  else pick_kernel<64><<<(unsigned)geo.rows, kPickThreads, smem, cs>>>(a);
-  RDKV_CHECK_LAUNCH("4-bit cache page selection");
+  const bool wide = cache->head_dim == 128;
+  RDKV_TRY_CUDA(launch_after(wide ? score_kernel<128> : score_kernel<64>, grid, 32 * kScoreWarps, 0, cs, a), "4-bit cache page scores");
+  count_launch();
+  RDKV_TRY_CUDA(launch_after(wide ? pick_kernel<128> : pick_kernel<64>, dim3((unsigned)geo.rows), kPickThreads, smem, cs, a),
+                "4-bit cache page selection");
+  count_launch();
   return RDKV_OK;
 }

@@ -758,6 +758,7 @@ class Compressor:
 
 
 # ---------------------------------------------------------------- 4-bit cache, quantised as it is written
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device: torch.cuda.current_stream() costs a microsecond more
 _Q4_DTYPES = {torch.float16: RDKV_F16, torch.float32: RDKV_F32, torch.bfloat16: RDKV_BF16}
 
 
@@ -830,16 +831,14 @@ class Q4Cache:
         return ws
 
 
-def _q4_on(cache, stream, call, *args):
-    """call(cache, *args, stream pointer) with `stream` (default: the device's current one) and the cache's
-    device current, so that what the call allocates belongs to that stream."""
+def _q4_elsewhere(cache, stream, call, *args):
+    """call(cache, *args) with `stream` (or the device's current one) and the cache's device current, so that
+    what the call allocates belongs to that stream."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return call(cache, *args, stream.cuda_stream)
-    if cache._index == torch.cuda.current_device():
-        return call(cache, *args, torch._C._cuda_getCurrentRawStream(cache._index))
+            return call(cache, *args)
     with torch.cuda.device(cache.device):
-        return call(cache, *args, torch._C._cuda_getCurrentRawStream(cache._index))
+        return call(cache, *args)
 
 
 def _q4_index(cache, t, n, name):
@@ -848,7 +847,23 @@ def _q4_index(cache, t, n, name):
     return None if t is None else t.data_ptr()
 
 
+def _q4_remember(cache, key, found):
+    if len(cache._seen) >= 256:
+        cache._seen.clear()
+    cache._seen[key] = found
+
+
 def _q4_rows(cache, k, v, row_start, max_rows):
+    """(dtype code, row stride, max_rows) of rows k, v [rows, h_kv, D] or [batch, n, h_kv, D]."""
+    key = k.shape, v.shape, k.stride(), v.stride(), k.dtype, v.dtype, k.device, v.device, row_start is None, max_rows
+    found = cache._seen.get(key)
+    if found is None:
+        found = _q4_check_rows(cache, k, v, row_start, max_rows)
+        _q4_remember(cache, key, found)
+    return found
+
+
+def _q4_check_rows(cache, k, v, row_start, max_rows):
     """(dtype code, row stride, max_rows) of rows k, v [rows, h_kv, D] or [batch, n, h_kv, D]."""
     _q4_require(k.shape == v.shape and k.dtype == v.dtype and k.dtype in _Q4_DTYPES and k.dim() in (3, 4)
                 and k.shape[-2:] == (cache.h_kv, cache.head_dim) and k.device == v.device == cache.device,
@@ -883,23 +898,19 @@ def rdkv_q4_write(cache, k, v, row_start=None, max_rows=None, stream=None):
     """Quantises rows k, v into the cache: [batch, n, h_kv, D], the last n tokens of every sequence, or
     [rows, h_kv, D] with row_start int32 [batch + 1] (sequence b's rows, at most max_rows of them).
     cache.lens must already count them."""
-    _q4_on(cache, stream, _q4_write, k, v, row_start, max_rows)
-
-
-def _q4_write(cache, k, v, row_start, max_rows, s):
+    if stream is not None or cache._index != torch.cuda.current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q4_write, k, v, row_start, max_rows)
     start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
     code, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
-    _check(lib().rdkv_q4_write(cache._ref, code, k.data_ptr(), v.data_ptr(), stride, start, n, s))
+    _check(lib().rdkv_q4_write(cache._ref, code, k.data_ptr(), v.data_ptr(), stride, start, n, _raw_stream(cache._index)))
 
 
 def rdkv_q4_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype=torch.float16, out=None, stream=None):
     """Rows back as (k, v): max_rows of every sequence from position first (int32 [batch], default 0), as
     [batch, max_rows, h_kv, D], or with row_start (int32 [batch + 1]) as [n_rows, h_kv, D].  `out`: a pair
     of tensors to fill instead of new ones.  Rows past a sequence's length are not written."""
-    return _q4_on(cache, stream, _q4_read, max_rows, row_start, first, n_rows, dtype, out)
-
-
-def _q4_read(cache, max_rows, row_start, first, n_rows, dtype, out, s):
+    if stream is not None or cache._index != torch.cuda.current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q4_read, max_rows, row_start, first, n_rows, dtype, out)
     start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
     at = _q4_index(cache, first, cache.batch, "first")
     if out is None:
@@ -909,10 +920,12 @@ def _q4_read(cache, max_rows, row_start, first, n_rows, dtype, out, s):
         else:
             _q4_require(n_rows is not None, "row_start needs n_rows, the rows of the outputs")
             shape = (n_rows, cache.h_kv, cache.head_dim)
-        out = torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device)
-    k, v = out
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
     code, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
-    _check(lib().rdkv_q4_read(cache._ref, code, k.data_ptr(), v.data_ptr(), stride, start, at, n, s))
+    _check(lib().rdkv_q4_read(cache._ref, code, k.data_ptr(), v.data_ptr(), stride, start, at, n, _raw_stream(cache._index)))
     return k, v
 
 
@@ -921,7 +934,8 @@ def _q4_queries(cache, q):
     key = q.shape, q.stride(), q.dtype, q.device
     found = cache._seen.get(key)
     if found is None:
-        found = cache._seen[key] = _q4_check_queries(cache, q)
+        found = _q4_check_queries(cache, q)
+        _q4_remember(cache, key, found)
     return found
 
 
@@ -942,18 +956,18 @@ def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None
     """Attention of the newest tokens' queries q [batch, n_q, h_q, D] (or [batch, h_q, D]) over the cache:
     (out in q's shape and out_dtype, lse fp32 without D).  sel: pages int32 [batch, n_q, h_kv, n_sel] (or
     without n_q) to attend instead of all.  out_dtype: q's type (default) or torch.float32."""
-    return _q4_on(cache, stream, _q4_attn, q, sel, out, lse, out_dtype, ws)
-
-
-def _q4_attn(cache, q, sel, out, lse, out_dtype, ws, s):
+    if stream is not None or cache._index != torch.cuda.current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q4_attn, q, sel, out, lse, out_dtype, ws)
+    s = _raw_stream(cache._index)
     code, h_q, n_q, stride = _q4_queries(cache, q)
     shape = q.shape
     if out is None:
+        _q4_require(out_dtype in (None, q.dtype, torch.float32), "out must be in q's type or fp32")
         out = torch.empty(shape, dtype=out_dtype or q.dtype, device=cache.device)
     else:
         _q4_require(out.shape == shape and out.is_contiguous() and out.device == cache.device
                     and out_dtype in (None, out.dtype), "out must be dense and in q's shape")
-    _q4_require(out.dtype in (q.dtype, torch.float32), "out must be in q's type or fp32")
+        _q4_require(out.dtype in (q.dtype, torch.float32), "out must be in q's type or fp32")
     if lse is None:
         lse = torch.empty(shape[:-1], dtype=torch.float32, device=cache.device)
     else:
@@ -973,10 +987,9 @@ def _q4_attn(cache, q, sel, out, lse, out_dtype, ws, s):
 def rdkv_q4_select(cache, q, n_keep, n_first=1, n_last=1, out=None, ws=None, stream=None):
     """Pages for rdkv_q4_attn's `sel`: int32 [batch, n_q, h_kv, n_keep] (without n_q for q [batch, h_q, D]),
     ascending, -1 behind the last: the first n_first, the last n_last and the best others."""
-    return _q4_on(cache, stream, _q4_select, q, n_keep, n_first, n_last, out, ws)
-
-
-def _q4_select(cache, q, n_keep, n_first, n_last, out, ws, s):
+    if stream is not None or cache._index != torch.cuda.current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q4_select, q, n_keep, n_first, n_last, out, ws)
+    s = _raw_stream(cache._index)
     code, h_q, n_q, stride = _q4_queries(cache, q)
     _q4_require(cache.bounds is not None, "the cache keeps no bounds")
     _q4_require(n_keep >= 1, f"n_keep {n_keep}")
@@ -996,4 +1009,6 @@ def _q4_select(cache, q, n_keep, n_first, n_last, out, ws, s):
 def rdkv_q4_status(cache, stream=None):
     """What the calls on this cache reported on the device since the last read (RDKV_OK: nothing);
     synchronises the stream."""
-    return _q4_on(cache, stream, lambda c, s: lib().rdkv_q4_status(c._ref, s))
+    if stream is not None or cache._index != torch.cuda.current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q4_status)
+    return lib().rdkv_q4_status(cache._ref, _raw_stream(cache._index))

@@ -176,7 +176,7 @@ def test_the_binding_refuses_wrong_tensors(L):
     with pytest.raises(rdkv.RDKVError):
         rdkv.Q4Cache(0, 1, 64, 64, "cpu")
     cache = rdkv.Q4Cache.__new__(rdkv.Q4Cache)       # the checks of the rows alone, on CPU tensors
-    cache.batch, cache.h_kv, cache.head_dim, cache.device = 2, 2, 64, torch.device("cpu")
+    cache.batch, cache.h_kv, cache.head_dim, cache.device, cache._seen = 2, 2, 64, torch.device("cpu"), {}
     rows = torch.zeros(2, 3, 2, 64, dtype=torch.float16)
     assert rdkv._q4_rows(cache, rows, rows, None, None) == (0, 128, 3)
     wide = torch.zeros(2, 3, 6, 64, dtype=torch.float16)
@@ -191,7 +191,6 @@ def test_the_binding_refuses_wrong_tensors(L):
     assert rdkv._q4_rows(cache, flat[:5], flat[:5], flat, 4) == (0, 128, 4)
     with pytest.raises(rdkv.RDKVError):
         rdkv._q4_rows(cache, flat[:5], flat[:5], None, None)
-    cache._seen = {}
     q = torch.zeros(2, 3, 4, 64)
     assert rdkv._q4_queries(cache, q) == (1, 4, 3, 256)
     assert rdkv._q4_queries(cache, torch.zeros(2, 3, 8, 64)[:, :, 4:]) == (1, 4, 3, 512)
