@@ -3,10 +3,10 @@
 //   score(page) = max over the G query heads of sum_c max(q_c lo_c, q_c hi_c)
 //               = max over heads of (max(q, 0) . hi + min(q, 0) . lo)
 //
-// Two kernels.  score_kernel takes the sums as tensor-core products (pages on M, the group's heads on N,
-// the 2 D bounds on K), each within eps of the exact sum; pick_kernel finds, per (sequence, query token, KV
-// head), an interval around the n-th best score, takes what lies above it by more than the error, and sums
-// only the few pages within the error again, to twice fp32's precision, so that the order next to the
+// The blocks of a row (sequence, query token, KV head) take the sums as tensor-core products (pages on M, the
+// group's heads on N, the 2 D bounds on K), each within eps of the exact sum.  The row's last block to finish
+// then finds an interval around the n-th best score, takes what lies above it by more than the error, and
+// sums only the few pages within the error again, to twice fp32's precision, so that the order next to the
 // border is the exact one.
 #include "q4.cuh"
 
@@ -21,12 +21,13 @@ struct SelectArgs {
   float* error;  // [rows][tiles]: bound of a tile's scores' errors
   int32_t* list;  // [rows][page_stride]: pages near the border
   float2* value;  // [rows][page_stride]: their sums, high and low part
+  int32_t* tickets;  // [rows] blocks that have written their scores
   int64_t q_stride;
   int dtype, n_q, G, keep, first, last, tiles;
 };
 
 constexpr int kTilePages = 16;
-constexpr int kScoreWarps = 4;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
 
 // Pages of row (b, t) that hold a key its query token sees.
 __device__ __forceinline__ int pages_seen(const SelectArgs& a, int b, int t) {
@@ -48,19 +49,12 @@ __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// One warp a tile of 16 pages: every bound is read once, 16 bytes a lane and load, all in flight together.
+// This warp's tiles of 16 pages (tile, tile + step, ..): every bound is read once, 16 bytes a lane and load, a
+// tile's loads all in flight together.
 template <int D>
-__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(SelectArgs a) {
+__device__ __forceinline__ void score_tiles(const SelectArgs& a, int row, int b, int t, int h, int P, int tile, int step) {
   constexpr int NC = D / 32;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x % 32, g = lane / 4, qd = lane % 4;
-  const int row = blockIdx.y, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
-  const int P = pages_seen(a, b, t);
-  if (P <= a.keep) return;  // every page is kept
-  const int n_tiles = ceil_div(P, kTilePages);
-  int tile = blockIdx.x * kScoreWarps + threadIdx.x / 32;
-  if (tile >= n_tiles) return;
+  const int lane = threadIdx.x % 32, g = lane / 4, qd = lane % 4, bt = row / a.c.h_kv, n_tiles = ceil_div(P, kTilePages);
   // B: head g of the group, its channels 32 i + 8 qd .. + 7, positive and negative parts and magnitudes
   uint32_t pos[NC][4], neg[NC][4], mag[NC][4];
   float back;
@@ -105,7 +99,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(SelectArgs a) {
   // and bf16, and 2^-11 for fp32.
   const float rel = a.dtype == RDKV_F32 ? 0.0006103515625f + 0.0001220703125f : 0.0001220703125f;
   const float back0 = __shfl_sync(0xffffffffu, back, 8 * qd), back1 = __shfl_sync(0xffffffffu, back, 8 * qd + 4);
-  for (; tile < n_tiles; tile += gridDim.x * kScoreWarps) {
+  for (; tile < n_tiles; tile += step) {
     uint4 lo[2][NC], hi[2][NC];
     bool bad[2];
 #pragma unroll
@@ -166,95 +160,120 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ bool above(float2 a, float2 b) { return a.x > b.x || (a.x == b.x && a.y > b.y); }
 
-constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
-constexpr int kPickShared = 12288;  // scores that are kept in shared memory (longer rows are read through L2)
+constexpr int kShared = 11264;  // scores that are kept in shared memory (longer rows are read through L2)
+constexpr int kMids = 7;        // inner ends of the eight parts an interval is cut into
 
-// Sum over the block, for every thread.
-__device__ __forceinline__ int3 block_sum(int3 v, int3* part) {
-  v.x = __reduce_add_sync(0xffffffffu, v.x), v.y = __reduce_add_sync(0xffffffffu, v.y), v.z = __reduce_add_sync(0xffffffffu, v.z);
+struct Counts {
+  int n[kMids + 1];
+};
+// Sums over the block, for every thread (one barrier: the two places of `part` take turns).
+__device__ __forceinline__ Counts block_sum(Counts v, Counts* part, int turn) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int j = 0; j <= kMids; ++j) v.n[j] = __reduce_add_sync(0xffffffffu, v.n[j]);
+  part += kWarps * (turn & 1);
+  if (lane == 0) part[threadIdx.x / 32] = v;
   __syncthreads();
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-  __syncthreads();
-  const int3 w = part[threadIdx.x % kPickWarps];
-  const bool once = threadIdx.x % 32 < kPickWarps;
-  return make_int3(__reduce_add_sync(0xffffffffu, once ? w.x : 0), __reduce_add_sync(0xffffffffu, once ? w.y : 0),
-                   __reduce_add_sync(0xffffffffu, once ? w.z : 0));
+  const Counts w = part[lane % kWarps];
+#pragma unroll
+  for (int j = 0; j <= kMids; ++j) v.n[j] = __reduce_add_sync(0xffffffffu, lane < kWarps ? w.n[j] : 0);
+  return v;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a) {
+__global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   extern __shared__ float score_s[];
-  __shared__ float part_f[kPickWarps][3];
-  __shared__ int3 part[kPickWarps];
-  __shared__ int list_n;
+  __shared__ float part_f[kWarps][3];
+  __shared__ Counts part[2 * kWarps];
+  __shared__ int list_n, last_s;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int row = blockIdx.x, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
+  const int row = blockIdx.y, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
   const int P = pages_seen(a, b, t);
   int32_t* sel = a.sel + (int64_t)row * a.keep;
   if (P <= a.keep) {
-    for (int i = tid; i < a.keep; i += kPickThreads) sel[i] = i < P ? i : -1;
+    if (blockIdx.x == 0)
+      for (int i = tid; i < a.keep; i += kThreads) sel[i] = i < P ? i : -1;
     return;
   }
+  const int blocks = min((int)gridDim.x, ceil_div(ceil_div(P, kTilePages), kWarps));
+  if ((int)blockIdx.x >= blocks) return;
+  score_tiles<D>(a, row, b, t, h, P, blockIdx.x * kWarps + warp, blocks * kWarps);
+  __syncthreads();
+  if (tid == 0) {
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.tickets + row) : "memory");
+    last_s = before == blocks - 1;
+    if (last_s) a.tickets[row] = 0;
+    list_n = 0;
+  }
+  __syncthreads();
+  if (!last_s) return;
   float* score = a.score + (int64_t)row * a.c.page_stride;
   const int lo_p = a.first, hi_p = P - a.last, want = a.keep - a.first - a.last;  // of hi_p - lo_p > want pages
   float top = -INFINITY, low = INFINITY, eps = 0.0f;
-  const bool here = P <= kPickShared;
-  for (int p = tid; p < P; p += kPickThreads) {
+  const bool here = P <= kShared;
+  for (int p = tid; p < P; p += kThreads) {
     const float s = __ldcg(score + p);
     if (here) score_s[p] = s;
     if (p >= lo_p && p < hi_p) top = fmaxf(top, s), low = fminf(low, s);
   }
-  for (int i = tid; i < ceil_div(P, kTilePages); i += kPickThreads) eps = fmaxf(eps, __ldcg(a.error + (int64_t)row * a.tiles + i));
+  for (int i = tid; i < ceil_div(P, kTilePages); i += kThreads) eps = fmaxf(eps, __ldcg(a.error + (int64_t)row * a.tiles + i));
   for (int d = 16; d; d >>= 1) {
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
     eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, d));
   }
   if (lane == 0) part_f[warp][0] = top, part_f[warp][1] = low, part_f[warp][2] = eps;
-  if (tid == 0) list_n = 0;
   __syncthreads();
-  for (int w = 0; w < kPickWarps; ++w) top = fmaxf(top, part_f[w][0]), low = fminf(low, part_f[w][1]), eps = fmaxf(eps, part_f[w][2]);
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_f[w][0]), low = fminf(low, part_f[w][1]), eps = fmaxf(eps, part_f[w][2]);
   if (!(eps <= FLT_MAX)) eps = FLT_MAX;
   if (here) score = score_s;
   if (want > 0) {
     // [lo, hi) holds the want-th best score: at least `want` are >= lo, fewer are >= hi
     float lo = low, hi = top < FLT_MAX ? nextafterf(top, INFINITY) : INFINITY;
-    for (int turn = 0; turn < 40; ++turn) {
-      const float m1 = 0.75f * lo + 0.25f * fminf(hi, FLT_MAX), m2 = 0.5f * lo + 0.5f * fminf(hi, FLT_MAX),
-                  m3 = 0.25f * lo + 0.75f * fminf(hi, FLT_MAX);
-      if (hi - lo <= eps || !(m2 > lo && m2 < hi)) break;
-      int3 n = make_int3(0, 0, 0);
-      for (int p = lo_p + tid; p < hi_p; p += kPickThreads) {
+    int turn = 0;
+    for (; turn < 40; ++turn) {
+      const float end = fminf(hi, FLT_MAX);
+      float mid[kMids];
+#pragma unroll
+      for (int j = 0; j < kMids; ++j) mid[j] = (0.125f * (kMids - j)) * lo + (0.125f * (j + 1)) * end;
+      if (hi - lo <= eps || !(mid[kMids / 2] > lo && mid[kMids / 2] < hi)) break;
+      Counts n = {};
+      for (int p = lo_p + tid; p < hi_p; p += kThreads) {
         const float s = score[p];
-        n.x += s >= m1, n.y += s >= m2, n.z += s >= m3;
+#pragma unroll
+        for (int j = 0; j < kMids; ++j) n.n[j] += s >= mid[j];
       }
-      n = block_sum(n, part);
-      if (n.z >= want) lo = fmaxf(lo, m3);
-      else if (n.y >= want) lo = m2, hi = m3 > m2 ? m3 : hi;
-      else if (n.x >= want) lo = fmaxf(lo, m1), hi = m2;
-      else hi = m1 > lo ? m1 : m2;
+      n = block_sum(n, part, turn);
+      // the last end that enough scores reach, and the one after it
+#pragma unroll
+      for (int j = kMids - 1; j >= 0; --j)
+        if (n.n[j] < want) hi = fminf(hi, mid[j]);
+#pragma unroll
+      for (int j = 0; j < kMids; ++j)
+        if (n.n[j] >= want) lo = fmaxf(lo, mid[j]);
     }
     // in: above the interval by more than twice the error; near: within it
     const float sure = hi + 2.0f * eps, out = lo - 2.0f * eps;
-    int3 n = make_int3(0, 0, 0);
-    for (int p = lo_p + tid; p < hi_p; p += kPickThreads) {
+    Counts n = {};
+    for (int p = lo_p + tid; p < hi_p; p += kThreads) {
       const float s = score[p];
       const bool in = s > sure, near = !in && s >= out;
-      n.x += in, n.y += near;
+      n.n[0] += in, n.n[1] += near;
       if (near) a.list[(int64_t)row * a.c.page_stride + atomicAdd(&list_n, 1)] = p;
       score[p] = in ? INFINITY : near ? 0.0f : -INFINITY;
     }
-    n = block_sum(n, part);
-    const int need = want - n.x, near = n.y;
+    n = block_sum(n, part, turn);
+    const int need = want - n.n[0], near = n.n[1];
     const int32_t* list = a.list + (int64_t)row * a.c.page_stride;
     if (near <= need) {
-      for (int i = tid; i < near; i += kPickThreads) score[list[i]] = INFINITY;
+      for (int i = tid; i < near; i += kThreads) score[list[i]] = INFINITY;
     } else {
       // their sums again, a page a warp
       float2* value = a.value + (int64_t)row * a.c.page_stride;
-      for (int i = warp; i < near; i += kPickWarps) {
+      for (int i = warp; i < near; i += kWarps) {
         const int phys = __ldg(a.c.page_table + (int64_t)b * a.c.page_stride + list[i]);
         float2 best = make_float2(-INFINITY, 0.0f);
         if (phys >= 0 && phys < a.c.n_pages) {
@@ -280,7 +299,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a) {
         if (lane == 0) value[i] = best;
       }
       __syncthreads();
-      for (int i = tid; i < near; i += kPickThreads) {
+      for (int i = tid; i < near; i += kThreads) {
         const float2 v = value[i];
         const int p = list[i];
         int before = 0;
@@ -289,9 +308,9 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a) {
       }
     }
   }
-  __syncthreads();
+  __syncthreads();  // (also: both places of part are free)
   // the kept pages in order: each thread its run of pages
-  const int per = ceil_div(P, kPickThreads), p0 = min(P, tid * per), p1 = min(P, p0 + per);
+  const int per = ceil_div(P, kThreads), p0 = min(P, tid * per), p1 = min(P, p0 + per);
   auto kept = [&](int p) { return p < lo_p || p >= hi_p || (want > 0 && score[p] == INFINITY); };
   int n = 0;
   for (int p = p0; p < p1; ++p) n += kept(p);
@@ -300,10 +319,10 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a) {
     const int x = __shfl_up_sync(0xffffffffu, at, d);
     if (lane >= d) at += x;
   }
-  if (lane == 31) part[warp].x = at;
+  if (lane == 31) part[warp].n[0] = at;
   __syncthreads();
   at -= n;
-  for (int w = 0; w < warp; ++w) at += part[w].x;
+  for (int w = 0; w < warp; ++w) at += part[w].n[0];
   for (int p = p0; p < p1 && n > 0; ++p)
     if (kept(p) && at < a.keep) sel[at++] = p;
 }
@@ -315,6 +334,7 @@ using namespace rdkv;
 using namespace rdkv::q4;
 
 namespace {
+constexpr int kMaxRows = 65535;  // the grid's second size
 struct SelectGeometry {
   int64_t rows;
   int tiles;
@@ -325,7 +345,7 @@ SelectGeometry select_geometry(const rdkv_q4_cache* c, int n_q) {
   o.rows = (int64_t)c->batch * n_q * c->h_kv;
   o.tiles = ceil_div(c->page_stride, kTilePages);
   const int64_t pages = o.rows * c->page_stride;
-  o.value_at = 0;
+  o.value_at = 4 * (kMaxRows + 1);  // after the tickets, whose place is the same for every shape
   o.error_at = (size_t)align_up(8 * pages, 256);
   o.list_at = o.error_at + (size_t)align_up(4 * o.rows * o.tiles, 256);
   o.bytes = o.list_at + 2 * (size_t)align_up(4 * pages, 256);
@@ -346,24 +366,21 @@ extern "C" rdkv_status rdkv_q4_select(const rdkv_q4_cache* cache, int32_t dtype,
   RDKV_REQUIRE(n_keep >= 1 && n_first >= 0 && n_last >= 0 && (int64_t)n_first + n_last <= n_keep, RDKV_ERR_INVALID_ARG,
                "n_keep=%d n_first=%d n_last=%d", n_keep, n_first, n_last);
   const SelectGeometry geo = select_geometry(cache, n_q);
-  RDKV_REQUIRE(geo.rows <= 65535, RDKV_ERR_UNSUPPORTED, "more than 65,535 (sequence, query token, KV head) rows");
+  RDKV_REQUIRE(geo.rows <= kMaxRows, RDKV_ERR_UNSUPPORTED, "more than 65,535 (sequence, query token, KV head) rows");
   RDKV_REQUIRE(ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= geo.bytes, RDKV_ERR_WORKSPACE,
                "selection workspace too small (%zu < %zu) or unaligned", ws_bytes, geo.bytes);
   char* w = static_cast<char*>(ws);
   const SelectArgs a{view_of(cache), q, sel,
                      reinterpret_cast<float*>(w + geo.list_at + align_up(4 * geo.rows * cache->page_stride, 256)),
                      reinterpret_cast<float*>(w + geo.error_at), reinterpret_cast<int32_t*>(w + geo.list_at),
-                     reinterpret_cast<float2*>(w + geo.value_at), q_stride, dtype, n_q, h_q / cache->h_kv, n_keep, n_first, n_last,
+                     reinterpret_cast<float2*>(w + geo.value_at), reinterpret_cast<int32_t*>(w), q_stride, dtype, n_q, h_q / cache->h_kv, n_keep, n_first, n_last,
                      geo.tiles};
   cudaStream_t cs = (cudaStream_t)stream;
   // a tile a warp, as far as about four blocks an SM go; warps take further tiles in turn
-  const int64_t most = std::max<int64_t>(1, 8LL * num_sms() / geo.rows);
-  const dim3 grid((unsigned)std::min<int64_t>(ceil_div(geo.tiles, kScoreWarps), most), (unsigned)geo.rows);
-  const size_t smem = 4 * (size_t)std::min(cache->page_stride, kPickShared);
-  const bool wide = cache->head_dim == 128;
-  RDKV_TRY_CUDA(launch_after(wide ? score_kernel<128> : score_kernel<64>, grid, 32 * kScoreWarps, 0, cs, a), "4-bit cache page scores");
-  count_launch();
-  RDKV_TRY_CUDA(launch_after(wide ? pick_kernel<128> : pick_kernel<64>, dim3((unsigned)geo.rows), kPickThreads, smem, cs, a),
+  const int64_t most = std::max<int64_t>(1, 4LL * num_sms() / geo.rows);
+  const dim3 grid((unsigned)std::min<int64_t>(ceil_div(geo.tiles, kWarps), most), (unsigned)geo.rows);
+  const size_t smem = 4 * (size_t)std::min(cache->page_stride, kShared);
+  RDKV_TRY_CUDA(launch_after(cache->head_dim == 128 ? select_kernel<128> : select_kernel<64>, grid, kThreads, smem, cs, a),
                 "4-bit cache page selection");
   count_launch();
   return RDKV_OK;

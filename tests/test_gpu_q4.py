@@ -363,6 +363,28 @@ def test_near_scores_are_told_apart():
     assert rdkv.rdkv_q4_select(c, q.to(DEV), 50)[0, 0].tolist() == exp
 
 
+@pytest.mark.parametrize("P,keep,first,last", [(11264, 100, 1, 1), (11265, 64, 0, 2), (20011, 3000, 5, 5), (20011, 1, 0, 0)])
+def test_selection_over_rows_longer_than_shared_memory(P, keep, first, last):
+    D, h = 64, 2
+    c = rdkv.Q4Cache(1, h, D, 64 * P, DEV, pages=torch.zeros(1, h, 80 * D, dtype=torch.uint8, device=DEV).expand(P, -1, -1).contiguous(),
+                     lens=torch.tensor([64 * P - 7], dtype=torch.int32, device=DEV))
+    g = torch.Generator().manual_seed(P)
+    e = torch.randn(P, h, 2, D, generator=g).sort(2).values.half()
+    c.bounds.copy_(e)
+    q = torch.randn(1, 3 * h, D, generator=g).half()
+    for _ in range(2):
+        sel = rdkv.rdkv_q4_select(c, q.to(DEV), keep, n_first=first, n_last=last)
+        for j in range(h):
+            s = O.q4_scores(q[0, 3 * j:3 * j + 3].double().numpy(), e[:, j].numpy())
+            assert sel[0, j].tolist() == O.q4_select(s, keep, first, last)
+    # the same workspace serves other shapes in between
+    small, kh, vh = _filled([64 * 9], 1, 64, torch.float16)
+    small._ws = c._ws
+    qs = _rows(1, 2, 64, torch.float16, 1)
+    rdkv.rdkv_q4_select(small, qs.to(DEV), 3)
+    assert torch.equal(rdkv.rdkv_q4_select(c, q.to(DEV), keep, n_first=first, n_last=last), sel)
+
+
 def test_a_callers_own_pages():
     lens = [64 * 9 + 3, 70]
     c, kh, vh = _filled(lens, 2, 64, torch.float16)
