@@ -161,31 +161,34 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ bool above(float2 a, float2 b) { return a.x > b.x || (a.x == b.x && a.y > b.y); }
 
 constexpr int kShared = 11264;  // scores that are kept in shared memory (longer rows are read through L2)
-constexpr int kMids = 7;        // inner ends of the eight parts an interval is cut into
+constexpr int kBins = kThreads;  // parts an interval is cut into, a thread each
 
-struct Counts {
-  int n[kMids + 1];
-};
-// Sums over the block, for every thread (one barrier: the two places of `part` take turns).
-__device__ __forceinline__ Counts block_sum(Counts v, Counts* part, int turn) {
-  const int lane = threadIdx.x % 32;
-#pragma unroll
-  for (int j = 0; j <= kMids; ++j) v.n[j] = __reduce_add_sync(0xffffffffu, v.n[j]);
-  part += kWarps * (turn & 1);
-  if (lane == 0) part[threadIdx.x / 32] = v;
+// Sum of v over the threads before this one, and over all of them (two barriers).
+__device__ __forceinline__ int2 block_scan(int v, int* part) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int in = v;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, in, d);
+    if (lane >= d) in += x;
+  }
+  if (lane == 31) part[warp] = in;
   __syncthreads();
-  const Counts w = part[lane % kWarps];
+  int before = in - v, all = 0;
 #pragma unroll
-  for (int j = 0; j <= kMids; ++j) v.n[j] = __reduce_add_sync(0xffffffffu, lane < kWarps ? w.n[j] : 0);
-  return v;
+  for (int w = 0; w < kWarps; ++w) {
+    before += w < warp ? part[w] : 0;
+    all += part[w];
+  }
+  __syncthreads();
+  return make_int2(before, all);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   extern __shared__ float score_s[];
   __shared__ float part_f[kWarps][3];
-  __shared__ Counts part[2 * kWarps];
-  __shared__ int list_n, last_s;
+  __shared__ int part[kWarps], bin_s[kBins];
+  __shared__ int list_n, sure_n, last_s, found_s;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -206,12 +209,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
     asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.tickets + row) : "memory");
     last_s = before == blocks - 1;
     if (last_s) a.tickets[row] = 0;
-    list_n = 0;
+    list_n = 0, sure_n = 0;
   }
   __syncthreads();
   if (!last_s) return;
   float* score = a.score + (int64_t)row * a.c.page_stride;
   const int lo_p = a.first, hi_p = P - a.last, want = a.keep - a.first - a.last;  // of hi_p - lo_p > want pages
+  bin_s[tid] = 0;
   float top = -INFINITY, low = INFINITY, eps = 0.0f;
   const bool here = P <= kShared;
   for (int p = tid; p < P; p += kThreads) {
@@ -231,42 +235,50 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   if (!(eps <= FLT_MAX)) eps = FLT_MAX;
   if (here) score = score_s;
   if (want > 0) {
-    // [lo, hi) holds the want-th best score: at least `want` are >= lo, fewer are >= hi
-    float lo = low, hi = top < FLT_MAX ? nextafterf(top, INFINITY) : INFINITY;
-    int turn = 0;
-    for (; turn < 40; ++turn) {
-      const float end = fminf(hi, FLT_MAX);
-      float mid[kMids];
-#pragma unroll
-      for (int j = 0; j < kMids; ++j) mid[j] = (0.125f * (kMids - j)) * lo + (0.125f * (j + 1)) * end;
-      if (hi - lo <= eps || !(mid[kMids / 2] > lo && mid[kMids / 2] < hi)) break;
-      Counts n = {};
+    // [lo, hi] holds the want-th best score: its part of 256, counted from the top, then that one's part, until
+    // the interval is narrower than the error (an interval widened by the rounding of its ends still holds it)
+    float lo = low, hi = top;
+    int above_n = 0;  // scores above the interval
+    for (int turn = 0; turn < 8 && hi - lo > eps; ++turn) {
+      const float from = lo, width = hi - lo, per = (float)kBins / width;
+      if (!(width < FLT_MAX)) break;
+#pragma unroll 4
       for (int p = lo_p + tid; p < hi_p; p += kThreads) {
         const float s = score[p];
-#pragma unroll
-        for (int j = 0; j < kMids; ++j) n.n[j] += s >= mid[j];
+        if (s >= from && s <= hi) atomicAdd(bin_s + kBins - 1 - min(kBins - 1, (int)((s - from) * per)), 1);
       }
-      n = block_sum(n, part, turn);
-      // the last end that enough scores reach, and the one after it
-#pragma unroll
-      for (int j = kMids - 1; j >= 0; --j)
-        if (n.n[j] < want) hi = fminf(hi, mid[j]);
-#pragma unroll
-      for (int j = 0; j < kMids; ++j)
-        if (n.n[j] >= want) lo = fmaxf(lo, mid[j]);
+      __syncthreads();
+      const int mine = bin_s[tid];
+      bin_s[tid] = 0;
+      const int before = above_n + block_scan(mine, part).x;  // thread 0 has the top part
+      if (before < want && before + mine >= want) found_s = tid;
+      __syncthreads();
+      const int j = kBins - 1 - found_s;
+      const float slack = 4.0f * FLT_EPSILON * fmaxf(fabsf(from), fabsf(hi)) + 4.0f * FLT_EPSILON * width;
+      const float l = from + width * ((float)j / kBins) - slack, u = from + width * ((float)(j + 1) / kBins) + slack;
+      const float was = hi - lo;
+      lo = fmaxf(lo, l), hi = fminf(hi, u);
+      if (!(hi - lo < 0.5f * was)) break;
+      int over = 0;
+#pragma unroll 4
+      for (int p = lo_p + tid; p < hi_p; p += kThreads) over += score[p] > hi;
+      above_n = block_scan(over, part).y;
     }
     // in: above the interval by more than twice the error; near: within it
     const float sure = hi + 2.0f * eps, out = lo - 2.0f * eps;
-    Counts n = {};
+    int in_n = 0;
+#pragma unroll 4
     for (int p = lo_p + tid; p < hi_p; p += kThreads) {
       const float s = score[p];
       const bool in = s > sure, near = !in && s >= out;
-      n.n[0] += in, n.n[1] += near;
+      in_n += in;
       if (near) a.list[(int64_t)row * a.c.page_stride + atomicAdd(&list_n, 1)] = p;
-      score[p] = in ? INFINITY : near ? 0.0f : -INFINITY;
+      score[p] = in ? INFINITY : -INFINITY;
     }
-    n = block_sum(n, part, turn);
-    const int need = want - n.n[0], near = n.n[1];
+    in_n = __reduce_add_sync(0xffffffffu, in_n);
+    if (lane == 0 && in_n) atomicAdd(&sure_n, in_n);
+    __syncthreads();
+    const int need = want - sure_n, near = list_n;
     const int32_t* list = a.list + (int64_t)row * a.c.page_stride;
     if (near <= need) {
       for (int i = tid; i < near; i += kThreads) score[list[i]] = INFINITY;
@@ -278,17 +290,22 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
         float2 best = make_float2(-INFINITY, 0.0f);
         if (phys >= 0 && phys < a.c.n_pages) {
           const __half* e = a.c.bounds + ((int64_t)phys * a.c.h_kv + h) * 2 * D;
-          float l[D / 32], u[D / 32];
+          float l[D / 32], u[D / 32], x[8][D / 32];
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) l[c] = __half2float(e[32 * c + lane]), u[c] = __half2float(e[D + 32 * c + lane]);
-#pragma unroll 1
-          for (int g = 0; g < a.G; ++g) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+              x[g][c] = g < a.G ? load_q(a.q, (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 32 * c + lane, a.dtype) : 0.0f;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            if (g >= a.G) break;
             float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-              const float x = load_q(a.q, (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 32 * c + lane, a.dtype);
-              const float y = x > 0.0f ? u[c] : l[c], p = x * y;
-              sum = add2(sum, make_float2(p, fmaf(x, y, -p)));
+              const float y = x[g][c] > 0.0f ? u[c] : l[c], p = x[g][c] * y;
+              sum = add2(sum, make_float2(p, fmaf(x[g][c], y, -p)));
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1)
@@ -308,23 +325,28 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
       }
     }
   }
-  __syncthreads();  // (also: both places of part are free)
-  // the kept pages in order: each thread its run of pages
-  const int per = ceil_div(P, kThreads), p0 = min(P, tid * per), p1 = min(P, p0 + per);
-  auto kept = [&](int p) { return p < lo_p || p >= hi_p || (want > 0 && score[p] == INFINITY); };
-  int n = 0;
-  for (int p = p0; p < p1; ++p) n += kept(p);
-  int at = n;
-  for (int d = 1; d < 32; d <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, at, d);
-    if (lane >= d) at += x;
-  }
-  if (lane == 31) part[warp].n[0] = at;
   __syncthreads();
-  at -= n;
-  for (int w = 0; w < warp; ++w) at += part[w].n[0];
-  for (int p = p0; p < p1 && n > 0; ++p)
-    if (kept(p) && at < a.keep) sel[at++] = p;
+  // the kept pages in order, 32 of a warp at a time: each warp counts its run of pages, then writes them
+  const int words = ceil_div(P, 32), per = ceil_div(words, kWarps), w0 = min(words, warp * per), w1 = min(words, w0 + per);
+  auto kept = [&](int w) {
+    const int p = 32 * w + lane;
+    return __ballot_sync(0xffffffffu, p < P && (p < lo_p || p >= hi_p || (want > 0 && score[p] == INFINITY)));
+  };
+  int n = 0;
+#pragma unroll 4
+  for (int w = w0; w < w1; ++w) n += __popc(kept(w));
+  if (lane == 0) part[warp] = n;
+  __syncthreads();
+  int at = 0;
+  for (int w = 0; w < warp; ++w) at += part[w];
+  if (n == 0) return;
+#pragma unroll 4
+  for (int w = w0; w < w1; ++w) {
+    const uint32_t mask = kept(w);
+    const int to = at + __popc(mask & ((1u << lane) - 1u));
+    if ((mask >> lane & 1) && to < a.keep) sel[to] = 32 * w + lane;
+    at += __popc(mask);
+  }
 }
 
 }  // namespace q4
@@ -338,7 +360,7 @@ constexpr int kMaxRows = 65535;  // the grid's second size
 struct SelectGeometry {
   int64_t rows;
   int tiles;
-  size_t error_at, list_at, value_at, bytes;
+  size_t value_at, error_at, list_at, score_at, bytes;
 };
 SelectGeometry select_geometry(const rdkv_q4_cache* c, int n_q) {
   SelectGeometry o;
@@ -346,9 +368,10 @@ SelectGeometry select_geometry(const rdkv_q4_cache* c, int n_q) {
   o.tiles = ceil_div(c->page_stride, kTilePages);
   const int64_t pages = o.rows * c->page_stride;
   o.value_at = 4 * (kMaxRows + 1);  // after the tickets, whose place is the same for every shape
-  o.error_at = (size_t)align_up(8 * pages, 256);
+  o.error_at = o.value_at + (size_t)align_up(8 * pages, 256);
   o.list_at = o.error_at + (size_t)align_up(4 * o.rows * o.tiles, 256);
-  o.bytes = o.list_at + 2 * (size_t)align_up(4 * pages, 256);
+  o.score_at = o.list_at + (size_t)align_up(4 * pages, 256);
+  o.bytes = o.score_at + (size_t)align_up(4 * pages, 256);
   return o;
 }
 }  // namespace
@@ -371,7 +394,7 @@ extern "C" rdkv_status rdkv_q4_select(const rdkv_q4_cache* cache, int32_t dtype,
                "selection workspace too small (%zu < %zu) or unaligned", ws_bytes, geo.bytes);
   char* w = static_cast<char*>(ws);
   const SelectArgs a{view_of(cache), q, sel,
-                     reinterpret_cast<float*>(w + geo.list_at + align_up(4 * geo.rows * cache->page_stride, 256)),
+                     reinterpret_cast<float*>(w + geo.score_at),
                      reinterpret_cast<float*>(w + geo.error_at), reinterpret_cast<int32_t*>(w + geo.list_at),
                      reinterpret_cast<float2*>(w + geo.value_at), reinterpret_cast<int32_t*>(w), q_stride, dtype, n_q, h_q / cache->h_kv, n_keep, n_first, n_last,
                      geo.tiles};

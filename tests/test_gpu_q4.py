@@ -396,6 +396,43 @@ def test_a_callers_own_pages():
 
 
 # ---------------------------------------------------------------- bad device data, streams, graphs
+@pytest.mark.parametrize("lens,h,G,T", [([64 * 47 - 3] * 25, 4, 5, 1), ([64 * 300], 1, 8, 3), ([70, 64 * 40, 0], 2, 3, 2), ([1], 1, 1, 64)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nothing_is_written_outside_workspaces_and_outputs(D, lens, h, G, T):
+    """Guard words behind every workspace and output stay as they were; the counters are zero again."""
+    c, _, _ = _filled(lens, h, D, torch.bfloat16)
+    B = len(lens)
+    q = _rows(B * T, h * G, D, torch.bfloat16, 9).view(B, T, h * G, D).to(DEV)
+
+    def guarded(shape, dtype):
+        n = math.prod(shape)
+        big = torch.full((n + 4096,), 77, dtype=dtype, device=DEV)
+        return big, big[:n].view(shape)
+
+    for kind in ("select", "attn", "attn sel", "attn f32"):
+        fn = rdkv.lib().rdkv_q4_select_workspace_bytes if kind == "select" else rdkv.lib().rdkv_q4_attn_workspace_bytes
+        nb = fn(ctypes.byref(c.c), h * G, T)
+        big = torch.zeros(nb + 4096, dtype=torch.uint8, device=DEV)
+        big[nb:] = 0xA5
+        ws = big[:nb]
+        for _ in range(2):
+            if kind == "select":
+                guards = [guarded((B, T, h, 9), torch.int32)]
+                rdkv.rdkv_q4_select(c, q, 9, out=guards[0][1], ws=ws)
+                sel = guards[0][1].clone()
+                assert (sel >= -1).all() and (sel < c.page_table.shape[1]).all()
+            else:
+                guards = [guarded(q.shape, torch.float32 if kind == "attn f32" else q.dtype), guarded(q.shape[:-1], torch.float32)]
+                rdkv.rdkv_q4_attn(c, q, sel=sel if kind == "attn sel" else None, out=guards[0][1], lse=guards[1][1], ws=ws)
+        assert (big[nb:] == 0xA5).all(), kind
+        for b, x in guards:
+            assert (b[x.numel():] == 77).all(), kind
+        # counters: where the tickets lie, everything is zero again
+        t = ws[:4 * 65536] if kind == "select" else ws[nb - -(-4 * B * T * h // 256) * 256:]
+        assert (t == 0).all(), kind
+    assert rdkv.rdkv_q4_status(c) == 0
+
+
 def test_bad_pages_and_lengths_are_left_out_and_reported():
     lens = [200, 130]
     c, kh, vh = _filled(lens, 1, 64, torch.float16, stride=4)
