@@ -202,6 +202,7 @@ struct Warp {
   using L = Layout<D>;
   uint32_t q[2][NG][4];  // A registers: rows g, and rows g + 8 (the chunk's second half, or the low parts of the first)
   uint32_t qz[2];        // A registers of the zeros' product
+  float qs[NG];          // (PREC) the same sums in fp32
   float scale[NT];        // 2^(15 - s): a row's logits are held times 2^(s - 15)
   float ref[NT], l[NT];   // the running maximum (base 2) and this lane's share of the sum
   float o[NT][NG][2][4];
@@ -280,6 +281,10 @@ struct Warp {
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
         sum[i] *= kK / 32768.0f;
       }
+      if constexpr (PREC) {
+#pragma unroll
+        for (int i = 0; i < NG; ++i) qs[i] = sum[i];
+      }
       // k slots 0 .. NG - 1: the sums' fp16 parts, the next NG: the remainders
       uint32_t hi[NG / 2], lo[NG / 2];
 #pragma unroll
@@ -324,7 +329,8 @@ struct Warp {
   // bits) or be hidden from some rows (row n of this lane sees low[n] of the page's tokens).
   template <bool kTail>
   __device__ __forceinline__ void page(const uint8_t* k, int g, int qd, int live, const int (&low)[NT]) {
-    constexpr float kK = 512.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+    constexpr float kUnit = PREC ? 1.0f : 16777216.0f;  // of the codes in the products
+    constexpr float kK = kUnit / 32768.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
     {  // The weights' exponent follows the largest value scale met, so that weight times scale stays in
        // fp16's range: with the weight at most 2^(4 + off) and the scale below 2^(e + 1), the product is
        // below 2^13, and off <= 11 keeps the weight itself in range.  (PREC: weights at most 2^off, products
@@ -357,15 +363,25 @@ struct Warp {
         uint32_t w[NG], sw[NG];
         lds_groups<NG>(k + L::kKCodes + ((tok + g) * 4 + qd) * NG * 4, w);
         lds_groups<NG>(k + L::kKScales + (tok / 2 + qd) * NG * 4, sw);
-        const uint32_t zw = reinterpret_cast<const uint32_t*>(k + L::kKZeros)[(tok + g) * (NG / 2) + (NG == 4 ? qd & 1 : 0)];
-        float z[4];
-        mma8z(z, qz[0], qz[1], zw);
+        float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (PREC) {  // the keys' middles (zero + 8 scale), in fp32
+          uint32_t zw[NG];
+          lds_groups<NG>(k + L::kKZeros + (tok + 2 * qd) * NG * 2, zw);
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {  // words 0 .. NG / 2 - 1: the even token's groups in pairs, then the odd one's
+            const float2 f = unpack2(sw[i]), e = unpack2(zw[i / 2]), o = unpack2(zw[NG / 2 + i / 2]);
+            z[0] = fmaf(fmaf(8.0f, f.x, i & 1 ? e.y : e.x), qs[i], z[0]);
+            z[1] = fmaf(fmaf(8.0f, f.y, i & 1 ? o.y : o.x), qs[i], z[1]);
+          }
+        } else {
+          mma8z(z, qz[0], qz[1], reinterpret_cast<const uint32_t*>(k + L::kKZeros)[(tok + g) * (NG / 2) + (NG == 4 ? qd & 1 : 0)]);
+        }
         float2 s[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[n] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          const Pairs p = code_pairs(w[i]);
+          const Pairs p = PREC ? centred_pairs(w[i]) : code_pairs(w[i]);
           float c[4];
           mma16z(c, q[0][i][0], q[1][i][0], q[0][i][1], q[1][i][1], p.a, p.b);
           mma16(c, q[0][i][2], q[1][i][2], q[0][i][3], q[1][i][3], p.c, p.d);
@@ -445,8 +461,9 @@ struct Warp {
             const float(&x)[4] = p[n][t];
             hi[n][t][0] = pack2(x[0], x[1]), hi[n][t][1] = pack2(x[2], x[3]);
             lo[n][t][0] = rest2(x[0], x[1], hi[n][t][0]), lo[n][t][1] = rest2(x[2], x[3], hi[n][t][1]);
-            if (t == 0) mma16z(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
-            else mma16(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
+            if (t == 0) mma16z(cz[n], z0, 0u, z1, 0u, lo[n][t][0], lo[n][t][1]);
+            else mma16(cz[n], z0, 0u, z1, 0u, lo[n][t][0], lo[n][t][1]);
+            mma16(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
           }
         }
       }
@@ -533,7 +550,7 @@ struct Warp {
           z0 = __shfl_sync(0xffffffffu, oz[n][0], 4 * i + qd), z1 = __shfl_sync(0xffffffffu, oz[n][1], 4 * i + qd);
         }
         const float(&c)[2][4] = o[n][i];
-        constexpr float a = PREC ? 1.0f : 16777216.0f, b = a / 16.0f;  // the codes' units
+        constexpr float a = PREC ? 1.0f : 16777216.0f, b = a / 16.0f;  // the codes' units, as in page()
         put(8 * n + 2 * qd, 32 * i + 4 * g, l0,
             make_float4(fmaf(c[0][0], a, z0), fmaf(c[0][2], b, z0), fmaf(c[1][0], a, z0), fmaf(c[1][2], b, z0)));
         put(8 * n + 2 * qd + 1, 32 * i + 4 * g, l1,
