@@ -135,10 +135,18 @@ __device__ __forceinline__ uint32_t minus(uint32_t w, uint32_t one) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&one));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ Pairs centred_pairs(uint32_t w) {
-  const Pairs p = code_pairs(w);
-  constexpr uint32_t k1024 = 0x64006400u, k1032 = 0x64086408u, k1152 = 0x64806480u;
-  return Pairs{minus(p.a | k1024, k1032), minus(p.b | k1024, k1152), minus(p.c | k1024, k1032), minus(p.d | k1024, k1152)};
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(bits));
+  return d;
+}
+// k1024: the exponent's bits, in a register that the compiler takes for a variable, so that mask and bits are
+// one instruction (it can hold one constant only).
+__device__ __forceinline__ Pairs centred_pairs(uint32_t w, uint32_t k1024) {
+  const uint32_t u = w >> 8;
+  constexpr uint32_t k1032 = 0x64086408u, k1152 = 0x64806480u;
+  return Pairs{minus(and_or(w, 0x000f000fu, k1024), k1032), minus(and_or(w, 0x00f000f0u, k1024), k1152),
+               minus(and_or(u, 0x000f000fu, k1024), k1032), minus(and_or(u, 0x00f000f0u, k1024), k1152)};
 }
 
 // A piece of a unit: ROWS x D sums and each row's reference (base 2) and sum of weights.
@@ -331,6 +339,8 @@ struct Warp {
   __device__ __forceinline__ void page(const uint8_t* k, int g, int qd, int live, const int (&low)[NT]) {
     constexpr float kUnit = PREC ? 1.0f : 16777216.0f;  // of the codes in the products
     constexpr float kK = kUnit / 32768.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+    uint32_t k1024;
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
     {  // The weights' exponent follows the largest value scale met, so that weight times scale stays in
        // fp16's range: with the weight at most 2^(4 + off) and the scale below 2^(e + 1), the product is
        // below 2^13, and off <= 11 keeps the weight itself in range.  (PREC: weights at most 2^off, products
@@ -381,7 +391,7 @@ struct Warp {
         for (int n = 0; n < NT; ++n) s[n] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          const Pairs p = PREC ? centred_pairs(w[i]) : code_pairs(w[i]);
+          const Pairs p = PREC ? centred_pairs(w[i], k1024) : code_pairs(w[i]);
           float c[4];
           mma16z(c, q[0][i][0], q[1][i][0], q[0][i][1], q[1][i][1], p.a, p.b);
           mma16(c, q[0][i][2], q[1][i][2], q[0][i][3], q[1][i][3], p.c, p.d);
@@ -416,8 +426,8 @@ struct Warp {
           rescale(n, f, qd);
         }
       }
-      // the weights, as fp16 parts and remainders, in the order of the values' products: 16 tokens a step
-      uint32_t hi[NT][kTurn / 16][2], lo[NT][kTurn / 16][2], s0[kTurn / 16][NG], s1[kTurn / 16][NG], w0[kTurn / 16][NG], w1[kTurn / 16][NG];
+      // the weights, in fp16 too, in the order of the values' products: 16 tokens a step
+      uint32_t hi[NT][kTurn / 16][2], s0[kTurn / 16][NG], s1[kTurn / 16][NG], w0[kTurn / 16][NG], w1[kTurn / 16][NG];
       float p[NT][kTurn / 16][4], cz[NT][4];
 #pragma unroll
       for (int t = 0; t < kTurn / 16; ++t) {
@@ -453,17 +463,16 @@ struct Warp {
             oz[0][i] += (x[0] * fmaf(8.0f, f0.x, a0.x) + x[1] * fmaf(8.0f, f0.y, a0.y)) +
                         (x[2] * fmaf(8.0f, f1.x, a1.x) + x[3] * fmaf(8.0f, f1.y, a1.y));
           }
-        } else {  // one product; rows g >= NG of its operand are zero
-          const uint32_t* zs = reinterpret_cast<const uint32_t*>(k + L::kVZeros) + g % NG;
-          const uint32_t z0 = zs[p0 * NG] & (g < NG ? keep0 : 0u), z1 = zs[p1 * NG] & (g < NG ? keep1 : 0u);
+        } else {  // the same as one product of the middles in fp16; rows g >= NG of its operand are zero
+          const uint32_t *zs = reinterpret_cast<const uint32_t*>(k + L::kVZeros) + g % NG, *ss = zs - L::kMeta / 4;
+          const uint32_t z0 = hfma2(ss[p0 * NG], 0x48004800u, zs[p0 * NG]) & (g < NG ? keep0 : 0u);
+          const uint32_t z1 = hfma2(ss[p1 * NG], 0x48004800u, zs[p1 * NG]) & (g < NG ? keep1 : 0u);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const float(&x)[4] = p[n][t];
             hi[n][t][0] = pack2(x[0], x[1]), hi[n][t][1] = pack2(x[2], x[3]);
-            lo[n][t][0] = rest2(x[0], x[1], hi[n][t][0]), lo[n][t][1] = rest2(x[2], x[3], hi[n][t][1]);
-            if (t == 0) mma16z(cz[n], z0, 0u, z1, 0u, lo[n][t][0], lo[n][t][1]);
-            else mma16(cz[n], z0, 0u, z1, 0u, lo[n][t][0], lo[n][t][1]);
-            mma16(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
+            if (t == 0) mma16z(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
+            else mma16(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
           }
         }
       }
@@ -480,8 +489,7 @@ struct Warp {
         float c[NT][2][4];
 #pragma unroll
         for (int t = 0; t < kTurn / 16; ++t) {
-          const Pairs x = PREC ? centred_pairs(w0[t][i]) : code_pairs(w0[t][i]);
-          const Pairs y = PREC ? centred_pairs(w1[t][i]) : code_pairs(w1[t][i]);
+          const Pairs x = centred_pairs(w0[t][i], k1024), y = centred_pairs(w1[t][i], k1024);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             uint32_t b0, b1;
@@ -500,9 +508,7 @@ struct Warp {
                 mma16(c[n][1], x.c, x.d, y.c, y.d, c0, c1);
               }
             } else {
-              // weight times scale, rounded to fp16 once: the weight as an fp16 part and its remainder
-              b0 = hfma2(hi[n][t][0], s0[t][i], hmul2(lo[n][t][0], s0[t][i]));
-              b1 = hfma2(hi[n][t][1], s1[t][i], hmul2(lo[n][t][1], s1[t][i]));
+              b0 = hmul2(hi[n][t][0], s0[t][i]), b1 = hmul2(hi[n][t][1], s1[t][i]);
             }
             if (t == 0 && !PREC) {
               mma16z(c[n][0], x.a, x.b, y.a, y.b, b0, b1);
@@ -550,7 +556,7 @@ struct Warp {
           z0 = __shfl_sync(0xffffffffu, oz[n][0], 4 * i + qd), z1 = __shfl_sync(0xffffffffu, oz[n][1], 4 * i + qd);
         }
         const float(&c)[2][4] = o[n][i];
-        constexpr float a = PREC ? 1.0f : 16777216.0f, b = a / 16.0f;  // the codes' units, as in page()
+        constexpr float a = 1.0f, b = 0.0625f;  // the codes' units
         put(8 * n + 2 * qd, 32 * i + 4 * g, l0,
             make_float4(fmaf(c[0][0], a, z0), fmaf(c[0][2], b, z0), fmaf(c[1][0], a, z0), fmaf(c[1][2], b, z0)));
         put(8 * n + 2 * qd + 1, 32 * i + 4 * g, l1,
