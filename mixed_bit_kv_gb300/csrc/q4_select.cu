@@ -20,10 +20,11 @@ struct SelectArgs {
   float* score;  // [rows][page_stride]
   float* error;  // [rows][tiles]: bound of a tile's scores' errors
   int32_t* list;  // [rows][page_stride]: pages near the border
+  uint32_t* mask;  // [rows][words]: kept pages, for rows that do not fit in shared memory
   float2* value;  // [rows][page_stride]: their sums, high and low part
   int32_t* tickets;  // [rows] blocks that have written their scores
   int64_t q_stride;
-  int dtype, n_q, G, keep, first, last, tiles;
+  int dtype, n_q, G, keep, first, last, tiles, words;
 };
 
 constexpr int kTilePages = 16;
@@ -160,8 +161,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ bool above(float2 a, float2 b) { return a.x > b.x || (a.x == b.x && a.y > b.y); }
 
-constexpr int kShared = 11264;  // scores that are kept in shared memory (longer rows are read through L2)
-constexpr int kBins = kThreads;  // parts an interval is cut into, a thread each
+constexpr int kShared = 8192;  // scores that are kept in shared memory (longer rows are read through L2)
+constexpr int kPer = 8, kBins = kPer * kThreads;  // parts an interval is cut into, eight a thread
+constexpr int kFew = 32;                          // pages near the border whose sums are taken a head a warp
 
 // Sum of v over the threads before this one, and over all of them (two barriers).
 __device__ __forceinline__ int2 block_scan(int v, int* part) {
@@ -187,8 +189,11 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   extern __shared__ float score_s[];
   __shared__ float part_f[kWarps][3];
-  __shared__ int part[kWarps], bin_s[kBins];
-  __shared__ int list_n, sure_n, last_s, found_s;
+  __shared__ __align__(16) int bin_s[kBins];
+  __shared__ int part[kWarps], list_s[kFew];
+  __shared__ uint32_t mask_s[kShared / 32];
+  __shared__ float2 value_s[kFew][8];
+  __shared__ int list_n, sure_n, last_s, found_s, found_n;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -215,7 +220,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   if (!last_s) return;
   float* score = a.score + (int64_t)row * a.c.page_stride;
   const int lo_p = a.first, hi_p = P - a.last, want = a.keep - a.first - a.last;  // of hi_p - lo_p > want pages
-  bin_s[tid] = 0;
+  int4* mine_s = reinterpret_cast<int4*>(bin_s) + 2 * tid;  // this thread's parts
+  mine_s[0] = mine_s[1] = make_int4(0, 0, 0, 0);
   float top = -INFINITY, low = INFINITY, eps = 0.0f;
   const bool here = P <= kShared;
   for (int p = tid; p < P; p += kThreads) {
@@ -234,11 +240,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_f[w][0]), low = fminf(low, part_f[w][1]), eps = fmaxf(eps, part_f[w][2]);
   if (!(eps <= FLT_MAX)) eps = FLT_MAX;
   if (here) score = score_s;
+  float lo = low, hi = top;
   if (want > 0) {
-    // [lo, hi] holds the want-th best score: its part of 256, counted from the top, then that one's part, until
-    // the interval is narrower than the error (an interval widened by the rounding of its ends still holds it)
-    float lo = low, hi = top;
+    // [lo, hi] holds the want-th best score: its part of 2048, counted from the top, then that one's part, until
+    // the interval is narrower than the error or holds few (an interval widened by the rounding of its ends
+    // still holds it)
     int above_n = 0;  // scores above the interval
+#pragma unroll 1
     for (int turn = 0; turn < 8 && hi - lo > eps; ++turn) {
       const float from = lo, width = hi - lo, per = (float)kBins / width;
       if (!(width < FLT_MAX)) break;
@@ -248,104 +256,136 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
         if (s >= from && s <= hi) atomicAdd(bin_s + kBins - 1 - min(kBins - 1, (int)((s - from) * per)), 1);
       }
       __syncthreads();
-      const int mine = bin_s[tid];
-      bin_s[tid] = 0;
-      const int before = above_n + block_scan(mine, part).x;  // thread 0 has the top part
-      if (before < want && before + mine >= want) found_s = tid;
+      const int4 x = mine_s[0], y = mine_s[1];
+      mine_s[0] = mine_s[1] = make_int4(0, 0, 0, 0);
+      const int n[kPer] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      const int mine = ((x.x + x.y) + (x.z + x.w)) + ((y.x + y.y) + (y.z + y.w));
+      int before = above_n + block_scan(mine, part).x;  // thread 0 has the top parts
+      if (before < want && before + mine >= want) {
+        int j = 0;
+#pragma unroll
+        for (int i = 0; i < kPer - 1; ++i)
+          if (j == i && before + n[i] < want) before += n[i], j = i + 1;
+        int in = n[0];
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) in = j == i ? n[i] : in;
+        found_s = kBins - 1 - (kPer * tid + j), found_n = in;
+      }
       __syncthreads();
-      const int j = kBins - 1 - found_s;
+      const int j = found_s;
       const float slack = 4.0f * FLT_EPSILON * fmaxf(fabsf(from), fabsf(hi)) + 4.0f * FLT_EPSILON * width;
       const float l = from + width * ((float)j / kBins) - slack, u = from + width * ((float)(j + 1) / kBins) + slack;
       const float was = hi - lo;
       lo = fmaxf(lo, l), hi = fminf(hi, u);
-      if (!(hi - lo < 0.5f * was)) break;
+      if (found_n <= 4 || !(hi - lo < 0.5f * was)) break;
       int over = 0;
 #pragma unroll 4
       for (int p = lo_p + tid; p < hi_p; p += kThreads) over += score[p] > hi;
       above_n = block_scan(over, part).y;
     }
-    // in: above the interval by more than twice the error; near: within it
-    const float sure = hi + 2.0f * eps, out = lo - 2.0f * eps;
+  }
+  // in: above the interval by more than twice the error, or one of the first or last; near: within it
+  const float sure = hi + 2.0f * eps, out = lo - 2.0f * eps;
+  uint32_t* mask = here ? mask_s : a.mask + (int64_t)row * a.words;
+  int32_t* list = a.list + (int64_t)row * a.c.page_stride;
+  const int words = ceil_div(P, 32);
+  {
     int in_n = 0;
 #pragma unroll 4
-    for (int p = lo_p + tid; p < hi_p; p += kThreads) {
-      const float s = score[p];
-      const bool in = s > sure, near = !in && s >= out;
-      in_n += in;
-      if (near) a.list[(int64_t)row * a.c.page_stride + atomicAdd(&list_n, 1)] = p;
-      score[p] = in ? INFINITY : -INFINITY;
+    for (int w = warp; w < words; w += kWarps) {
+      const int p = 32 * w + lane;
+      const bool mid = p >= lo_p && p < hi_p;
+      const float s = mid ? score[p] : -INFINITY;
+      const bool in = mid && want > 0 && s > sure, near = mid && want > 0 && !in && s >= out;
+      const uint32_t kept = __ballot_sync(0xffffffffu, p < P && (in || !mid)), mids = __ballot_sync(0xffffffffu, in);
+      if (lane == 0) mask[w] = kept;
+      in_n += __popc(mids);
+      if (near) {
+        const int i = atomicAdd(&list_n, 1);
+        list[i] = p;
+        if (i < kFew) list_s[i] = p;
+      }
     }
-    in_n = __reduce_add_sync(0xffffffffu, in_n);
     if (lane == 0 && in_n) atomicAdd(&sure_n, in_n);
-    __syncthreads();
-    const int need = want - sure_n, near = list_n;
-    const int32_t* list = a.list + (int64_t)row * a.c.page_stride;
-    if (near <= need) {
-      for (int i = tid; i < near; i += kThreads) score[list[i]] = INFINITY;
-    } else {
-      // their sums again, a page a warp
-      float2* value = a.value + (int64_t)row * a.c.page_stride;
-      for (int i = warp; i < near; i += kWarps) {
-        const int phys = __ldg(a.c.page_table + (int64_t)b * a.c.page_stride + list[i]);
-        float2 best = make_float2(-INFINITY, 0.0f);
-        if (phys >= 0 && phys < a.c.n_pages) {
-          const __half* e = a.c.bounds + ((int64_t)phys * a.c.h_kv + h) * 2 * D;
-          float l[D / 32], u[D / 32], x[8][D / 32];
+  }
+  __syncthreads();
+  const int need = want - sure_n, near = list_n;
+  auto keep_page = [&](int p) { atomicOr(mask + p / 32, 1u << p % 32); };
+  if (near <= need) {
+    for (int i = tid; i < near; i += kThreads) keep_page(list[i]);
+  } else if (need > 0) {
+    // their sums again: a head of a page a warp, or (many) a page a warp
+    float2* value = a.value + (int64_t)row * a.c.page_stride;
+    const bool few = near <= kFew;
+#pragma unroll 1
+    for (int task = warp; task < (few ? near * a.G : near); task += kWarps) {
+      const int i = few ? task / a.G : task, g0 = few ? task - i * a.G : 0, g1 = few ? g0 + 1 : a.G;
+      const int phys = __ldg(a.c.page_table + (int64_t)b * a.c.page_stride + (few ? list_s[i] : list[i]));
+      float2 best = make_float2(-INFINITY, 0.0f);
+      if (phys >= 0 && phys < a.c.n_pages) {
+        const __half* e = a.c.bounds + ((int64_t)phys * a.c.h_kv + h) * 2 * D;
+#pragma unroll 1
+        for (int g = g0; g < g1; ++g) {
+          float2 sum = make_float2(0.0f, 0.0f);
+          float x[D / 32], l[D / 32], u[D / 32];
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) l[c] = __half2float(e[32 * c + lane]), u[c] = __half2float(e[D + 32 * c + lane]);
-#pragma unroll
-          for (int g = 0; g < 8; ++g)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c)
-              x[g][c] = g < a.G ? load_q(a.q, (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 32 * c + lane, a.dtype) : 0.0f;
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            if (g >= a.G) break;
-            float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              const float y = x[g][c] > 0.0f ? u[c] : l[c], p = x[g][c] * y;
-              sum = add2(sum, make_float2(p, fmaf(x[g][c], y, -p)));
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1)
-              sum = add2(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, d), __shfl_xor_sync(0xffffffffu, sum.y, d)));
-            if (above(sum, best)) best = sum;
+          for (int c = 0; c < D / 32; ++c) {
+            x[c] = load_q(a.q, (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 32 * c + lane, a.dtype);
+            l[c] = __half2float(e[32 * c + lane]), u[c] = __half2float(e[D + 32 * c + lane]);
           }
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const float y = x[c] > 0.0f ? u[c] : l[c], p = x[c] * y;
+            sum = add2(sum, make_float2(p, fmaf(x[c], y, -p)));
+          }
+#pragma unroll 1
+          for (int d = 16; d; d >>= 1)
+            sum = add2(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, d), __shfl_xor_sync(0xffffffffu, sum.y, d)));
+          if (above(sum, best)) best = sum;
         }
-        if (lane == 0) value[i] = best;
+      }
+      if (lane == 0) {
+        if (few) value_s[i][g0] = best;
+        else value[i] = best;
+      }
+    }
+    __syncthreads();
+    if (few) {
+      if (warp == 0 && lane < near) {
+        float2 best = value_s[lane][0];
+        for (int g = 1; g < a.G; ++g)
+          if (above(value_s[lane][g], best)) best = value_s[lane][g];
+        value_s[lane][0] = best;
       }
       __syncthreads();
-      for (int i = tid; i < near; i += kThreads) {
-        const float2 v = value[i];
-        const int p = list[i];
-        int before = 0;
-        for (int j = 0; j < near; ++j) before += above(value[j], v) || (!above(v, value[j]) && list[j] < p);
-        if (before < need) score[p] = INFINITY;
+    }
+    auto value_of = [&](int j) { return few ? value_s[j][0] : value[j]; };
+    for (int i = tid; i < near; i += kThreads) {
+      const float2 v = value_of(i);
+      const int p = list[i];
+      int before = 0;
+      for (int j = 0; j < near; ++j) {
+        const float2 o = value_of(j);
+        before += above(o, v) || (!above(v, o) && list[j] < p);
       }
+      if (before < need) keep_page(p);
     }
   }
   __syncthreads();
-  // the kept pages in order, 32 of a warp at a time: each warp counts its run of pages, then writes them
-  const int words = ceil_div(P, 32), per = ceil_div(words, kWarps), w0 = min(words, warp * per), w1 = min(words, w0 + per);
-  auto kept = [&](int w) {
-    const int p = 32 * w + lane;
-    return __ballot_sync(0xffffffffu, p < P && (p < lo_p || p >= hi_p || (want > 0 && score[p] == INFINITY)));
-  };
-  int n = 0;
-#pragma unroll 4
-  for (int w = w0; w < w1; ++w) n += __popc(kept(w));
-  if (lane == 0) part[warp] = n;
-  __syncthreads();
-  int at = 0;
-  for (int w = 0; w < warp; ++w) at += part[w];
-  if (n == 0) return;
-#pragma unroll 4
-  for (int w = w0; w < w1; ++w) {
-    const uint32_t mask = kept(w);
-    const int to = at + __popc(mask & ((1u << lane) - 1u));
-    if ((mask >> lane & 1) && to < a.keep) sel[to] = 32 * w + lane;
-    at += __popc(mask);
+  // the kept pages in order: a run of words a lane
+  if (warp == 0) {
+    const int per = ceil_div(words, 32), w0 = min(words, lane * per), w1 = min(words, w0 + per);
+    int n = 0;
+    auto word = [&](int w) { return here ? mask[w] : __ldcg(mask + w); };  // (atomics have changed it in L2)
+    for (int w = w0; w < w1; ++w) n += __popc(word(w));
+    int at = n;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, at, d);
+      if (lane >= d) at += x;
+    }
+    at -= n;
+    for (int w = w0; w < w1; ++w)
+      for (uint32_t m = word(w); m && at < a.keep; m &= m - 1) sel[at++] = 32 * w + __ffs(m) - 1;
   }
 }
 
@@ -360,7 +400,7 @@ constexpr int kMaxRows = 65535;  // the grid's second size
 struct SelectGeometry {
   int64_t rows;
   int tiles;
-  size_t value_at, error_at, list_at, score_at, bytes;
+  size_t value_at, error_at, list_at, score_at, mask_at, bytes;
 };
 SelectGeometry select_geometry(const rdkv_q4_cache* c, int n_q) {
   SelectGeometry o;
@@ -371,7 +411,8 @@ SelectGeometry select_geometry(const rdkv_q4_cache* c, int n_q) {
   o.error_at = o.value_at + (size_t)align_up(8 * pages, 256);
   o.list_at = o.error_at + (size_t)align_up(4 * o.rows * o.tiles, 256);
   o.score_at = o.list_at + (size_t)align_up(4 * pages, 256);
-  o.bytes = o.score_at + (size_t)align_up(4 * pages, 256);
+  o.mask_at = o.score_at + (size_t)align_up(4 * pages, 256);
+  o.bytes = o.mask_at + (size_t)align_up(4 * o.rows * ceil_div(c->page_stride, 32), 256);
   return o;
 }
 }  // namespace
@@ -396,8 +437,9 @@ extern "C" rdkv_status rdkv_q4_select(const rdkv_q4_cache* cache, int32_t dtype,
   const SelectArgs a{view_of(cache), q, sel,
                      reinterpret_cast<float*>(w + geo.score_at),
                      reinterpret_cast<float*>(w + geo.error_at), reinterpret_cast<int32_t*>(w + geo.list_at),
+                     reinterpret_cast<uint32_t*>(w + geo.mask_at),
                      reinterpret_cast<float2*>(w + geo.value_at), reinterpret_cast<int32_t*>(w), q_stride, dtype, n_q, h_q / cache->h_kv, n_keep, n_first, n_last,
-                     geo.tiles};
+                     geo.tiles, ceil_div(cache->page_stride, 32)};
   cudaStream_t cs = (cudaStream_t)stream;
   // a tile a warp, as far as about four blocks an SM go; warps take further tiles in turn
   const int64_t most = std::max<int64_t>(1, 4LL * num_sms() / geo.rows);

@@ -363,7 +363,7 @@ def test_near_scores_are_told_apart():
     assert rdkv.rdkv_q4_select(c, q.to(DEV), 50)[0, 0].tolist() == exp
 
 
-@pytest.mark.parametrize("P,keep,first,last", [(11264, 100, 1, 1), (11265, 64, 0, 2), (20011, 3000, 5, 5), (20011, 1, 0, 0)])
+@pytest.mark.parametrize("P,keep,first,last", [(8192, 100, 1, 1), (8193, 64, 0, 2), (20011, 3000, 5, 5), (20011, 1, 0, 0)])
 def test_selection_over_rows_longer_than_shared_memory(P, keep, first, last):
     D, h = 64, 2
     c = rdkv.Q4Cache(1, h, D, 64 * P, DEV, pages=torch.zeros(1, h, 80 * D, dtype=torch.uint8, device=DEV).expand(P, -1, -1).contiguous(),
