@@ -577,8 +577,11 @@ rdkv_status rdkv_allocate_at_levels(const rdkv_shape* seg, int32_t per_head, con
  * RDKV_BF16).  pages and bounds 16-byte aligned. */
 enum { RDKV_BF16 = 2 };
 #define RDKV_Q4_PAGE_TOKENS 64
-/* Most query tokens of a sequence in one rdkv_q4_attn or rdkv_q4_select. */
+/* Most query tokens of a sequence in one rdkv_q4_attn or rdkv_q4_select; batch *
+ * n_q * h_kv is at most 65,535 in both (else RDKV_ERR_UNSUPPORTED). */
 #define RDKV_Q4_MAX_QUERIES 64
+/* Bytes at the start of their workspaces that hold counters. */
+#define RDKV_Q4_COUNTER_BYTES 262144
 typedef struct rdkv_q4_cache {
   int32_t batch, h_kv, head_dim;
   int32_t n_pages;            /* pages of the pool */
@@ -631,10 +634,12 @@ rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, voi
  * into the sequence's pages, position / 64; entries < 0 or past its last page
  * are left out; an index must not occur twice).
  *
- * ws: rdkv_q4_attn_workspace_bytes bytes, 16-byte aligned, zero-filled before its first use; every
- * call leaves its counters at zero again, so calls of any shape that need no
- * more bytes may follow one another on it.  Calls that may run at the same time
- * (two streams, two captured graphs) need one each. */
+ * ws: rdkv_q4_attn_workspace_bytes bytes, 16-byte aligned, its first
+ * RDKV_Q4_COUNTER_BYTES zero before its first use; every call leaves them zero
+ * again (unless it reported RDKV_ERR_TIMEOUT: clear them then), so calls of any
+ * shape that need no more bytes, of rdkv_q4_select too, may follow one another
+ * on it.  Calls that may run at the same time (two streams, two captured
+ * graphs) need one each. */
 size_t rdkv_q4_attn_workspace_bytes(const rdkv_q4_cache* cache, int32_t h_q, int32_t n_q);
 rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
                          int32_t n_q, const int32_t* sel, int32_t n_sel, void* out, int32_t out_dtype, float* lse,

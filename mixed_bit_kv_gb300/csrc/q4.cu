@@ -53,6 +53,9 @@ rdkv_status check_queries(const rdkv_q4_cache* c, int32_t h_q, int32_t n_q) {
   RDKV_REQUIRE(h_q / c->h_kv <= 8, RDKV_ERR_UNSUPPORTED, "group size %d > 8", h_q / c->h_kv);
   RDKV_REQUIRE(n_q >= 1, RDKV_ERR_INVALID_ARG, "n_q %d", n_q);
   RDKV_REQUIRE(n_q <= RDKV_Q4_MAX_QUERIES, RDKV_ERR_UNSUPPORTED, "n_q %d > %d", n_q, RDKV_Q4_MAX_QUERIES);
+  // a counter each in the workspaces; also a grid's second size
+  RDKV_REQUIRE((int64_t)c->batch * n_q * c->h_kv <= RDKV_Q4_COUNTER_BYTES / 4 - 1, RDKV_ERR_UNSUPPORTED,
+               "more than 65,535 (sequence, query token, KV head) triples");
   return RDKV_OK;
 }
 
@@ -88,18 +91,18 @@ struct Run {
 template <bool kWrite>
 __device__ __forceinline__ Run find_run(const View& v, const Rows& r, int b, int run) {
   Run o{0, -1, 0, 0};
-  const int len = __ldg(v.lens + b);
+  const int len = fetch(v.lens + b);
   const int64_t cap = (int64_t)v.page_stride * kPage;
   int64_t r0, n;
   if (r.start) {
-    r0 = __ldg(r.start + b);
-    n = (int64_t)__ldg(r.start + b + 1) - r0;
+    r0 = fetch(r.start + b);
+    n = (int64_t)fetch(r.start + b + 1) - r0;
   } else {
     r0 = (int64_t)b * r.max_rows;
     n = len > 0 || !kWrite ? r.max_rows : 0;
   }
   if (n == 0) return o;
-  const int64_t first = kWrite ? (int64_t)len - n : r.first ? (int64_t)__ldg(r.first + b) : 0;
+  const int64_t first = kWrite ? (int64_t)len - n : r.first ? (int64_t)fetch(r.first + b) : 0;
   if (n < 0 || n > r.max_rows || r0 < 0 || first < 0 || len < 0) {
     if (threadIdx.x == 0) raise(v, RDKV_ERR_INVALID_ARG);
     return o;
@@ -115,7 +118,7 @@ __device__ __forceinline__ Run find_run(const View& v, const Rows& r, int b, int
   o.s0 = (int)(max(first, t0) - t0);
   o.s1 = (int)(min(end, t0 + kPage) - t0);
   o.row = r0 + (t0 + o.s0 - first);
-  o.page = __ldg(v.page_table + (int64_t)b * v.page_stride + lp);
+  o.page = fetch(v.page_table + (int64_t)b * v.page_stride + lp);
   if (o.page < 0 || o.page >= v.n_pages) {
     if (threadIdx.x == 0) raise(v, RDKV_ERR_INVALID_ARG);
     o.page = -1;
@@ -152,7 +155,7 @@ struct Raw<float> {
 template <typename T>
 __device__ __forceinline__ Raw<T> load_raw(const T* p, int gap) {
   using W = decltype(Raw<T>::a);
-  return Raw<T>{__ldg(reinterpret_cast<const W*>(p)), __ldg(reinterpret_cast<const W*>(p + gap))};
+  return Raw<T>{fetch(reinterpret_cast<const W*>(p)), fetch(reinterpret_cast<const W*>(p + gap))};
 }
 __device__ __forceinline__ void widen(const Raw<__half>& r, float (&x)[8]) {
   const uint32_t w[4] = {r.a.x, r.a.y, r.b.x, r.b.y};
@@ -297,12 +300,11 @@ __device__ __forceinline__ __half2 cut_half2(float lo, float hi) {
 // sectors.  Every load of a thread's kSteps pairs is under way before the first is used.  kThreads, kSteps:
 // as few as the call's rows need (a decode step has one token a sequence).
 template <typename T, int D, int kThreads, int kSteps>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) write_kernel(View v, Rows r, const T* __restrict__ k, const T* __restrict__ vv) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) write_kernel(View v, Rows r, const T* k, const T* vv) {
   using L = Layout<D>;
   constexpr int kLanes = D / 8, kPairs = kThreads / kLanes, kWarps = kThreads / 32, NG = L::NG;
   __shared__ __half2 lo_s[kWarps][D / 2], hi_s[kWarps][D / 2];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   const int h = blockIdx.x % v.h_kv, u = blockIdx.x / v.h_kv, run = u % r.runs, b = u / r.runs;
   const Run w = find_run<true>(v, r, b, run);
   if (w.page < 0) return;
@@ -401,17 +403,16 @@ __device__ __forceinline__ float value_of(uint32_t code, float scale, float zero
 
 // The same blocks the other way: eight channels in a row of a token pair a thread.
 template <typename T, int D, int kThreads, int kSteps>
-__global__ void __launch_bounds__(kThreads) read_kernel(View v, Rows r, T* __restrict__ k, T* __restrict__ vv) {
+__global__ void __launch_bounds__(kThreads) read_kernel(View v, Rows r, T* k, T* vv) {
   using L = Layout<D>;
   constexpr int kLanes = D / 8, kPairs = kThreads / kLanes, NG = L::NG;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   const int h = blockIdx.x % v.h_kv, u = blockIdx.x / v.h_kv, run = u % r.runs, b = u / r.runs;
   const Run w = find_run<false>(v, r, b, run);
   if (w.page < 0) return;
   const uint8_t* page = v.pages + ((int64_t)w.page * v.h_kv + h) * L::kBytes;
   const int l = threadIdx.x % kLanes, grp = l / 4, q = l % 4, first = w.s0 / 2 + threadIdx.x / kLanes;
-  auto word = [&](int at, int index) { return __ldg(reinterpret_cast<const uint32_t*>(page + at) + index); };
+  auto word = [&](int at, int index) { return fetch(reinterpret_cast<const uint32_t*>(page + at) + index); };
   uint32_t kc[kSteps][2], vc[kSteps][2], ks[kSteps], vs[kSteps], vz[kSteps];
   uint16_t kz[kSteps][2];
 #pragma unroll
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(View v, Rows r, T* __res
     for (int j = 0; j < 2; ++j) {
       kc[i][j] = word(L::kKCodes, ((2 * pair + j) * 4 + q) * NG + grp);
       vc[i][j] = word(L::kVCodes, (pair * 8 + 2 * q + j) * NG + grp);
-      kz[i][j] = __ldg(reinterpret_cast<const uint16_t*>(page + L::kKZeros) + (2 * pair + j) * NG + grp);
+      kz[i][j] = fetch(reinterpret_cast<const uint16_t*>(page + L::kKZeros) + (2 * pair + j) * NG + grp);
     }
   }
 #pragma unroll

@@ -42,11 +42,41 @@ inline View view_of(const rdkv_q4_cache* c) {
               c->status};
 }
 
+// Loads of what the kernel before may have written.  These kernels are set up while that one still runs
+// (launch_after), so the read-only path, whose data must not change during the kernel, is not for them; and the
+// volatile statements keep their place behind the wait.
+__device__ __forceinline__ uint16_t fetch(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t fetch(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int32_t fetch(const int32_t* p) { return (int32_t)fetch(reinterpret_cast<const uint32_t*>(p)); }
+__device__ __forceinline__ uint2 fetch(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 fetch(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// Lets the next kernel on the stream be set up, and waits for the one before to end.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ void raise(const View& v, int code) { atomicMax(v.status, code); }
 
 // Tokens that sequence b holds, cut to what its page table can hold.
 __device__ __forceinline__ int held_tokens(const View& v, int b) {
-  const int n = __ldg(v.lens + b);
+  const int n = fetch(v.lens + b);
   return max(0, (int)min((int64_t)n, (int64_t)v.page_stride * kPage));
 }
 
@@ -56,7 +86,7 @@ struct Eight;  // eight consecutive channels
 template <>
 struct Eight<__half> {
   static __device__ __forceinline__ void load(const __half* p, float (&x)[8]) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 u = fetch(reinterpret_cast<const uint4*>(p));
     const __half2* h = reinterpret_cast<const __half2*>(&u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -76,7 +106,7 @@ struct Eight<__half> {
 template <>
 struct Eight<__nv_bfloat16> {
   static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 u = fetch(reinterpret_cast<const uint4*>(p));
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -95,8 +125,10 @@ struct Eight<__nv_bfloat16> {
 template <>
 struct Eight<float> {
   static __device__ __forceinline__ void load(const float* p, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    const uint4 a = fetch(reinterpret_cast<const uint4*>(p)), b = fetch(reinterpret_cast<const uint4*>(p) + 1);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
   }
   static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);

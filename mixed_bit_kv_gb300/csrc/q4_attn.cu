@@ -224,7 +224,7 @@ struct Warp {
   struct Rows {
     uint4 w[NT][NG][2];
   };
-  __device__ __forceinline__ static void fetch(const AttnArgs& a, const Unit& un, int g, int qd, Rows& r) {
+  __device__ __forceinline__ static void queries(const AttnArgs& a, const Unit& un, int g, int qd, Rows& r) {
     const int size = a.dtype == RDKV_F32 ? 4 : 2;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -234,8 +234,8 @@ struct Warp {
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + (real ? at * size : 0));
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        r.w[n][i][0] = real ? __ldg(src + 2 * i * size) : make_uint4(0, 0, 0, 0);
-        if (PREC) r.w[n][i][1] = real && size == 4 ? __ldg(src + 2 * i * size + 1) : make_uint4(0, 0, 0, 0);
+        r.w[n][i][0] = real ? fetch(src + 2 * i * size) : make_uint4(0, 0, 0, 0);
+        if (PREC) r.w[n][i][1] = real && size == 4 ? fetch(src + 2 * i * size + 1) : make_uint4(0, 0, 0, 0);
       }
     }
   }
@@ -634,15 +634,12 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   if (tid == 0) total_s = 0, valid_s = start_s = end_s = 0;
   if (lane < NS) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bars + lane)) : "memory");
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  // the kernel after this one may be set up beside it; nothing that the kernel before wrote is read until
-  // that one has ended
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
 
   // ---- the items of all units, and where this warp's run of them begins
   if (blockIdx.x == 0)
     for (int i = tid; i < a.c.batch; i += 32 * NW) {
-      const int len = __ldg(a.c.lens + i);
+      const int len = fetch(a.c.lens + i);
       if (len < 0) raise(a.c, RDKV_ERR_INVALID_ARG);
       if ((int64_t)len > (int64_t)a.c.page_stride * kPage) raise(a.c, RDKV_ERR_CAPACITY);
     }
@@ -719,11 +716,11 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       const int unit = b1 * H + h1, b = b1 / a.n_chunks;
       int lp = p1;
       if (a.sel) {
-        lp = __ldg(a.sel + (int64_t)unit * a.n_sel + p1);
+        lp = fetch(a.sel + (int64_t)unit * a.n_sel + p1);
         if (lp < 0 || (int64_t)lp * kPage >= seen_by(a, b, b1 % a.n_chunks)) lp = -1;
       }
       if (lp >= 0) {
-        e.x = __ldg(a.c.page_table + (int64_t)b * a.c.page_stride + lp);
+        e.x = fetch(a.c.page_table + (int64_t)b * a.c.page_stride + lp);
         if (e.x < 0 || e.x >= a.c.n_pages) {
           raise(a.c, RDKV_ERR_INVALID_ARG);
           e.x = -1;
@@ -775,7 +772,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     // the first queries are asked for before the pages, behind which they would wait
     typename Warp<D, NT, PREC>::Rows x;
     un = unit_at(a, info[0].z);
-    w.fetch(a, un, g, qd, x);
+    w.queries(a, un, g, qd, x);
 #pragma unroll 1
     for (int j = 0; j < min(NS, n_items); ++j) issue(j);
     w.begin(a.dtype, x, qd);
@@ -787,7 +784,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     if (!in_unit) {
       typename Warp<D, NT, PREC>::Rows x;
       un = unit_at(a, e.z);
-      w.fetch(a, un, g, qd, x);
+      w.queries(a, un, g, qd, x);
       w.begin(a.dtype, x, qd);
     }
     if (!in_unit || i == 0) {
@@ -927,13 +924,13 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- launch
-// The workspace has the same places for every shape, so that calls of any shape may follow one another:
-// pieces of the largest variant, then the tickets.
-constexpr int kMaxWarps = 12;
+// The workspace has the same places for every shape, so that calls of any shape may follow one another: the
+// tickets, then pieces of the largest variant.
+constexpr int kMaxWarps = 8;
 
 struct Geometry {
   int chunk, n_chunks, nt, grid;
-  size_t parts_at, tickets_at, bytes;
+  size_t heads_at, parts_at, bytes;
 };
 
 static Geometry geometry(const rdkv_q4_cache* c, int h_q, int n_q, bool prec, bool own_pages) {
@@ -945,10 +942,10 @@ static Geometry geometry(const rdkv_q4_cache* c, int h_q, int n_q, bool prec, bo
   o.n_chunks = ceil_div(n_q, o.chunk);
   o.nt = o.chunk * G > 8 ? 2 : 1;
   o.grid = num_sms();
-  const int64_t tickets = (int64_t)c->batch * n_q * c->h_kv, part = 4LL * Partial<128, 2>::kFloats;
-  o.parts_at = (size_t)align_up((int64_t)o.grid * kMaxWarps * part, 256);
-  o.tickets_at = o.parts_at + (size_t)align_up(2LL * o.grid * part, 256);
-  o.bytes = o.tickets_at + (size_t)align_up(4 * tickets, 256);
+  const int64_t part = 4LL * Partial<128, 2>::kFloats;
+  o.heads_at = RDKV_Q4_COUNTER_BYTES;
+  o.parts_at = o.heads_at + (size_t)align_up((int64_t)o.grid * kMaxWarps * part, 256);
+  o.bytes = o.parts_at + (size_t)align_up(2LL * o.grid * part, 256);
   return o;
 }
 
@@ -998,8 +995,8 @@ extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, c
   RDKV_REQUIRE(ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= geo.bytes, RDKV_ERR_WORKSPACE,
                "attention workspace too small (%zu < %zu) or unaligned", ws_bytes, geo.bytes);
   char* w = static_cast<char*>(ws);
-  const AttnArgs a{view_of(cache), q, out, lse, sel, reinterpret_cast<float*>(w), reinterpret_cast<float*>(w + geo.parts_at),
-                   reinterpret_cast<int32_t*>(w + geo.tickets_at), q_stride, dtype, out_dtype, n_q, h_q / cache->h_kv, n_sel,
+  const AttnArgs a{view_of(cache), q, out, lse, sel, reinterpret_cast<float*>(w + geo.heads_at),
+                   reinterpret_cast<float*>(w + geo.parts_at), reinterpret_cast<int32_t*>(w), q_stride, dtype, out_dtype, n_q, h_q / cache->h_kv, n_sel,
                    geo.chunk, geo.n_chunks};
   cudaStream_t cs = (cudaStream_t)stream;
   if (cache->head_dim == 128) {

@@ -106,12 +106,12 @@ __device__ __forceinline__ void score_tiles(const SelectArgs& a, int row, int b,
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int p = min(tile * kTilePages + 8 * r + g, P - 1);
-      const int phys = __ldg(a.c.page_table + (int64_t)b * a.c.page_stride + p);
+      const int phys = fetch(a.c.page_table + (int64_t)b * a.c.page_stride + p);
       bad[r] = phys < 0 || phys >= a.c.n_pages;
       if (bad[r] && qd == 0) raise(a.c, RDKV_ERR_INVALID_ARG);
       const uint4* e = reinterpret_cast<const uint4*>(a.c.bounds + ((int64_t)(bad[r] ? 0 : phys) * a.c.h_kv + h) * 2 * D) + qd;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) lo[r][i] = __ldg(e + 4 * i), hi[r][i] = __ldg(e + D / 8 + 4 * i);
+      for (int i = 0; i < NC; ++i) lo[r][i] = fetch(e + 4 * i), hi[r][i] = fetch(e + D / 8 + 4 * i);
     }
     float s[4] = {}, m[4] = {};
 #pragma unroll
@@ -194,8 +194,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   __shared__ uint32_t mask_s[kShared / 32];
   __shared__ float2 value_s[kFew][8];
   __shared__ int list_n, sure_n, last_s, found_s, found_n;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int row = blockIdx.y, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
   const int P = pages_seen(a, b, t);
@@ -320,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
 #pragma unroll 1
     for (int task = warp; task < (few ? near * a.G : near); task += kWarps) {
       const int i = few ? task / a.G : task, g0 = few ? task - i * a.G : 0, g1 = few ? g0 + 1 : a.G;
-      const int phys = __ldg(a.c.page_table + (int64_t)b * a.c.page_stride + (few ? list_s[i] : list[i]));
+      const int phys = fetch(a.c.page_table + (int64_t)b * a.c.page_stride + (few ? list_s[i] : list[i]));
       float2 best = make_float2(-INFINITY, 0.0f);
       if (phys >= 0 && phys < a.c.n_pages) {
         const __half* e = a.c.bounds + ((int64_t)phys * a.c.h_kv + h) * 2 * D;
@@ -396,7 +395,6 @@ using namespace rdkv;
 using namespace rdkv::q4;
 
 namespace {
-constexpr int kMaxRows = 65535;  // the grid's second size
 struct SelectGeometry {
   int64_t rows;
   int tiles;
@@ -407,7 +405,7 @@ SelectGeometry select_geometry(const rdkv_q4_cache* c, int n_q) {
   o.rows = (int64_t)c->batch * n_q * c->h_kv;
   o.tiles = ceil_div(c->page_stride, kTilePages);
   const int64_t pages = o.rows * c->page_stride;
-  o.value_at = 4 * (kMaxRows + 1);  // after the tickets, whose place is the same for every shape
+  o.value_at = RDKV_Q4_COUNTER_BYTES;  // after the tickets, whose place is the same for every shape
   o.error_at = o.value_at + (size_t)align_up(8 * pages, 256);
   o.list_at = o.error_at + (size_t)align_up(4 * o.rows * o.tiles, 256);
   o.score_at = o.list_at + (size_t)align_up(4 * pages, 256);
@@ -430,7 +428,6 @@ extern "C" rdkv_status rdkv_q4_select(const rdkv_q4_cache* cache, int32_t dtype,
   RDKV_REQUIRE(n_keep >= 1 && n_first >= 0 && n_last >= 0 && (int64_t)n_first + n_last <= n_keep, RDKV_ERR_INVALID_ARG,
                "n_keep=%d n_first=%d n_last=%d", n_keep, n_first, n_last);
   const SelectGeometry geo = select_geometry(cache, n_q);
-  RDKV_REQUIRE(geo.rows <= kMaxRows, RDKV_ERR_UNSUPPORTED, "more than 65,535 (sequence, query token, KV head) rows");
   RDKV_REQUIRE(ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= geo.bytes, RDKV_ERR_WORKSPACE,
                "selection workspace too small (%zu < %zu) or unaligned", ws_bytes, geo.bytes);
   char* w = static_cast<char*>(ws);

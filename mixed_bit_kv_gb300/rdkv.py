@@ -75,6 +75,7 @@ A_PAGE_BYTES = 65536  # RDKV_ZONE_A_PAGE_BYTES
 B_PAGE_ROWS = 16  # RDKV_ZONE_B_PAGE_ROWS
 Q4_PAGE_TOKENS = 64  # RDKV_Q4_PAGE_TOKENS
 Q4_MAX_QUERIES = 64  # RDKV_Q4_MAX_QUERIES
+Q4_COUNTER_BYTES = 262144  # RDKV_Q4_COUNTER_BYTES
 
 
 HEAD_PLAN_DTYPE = [("n_v", "<i4", 4), ("tiles", "<i4", 4), ("n_k", "<i4", 5), ("k_words", "<i4", 4),
@@ -813,21 +814,23 @@ class Q4Cache:
         self._ws, self._seen = {}, {}  # workspaces by stream; what the checks found for queries of a shape and type
 
     def workspace(self, kind, h_q, n_q, s):
-        """The zero-filled workspace of rdkv_q4_attn ("attn") or rdkv_q4_select ("select") calls on the current
-        stream s.  While a graph is being captured: one of that call's own, cleared in the graph (two captured
-        graphs may run at once)."""
+        """The workspace of rdkv_q4_attn ("attn") or rdkv_q4_select ("select") calls on the current stream s, its
+        counters zero.  While a graph is being captured: one of that call's own, cleared in the graph (two
+        captured graphs may run at once)."""
         nb = self._ws.get((kind, h_q, n_q))
         if nb is None:
             fn = lib().rdkv_q4_attn_workspace_bytes if kind == "attn" else lib().rdkv_q4_select_workspace_bytes
             nb = fn(self._ref, h_q, n_q)
             if nb == 0:
-                raise RDKVError(RDKV_ERR_INVALID_ARG, lib().rdkv_last_error_string().decode())
+                raise RDKVError(RDKV_ERR_UNSUPPORTED, lib().rdkv_last_error_string().decode())
             self._ws[kind, h_q, n_q] = nb
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(nb, dtype=torch.uint8, device=self.device)
-        ws = self._ws.get((kind, s))
+        capturing = torch.cuda.is_current_stream_capturing()
+        ws = None if capturing else self._ws.get((kind, s))
         if ws is None or ws.numel() < nb:
-            ws = self._ws[kind, s] = torch.zeros(nb, dtype=torch.uint8, device=self.device)
+            ws = torch.empty(nb, dtype=torch.uint8, device=self.device)
+            ws[:Q4_COUNTER_BYTES].zero_()
+            if not capturing:
+                self._ws[kind, s] = ws
         return ws
 
 

@@ -161,6 +161,8 @@ def test_sizes(L):
     for fn in (L.rdkv_q4_attn_workspace_bytes, L.rdkv_q4_select_workspace_bytes):
         assert fn(ctypes.byref(c), 4, 1) > 0
         assert fn(ctypes.byref(c), 4, 1) % 16 == 0
+        big = _struct(batch=512, h_kv=8)
+        assert fn(ctypes.byref(big), 8, 15) > 0 and fn(ctypes.byref(big), 8, 16) == 0
         assert fn(ctypes.byref(c), 5, 1) == fn(ctypes.byref(c), 4, 65) == fn(ctypes.byref(_struct(head_dim=32)), 4, 1) == 0
     # the other calls of the library still take no bf16
     s = rdkv.make_shape(1, 64, 4, 2, 64, 0, "f16")
