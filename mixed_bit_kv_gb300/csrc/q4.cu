@@ -287,13 +287,6 @@ __device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d) 
   return __float_as_uint(fmaf(d, 4096.0f, fmaf(c, 256.0f, fmaf(b, 16.0f, a))) + 8388608.0f);  // the low 16 bits
 }
 __device__ __forceinline__ uint32_t low_halves(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x5410); }
-// Two values in fp16, cut to its range.
-__device__ __forceinline__ __half2 cut_half2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return *reinterpret_cast<const __half2*>(&d);
-}
-
 // One block per (sequence, page that its rows touch, KV head), heads fastest: neighbouring blocks read
 // neighbouring memory.  A thread has eight channels of a token pair: of K eight in a row (a code word of each
 // token), of V the runs 4 q and 4 q + 16 (two words that hold both tokens), so that a warp's stores fill whole
@@ -344,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) write_kerne
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 y = fma_f32x2(make_float2(c.p.scale, c.p.scale), make_float2(c.c[2 * e], c.c[2 * e + 1]), make_float2(c.p.zero, c.p.zero));
-            const __half2 z = cut_half2(y.x, y.y);
+            const uint32_t zw = cut_half2(y.x, y.y);
+          const __half2 z = *reinterpret_cast<const __half2*>(&zw);
             lo[e] = __hmin2(lo[e], z), hi[e] = __hmax2(hi[e], z);
           }
         }
@@ -397,9 +391,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) write_kerne
   }
 }
 
-__device__ __forceinline__ float value_of(uint32_t code, float scale, float zero) {
-  return fmaf(scale, __uint_as_float(code | 0x4b000000u) - 8388608.0f, zero);
+// The values of a code word's four pairs (codes at bits 0 and 16, 4 and 20, 8 and 24, 12 and 28): a code at bit
+// p < 8 of a half word is the fp16 subnormal code 2^(p - 24), exactly, and so is its product with a scale.
+// scale: of the low and the high halves, times 2^24.
+__device__ __forceinline__ void word_values(uint32_t w, float2 scale, float2 zero, float2 (&x)[4]) {
+  const float2 less = make_float2(scale.x * 0.0625f, scale.y * 0.0625f);
+  const uint32_t u = w >> 8, p[4] = {w & 0x000f000fu, w & 0x00f000f0u, u & 0x000f000fu, u & 0x00f000f0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = fma_f32x2(__half22float2(*reinterpret_cast<const __half2*>(&p[i])), i & 1 ? less : scale, zero);
 }
+__device__ __forceinline__ float half_of(uint32_t w, int i) { return __half2float(__ushort_as_half((uint16_t)(w >> (16 * i)))); }
 
 // The same blocks the other way: eight channels in a row of a token pair a thread.
 template <typename T, int D, int kThreads, int kSteps>
@@ -427,21 +428,25 @@ __global__ void __launch_bounds__(kThreads) read_kernel(View v, Rows r, T* k, T*
     }
   }
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i)
+  for (int i = 0; i < kSteps; ++i) {
+    constexpr float kUnit = 16777216.0f;
+    float2 v0[4], v1[4];  // channels 8 l .. + 3 and + 4 .. 7 of both tokens
+    const float2 vscale = make_float2(half_of(vs[i], 0) * kUnit, half_of(vs[i], 1) * kUnit), vzero = make_float2(half_of(vz[i], 0), half_of(vz[i], 1));
+    word_values(vc[i][0], vscale, vzero, v0);
+    word_values(vc[i][1], vscale, vzero, v1);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int s = 2 * (first + i * kPairs) + j;
       if (s < w.s0 || s >= w.s1) continue;
       const int64_t at = (w.row + s - w.s0) * r.stride + (int64_t)h * D + 8 * l;
-      float x[8], sc = __half2float(__ushort_as_half((uint16_t)(ks[i] >> (16 * j)))), z = __half2float(__ushort_as_half(kz[i][j]));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = value_of((kc[i][j] >> bit_off(e, 4)) & 15u, sc, z);
-      Eight<T>::store(k + at, x);
-      sc = __half2float(__ushort_as_half((uint16_t)(vs[i] >> (16 * j)))), z = __half2float(__ushort_as_half((uint16_t)(vz[i] >> (16 * j))));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = value_of((vc[i][e / 4] >> (16 * j + 4 * (e % 4))) & 15u, sc, z);
-      Eight<T>::store(vv + at, x);
+      const float sc = half_of(ks[i], j) * kUnit, z = half_of(kz[i][j], 0);
+      float2 x[4];
+      word_values(kc[i][j], make_float2(sc, sc), make_float2(z, z), x);
+      Eight<T>::store(k + at, {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y});
+      if (j == 0) Eight<T>::store(vv + at, {v0[0].x, v0[1].x, v0[2].x, v0[3].x, v1[0].x, v1[1].x, v1[2].x, v1[3].x});
+      else Eight<T>::store(vv + at, {v0[0].y, v0[1].y, v0[2].y, v0[3].y, v1[0].y, v1[1].y, v1[2].y, v1[3].y});
     }
+  }
 }
 
 static rdkv_status grid_of(const rdkv_q4_cache* c, Rows* r, int64_t* blocks) {

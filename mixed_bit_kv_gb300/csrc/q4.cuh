@@ -81,6 +81,12 @@ __device__ __forceinline__ int held_tokens(const View& v, int b) {
 }
 
 // ---------------------------------------------------------------- rows of the model's types
+// Two values in fp16, cut to its range.
+__device__ __forceinline__ uint32_t cut_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
 template <typename T>
 struct Eight;  // eight consecutive channels
 template <>
@@ -95,12 +101,8 @@ struct Eight<__half> {
     }
   }
   static __device__ __forceinline__ void store(__half* p, const float (&x)[8]) {
-    uint4 u;
-    __half2* h = reinterpret_cast<__half2*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      h[i] = __floats2half2_rn(fminf(fmaxf(x[2 * i], -kHalfMax), kHalfMax), fminf(fmaxf(x[2 * i + 1], -kHalfMax), kHalfMax));
-    *reinterpret_cast<uint4*>(p) = u;
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(cut_half2(x[0], x[1]), cut_half2(x[2], x[3]), cut_half2(x[4], x[5]), cut_half2(x[6], x[7]));
   }
 };
 template <>
