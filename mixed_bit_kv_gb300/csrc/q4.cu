@@ -291,7 +291,11 @@ __device__ __forceinline__ uint32_t low_halves(uint32_t lo, uint32_t hi) { retur
 // neighbouring memory.  A thread has eight channels of a token pair: of K eight in a row (a code word of each
 // token), of V the runs 4 q and 4 q + 16 (two words that hold both tokens), so that a warp's stores fill whole
 // sectors.  Every load of a thread's kSteps pairs is under way before the first is used.  kThreads, kSteps:
-// as few as the call's rows need (a decode step has one token a sequence).
+// as few as the call's rows need (a decode step has one token a sequence: 3.8 us for 32 sequences of 8 heads
+// with 32 threads a block, 9.8 with 256).
+//   Bound: 47 us for 32,768 rows of 8 heads at D = 128 in fp16 (134 MB read, 42 MB written: 3.7 TB/s), by the
+// quantiser's instructions (about 1,200 a warp and page half).  As one division a value it took 94 us; with the
+// tests as short-circuit conditions 76; with an exact way for the whole group on a near half 54.
 template <typename T, int D, int kThreads, int kSteps>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) write_kernel(View v, Rows r, const T* k, const T* vv) {
   using L = Layout<D>;
@@ -402,7 +406,9 @@ __device__ __forceinline__ void word_values(uint32_t w, float2 scale, float2 zer
 }
 __device__ __forceinline__ float half_of(uint32_t w, int i) { return __half2float(__ushort_as_half((uint16_t)(w >> (16 * i)))); }
 
-// The same blocks the other way: eight channels in a row of a token pair a thread.
+// The same blocks the other way: eight channels in a row of a token pair a thread.  Bound: 190 us for eight 32K
+// caches of 8 heads in fp16 (235 MB read, 866 MB written: 5.8 TB/s, 85 % of the measured copy); 200 us with
+// integer conversions, whose shifts and clamps filled the ALU.
 template <typename T, int D, int kThreads, int kSteps>
 __global__ void __launch_bounds__(kThreads) read_kernel(View v, Rows r, T* k, T* vv) {
   using L = Layout<D>;

@@ -6,18 +6,30 @@
 //
 // Work.  A unit is (sequence, chunk of query tokens, KV head): up to 8 NT query rows, NT = 1 or 2, that
 // share the unit's keys; an item is one page (64 tokens) of a unit.  The items of all units, one after
-// another, are dealt evenly to the warps of the grid (one block an SM): each warp takes a run of items
-// and works alone, copying pages into its own ring with bulk copies.  Units that end
-// inside a warp's run are written by it; the pieces of the others are joined per block in shared memory
-// and, where a unit spans blocks, by the last of its blocks through the workspace.
+// another, are dealt evenly to the warps of the grid (one block of eight warps an SM): each warp takes a run
+// of items and works alone, copying pages into its own ring of two with bulk copies, so that no barrier
+// stands between the pages.  Units that end inside a warp's run are written by it; the pieces of the others
+// are joined per block in shared memory and, where a unit spans blocks, by the last of its blocks through
+// the workspace, always in the same order: the result does not depend on who comes first.
 //
 // Products: mma.sync, queries on M and tokens on N for the logits, channels on M and queries on N for the
 // values.  A code at bit p < 8 of a half word is the fp16 subnormal code 2^(p - 24), so one AND makes two
-// codes an operand register; the units are undone in fp32.  Each group's logits accumulate on their own
-// and take the token's scale in fp32; the zeros' part is one more product, of the queries' group sums
-// (fp16 high part and remainder).  A weight times its values' scale is rounded to fp16 once; for fp32
-// outputs (PREC) the product keeps a remainder too.  With one row set (NT = 1) the rows 8 .. 15 of the
-// logits' products hold the queries' low parts, which fp32 queries need.
+// codes of the keys an operand register; the units are undone in fp32.  Each group's logits accumulate on
+// their own and take the token's scale in fp32; the zeros' part is one more product, of the queries' group
+// sums (fp16 high part and remainder).  The values are taken as zero + 8 scale and scale (code - 8): what
+// fp16 and the tensor core (it cuts, it does not round) lose is then lost of a small sum, not of the
+// difference of two large ones.  For fp32 outputs (PREC) the keys are split the same way, the middles' part
+// is summed in fp32, weight times scale keeps a remainder, and the rows 8 .. 15 of the logits' products
+// hold the queries' low parts.
+//
+// Bound.  160 bytes a token and KV head at D = 128: 72 % of the measured copy bandwidth at 262,144 tokens (68.7
+// us for 335 MB).  The page loop alone runs at 88 %; it issues about 1,190 instructions a page (a third of
+// them to unpack codes), at 2.2 a cycle and SM, with ALU, FMA and tensor pipes each 25 to 45 % busy.  Start
+// (lengths, page table, queries, first page: each a trip to memory) and joins take about 10 us of every call.
+//   Measured and not kept (us at 262,144 tokens, one box a pair): 11 or 12 warps of 168 registers 74 .. 79
+// against 69, 16 of 128 74; 16 or 32 tokens under way at once 79 and 72 against 64's 69; pages copied with the
+// 128-byte swizzle of a tensor map, which takes away the values' four-fold bank conflicts (96 of 270
+// shared-memory cycles a page), 75 against 73; the same through 21 copies a page into shifted quarters, 91.
 #include <atomic>
 
 #include "q4.cuh"
@@ -39,7 +51,7 @@ struct AttnArgs {
 };
 
 constexpr long long kWaitCycles = 4000000000LL;  // a bounded wait, about two seconds
-constexpr int kMinItems = 4;
+constexpr int kMinItems = 4;                     // of a block (1 to 8: within 3 % of one another on the smallest calls)
 constexpr int kInfo = 32;                        // items whose places a warp knows ahead
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -216,7 +228,9 @@ struct Warp {
   float o[NT][NG][2][4];
   float oz[NT][PREC ? NG : 2];  // the zeros' part: by row g < NG = group and columns, or (PREC) this lane's row's, by group
   int off;                      // weights are held times 2^off
-  static constexpr int kTurn = NT == 1 && !PREC ? 64 : 32;  // tokens whose products are under way together
+  // Tokens whose products are under way together: as many as the registers hold (72B-shaped layer: 64 in 68.7
+  // us, 32 in 72.1; with two row sets 32 in 51.9 us on the drafted tokens, 64 spill: 63.9)
+  static constexpr int kTurn = NT == 1 && !PREC ? 64 : 32;
   static constexpr int kMaxOff = PREC ? 23 : 11;
 
   // This lane's channels of the unit's query rows, as they lie in memory (rows past the last: zero).  Kept
@@ -362,8 +376,6 @@ struct Warp {
         off = now;
       }
     }
-    // 32 tokens a turn: enough independent products to hide their latency, and a body that stays in the
-    // instruction cache
 #pragma unroll 1
     for (int t32 = 0; t32 < kPage; t32 += kTurn) {
       float2 u[NT][kTurn / 8];  // logits (base 2, times 2^(s - 15)) of tokens t32 + 8 t + 2 qd + {0, 1}
@@ -476,10 +488,9 @@ struct Warp {
           }
         }
       }
-      // The tensor core cuts what it adds to an accumulator (it does not round), which the difference of the
-      // two large sums would show: its accumulators start at zero every turn, and the sums over the turns are
-      // rounded fp32 additions.  PREC: codes less eight and the high parts on a grid of 1/4 (11 bits below
-      // 2^9) make every product and sum of theirs an exact integer of that grid.
+      // The tensor core cuts what it adds to an accumulator: its accumulators start at zero every turn, and the
+      // sums over the turns are rounded fp32 additions.  PREC: codes less eight and the high parts on a grid of
+      // 1/4 (11 bits below 2^9) make every product and sum of theirs an exact integer of that grid.
       if constexpr (!PREC) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) oz[n][0] += cz[n][0], oz[n][1] += cz[n][1];
@@ -668,7 +679,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       if (tid < un.rows) put_lse(a, row_at(a, un, tid), 0.0f, 0.0f);
     }
   }
-  // a block for every kMinItems items: few items stay in few blocks, whose joins are cheap
+  // a block for every kMinItems items: few items stay in few blocks
   const int nb = min((int)gridDim.x, ceil_div(total, kMinItems));
   if ((int)blockIdx.x >= nb) return;
   const int nw = nb * NW, me = blockIdx.x * NW + warp;

@@ -8,6 +8,9 @@
 // then finds an interval around the n-th best score, takes what lies above it by more than the error, and
 // sums only the few pages within the error again, to twice fp32's precision, so that the order next to the
 // border is the exact one.
+//   Bound: latency.  13.0 us for 64 of 2,048 pages of 8 heads (8.4 MB of bounds): 3 us to the scores, 1 for the
+// ticket, 1 to read the scores again, the rest the block's own turns.  As two launches 13.9; four ends of an
+// interval a turn instead of 2,048 parts 14.4.
 #include "q4.cuh"
 
 namespace rdkv {
