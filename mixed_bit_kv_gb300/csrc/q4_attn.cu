@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) low[n] = held - a.n_q + min(un.t0 + (g + 8 * n) / a.G, a.n_q - 1) + 1;
     }
-    if (!wait_for(bars + i % NS, (i / NS) & 1)) {
+    if (!__all_sync(0xffffffffu, wait_for(bars + i % NS, (i / NS) & 1))) {  // the warp goes on, or stops, as one
       ok = false;
       break;
     }
