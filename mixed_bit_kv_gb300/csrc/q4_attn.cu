@@ -12,24 +12,26 @@
 // are joined per block in shared memory and, where a unit spans blocks, by the last of its blocks through
 // the workspace, always in the same order: the result does not depend on who comes first.
 //
-// Products: mma.sync, queries on M and tokens on N for the logits, channels on M and queries on N for the
-// values.  A code at bit p < 8 of a half word is the fp16 subnormal code 2^(p - 24), so one AND makes two
-// codes of the keys an operand register; the units are undone in fp32.  Each group's logits accumulate on
-// their own and take the token's scale in fp32; the zeros' part is one more product, of the queries' group
-// sums (fp16 high part and remainder).  The values are taken as zero + 8 scale and scale (code - 8): what
+// Products: mma.sync, channels on M and queries on N for the values; for the logits tokens on M and queries on N
+// where the unit has up to eight rows and 16-bit outputs, else queries on M (rows 8 .. 15 a second eight, or
+// the first's low parts) and tokens on N.  A code at bit p < 8 of a half word is the fp16 subnormal code 2^(p - 24),
+// so one AND makes two codes of the keys an operand register; the units are undone in fp32.  Each group's logits
+// accumulate on their own and take the token's scale in fp32; the zeros' part is one more product, of the queries'
+// group sums (fp16 high part and remainder).  The values are taken as zero + 8 scale and scale (code - 8): what
 // fp16 and the tensor core (it cuts, it does not round) lose is then lost of a small sum, not of the
 // difference of two large ones.  For fp32 outputs (PREC) the keys are split the same way, the middles' part
-// is summed in fp32, weight times scale keeps a remainder, and the rows 8 .. 15 of the logits' products
-// hold the queries' low parts.
+// is summed in fp32, and weight times scale keeps a remainder.
 //
-// Bound.  160 bytes a token and KV head at D = 128: 72 % of the measured copy bandwidth at 262,144 tokens (68.7
-// us for 335 MB).  The page loop alone runs at 88 %; it issues about 1,190 instructions a page (a third of
-// them to unpack codes), at 2.2 a cycle and SM, with ALU, FMA and tensor pipes each 25 to 45 % busy.  Start
-// (lengths, page table, queries, first page: each a trip to memory) and joins take about 10 us of every call.
-//   Measured and not kept (us at 262,144 tokens, one box a pair): 11 or 12 warps of 168 registers 74 .. 79
-// against 69, 16 of 128 74; 16 or 32 tokens under way at once 79 and 72 against 64's 69; pages copied with the
-// 128-byte swizzle of a tensor map, which takes away the values' four-fold bank conflicts (96 of 270
-// shared-memory cycles a page), 75 against 73; the same through 21 copies a page into shifted quarters, 91.
+// Bound.  160 bytes a token and KV head at D = 128: 79 % of the measured copy bandwidth at 262,144 tokens (62.6
+// us for 335 MB).  A scheduler has two warps, whose products wait for one another: a page of up to eight rows takes
+// 72 products (104 with the queries on M and half of its rows empty: 68.5 us).  About 1,150 instructions a page,
+// a third of them to unpack codes.  Start (lengths, page table, queries, first page: each a trip to memory) and
+// joins take about 10 us of every call.
+//   Measured and not kept (us at 262,144 tokens, against 68.5 .. 69): 11 or 12 warps of 168 registers 74 .. 79, 16
+// of 128 74; 16 or 32 tokens under way at once 79 and 72; pages copied with the 128-byte swizzle of a tensor map,
+// which takes away the values' four-fold bank conflicts (96 of 270 shared-memory cycles a page), 75 against 73; the
+// same through 21 copies a page into shifted quarters, 91; the values' codes as subnormals too, less eight times the
+// weights' sum by one more product a group: 128 instructions a page fewer, 16 products more, 70.4.
 #include <atomic>
 
 #include "q4.cuh"
@@ -90,6 +92,12 @@ __device__ __forceinline__ void mma8z(float (&c)[4], uint32_t a0, uint32_t a1, u
   asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
+}
+// an 8 x 8 matrix of halves, a row in four lanes, transposed
+__device__ __forceinline__ uint32_t transposed(uint32_t w) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(w));
+  return d;
 }
 // two fp32 products and sums in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -220,11 +228,18 @@ template <int D, int NT, bool PREC>
 struct Warp {
   static constexpr int NG = D / kGroup;
   using L = Layout<D>;
-  uint32_t q[2][NG][4];  // A registers: rows g, and rows g + 8 (the chunk's second half, or the low parts of the first)
-  uint32_t qz[2];        // A registers of the zeros' product
-  float qs[NG];          // (PREC) the same sums in fp32
-  float scale[NT];        // 2^(15 - s): a row's logits are held times 2^(s - 15)
-  float ref[NT], l[NT];   // the running maximum (base 2) and this lane's share of the sum
+  // Eight rows in 16 bits: tokens on M, queries on N for the logits too, with no rows for low parts: half as
+  // many products, whose weights one transposition a tile turns into the values' operand.
+  static constexpr bool kCols = NT == 1 && !PREC;
+  // The query rows whose statistics a lane keeps: g (+ 8), or its columns 2 qd and 2 qd + 1.
+  static constexpr int kStats = kCols ? 2 : NT;
+  static __device__ __forceinline__ int stat_row(int n, int g, int qd) { return kCols ? 2 * qd + n : g + 8 * n; }
+
+  uint32_t q[kCols ? 1 : 2][NG][4];  // operand registers: rows g, and rows g + 8 (the chunk's second half, or the low parts of the first)
+  uint32_t qz[2];                    // operand registers of the zeros' product
+  float qs[NG];                      // (PREC) the same sums in fp32
+  float scale[kStats];               // 2^(15 - s): a row's logits are held times 2^(s - 15)
+  float ref[kStats], l[kStats];      // the running maximum (base 2) and this lane's share of the sum
   float o[NT][NG][2][4];
   float oz[NT][PREC ? NG : 2];  // the zeros' part: by row g < NG = group and columns, or (PREC) this lane's row's, by group
   int off;                      // weights are held times 2^off
@@ -285,7 +300,13 @@ struct Warp {
       const int e2 = (int)(__float_as_uint(top) >> 23) - 127;
       const int s = top > 0.0f ? max(-96, min(111, 14 - e2)) : 0;
       const float up = __uint_as_float((uint32_t)(s + 127) << 23);
-      scale[n] = __uint_as_float((uint32_t)(15 - s + 127) << 23);
+      const float down = __uint_as_float((uint32_t)(15 - s + 127) << 23);
+      if constexpr (kCols) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) scale[j] = __shfl_sync(0xffffffffu, down, 8 * qd + 4 * j);
+      } else {
+        scale[n] = down;
+      }
       float sum[NG];
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
@@ -297,7 +318,7 @@ struct Warp {
           // pairs 1 and 3 meet codes that stand for sixteen times as much
           const float f = j & 1 ? 0.0625f : 1.0f, y0 = x[i][2 * j] * f, y1 = x[i][2 * j + 1] * f;
           q[n][i][j] = pack2(y0, y1);
-          if constexpr (NT == 1) q[1][i][j] = rest2(y0, y1, q[0][i][j]);
+          if constexpr (PREC) q[1][i][j] = rest2(y0, y1, q[0][i][j]);
         }
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
@@ -317,8 +338,6 @@ struct Warp {
       if constexpr (NT == 1) qz[1] = 0u;
       if constexpr (NG == 4) qz[n] = qd == 0 ? hi[0] : qd == 1 ? hi[1] : qd == 2 ? lo[0] : lo[1];
       else qz[n] = qd == 0 ? hi[0] : qd == 1 ? lo[0] : 0u;
-      ref[n] = -INFINITY;
-      l[n] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -326,14 +345,17 @@ struct Warp {
 #pragma unroll
       for (int j = 0; j < (PREC ? NG : 2); ++j) oz[n][j] = 0.0f;
     }
+#pragma unroll
+    for (int n = 0; n < kStats; ++n) ref[n] = -INFINITY, l[n] = 0.0f;
     off = kMaxOff;
   }
 
-  // Row sums and weighted sums times f, each lane's row's own.
-  __device__ __forceinline__ void rescale(int n, float f, int qd) {
+  // Row sums and weighted sums times f, each lane's row's own (of its columns: f and g).
+  __device__ __forceinline__ void rescale(int n, float f, float g, int qd) {
     l[n] *= f;
+    if constexpr (kCols) l[1] *= g;
     // columns 2 qd and 2 qd + 1 of the sums are rows that lanes 8 qd and 8 qd + 4 keep
-    const float f0 = __shfl_sync(0xffffffffu, f, 8 * qd), f1 = __shfl_sync(0xffffffffu, f, 8 * qd + 4);
+    const float f0 = kCols ? f : __shfl_sync(0xffffffffu, f, 8 * qd), f1 = kCols ? g : __shfl_sync(0xffffffffu, f, 8 * qd + 4);
 #pragma unroll
     for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -350,7 +372,7 @@ struct Warp {
   // One page.  kTail: its last tokens may hold nothing (live of them do; what the others hold is arbitrary
   // bits) or be hidden from some rows (row n of this lane sees low[n] of the page's tokens).
   template <bool kTail>
-  __device__ __forceinline__ void page(const uint8_t* k, int g, int qd, int live, const int (&low)[NT]) {
+  __device__ __forceinline__ void page(const uint8_t* k, int g, int qd, int live, const int (&low)[kStats]) {
     constexpr float kUnit = PREC ? 1.0f : 16777216.0f;  // of the codes in the products
     constexpr float kK = kUnit / 32768.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
     uint32_t k1024;
@@ -372,15 +394,50 @@ struct Warp {
       if (now < off) {
         const float f = __uint_as_float((uint32_t)(now - off + 127) << 23);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) rescale(n, f, qd);
+        for (int n = 0; n < NT; ++n) rescale(n, f, f, qd);
         off = now;
       }
     }
 #pragma unroll 1
     for (int t32 = 0; t32 < kPage; t32 += kTurn) {
-      float2 u[NT][kTurn / 8];  // logits (base 2, times 2^(s - 15)) of tokens t32 + 8 t + 2 qd + {0, 1}
+      // logits (base 2, times 2^(s - 15)): of tokens t32 + 8 t + 2 qd + {0, 1}, or (kCols) of token t32 + 8 t + g
+      // and both columns
+      float2 u[NT][kTurn / 8];
+      if constexpr (kCols) {
 #pragma unroll
-      for (int t = 0; t < kTurn / 8; ++t) {
+        for (int t = 0; t < kTurn / 8; t += 2) {
+          const int tok = t32 + 8 * t + g;
+          uint32_t w0[NG], w1[NG], s0[NG], s1[NG];
+          lds_groups<NG>(k + L::kKCodes + (tok * 4 + qd) * NG * 4, w0);
+          lds_groups<NG>(k + L::kKCodes + ((tok + 8) * 4 + qd) * NG * 4, w1);
+          lds_groups<NG>(k + L::kKScales + tok / 2 * NG * 4, s0);
+          lds_groups<NG>(k + L::kKScales + (tok / 2 + 4) * NG * 4, s1);
+          const uint32_t* zw = reinterpret_cast<const uint32_t*>(k + L::kKZeros) + tok * (NG / 2) + (NG == 4 ? qd & 1 : 0);
+          float z[4];
+          mma8z(z, zw[0], zw[8 * (NG / 2)], qz[0]);
+          float2 a0 = make_float2(0.0f, 0.0f), a1 = a0;
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            const Pairs x = code_pairs(w0[i]), y = code_pairs(w1[i]);
+            float c[4];
+            mma16z(c, x.a, y.a, x.b, y.b, q[0][i][0], q[0][i][1]);
+            mma16(c, x.c, y.c, x.d, y.d, q[0][i][2], q[0][i][3]);
+            const float2 f = unpack2(__byte_perm(s0[i], s1[i], g & 1 ? 0x7632 : 0x5410));  // tokens tok and tok + 8
+            a0.x = fmaf(f.x, c[0], a0.x), a0.y = fmaf(f.x, c[1], a0.y);
+            a1.x = fmaf(f.y, c[2], a1.x), a1.y = fmaf(f.y, c[3], a1.y);
+          }
+          u[0][t] = fma2(a0, make_float2(kK, kK), make_float2(z[0], z[1]));
+          u[0][t + 1] = fma2(a1, make_float2(kK, kK), make_float2(z[2], z[3]));
+          if (kTail) {
+            if (tok >= low[0]) u[0][t].x = -INFINITY;
+            if (tok >= low[kStats - 1]) u[0][t].y = -INFINITY;
+            if (tok + 8 >= low[0]) u[0][t + 1].x = -INFINITY;
+            if (tok + 8 >= low[kStats - 1]) u[0][t + 1].y = -INFINITY;
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; !kCols && t < kTurn / 8; ++t) {
         const int tok = t32 + 8 * t;
         uint32_t w[NG], sw[NG];
         lds_groups<NG>(k + L::kKCodes + ((tok + g) * 4 + qd) * NG * 4, w);
@@ -404,9 +461,10 @@ struct Warp {
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
           const Pairs p = PREC ? centred_pairs(w[i], k1024) : code_pairs(w[i]);
+          constexpr int k1 = kCols ? 0 : 1;
           float c[4];
-          mma16z(c, q[0][i][0], q[1][i][0], q[0][i][1], q[1][i][1], p.a, p.b);
-          mma16(c, q[0][i][2], q[1][i][2], q[0][i][3], q[1][i][3], p.c, p.d);
+          mma16z(c, q[0][i][0], q[k1][i][0], q[0][i][1], q[k1][i][1], p.a, p.b);
+          mma16(c, q[0][i][2], q[k1][i][2], q[0][i][3], q[k1][i][3], p.c, p.d);
           const float2 f = unpack2(sw[i]);
           if constexpr (PREC) c[0] += c[2], c[1] += c[3];
           s[0] = fma2(f, make_float2(c[0], c[1]), s[0]);
@@ -423,8 +481,26 @@ struct Warp {
       }
       // a row's reference rises when a logit passes it by more than 4, so that weights stay at most 2^4
       // (PREC: whenever one passes it)
+      if constexpr (kCols) {
+        float m0 = u[0][0].x, m1 = u[0][0].y;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+        for (int t = 1; t < kTurn / 8; ++t) m0 = fmaxf(m0, u[0][t].x), m1 = fmaxf(m1, u[0][t].y);
+        m0 *= scale[0], m1 *= scale[kStats - 1];
+        if (__any_sync(0xffffffffu, m0 > ref[0] + 4.0f || m1 > ref[kStats - 1] + 4.0f)) {
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+          }
+          m0 = fmaxf(m0, ref[0]), m1 = fmaxf(m1, ref[kStats - 1]);
+          const float f0 = ref[0] == -INFINITY ? 0.0f : ex2(ref[0] - m0);
+          const float f1 = ref[kStats - 1] == -INFINITY ? 0.0f : ex2(ref[kStats - 1] - m1);
+          ref[0] = m0, ref[kStats - 1] = m1;
+          rescale(0, f0, f1, qd);
+        }
+      }
+#pragma unroll
+      for (int n = 0; !kCols && n < NT; ++n) {
         float m = fmaxf(u[n][0].x, u[n][0].y);
 #pragma unroll
         for (int t = 1; t < kTurn / 8; ++t) m = fmaxf(m, fmaxf(u[n][t].x, u[n][t].y));
@@ -435,7 +511,7 @@ struct Warp {
           m = fmaxf(m, ref[n]);
           const float f = ref[n] == -INFINITY ? 0.0f : ex2(ref[n] - m);
           ref[n] = m;
-          rescale(n, f, qd);
+          rescale(n, f, f, qd);
         }
       }
       // the weights, in fp16 too, in the order of the values' products: 16 tokens a step
@@ -455,8 +531,19 @@ struct Warp {
 #pragma unroll
           for (int i = 0; i < NG; ++i) s0[t][i] &= keep0, s1[t][i] &= keep1;
         }
+        if constexpr (kCols) {
+          const float2 r = make_float2((float)off - (ref[0] == -INFINITY ? 0.0f : ref[0]),
+                                       (float)off - (ref[kStats - 1] == -INFINITY ? 0.0f : ref[kStats - 1]));
+          const float2 up = make_float2(scale[0], scale[kStats - 1]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+          for (int m = 0; m < 2; ++m) {
+            const float2 y = fma2(u[0][2 * t + m], up, r), x = make_float2(ex2(y.x), ex2(y.y));
+            l[0] += x.x, l[kStats - 1] += x.y;
+            hi[0][t][m] = transposed(pack2(x.x, x.y));
+          }
+        }
+#pragma unroll
+        for (int n = 0; !kCols && n < NT; ++n) {
           const float r = (float)off - (ref[n] == -INFINITY ? 0.0f : ref[n]);
           const float2 y0 = fma2(u[n][2 * t], make_float2(scale[n], scale[n]), make_float2(r, r));
           const float2 y1 = fma2(u[n][2 * t + 1], make_float2(scale[n], scale[n]), make_float2(r, r));
@@ -482,7 +569,7 @@ struct Warp {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const float(&x)[4] = p[n][t];
-            hi[n][t][0] = pack2(x[0], x[1]), hi[n][t][1] = pack2(x[2], x[3]);
+            if constexpr (!kCols) hi[n][t][0] = pack2(x[0], x[1]), hi[n][t][1] = pack2(x[2], x[3]);
             if (t == 0) mma16z(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
             else mma16(cz[n], z0, 0u, z1, 0u, hi[n][t][0], hi[n][t][1]);
           }
@@ -549,12 +636,17 @@ struct Warp {
   __device__ __forceinline__ void finish(int g, int qd, Put put, Stat stat) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float sum = l[n];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const float m = ref[n] == -INFINITY ? -INFINITY : ref[n] - (float)off;
-      // the sums' columns are rows of lanes 8 qd and 8 qd + 4
-      const float l0 = __shfl_sync(0xffffffffu, sum, 8 * qd), l1 = __shfl_sync(0xffffffffu, sum, 8 * qd + 4);
+      float sum = l[n], m = ref[n] == -INFINITY ? -INFINITY : ref[n] - (float)off, l0, l1;
+      if constexpr (kCols) {
+        l0 = l[0], l1 = l[1];
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) l0 += __shfl_xor_sync(0xffffffffu, l0, d), l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      } else {
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        // the sums' columns are rows of lanes 8 qd and 8 qd + 4
+        l0 = __shfl_sync(0xffffffffu, sum, 8 * qd), l1 = __shfl_sync(0xffffffffu, sum, 8 * qd + 4);
+      }
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         float z0, z1;
@@ -573,7 +665,11 @@ struct Warp {
         put(8 * n + 2 * qd + 1, 32 * i + 4 * g, l1,
             make_float4(fmaf(c[0][1], a, z1), fmaf(c[0][3], b, z1), fmaf(c[1][1], a, z1), fmaf(c[1][3], b, z1)));
       }
-      if (qd == 0) stat(8 * n + g, m, sum);
+      if constexpr (kCols) {
+        if (g == 0) stat(2 * qd, m, l0), stat(2 * qd + 1, ref[1] == -INFINITY ? -INFINITY : ref[1] - (float)off, l1);
+      } else {
+        if (qd == 0) stat(8 * n + g, m, sum);
+      }
     }
   }
 };
@@ -775,7 +871,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   Warp<D, NT, PREC> w;
   bool in_unit = false, began = false, ok = true;
   int held = 0;  // tokens of the unit's sequence
-  int low[NT];   // keys that this lane's rows see
+  using W = Warp<D, NT, PREC>;
+  int low[W::kStats];  // keys that this lane's rows see
   Unit un{0, 0, 0, 0};
   int i = 0;
   if (n_items > 0) {
@@ -802,7 +899,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       in_unit = true, began = e.w & 1;
       held = held_tokens(a.c, un.b);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) low[n] = held - a.n_q + min(un.t0 + (g + 8 * n) / a.G, a.n_q - 1) + 1;
+      for (int n = 0; n < W::kStats; ++n) low[n] = held - a.n_q + min(un.t0 + W::stat_row(n, g, qd) / a.G, a.n_q - 1) + 1;
     }
     if (!__all_sync(0xffffffffu, wait_for(bars + i % NS, (i / NS) & 1))) {  // the warp goes on, or stops, as one
       ok = false;
@@ -810,10 +907,10 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     }
     if (e.x >= 0) {
       const uint8_t* page = ring + i % NS * L::kBytes;
-      int see[NT];
+      int see[W::kStats];
       bool cut = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) see[n] = low[n] - e.y * kPage, cut |= see[n] < kPage;
+      for (int n = 0; n < W::kStats; ++n) see[n] = low[n] - e.y * kPage, cut |= see[n] < kPage;
       if (__any_sync(0xffffffffu, cut)) w.template page<true>(page, g, qd, held - e.y * kPage, see);
       else w.template page<false>(page, g, qd, kPage, see);
     }
