@@ -243,8 +243,8 @@ struct Warp {
   float o[NT][NG][2][4];
   float oz[NT][PREC ? NG : 2];  // the zeros' part: by row g < NG = group and columns, or (PREC) this lane's row's, by group
   int off;                      // weights are held times 2^off
-  // Tokens whose products are under way together: as many as the registers hold (72B-shaped layer: 64 in 68.7
-  // us, 32 in 72.1; with two row sets 32 in 51.9 us on the drafted tokens, 64 spill: 63.9)
+  // Tokens whose products are under way together: as many as the registers hold (72B-shaped layer: 64 in 62.5
+  // us, 32 in 68.3; with two row sets 32 in 51.9 us on the drafted tokens, 64 spill: 63.9)
   static constexpr int kTurn = NT == 1 && !PREC ? 64 : 32;
   static constexpr int kMaxOff = PREC ? 23 : 11;
 
@@ -369,10 +369,22 @@ struct Warp {
     }
   }
 
-  // One page.  kTail: its last tokens may hold nothing (live of them do; what the others hold is arbitrary
-  // bits) or be hidden from some rows (row n of this lane sees low[n] of the page's tokens).
-  template <bool kTail>
-  __device__ __forceinline__ void page(const uint8_t* k, int g, int qd, int live, const int (&low)[kStats]) {
+  // One page.  cut (the same in all lanes): its last tokens may hold nothing (live of them do; what the others
+  // hold is arbitrary bits, which logits and values must not meet) or be hidden from some rows (row n of this
+  // lane sees low[n] of the page's tokens).  One body for all pages: it runs once or a few times a call, and the
+  // time to fetch a second one shows.
+  __device__ __forceinline__ void page(uint8_t* k, int g, int qd, bool cut, int live, const int (&low)[kStats]) {
+    if (cut && live < kPage) {  // the values' scales and zeros of tokens that hold nothing: zero
+      const int lane = 4 * g + qd;
+      if (2 * lane + 1 >= live) {
+        const uint32_t keep = 2 * lane < live ? 0xffffu : 0u;
+        uint32_t* w = reinterpret_cast<uint32_t*>(k + L::kVScales) + lane * NG;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) w[i] &= keep, w[i + L::kMeta / 4] &= keep;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into the stage
+      __syncwarp();
+    }
     constexpr float kUnit = PREC ? 1.0f : 16777216.0f;  // of the codes in the products
     constexpr float kK = kUnit / 32768.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
     uint32_t k1024;
@@ -386,7 +398,6 @@ struct Warp {
       lds_groups<NG>(k + L::kVScales + lane * NG * 4, sw);
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        if (kTail) sw[i] &= (2 * lane < live ? 0xffffu : 0u) | (2 * lane + 1 < live ? 0xffff0000u : 0u);
         top = __vmaxu2(top, sw[i]);
       }
       top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
@@ -428,12 +439,6 @@ struct Warp {
           }
           u[0][t] = fma2(a0, make_float2(kK, kK), make_float2(z[0], z[1]));
           u[0][t + 1] = fma2(a1, make_float2(kK, kK), make_float2(z[2], z[3]));
-          if (kTail) {
-            if (tok >= low[0]) u[0][t].x = -INFINITY;
-            if (tok >= low[kStats - 1]) u[0][t].y = -INFINITY;
-            if (tok + 8 >= low[0]) u[0][t + 1].x = -INFINITY;
-            if (tok + 8 >= low[kStats - 1]) u[0][t + 1].y = -INFINITY;
-          }
         }
       }
 #pragma unroll
@@ -473,11 +478,17 @@ struct Warp {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           u[n][t] = fma2(s[n], make_float2(kK, kK), make_float2(z[2 * n], z[2 * n + 1]));
-          if (kTail) {
-            if (tok + 2 * qd >= low[n]) u[n][t].x = -INFINITY;
-            if (tok + 2 * qd + 1 >= low[n]) u[n][t].y = -INFINITY;
-          }
         }
+      }
+      if (cut) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int t = 0; t < kTurn / 8; ++t) {
+            const int tok = t32 + 8 * t + (kCols ? g : 2 * qd);
+            if (tok >= low[n]) u[n][t].x = -INFINITY;
+            if (tok + (kCols ? 0 : 1) >= low[kCols ? kStats - 1 : n]) u[n][t].y = -INFINITY;
+          }
       }
       // a row's reference rises when a logit passes it by more than 4, so that weights stay at most 2^4
       // (PREC: whenever one passes it)
@@ -524,13 +535,6 @@ struct Warp {
         lds_groups<NG>(k + L::kVCodes + (p1 * 8 + g) * NG * 4, w1[t]);
         lds_groups<NG>(k + L::kVScales + p0 * NG * 4, s0[t]);
         lds_groups<NG>(k + L::kVScales + p1 * NG * 4, s1[t]);
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if (kTail) {
-          keep0 = (2 * p0 < live ? 0xffffu : 0u) | (2 * p0 + 1 < live ? 0xffff0000u : 0u);
-          keep1 = (2 * p1 < live ? 0xffffu : 0u) | (2 * p1 + 1 < live ? 0xffff0000u : 0u);
-#pragma unroll
-          for (int i = 0; i < NG; ++i) s0[t][i] &= keep0, s1[t][i] &= keep1;
-        }
         if constexpr (kCols) {
           const float2 r = make_float2((float)off - (ref[0] == -INFINITY ? 0.0f : ref[0]),
                                        (float)off - (ref[kStats - 1] == -INFINITY ? 0.0f : ref[kStats - 1]));
@@ -557,15 +561,15 @@ struct Warp {
           lds_groups<NG>(k + L::kVZeros + p1 * NG * 4, z1);
 #pragma unroll
           for (int i = 0; i < NG; ++i) {
-            const float2 a0 = unpack2(z0[i] & keep0), a1 = unpack2(z1[i] & keep1), f0 = unpack2(s0[t][i]), f1 = unpack2(s1[t][i]);
+            const float2 a0 = unpack2(z0[i]), a1 = unpack2(z1[i]), f0 = unpack2(s0[t][i]), f1 = unpack2(s1[t][i]);
             const float(&x)[4] = p[0][t];
             oz[0][i] += (x[0] * fmaf(8.0f, f0.x, a0.x) + x[1] * fmaf(8.0f, f0.y, a0.y)) +
                         (x[2] * fmaf(8.0f, f1.x, a1.x) + x[3] * fmaf(8.0f, f1.y, a1.y));
           }
-        } else {  // the same as one product of the middles in fp16; rows g >= NG of its operand are zero
+        } else {  // the same as one product of the middles in fp16 (rows g >= NG of its operand are not used)
           const uint32_t *zs = reinterpret_cast<const uint32_t*>(k + L::kVZeros) + g % NG, *ss = zs - L::kMeta / 4;
-          const uint32_t z0 = hfma2(ss[p0 * NG], 0x48004800u, zs[p0 * NG]) & (g < NG ? keep0 : 0u);
-          const uint32_t z1 = hfma2(ss[p1 * NG], 0x48004800u, zs[p1 * NG]) & (g < NG ? keep1 : 0u);
+          const uint32_t z0 = hfma2(ss[p0 * NG], 0x48004800u, zs[p0 * NG]);
+          const uint32_t z1 = hfma2(ss[p1 * NG], 0x48004800u, zs[p1 * NG]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const float(&x)[4] = p[n][t];
@@ -682,28 +686,28 @@ struct Piece {
 // Joins pieces of one query row: a lane's four channels of the sums and, in every lane, the row's reference
 // and sum.  n pieces, m_of(i), l_of(i) their statistics, y_of(i) this lane's channels: the loads of up to 16
 // pieces are under way together.
-template <class M, class L, class Y>
+template <int J, class M, class L, class Y>
 __device__ __forceinline__ void join_row(int n, int lane, M m_of, L l_of, Y y_of, float4& o, float& top, float& sum) {
   o = make_float4(0, 0, 0, 0);
   top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += 16) {
-    const bool mine = lane < 16 && i0 + lane < n;
+  for (int i0 = 0; i0 < n; i0 += J) {
+    const bool mine = lane < J && i0 + lane < n;
     const float m = mine ? m_of(i0 + lane) : -INFINITY, l = mine ? l_of(i0 + lane) : 0.0f;
-    float4 y[16];
+    float4 y[J];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = i0 + i < n ? y_of(i0 + i) : make_float4(0, 0, 0, 0);
+    for (int i = 0; i < J; ++i) y[i] = i0 + i < n ? y_of(i0 + i) : make_float4(0, 0, 0, 0);
     float now = m;
-    for (int d = 8; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+    for (int d = J / 2; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
     now = fmaxf(top, __shfl_sync(0xffffffffu, now, 0));
     const float back = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
     top = now;
     o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
     float part = f * l;
-    for (int d = 8; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+    for (int d = J / 2; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
     sum = fmaf(sum, back, __shfl_sync(0xffffffffu, part, 0));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < J; ++i) {
       const float w = __shfl_sync(0xffffffffu, f, i);
       o.x = fmaf(w, y[i].x, o.x), o.y = fmaf(w, y[i].y, o.y), o.z = fmaf(w, y[i].z, o.z), o.w = fmaf(w, y[i].w, o.w);
     }
@@ -906,13 +910,11 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       break;
     }
     if (e.x >= 0) {
-      const uint8_t* page = ring + i % NS * L::kBytes;
       int see[W::kStats];
       bool cut = false;
 #pragma unroll
       for (int n = 0; n < W::kStats; ++n) see[n] = low[n] - e.y * kPage, cut |= see[n] < kPage;
-      if (__any_sync(0xffffffffu, cut)) w.template page<true>(page, g, qd, held - e.y * kPage, see);
-      else w.template page<false>(page, g, qd, kPage, see);
+      w.page(ring + i % NS * L::kBytes, g, qd, __any_sync(0xffffffffu, cut), held - e.y * kPage, see);
     }
     __syncwarp();
     if (i + NS < n_items) issue(i + NS);
@@ -979,7 +981,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       float4 o;
       float m, l;
       const int ch = 4 * lane % D;
-      join_row(
+      join_row<8>(
           n, lane, [&](int j) { return src(j)[P::kRows * D + row]; }, [&](int j) { return src(j)[P::kRows * (D + 1) + row]; },
           [&](int j) { return *reinterpret_cast<const float4*>(src(j) + row * D + ch); }, o, m, l);
       if (whole) {
@@ -1020,7 +1022,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       float4 o;
       float m, l;
       const int ch = 4 * lane % D;
-      join_row(
+      join_row<16>(
           n, lane, [&](int j) { return __ldcg(part(j) + P::kRows * D + row); },
           [&](int j) { return __ldcg(part(j) + P::kRows * (D + 1) + row); },
           [&](int j) { return __ldcg(reinterpret_cast<const float4*>(part(j) + row * D + ch)); }, o, m, l);

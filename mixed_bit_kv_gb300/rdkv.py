@@ -760,6 +760,7 @@ class Compressor:
 
 # ---------------------------------------------------------------- 4-bit cache, quantised as it is written
 _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device: torch.cuda.current_stream() costs a microsecond more
+_current_device = torch._C._cuda_getDevice  # the cache's tensors have initialised CUDA
 _Q4_DTYPES = {torch.float16: RDKV_F16, torch.float32: RDKV_F32, torch.bfloat16: RDKV_BF16}
 
 
@@ -901,7 +902,7 @@ def rdkv_q4_write(cache, k, v, row_start=None, max_rows=None, stream=None):
     """Quantises rows k, v into the cache: [batch, n, h_kv, D], the last n tokens of every sequence, or
     [rows, h_kv, D] with row_start int32 [batch + 1] (sequence b's rows, at most max_rows of them).
     cache.lens must already count them."""
-    if stream is not None or cache._index != torch.cuda.current_device():
+    if stream is not None or cache._index != _current_device():
         return _q4_elsewhere(cache, stream, rdkv_q4_write, k, v, row_start, max_rows)
     start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
     code, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
@@ -912,7 +913,7 @@ def rdkv_q4_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype
     """Rows back as (k, v): max_rows of every sequence from position first (int32 [batch], default 0), as
     [batch, max_rows, h_kv, D], or with row_start (int32 [batch + 1]) as [n_rows, h_kv, D].  `out`: a pair
     of tensors to fill instead of new ones.  Rows past a sequence's length are not written."""
-    if stream is not None or cache._index != torch.cuda.current_device():
+    if stream is not None or cache._index != _current_device():
         return _q4_elsewhere(cache, stream, rdkv_q4_read, max_rows, row_start, first, n_rows, dtype, out)
     start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
     at = _q4_index(cache, first, cache.batch, "first")
@@ -959,14 +960,17 @@ def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None
     """Attention of the newest tokens' queries q [batch, n_q, h_q, D] (or [batch, h_q, D]) over the cache:
     (out in q's shape and out_dtype, lse fp32 without D).  sel: pages int32 [batch, n_q, h_kv, n_sel] (or
     without n_q) to attend instead of all.  out_dtype: q's type (default) or torch.float32."""
-    if stream is not None or cache._index != torch.cuda.current_device():
+    if stream is not None or cache._index != _current_device():
         return _q4_elsewhere(cache, stream, rdkv_q4_attn, q, sel, out, lse, out_dtype, ws)
     s = _raw_stream(cache._index)
     code, h_q, n_q, stride = _q4_queries(cache, q)
     shape = q.shape
     if out is None:
         _q4_require(out_dtype in (None, q.dtype, torch.float32), "out must be in q's type or fp32")
-        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=cache.device)
+        if out_dtype is None and q.is_contiguous():
+            out = torch.empty_like(q)
+        else:
+            out = torch.empty(shape, dtype=out_dtype or q.dtype, device=cache.device)
     else:
         _q4_require(out.shape == shape and out.is_contiguous() and out.device == cache.device
                     and out_dtype in (None, out.dtype), "out must be dense and in q's shape")
@@ -990,7 +994,7 @@ def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None
 def rdkv_q4_select(cache, q, n_keep, n_first=1, n_last=1, out=None, ws=None, stream=None):
     """Pages for rdkv_q4_attn's `sel`: int32 [batch, n_q, h_kv, n_keep] (without n_q for q [batch, h_q, D]),
     ascending, -1 behind the last: the first n_first, the last n_last and the best others."""
-    if stream is not None or cache._index != torch.cuda.current_device():
+    if stream is not None or cache._index != _current_device():
         return _q4_elsewhere(cache, stream, rdkv_q4_select, q, n_keep, n_first, n_last, out, ws)
     s = _raw_stream(cache._index)
     code, h_q, n_q, stride = _q4_queries(cache, q)
@@ -1012,6 +1016,6 @@ def rdkv_q4_select(cache, q, n_keep, n_first=1, n_last=1, out=None, ws=None, str
 def rdkv_q4_status(cache, stream=None):
     """What the calls on this cache reported on the device since the last read (RDKV_OK: nothing);
     synchronises the stream."""
-    if stream is not None or cache._index != torch.cuda.current_device():
+    if stream is not None or cache._index != _current_device():
         return _q4_elsewhere(cache, stream, rdkv_q4_status)
     return lib().rdkv_q4_status(cache._ref, _raw_stream(cache._index))
