@@ -846,9 +846,11 @@ def _q4_elsewhere(cache, stream, call, *args):
 
 
 def _q4_index(cache, t, n, name):
-    _q4_require(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n and t.device == cache.device),
-                f"{name} must be a dense int32 tensor of {n} on {cache.device}")
-    return None if t is None else t.data_ptr()
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != cache.device:
+        raise RDKVError(RDKV_ERR_INVALID_ARG, f"{name} must be a dense int32 tensor of {n} on {cache.device}")
+    return t.data_ptr()
 
 
 def _q4_remember(cache, key, found):
@@ -918,17 +920,26 @@ def rdkv_q4_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype
     start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
     at = _q4_index(cache, first, cache.batch, "first")
     if out is None:
-        _q4_require(dtype in _Q4_DTYPES, f"dtype {dtype}")
-        if row_start is None:
-            shape = (cache.batch, max_rows, cache.h_kv, cache.head_dim)
+        key = row_start is None, max_rows, n_rows, dtype
+        found = cache._seen.get(key)
+        if found is None:
+            _q4_require(dtype in _Q4_DTYPES, f"dtype {dtype}")
+            if row_start is None:
+                shape = (cache.batch, max_rows, cache.h_kv, cache.head_dim)
+            else:
+                _q4_require(n_rows is not None, "row_start needs n_rows, the rows of the outputs")
+                shape = (n_rows, cache.h_kv, cache.head_dim)
+            k = torch.empty(shape, dtype=dtype, device=cache.device)
+            v = torch.empty_like(k)
+            found = (torch.Size(shape), *_q4_check_rows(cache, k, v, row_start, max_rows))
+            _q4_remember(cache, key, found)
         else:
-            _q4_require(n_rows is not None, "row_start needs n_rows, the rows of the outputs")
-            shape = (n_rows, cache.h_kv, cache.head_dim)
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
-        v = torch.empty_like(k)
+            k = torch.empty(found[0], dtype=dtype, device=cache.device)
+            v = torch.empty_like(k)
+        _, code, stride, n = found
     else:
         k, v = out
-    code, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
+        code, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
     _check(lib().rdkv_q4_read(cache._ref, code, k.data_ptr(), v.data_ptr(), stride, start, at, n, _raw_stream(cache._index)))
     return k, v
 
@@ -966,10 +977,10 @@ def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None
     code, h_q, n_q, stride = _q4_queries(cache, q)
     shape = q.shape
     if out is None:
-        _q4_require(out_dtype in (None, q.dtype, torch.float32), "out must be in q's type or fp32")
         if out_dtype is None and q.is_contiguous():
             out = torch.empty_like(q)
         else:
+            _q4_require(out_dtype in (None, q.dtype, torch.float32), "out must be in q's type or fp32")
             out = torch.empty(shape, dtype=out_dtype or q.dtype, device=cache.device)
     else:
         _q4_require(out.shape == shape and out.is_contiguous() and out.device == cache.device
@@ -999,7 +1010,8 @@ def rdkv_q4_select(cache, q, n_keep, n_first=1, n_last=1, out=None, ws=None, str
     s = _raw_stream(cache._index)
     code, h_q, n_q, stride = _q4_queries(cache, q)
     _q4_require(cache.bounds is not None, "the cache keeps no bounds")
-    _q4_require(n_keep >= 1, f"n_keep {n_keep}")
+    if n_keep < 1:
+        raise RDKVError(RDKV_ERR_INVALID_ARG, f"n_keep {n_keep}")
     shape = (*q.shape[:-2], cache.h_kv, n_keep)
     if out is None:
         out = torch.empty(shape, dtype=torch.int32, device=cache.device)
