@@ -597,7 +597,8 @@ typedef struct rdkv_q4_cache {
 size_t rdkv_q4_page_bytes(int32_t head_dim);
 
 /* Writes new rows k, v [rows][h_kv][head_dim] in `dtype`, consecutive rows
- * row_stride elements apart (>= h_kv * head_dim).  Sequence b's rows are
+ * row_stride elements apart (>= h_kv * head_dim).  rows counts them all: a
+ * sequence whose rows end past it gets none (RDKV_ERR_INVALID_ARG in *status).  Sequence b's rows are
  * [row_start[b], row_start[b + 1]) (int32 [batch + 1], device), at most
  * max_rows of them, or, with row_start NULL, max_rows rows each, sequence after
  * sequence.  They are its LAST tokens: row i of n goes to position
@@ -606,15 +607,15 @@ size_t rdkv_q4_page_bytes(int32_t head_dim);
  * with row_start NULL a sequence of length 0 is an empty slot: its rows are
  * skipped.  Rows past row_start[batch] are not read.  k, v 16-byte aligned, row_stride a
  * multiple of 16 bytes. */
-rdkv_status rdkv_q4_write(const rdkv_q4_cache* cache, int32_t dtype, const void* k, const void* v, int64_t row_stride,
-                          const int32_t* row_start, int32_t max_rows, void* stream);
+rdkv_status rdkv_q4_write(const rdkv_q4_cache* cache, int32_t dtype, const void* k, const void* v, int64_t rows,
+                          int64_t row_stride, const int32_t* row_start, int32_t max_rows, void* stream);
 
 /* Reads rows back, x^ rounded to `dtype` (fp16 saturates at +-65504): k, v as for rdkv_q4_write,
  * row i of sequence b from position first[b] + i (int32 [batch], device; NULL:
  * 0).  Rows at positions past lens[b] are left as they were, and so are rows
  * of k, v that belong to no sequence. */
-rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, void* v, int64_t row_stride,
-                         const int32_t* row_start, const int32_t* first, int32_t max_rows, void* stream);
+rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, void* v, int64_t rows,
+                         int64_t row_stride, const int32_t* row_start, const int32_t* first, int32_t max_rows, void* stream);
 
 /* Attention of the n_q (1 .. RDKV_Q4_MAX_QUERIES) newest tokens of every
  * sequence over its cache: query token i of sequence b sees positions

@@ -31,13 +31,15 @@ static rdkv_status check_dtype(int32_t dtype) {
   return RDKV_OK;
 }
 
-rdkv_status check_rows(const rdkv_q4_cache* c, int32_t dtype, const void* k, const void* v, int64_t row_stride,
-                       int32_t max_rows) {
+rdkv_status check_rows(const rdkv_q4_cache* c, int32_t dtype, const void* k, const void* v, int64_t rows, int64_t row_stride,
+                       const int32_t* row_start, int32_t max_rows) {
   rdkv_status st = check_cache(c);
   if (st != RDKV_OK) return st;
   st = check_dtype(dtype);
   if (st != RDKV_OK) return st;
   RDKV_REQUIRE(max_rows >= 0, RDKV_ERR_INVALID_ARG, "max_rows %d", max_rows);
+  RDKV_REQUIRE(rows >= (row_start ? 0 : (int64_t)c->batch * max_rows), RDKV_ERR_INVALID_ARG, "%lld rows for %d sequences of %d",
+               (long long)rows, c->batch, max_rows);
   RDKV_REQUIRE((k && v) || max_rows == 0, RDKV_ERR_INVALID_ARG, "NULL rows");
   RDKV_REQUIRE(((uintptr_t)k | (uintptr_t)v) % 16 == 0 && row_stride % (16 / size_of(dtype)) == 0, RDKV_ERR_INVALID_ARG,
                "rows must be 16-byte aligned (row_stride %lld)", (long long)row_stride);
@@ -74,7 +76,7 @@ rdkv_status check_q(const rdkv_q4_cache* c, int32_t dtype, const void* q, int64_
 
 // ---------------------------------------------------------------- rows and the pages they fall in
 struct Rows {
-  int64_t stride;
+  int64_t n, stride;     // rows of k and v, elements between them
   const int32_t* start;  // or NULL: max_rows rows a sequence
   const int32_t* first;  // reading: position of a sequence's first row (NULL: 0)
   int32_t max_rows;
@@ -103,7 +105,7 @@ __device__ __forceinline__ Run find_run(const View& v, const Rows& r, int b, int
   }
   if (n == 0) return o;
   const int64_t first = kWrite ? (int64_t)len - n : r.first ? (int64_t)fetch(r.first + b) : 0;
-  if (n < 0 || n > r.max_rows || r0 < 0 || first < 0 || len < 0) {
+  if (n < 0 || n > r.max_rows || r0 < 0 || r0 + n > r.n || first < 0 || len < 0) {
     if (threadIdx.x == 0) raise(v, RDKV_ERR_INVALID_ARG);
     return o;
   }
@@ -495,11 +497,11 @@ cudaError_t launch_read(unsigned blocks, const View& view, const Rows& r, void* 
 }  // namespace
 
 extern "C" rdkv_status rdkv_q4_write(const rdkv_q4_cache* cache, int32_t dtype, const void* k, const void* v,
-                                     int64_t row_stride, const int32_t* row_start, int32_t max_rows, void* stream) {
-  rdkv_status st = check_rows(cache, dtype, k, v, row_stride, max_rows);
+                                     int64_t rows, int64_t row_stride, const int32_t* row_start, int32_t max_rows, void* stream) {
+  rdkv_status st = check_rows(cache, dtype, k, v, rows, row_stride, row_start, max_rows);
   if (st != RDKV_OK) return st;
   if (max_rows == 0) return RDKV_OK;
-  Rows r{row_stride, row_start, nullptr, max_rows, 0};
+  Rows r{rows, row_stride, row_start, nullptr, max_rows, 0};
   int64_t blocks;
   st = grid_of(cache, &r, &blocks);
   if (st != RDKV_OK) return st;
@@ -515,12 +517,12 @@ extern "C" rdkv_status rdkv_q4_write(const rdkv_q4_cache* cache, int32_t dtype, 
   return RDKV_OK;
 }
 
-extern "C" rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, void* v, int64_t row_stride,
-                                    const int32_t* row_start, const int32_t* first, int32_t max_rows, void* stream) {
-  rdkv_status st = check_rows(cache, dtype, k, v, row_stride, max_rows);
+extern "C" rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, void* v, int64_t rows,
+                                    int64_t row_stride, const int32_t* row_start, const int32_t* first, int32_t max_rows, void* stream) {
+  rdkv_status st = check_rows(cache, dtype, k, v, rows, row_stride, row_start, max_rows);
   if (st != RDKV_OK) return st;
   if (max_rows == 0) return RDKV_OK;
-  Rows r{row_stride, row_start, first, max_rows, 0};
+  Rows r{rows, row_stride, row_start, first, max_rows, 0};
   int64_t blocks;
   st = grid_of(cache, &r, &blocks);
   if (st != RDKV_OK) return st;

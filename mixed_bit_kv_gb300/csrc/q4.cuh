@@ -167,8 +167,8 @@ inline cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, size_t sm
 // ---------------------------------------------------------------- host checks
 inline int size_of(int32_t dtype) { return dtype == RDKV_F32 ? 4 : 2; }
 rdkv_status check_cache(const rdkv_q4_cache* c);
-rdkv_status check_rows(const rdkv_q4_cache* c, int32_t dtype, const void* k, const void* v, int64_t row_stride,
-                       int32_t max_rows);
+rdkv_status check_rows(const rdkv_q4_cache* c, int32_t dtype, const void* k, const void* v, int64_t rows, int64_t row_stride,
+                       const int32_t* row_start, int32_t max_rows);
 rdkv_status check_queries(const rdkv_q4_cache* c, int32_t h_q, int32_t n_q);
 rdkv_status check_q(const rdkv_q4_cache* c, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q, int32_t n_q);
 

@@ -143,8 +143,8 @@ def lib():
             "rdkv_allocate_pack": (ctypes.c_int, [cp, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float,
                                                   _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
             "rdkv_q4_page_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
-            "rdkv_q4_write": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_int64, _P, ctypes.c_int32, _P]),
-            "rdkv_q4_read": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_int32, _P]),
+            "rdkv_q4_write": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int32, _P]),
+            "rdkv_q4_read": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, ctypes.c_int32, _P]),
             "rdkv_q4_attn_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32]),
             "rdkv_q4_attn": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P,
                                             ctypes.c_int32, _P, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P]),
@@ -860,7 +860,7 @@ def _q4_remember(cache, key, found):
 
 
 def _q4_rows(cache, k, v, row_start, max_rows):
-    """(dtype code, row stride, max_rows) of rows k, v [rows, h_kv, D] or [batch, n, h_kv, D]."""
+    """(dtype code, rows, row stride, max_rows) of rows k, v [rows, h_kv, D] or [batch, n, h_kv, D]."""
     key = k.shape, v.shape, k.stride(), v.stride(), k.dtype, v.dtype, k.device, v.device, row_start is None, max_rows
     found = cache._seen.get(key)
     if found is None:
@@ -870,7 +870,7 @@ def _q4_rows(cache, k, v, row_start, max_rows):
 
 
 def _q4_check_rows(cache, k, v, row_start, max_rows):
-    """(dtype code, row stride, max_rows) of rows k, v [rows, h_kv, D] or [batch, n, h_kv, D]."""
+    """(dtype code, rows, row stride, max_rows) of rows k, v [rows, h_kv, D] or [batch, n, h_kv, D]."""
     _q4_require(k.shape == v.shape and k.dtype == v.dtype and k.dtype in _Q4_DTYPES and k.dim() in (3, 4)
                 and k.shape[-2:] == (cache.h_kv, cache.head_dim) and k.device == v.device == cache.device,
                 f"k and v must be rows [.., {cache.h_kv}, {cache.head_dim}] of one type on {cache.device}")
@@ -891,13 +891,13 @@ def _q4_check_rows(cache, k, v, row_start, max_rows):
         else:
             max_rows = n if max_rows is None else max_rows
     if k.numel() == 0:
-        return _Q4_DTYPES[k.dtype], cache.h_kv * cache.head_dim, 0
+        return _Q4_DTYPES[k.dtype], 0, cache.h_kv * cache.head_dim, 0
     if k.shape[0] == 1 and (k.dim() == 3 or n == 1):  # one row in all: its stride says nothing
         stride = other = cache.h_kv * cache.head_dim
     _q4_require(stride == other and k.stride(-1) == v.stride(-1) == 1
                 and (cache.h_kv == 1 or k.stride(-2) == v.stride(-2) == cache.head_dim),
                 "k and v need dense heads and the same distance between rows")
-    return _Q4_DTYPES[k.dtype], stride, int(max_rows)
+    return _Q4_DTYPES[k.dtype], k.shape[0] * (n if k.dim() == 4 else 1), stride, int(max_rows)
 
 
 def rdkv_q4_write(cache, k, v, row_start=None, max_rows=None, stream=None):
@@ -907,8 +907,8 @@ def rdkv_q4_write(cache, k, v, row_start=None, max_rows=None, stream=None):
     if stream is not None or cache._index != _current_device():
         return _q4_elsewhere(cache, stream, rdkv_q4_write, k, v, row_start, max_rows)
     start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
-    code, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
-    _check(lib().rdkv_q4_write(cache._ref, code, k.data_ptr(), v.data_ptr(), stride, start, n, _raw_stream(cache._index)))
+    code, rows, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
+    _check(lib().rdkv_q4_write(cache._ref, code, k.data_ptr(), v.data_ptr(), rows, stride, start, n, _raw_stream(cache._index)))
 
 
 def rdkv_q4_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype=torch.float16, out=None, stream=None):
@@ -936,11 +936,11 @@ def rdkv_q4_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype
         else:
             k = torch.empty(found[0], dtype=dtype, device=cache.device)
             v = torch.empty_like(k)
-        _, code, stride, n = found
+        _, code, rows, stride, n = found
     else:
         k, v = out
-        code, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
-    _check(lib().rdkv_q4_read(cache._ref, code, k.data_ptr(), v.data_ptr(), stride, start, at, n, _raw_stream(cache._index)))
+        code, rows, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
+    _check(lib().rdkv_q4_read(cache._ref, code, k.data_ptr(), v.data_ptr(), rows, stride, start, at, n, _raw_stream(cache._index)))
     return k, v
 
 

@@ -467,13 +467,19 @@ def test_bad_pages_and_lengths_are_left_out_and_reported():
         rdkv.rdkv_q4_write(c, row, row)
         assert rdkv.rdkv_q4_status(c) == code
         assert torch.equal(c.pages, before)
-    # more rows than tokens, than max_rows, or backwards
+    # more rows than tokens, than max_rows, backwards, or past the last row
     c.lens.copy_(torch.tensor([5, 130], dtype=torch.int32))
     rows = _rows(20, 1, 64, torch.float16, 3).to(DEV)
-    for start, most in (([0, 6, 6], 20), ([0, 4, 4], 3), ([4, 0, 0], 20), ([-3, 0, 0], 20)):
+    for start, most in (([0, 6, 6], 20), ([0, 4, 4], 3), ([4, 0, 0], 20), ([-3, 0, 0], 20), ([17, 21, 21], 20),
+                        ([2 ** 31 - 4, 2 ** 31 - 1, 2 ** 31 - 1], 20)):
         rdkv.rdkv_q4_write(c, rows, rows, row_start=torch.tensor(start, dtype=torch.int32, device=DEV), max_rows=most)
         assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_ERR_INVALID_ARG
         assert torch.equal(c.pages, before)
+    guard = torch.full((24, 1, 64), 7.0, dtype=torch.float16, device=DEV)
+    out = guard[:20].view(20, 1, 64), guard.clone()[:20]
+    rdkv.rdkv_q4_read(c, 20, row_start=torch.tensor([17, 21, 21], dtype=torch.int32, device=DEV), out=out)
+    assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_ERR_INVALID_ARG
+    assert (guard == 7).all() and (out[1] == 7).all()
 
 
 def test_a_side_stream_two_graphs_and_replays():

@@ -97,14 +97,14 @@ BAD_CACHES = [(dict(head_dim=96), rdkv.RDKV_ERR_UNSUPPORTED), (dict(batch=0), rd
 
 
 def _call(L, which, c, **kw):
-    a = dict(dtype=0, k=4096, v=4096, stride=128, rows=3, q=4096, q_stride=256, h_q=4, n_q=1, sel=None, n_sel=0, out=4096,
+    a = dict(dtype=0, k=4096, v=4096, stride=128, rows=3, total=1 << 40, starts=None, q=4096, q_stride=256, h_q=4, n_q=1, sel=None, n_sel=0, out=4096,
              out_dtype=0, keep=4, first=1, last=1, ws=4096, ws_bytes=1 << 40)
     a.update(kw)
     r = ctypes.byref(c) if c is not None else None
     if which == "write":
-        return L.rdkv_q4_write(r, a["dtype"], a["k"], a["v"], a["stride"], None, a["rows"], None)
+        return L.rdkv_q4_write(r, a["dtype"], a["k"], a["v"], a["total"], a["stride"], a["starts"], a["rows"], None)
     if which == "read":
-        return L.rdkv_q4_read(r, a["dtype"], a["k"], a["v"], a["stride"], None, None, a["rows"], None)
+        return L.rdkv_q4_read(r, a["dtype"], a["k"], a["v"], a["total"], a["stride"], a["starts"], None, a["rows"], None)
     if which == "attn":
         return L.rdkv_q4_attn(r, a["dtype"], a["q"], a["q_stride"], a["h_q"], a["n_q"], a["sel"], a["n_sel"], a["out"],
                               a["out_dtype"], None, a["ws"], a["ws_bytes"], None)
@@ -126,6 +126,8 @@ def test_bad_caches_are_refused(L, which):
     ("write", dict(dtype=3), rdkv.RDKV_ERR_UNSUPPORTED), ("write", dict(k=None), rdkv.RDKV_ERR_INVALID_ARG),
     ("write", dict(v=4098), rdkv.RDKV_ERR_INVALID_ARG), ("write", dict(stride=127), rdkv.RDKV_ERR_INVALID_ARG),
     ("write", dict(stride=132), rdkv.RDKV_ERR_INVALID_ARG), ("write", dict(rows=-1), rdkv.RDKV_ERR_INVALID_ARG),
+    ("write", dict(total=2), rdkv.RDKV_ERR_INVALID_ARG), ("read", dict(total=2), rdkv.RDKV_ERR_INVALID_ARG),
+    ("read", dict(total=-1, starts=4096), rdkv.RDKV_ERR_INVALID_ARG),
     ("read", dict(dtype=-1), rdkv.RDKV_ERR_UNSUPPORTED), ("read", dict(k=4104), rdkv.RDKV_ERR_INVALID_ARG),
     ("attn", dict(dtype=9), rdkv.RDKV_ERR_UNSUPPORTED), ("attn", dict(q=None), rdkv.RDKV_ERR_INVALID_ARG),
     ("attn", dict(q=4104), rdkv.RDKV_ERR_INVALID_ARG), ("attn", dict(q_stride=255), rdkv.RDKV_ERR_INVALID_ARG),
@@ -180,17 +182,17 @@ def test_the_binding_refuses_wrong_tensors(L):
     cache = rdkv.Q4Cache.__new__(rdkv.Q4Cache)       # the checks of the rows alone, on CPU tensors
     cache.batch, cache.h_kv, cache.head_dim, cache.device, cache._seen = 2, 2, 64, torch.device("cpu"), {}
     rows = torch.zeros(2, 3, 2, 64, dtype=torch.float16)
-    assert rdkv._q4_rows(cache, rows, rows, None, None) == (0, 128, 3)
+    assert rdkv._q4_rows(cache, rows, rows, None, None) == (0, 6, 128, 3)
     wide = torch.zeros(2, 3, 6, 64, dtype=torch.float16)
-    assert rdkv._q4_rows(cache, wide[:, :, 2:4], wide[:, :, 4:], None, None) == (0, 384, 3)
+    assert rdkv._q4_rows(cache, wide[:, :, 2:4], wide[:, :, 4:], None, None) == (0, 6, 384, 3)
     for k, v in ((rows, rows.float()), (rows.double(), rows.double()), (rows[..., ::2], rows[..., ::2]),
                  (rows.transpose(0, 1)[:2], rows.transpose(0, 1)[:2]), (wide[:, :2, :2], wide[:, :2, :2]),
                  (rows[:, :, :1], rows[:, :, :1]), (wide[:, :, :2], rows), (wide[:, :, ::3], wide[:, :, ::3])):
         with pytest.raises(rdkv.RDKVError):
             rdkv._q4_rows(cache, k, v, None, None)
     flat = rows.view(6, 2, 64)
-    assert rdkv._q4_rows(cache, flat, flat, None, None) == (0, 128, 3)
-    assert rdkv._q4_rows(cache, flat[:5], flat[:5], flat, 4) == (0, 128, 4)
+    assert rdkv._q4_rows(cache, flat, flat, None, None) == (0, 6, 128, 3)
+    assert rdkv._q4_rows(cache, flat[:5], flat[:5], flat, 4) == (0, 5, 128, 4)
     with pytest.raises(rdkv.RDKVError):
         rdkv._q4_rows(cache, flat[:5], flat[:5], None, None)
     q = torch.zeros(2, 3, 4, 64)
