@@ -160,6 +160,14 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(bits));
   return d;
 }
+// Two values of at most 2^15 (or, a sixteenth, 2^11) rounded to multiples of 16 (of 1) or of twice or four times that:
+// half of the value added to 24,576 and taken off again.
+__device__ __forceinline__ uint32_t whole16(uint32_t w, bool sixteenth) {
+  const __half2 v = *reinterpret_cast<const __half2*>(&w), k = __float2half2_rn(24576.0f);
+  const __half2 h = __hsub2(__hfma2(v, __float2half2_rn(sixteenth ? 8.0f : 0.5f), k), k);
+  const __half2 d = __hmul2(h, __float2half2_rn(sixteenth ? 0.125f : 2.0f));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
 // k1024: the exponent's bits, in a register that the compiler takes for a variable, so that mask and bits are
 // one instruction (it can hold one constant only).
 __device__ __forceinline__ Pairs centred_pairs(uint32_t w, uint32_t k1024) {
@@ -369,14 +377,45 @@ struct Warp {
     }
   }
 
+  // (kCols) The tensor core cuts its sums some 2^-23 below their largest product: 1e-5 of a logit of fp16 queries.  Long
+  // rows average that away; one of a single page may not, so its queries are taken in two parts: multiples of 16 (their
+  // largest value is 2^15), whose products and sums with codes are all whole, and what that leaves.  This takes the
+  // second part's logits (base 2, times 2^(s - 15), in the order of page()) to r and leaves the first in q.  (lse of
+  // one or two tokens: 4e-7 off instead of 1.4e-6.  With two row sets its code costs 5 % on drafted tokens.)
+  __device__ __forceinline__ void split(const uint8_t* k, float2* r, int g, int qd) {
+    constexpr float kK = 16777216.0f / 32768.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+    auto left = [&](int i, int j) { return minus(q[0][i][j], whole16(q[0][i][j], j & 1)); };
+#pragma unroll 1
+    for (int t = 0; t < kPage / 8; ++t) {  // eight tokens, on the upper half of M
+      uint32_t w[NG], sw[NG];
+      lds_groups<NG>(k + L::kKCodes + ((8 * t + g) * 4 + qd) * NG * 4, w);
+      lds_groups<NG>(k + L::kKScales + (8 * t + g) / 2 * NG * 4, sw);
+      float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const Pairs p = code_pairs(w[i]);
+        const float2 f = unpack2(sw[i]);
+        float c[4];
+        mma16z(c, p.a, 0u, p.b, 0u, left(i, 0), left(i, 1));
+        mma16(c, p.c, 0u, p.d, 0u, left(i, 2), left(i, 3));
+        s.x = fmaf(g & 1 ? f.y : f.x, c[0], s.x), s.y = fmaf(g & 1 ? f.y : f.x, c[1], s.y);
+      }
+      r[t * 32 + 4 * g + qd] = make_float2(s.x * kK, s.y * kK);
+    }
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[0][i][j] = whole16(q[0][i][j], j & 1);
+  }
+
   // One page.  cut (the same in all lanes): its last tokens may hold nothing (live of them do; what the others
   // hold is arbitrary bits, which logits and values must not meet) or be hidden from some rows (row n of this
-  // lane sees low[n] of the page's tokens).  One body for all pages: it runs once or a few times a call, and the
+  // lane sees low[n] of the page's tokens), or it is (only) the unit's one page.  One body for all pages: it runs once or a few times a call, and the
   // time to fetch a second one shows.
-  __device__ __forceinline__ void page(uint8_t* k, int g, int qd, bool cut, int live, const int (&low)[kStats]) {
-    if (cut && live < kPage) {  // the values' scales and zeros of tokens that hold nothing: zero
+  __device__ __forceinline__ void page(uint8_t* k, const float2* r, int g, int qd, bool cut, bool only, int live, const int (&low)[kStats]) {
+    if (cut) {
       const int lane = 4 * g + qd;
-      if (2 * lane + 1 >= live) {
+      if (2 * lane + 1 >= live) {  // the values' scales and zeros of tokens that hold nothing: zero
         const uint32_t keep = 2 * lane < live ? 0xffffu : 0u;
         uint32_t* w = reinterpret_cast<uint32_t*>(k + L::kVScales) + lane * NG;
 #pragma unroll
@@ -481,6 +520,12 @@ struct Warp {
         }
       }
       if (cut) {
+        if constexpr (kCols) {
+          if (only) {
+#pragma unroll
+            for (int t = 0; t < kTurn / 8; ++t) u[0][t] = add2f(u[0][t], r[(t32 / 8 + t) * 32 + 4 * g + qd]);
+          }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -723,7 +768,9 @@ struct Smem {
   static constexpr int kRing = NS * Layout<D>::kBytes;
   static_assert(Partial<D, NT>::kFloats * 4 <= kRing, "a warp's piece goes into its ring");
   static_assert(2 * NW <= 32, "a lane a piece");
-  static constexpr size_t kBars = (size_t)NW * kRing, kInfoAt = kBars + 16 * ((NW * NS + 1) / 2), kBytes = kInfoAt + 16 * NW * kInfo;
+  static constexpr size_t kBars = (size_t)NW * kRing, kInfoAt = kBars + 16 * ((NW * NS + 1) / 2), kRestAt = kInfoAt + 16 * NW * kInfo;
+  static constexpr int kRest = Warp<D, NT, PREC>::kCols ? kPage / 8 * 32 : 0;  // logits of a warp's page
+  static constexpr size_t kBytes = kRestAt + 8 * (size_t)NW * kRest;
 };
 
 template <int D, int NT, bool PREC, int NW, int NS>
@@ -740,6 +787,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, qd = lane % 4, H = a.c.h_kv;
   uint8_t* ring = smem + (size_t)warp * S::kRing;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * NS;
+  float2* rest = reinterpret_cast<float2*>(smem + S::kRestAt) + warp * S::kRest;
   int4* info = reinterpret_cast<int4*>(smem + S::kInfoAt) + warp * kInfo;
   const int BC = a.c.batch * a.n_chunks;
   if (tid == 0) total_s = 0, valid_s = start_s = end_s = 0;
@@ -904,6 +952,10 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       held = held_tokens(a.c, un.b);
 #pragma unroll
       for (int n = 0; n < W::kStats; ++n) low[n] = held - a.n_q + min(un.t0 + W::stat_row(n, g, qd) / a.G, a.n_q - 1) + 1;
+      if constexpr (W::kCols) {
+        if ((e.w & 3) == 3 && e.x >= 0 && __all_sync(0xffffffffu, wait_for(bars + i % NS, (i / NS) & 1)))
+          w.split(ring + i % NS * L::kBytes, rest, g, qd);
+      }
     }
     if (!__all_sync(0xffffffffu, wait_for(bars + i % NS, (i / NS) & 1))) {  // the warp goes on, or stops, as one
       ok = false;
@@ -911,10 +963,11 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     }
     if (e.x >= 0) {
       int see[W::kStats];
+      const bool only = W::kCols && (e.w & 3) == 3;
       bool cut = false;
 #pragma unroll
       for (int n = 0; n < W::kStats; ++n) see[n] = low[n] - e.y * kPage, cut |= see[n] < kPage;
-      w.page(ring + i % NS * L::kBytes, g, qd, __any_sync(0xffffffffu, cut), held - e.y * kPage, see);
+      w.page(ring + i % NS * L::kBytes, rest, g, qd, only || __any_sync(0xffffffffu, cut), only, held - e.y * kPage, see);
     }
     __syncwarp();
     if (i + NS < n_items) issue(i + NS);
