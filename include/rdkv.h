@@ -633,7 +633,8 @@ rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, voi
  * rdkv_q4_select's output, or the caller's own choice): query token i's heads of
  * KV head j see only the positions that also lie in one of those pages (indices
  * into the sequence's pages, position / 64; entries < 0 or past its last page
- * are left out; an index must not occur twice).
+ * are left out; an index must not occur twice), n_sel >= 1 (none to be seen:
+ * entries of -1).
  *
  * ws: rdkv_q4_attn_workspace_bytes bytes, 16-byte aligned, its first
  * RDKV_Q4_COUNTER_BYTES zero before its first use; every call leaves them zero

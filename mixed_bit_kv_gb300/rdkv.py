@@ -967,10 +967,21 @@ def _q4_check_queries(cache, q):
     return _Q4_DTYPES[q.dtype], h_q, n_q, stride
 
 
+def _q4_selection(cache, sel, n_q):
+    """(n_sel, pointer) of pages sel [batch, n_q, h_kv, n_sel], or, for one query token, [batch, h_kv, n_sel].  None:
+    every position.  An empty selection has no pointer, which would mean every position too: it is refused."""
+    if sel is None:
+        return 0, None
+    _q4_require(sel.dim() in (3, 4) and sel.shape[-1] >= 1
+                and (sel.shape[:-1] == (cache.batch, n_q, cache.h_kv) or n_q == 1 and sel.shape[:-1] == (cache.batch, cache.h_kv)),
+                f"sel must be [{cache.batch}, {n_q}, {cache.h_kv}, n_sel] with n_sel >= 1")
+    return sel.shape[-1], _q4_index(cache, sel, sel.numel(), "sel")
+
+
 def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None, stream=None):
     """Attention of the newest tokens' queries q [batch, n_q, h_q, D] (or [batch, h_q, D]) over the cache:
-    (out in q's shape and out_dtype, lse fp32 without D).  sel: pages int32 [batch, n_q, h_kv, n_sel] (or
-    without n_q) to attend instead of all.  out_dtype: q's type (default) or torch.float32."""
+    (out in q's shape and out_dtype, lse fp32 without D).  sel: pages int32 [batch, n_q, h_kv, n_sel] (for one
+    query token also without n_q), n_sel >= 1, to attend instead of all.  out_dtype: q's type (default) or torch.float32."""
     if stream is not None or cache._index != _current_device():
         return _q4_elsewhere(cache, stream, rdkv_q4_attn, q, sel, out, lse, out_dtype, ws)
     s = _raw_stream(cache._index)
@@ -991,10 +1002,7 @@ def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None
     else:
         _q4_require(lse.shape == q.shape[:-1] and lse.dtype == torch.float32 and lse.is_contiguous()
                     and lse.device == cache.device, "lse must be dense fp32 in q's shape without its last size")
-    n_sel, sel_ptr = 0, None
-    if sel is not None:
-        n_sel = sel.shape[-1]
-        sel_ptr = _q4_index(cache, sel, cache.batch * n_q * cache.h_kv * n_sel, "sel")
+    n_sel, sel_ptr = _q4_selection(cache, sel, n_q)
     if ws is None:
         ws = cache.workspace("attn", h_q, n_q, s)
     _check(lib().rdkv_q4_attn(cache._ref, code, q.data_ptr(), stride, h_q, n_q, sel_ptr, n_sel, out.data_ptr(),
