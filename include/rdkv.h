@@ -443,7 +443,7 @@ rdkv_status rdkv_decode_step_lse(rdkv_cache* cache, const void* q, const void* k
  * per row.  outs [n_parts][rows][head_dim], lses [n_parts][rows] fp32 device
  * (rows = B * H_q for decode outputs); out [rows][head_dim] and lse_out
  * [rows] (may be NULL) fp32 device.  Parts with lse = -inf weigh 0; a row with
- * no keys in any part gets out 0, lse -inf.  out may alias outs[0]; lse_out
+ * no keys in any part gets out 0, lse -inf; one with a NaN lse gets NaN.  out may alias outs[0]; lse_out
  * must not alias lses. */
 rdkv_status rdkv_merge_attn(int32_t n_parts, const float* outs, const float* lses, int64_t rows,
                             int32_t head_dim, float* out, float* lse_out, void* stream);
@@ -622,7 +622,9 @@ rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, voi
  * [0, lens[b] - n_q + i + 1), and for query head h (KV head h / G)
  *   out = sum_t softmax_t(q . k^_t / sqrt(head_dim)) v^_t,
  *   lse = ln sum_t exp(q . k^_t / sqrt(head_dim))
- * (no position seen: out 0, lse -inf).  q [batch][n_q][h_q][head_dim] in
+ * (no position seen: out 0, lse -inf; a query that holds a NaN and sees a
+ * position: out and lse NaN, the other queries' as they are).  q
+ * [batch][n_q][h_q][head_dim] in
  * `dtype`, consecutive tokens q_stride elements apart (16-byte aligned,
  * q_stride a multiple of 16 bytes); out [batch][n_q][h_q][head_dim] dense in
  * out_dtype, which is dtype or RDKV_F32 (fp32 outputs are computed to fp32

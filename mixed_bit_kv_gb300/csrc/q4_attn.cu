@@ -227,8 +227,9 @@ __device__ __forceinline__ void put4(const AttnArgs& a, int64_t at, float4 o) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = w;
   }
 }
+// (a NaN sum, of a query that holds one, is not a sum of nothing)
 __device__ __forceinline__ void put_lse(const AttnArgs& a, int64_t row, float m, float l) {
-  if (a.lse) a.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (a.lse) a.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // One warp's running state over the pages of one unit.
@@ -760,7 +761,7 @@ __device__ __forceinline__ void join_row(int n, int lane, M m_of, L l_of, Y y_of
   }
 }
 __device__ __forceinline__ float4 scaled(float4 o, float l) {
-  const float f = l > 0.0f ? 1.0f / l : 0.0f;
+  const float f = l != 0.0f ? 1.0f / l : 0.0f;
   return make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 }
 

@@ -18,12 +18,16 @@
 namespace rdkv {
 
 // ---------------------------------------------------------------- merge of disjoint parts
-// One block per row: weights e^(lse_i - M) of the parts, then the weighted mean of their outputs.
+// One block per row: weights e^(lse_i - M) of the parts, then the weighted mean of their outputs.  A NaN lse
+// is kept as the largest and makes the row NaN (as a largest of numbers alone it would weigh nothing).
 __global__ void merge_attn_kernel(int n_parts, const float* outs, const float* __restrict__ lses, int64_t rows, int D,
                                   float* out, float* __restrict__ lse_out) {
   const int64_t row = blockIdx.x;
   float M = -INFINITY;
-  for (int i = 0; i < n_parts; ++i) M = fmaxf(M, lses[(int64_t)i * rows + row]);
+  for (int i = 0; i < n_parts; ++i) {
+    const float x = lses[(int64_t)i * rows + row];
+    M = x > M || x != x ? x : M;
+  }
   float tot = 0.f;
   if (M != -INFINITY)
     for (int i = 0; i < n_parts; ++i) tot += expf(lses[(int64_t)i * rows + row] - M);  // exp(-inf) = 0
@@ -32,12 +36,12 @@ __global__ void merge_attn_kernel(int n_parts, const float* outs, const float* _
     if (M != -INFINITY)
       for (int i = 0; i < n_parts; ++i) {
         const float w = expf(lses[(int64_t)i * rows + row] - M);
-        if (w > 0.f) acc = fmaf(w, outs[((int64_t)i * rows + row) * D + c], acc);
+        if (w != 0.f) acc = fmaf(w, outs[((int64_t)i * rows + row) * D + c], acc);
       }
     // a thread reads and writes only its own element of the row: out may alias outs[0]
-    out[row * D + c] = tot > 0.f ? acc / tot : 0.f;
+    out[row * D + c] = tot != 0.f ? acc / tot : 0.f;
   }
-  if (lse_out && threadIdx.x == 0) lse_out[row] = tot > 0.f ? M + logf(tot) : -INFINITY;
+  if (lse_out && threadIdx.x == 0) lse_out[row] = tot != 0.f ? M + logf(tot) : -INFINITY;
 }
 
 // ---------------------------------------------------------------- taking zone-C rows

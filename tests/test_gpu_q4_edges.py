@@ -37,3 +37,64 @@ def test_an_empty_or_misshapen_selection_is_refused(T):
     sel[:] = -1                                    # a selection of no page that has a size: nothing is seen
     o, lse = rdkv.rdkv_q4_attn(c, q.to(DEV), sel=sel)
     assert (o == 0).all() and (lse == -math.inf).all() and rdkv.rdkv_q4_status(c) == 0
+
+
+# ---------------------------------------------------------------- non-finite and huge queries
+@pytest.mark.parametrize("dtype,out,D,G,T", [("f16", "f16", 128, 4, 1), ("bf16", "bf16", 64, 3, 4), ("f32", "f32", 64, 8, 1),
+                                             ("f16", "f32", 128, 5, 2), ("bf16", "bf16", 128, 8, 2), ("f16", "f16", 64, 1, 1)])
+@pytest.mark.parametrize("selected", [False, True])
+def test_a_nan_query_is_nan_in_out_and_lse_alone(dtype, out, D, G, T, selected):
+    """One channel of one query row per sequence is NaN: that row is NaN over whatever it sees (pieces of several blocks, one
+    page, a single token), 0 and -inf over nothing, and the other rows hold what they should."""
+    dt, lens, h = TYPES[dtype], [9000, 65, 0, T, 1], 2
+    c, kh, vh = _filled(lens, h, D, dt)
+    q = _rows(len(lens) * T, h * G, D, dt, 9).view(len(lens), T, h * G, D)
+    bad = T - 1, G - 1                             # the last token's last head of the first KV head
+    q[:, bad[0], bad[1], 5] = float("nan")
+    sel = None
+    if selected:
+        sel = torch.arange(3, dtype=torch.int32).repeat(len(lens), T, h, 1)
+        sel[0, :, :, 2] = 140
+    o, lse = rdkv.rdkv_q4_attn(c, q.to(DEV), sel=None if sel is None else sel.to(DEV), out_dtype=TYPES[out])
+    assert rdkv.rdkv_q4_status(c) == 0
+    for b, n in enumerate(lens):
+        row, of = o[b, bad[0], bad[1]], lse[b, bad[0], bad[1]]
+        if n:
+            assert row.isnan().all() and of.isnan(), b
+        else:
+            assert (row == 0).all() and of == -math.inf
+    # and nothing else is: four of the five sequences hold a token, the other heads hold the formula's values
+    assert o.isnan().sum() == 4 * D and lse.isnan().sum() == 4
+    fine = [i for i in range(h * G) if i != bad[1]]
+    for j in range(h):
+        heads = [i for i in fine if i // G == j]
+        if heads:
+            _check_attention(q[:, :, heads], [x[:, j:j + 1] for x in kh], [x[:, j:j + 1] for x in vh], o[:, :, heads], lse[:, :, heads],
+                             None if sel is None else sel[:, :, j:j + 1].numpy())
+
+
+def test_a_nan_lse_stays_in_the_merge():
+    outs = torch.randn(3, 5, 64, device=DEV)
+    lses = torch.tensor([[0.5, float("nan"), -math.inf, 1.0, -math.inf], [1.5, 2.0, float("nan"), -math.inf, -math.inf],
+                         [-math.inf, -math.inf, -math.inf, 3.0, -math.inf]], device=DEV)
+    outs[0, 1], outs[1, 2] = float("nan"), float("nan")
+    out, lse = rdkv.rdkv_merge_attn(outs, lses)
+    assert out[1:3].isnan().all() and lse[1:3].isnan().all()
+    assert (out[4] == 0).all() and lse[4] == -math.inf
+    for r in (0, 3):
+        w = lses[:, r].double().softmax(0)
+        exp = (w[:, None] * outs[:, r].double()).sum(0)
+        # three products, two sums, a quotient and the exponentials: a few roundings of 2^-24
+        assert (out[r].double() - exp).abs().max() <= 2.0 ** -20 * outs[:, r].abs().max()
+        assert abs(lse[r].double() - lses[:, r].double().logsumexp(0)) <= 2.0 ** -20 * 4
+
+
+def test_a_nan_query_stays_nan_behind_the_merge_with_another_cache():
+    c, kh, vh = _filled([70, 70], 1, 64, torch.float32)
+    q = _rows(2, 2, 64, torch.float32, 9)
+    q[1, 0, 3] = float("nan")
+    outs, lses = torch.zeros(2, 2, 2, 64, device=DEV), torch.zeros(2, 2, 2, device=DEV)
+    rdkv.rdkv_q4_attn(c, q.to(DEV), out=outs[0], lse=lses[0])
+    out, lse = rdkv.rdkv_merge_attn(outs, lses)
+    assert out[1, 0].isnan().all() and lse[1, 0].isnan()
+    assert out[0].isfinite().all() and out[1, 1].isfinite().all() and lse[0].isfinite().all() and lse[1, 1].isfinite()
