@@ -247,7 +247,7 @@ struct Warp {
   uint32_t q[kCols ? 1 : 2][NG][4];  // operand registers: rows g, and rows g + 8 (the chunk's second half, or the low parts of the first)
   uint32_t qz[2];                    // operand registers of the zeros' product
   float qs[NG];                      // (PREC) the same sums in fp32
-  float scale[kStats];               // 2^(15 - s): a row's logits are held times 2^(s - 15)
+  float scale[kStats];               // 2^(14 - s): a row's logits are held times 2^(s - 14)
   float ref[kStats], l[kStats];      // the running maximum (base 2) and this lane's share of the sum
   float o[NT][NG][2][4];
   float oz[NT][PREC ? NG : 2];  // the zeros' part: by row g < NG = group and columns, or (PREC) this lane's row's, by group
@@ -305,11 +305,12 @@ struct Warp {
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // the row times 2^s, its largest value in [2^14, 2^15): what fp16 drops is 2^-25 against that
+      // the row times 2^s, its largest value in [2^14, 2^15): what fp16 drops is 2^-25 against that.  Down to s =
+      // -113 and its inverse 2^127, so that every finite row has its place.
       const int e2 = (int)(__float_as_uint(top) >> 23) - 127;
-      const int s = top > 0.0f ? max(-96, min(111, 14 - e2)) : 0;
+      const int s = top > 0.0f ? max(-113, min(111, 14 - e2)) : 0;
       const float up = __uint_as_float((uint32_t)(s + 127) << 23);
-      const float down = __uint_as_float((uint32_t)(15 - s + 127) << 23);
+      const float down = __uint_as_float((uint32_t)(14 - s + 127) << 23);
       if constexpr (kCols) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) scale[j] = __shfl_sync(0xffffffffu, down, 8 * qd + 4 * j);
@@ -331,7 +332,7 @@ struct Warp {
         }
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-        sum[i] *= kK / 32768.0f;
+        sum[i] *= kK / 16384.0f;
       }
       if constexpr (PREC) {
 #pragma unroll
@@ -381,10 +382,10 @@ struct Warp {
   // (kCols) The tensor core cuts its sums some 2^-23 below their largest product: 1e-5 of a logit of fp16 queries.  Long
   // rows average that away; one of a single page may not, so its queries are taken in two parts: multiples of 16 (their
   // largest value is 2^15), whose products and sums with codes are all whole, and what that leaves.  This takes the
-  // second part's logits (base 2, times 2^(s - 15), in the order of page()) to r and leaves the first in q.  (lse of
+  // second part's logits (base 2, times 2^(s - 14), in the order of page()) to r and leaves the first in q.  (lse of
   // one or two tokens: 4e-7 off instead of 1.4e-6.  With two row sets its code costs 5 % on drafted tokens.)
   __device__ __forceinline__ void split(const uint8_t* k, float2* r, int g, int qd) {
-    constexpr float kK = 16777216.0f / 32768.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+    constexpr float kK = 16777216.0f / 16384.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
     auto left = [&](int i, int j) { return minus(q[0][i][j], whole16(q[0][i][j], j & 1)); };
 #pragma unroll 1
     for (int t = 0; t < kPage / 8; ++t) {  // eight tokens, on the upper half of M
@@ -426,7 +427,7 @@ struct Warp {
       __syncwarp();
     }
     constexpr float kUnit = PREC ? 1.0f : 16777216.0f;  // of the codes in the products
-    constexpr float kK = kUnit / 32768.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
+    constexpr float kK = kUnit / 16384.0f * 1.4426950408889634f / (D == 128 ? 11.313708498984761f : 8.0f);
     uint32_t k1024;
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
     {  // The weights' exponent follows the largest value scale met, so that weight times scale stays in
@@ -451,7 +452,7 @@ struct Warp {
     }
 #pragma unroll 1
     for (int t32 = 0; t32 < kPage; t32 += kTurn) {
-      // logits (base 2, times 2^(s - 15)): of tokens t32 + 8 t + 2 qd + {0, 1}, or (kCols) of token t32 + 8 t + g
+      // logits (base 2, times 2^(s - 14)): of tokens t32 + 8 t + 2 qd + {0, 1}, or (kCols) of token t32 + 8 t + g
       // and both columns
       float2 u[NT][kTurn / 8];
       if constexpr (kCols) {

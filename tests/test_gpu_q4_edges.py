@@ -73,6 +73,44 @@ def test_a_nan_query_is_nan_in_out_and_lse_alone(dtype, out, D, G, T, selected):
                              None if sel is None else sel[:, :, j:j + 1].numpy())
 
 
+@pytest.mark.parametrize("dtype,out,T", [("bf16", "bf16", 1), ("bf16", "bf16", 3), ("f32", "f32", 1), ("bf16", "f32", 2)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("exponent", [90, 112, 114, 120, 127])
+def test_queries_as_large_as_their_type_allows(exponent, D, dtype, out, T):
+    """Queries of up to 2^128 against keys so small that the logits are finite: one key takes all, and lse is its logit.
+
+    A logit is off by at most 2^-17 of sum_c |q_c k_c| / sqrt(D) (the bound of the other tests); seeds are such that the best
+    key leads by more than twice that, so the others weigh nothing, and an output is the best key's value: rounded to the
+    output's type (eps / 2), with the weight and weight times scale in fp16 (2^-11 each) for 16-bit outputs, 2^-20 for fp32."""
+    lens = [700, 40]
+    c = _cache(lens, 1, D)
+    k = [(_rows(n, 1, D, torch.float32, 20 + i) * 2.0 ** (6 - exponent / 6)).to(TYPES[dtype]) for i, n in enumerate(lens)]
+    v = [_rows(n, 1, D, TYPES[dtype], 30 + i) for i, n in enumerate(lens)]
+    start = torch.tensor([0, lens[0], sum(lens)], dtype=torch.int32, device=DEV)
+    rdkv.rdkv_q4_write(c, torch.cat(k).to(DEV), torch.cat(v).to(DEV), row_start=start, max_rows=max(lens))
+    g = torch.Generator().manual_seed(7)
+    q = (torch.rand(2, T, 4, D, generator=g) * 1.9 + 0.05) * torch.where(torch.rand(2, T, 4, D, generator=g) < 0.5, -1.0, 1.0)
+    q = (q * 2.0 ** exponent).to(TYPES[dtype])
+    assert q.isfinite().all()
+    o, lse = rdkv.rdkv_q4_attn(c, q.to(DEV), out_dtype=TYPES[out])
+    assert rdkv.rdkv_q4_status(c) == 0
+    eps = torch.finfo(TYPES[out]).eps / 2
+    checked = 0
+    for b, n in enumerate(lens):
+        kh, vh = (O.q4_values(*O.q4_quantize(x[b].float().numpy()))[:, 0] for x in (k, v))
+        for t in range(T):
+            for j in range(4):
+                s = kh[:n - T + t + 1] @ q[b, t, j].double().numpy() / math.sqrt(D)
+                off = 2.0 ** -17 * (np.abs(kh) @ np.abs(q[b, t, j].double().numpy())).max() / math.sqrt(D)
+                assert s.max() < 2.0 ** 127 and abs(lse[b, t, j].item() - s.max()) <= off + 2.0 ** -20 * abs(s.max()), (b, t, j)
+                if np.sort(s)[-1] - np.sort(s)[-2] > 2 * off + 40:
+                    best = vh[s.argmax()]
+                    tol = eps * np.abs(best) + (2.0 ** -20 if out == "f32" else 2 * 2.0 ** -11) * np.abs(vh).max()
+                    assert (np.abs(o[b, t, j].double().cpu().numpy() - best) <= tol).all(), (b, t, j)
+                    checked += 1
+    assert checked >= 6 * T
+
+
 def test_a_nan_lse_stays_in_the_merge():
     outs = torch.randn(3, 5, 64, device=DEV)
     lses = torch.tensor([[0.5, float("nan"), -math.inf, 1.0, -math.inf], [1.5, 2.0, float("nan"), -math.inf, -math.inf],
