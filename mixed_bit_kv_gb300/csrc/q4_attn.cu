@@ -219,7 +219,8 @@ __device__ __forceinline__ void put4(const AttnArgs& a, int64_t at, float4 o) {
   } else {
     uint2 w;
     if (a.out_dtype == RDKV_F16) {
-      w = make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
+      // a mean is no larger than the values (65504 at most), but the weights it is taken with are rounded
+      w = make_uint2(cut_half2(o.x, o.y), cut_half2(o.z, o.w));
     } else {
       const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
       w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));

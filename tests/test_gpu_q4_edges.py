@@ -136,3 +136,30 @@ def test_a_nan_query_stays_nan_behind_the_merge_with_another_cache():
     out, lse = rdkv.rdkv_merge_attn(outs, lses)
     assert out[1, 0].isnan().all() and lse[1, 0].isnan()
     assert out[0].isfinite().all() and out[1, 1].isfinite().all() and lse[0].isfinite().all() and lse[1, 1].isfinite()
+
+
+# ---------------------------------------------------------------- values next to fp16's largest
+@pytest.mark.parametrize("D,G,T", [(128, 8, 1), (64, 4, 1), (128, 8, 2)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_outputs_of_values_next_to_the_largest_fp16(dtype, D, G, T):
+    """Every value is 65504 (or -65504) and so is every mean of them.  The later keys' weights lie where fp16 rounds
+    them up by almost 2^-11: their sum is up to 2^-11 larger than the sum they are divided by, which rounds past
+    fp16's largest value, so outputs in fp16 have to end there."""
+    B, n = 1500, 256
+    c = _cache([n] * B, 1, D)
+    k = torch.zeros(B, n, 1, D)
+    k[:, 64:] = 1.0                                # logits: 0, and the log of the weights below
+    v = torch.full((B, n, 1, D), 65504.0)
+    v[..., 1::2] = -65504.0
+    v[:, :, :, 32:] = 65504.0
+    k, v = k.to(TYPES[dtype]).to(DEV), v.half().to(TYPES[dtype]).to(DEV)
+    rdkv.rdkv_q4_write(c, k, v)
+    w = torch.linspace(4.5e-4, 7e-4, T * G)
+    q = (torch.log1p(w) / math.sqrt(D)).view(1, T, G, 1).expand(B, T, G, D).contiguous().to(TYPES[dtype])
+    o, lse = rdkv.rdkv_q4_attn(c, q.to(DEV))
+    held = rdkv.rdkv_q4_read(c, 1, dtype=torch.float32)[1][0, 0, 0]
+    # eps / 2 of the value; 2^-11 and once more 2^-11 for the weights and weight times scale; fp16's largest value
+    eps = torch.finfo(TYPES[dtype]).eps / 2
+    exp = held.double()
+    assert o.isfinite().all()
+    assert ((o.double() - exp).abs() <= (eps + 2 * 2.0 ** -11) * 65504).all()
