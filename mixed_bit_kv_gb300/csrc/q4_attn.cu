@@ -125,11 +125,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-// the remainders of two values past their fp16 parts
+// the remainders of two values past their fp16 parts, times kUp
+template <int kUp = 1>
 __device__ __forceinline__ uint32_t rest2(float lo, float hi, uint32_t w) {
   const float2 f = unpack2(w);
-  return pack2(lo - f.x, hi - f.y);
+  return pack2((lo - f.x) * kUp, (hi - f.y) * kUp);
 }
+constexpr int kRest = 4096;  // of the weights' remainders: a fp16 part of up to 2^9 leaves up to 2^-3
 template <int NG>
 __device__ __forceinline__ void lds_groups(const uint8_t* p, uint32_t (&w)[NG]) {
   if constexpr (NG == 4) {
@@ -628,15 +630,16 @@ struct Warp {
         }
       }
       // The tensor core cuts what it adds to an accumulator: its accumulators start at zero every turn, and the
-      // sums over the turns are rounded fp32 additions.  PREC: codes less eight and the high parts on a grid of
-      // 1/4 (11 bits below 2^9) make every product and sum of theirs an exact integer of that grid.
+      // sums over the turns are rounded fp32 additions.  PREC: weight times scale (below 2^9) as its fp16 part and,
+      // in accumulators of their own and times 2^12, the remainders: 22 bits of every product down to 2^-15, so that
+      // a group of small values, or many keys of small weight, keep theirs beside the largest.
       if constexpr (!PREC) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) oz[n][0] += cz[n][0], oz[n][1] += cz[n][1];
       }
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        float c[NT][2][4];
+        float c[NT][2][4], rest[PREC ? 2 : 1][4];
 #pragma unroll
         for (int t = 0; t < kTurn / 16; ++t) {
           const Pairs x = centred_pairs(w0[t][i], k1024), y = centred_pairs(w1[t][i], k1024);
@@ -646,21 +649,19 @@ struct Warp {
             if constexpr (PREC) {
               const float2 f0 = unpack2(s0[t][i]), f1 = unpack2(s1[t][i]);
               const float e0 = p[n][t][0] * f0.x, e1 = p[n][t][1] * f0.y, e2 = p[n][t][2] * f1.x, e3 = p[n][t][3] * f1.y;
-              constexpr float kGrid = 3145728.0f;  // 1.5 2^21: its last place is 1/4
-              b0 = pack2(__fadd_rn(__fadd_rn(e0, kGrid), -kGrid), __fadd_rn(__fadd_rn(e1, kGrid), -kGrid));
-              b1 = pack2(__fadd_rn(__fadd_rn(e2, kGrid), -kGrid), __fadd_rn(__fadd_rn(e3, kGrid), -kGrid));
-              const uint32_t c0 = rest2(e0, e1, b0), c1 = rest2(e2, e3, b1);
+              b0 = pack2(e0, e1), b1 = pack2(e2, e3);
+              const uint32_t c0 = rest2<kRest>(e0, e1, b0), c1 = rest2<kRest>(e2, e3, b1);
               if (t == 0) {
-                mma16z(c[n][0], x.a, x.b, y.a, y.b, c0, c1);
-                mma16z(c[n][1], x.c, x.d, y.c, y.d, c0, c1);
+                mma16z(rest[0], x.a, x.b, y.a, y.b, c0, c1);
+                mma16z(rest[1], x.c, x.d, y.c, y.d, c0, c1);
               } else {
-                mma16(c[n][0], x.a, x.b, y.a, y.b, c0, c1);
-                mma16(c[n][1], x.c, x.d, y.c, y.d, c0, c1);
+                mma16(rest[0], x.a, x.b, y.a, y.b, c0, c1);
+                mma16(rest[1], x.c, x.d, y.c, y.d, c0, c1);
               }
             } else {
               b0 = hmul2(hi[n][t][0], s0[t][i]), b1 = hmul2(hi[n][t][1], s1[t][i]);
             }
-            if (t == 0 && !PREC) {
+            if (t == 0) {
               mma16z(c[n][0], x.a, x.b, y.a, y.b, b0, b1);
               mma16z(c[n][1], x.c, x.d, y.c, y.d, b0, b1);
             } else {
@@ -675,7 +676,9 @@ struct Warp {
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {
-              const float2 y = add2f(make_float2(o[n][i][m][j], o[n][i][m][j + 1]), make_float2(c[n][m][j], c[n][m][j + 1]));
+              float2 sum = make_float2(c[n][m][j], c[n][m][j + 1]);
+              if constexpr (PREC) sum = fma2(make_float2(rest[m][j], rest[m][j + 1]), make_float2(1.0f / kRest, 1.0f / kRest), sum);
+              const float2 y = add2f(make_float2(o[n][i][m][j], o[n][i][m][j + 1]), sum);
               o[n][i][m][j] = y.x, o[n][i][m][j + 1] = y.y;
             }
       }
@@ -773,8 +776,8 @@ struct Smem {
   static_assert(Partial<D, NT>::kFloats * 4 <= kRing, "a warp's piece goes into its ring");
   static_assert(2 * NW <= 32, "a lane a piece");
   static constexpr size_t kBars = (size_t)NW * kRing, kInfoAt = kBars + 16 * ((NW * NS + 1) / 2), kRestAt = kInfoAt + 16 * NW * kInfo;
-  static constexpr int kRest = Warp<D, NT, PREC>::kCols ? kPage / 8 * 32 : 0;  // logits of a warp's page
-  static constexpr size_t kBytes = kRestAt + 8 * (size_t)NW * kRest;
+  static constexpr int kRestLogits = Warp<D, NT, PREC>::kCols ? kPage / 8 * 32 : 0;  // logits of a warp's page
+  static constexpr size_t kBytes = kRestAt + 8 * (size_t)NW * kRestLogits;
 };
 
 template <int D, int NT, bool PREC, int NW, int NS>
@@ -791,7 +794,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, qd = lane % 4, H = a.c.h_kv;
   uint8_t* ring = smem + (size_t)warp * S::kRing;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * NS;
-  float2* rest = reinterpret_cast<float2*>(smem + S::kRestAt) + warp * S::kRest;
+  float2* rest = reinterpret_cast<float2*>(smem + S::kRestAt) + warp * S::kRestLogits;
   int4* info = reinterpret_cast<int4*>(smem + S::kInfoAt) + warp * kInfo;
   const int BC = a.c.batch * a.n_chunks;
   if (tid == 0) total_s = 0, valid_s = start_s = end_s = 0;

@@ -163,3 +163,58 @@ def test_outputs_of_values_next_to_the_largest_fp16(dtype, D, G, T):
     exp = held.double()
     assert o.isfinite().all()
     assert ((o.double() - exp).abs() <= (eps + 2 * 2.0 ** -11) * 65504).all()
+
+
+# ---------------------------------------------------------------- fp32 outputs
+def _check_fp32_outputs(k, v, q, logit):
+    """fp32 outputs of one sequence (k, v [n, 1, D], q [1, 1, G, D]) against 64 bits, relative to what each group of 32
+    channels weighs: sum_t p_t max_c |v_tc| over its own channels c, not over the largest of another group.
+
+    A value is taken as the group's middle (|middle| + |code - 8| scale <= 2.1 max_c |v_tc|) and the code's part, whose
+    weight times scale is held in 22 bits (2^-23) and summed with cuts of at most 17 2^-23 of the largest product twice
+    for every 32 tokens: together below 2^-17.5; n / 32 sums of those are rounded, 2^-24 each.  `logit` is the largest
+    error of a logit; it and the exponential (2^-21) change the weights and their sum."""
+    n, _, D = k.shape
+    c = _cache([n], 1, D)
+    rdkv.rdkv_q4_write(c, k[None].to(DEV), v[None].to(DEV))
+    kh, vh = (O.q4_values(*O.q4_quantize(x.float().numpy()))[:, 0] for x in (k, v))
+    o, lse = rdkv.rdkv_q4_attn(c, q.to(DEV), out_dtype=torch.float32)
+    assert rdkv.rdkv_q4_status(c) == 0
+    big = np.repeat(np.abs(vh).reshape(n, D // 32, 32).max(-1), 32, 1)
+    for j in range(q.shape[2]):
+        s = kh @ q[0, 0, j].double().numpy() / math.sqrt(D)
+        p = np.exp(s - s.max())
+        tol = (2 * (logit + 2.0 ** -21) + 2.0 ** -17.5 + n / 32 * 2.0 ** -24) * (p @ big) / p.sum()
+        err = np.abs(o[0, 0, j].double().cpu().numpy() - p @ vh / p.sum())
+        assert (err <= tol).all(), (j, (err / tol).max())
+        assert abs(lse[0, 0, j].item() - (s.max() + math.log(p.sum()))) <= logit + 2.0 ** -21 + n * 2.0 ** -24 / 8
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_fp32_outputs_where_one_key_takes_the_weight_and_others_the_values(D, dtype):
+    """The first key weighs 2^e and its value is zero; the other keys weigh 1 and hold the same value each, so that
+    nothing averages out.  A logit is one product (a few roundings of 2^-24 of up to 14.3)."""
+    n = 64 * 20
+    g = torch.Generator().manual_seed(1)
+    k, v = torch.zeros(n, 1, D), torch.randn(1, 1, D, generator=g).repeat(n, 1, 1)
+    k[0], v[0] = 1.0, 0.0
+    q = torch.zeros(1, 1, 6, D)
+    q[..., 3] = torch.tensor([3.37, 9.61, 12.71, 13.19, 16.23, 20.6]) * math.log(2) * math.sqrt(D)
+    _check_fp32_outputs(*(x.to(TYPES[dtype]) for x in (k, v, q)), logit=4 * 2.0 ** -24 * 14.3)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("ratio", [1.0, 2.0 ** 10, 2.0 ** 20])
+@pytest.mark.parametrize("n", [1, 3, 64, 64 * 9 + 1])
+def test_fp32_outputs_of_groups_of_very_different_size(n, ratio, D, dtype):
+    """The first two groups' values are `ratio` apart.  The logits are exact: 0, or one product with a key of 0 or 1."""
+    g = torch.Generator().manual_seed(2)
+    k = torch.randint(0, 2, (n, 1, 1), generator=g).float().expand(n, 1, D).contiguous()
+    v = torch.randn(n, 1, D, generator=g)
+    v[..., :32] *= math.sqrt(ratio)
+    v[..., 32:64] /= math.sqrt(ratio)
+    q = torch.zeros(1, 1, 4, D)
+    q[..., 3] = torch.tensor([0.0, 0.1, 1.3, 3.3]) * math.sqrt(D)
+    _check_fp32_outputs(*(x.to(TYPES[dtype]) for x in (k, v, q)), logit=4 * 2.0 ** -24 * 3.3)
