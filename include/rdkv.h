@@ -640,7 +640,7 @@ rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, voi
  *
  * ws: rdkv_q4_attn_workspace_bytes bytes, 16-byte aligned, its first
  * RDKV_Q4_COUNTER_BYTES zero before its first use; every call leaves them zero
- * again (unless it reported RDKV_ERR_TIMEOUT: clear them then), so calls of any
+ * again, one that reports RDKV_ERR_TIMEOUT too, so calls of any
  * shape that need no more bytes, of rdkv_q4_select too, may follow one another
  * on it.  Calls that may run at the same time (two streams, two captured
  * graphs) need one each. */
@@ -648,6 +648,20 @@ size_t rdkv_q4_attn_workspace_bytes(const rdkv_q4_cache* cache, int32_t h_q, int
 rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
                          int32_t n_q, const int32_t* sel, int32_t n_sel, void* out, int32_t out_dtype, float* lse,
                          void* ws, size_t ws_bytes, void* stream);
+
+/* Failure-detection self-test of rdkv_q4_attn: its kernel on the same arguments,
+ * but the pages of a sequence whose index plus KV head is a multiple of
+ * `withhold` (>= 1; 1: all) are waited for and never copied.  Each warp that
+ * meets one waits for `wait_cycles` SM clock cycles (clamped to [1e5, 4e9]; 2e6
+ * is about 1 ms), reports RDKV_ERR_TIMEOUT in *status and leaves out what was
+ * left of its pages, as if a copy never completed.  Nothing faults or hangs;
+ * out and lse hold no attention result where a page was left out (all rows are
+ * written), and ws serves the next call.  RDKV_ERR_INVALID_ARG for withhold or
+ * wait_cycles <= 0, else as rdkv_q4_attn. */
+rdkv_status rdkv_q4_timeout_selftest(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride,
+                                     int32_t h_q, int32_t n_q, const int32_t* sel, int32_t n_sel, void* out,
+                                     int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, int32_t withhold,
+                                     int64_t wait_cycles, void* stream);
 
 /* Chooses n_keep pages for every (sequence, query token, KV head): sel
  * [batch][n_q][h_kv][n_keep] int32, ascending, -1 behind the last.  Of the P

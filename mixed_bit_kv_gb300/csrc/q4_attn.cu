@@ -50,9 +50,12 @@ struct AttnArgs {
   int32_t* tickets;  // [units] blocks that have written their part
   int64_t q_stride;
   int dtype, out_dtype, n_q, G, n_sel, chunk, n_chunks;  // chunk: query tokens of a unit
+  int withhold;           // 0, or (the self-test) pages with (index + KV head) % withhold == 0 are waited for, not copied
+  long long wait_cycles;  // limit of a wait for a page
 };
 
 constexpr long long kWaitCycles = 4000000000LL;  // a bounded wait, about two seconds
+constexpr long long kMinWaitCycles = 100000;     // shortest limit the self-test may ask for
 constexpr int kMinItems = 4;                     // of a block (1 to 8: within 3 % of one another on the smallest calls)
 constexpr int kInfo = 32;                        // items whose places a warp knows ahead
 
@@ -65,11 +68,11 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
                : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, long long limit) {
   if (try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!try_wait(bar, parity))
-    if (clock64() - t0 > kWaitCycles) return false;
+    if (clock64() - t0 > limit) return false;
   return true;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -863,8 +866,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       before += __shfl_sync(0xffffffffu, in, 31);
     }
   }
-  // The next n items' places, one a lane: (physical page, head) (-1: nothing to copy), logical page, unit,
-  // and whether the item is its unit's first or last.
+  // The next n items' places, one a lane: (physical page, head) (-1: nothing to copy, -2: a copy withheld),
+  // logical page, unit, and whether the item is its unit's first (1) or last (2).
   int known = 0;
   auto look_up = [&](int n) {
     const int i = known + lane;
@@ -891,7 +894,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
           raise(a.c, RDKV_ERR_INVALID_ARG);
           e.x = -1;
         } else {
-          e.x = e.x * H + h1;
+          e.x = a.withhold && (lp + h1) % a.withhold == 0 ? -2 : e.x * H + h1;
         }
       }
       e.y = lp, e.z = unit, e.w = (p1 == 0 ? 1 : 0) | (p1 == c1 - 1 ? 2 : 0);
@@ -913,7 +916,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       const int4 e = info[i % kInfo];
       const uint32_t bar = smem_u32(bars + i % NS);
       if (e.x < 0) {
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+        if (e.x == -1) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+        else asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 16;" ::"r"(bar) : "memory");
       } else {
         const uint8_t* src = a.c.pages + (int64_t)e.x * L::kBytes;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(L::kBytes) : "memory");
@@ -924,6 +928,16 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       }
     }
     __syncwarp();
+  };
+
+  // Enters the piece of a unit that this warp has written up to item i.
+  auto leave_piece = [&](int i, int unit, bool began, bool ends) {
+    const int at = 2 * warp + (ends ? 0 : 1), items = items_of(a, unit / H);
+    // the unit's first item: this one is its last, or the lookup stands one past the run's last item
+    piece_s[at] = Piece{ends ? w0 + i - (items - 1) : w1 - p, unit, items};
+    atomicOr(&valid_s, 1u << at);
+    if (began) atomicOr(&start_s, 1u << at);
+    if (ends) atomicOr(&end_s, 1u << at);
   };
 
   // ---- the run
@@ -962,11 +976,11 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       for (int n = 0; n < W::kStats; ++n) low[n] = held - a.n_q + min(un.t0 + W::stat_row(n, g, qd) / a.G, a.n_q - 1) + 1;
       if constexpr (W::kCols) {  // (in the page's branch below: 2.5 % more at 262,144 tokens)
         // a page that has not landed by now is taken with whole queries, if it lands in the wait below
-        only = (e.w & 3) == 3 && e.x >= 0 && __all_sync(0xffffffffu, wait_for(bars + i % NS, (i / NS) & 1));
+        only = (e.w & 3) == 3 && e.x >= 0 && __all_sync(0xffffffffu, wait_for(bars + i % NS, (i / NS) & 1, a.wait_cycles));
         if (only) w.split(ring + i % NS * L::kBytes, rest, g, qd);
       }
     }
-    if (!__all_sync(0xffffffffu, wait_for(bars + i % NS, (i / NS) & 1))) {  // the warp goes on, or stops, as one
+    if (!__all_sync(0xffffffffu, wait_for(bars + i % NS, (i / NS) & 1, a.wait_cycles))) {  // the warp goes on, or stops, as one
       ok = false;
       break;
     }
@@ -997,21 +1011,39 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
         w.finish(
             g, qd, [&](int row, int ch, float, float4 o) { *reinterpret_cast<float4*>(dst + row * D + ch) = o; },
             [&](int row, float m, float l) { dst[P::kRows * D + row] = m, dst[P::kRows * (D + 1) + row] = l; });
-        if (lane == 0) {
-          const int at = 2 * warp + (ends ? 0 : 1), items = items_of(a, e.z / H);
-          // the unit's first item: this one is its last, or the lookup stands one past the run's last item
-          piece_s[at] = Piece{ends ? w0 + i - (items - 1) : w1 - p, e.z, items};
-          atomicOr(&valid_s, 1u << at);
-          if (began) atomicOr(&start_s, 1u << at);
-          if (ends) atomicOr(&end_s, 1u << at);
-        }
+        if (lane == 0) leave_piece(i, e.z, began, ends);
       }
       in_unit = false;
     }
   }
-  if (!ok) {  // a wait ran out: report it, and let the copies under way land (again with a limit)
+  if (!ok) {
+    // A wait ran out: report it and let the copies under way land (again with a limit; a withheld one is none).  The
+    // units of the rest of the run get pieces that hold nothing, so that their blocks' tickets come out even and the
+    // workspace serves the next call.
     if (lane == 0) raise(a.c, RDKV_ERR_TIMEOUT);
-    for (int j = i; j < min(i + NS, n_items); ++j) wait_for(bars + j % NS, (j / NS) & 1);
+#pragma unroll 1
+    for (int j = i; j < min(i + NS, n_items); ++j)
+      if (info[j % kInfo].x != -2) wait_for(bars + j % NS, (j / NS) & 1, kWaitCycles);
+    __syncwarp();
+#pragma unroll 1
+    for (; i < n_items; ++i) {
+      if (i >= known) look_up(kInfo / 2);
+      const int4 e = info[i % kInfo];
+      if (!in_unit) in_unit = true, began = e.w & 1;
+      if (!(e.w & 2) && i < n_items - 1) continue;
+      const bool ends = e.w & 2;
+      if (began && ends) {
+        un = unit_at(a, e.z);
+        for (int x = lane; x < un.rows * (D / 4); x += 32)
+          put4(a, row_at(a, un, x / (D / 4)) * D + x % (D / 4) * 4, make_float4(0, 0, 0, 0));
+        if (lane < un.rows) put_lse(a, row_at(a, un, lane), 0.0f, 0.0f);
+      } else {
+        float* dst = ends ? a.heads + (int64_t)me * P::kFloats : reinterpret_cast<float*>(ring);
+        for (int x = lane; x < P::kFloats; x += 32) dst[x] = x / P::kRows == D ? -INFINITY : 0.0f;
+        if (lane == 0) leave_piece(i, e.z, began, ends);
+      }
+      in_unit = false;
+    }
   }
   __syncthreads();
 
@@ -1150,9 +1182,10 @@ extern "C" size_t rdkv_q4_attn_workspace_bytes(const rdkv_q4_cache* cache, int32
   return geometry(cache, h_q, n_q, false, false).bytes;
 }
 
-extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
-                                    int32_t n_q, const int32_t* sel, int32_t n_sel, void* out, int32_t out_dtype, float* lse,
-                                    void* ws, size_t ws_bytes, void* stream) {
+// withhold > 0: the self-test
+static rdkv_status attn_impl(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q, int32_t n_q,
+                             const int32_t* sel, int32_t n_sel, void* out, int32_t out_dtype, float* lse, void* ws, size_t ws_bytes,
+                             void* stream, int withhold, long long wait_cycles) {
   rdkv_status st = check_q(cache, dtype, q, q_stride, h_q, n_q);
   if (st != RDKV_OK) return st;
   RDKV_REQUIRE(out != nullptr, RDKV_ERR_INVALID_ARG, "NULL output");
@@ -1168,7 +1201,7 @@ extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, c
   char* w = static_cast<char*>(ws);
   const AttnArgs a{view_of(cache), q, out, lse, sel, reinterpret_cast<float*>(w + geo.heads_at),
                    reinterpret_cast<float*>(w + geo.parts_at), reinterpret_cast<int32_t*>(w), q_stride, dtype, out_dtype, n_q, h_q / cache->h_kv, n_sel,
-                   geo.chunk, geo.n_chunks};
+                   geo.chunk, geo.n_chunks, withhold, wait_cycles};
   cudaStream_t cs = (cudaStream_t)stream;
   if (cache->head_dim == 128) {
     if (prec) return launch<128, 1, true, 8, 2>(a, geo.grid, cs);
@@ -1178,4 +1211,20 @@ extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, c
   if (prec) return launch<64, 1, true, 8, 4>(a, geo.grid, cs);
   if (geo.nt == 2) return launch<64, 2, false, 8, 4>(a, geo.grid, cs);
   return launch<64, 1, false, 8, 4>(a, geo.grid, cs);
+}
+
+extern "C" rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
+                                    int32_t n_q, const int32_t* sel, int32_t n_sel, void* out, int32_t out_dtype, float* lse,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  return attn_impl(cache, dtype, q, q_stride, h_q, n_q, sel, n_sel, out, out_dtype, lse, ws, ws_bytes, stream, 0, kWaitCycles);
+}
+
+extern "C" rdkv_status rdkv_q4_timeout_selftest(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride,
+                                                int32_t h_q, int32_t n_q, const int32_t* sel, int32_t n_sel, void* out,
+                                                int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, int32_t withhold,
+                                                int64_t wait_cycles, void* stream) {
+  RDKV_REQUIRE(withhold >= 1, RDKV_ERR_INVALID_ARG, "withhold %d must be positive", withhold);
+  RDKV_REQUIRE(wait_cycles > 0, RDKV_ERR_INVALID_ARG, "wait_cycles %lld must be positive", (long long)wait_cycles);
+  return attn_impl(cache, dtype, q, q_stride, h_q, n_q, sel, n_sel, out, out_dtype, lse, ws, ws_bytes, stream, withhold,
+                   std::min(kWaitCycles, std::max(kMinWaitCycles, (long long)wait_cycles)));
 }

@@ -33,7 +33,7 @@ EXPORTED = (
     "rdkv_decode_ragged_workspace_bytes", "rdkv_decode_ragged", "rdkv_decode_ragged_status",
     "rdkv_allocate_pack_workspace_bytes", "rdkv_allocate_pack",
     "rdkv_q4_page_bytes", "rdkv_q4_write", "rdkv_q4_read", "rdkv_q4_attn_workspace_bytes", "rdkv_q4_attn",
-    "rdkv_q4_select_workspace_bytes", "rdkv_q4_select", "rdkv_q4_status",
+    "rdkv_q4_select_workspace_bytes", "rdkv_q4_select", "rdkv_q4_status", "rdkv_q4_timeout_selftest",
 )
 RDKV_CALL_SCORE, RDKV_CALL_ALLOCATE, RDKV_CALL_DECODE = 0, 1, 2
 
@@ -152,6 +152,9 @@ def lib():
             "rdkv_q4_select": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64] + [ctypes.c_int32] * 5
                                + [_P, _P, ctypes.c_size_t, _P]),
             "rdkv_q4_status": (ctypes.c_int, [_P, _P]),
+            "rdkv_q4_timeout_selftest": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                                        _P, ctypes.c_int32, _P, ctypes.c_int32, _P, _P, ctypes.c_size_t,
+                                                        ctypes.c_int32, ctypes.c_int64, _P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -1007,6 +1010,25 @@ def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None
         ws = cache.workspace("attn", h_q, n_q, s)
     _check(lib().rdkv_q4_attn(cache._ref, code, q.data_ptr(), stride, h_q, n_q, sel_ptr, n_sel, out.data_ptr(),
                               _Q4_DTYPES[out.dtype], lse.data_ptr(), ws.data_ptr(), ws.numel(), s))
+    return out, lse
+
+
+def rdkv_q4_timeout_selftest(cache, q, sel=None, out_dtype=None, withhold=1, wait_cycles=2_000_000, ws=None, stream=None):
+    """rdkv_q4_attn with the pages whose index plus KV head is a multiple of `withhold` waited for and never
+    copied: the waits run out after wait_cycles SM cycles each and rdkv_q4_status reports RDKV_ERR_TIMEOUT.
+    Returns (out, lse), which are no results."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q4_timeout_selftest, q, sel, out_dtype, withhold, wait_cycles, ws)
+    s = _raw_stream(cache._index)
+    code, h_q, n_q, stride = _q4_queries(cache, q)
+    out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=cache.device)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=cache.device)
+    n_sel, sel_ptr = _q4_selection(cache, sel, n_q)
+    if ws is None:
+        ws = cache.workspace("attn", h_q, n_q, s)
+    _check(lib().rdkv_q4_timeout_selftest(cache._ref, code, q.data_ptr(), stride, h_q, n_q, sel_ptr, n_sel, out.data_ptr(),
+                                          _Q4_DTYPES[out.dtype], lse.data_ptr(), ws.data_ptr(), ws.numel(), int(withhold),
+                                          int(wait_cycles), s))
     return out, lse
 
 

@@ -218,3 +218,40 @@ def test_fp32_outputs_of_groups_of_very_different_size(n, ratio, D, dtype):
     q = torch.zeros(1, 1, 4, D)
     q[..., 3] = torch.tensor([0.0, 0.1, 1.3, 3.3]) * math.sqrt(D)
     _check_fp32_outputs(*(x.to(TYPES[dtype]) for x in (k, v, q)), logit=4 * 2.0 ** -24 * 3.3)
+
+
+# ---------------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("dtype,out,D,G,T,lens", [
+    ("f16", "f16", 128, 4, 1, [64 * 700, 65, 0, 1]), ("bf16", "bf16", 64, 3, 1, [64 * 700 - 5]), ("f16", "f16", 128, 8, 2, [64 * 300, 64 * 30 + 1]),
+    ("f32", "f32", 64, 5, 1, [64 * 500, 3]), ("bf16", "f32", 128, 8, 4, [64 * 100, 0, 130]), ("f16", "f16", 64, 1, 1, [1 + 37 * i % 190 for i in range(300)]),
+])
+@pytest.mark.parametrize("withhold", [1, 2, 7, 65])
+def test_waits_that_run_out_are_reported_and_the_workspace_serves_on(withhold, dtype, out, D, G, T, lens):
+    """Pages that are waited for and never copied, all of them and a few: the call ends, reports RDKV_ERR_TIMEOUT, writes
+    every row and nothing else, leaves its counters at zero, and the calls after it on the same workspace are right."""
+    dt, h = TYPES[dtype], 2
+    c, kh, vh = _filled(lens, h, D, dt)
+    B = len(lens)
+    q = _rows(B * T, h * G, D, dt, 9).view(B, T, h * G, D).to(DEV)
+    ref = rdkv.rdkv_q4_attn(c, q, out_dtype=TYPES[out])
+    sel = torch.arange(3, dtype=torch.int32, device=DEV).repeat(B, T, h, 1)
+    ref_sel = rdkv.rdkv_q4_attn(c, q, sel=sel, out_dtype=TYPES[out])
+    assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_OK
+    for pages in (None, sel):
+        ws = c.workspace("attn", h * G, T, torch.cuda.current_stream().cuda_stream)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        o, lse = rdkv.rdkv_q4_timeout_selftest(c, q, sel=pages, out_dtype=TYPES[out], withhold=withhold)
+        b.record()
+        hit = any((p + j) % withhold == 0 for n in lens for p in range(-(-n // 64)) for j in range(h)
+                  if pages is None or p < 3)
+        assert rdkv.rdkv_q4_status(c) == (rdkv.RDKV_ERR_TIMEOUT if hit else rdkv.RDKV_OK)
+        assert a.elapsed_time(b) < 200             # one limit of about a millisecond a warp
+        assert (ws[:rdkv.Q4_COUNTER_BYTES] == 0).all()
+        assert o.isfinite().all() and not lse.isnan().any() and (lse < math.inf).all()
+        for _ in range(2):
+            for x, y in ((rdkv.rdkv_q4_attn(c, q, out_dtype=TYPES[out]), ref), (rdkv.rdkv_q4_attn(c, q, sel=sel, out_dtype=TYPES[out]), ref_sel)):
+                assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+        assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_OK
+        if withhold == 1:                          # no page at all: nothing is seen
+            assert (o == 0).all() and (lse == -math.inf).all()

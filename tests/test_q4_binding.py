@@ -1,4 +1,6 @@
 """The 4-bit cache's binding without a GPU: what it refuses before it calls the library."""
+import ctypes
+
 import pytest
 import torch
 
@@ -25,3 +27,18 @@ def test_selections_need_their_own_shape_and_a_page():
                      (sel[..., ::2], 4), (torch.tensor(1, dtype=torch.int32), 1)):
         with pytest.raises(rdkv.RDKVError):
             rdkv._q4_selection(cache, bad, n_q)
+
+
+def test_the_timeout_selftest_refuses_limits_that_are_not_positive():
+    import __graft_entry__
+    __graft_entry__.build()
+    L = rdkv.lib()
+    c = rdkv.Q4CacheStruct(2, 2, 64, 8, 4, 4096, 8192, 256, 512, 1024)
+    before = L.rdkv_launch_count()
+    for withhold, cycles, h_q, ws, code in ((0, 1000, 4, 1 << 40, rdkv.RDKV_ERR_INVALID_ARG), (-1, 1000, 4, 1 << 40, rdkv.RDKV_ERR_INVALID_ARG),
+                                            (1, 0, 4, 1 << 40, rdkv.RDKV_ERR_INVALID_ARG), (1, -5, 4, 1 << 40, rdkv.RDKV_ERR_INVALID_ARG),
+                                            (1, 1000, 3, 1 << 40, rdkv.RDKV_ERR_INVALID_ARG), (1, 1000, 4, 16, rdkv.RDKV_ERR_WORKSPACE)):
+        assert L.rdkv_q4_timeout_selftest(ctypes.byref(c), 0, 4096, 256, h_q, 1, None, 0, 4096, 0, None, 4096, ws, withhold, cycles,
+                                          None) == code
+        assert L.rdkv_last_error_string()
+    assert L.rdkv_launch_count() == before
