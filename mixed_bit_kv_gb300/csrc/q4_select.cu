@@ -53,6 +53,12 @@ __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
+__device__ __forceinline__ void load_eight(const void* q, int64_t at, int dtype, float (&x)[8]) {
+  if (dtype == RDKV_F16) Eight<__half>::load(static_cast<const __half*>(q) + at, x);
+  else if (dtype == RDKV_BF16) Eight<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(q) + at, x);
+  else Eight<float>::load(static_cast<const float*>(q) + at, x);
+}
+
 // This warp's tiles of 16 pages (tile, tile + step, ..): every bound is read once, 16 bytes a lane and load, a
 // tile's loads all in flight together.
 template <int D>
@@ -72,9 +78,7 @@ __device__ __forceinline__ void score_tiles(const SelectArgs& a, int row, int b,
       const int64_t at = (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 8 * qd;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        if (a.dtype == RDKV_F16) Eight<__half>::load(static_cast<const __half*>(a.q) + at + 32 * i, x[i]);
-        else if (a.dtype == RDKV_BF16) Eight<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(a.q) + at + 32 * i, x[i]);
-        else Eight<float>::load(static_cast<const float*>(a.q) + at + 32 * i, x[i]);
+        load_eight(a.q, at + 32 * i, a.dtype, x[i]);
       }
     }
 #pragma unroll
@@ -162,6 +166,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   const float lo = s.y + (a.y + b.y), hi = s.x + lo;
   return make_float2(hi, lo - (hi - s.x));
 }
+__device__ __forceinline__ float2 add_product(float2 sum, float x, float y) {
+  const float p = x * y;
+  return add2(sum, make_float2(p, fmaf(x, y, -p)));
+}
 __device__ __forceinline__ bool above(float2 a, float2 b) { return a.x > b.x || (a.x == b.x && a.y > b.y); }
 
 constexpr int kShared = 8192;  // scores that are kept in shared memory (longer rows are read through L2)
@@ -188,6 +196,49 @@ __device__ __forceinline__ int2 block_scan(int v, int* part) {
   return make_int2(before, all);
 }
 
+// The part that holds the want-th of what bin_s counts, from its first part on, behind `above` others (all threads
+// take part; the counts are cleared).
+struct Border {
+  int part, before, in;  // the part, what lies above it and in it
+};
+__device__ __forceinline__ Border find_border(int* bin_s, int* part, Border* found_s, int want, int above) {
+  int4* mine_s = reinterpret_cast<int4*>(bin_s) + 2 * threadIdx.x;
+  __syncthreads();
+  const int4 x = mine_s[0], y = mine_s[1];
+  mine_s[0] = mine_s[1] = make_int4(0, 0, 0, 0);
+  const int n[kPer] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  const int mine = ((x.x + x.y) + (x.z + x.w)) + ((y.x + y.y) + (y.z + y.w));
+  int before = above + block_scan(mine, part).x;
+  if (before < want && before + mine >= want) {
+    int j = 0;
+#pragma unroll
+    for (int i = 0; i < kPer - 1; ++i)
+      if (j == i && before + n[i] < want) before += n[i], j = i + 1;
+    int in = n[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) in = j == i ? n[i] : in;
+    *found_s = Border{kPer * (int)threadIdx.x + j, before, in};
+  }
+  __syncthreads();
+  return *found_s;
+}
+
+// Order of pages near the border as a number of three words: the sum's high part, its low part, and the page (the
+// lower the larger).
+struct Key {
+  uint32_t w[3];
+};
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);  // (-0 is 0)
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ Key key_of(float2 sum, int page) {  // (infinite sums have no low part)
+  return Key{{ordered(sum.x), ordered(sum.y == sum.y ? sum.y : 0.0f), 0xffffffffu - (uint32_t)page}};
+}
+__device__ __forceinline__ bool at_least(const Key& a, const Key& b) {
+  return a.w[0] != b.w[0] ? a.w[0] > b.w[0] : a.w[1] != b.w[1] ? a.w[1] > b.w[1] : a.w[2] >= b.w[2];
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   extern __shared__ float score_s[];
@@ -196,7 +247,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   __shared__ int part[kWarps], list_s[kFew];
   __shared__ uint32_t mask_s[kShared / 32];
   __shared__ float2 value_s[kFew][8];
-  __shared__ int list_n, sure_n, last_s, found_s, found_n;
+  __shared__ int list_n, sure_n, last_s;
+  __shared__ Border found_s;
   after_previous();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int row = blockIdx.y, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
@@ -257,29 +309,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
         const float s = score[p];
         if (s >= from && s <= hi) atomicAdd(bin_s + kBins - 1 - min(kBins - 1, (int)((s - from) * per)), 1);
       }
-      __syncthreads();
-      const int4 x = mine_s[0], y = mine_s[1];
-      mine_s[0] = mine_s[1] = make_int4(0, 0, 0, 0);
-      const int n[kPer] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      const int mine = ((x.x + x.y) + (x.z + x.w)) + ((y.x + y.y) + (y.z + y.w));
-      int before = above_n + block_scan(mine, part).x;  // thread 0 has the top parts
-      if (before < want && before + mine >= want) {
-        int j = 0;
-#pragma unroll
-        for (int i = 0; i < kPer - 1; ++i)
-          if (j == i && before + n[i] < want) before += n[i], j = i + 1;
-        int in = n[0];
-#pragma unroll
-        for (int i = 1; i < kPer; ++i) in = j == i ? n[i] : in;
-        found_s = kBins - 1 - (kPer * tid + j), found_n = in;
-      }
-      __syncthreads();
-      const int j = found_s;
+      const Border at = find_border(bin_s, part, &found_s, want, above_n);  // thread 0 has the top parts
+      const int j = kBins - 1 - at.part;
       const float slack = 4.0f * FLT_EPSILON * fmaxf(fabsf(from), fabsf(hi)) + 4.0f * FLT_EPSILON * width;
       const float l = from + width * ((float)j / kBins) - slack, u = from + width * ((float)(j + 1) / kBins) + slack;
       const float was = hi - lo;
       lo = fmaxf(lo, l), hi = fminf(hi, u);
-      if (found_n <= 4 || !(hi - lo < 0.5f * was)) break;
+      if (at.in <= 4 || !(hi - lo < 0.5f * was)) break;
       int over = 0;
 #pragma unroll 4
       for (int p = lo_p + tid; p < hi_p; p += kThreads) over += score[p] > hi;
@@ -316,18 +352,17 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   if (near <= need) {
     for (int i = tid; i < near; i += kThreads) keep_page(list[i]);
   } else if (need > 0) {
-    // their sums again: a head of a page a warp, or (many) a page a warp
+    // their sums again: a head of a page a warp, or (many) a page eight lanes
     float2* value = a.value + (int64_t)row * a.c.page_stride;
     const bool few = near <= kFew;
+    if (few) {
 #pragma unroll 1
-    for (int task = warp; task < (few ? near * a.G : near); task += kWarps) {
-      const int i = few ? task / a.G : task, g0 = few ? task - i * a.G : 0, g1 = few ? g0 + 1 : a.G;
-      const int phys = fetch(a.c.page_table + (int64_t)b * a.c.page_stride + (few ? list_s[i] : list[i]));
-      float2 best = make_float2(-INFINITY, 0.0f);
-      if (phys >= 0 && phys < a.c.n_pages) {
-        const __half* e = a.c.bounds + ((int64_t)phys * a.c.h_kv + h) * 2 * D;
-#pragma unroll 1
-        for (int g = g0; g < g1; ++g) {
+      for (int task = warp; task < near * a.G; task += kWarps) {
+        const int i = task / a.G, g = task - i * a.G;
+        const int phys = fetch(a.c.page_table + (int64_t)b * a.c.page_stride + list_s[i]);
+        float2 best = make_float2(-INFINITY, 0.0f);
+        if (phys >= 0 && phys < a.c.n_pages) {
+          const __half* e = a.c.bounds + ((int64_t)phys * a.c.h_kv + h) * 2 * D;
           float2 sum = make_float2(0.0f, 0.0f);
           float x[D / 32], l[D / 32], u[D / 32];
 #pragma unroll
@@ -336,19 +371,47 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
             l[c] = __half2float(e[32 * c + lane]), u[c] = __half2float(e[D + 32 * c + lane]);
           }
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const float y = x[c] > 0.0f ? u[c] : l[c], p = x[c] * y;
-            sum = add2(sum, make_float2(p, fmaf(x[c], y, -p)));
-          }
+          for (int c = 0; c < D / 32; ++c) sum = add_product(sum, x[c], x[c] > 0.0f ? u[c] : l[c]);
 #pragma unroll 1
           for (int d = 16; d; d >>= 1)
             sum = add2(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, d), __shfl_xor_sync(0xffffffffu, sum.y, d)));
           if (above(sum, best)) best = sum;
         }
+        if (lane == 0) value_s[i][g] = best;
       }
-      if (lane == 0) {
-        if (few) value_s[i][g0] = best;
-        else value[i] = best;
+    } else {
+#pragma unroll 1
+      for (int i0 = 4 * warp; i0 < near; i0 += 4 * kWarps) {
+        const int i = i0 + lane / 8;
+        const int phys = i < near ? fetch(a.c.page_table + (int64_t)b * a.c.page_stride + list[i]) : -1;
+        const bool ok = phys >= 0 && phys < a.c.n_pages;
+        const uint4* e = reinterpret_cast<const uint4*>(a.c.bounds + ((int64_t)(ok ? phys : 0) * a.c.h_kv + h) * 2 * D) + lane % 8;
+        uint4 l[D / 64], u[D / 64];  // this lane's channels 64 c + 8 (lane % 8) .. + 7
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) l[c] = fetch(e + 8 * c), u[c] = fetch(e + D / 8 + 8 * c);
+        float2 best = make_float2(-INFINITY, 0.0f);
+#pragma unroll 1
+        for (int g = 0; g < a.G; ++g) {
+          const int64_t at = (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 8 * (lane % 8);
+          float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            float x[8];
+            load_eight(a.q, at + 64 * c, a.dtype, x);
+            const uint32_t lw[4] = {l[c].x, l[c].y, l[c].z, l[c].w}, uw[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 lo2 = __half22float2(*reinterpret_cast<const __half2*>(&lw[j])), hi2 = __half22float2(*reinterpret_cast<const __half2*>(&uw[j]));
+              sum = add_product(sum, x[2 * j], x[2 * j] > 0.0f ? hi2.x : lo2.x);
+              sum = add_product(sum, x[2 * j + 1], x[2 * j + 1] > 0.0f ? hi2.y : lo2.y);
+            }
+          }
+#pragma unroll
+          for (int d = 4; d; d >>= 1)
+            sum = add2(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, d), __shfl_xor_sync(0xffffffffu, sum.y, d)));
+          if (ok && above(sum, best)) best = sum;
+        }
+        if (lane % 8 == 0 && i < near) value[i] = best;
       }
     }
     __syncthreads();
@@ -361,16 +424,49 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
       }
       __syncthreads();
     }
-    auto value_of = [&](int j) { return few ? value_s[j][0] : value[j]; };
-    for (int i = tid; i < near; i += kThreads) {
-      const float2 v = value_of(i);
-      const int p = list[i];
-      int before = 0;
-      for (int j = 0; j < near; ++j) {
-        const float2 o = value_of(j);
-        before += above(o, v) || (!above(v, o) && list[j] < p);
+    if (few) {
+      if (tid < near) {
+        const float2 v = value_s[tid][0];
+        const int p = list_s[tid];
+        int before = 0;
+        for (int j = 0; j < near; ++j) {
+          const float2 o = value_s[j][0];
+          before += above(o, v) || (!above(v, o) && list_s[j] < p);
+        }
+        if (before < need) keep_page(p);
       }
-      if (before < need) keep_page(p);
+    } else {
+      // the need-th best: the digits of its key one after another, until all that share them are wanted
+      Key edge{{0, 0, 0}};
+      int taken = 0;
+#pragma unroll 1
+      for (int d = 0; d < 9; ++d) {
+        const int w = d / 3, low = d % 3 == 0 ? 21 : d % 3 == 1 ? 10 : 0;  // the digit: bits low .. top - 1 of word w
+        const int top = d % 3 == 0 ? 32 : d % 3 == 1 ? 21 : 10;
+        int run = -1, n = 0;  // counts of equal digits are added as one (equal scores would queue for one address)
+#pragma unroll 1
+        for (int i = tid; i < near; i += kThreads) {
+          const Key k = key_of(value[i], list[i]);
+          const uint32_t word = w == 0 ? k.w[0] : w == 1 ? k.w[1] : k.w[2], at = w == 0 ? edge.w[0] : w == 1 ? edge.w[1] : edge.w[2];
+          if ((w > 0 && k.w[0] != edge.w[0]) || (w > 1 && k.w[1] != edge.w[1]) || ((uint64_t)(word ^ at) >> top) != 0) continue;
+          const int digit = kBins - 1 - (int)((word >> low) & (kBins - 1) & ((1u << (top - low)) - 1u));
+          if (digit != run) {
+            if (n) atomicAdd(bin_s + run, n);
+            run = digit, n = 0;
+          }
+          ++n;
+        }
+        if (n) atomicAdd(bin_s + run, n);
+        const Border at = find_border(bin_s, part, &found_s, need, taken);
+        const uint32_t digit = (uint32_t)(kBins - 1 - at.part) << low;
+        if (w == 0) edge.w[0] |= digit;
+        else if (w == 1) edge.w[1] |= digit;
+        else edge.w[2] |= digit;
+        taken = at.before;
+        if (taken + at.in == need) break;
+      }
+      for (int i = tid; i < near; i += kThreads)
+        if (at_least(key_of(value[i], list[i]), edge)) keep_page(list[i]);
     }
   }
   __syncthreads();

@@ -255,3 +255,53 @@ def test_waits_that_run_out_are_reported_and_the_workspace_serves_on(withhold, d
         assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_OK
         if withhold == 1:                          # no page at all: nothing is seen
             assert (o == 0).all() and (lse == -math.inf).all()
+
+
+# ---------------------------------------------------------------- selections of many pages next to one another
+def _bounded(P, h, D, bounds):
+    """A cache of P pages whose bounds are given and whose pages are not read."""
+    c = rdkv.Q4Cache(1, h, D, 64 * P, DEV, pages=torch.zeros(P, h, 80 * D, dtype=torch.uint8, device=DEV),
+                     lens=torch.tensor([64 * P - 5], dtype=torch.int32, device=DEV))
+    c.bounds.copy_(bounds)
+    return c
+
+
+def _check_selection(c, q, bounds, keep, first, last, missing=(), limit=None):
+    """Against 64 bits; pages in `missing` (no valid place) come behind all others."""
+    h = bounds.shape[1]
+    G = q.shape[1] // h
+    run = lambda: rdkv.rdkv_q4_select(c, q.to(DEV), keep, n_first=first, n_last=last)
+    sel = run()
+    for j in range(h):
+        s = O.q4_scores(q[0, G * j:G * j + G].double().numpy(), bounds[:, j].double().numpy())
+        s[list(missing)] = -np.inf
+        assert sel[0, j].tolist() == O.q4_select(s, keep, first, last), j
+    assert torch.equal(run(), sel)
+    if limit is not None:                          # (every inner step a pair of pages: 20 to 100 ms)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        run()
+        b.record()
+        b.synchronize()
+        assert a.elapsed_time(b) < limit
+
+
+@pytest.mark.parametrize("P,keep,first,last", [(33, 8, 1, 1), (600, 64, 0, 0), (8193, 9, 2, 3), (16500, 100, 1, 2), (16500, 16000, 1, 1), (20011, 1, 0, 0)])
+@pytest.mark.parametrize("D,dtype", [(64, "f16"), (128, "bf16"), (64, "f32")])
+def test_selection_among_equal_and_nearly_equal_scores(D, dtype, P, keep, first, last):
+    """All scores equal; in runs of equal ones; a zero query; scores that differ in their last bits.  The order is exact,
+    and the time goes with the number of pages."""
+    g = torch.Generator().manual_seed(P)
+    q = torch.randn(1, 6, D, generator=g).to(TYPES[dtype])
+    one = torch.randn(1, 2, 2, D, generator=g).sort(2).values.half()
+    c = _bounded(P, 2, D, one.expand(P, -1, -1, -1))
+    _check_selection(c, q, one.expand(P, -1, -1, -1), keep, first, last, limit=5.0)
+    _check_selection(c, torch.zeros_like(q), one.expand(P, -1, -1, -1), keep, first, last, limit=5.0)
+    steps = torch.randint(0, 40, (P, 1, 1, 1), generator=g)
+    near = one.repeat(P, 1, 1, 1)                  # one channel tells the pages apart, by forty of fp16's smallest steps
+    near[:, :, :, 5] = (steps[..., 0].float() * 2.0 ** -24).half()
+    c.bounds.copy_(near)
+    _check_selection(c, q, near, keep, first, last, limit=5.0)
+    runs = one * (1 + steps.float() / 64).half()   # forty scores, each of many pages
+    c.bounds.copy_(runs)
+    _check_selection(c, q, runs, keep, first, last, limit=5.0)
