@@ -142,12 +142,14 @@ __device__ __forceinline__ void score_tiles(const SelectArgs& a, int row, int b,
     float err = 0.0f;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+      const int p = tile * kTilePages + 8 * r + g;
+      // (pages that are kept anyway, and those without a place, say nothing about the error of the others)
+      const bool counts = !bad[r] && p >= a.first && p < P - a.last;
       float x = -INFINITY;
-      if (2 * qd < a.G) x = s[2 * r] * back0, err = fmaxf(err, m[2 * r] * back0);
-      if (2 * qd + 1 < a.G) x = fmaxf(x, s[2 * r + 1] * back1), err = fmaxf(err, m[2 * r + 1] * back1);
+      if (2 * qd < a.G) x = s[2 * r] * back0, err = fmaxf(err, counts ? m[2 * r] * back0 : 0.0f);
+      if (2 * qd + 1 < a.G) x = fmaxf(x, s[2 * r + 1] * back1), err = fmaxf(err, counts ? m[2 * r + 1] * back1 : 0.0f);
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-      const int p = tile * kTilePages + 8 * r + g;
       if (qd == 0 && p < P)
         a.score[(int64_t)row * a.c.page_stride + p] = bad[r] || !(x > -FLT_MAX) ? -FLT_MAX : fminf(x, FLT_MAX);
     }
@@ -277,11 +279,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   int4* mine_s = reinterpret_cast<int4*>(bin_s) + 2 * tid;  // this thread's parts
   mine_s[0] = mine_s[1] = make_int4(0, 0, 0, 0);
   float top = -INFINITY, low = INFINITY, eps = 0.0f;
+  int scored = 0;  // pages with a score: others (no place, or nothing but NaN) hold -FLT_MAX and come behind them
   const bool here = P <= kShared;
   for (int p = tid; p < P; p += kThreads) {
     const float s = __ldcg(score + p);
     if (here) score_s[p] = s;
-    if (p >= lo_p && p < hi_p) top = fmaxf(top, s), low = fminf(low, s);
+    if (p >= lo_p && p < hi_p && s > -FLT_MAX) top = fmaxf(top, s), low = fminf(low, s), ++scored;
   }
   for (int i = tid; i < ceil_div(P, kTilePages); i += kThreads) eps = fmaxf(eps, __ldcg(a.error + (int64_t)row * a.tiles + i));
   for (int d = 16; d; d >>= 1) {
@@ -289,12 +292,16 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
     low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
     eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, d));
   }
-  if (lane == 0) part_f[warp][0] = top, part_f[warp][1] = low, part_f[warp][2] = eps;
+  scored = __reduce_add_sync(0xffffffffu, scored);
+  if (lane == 0) part_f[warp][0] = top, part_f[warp][1] = low, part_f[warp][2] = eps, part[warp] = scored;
   __syncthreads();
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_f[w][0]), low = fminf(low, part_f[w][1]), eps = fmaxf(eps, part_f[w][2]);
+  scored = 0;
+  for (int w = 0; w < kWarps; ++w)
+    top = fmaxf(top, part_f[w][0]), low = fminf(low, part_f[w][1]), eps = fmaxf(eps, part_f[w][2]), scored += part[w];
   if (!(eps <= FLT_MAX)) eps = FLT_MAX;
   if (here) score = score_s;
   float lo = low, hi = top;
+  if (scored < want) lo = hi = -FLT_MAX;  // the border lies behind all scores
   if (want > 0) {
     // [lo, hi] holds the want-th best score: its part of 2048, counted from the top, then that one's part, until
     // the interval is narrower than the error or holds few (an interval widened by the rounding of its ends

@@ -305,3 +305,26 @@ def test_selection_among_equal_and_nearly_equal_scores(D, dtype, P, keep, first,
     runs = one * (1 + steps.float() / 64).half()   # forty scores, each of many pages
     c.bounds.copy_(runs)
     _check_selection(c, q, runs, keep, first, last, limit=5.0)
+
+
+@pytest.mark.parametrize("P,keep,first,last", [(16500, 64, 1, 2), (300, 20, 2, 2)])
+@pytest.mark.parametrize("D,dtype", [(64, "f16"), (128, "bf16"), (64, "f32")])
+def test_pages_without_a_place_or_kept_anyway_do_not_blur_the_others(D, dtype, P, keep, first, last):
+    """A page outside the pool has no score, and a first or last page may have a huge one: neither makes the others'
+    order uncertain (a page that has no place comes behind all that have one, in order)."""
+    g = torch.Generator().manual_seed(P)
+    q = torch.randn(1, 6, D, generator=g).to(TYPES[dtype])
+    e = torch.randn(P, 2, 2, D, generator=g).sort(2).values.half()
+    huge = e.clone()
+    huge[:first, :, 0], huge[P - last:, :, 1] = -60000.0, 60000.0
+    c = _bounded(P, 2, D, huge)
+    _check_selection(c, q, huge, keep, first, last, limit=0.4)
+    missing = [7, 77, P - last - 1]
+    c.page_table[0, missing] = torch.tensor([-1, P, 1 << 30], dtype=torch.int32, device=DEV)
+    _check_selection(c, q, huge, keep, first, last, missing, limit=0.4)
+    assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_ERR_INVALID_ARG
+    # fewer scores than pages to keep: the others follow in order
+    some = torch.randperm(P, generator=g)[:P - first - last - 5].tolist()
+    missing = [p for p in some if first <= p < P - last]
+    c.page_table[0, missing] = -1
+    _check_selection(c, q, huge, keep, first, last, missing)
