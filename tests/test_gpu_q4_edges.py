@@ -325,6 +325,6 @@ def test_pages_without_a_place_or_kept_anyway_do_not_blur_the_others(D, dtype, P
     assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_ERR_INVALID_ARG
     # fewer scores than pages to keep: the others follow in order
     some = torch.randperm(P, generator=g)[:P - first - last - 5].tolist()
-    missing = [p for p in some if first <= p < P - last]
+    missing = sorted({*missing, *(p for p in some if first <= p < P - last)})
     c.page_table[0, missing] = -1
     _check_selection(c, q, huge, keep, first, last, missing)
