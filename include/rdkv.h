@@ -670,7 +670,10 @@ rdkv_status rdkv_q4_timeout_selftest(const rdkv_q4_cache* cache, int32_t dtype, 
  *   score(page) = max over the G query heads of sum_c max(q_c lo_c, q_c hi_c),
  * lo and hi the page's `bounds`: no logit of the page's keys (up to the bounds'
  * fp16 rounding) is larger than score / sqrt(head_dim).  Equal scores: the lower
- * page first; the order is that of sums carried to twice fp32's precision.
+ * page first; the order is that of sums carried to twice fp32's precision.  A
+ * query head that holds a NaN or an infinity takes no part in the maximum; with
+ * no other head, and for pages outside the pool (RDKV_ERR_INVALID_ARG in
+ * *status), there is no score: such pages come last, the lower first.
  * q, q_stride, h_q, n_q as for rdkv_q4_attn; 0 <= n_first, 0 <= n_last,
  * n_first + n_last <= n_keep, 1 <= n_keep; cache->bounds not NULL; ws as for
  * rdkv_q4_attn, sized by rdkv_q4_select_workspace_bytes. */

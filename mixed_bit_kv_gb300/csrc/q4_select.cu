@@ -60,16 +60,17 @@ __device__ __forceinline__ void load_eight(const void* q, int64_t at, int dtype,
 }
 
 // This warp's tiles of 16 pages (tile, tile + step, ..): every bound is read once, 16 bytes a lane and load, a
-// tile's loads all in flight together.
+// tile's loads all in flight together.  Returns the power of two by which the row's queries are taken: 1, or what keeps
+// the sums of very large or small ones inside fp32's range.  A head that holds a NaN or an infinity takes no part.
 template <int D>
-__device__ __forceinline__ void score_tiles(const SelectArgs& a, int row, int b, int t, int h, int P, int tile, int step) {
+__device__ __forceinline__ float score_tiles(const SelectArgs& a, int row, int b, int t, int h, int P, int tile, int step) {
   constexpr int NC = D / 32;
   const int lane = threadIdx.x % 32, g = lane / 4, qd = lane % 4, bt = row / a.c.h_kv, n_tiles = ceil_div(P, kTilePages);
   // B: head g of the group, its channels 32 i + 8 qd .. + 7, positive and negative parts and magnitudes
   uint32_t pos[NC][4], neg[NC][4], mag[NC][4];
-  float back;
+  float back, unit;
   {
-    float x[NC][8], top = 0.0f;
+    float x[NC][8], top = 0.0f, odd = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -84,13 +85,19 @@ __device__ __forceinline__ void score_tiles(const SelectArgs& a, int row, int b,
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e])), odd = fmaf(x[i][e], 0.0f, odd);  // NaN where one is not finite
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    odd += __shfl_xor_sync(0xffffffffu, odd, 1);
+    odd += __shfl_xor_sync(0xffffffffu, odd, 2);
+    float most = odd == 0.0f ? top : 0.0f;
+    for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    unit = most >= 1.8446744e19f ? 5.4210109e-20f : most > 0.0f && most < 1e-12f ? 1.8446744e19f : 1.0f;  // 2^64
+    top *= unit;
     // the head times 2^s, its largest value in [1, 2)
     const int s = top > 0.0f ? max(-100, min(100, 127 - (int)(__float_as_uint(top) >> 23))) : 0;
-    const float up = __uint_as_float((uint32_t)(s + 127) << 23);
-    back = __uint_as_float((uint32_t)(127 - s) << 23);
+    const float up = __uint_as_float((uint32_t)(s + 127) << 23) * unit;
+    back = odd == 0.0f ? __uint_as_float((uint32_t)(127 - s) << 23) : NAN;  // (maxima drop it)
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -156,6 +163,7 @@ __device__ __forceinline__ void score_tiles(const SelectArgs& a, int row, int b,
     for (int d = 16; d; d >>= 1) err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, d));
     if (lane == 0) a.error[(int64_t)row * a.tiles + tile] = err * rel;
   }
+  return unit;
 }
 
 // Sums of a high and a low part (about twice fp32's precision).
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   }
   const int blocks = min((int)gridDim.x, ceil_div(ceil_div(P, kTilePages), kWarps));
   if ((int)blockIdx.x >= blocks) return;
-  score_tiles<D>(a, row, b, t, h, P, blockIdx.x * kWarps + warp, blocks * kWarps);
+  const float unit = score_tiles<D>(a, row, b, t, h, P, blockIdx.x * kWarps + warp, blocks * kWarps);
   __syncthreads();
   if (tid == 0) {
     int before;
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
           float x[D / 32], l[D / 32], u[D / 32];
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            x[c] = load_q(a.q, (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 32 * c + lane, a.dtype);
+            x[c] = unit * load_q(a.q, (int64_t)bt * a.q_stride + ((int64_t)h * a.G + g) * D + 32 * c + lane, a.dtype);
             l[c] = __half2float(e[32 * c + lane]), u[c] = __half2float(e[D + 32 * c + lane]);
           }
 #pragma unroll
@@ -405,6 +413,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
           for (int c = 0; c < D / 64; ++c) {
             float x[8];
             load_eight(a.q, at + 64 * c, a.dtype, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= unit;
             const uint32_t lw[4] = {l[c].x, l[c].y, l[c].z, l[c].w}, uw[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

@@ -328,3 +328,38 @@ def test_pages_without_a_place_or_kept_anyway_do_not_blur_the_others(D, dtype, P
     missing = sorted({*missing, *(p for p in some if first <= p < P - last)})
     c.page_table[0, missing] = -1
     _check_selection(c, q, huge, keep, first, last, missing)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("exponent", [-120, -60, 60, 101, 115, 127])
+@pytest.mark.parametrize("P", [40, 700])
+def test_selection_for_queries_of_any_size(P, exponent, dtype):
+    """The sums' range is that of the queries: up to 2^127 times 65504 times the channels."""
+    g = torch.Generator().manual_seed(P)
+    e = (torch.randn(P, 2, 2, 64, generator=g) * 2.0 ** torch.randint(-8, 9, (P, 2, 1, 1), generator=g)).sort(2).values.half()
+    e[3, :, 1, 7] = 65504.0
+    q = torch.randn(1, 4, 64, generator=g).div(8).mul(2.0 ** exponent).to(TYPES[dtype])
+    assert q.isfinite().all()
+    c = _bounded(P, 2, 64, e)
+    _check_selection(c, q, e, 12, 1, 1)
+    q[:, 1] *= 2.0 ** -20                          # heads of very different size
+    _check_selection(c, q, e, 12, 1, 1)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("P", [40, 700])
+def test_heads_that_are_not_finite_leave_the_selection_to_the_others(P, dtype):
+    g = torch.Generator().manual_seed(P)
+    e = (torch.randn(P, 2, 2, 128, generator=g) - 3 * (torch.rand(P, 2, 1, 1, generator=g) < 0.5)).sort(2).values.half()
+    q = torch.randn(1, 6, 128, generator=g).to(TYPES[dtype])
+    c = _bounded(P, 2, 128, e)
+    fine = rdkv.rdkv_q4_select(c, q[:, [0, 2, 3, 5]].contiguous().to(DEV), 12)
+    bad = q.clone()
+    bad[0, 1, 9], bad[0, 4, 100], bad[0, 4, 3] = float("nan"), float("inf"), float("-inf")
+    assert torch.equal(rdkv.rdkv_q4_select(c, bad.to(DEV), 12), fine)
+    for value in (float("nan"), float("inf")):     # no head left: the first pages and the last
+        bad = q.clone()
+        bad[0, 3:] = value
+        got = rdkv.rdkv_q4_select(c, bad.to(DEV), 12)
+        assert got[0, 1].tolist() == list(range(11)) + [P - 1]
+        assert torch.equal(got[0, 0], rdkv.rdkv_q4_select(c, q.to(DEV), 12)[0, 0])
