@@ -602,8 +602,8 @@ size_t rdkv_q4_page_bytes(int32_t head_dim);
  * [row_start[b], row_start[b + 1]) (int32 [batch + 1], device), at most
  * max_rows of them, or, with row_start NULL, max_rows rows each, sequence after
  * sequence.  They are its LAST tokens: row i of n goes to position
- * lens[b] - n + i.  With row_start, a sequence with more than max_rows rows or
- * more rows than lens[b] gets none written (RDKV_ERR_INVALID_ARG in *status);
+ * lens[b] - n + i.  A sequence with more rows than lens[b] (or, with row_start,
+ * than max_rows) gets none written (RDKV_ERR_INVALID_ARG in *status); but
  * with row_start NULL a sequence of length 0 is an empty slot: its rows are
  * skipped.  Rows past row_start[batch] are not read.  k, v 16-byte aligned, row_stride a
  * multiple of 16 bytes. */

@@ -101,7 +101,7 @@ __device__ __forceinline__ Run find_run(const View& v, const Rows& r, int b, int
     n = (int64_t)fetch(r.start + b + 1) - r0;
   } else {
     r0 = (int64_t)b * r.max_rows;
-    n = len > 0 || !kWrite ? r.max_rows : 0;
+    n = len != 0 || !kWrite ? r.max_rows : 0;
   }
   if (n == 0) return o;
   const int64_t first = kWrite ? (int64_t)len - n : r.first ? (int64_t)fetch(r.first + b) : 0;

@@ -363,3 +363,17 @@ def test_heads_that_are_not_finite_leave_the_selection_to_the_others(P, dtype):
         got = rdkv.rdkv_q4_select(c, bad.to(DEV), 12)
         assert got[0, 1].tolist() == list(range(11)) + [P - 1]
         assert torch.equal(got[0, 0], rdkv.rdkv_q4_select(c, q.to(DEV), 12)[0, 0])
+
+
+# ---------------------------------------------------------------- lengths that do not fit
+def test_rows_without_row_start_for_too_short_lengths_are_reported():
+    """A length of zero is an empty slot; one below the number of rows, negative ones among them, is a mistake."""
+    for n, code in ((0, rdkv.RDKV_OK), (1, rdkv.RDKV_ERR_INVALID_ARG), (-1, rdkv.RDKV_ERR_INVALID_ARG), (-2 ** 31, rdkv.RDKV_ERR_INVALID_ARG), (2, rdkv.RDKV_OK)):
+        c, _, _ = _filled([70, 70], 1, 64, torch.float16)
+        before = c.pages.clone()
+        c.lens.copy_(torch.tensor([n, 70], dtype=torch.int32))
+        rows = _rows(4, 1, 64, torch.float16, 3).view(2, 2, 1, 64).to(DEV)
+        rdkv.rdkv_q4_write(c, rows, rows)
+        assert rdkv.rdkv_q4_status(c) == code
+        first = c.page_table[0, 0].long()
+        assert torch.equal(c.pages[first], before[first]) == (n != 2) and not torch.equal(c.pages, before)
