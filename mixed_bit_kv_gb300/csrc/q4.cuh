@@ -74,6 +74,12 @@ __device__ __forceinline__ void after_previous() {
 
 __device__ __forceinline__ void raise(const View& v, int code) { atomicMax(v.status, code); }
 
+// Reports a length that no sequence can have.
+__device__ __forceinline__ void check_length(const View& v, int b) {
+  const int len = fetch(v.lens + b);
+  if (len < 0) raise(v, RDKV_ERR_INVALID_ARG);
+  if ((int64_t)len > (int64_t)v.page_stride * kPage) raise(v, RDKV_ERR_CAPACITY);
+}
 // Tokens that sequence b holds, cut to what its page table can hold.
 __device__ __forceinline__ int held_tokens(const View& v, int b) {
   const int n = fetch(v.lens + b);

@@ -807,11 +807,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
 
   // ---- the items of all units, and where this warp's run of them begins
   if (blockIdx.x == 0)
-    for (int i = tid; i < a.c.batch; i += 32 * NW) {
-      const int len = fetch(a.c.lens + i);
-      if (len < 0) raise(a.c, RDKV_ERR_INVALID_ARG);
-      if ((int64_t)len > (int64_t)a.c.page_stride * kPage) raise(a.c, RDKV_ERR_CAPACITY);
-    }
+    for (int i = tid; i < a.c.batch; i += 32 * NW) check_length(a.c, i);
   const int c0 = lane < BC ? items_of(a, lane) : 0;  // of the first 32 (sequence, chunk) pairs
   int total;  // the host has made sure that all units' items fit
   if (BC <= 32) {

@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int row = blockIdx.y, h = row % a.c.h_kv, bt = row / a.c.h_kv, t = bt % a.n_q, b = bt / a.n_q;
   const int P = pages_seen(a, b, t);
+  if (blockIdx.x == 0 && t == 0 && h == 0 && tid == 0) check_length(a.c, b);
   int32_t* sel = a.sel + (int64_t)row * a.keep;
   if (P <= a.keep) {
     if (blockIdx.x == 0)

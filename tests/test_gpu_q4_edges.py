@@ -377,3 +377,25 @@ def test_rows_without_row_start_for_too_short_lengths_are_reported():
         assert rdkv.rdkv_q4_status(c) == code
         first = c.page_table[0, 0].long()
         assert torch.equal(c.pages[first], before[first]) == (n != 2) and not torch.equal(c.pages, before)
+
+
+def test_lengths_that_no_sequence_can_have_are_reported_by_every_call():
+    for lens, code in (([130, 257, 0], rdkv.RDKV_ERR_CAPACITY), ([-1, 130, 0], rdkv.RDKV_ERR_INVALID_ARG), ([256, 0, 2 ** 31 - 1], rdkv.RDKV_ERR_CAPACITY)):
+        c, _, _ = _filled([256, 256, 256], 2, 64, torch.float16)
+        q = _rows(3 * 2, 4, 64, torch.float16, 9).view(3, 2, 4, 64).to(DEV)
+        rows = _rows(3, 2, 64, torch.float16, 3).view(3, 1, 2, 64).to(DEV)
+        c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        held = torch.tensor([min(max(n, 0), 256) for n in lens], dtype=torch.int32)
+        sel = rdkv.rdkv_q4_select(c, q, 3)
+        assert rdkv.rdkv_q4_status(c) == code
+        out, lse = rdkv.rdkv_q4_attn(c, q, sel=sel)
+        assert rdkv.rdkv_q4_status(c) == code
+        rdkv.rdkv_q4_write(c, rows, rows)
+        assert rdkv.rdkv_q4_status(c) == code
+        rdkv.rdkv_q4_read(c, 257)
+        assert rdkv.rdkv_q4_status(c) == code
+        c, _, _ = _filled([256, 256, 256], 2, 64, torch.float16)  # as if the table's end were the length
+        c.lens.copy_(held)
+        ref = rdkv.rdkv_q4_select(c, q, 3)
+        assert torch.equal(sel, ref) and torch.equal(rdkv.rdkv_q4_attn(c, q, sel=ref)[0], out)
+        assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_OK
