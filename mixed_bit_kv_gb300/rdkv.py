@@ -762,8 +762,10 @@ class Compressor:
 
 
 # ---------------------------------------------------------------- 4-bit cache, quantised as it is written
-_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device: torch.cuda.current_stream() costs a microsecond more
-_current_device = torch._C._cuda_getDevice  # the cache's tensors have initialised CUDA
+# The current raw stream of a device (torch.cuda.current_stream() costs a microsecond more) and the current device (the
+# cache's tensors have initialised CUDA); a torch without these names, such as one built for the CPU, takes the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _Q4_DTYPES = {torch.float16: RDKV_F16, torch.float32: RDKV_F32, torch.bfloat16: RDKV_BF16}
 
 

@@ -1,5 +1,8 @@
 """The 4-bit cache's binding without a GPU: what it refuses before it calls the library."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -42,3 +45,16 @@ def test_the_timeout_selftest_refuses_limits_that_are_not_positive():
                                           None) == code
         assert L.rdkv_last_error_string()
     assert L.rdkv_launch_count() == before
+
+
+def test_the_binding_is_imported_by_a_torch_without_cuda_names():
+    """As a torch built for the CPU has none of them: the module loads, and what needs a GPU says so."""
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda')]: delattr(torch._C, name)\n"
+            "from mixed_bit_kv_gb300 import rdkv\n"
+            "assert rdkv.lib().rdkv_version() >= 1\n"
+            "try: rdkv.Q4Cache(1, 1, 64, 64, 'cpu')\n"
+            "except rdkv.RDKVError: print('refused')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and got.stdout.strip() == "refused", got.stderr
