@@ -774,6 +774,21 @@ def _q4_require(ok, msg):
         raise RDKVError(RDKV_ERR_INVALID_ARG, msg)
 
 
+def _q4_fixed(name):
+    """A tensor of a Q4Cache that its C struct points at: it changes in place, and another one is refused (the calls
+    would go on with the old one's memory, which is freed with it)."""
+    slot = "_" + name
+
+    def get(cache):
+        return getattr(cache, slot)
+
+    def put(cache, t):
+        _q4_require(not hasattr(cache, slot) or getattr(cache, slot) is t, f"{name} changes in place (copy_, add_, +=), or in a new Q4Cache")
+        setattr(cache, slot, t)
+
+    return property(get, put)
+
+
 class Q4Cache:
     """A 4-bit cache of `batch` sequences (slots) of up to max_tokens tokens: its pages, page table,
     lengths and the C struct that points at them.
@@ -781,8 +796,10 @@ class Q4Cache:
     The buffers are allocated unless given: pages uint8 [n_pages, h_kv, 80 * head_dim], bounds fp16
     [n_pages, h_kv, 2, head_dim] (False: none, no rdkv_q4_select), page_table int32 [batch, stride] and
     lens int32 [batch]; caches may share pages and bounds (a pool) under their own tables.  Without a
-    table every sequence gets its own run of pages.  lens is the caller's: raise it before
+    table every sequence gets its own run of pages.  lens is the caller's: raise it, in place, before
     rdkv_q4_write, which writes the last rows of each sequence."""
+
+    pages, bounds, page_table, lens, status = map(_q4_fixed, ("pages", "bounds", "page_table", "lens", "status"))
 
     def __init__(self, batch, h_kv, head_dim, max_tokens, device, pages=None, bounds=None, page_table=None, lens=None):
         _q4_require(batch >= 1 and h_kv >= 1 and max_tokens >= 1, "batch, h_kv and max_tokens must be positive")

@@ -399,3 +399,15 @@ def test_lengths_that_no_sequence_can_have_are_reported_by_every_call():
         ref = rdkv.rdkv_q4_select(c, q, 3)
         assert torch.equal(sel, ref) and torch.equal(rdkv.rdkv_q4_attn(c, q, sel=ref)[0], out)
         assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_OK
+
+
+def test_replaced_lengths_are_refused_and_raised_ones_seen():
+    c, kh, vh = _filled([200], 1, 64, torch.float16)
+    q = _rows(1, 2, 64, torch.float16, 9).view(1, 1, 2, 64)
+    with pytest.raises(rdkv.RDKVError):
+        c.lens = c.lens - 100
+    c.lens -= 100
+    o, lse = rdkv.rdkv_q4_attn(c, q.to(DEV))
+    _check_attention(q, [kh[0][:100]], [vh[0][:100]], o, lse)
+    with pytest.raises(rdkv.RDKVError):
+        c.page_table = c.page_table.clone()

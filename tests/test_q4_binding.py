@@ -58,3 +58,21 @@ def test_the_binding_is_imported_by_a_torch_without_cuda_names():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     got = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert got.returncode == 0 and got.stdout.strip() == "refused", got.stderr
+
+
+def test_the_tensors_behind_the_struct_change_in_place_only():
+    cache = rdkv.Q4Cache.__new__(rdkv.Q4Cache)
+    for name in ("pages", "bounds", "page_table", "lens", "status"):
+        t = torch.zeros(3, dtype=torch.int32)
+        setattr(cache, name, t)
+        assert getattr(cache, name) is t
+        with pytest.raises(rdkv.RDKVError):
+            setattr(cache, name, t + 1)
+        assert getattr(cache, name) is t and (t == 0).all()
+    cache.lens += 1                                  # the same tensor
+    cache.lens[0] = 7
+    assert cache.lens.tolist() == [7, 1, 1]
+    cache = rdkv.Q4Cache.__new__(rdkv.Q4Cache)
+    cache.bounds = None                              # a cache without bounds gets none later
+    with pytest.raises(rdkv.RDKVError):
+        cache.bounds = torch.zeros(3)
