@@ -861,6 +861,7 @@ def _q4_elsewhere(cache, stream, call, *args):
     """call(cache, *args) with `stream` (or the device's current one) and the cache's device current, so that
     what the call allocates belongs to that stream."""
     if stream is not None:
+        _q4_require(stream.device == cache.device, f"a stream of {stream.device} for a cache on {cache.device}")
         with torch.cuda.stream(stream):
             return call(cache, *args)
     with torch.cuda.device(cache.device):

@@ -3,6 +3,7 @@ import ctypes
 import os
 import subprocess
 import sys
+import types
 
 import pytest
 import torch
@@ -76,3 +77,16 @@ def test_the_tensors_behind_the_struct_change_in_place_only():
     cache.bounds = None                              # a cache without bounds gets none later
     with pytest.raises(rdkv.RDKVError):
         cache.bounds = torch.zeros(3)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """(It was passed over: the call ran on the current stream of the cache's device.)"""
+    cache = _cache()
+    cache.device, cache._index = torch.device("cuda", 0), 0
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1))
+    q = torch.zeros(2, 1, 3, 64)
+    for call in (lambda: rdkv.rdkv_q4_write(cache, q, q, stream=stream), lambda: rdkv.rdkv_q4_read(cache, 1, stream=stream),
+                 lambda: rdkv.rdkv_q4_attn(cache, q, stream=stream), lambda: rdkv.rdkv_q4_select(cache, q, 1, stream=stream),
+                 lambda: rdkv.rdkv_q4_status(cache, stream=stream), lambda: rdkv.rdkv_q4_timeout_selftest(cache, q, stream=stream)):
+        with pytest.raises(rdkv.RDKVError, match="cuda:1"):
+            call()
