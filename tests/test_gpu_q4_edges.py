@@ -411,3 +411,57 @@ def test_replaced_lengths_are_refused_and_raised_ones_seen():
     _check_attention(q, [kh[0][:100]], [vh[0][:100]], o, lse)
     with pytest.raises(rdkv.RDKVError):
         c.page_table = c.page_table.clone()
+
+
+# ---------------------------------------------------------------- at the same time
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32")])
+def test_two_captured_graphs_run_at_once(dtype, out):
+    """Two graphs of calls on one cache, whose sequences span several blocks of some SMs, replayed on two streams without
+    waiting for one another, beside eager calls on a third: each has counters of its own, and every result is right."""
+    dt, h, G, D = TYPES[dtype], 1, 4, 128
+    c, _, _ = _filled([64 * 90 + 3, 64 * 61], h, D, dt)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    qs = [_rows(2, h * G, D, dt, 50 + i).view(2, 1, h * G, D).to(DEV) for i in range(3)]
+
+    def step(q):
+        sel = rdkv.rdkv_q4_select(c, q, 40)
+        return (*rdkv.rdkv_q4_attn(c, q, out_dtype=TYPES[out]), *rdkv.rdkv_q4_attn(c, q, sel=sel, out_dtype=TYPES[out]), sel)
+
+    used, workspace = set(), c.workspace
+
+    def recorded(*args):
+        ws = workspace(*args)
+        used.add(ws.data_ptr())
+        return ws
+
+    c.workspace = recorded
+    refs = [step(q) for q in qs]
+    torch.cuda.synchronize()
+    graphs, got, places = [], [], [set(used)]
+    for q in qs[:2]:
+        used.clear()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append([step(q) for _ in range(12)])
+        graphs.append(g)
+        places.append(set(used))
+    torch.cuda.synchronize()
+    assert all(places) and not (places[0] & places[1] or places[0] & places[2] or places[1] & places[2])
+    for _ in range(10):
+        for steps in got:
+            for x in steps:
+                for t in x:
+                    t.fill_(-7)
+        torch.cuda.synchronize()
+        for _ in range(6):                         # each replay overwrites the same outputs
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+            with torch.cuda.stream(streams[2]):
+                eager = [step(qs[2]) for _ in range(4)]
+        torch.cuda.synchronize()
+        for steps, ref in (*zip(got, refs), (eager, refs[2])):
+            for x in steps:
+                for a, b in zip(x, ref):
+                    assert torch.equal(a, b)
+    assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_OK
