@@ -868,6 +868,10 @@ def _q4_elsewhere(cache, stream, call, *args):
         return call(cache, *args)
 
 
+def _q4_check_ws(cache, ws):
+    _q4_require(ws.device == cache.device and ws.is_contiguous(), f"ws must be dense and on {cache.device}")
+
+
 def _q4_index(cache, t, n, name):
     if t is None:
         return None
@@ -1028,6 +1032,8 @@ def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None
     n_sel, sel_ptr = _q4_selection(cache, sel, n_q)
     if ws is None:
         ws = cache.workspace("attn", h_q, n_q, s)
+    else:
+        _q4_check_ws(cache, ws)
     _check(lib().rdkv_q4_attn(cache._ref, code, q.data_ptr(), stride, h_q, n_q, sel_ptr, n_sel, out.data_ptr(),
                               _Q4_DTYPES[out.dtype], lse.data_ptr(), ws.data_ptr(), ws.numel(), s))
     return out, lse
@@ -1046,6 +1052,8 @@ def rdkv_q4_timeout_selftest(cache, q, sel=None, out_dtype=None, withhold=1, wai
     n_sel, sel_ptr = _q4_selection(cache, sel, n_q)
     if ws is None:
         ws = cache.workspace("attn", h_q, n_q, s)
+    else:
+        _q4_check_ws(cache, ws)
     _check(lib().rdkv_q4_timeout_selftest(cache._ref, code, q.data_ptr(), stride, h_q, n_q, sel_ptr, n_sel, out.data_ptr(),
                                           _Q4_DTYPES[out.dtype], lse.data_ptr(), ws.data_ptr(), ws.numel(), int(withhold),
                                           int(wait_cycles), s))
@@ -1070,6 +1078,8 @@ def rdkv_q4_select(cache, q, n_keep, n_first=1, n_last=1, out=None, ws=None, str
                     and out.device == cache.device, f"out must be a dense int32 {list(shape)}")
     if ws is None:
         ws = cache.workspace("select", h_q, n_q, s)
+    else:
+        _q4_check_ws(cache, ws)
     _check(lib().rdkv_q4_select(cache._ref, code, q.data_ptr(), stride, h_q, n_q, n_keep, n_first, n_last,
                                 out.data_ptr(), ws.data_ptr(), ws.numel(), s))
     return out

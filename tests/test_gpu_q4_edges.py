@@ -465,3 +465,16 @@ def test_two_captured_graphs_run_at_once(dtype, out):
                 for a, b in zip(x, ref):
                     assert torch.equal(a, b)
     assert rdkv.rdkv_q4_status(c) == rdkv.RDKV_OK
+
+
+def test_workspaces_on_the_host_are_refused_before_any_launch():
+    c, kh, vh = _filled([200], 1, 64, torch.float16)
+    q = _rows(1, 2, 64, torch.float16, 9).view(1, 1, 2, 64).to(DEV)
+    host = torch.zeros(64 << 20, dtype=torch.uint8)
+    before = rdkv.lib().rdkv_launch_count()
+    for call in (lambda ws: rdkv.rdkv_q4_attn(c, q, ws=ws), lambda ws: rdkv.rdkv_q4_select(c, q, 2, ws=ws),
+                 lambda ws: rdkv.rdkv_q4_timeout_selftest(c, q, ws=ws)):
+        for ws in (host, host.to(DEV)[::2]):
+            with pytest.raises(rdkv.RDKVError):
+                call(ws)
+    assert rdkv.lib().rdkv_launch_count() == before

@@ -90,3 +90,12 @@ def test_a_stream_of_another_device_is_refused():
                  lambda: rdkv.rdkv_q4_status(cache, stream=stream), lambda: rdkv.rdkv_q4_timeout_selftest(cache, q, stream=stream)):
         with pytest.raises(rdkv.RDKVError, match="cuda:1"):
             call()
+
+
+def test_workspaces_elsewhere_are_refused():
+    """A host tensor's address would be one that the GPU cannot reach."""
+    cache = _cache()
+    rdkv._q4_check_ws(cache, torch.zeros(8, dtype=torch.uint8))
+    for bad in (torch.zeros(8, dtype=torch.uint8, device="meta"), torch.zeros(8, 8, dtype=torch.uint8)[:, ::2]):
+        with pytest.raises(rdkv.RDKVError):
+            rdkv._q4_check_ws(cache, bad)
