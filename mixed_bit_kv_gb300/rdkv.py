@@ -917,6 +917,7 @@ def _q4_check_rows(cache, k, v, row_start, max_rows):
             _q4_require(max_rows * cache.batch == n, f"{n} rows for {cache.batch} sequences: give row_start")
         else:
             max_rows = n if max_rows is None else max_rows
+    _q4_require(0 <= max_rows < 2 ** 31, f"max_rows {max_rows}")  # (as a 32-bit argument it would wrap)
     if k.numel() == 0:
         return _Q4_DTYPES[k.dtype], 0, cache.h_kv * cache.head_dim, 0
     if k.shape[0] == 1 and (k.dim() == 3 or n == 1):  # one row in all: its stride says nothing
@@ -1068,8 +1069,8 @@ def rdkv_q4_select(cache, q, n_keep, n_first=1, n_last=1, out=None, ws=None, str
     s = _raw_stream(cache._index)
     code, h_q, n_q, stride = _q4_queries(cache, q)
     _q4_require(cache.bounds is not None, "the cache keeps no bounds")
-    if n_keep < 1:
-        raise RDKVError(RDKV_ERR_INVALID_ARG, f"n_keep {n_keep}")
+    if not (1 <= n_keep < 2 ** 31 and 0 <= n_first <= n_keep and 0 <= n_last <= n_keep):  # (32-bit arguments wrap)
+        raise RDKVError(RDKV_ERR_INVALID_ARG, f"n_keep {n_keep}, n_first {n_first}, n_last {n_last}")
     shape = (*q.shape[:-2], cache.h_kv, n_keep)
     if out is None:
         out = torch.empty(shape, dtype=torch.int32, device=cache.device)

@@ -478,3 +478,14 @@ def test_workspaces_on_the_host_are_refused_before_any_launch():
             with pytest.raises(rdkv.RDKVError):
                 call(ws)
     assert rdkv.lib().rdkv_launch_count() == before
+
+
+def test_counts_past_thirty_two_bits_are_refused_by_the_selection():
+    c, kh, vh = _filled([200], 1, 64, torch.float16)
+    q = _rows(1, 2, 64, torch.float16, 9).view(1, 1, 2, 64).to(DEV)
+    out = torch.zeros(1, 1, 1, 3, dtype=torch.int32, device=DEV)
+    for n in ((3, 2 ** 32, 1), (3, 1, 2 ** 32 + 1), (3, -1, 1), (3, 2, 2), (0, 0, 0), (-1, 0, 0)):
+        with pytest.raises(rdkv.RDKVError):
+            rdkv.rdkv_q4_select(c, q, n[0], n_first=n[1], n_last=n[2], out=out)
+    with pytest.raises(rdkv.RDKVError):
+        rdkv.rdkv_q4_read(c, 2 ** 32, row_start=torch.tensor([0, 1], dtype=torch.int32, device=DEV), n_rows=1)

@@ -99,3 +99,14 @@ def test_workspaces_elsewhere_are_refused():
     for bad in (torch.zeros(8, dtype=torch.uint8, device="meta"), torch.zeros(8, 8, dtype=torch.uint8)[:, ::2]):
         with pytest.raises(rdkv.RDKVError):
             rdkv._q4_check_ws(cache, bad)
+
+
+def test_counts_past_thirty_two_bits_are_refused_instead_of_wrapped():
+    """2^32 rows would have been taken for none, and written nothing."""
+    cache = _cache(h_kv=2)
+    rows = torch.zeros(6, 2, 64, dtype=torch.float16)
+    start = torch.zeros(3, dtype=torch.int32)
+    assert rdkv._q4_rows(cache, rows, rows, start, 2 ** 31 - 1)[3] == 2 ** 31 - 1
+    for bad in (2 ** 31, 2 ** 32, 2 ** 32 + 1, -1):
+        with pytest.raises(rdkv.RDKVError):
+            rdkv._q4_rows(cache, rows, rows, start, bad)
