@@ -128,18 +128,6 @@ __device__ __forceinline__ Run find_run(const View& v, const Rows& r, int b, int
   return o;
 }
 
-__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)), "l"(*reinterpret_cast<const uint64_t*>(&c)));
-  return *reinterpret_cast<const float2*>(&d);
-}
-__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
-  return *reinterpret_cast<const float2*>(&d);
-}
 __device__ __forceinline__ float2 wide2(__half2 v) { return __half22float2(v); }
 __device__ __forceinline__ float2 wide2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
 __device__ __forceinline__ __half2 halves_of(__half a, __half b) { return __halves2half2(a, b); }
@@ -260,9 +248,9 @@ __device__ __forceinline__ Codes quantise8(const Raw<T>& raw) {
   float far = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
-    const float2 d = add_f32x2(make_float2(x[i], x[i + 1]), zero);
-    const float2 c = add_f32x2(fma_f32x2(d, rs2, up), down);
-    const float2 e = fma_f32x2(d, rs2, make_float2(-c.x, -c.y));
+    const float2 d = add2f(make_float2(x[i], x[i + 1]), zero);
+    const float2 c = add2f(fma2(d, rs2, up), down);
+    const float2 e = fma2(d, rs2, make_float2(-c.x, -c.y));
     r.c[i] = c.x, r.c[i + 1] = c.y;
     asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(far) : "f"(fabsf(e.x)), "f"(fabsf(e.y)));
   }
@@ -342,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) write_kerne
           if (q == 0) reinterpret_cast<uint16_t*>(page + L::kKZeros)[(2 * pair + j) * NG + grp] = c.p.zero_h;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 y = fma_f32x2(make_float2(c.p.scale, c.p.scale), make_float2(c.c[2 * e], c.c[2 * e + 1]), make_float2(c.p.zero, c.p.zero));
+            const float2 y = fma2(make_float2(c.p.scale, c.p.scale), make_float2(c.c[2 * e], c.c[2 * e + 1]), make_float2(c.p.zero, c.p.zero));
             const uint32_t zw = cut_half2(y.x, y.y);
           const __half2 z = *reinterpret_cast<const __half2*>(&zw);
             lo[e] = __hmin2(lo[e], z), hi[e] = __hmax2(hi[e], z);
@@ -402,9 +390,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) write_kerne
 // scale: of the low and the high halves, times 2^24.
 __device__ __forceinline__ void word_values(uint32_t w, float2 scale, float2 zero, float2 (&x)[4]) {
   const float2 less = make_float2(scale.x * 0.0625f, scale.y * 0.0625f);
-  const uint32_t u = w >> 8, p[4] = {w & 0x000f000fu, w & 0x00f000f0u, u & 0x000f000fu, u & 0x00f000f0u};
+  const Pairs c = code_pairs(w);
+  const uint32_t p[4] = {c.a, c.b, c.c, c.d};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = fma_f32x2(__half22float2(*reinterpret_cast<const __half2*>(&p[i])), i & 1 ? less : scale, zero);
+  for (int i = 0; i < 4; ++i) x[i] = fma2(__half22float2(*reinterpret_cast<const __half2*>(&p[i])), i & 1 ? less : scale, zero);
 }
 __device__ __forceinline__ float half_of(uint32_t w, int i) { return __half2float(__ushort_as_half((uint16_t)(w >> (16 * i)))); }
 

@@ -144,16 +144,39 @@ struct Eight<float> {
   }
 };
 
-// One value in a type that is named at run time (outputs of the merges, where the rows are few).
-__device__ __forceinline__ void store_as(void* p, int64_t i, int dtype, float x) {
-  if (dtype == RDKV_F32) static_cast<float*>(p)[i] = x;
-  else if (dtype == RDKV_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
-  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
-}
+// One value of a type that is named at run time.
 __device__ __forceinline__ float load_q(const void* p, int64_t i, int dtype) {
   if (dtype == RDKV_F32) return static_cast<const float*>(p)[i];
   if (dtype == RDKV_F16) return __half2float(static_cast<const __half*>(p)[i]);
   return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// ---------------------------------------------------------------- arithmetic
+// two fp32 products and sums in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)), "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 add2f(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four pairs of codes of a word: at bits 0 and 16 (2^-24), 4 and 20 (2^-20), and the same of the upper bytes.
+struct Pairs {
+  uint32_t a, b, c, d;
+};
+__device__ __forceinline__ Pairs code_pairs(uint32_t w) {
+  const uint32_t u = w >> 8;
+  return Pairs{w & 0x000f000fu, w & 0x00f000f0u, u & 0x000f000fu, u & 0x00f000f0u};
 }
 
 // ---------------------------------------------------------------- launches

@@ -39,11 +39,6 @@ __device__ __forceinline__ int pages_seen(const SelectArgs& a, int b, int t) {
   return seen > 0 ? ceil_div(seen, kPage) : 0;
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t half2_of(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -140,9 +135,9 @@ __device__ __forceinline__ float score_tiles(const SelectArgs& a, int row, int b
       }
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
-        mma_f16(s, h0[j], h1[j], h0[j + 1], h1[j + 1], pos[i][j], pos[i][j + 1]);
-        mma_f16(s, l0[j], l1[j], l0[j + 1], l1[j + 1], neg[i][j], neg[i][j + 1]);
-        mma_f16(m, b0[j], b1[j], b0[j + 1], b1[j + 1], mag[i][j], mag[i][j + 1]);
+        mma16(s, h0[j], h1[j], h0[j + 1], h1[j + 1], pos[i][j], pos[i][j + 1]);
+        mma16(s, l0[j], l1[j], l0[j + 1], l1[j + 1], neg[i][j], neg[i][j + 1]);
+        mma16(m, b0[j], b1[j], b0[j + 1], b1[j + 1], mag[i][j], mag[i][j + 1]);
       }
     }
     // rows g, g + 8 are pages, columns 2 qd, 2 qd + 1 heads
