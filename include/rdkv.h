@@ -627,8 +627,10 @@ rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, voi
  * [batch][n_q][h_q][head_dim] in
  * `dtype`, consecutive tokens q_stride elements apart (16-byte aligned,
  * q_stride a multiple of 16 bytes); out [batch][n_q][h_q][head_dim] dense in
- * out_dtype, which is dtype or RDKV_F32 (fp32 outputs are computed to fp32
- * accuracy, the others to their type's); lse [batch][n_q][h_q] fp32 or NULL.
+ * out_dtype, which is dtype or RDKV_F32.  Sums are fp32.  For fp32 outputs every
+ * operand is held in 22 bits or more; for 16-bit outputs the weights, weight
+ * times scale and the groups' middles are rounded to fp16, which together adds
+ * less to an output's error than its own rounding does.  lse [batch][n_q][h_q] fp32 or NULL.
  * fp32 out and lse join other caches' attention through rdkv_merge_attn.
  *
  * sel NULL: every position.  Else sel [batch][n_q][h_kv][n_sel] (int32, device;
@@ -643,7 +645,8 @@ rdkv_status rdkv_q4_read(const rdkv_q4_cache* cache, int32_t dtype, void* k, voi
  * again, one that reports RDKV_ERR_TIMEOUT too, so calls of any
  * shape that need no more bytes, of rdkv_q4_select too, may follow one another
  * on it.  Calls that may run at the same time (two streams, two captured
- * graphs) need one each. */
+ * graphs) need one each.  batch * n_q * h_kv * page_stride (with sel: * n_sel)
+ * is at most 2^31 - 1 (else RDKV_ERR_UNSUPPORTED). */
 size_t rdkv_q4_attn_workspace_bytes(const rdkv_q4_cache* cache, int32_t h_q, int32_t n_q);
 rdkv_status rdkv_q4_attn(const rdkv_q4_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
                          int32_t n_q, const int32_t* sel, int32_t n_sel, void* out, int32_t out_dtype, float* lse,

@@ -283,8 +283,9 @@ __device__ __forceinline__ uint32_t low_halves(uint32_t lo, uint32_t hi) { retur
 // sectors.  Every load of a thread's kSteps pairs is under way before the first is used.  kThreads, kSteps:
 // as few as the call's rows need (a decode step has one token a sequence: 3.8 us for 32 sequences of 8 heads
 // with 32 threads a block, 9.8 with 256).
-//   Bound: 47 us for 32,768 rows of 8 heads at D = 128 in fp16 (134 MB read, 42 MB written: 3.7 TB/s), by the
-// quantiser's instructions (about 1,200 a warp and page half).  As one division a value it took 94 us; with the
+//   Bound: 47 us for 32,768 rows of 8 heads at D = 128 in fp16 (134 MB read, 42 MB written: 3.7 TB/s).  A warp runs
+// 1,180 instructions for both halves of its eight rows; the issue slots are 71 % used, the ALU 52 %, DRAM 46 %, and
+// warps wait for their rows as often as for one another (22 of 64 warps fit at 80 registers).  As one division a value it took 94 us; with the
 // tests as short-circuit conditions 76; with an exact way for the whole group on a near half 54.
 template <typename T, int D, int kThreads, int kSteps>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) write_kernel(View v, Rows r, const T* k, const T* vv) {

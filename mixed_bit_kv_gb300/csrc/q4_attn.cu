@@ -22,11 +22,23 @@
 // difference of two large ones.  For fp32 outputs (PREC) the keys are split the same way, the middles' part
 // is summed in fp32, and weight times scale keeps a remainder.
 //
-// Bound.  160 bytes a token and KV head at D = 128: 79 % of the measured copy bandwidth at 262,144 tokens (62.6
+// Roundings.  Logits, maxima, weights' sums and outputs' sums are fp32 in every variant.  The operands of the tensor
+// cores are fp16:
+//   16-bit outputs  fp16 and bf16 queries as they are (a row times a power of two); a weight, once more weight times
+//           scale, and the middle zero + 8 scale, 2^-11 of each: together less than the outputs' own rounding (fp16 outputs
+//           are 2.1e-4 off when fp32 sums are rounded once, 2.1e-4 .. 2.3e-4 here).  Carrying them in two parts is the fp32
+//           variant: 111 us for 64 at 262,144 tokens.
+//   fp32 outputs  queries in two parts (22 bits of 24), weight times scale in two parts (22 bits), the middles and the
+//           weights themselves in fp32: 4.4e-7 off at 513 tokens, where plain fp32 sums are 5.2e-7 off.
+// A weight has those bits while its part of an operand is a normal fp16 number: 16-bit outputs down to 2^-25 of the
+// largest weight where the values' scales are below 1/4, to 2^-9 at the largest scale there is (values of 65504).
+//
+// Bound.  160 bytes a token and KV head at D = 128: 79 % of the measured copy bandwidth at 262,144 tokens (62.8
 // us for 335 MB).  A scheduler has two warps, whose products wait for one another: a page of up to eight rows takes
 // 72 products (104 with the queries on M and half of its rows empty: 68.5 us).  About 1,150 instructions a page,
 // a third of them to unpack codes.  Start (lengths, page table, queries, first page: each a trip to memory) and
-// joins take about 10 us of every call.
+// joins take about 10 us of every call.  Two row sets: 136 products a page, 1,600 instructions, 255 registers; the
+// tensor pipe is 26 % busy and the issue slots 37 %: the latency of two warps a scheduler again, not the products' rate.
 //   Measured and not kept (us at 262,144 tokens, against 68.5 .. 69): 11 or 12 warps of 168 registers 74 .. 79, 16
 // of 128 74; 16 or 32 tokens under way at once 79 and 72; pages copied with the 128-byte swizzle of a tensor map,
 // which takes away the values' four-fold bank conflicts (96 of 270 shared-memory cycles a page), 75 against 73; the

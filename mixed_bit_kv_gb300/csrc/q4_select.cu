@@ -6,8 +6,9 @@
 // The blocks of a row (sequence, query token, KV head) take the sums as tensor-core products (pages on M, the
 // group's heads on N, the 2 D bounds on K), each within eps of the exact sum.  The row's last block to finish
 // then finds an interval around the n-th best score, takes what lies above it by more than the error, and
-// sums only the few pages within the error again, to twice fp32's precision, so that the order next to the
-// border is the exact one.
+// sums only the pages within the error again, to twice fp32's precision, so that the order next to the
+// border is the exact one.  A few of them are ranked in pairs; many (equal scores put a whole row there) by the digits
+// of (sum, page), so that the time goes with their number: 0.13 ms for 2,048 equal pages, 0.93 for 16,384.
 //   Bound: latency.  13.0 us for 64 of 2,048 pages of 8 heads (8.4 MB of bounds): 3 us to the scores, 1 for the
 // ticket, 1 to read the scores again, the rest the block's own turns.  As two launches 13.9; four ends of an
 // interval a turn instead of 2,048 parts 14.4.
