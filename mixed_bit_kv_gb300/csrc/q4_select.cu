@@ -91,7 +91,8 @@ __device__ __forceinline__ float score_tiles(const SelectArgs& a, int row, int b
     unit = most >= 1.8446744e19f ? 5.4210109e-20f : most > 0.0f && most < 1e-12f ? 1.8446744e19f : 1.0f;  // 2^64
     top *= unit;
     // the head times 2^s, its largest value in [1, 2)
-    const int s = top > 0.0f ? max(-100, min(100, 127 - (int)(__float_as_uint(top) >> 23))) : 0;
+    // (times `unit` inside fp32's range)
+    const int s = top > 0.0f ? max(-100, min(unit > 1.0f ? 60 : 100, 127 - (int)(__float_as_uint(top) >> 23))) : 0;
     const float up = __uint_as_float((uint32_t)(s + 127) << 23) * unit;
     back = odd == 0.0f ? __uint_as_float((uint32_t)(127 - s) << 23) : NAN;  // (maxima drop it)
 #pragma unroll

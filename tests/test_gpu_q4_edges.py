@@ -346,6 +346,19 @@ def test_selection_for_queries_of_any_size(P, exponent, dtype):
     _check_selection(c, q, e, 12, 1, 1)
 
 
+@pytest.mark.parametrize("P", [40, 700])
+def test_selection_for_queries_with_heads_below_the_normal_numbers(P):
+    """A head of 2^-140 beside one of 2^-60 whose sums are negative everywhere: the small head's sums are the scores."""
+    g = torch.Generator().manual_seed(P)
+    e = (torch.rand(P, 1, 2, 64, generator=g) + 0.5).sort(2).values.half()
+    q = torch.zeros(1, 2, 64)
+    q[0, 0] = -(2.0 ** -60)
+    q[0, 1] = torch.randint(0, 3, (64,), generator=g).float() * 2.0 ** -140
+    q[0, 1, 5] = 0.0
+    c = _bounded(P, 1, 64, e)
+    _check_selection(c, q, e, 12, 1, 1)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("P", [40, 700])
 def test_heads_that_are_not_finite_leave_the_selection_to_the_others(P, dtype):
