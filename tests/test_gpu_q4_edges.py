@@ -353,10 +353,11 @@ def test_selection_for_queries_with_heads_below_the_normal_numbers(P):
     e = (torch.rand(P, 1, 2, 64, generator=g) + 0.5).sort(2).values.half()
     q = torch.zeros(1, 2, 64)
     q[0, 0] = -(2.0 ** -60)
-    q[0, 1] = torch.randint(0, 3, (64,), generator=g).float() * 2.0 ** -140
-    q[0, 1, 5] = 0.0
     c = _bounded(P, 1, 64, e)
-    _check_selection(c, q, e, 12, 1, 1)
+    for least in (0, -2):
+        q[0, 1] = torch.randint(least, 3, (64,), generator=g).float() * 2.0 ** -140
+        q[0, 1, 5] = 0.0
+        _check_selection(c, q, e, 12, 1, 1)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
