@@ -674,14 +674,16 @@ struct Warp {
   }
 
   // The unit's sums: put(row, first channel, four sums) for every row and channel of this lane, then
-  // stat(row, reference, sum) once a row.
+  // stat(row, reference, sum) once a row.  All without 2^off: a reference less off and the log of a sum times
+  // 2^off would both be rounded near 23, and their sum, the log-sum-exp of a few keys, by 1e-6.
   template <class Put, class Stat>
   __device__ __forceinline__ void finish(int g, int qd, Put put, Stat stat) {
+    const float a = __uint_as_float((uint32_t)(127 - off) << 23), b = 0.0625f * a;  // (b: of the codes' units)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float sum = l[n], m = ref[n] == -INFINITY ? -INFINITY : ref[n] - (float)off, l0, l1;
+      float sum = l[n] * a, l0, l1;
       if constexpr (kCols) {
-        l0 = l[0], l1 = l[1];
+        l0 = l[0] * a, l1 = l[1] * a;
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) l0 += __shfl_xor_sync(0xffffffffu, l0, d), l1 += __shfl_xor_sync(0xffffffffu, l1, d);
       } else {
@@ -702,16 +704,16 @@ struct Warp {
           z0 = __shfl_sync(0xffffffffu, oz[n][0], 4 * i + qd), z1 = __shfl_sync(0xffffffffu, oz[n][1], 4 * i + qd);
         }
         const float(&c)[2][4] = o[n][i];
-        constexpr float a = 1.0f, b = 0.0625f;  // the codes' units
+        z0 *= a, z1 *= a;
         put(8 * n + 2 * qd, 32 * i + 4 * g, l0,
             make_float4(fmaf(c[0][0], a, z0), fmaf(c[0][2], b, z0), fmaf(c[1][0], a, z0), fmaf(c[1][2], b, z0)));
         put(8 * n + 2 * qd + 1, 32 * i + 4 * g, l1,
             make_float4(fmaf(c[0][1], a, z1), fmaf(c[0][3], b, z1), fmaf(c[1][1], a, z1), fmaf(c[1][3], b, z1)));
       }
       if constexpr (kCols) {
-        if (g == 0) stat(2 * qd, m, l0), stat(2 * qd + 1, ref[1] == -INFINITY ? -INFINITY : ref[1] - (float)off, l1);
+        if (g == 0) stat(2 * qd, ref[0], l0), stat(2 * qd + 1, ref[1], l1);
       } else {
-        if (qd == 0) stat(8 * n + g, m, sum);
+        if (qd == 0) stat(8 * n + g, ref[n], sum);
       }
     }
   }

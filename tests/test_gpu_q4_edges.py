@@ -220,6 +220,23 @@ def test_fp32_outputs_of_groups_of_very_different_size(n, ratio, D, dtype):
     _check_fp32_outputs(*(x.to(TYPES[dtype]) for x in (k, v, q)), logit=4 * 2.0 ** -24 * 3.3)
 
 
+@pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("bf16", "bf16"), ("f32", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("D,T,mag", [(64, 1, 1e-3), (128, 1, 1.0), (128, 2, 1e-3), (64, 2, 100.0)])
+def test_lse_of_a_few_keys(D, T, mag, dtype, out):
+    """Keys of zero: every weight is one, exactly, and so are their sums up to 2^24: lse is the log of their number, to the
+    roundings of a base-2 log, of its sum with the reference (zero) and of the factor ln 2 (2^-24 each, and 2^-23 for
+    the log): whatever the values' scale is."""
+    lens = [T, T + 1, T + 2, T + 4, T + 6, 40, 63, 64, 65, 128, 129, 200, 700, 3001]
+    c = _cache(lens, 1, D)
+    v = _rows(sum(lens), 1, D, TYPES[dtype], 3, mag)
+    start = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+    rdkv.rdkv_q4_write(c, torch.zeros_like(v).to(DEV), v.to(DEV), row_start=start, max_rows=max(lens))
+    q = _rows(len(lens) * T, 4, D, TYPES[dtype], 9).view(len(lens), T, 4, D)
+    o, lse = rdkv.rdkv_q4_attn(c, q.to(DEV), out_dtype=TYPES[out])
+    exp = torch.tensor([[math.log(n - T + t + 1) for t in range(T)] for n in lens], dtype=torch.float64)[..., None]
+    assert ((lse.double().cpu() - exp).abs() <= 5 * 2.0 ** -24 * exp).all()
+
+
 # ---------------------------------------------------------------- waits that run out
 @pytest.mark.parametrize("dtype,out,D,G,T,lens", [
     ("f16", "f16", 128, 4, 1, [64 * 700, 65, 0, 1]), ("bf16", "bf16", 64, 3, 1, [64 * 700 - 5]), ("f16", "f16", 128, 8, 2, [64 * 300, 64 * 30 + 1]),
