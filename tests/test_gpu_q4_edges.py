@@ -237,6 +237,30 @@ def test_lse_of_a_few_keys(D, T, mag, dtype, out):
     assert ((lse.double().cpu() - exp).abs() <= 5 * 2.0 ** -24 * exp).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shift", [0.0, 20.0])
+def test_fp32_logits_of_single_keys(shift, dtype, D):
+    """One key a sequence: lse is its logit.  Queries are held in two fp16 parts (22 bits: 2^-22), whose products with
+    code - 8 are summed 16 at a time with at most 17 cuts of 2^-23 of the largest, twice a group; the group's middle
+    (`shift` makes it the larger part) is a fp32 product with the sum of the queries: some eight roundings of 2^-24 with the
+    sums over groups.  One part of the queries alone would be 2^-12 of each channel off, beyond this in most rows."""
+    B, h, G = 60, 2, 8
+    c = _cache([1] * B, h, D)
+    x = (_rows(B, h, D, torch.float32, 3) + shift).to(TYPES[dtype])
+    rdkv.rdkv_q4_write(c, x[:, None].to(DEV), x[:, None].to(DEV))
+    q = _rows(B, h * G, D, torch.float32, 4).view(B, 1, h * G, D).to(TYPES[dtype])
+    o, lse = rdkv.rdkv_q4_attn(c, q.to(DEV), out_dtype=torch.float32)
+    codes, scale, zero = O.q4_quantize(x.float().numpy())
+    codes = codes.reshape(B, h, 1, -1, 32).astype(np.float64) - 8
+    scale, zero = scale.astype(np.float64)[:, :, None, :, None], zero.astype(np.float64)[:, :, None, :, None]
+    qg = q.double().numpy().reshape(B, h, G, -1, 32)
+    exp = (qg * (zero + 8 * scale + scale * codes)).sum((-2, -1)) / math.sqrt(D)
+    tol = (2.0 ** -22 + 34 * 2.0 ** -23) * (np.abs(qg * codes) * scale).sum((-2, -1)) + 2.0 ** -21 * (np.abs(zero + 8 * scale) * np.abs(qg)).sum((-2, -1))
+    err = np.abs(lse.double().cpu().numpy().reshape(B, h, G) - exp)
+    assert (err <= tol / math.sqrt(D) + 2.0 ** -23 * np.abs(exp)).all(), (err / tol).max()
+
+
 # ---------------------------------------------------------------- waits that run out
 @pytest.mark.parametrize("dtype,out,D,G,T,lens", [
     ("f16", "f16", 128, 4, 1, [64 * 700, 65, 0, 1]), ("bf16", "bf16", 64, 3, 1, [64 * 700 - 5]), ("f16", "f16", 128, 8, 2, [64 * 300, 64 * 30 + 1]),
