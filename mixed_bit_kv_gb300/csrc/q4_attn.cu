@@ -26,7 +26,7 @@
 // cores are fp16:
 //   16-bit outputs  fp16 and bf16 queries as they are (a row times a power of two); a weight, once more weight times
 //           scale, and the middle zero + 8 scale, 2^-11 of each: together less than the outputs' own rounding (fp16 outputs
-//           are 2.1e-4 off when fp32 sums are rounded once, 2.1e-4 .. 2.3e-4 here).  Carrying them in two parts is the fp32
+//           are 2.1e-4 off when fp32 sums are rounded once, 2.1e-4 .. 2.4e-4 here).  Carrying them in two parts is the fp32
 //           variant: 111 us for 64 at 262,144 tokens.
 //   fp32 outputs  queries in two parts (22 bits of 24), weight times scale in two parts (22 bits), the middles and the
 //           weights themselves in fp32: 4.4e-7 off at 513 tokens, where plain fp32 sums are 5.2e-7 off.
