@@ -287,7 +287,8 @@ def test_waits_that_run_out_are_reported_and_the_workspace_serves_on(withhold, d
         hit = any((p + j) % withhold == 0 for n in lens for p in range(-(-n // 64)) for j in range(h)
                   if pages is None or p < 3)
         assert rdkv.rdkv_q4_status(c) == (rdkv.RDKV_ERR_TIMEOUT if hit else rdkv.RDKV_OK)
-        assert a.elapsed_time(b) < 200             # one limit of about a millisecond a warp
+        b.synchronize()
+        assert a.elapsed_time(b) < 1000            # a limit of about a millisecond a warp (an ordinary limit is two seconds)
         assert (ws[:rdkv.Q4_COUNTER_BYTES] == 0).all()
         assert o.isfinite().all() and not lse.isnan().any() and (lse < math.inf).all()
         for _ in range(2):
@@ -318,13 +319,16 @@ def _check_selection(c, q, bounds, keep, first, last, missing=(), limit=None):
         s[list(missing)] = -np.inf
         assert sel[0, j].tolist() == O.q4_select(s, keep, first, last), j
     assert torch.equal(run(), sel)
-    if limit is not None:                          # (every inner step a pair of pages: 20 to 100 ms)
-        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        a.record()
-        run()
-        b.record()
-        b.synchronize()
-        assert a.elapsed_time(b) < limit
+    if limit is not None:                          # (a step for every pair of pages: 20 to 100 ms)
+        best = math.inf
+        for _ in range(5):                         # the fastest of five: the host may be held up between the events
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            run()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        assert best < limit
 
 
 @pytest.mark.parametrize("P,keep,first,last", [(33, 8, 1, 1), (600, 64, 0, 0), (8193, 9, 2, 3), (16500, 100, 1, 2), (16500, 16000, 1, 1), (20011, 1, 0, 0)])
