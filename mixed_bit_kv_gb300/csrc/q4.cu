@@ -10,122 +10,27 @@ namespace q4 {
 
 // ---------------------------------------------------------------- host checks
 rdkv_status check_cache(const rdkv_q4_cache* c) {
-  RDKV_REQUIRE(c != nullptr, RDKV_ERR_INVALID_ARG, "cache is NULL");
-  RDKV_REQUIRE(c->batch >= 1 && c->h_kv >= 1 && c->n_pages >= 1 && c->page_stride >= 1, RDKV_ERR_INVALID_ARG,
-               "cache sizes must be positive (batch=%d h_kv=%d n_pages=%d page_stride=%d)", c->batch, c->h_kv,
-               c->n_pages, c->page_stride);
-  RDKV_REQUIRE(c->head_dim == 64 || c->head_dim == 128, RDKV_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}",
-               c->head_dim);
-  RDKV_REQUIRE((int64_t)c->page_stride * kPage <= INT32_MAX, RDKV_ERR_UNSUPPORTED,
-               "page_stride %d: more than 2^31 - 1 tokens a sequence", c->page_stride);
-  RDKV_REQUIRE((int64_t)c->n_pages * c->h_kv <= INT32_MAX, RDKV_ERR_UNSUPPORTED, "more than 2^31 - 1 (page, KV head) pairs");
-  RDKV_REQUIRE((int64_t)c->batch * c->h_kv <= 1 << 20, RDKV_ERR_UNSUPPORTED, "more than 2^20 (sequence, KV head) pairs");
-  RDKV_REQUIRE(c->pages && c->page_table && c->lens && c->status, RDKV_ERR_INVALID_ARG, "NULL pointer in the cache");
+  const rdkv_status st = check_pool(c);
+  if (st != RDKV_OK) return st;
   RDKV_REQUIRE(((uintptr_t)c->pages | (uintptr_t)c->bounds) % 16 == 0, RDKV_ERR_INVALID_ARG,
                "pages and bounds must be 16-byte aligned");
   return RDKV_OK;
 }
 
-static rdkv_status check_dtype(int32_t dtype) {
-  RDKV_REQUIRE(dtype == RDKV_F16 || dtype == RDKV_F32 || dtype == RDKV_BF16, RDKV_ERR_UNSUPPORTED, "dtype %d", dtype);
-  return RDKV_OK;
-}
-
 rdkv_status check_rows(const rdkv_q4_cache* c, int32_t dtype, const void* k, const void* v, int64_t rows, int64_t row_stride,
                        const int32_t* row_start, int32_t max_rows) {
-  rdkv_status st = check_cache(c);
-  if (st != RDKV_OK) return st;
-  st = check_dtype(dtype);
-  if (st != RDKV_OK) return st;
-  RDKV_REQUIRE(max_rows >= 0, RDKV_ERR_INVALID_ARG, "max_rows %d", max_rows);
-  RDKV_REQUIRE(rows >= (row_start ? 0 : (int64_t)c->batch * max_rows), RDKV_ERR_INVALID_ARG, "%lld rows for %d sequences of %d",
-               (long long)rows, c->batch, max_rows);
-  RDKV_REQUIRE((k && v) || max_rows == 0, RDKV_ERR_INVALID_ARG, "NULL rows");
-  RDKV_REQUIRE(((uintptr_t)k | (uintptr_t)v) % 16 == 0 && row_stride % (16 / size_of(dtype)) == 0, RDKV_ERR_INVALID_ARG,
-               "rows must be 16-byte aligned (row_stride %lld)", (long long)row_stride);
-  RDKV_REQUIRE(row_stride >= (int64_t)c->h_kv * c->head_dim, RDKV_ERR_INVALID_ARG, "row_stride %lld < h_kv * head_dim",
-               (long long)row_stride);
-  return RDKV_OK;
+  const rdkv_status st = check_cache(c);
+  return st != RDKV_OK ? st : check_rows_of(c, dtype, k, v, rows, row_stride, row_start, max_rows);
 }
 
 rdkv_status check_queries(const rdkv_q4_cache* c, int32_t h_q, int32_t n_q) {
-  rdkv_status st = check_cache(c);
-  if (st != RDKV_OK) return st;
-  RDKV_REQUIRE(h_q >= 1 && h_q % c->h_kv == 0, RDKV_ERR_INVALID_ARG, "h_q=%d is not a multiple of h_kv=%d", h_q, c->h_kv);
-  RDKV_REQUIRE(h_q / c->h_kv <= 8, RDKV_ERR_UNSUPPORTED, "group size %d > 8", h_q / c->h_kv);
-  RDKV_REQUIRE(n_q >= 1, RDKV_ERR_INVALID_ARG, "n_q %d", n_q);
-  RDKV_REQUIRE(n_q <= RDKV_Q4_MAX_QUERIES, RDKV_ERR_UNSUPPORTED, "n_q %d > %d", n_q, RDKV_Q4_MAX_QUERIES);
-  // a counter each in the workspaces; also a grid's second size
-  RDKV_REQUIRE((int64_t)c->batch * n_q * c->h_kv <= RDKV_Q4_COUNTER_BYTES / 4 - 1, RDKV_ERR_UNSUPPORTED,
-               "more than 65,535 (sequence, query token, KV head) triples");
-  return RDKV_OK;
+  const rdkv_status st = check_cache(c);
+  return st != RDKV_OK ? st : check_heads_of(c, h_q, n_q);
 }
 
 rdkv_status check_q(const rdkv_q4_cache* c, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q, int32_t n_q) {
-  rdkv_status st = check_queries(c, h_q, n_q);
-  if (st != RDKV_OK) return st;
-  st = check_dtype(dtype);
-  if (st != RDKV_OK) return st;
-  RDKV_REQUIRE(q != nullptr, RDKV_ERR_INVALID_ARG, "NULL queries");
-  RDKV_REQUIRE((uintptr_t)q % 16 == 0 && q_stride % (16 / size_of(dtype)) == 0, RDKV_ERR_INVALID_ARG,
-               "queries must be 16-byte aligned (q_stride %lld)", (long long)q_stride);
-  RDKV_REQUIRE(q_stride >= (int64_t)h_q * c->head_dim, RDKV_ERR_INVALID_ARG, "q_stride %lld < h_q * head_dim",
-               (long long)q_stride);
-  return RDKV_OK;
-}
-
-// ---------------------------------------------------------------- rows and the pages they fall in
-struct Rows {
-  int64_t n, stride;     // rows of k and v, elements between them
-  const int32_t* start;  // or NULL: max_rows rows a sequence
-  const int32_t* first;  // reading: position of a sequence's first row (NULL: 0)
-  int32_t max_rows;
-  int runs;              // pages that max_rows consecutive positions can touch
-};
-
-// The part of sequence b's rows that lies in its run-th page.
-struct Run {
-  int64_t row;   // row of the first token
-  int64_t page;  // physical page, -1: nothing to do
-  int s0, s1;    // slots [s0, s1)
-};
-
-template <bool kWrite>
-__device__ __forceinline__ Run find_run(const View& v, const Rows& r, int b, int run) {
-  Run o{0, -1, 0, 0};
-  const int len = fetch(v.lens + b);
-  const int64_t cap = (int64_t)v.page_stride * kPage;
-  int64_t r0, n;
-  if (r.start) {
-    r0 = fetch(r.start + b);
-    n = (int64_t)fetch(r.start + b + 1) - r0;
-  } else {
-    r0 = (int64_t)b * r.max_rows;
-    n = len != 0 || !kWrite ? r.max_rows : 0;
-  }
-  if (n == 0) return o;
-  const int64_t first = kWrite ? (int64_t)len - n : r.first ? (int64_t)fetch(r.first + b) : 0;
-  if (n < 0 || n > r.max_rows || r0 < 0 || r0 + n > r.n || first < 0 || len < 0) {
-    if (threadIdx.x == 0) raise(v, RDKV_ERR_INVALID_ARG);
-    return o;
-  }
-  int64_t end = first + n;
-  if (!kWrite) end = min(end, (int64_t)len);
-  if (end > cap) {
-    if (threadIdx.x == 0) raise(v, RDKV_ERR_CAPACITY);
-    end = cap;
-  }
-  const int64_t lp = first / kPage + run, t0 = lp * kPage;
-  if (t0 >= end) return o;
-  o.s0 = (int)(max(first, t0) - t0);
-  o.s1 = (int)(min(end, t0 + kPage) - t0);
-  o.row = r0 + (t0 + o.s0 - first);
-  o.page = fetch(v.page_table + (int64_t)b * v.page_stride + lp);
-  if (o.page < 0 || o.page >= v.n_pages) {
-    if (threadIdx.x == 0) raise(v, RDKV_ERR_INVALID_ARG);
-    o.page = -1;
-  }
-  return o;
+  const rdkv_status st = check_queries(c, h_q, n_q);
+  return st != RDKV_OK ? st : check_queries_of(c, dtype, q, q_stride, h_q);
 }
 
 __device__ __forceinline__ float2 wide2(__half2 v) { return __half22float2(v); }
@@ -445,14 +350,6 @@ __global__ void __launch_bounds__(kThreads) read_kernel(View v, Rows r, T* k, T*
       else Eight<T>::store(vv + at, {v0[0].y, v0[1].y, v0[2].y, v0[3].y, v1[0].y, v1[1].y, v1[2].y, v1[3].y});
     }
   }
-}
-
-static rdkv_status grid_of(const rdkv_q4_cache* c, Rows* r, int64_t* blocks) {
-  // max_rows positions from anywhere in a page, within what the table can hold
-  r->runs = (int)std::min<int64_t>(ceil_div64((int64_t)r->max_rows + kPage - 1, kPage), c->page_stride);
-  *blocks = (int64_t)c->batch * c->h_kv * r->runs;
-  RDKV_REQUIRE(*blocks <= INT32_MAX, RDKV_ERR_UNSUPPORTED, "max_rows %d: too many (sequence, head, page) items", r->max_rows);
-  return RDKV_OK;
 }
 
 }  // namespace q4

@@ -66,48 +66,13 @@ struct AttnArgs {
   long long wait_cycles;  // limit of a wait for a page
 };
 
-constexpr long long kWaitCycles = 4000000000LL;  // a bounded wait, about two seconds
-constexpr long long kMinWaitCycles = 100000;     // shortest limit the self-test may ask for
 constexpr int kMinItems = 4;                     // of a block (1 to 8: within 3 % of one another on the smallest calls)
 constexpr int kInfo = 32;                        // items whose places a warp knows ahead
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(ok)
-               : "r"(smem_u32(bar)), "r"(parity)
-               : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, long long limit) {
-  if (try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!try_wait(bar, parity))
-    if (clock64() - t0 > limit) return false;
-  return true;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// the same on a zero accumulator
-__device__ __forceinline__ void mma16z(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
 __device__ __forceinline__ void mma8z(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
-}
-// an 8 x 8 matrix of halves, a row in four lanes, transposed
-__device__ __forceinline__ uint32_t transposed(uint32_t w) {
-  uint32_t d;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(w));
-  return d;
 }
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&c));
@@ -116,17 +81,6 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&d);
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-// the remainders of two values past their fp16 parts, times kUp
-template <int kUp = 1>
-__device__ __forceinline__ uint32_t rest2(float lo, float hi, uint32_t w) {
-  const float2 f = unpack2(w);
-  return pack2((lo - f.x) * kUp, (hi - f.y) * kUp);
 }
 constexpr int kRest = 4096;  // of the weights' remainders: a fp16 part of up to 2^9 leaves up to 2^-3
 template <int NG>
@@ -181,14 +135,6 @@ __device__ __forceinline__ int items_of(const AttnArgs& a, int bc) {
   const int seen = seen_by(a, bc / a.n_chunks, bc % a.n_chunks);
   return seen <= 0 ? 0 : a.sel ? a.n_sel : ceil_div(seen, kPage);
 }
-
-// x / y for 0 <= x, 0 < y: 32 bits where they do (a 64-bit division takes some hundred instructions)
-__device__ __forceinline__ int quotient(int64_t x, int y) {
-  if ((x >> 32) == 0) return (int)((uint32_t)x / (uint32_t)y);
-  return (int)(x / y);
-}
-// The first of n items that part i of `parts` equal ones takes.
-__device__ __forceinline__ int share(int i, int n, int parts) { return quotient((int64_t)i * n, parts); }
 
 // What a unit's index stands for.
 struct Unit {
@@ -723,42 +669,6 @@ struct Warp {
 struct Piece {
   int base, unit, items;  // the unit's first item, the unit, its items
 };
-
-// Joins pieces of one query row: a lane's four channels of the sums and, in every lane, the row's reference
-// and sum.  n pieces, m_of(i), l_of(i) their statistics, y_of(i) this lane's channels: the loads of J
-// pieces are under way together.  Eight of a block's own (drafted tokens: 49.0 us; 51.1 with 16, 56.8 with 32, whose
-// code takes longer to fetch), 16 of other blocks' (32,777 tokens: 18.9 us; 19.3 with eight).
-template <int J, class M, class L, class Y>
-__device__ __forceinline__ void join_row(int n, int lane, M m_of, L l_of, Y y_of, float4& o, float& top, float& sum) {
-  o = make_float4(0, 0, 0, 0);
-  top = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += J) {
-    const bool mine = lane < J && i0 + lane < n;
-    const float m = mine ? m_of(i0 + lane) : -INFINITY, l = mine ? l_of(i0 + lane) : 0.0f;
-    float4 y[J];
-#pragma unroll
-    for (int i = 0; i < J; ++i) y[i] = i0 + i < n ? y_of(i0 + i) : make_float4(0, 0, 0, 0);
-    float now = m;
-    for (int d = J / 2; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
-    now = fmaxf(top, __shfl_sync(0xffffffffu, now, 0));
-    const float back = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
-    top = now;
-    o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
-    float part = f * l;
-    for (int d = J / 2; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-    sum = fmaf(sum, back, __shfl_sync(0xffffffffu, part, 0));
-#pragma unroll
-    for (int i = 0; i < J; ++i) {
-      const float w = __shfl_sync(0xffffffffu, f, i);
-      o.x = fmaf(w, y[i].x, o.x), o.y = fmaf(w, y[i].y, o.y), o.z = fmaf(w, y[i].z, o.z), o.w = fmaf(w, y[i].w, o.w);
-    }
-  }
-}
-__device__ __forceinline__ float4 scaled(float4 o, float l) {
-  const float f = l != 0.0f ? 1.0f / l : 0.0f;
-  return make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-}
 
 template <int D, int NT, bool PREC, int NW, int NS>
 struct Smem {
