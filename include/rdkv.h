@@ -573,8 +573,8 @@ rdkv_status rdkv_allocate_at_levels(const rdkv_shape* seg, int32_t per_head, con
  * and raises *status to that code; rdkv_q4_status reads and clears it.
  *
  * Supported: head_dim 64 or 128, 1 <= h_q / h_kv <= 8, rows and queries in
- * RDKV_F16, RDKV_F32 or RDKV_BF16 (the other calls of this library take no
- * RDKV_BF16).  pages and bounds 16-byte aligned. */
+ * RDKV_F16, RDKV_F32 or RDKV_BF16 (beside these calls and the 8-bit cache's, the
+ * calls of this library take no RDKV_BF16).  pages and bounds 16-byte aligned. */
 enum { RDKV_BF16 = 2 };
 #define RDKV_Q4_PAGE_TOKENS 64
 /* Most query tokens of a sequence in one rdkv_q4_attn or rdkv_q4_select; batch *
@@ -687,6 +687,112 @@ rdkv_status rdkv_q4_select(const rdkv_q4_cache* cache, int32_t dtype, const void
 
 /* Reads *status and clears it.  SYNCHRONISES `stream`. */
 rdkv_status rdkv_q4_status(const rdkv_q4_cache* cache, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit cache, kept at a budget by attention weight
+ * A cache of fp8 codes beside the 4-bit one, with the same pages, page table,
+ * lengths, status and rules for them (above); where its calls say nothing else,
+ * what the rdkv_q4_* calls say of sharing, streams and errors holds.  The keys of
+ * a (page, KV head), 64 tokens by head_dim channels, share one scale, and so do
+ * its values.  A scale is a power of two and a code is an e4m3 number:
+ *   scale = 2^e, e the smallest of -24 .. 7 with max |x| <= 448 2^e,
+ *   code = e4m3(x / scale) (nearest, ties to even),   x^ = scale * code.
+ * Values past +-57344 (infinities too) are held as +-57344, a NaN as 0.  A code's
+ * precision does not depend on the scale until x falls below 2^-6 scale, so rows
+ * that meet in one block, or whose block takes another scale, keep their values
+ * down to there: rows written behind others in a page raise its scales where
+ * they need more, the earlier codes are taken in the new scale (rounded once
+ * more where they are that small), and no write lowers a scale but the one that
+ * begins a page (slot 0).
+ *
+ * Layout.  pages [n_pages][h_kv][rdkv_q8_page_bytes(head_dim)]: 64 D bytes of
+ * key codes, then 64 D of value codes (D = head_dim),
+ *   keys    uint8 [32 token pairs][D / 64][2 tokens][64 channels];
+ *   values  uint8 [8 runs of 8 tokens][D / 64][8 g][4 token pairs][8 c][2 tokens]: channel
+ *           64 j + 8 g + c of run [..][j].
+ * scales [n_pages][h_kv][2] fp32: the keys' scale, the values'.
+ *
+ * Supported: head_dim, heads and types as for the 4-bit cache; pages 16-byte
+ * aligned, scales 8-byte aligned. */
+#define RDKV_Q8_PAGE_TOKENS 64
+#define RDKV_Q8_MAX_QUERIES 64
+#define RDKV_Q8_COUNTER_BYTES 262144
+typedef struct rdkv_q8_cache {
+  int32_t batch, h_kv, head_dim;
+  int32_t n_pages;            /* pages of the pool */
+  int32_t page_stride;        /* page-table entries of a sequence */
+  uint8_t* pages;
+  float* scales;
+  const int32_t* page_table;  /* [batch][page_stride] */
+  const int32_t* lens;        /* [batch] */
+  int32_t* status;            /* [1] */
+} rdkv_q8_cache;
+
+/* Bytes of one (page, KV head): 128 * head_dim; 0 for an unsupported head_dim. */
+size_t rdkv_q8_page_bytes(int32_t head_dim);
+
+/* Rows into the cache and back: arguments, positions and errors as
+ * rdkv_q4_write and rdkv_q4_read. */
+rdkv_status rdkv_q8_write(const rdkv_q8_cache* cache, int32_t dtype, const void* k, const void* v, int64_t rows,
+                          int64_t row_stride, const int32_t* row_start, int32_t max_rows, void* stream);
+rdkv_status rdkv_q8_read(const rdkv_q8_cache* cache, int32_t dtype, void* k, void* v, int64_t rows,
+                         int64_t row_stride, const int32_t* row_start, const int32_t* first, int32_t max_rows, void* stream);
+
+/* Attention of the n_q newest tokens of every sequence over its cache, q, out,
+ * lse and ws as for rdkv_q4_attn without a selection (the bytes from
+ * rdkv_q8_attn_workspace_bytes, the first RDKV_Q8_COUNTER_BYTES zero before the
+ * first use).  Sums are fp32; for 16-bit outputs the weights are rounded to
+ * fp16, for fp32 outputs every operand is held in 22 bits or more.
+ *
+ * mass NULL, or fp32 [batch][h_kv][mass_stride] (mass_stride >= 64 * page_stride):
+ * the weight that each held position p has received so far,
+ *   mass[b][j][p] += sum over query tokens i that see p and the G heads h of
+ *                    KV head j of exp(q_i,h . k^_p / sqrt(head_dim) - lse_i,h),
+ * summed in this order for every p, so that equal calls give equal bits.
+ * rdkv_score's w_tok of a prompt is the same sum over the prompt's queries: copied in, it is
+ * where the decode goes on.  A query head whose lse is not finite (it holds a NaN) adds
+ * nothing.  Positions that are not held are not touched: rows that are written
+ * over (rejected drafts) start with what mass holds at their positions, so
+ * zero it there.  with_mass of the workspace query: 1 for calls with mass (it
+ * then holds the logits too), and such calls add one launch. */
+size_t rdkv_q8_attn_workspace_bytes(const rdkv_q8_cache* cache, int32_t h_q, int32_t n_q, int32_t with_mass);
+rdkv_status rdkv_q8_attn(const rdkv_q8_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
+                         int32_t n_q, float* mass, int64_t mass_stride, void* out, int32_t out_dtype, float* lse,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* Failure-detection self-test of rdkv_q8_attn, as rdkv_q4_timeout_selftest is
+ * of rdkv_q4_attn (a page is withheld where its index plus the KV head is a
+ * multiple of `withhold`); takes no mass. */
+rdkv_status rdkv_q8_timeout_selftest(const rdkv_q8_cache* cache, int32_t dtype, const void* q, int64_t q_stride,
+                                     int32_t h_q, int32_t n_q, void* out, int32_t out_dtype, float* lse, void* ws,
+                                     size_t ws_bytes, int32_t withhold, int64_t wait_cycles, void* stream);
+
+/* Brings every sequence that holds more than n_keep tokens down to n_keep, in
+ * every KV head on its own: kept are the first n_first and the last n_last
+ * positions and, of the others, those with the most mass (equal mass: the
+ * lower position; a NaN counts as more than any number).  The kept rows move to positions
+ * 0 .. n_keep - 1 in their order, within the sequence's own pages, and their
+ * mass with them; the mass of positions n_keep .. lens[b] - 1 becomes 0, and so do
+ * the codes behind position n_keep - 1 in its page.
+ * kept [batch][h_kv][n_keep] int32: the position each row came from,
+ * ascending; -1 behind the last.  A sequence of at most n_keep tokens stays as
+ * it is (kept: its positions).  Pages whose rows all stay where they are stay as they
+ * are; another page takes the scales that its rows need, by the rule of a page written
+ * whole (values that fall below 2^-6 of their new scale are rounded once more).
+ *
+ * The caller lowers lens afterwards (min(lens[b], n_keep)), in place and on the
+ * stream, as it raises it before a write; pages past it are then free.
+ * 0 <= n_first, 0 <= n_last, n_first + n_last <= n_keep, 1 <= n_keep.  No page of
+ * a sequence that is brought down may be shared with another sequence.  A
+ * sequence with a page outside the pool (RDKV_ERR_INVALID_ARG in *status) is left as
+ * it is, rows and mass, and its kept are -1.  ws: rdkv_q8_evict_workspace_bytes bytes,
+ * 16-byte aligned, nothing in it needs to be zero; calls that may run at the
+ * same time need one each.  Two launches. */
+size_t rdkv_q8_evict_workspace_bytes(const rdkv_q8_cache* cache);
+rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, int64_t mass_stride, int32_t n_keep, int32_t n_first,
+                          int32_t n_last, int32_t* kept, void* ws, size_t ws_bytes, void* stream);
+
+/* Reads *status and clears it.  SYNCHRONISES `stream`. */
+rdkv_status rdkv_q8_status(const rdkv_q8_cache* cache, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "librdkv.so")
 
 RDKV_OK, RDKV_ERR_INVALID_ARG, RDKV_ERR_UNSUPPORTED, RDKV_ERR_CAPACITY = 0, 1, 2, 3
 RDKV_ERR_CUDA, RDKV_ERR_TIMEOUT, RDKV_ERR_WORKSPACE = 4, 5, 6
-RDKV_F16, RDKV_F32, RDKV_BF16 = 0, 1, 2  # RDKV_BF16: the 4-bit cache's calls only
+RDKV_F16, RDKV_F32, RDKV_BF16 = 0, 1, 2  # RDKV_BF16: the 4-bit and 8-bit caches' calls only
 RDKV_ALLOC_POOLED, RDKV_ALLOC_PER_HEAD, RDKV_ALLOC_TOPK, RDKV_ALLOC_THRESHOLD = 0, 1, 2, 3
 
 EXPORTED = (
@@ -34,6 +34,8 @@ EXPORTED = (
     "rdkv_allocate_pack_workspace_bytes", "rdkv_allocate_pack",
     "rdkv_q4_page_bytes", "rdkv_q4_write", "rdkv_q4_read", "rdkv_q4_attn_workspace_bytes", "rdkv_q4_attn",
     "rdkv_q4_select_workspace_bytes", "rdkv_q4_select", "rdkv_q4_status", "rdkv_q4_timeout_selftest",
+    "rdkv_q8_page_bytes", "rdkv_q8_write", "rdkv_q8_read", "rdkv_q8_attn_workspace_bytes", "rdkv_q8_attn",
+    "rdkv_q8_evict_workspace_bytes", "rdkv_q8_evict", "rdkv_q8_status", "rdkv_q8_timeout_selftest",
 )
 RDKV_CALL_SCORE, RDKV_CALL_ALLOCATE, RDKV_CALL_DECODE = 0, 1, 2
 
@@ -70,12 +72,21 @@ class Q4CacheStruct(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("batch", "h_kv", "head_dim", "n_pages", "page_stride")] + [
         (n, ctypes.c_void_p) for n in ("pages", "bounds", "page_table", "lens", "status")]
 
+
+class Q8CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "h_kv", "head_dim", "n_pages", "page_stride")] + [
+        (n, ctypes.c_void_p) for n in ("pages", "scales", "page_table", "lens", "status")]
+
+
 PAGE_ROWS = 16  # RDKV_ZONE_C_PAGE_ROWS
 A_PAGE_BYTES = 65536  # RDKV_ZONE_A_PAGE_BYTES
 B_PAGE_ROWS = 16  # RDKV_ZONE_B_PAGE_ROWS
 Q4_PAGE_TOKENS = 64  # RDKV_Q4_PAGE_TOKENS
 Q4_MAX_QUERIES = 64  # RDKV_Q4_MAX_QUERIES
 Q4_COUNTER_BYTES = 262144  # RDKV_Q4_COUNTER_BYTES
+Q8_PAGE_TOKENS = 64  # RDKV_Q8_PAGE_TOKENS
+Q8_MAX_QUERIES = 64  # RDKV_Q8_MAX_QUERIES
+Q8_COUNTER_BYTES = 262144  # RDKV_Q8_COUNTER_BYTES
 
 
 HEAD_PLAN_DTYPE = [("n_v", "<i4", 4), ("tiles", "<i4", 4), ("n_k", "<i4", 5), ("k_words", "<i4", 4),
@@ -155,6 +166,18 @@ def lib():
             "rdkv_q4_timeout_selftest": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                                         _P, ctypes.c_int32, _P, ctypes.c_int32, _P, _P, ctypes.c_size_t,
                                                         ctypes.c_int32, ctypes.c_int64, _P]),
+            "rdkv_q8_page_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+            "rdkv_q8_write": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int32, _P]),
+            "rdkv_q8_read": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, ctypes.c_int32, _P]),
+            "rdkv_q8_attn_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+            "rdkv_q8_attn": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P,
+                                            ctypes.c_int64, _P, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P]),
+            "rdkv_q8_evict_workspace_bytes": (ctypes.c_size_t, [_P]),
+            "rdkv_q8_evict": (ctypes.c_int, [_P, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P,
+                                             ctypes.c_size_t, _P]),
+            "rdkv_q8_status": (ctypes.c_int, [_P, _P]),
+            "rdkv_q8_timeout_selftest": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P,
+                                                        ctypes.c_int32, _P, _P, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, _P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -939,14 +962,8 @@ def rdkv_q4_write(cache, k, v, row_start=None, max_rows=None, stream=None):
     _check(lib().rdkv_q4_write(cache._ref, code, k.data_ptr(), v.data_ptr(), rows, stride, start, n, _raw_stream(cache._index)))
 
 
-def rdkv_q4_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype=torch.float16, out=None, stream=None):
-    """Rows back as (k, v): max_rows of every sequence from position first (int32 [batch], default 0), as
-    [batch, max_rows, h_kv, D], or with row_start (int32 [batch + 1]) as [n_rows, h_kv, D].  `out`: a pair
-    of tensors to fill instead of new ones.  Rows past a sequence's length are not written."""
-    if stream is not None or cache._index != _current_device():
-        return _q4_elsewhere(cache, stream, rdkv_q4_read, max_rows, row_start, first, n_rows, dtype, out)
-    start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
-    at = _q4_index(cache, first, cache.batch, "first")
+def _q4_outputs(cache, max_rows, row_start, n_rows, dtype, out):
+    """((k, v), dtype code, rows, row stride, max_rows) of the rows that a read fills."""
     if out is None:
         key = row_start is None, max_rows, n_rows, dtype
         found = cache._seen.get(key)
@@ -968,6 +985,18 @@ def rdkv_q4_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype
     else:
         k, v = out
         code, rows, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
+    return (k, v), code, rows, stride, n
+
+
+def rdkv_q4_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype=torch.float16, out=None, stream=None):
+    """Rows back as (k, v): max_rows of every sequence from position first (int32 [batch], default 0), as
+    [batch, max_rows, h_kv, D], or with row_start (int32 [batch + 1]) as [n_rows, h_kv, D].  `out`: a pair
+    of tensors to fill instead of new ones.  Rows past a sequence's length are not written."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q4_read, max_rows, row_start, first, n_rows, dtype, out)
+    start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
+    at = _q4_index(cache, first, cache.batch, "first")
+    (k, v), code, rows, stride, n = _q4_outputs(cache, max_rows, row_start, n_rows, dtype, out)
     _check(lib().rdkv_q4_read(cache._ref, code, k.data_ptr(), v.data_ptr(), rows, stride, start, at, n, _raw_stream(cache._index)))
     return k, v
 
@@ -1006,14 +1035,8 @@ def _q4_selection(cache, sel, n_q):
     return sel.shape[-1], _q4_index(cache, sel, sel.numel(), "sel")
 
 
-def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None, stream=None):
-    """Attention of the newest tokens' queries q [batch, n_q, h_q, D] (or [batch, h_q, D]) over the cache:
-    (out in q's shape and out_dtype, lse fp32 without D).  sel: pages int32 [batch, n_q, h_kv, n_sel] (for one
-    query token also without n_q), n_sel >= 1, to attend instead of all.  out_dtype: q's type (default) or torch.float32."""
-    if stream is not None or cache._index != _current_device():
-        return _q4_elsewhere(cache, stream, rdkv_q4_attn, q, sel, out, lse, out_dtype, ws)
-    s = _raw_stream(cache._index)
-    code, h_q, n_q, stride = _q4_queries(cache, q)
+def _q4_results(cache, q, out, lse, out_dtype):
+    """Outputs and log-sum-exps of an attention of q: those given, checked, or new ones."""
     shape = q.shape
     if out is None:
         if out_dtype is None and q.is_contiguous():
@@ -1030,6 +1053,18 @@ def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None
     else:
         _q4_require(lse.shape == q.shape[:-1] and lse.dtype == torch.float32 and lse.is_contiguous()
                     and lse.device == cache.device, "lse must be dense fp32 in q's shape without its last size")
+    return out, lse
+
+
+def rdkv_q4_attn(cache, q, sel=None, out=None, lse=None, out_dtype=None, ws=None, stream=None):
+    """Attention of the newest tokens' queries q [batch, n_q, h_q, D] (or [batch, h_q, D]) over the cache:
+    (out in q's shape and out_dtype, lse fp32 without D).  sel: pages int32 [batch, n_q, h_kv, n_sel] (for one
+    query token also without n_q), n_sel >= 1, to attend instead of all.  out_dtype: q's type (default) or torch.float32."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q4_attn, q, sel, out, lse, out_dtype, ws)
+    s = _raw_stream(cache._index)
+    code, h_q, n_q, stride = _q4_queries(cache, q)
+    out, lse = _q4_results(cache, q, out, lse, out_dtype)
     n_sel, sel_ptr = _q4_selection(cache, sel, n_q)
     if ws is None:
         ws = cache.workspace("attn", h_q, n_q, s)
@@ -1092,3 +1127,182 @@ def rdkv_q4_status(cache, stream=None):
     if stream is not None or cache._index != _current_device():
         return _q4_elsewhere(cache, stream, rdkv_q4_status)
     return lib().rdkv_q4_status(cache._ref, _raw_stream(cache._index))
+
+
+# ---------------------------------------------------------------- 8-bit cache
+class Q8Cache:
+    """An 8-bit cache of `batch` sequences (slots) of up to max_tokens tokens: fp8 codes with a power of two as the
+    scale of each (page, KV head), of its keys and of its values; its page table, lengths and the C struct
+    that points at them.
+
+    The buffers are allocated unless given: pages uint8 [n_pages, h_kv, 128 * head_dim], scales fp32
+    [n_pages, h_kv, 2], page_table int32 [batch, stride] and lens int32 [batch]; caches may share pages and
+    scales (a pool) under their own tables.  Without a table every sequence gets its own run of pages.  lens
+    is the caller's: raise it, in place, before rdkv_q8_write, and lower it after rdkv_q8_evict."""
+
+    pages, scales, page_table, lens, status = map(_q4_fixed, ("pages", "scales", "page_table", "lens", "status"))
+
+    def __init__(self, batch, h_kv, head_dim, max_tokens, device, pages=None, scales=None, page_table=None, lens=None):
+        _q4_require(batch >= 1 and h_kv >= 1 and max_tokens >= 1, "batch, h_kv and max_tokens must be positive")
+        page_bytes = lib().rdkv_q8_page_bytes(head_dim)
+        if page_bytes == 0:
+            raise RDKVError(RDKV_ERR_UNSUPPORTED, f"head_dim {head_dim} not in (64, 128)")
+        stride = -(-max_tokens // Q8_PAGE_TOKENS)
+        self.batch, self.h_kv, self.head_dim = batch, h_kv, head_dim
+        if pages is None:
+            pages = torch.zeros(batch * stride, h_kv, page_bytes, dtype=torch.uint8, device=device)
+        self.device, n_pages = pages.device, pages.shape[0]
+        _q4_require(self.device.type == "cuda", "the cache lives on a GPU")
+        if scales is None:
+            scales = torch.ones(n_pages, h_kv, 2, dtype=torch.float32, device=self.device)
+        if page_table is None:
+            _q4_require(n_pages >= batch * stride, f"{n_pages} pages for {batch} sequences of {stride}: give a page_table")
+            page_table = torch.arange(batch * stride, dtype=torch.int32, device=self.device).view(batch, stride)
+        if lens is None:
+            lens = torch.zeros(batch, dtype=torch.int32, device=self.device)
+        self.pages, self.scales, self.page_table, self.lens = pages, scales, page_table, lens
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        for name, t, dtype, shape in (("pages", pages, torch.uint8, (n_pages, h_kv, page_bytes)),
+                                      ("scales", scales, torch.float32, (n_pages, h_kv, 2)),
+                                      ("page_table", page_table, torch.int32, (batch, page_table.shape[-1])),
+                                      ("lens", lens, torch.int32, (batch,))):
+            _q4_require(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous() and t.device == self.device,
+                        f"{name} must be a dense {dtype} {list(shape)} on {self.device}")
+        _q4_require(page_table.shape[1] >= 1 and n_pages >= 1, "a cache needs pages")
+        self.max_tokens = page_table.shape[1] * Q8_PAGE_TOKENS  # that a sequence's table has room for
+        self.c = Q8CacheStruct(batch, h_kv, head_dim, n_pages, page_table.shape[1], pages.data_ptr(), scales.data_ptr(),
+                               page_table.data_ptr(), lens.data_ptr(), self.status.data_ptr())
+        self._ref = ctypes.addressof(self.c)
+        self._index = self.device.index
+        self._ws, self._seen = {}, {}  # workspaces by stream; what the checks found for rows and queries of a shape and type
+
+    def new_mass(self):
+        """Accumulated weights for rdkv_q8_attn and rdkv_q8_evict, zero: fp32 [batch, h_kv, max_tokens]."""
+        return torch.zeros(self.batch, self.h_kv, self.max_tokens, dtype=torch.float32, device=self.device)
+
+    def workspace(self, kind, h_q, n_q, s):
+        """The workspace of rdkv_q8_attn without ("attn") or with mass ("mass"), or of rdkv_q8_evict ("evict"), for
+        calls on the current stream s, its counters zero.  While a graph is being captured: one of that
+        call's own, cleared in the graph (two captured graphs may run at once)."""
+        nb = self._ws.get((kind, h_q, n_q))
+        if nb is None:
+            if kind == "evict":
+                nb = lib().rdkv_q8_evict_workspace_bytes(self._ref)
+            else:
+                nb = lib().rdkv_q8_attn_workspace_bytes(self._ref, h_q, n_q, kind == "mass")
+            if nb == 0:
+                raise RDKVError(RDKV_ERR_UNSUPPORTED, lib().rdkv_last_error_string().decode())
+            self._ws[kind, h_q, n_q] = nb
+        capturing = torch.cuda.is_current_stream_capturing()
+        ws = None if capturing else self._ws.get((kind, s))
+        if ws is None or ws.numel() < nb:
+            ws = torch.empty(nb, dtype=torch.uint8, device=self.device)
+            if kind != "evict":
+                ws[:Q8_COUNTER_BYTES].zero_()
+            if not capturing:
+                self._ws[kind, s] = ws
+        return ws
+
+
+def rdkv_q8_write(cache, k, v, row_start=None, max_rows=None, stream=None):
+    """Quantises rows k, v into the cache: [batch, n, h_kv, D], the last n tokens of every sequence, or
+    [rows, h_kv, D] with row_start int32 [batch + 1] (sequence b's rows, at most max_rows of them).
+    cache.lens must already count them."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q8_write, k, v, row_start, max_rows)
+    start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
+    code, rows, stride, n = _q4_rows(cache, k, v, row_start, max_rows)
+    _check(lib().rdkv_q8_write(cache._ref, code, k.data_ptr(), v.data_ptr(), rows, stride, start, n, _raw_stream(cache._index)))
+
+
+def rdkv_q8_read(cache, max_rows, row_start=None, first=None, n_rows=None, dtype=torch.float16, out=None, stream=None):
+    """Rows back as (k, v): max_rows of every sequence from position first (int32 [batch], default 0), as
+    [batch, max_rows, h_kv, D], or with row_start (int32 [batch + 1]) as [n_rows, h_kv, D].  `out`: a pair
+    of tensors to fill instead of new ones.  Rows past a sequence's length are not written."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q8_read, max_rows, row_start, first, n_rows, dtype, out)
+    start = _q4_index(cache, row_start, cache.batch + 1, "row_start")
+    at = _q4_index(cache, first, cache.batch, "first")
+    (k, v), code, rows, stride, n = _q4_outputs(cache, max_rows, row_start, n_rows, dtype, out)
+    _check(lib().rdkv_q8_read(cache._ref, code, k.data_ptr(), v.data_ptr(), rows, stride, start, at, n, _raw_stream(cache._index)))
+    return k, v
+
+
+def _q8_mass(cache, mass):
+    """(pointer, floats between rows) of accumulated weights."""
+    _q4_require(mass.dtype == torch.float32 and mass.dim() == 3 and mass.shape[:2] == (cache.batch, cache.h_kv)
+                and mass.shape[2] >= cache.max_tokens and mass.is_contiguous() and mass.device == cache.device,
+                f"mass must be a dense fp32 [{cache.batch}, {cache.h_kv}, >= {cache.max_tokens}] on {cache.device}")
+    return mass.data_ptr(), mass.shape[2]
+
+
+def rdkv_q8_attn(cache, q, mass=None, out=None, lse=None, out_dtype=None, ws=None, stream=None):
+    """Attention of the newest tokens' queries q [batch, n_q, h_q, D] (or [batch, h_q, D]) over the cache:
+    (out in q's shape and out_dtype, lse fp32 without D).  out_dtype: q's type (default) or torch.float32.  mass
+    (cache.new_mass()): takes the weight that each held position received, summed over the queries
+    that see it and the heads of its group."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q8_attn, q, mass, out, lse, out_dtype, ws)
+    s = _raw_stream(cache._index)
+    code, h_q, n_q, stride = _q4_queries(cache, q)
+    out, lse = _q4_results(cache, q, out, lse, out_dtype)
+    mass_ptr, mass_stride = (None, 0) if mass is None else _q8_mass(cache, mass)
+    if ws is None:
+        ws = cache.workspace("attn" if mass is None else "mass", h_q, n_q, s)
+    else:
+        _q4_check_ws(cache, ws)
+    _check(lib().rdkv_q8_attn(cache._ref, code, q.data_ptr(), stride, h_q, n_q, mass_ptr, mass_stride, out.data_ptr(),
+                              _Q4_DTYPES[out.dtype], lse.data_ptr(), ws.data_ptr(), ws.numel(), s))
+    return out, lse
+
+
+def rdkv_q8_timeout_selftest(cache, q, out_dtype=None, withhold=1, wait_cycles=2_000_000, ws=None, stream=None):
+    """rdkv_q8_attn with the pages whose index plus KV head is a multiple of `withhold` waited for and never
+    copied: the waits run out after wait_cycles SM cycles each and rdkv_q8_status reports RDKV_ERR_TIMEOUT.
+    Returns (out, lse), which are no results."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q8_timeout_selftest, q, out_dtype, withhold, wait_cycles, ws)
+    s = _raw_stream(cache._index)
+    code, h_q, n_q, stride = _q4_queries(cache, q)
+    out, lse = _q4_results(cache, q, None, None, out_dtype)
+    if ws is None:
+        ws = cache.workspace("attn", h_q, n_q, s)
+    else:
+        _q4_check_ws(cache, ws)
+    _check(lib().rdkv_q8_timeout_selftest(cache._ref, code, q.data_ptr(), stride, h_q, n_q, out.data_ptr(), _Q4_DTYPES[out.dtype],
+                                          lse.data_ptr(), ws.data_ptr(), ws.numel(), int(withhold), int(wait_cycles), s))
+    return out, lse
+
+
+def rdkv_q8_evict(cache, mass, n_keep, n_first=0, n_last=0, out=None, ws=None, stream=None):
+    """Brings sequences of more than n_keep tokens down to n_keep, each KV head on its own: the first n_first, the
+    last n_last and the others with the most mass stay, in order, at the front; mass moves with them.
+    Returns the positions they came from: int32 [batch, h_kv, n_keep], ascending, -1 behind the last.  Lower
+    the lengths afterwards: cache.lens.clamp_(max=n_keep)."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q8_evict, mass, n_keep, n_first, n_last, out, ws)
+    s = _raw_stream(cache._index)
+    mass_ptr, mass_stride = _q8_mass(cache, mass)
+    if not (1 <= n_keep < 2 ** 31 and 0 <= n_first <= n_keep and 0 <= n_last <= n_keep):  # (32-bit arguments wrap)
+        raise RDKVError(RDKV_ERR_INVALID_ARG, f"n_keep {n_keep}, n_first {n_first}, n_last {n_last}")
+    shape = (cache.batch, cache.h_kv, n_keep)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int32, device=cache.device)
+    else:
+        _q4_require(out.shape == shape and out.dtype == torch.int32 and out.is_contiguous()
+                    and out.device == cache.device, f"out must be a dense int32 {list(shape)}")
+    if ws is None:
+        ws = cache.workspace("evict", 0, 0, s)
+    else:
+        _q4_check_ws(cache, ws)
+    _check(lib().rdkv_q8_evict(cache._ref, mass_ptr, mass_stride, n_keep, n_first, n_last, out.data_ptr(), ws.data_ptr(),
+                               ws.numel(), s))
+    return out
+
+
+def rdkv_q8_status(cache, stream=None):
+    """What the calls on this cache reported on the device since the last read (RDKV_OK: nothing);
+    synchronises the stream."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q8_status)
+    return lib().rdkv_q8_status(cache._ref, _raw_stream(cache._index))
