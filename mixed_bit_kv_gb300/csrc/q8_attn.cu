@@ -21,7 +21,8 @@
 // Scales.  The keys' scale, 1 / sqrt(D), log2 e and the row's power of two are one factor of the page.  The values' scale
 // 2^f joins the exponent: what is held is 2^(s + f - ref), ref the running maximum of s + f, so that weights are rounded
 // relative to what they contribute, not to the largest probability, and a page of small values costs no bits of
-// one of large values.  The sum of weights takes 2^-f back, once a page.
+// one of large values.  The sum of weights takes 2^-f back, once a page.  (ref is held as its two parts, whose sum
+// would lose f beside a logit of 2^24.)
 //
 // Roundings.  Logits, maxima, sums of weights and outputs' sums are fp32.  The tensor core cuts what it adds to an
 // accumulator (it does not round), so its accumulators start at zero for every page and the pages' sums are fp32 additions.
@@ -96,8 +97,8 @@ __device__ __forceinline__ void put4(const AttnArgs& a, int64_t at, float4 o) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = w;
   }
 }
-// The row's log-sum-exp, of a reference and a sum that may be some 2^30: the sum's exponent goes to the reference first,
-// so that no two large parts that cancel are rounded.  (a NaN sum, of a query that holds one, is not a sum of nothing)
+// The row's log-sum-exp, of a reference and a sum that may be some 2^30 (the reference is the logit of the key that
+// contributes most, not the largest): the sum's exponent goes to the reference first, so that no two large parts that cancel are rounded.  (a NaN sum, of a query that holds one, is not a sum of nothing)
 __device__ __forceinline__ void put_lse(const AttnArgs& a, int64_t row, float m, float l) {
   if (a.lse) {
     const int e = (int)(__float_as_uint(l) >> 23 & 255u) - 127;
@@ -119,11 +120,12 @@ struct Warp {
   // numbers down to 2^-25 of the largest contribution (PREC: 2^-28).
   static constexpr int kOff = PREC ? 14 : 11;
   static constexpr int kRest = 2048;  // of the weights' remainders
+  static constexpr float kFar = 262144.0f;
 
   uint32_t q[kS][4][2 * NT];            // operand registers by 64 channels and 16 of them
   uint32_t qlow[PREC ? kS : 1][4][2];   // (PREC) the remainders
   float scale[2];                       // base-2 logits of sums of codes, the keys' scale aside
-  float ref[2], l[2];                   // the running maximum (base 2) and this lane's share of the sum
+  float ref[2], rf[2], l[2];            // the running maximum as a logit (base 2) and its values' exponent; this lane's share of the sum
   // kCols: [64 channels][pair m][channel 2 m, + 1 of this lane's 8 x columns]; else [64 channels][channel c of 8][rows x columns]
   float o[kS][kCols ? 4 : 8][4];
 
@@ -218,7 +220,7 @@ struct Warp {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][m][i] = 0.0f;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) ref[n] = -INFINITY, l[n] = 0.0f;
+    for (int n = 0; n < 2; ++n) ref[n] = -INFINITY, rf[n] = l[n] = 0.0f;
   }
 
   // Sums of a lane's two rows (or columns) times f0 and f1.
@@ -290,7 +292,7 @@ struct Warp {
   __device__ __forceinline__ void weigh(Logits& s, float2 page, int g, int qd, bool cut, const int (&see)[2], float* store, int pad,
                                         Weights& p) {
     const float f = (float)exponent(page.y);
-    const float sc[2] = {scale[0] * page.x, scale[1] * page.x};
+    float sc[2] = {scale[0] * page.x, scale[1] * page.x};
     if (cut) {
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
@@ -304,37 +306,49 @@ struct Warp {
         if constexpr (kCols) {
           if (2 * qd < pad) {
             float2* to = reinterpret_cast<float2*>(store + (16 * i + g) * pad + 2 * qd);
-            to[0] = make_float2(s.c[i][0] * sc[0], s.c[i][1] * sc[1]);
-            to[4 * pad] = make_float2(s.c[i][2] * sc[0], s.c[i][3] * sc[1]);
+            to[0] = make_float2(__fmul_rn(s.c[i][0], sc[0]), __fmul_rn(s.c[i][1], sc[1]));
+            to[4 * pad] = make_float2(__fmul_rn(s.c[i][2], sc[0]), __fmul_rn(s.c[i][3], sc[1]));
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (g + 8 * (e >> 1) < pad) store[token_of(i, e, g, qd) * pad + g + 8 * (e >> 1)] = s.c[i][e] * sc[e >> 1];
+            if (g + 8 * (e >> 1) < pad) store[token_of(i, e, g, qd) * pad + g + 8 * (e >> 1)] = __fmul_rn(s.c[i][e], sc[e >> 1]);
         }
       }
     }
-    // a row's reference rises when one of its logits and values' scale passes it by more than 4 (PREC: at all)
+    // a row's reference rises when one of its logits with the values' scale passes it by more than 4 (PREC: at all)
     float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) m[row_of(e)] = fmaxf(m[row_of(e)], s.c[i][e]);
-    m[0] = fmaf(m[0], sc[0], f), m[1] = fmaf(m[1], sc[1], f);
+    m[0] = __fmul_rn(m[0], sc[0]), m[1] = __fmul_rn(m[1], sc[1]);
     constexpr float kPast = PREC ? 0.0f : 4.0f;
-    if (__any_sync(0xffffffffu, m[0] > ref[0] + kPast || m[1] > ref[1] + kPast)) {
+    // (nothing seen yet: infinity; nothing seen in this page either: a NaN, which passes nothing)
+    if (__any_sync(0xffffffffu, (m[0] - ref[0]) + (f - rf[0]) > kPast || (m[1] - ref[1]) + (f - rf[1]) > kPast)) {
       float back[2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
 #pragma unroll
         for (int d = kCols ? 4 : 1; d < (kCols ? 32 : 4); d *= 2) m[n] = fmaxf(m[n], __shfl_xor_sync(0xffffffffu, m[n], d));
-        m[n] = fmaxf(m[n], ref[n]);
-        back[n] = ref[n] == -INFINITY ? 0.0f : ex2(ref[n] - m[n]);
-        ref[n] = m[n];
+        const float past = (m[n] - ref[n]) + (f - rf[n]);
+        back[n] = 1.0f;
+        if (past > 0.0f) back[n] = ex2(-past), ref[n] = m[n], rf[n] = f;
       }
       rescale(back[0], back[1]);
     }
-    const float up[2] = {(float)kOff + f - (ref[0] == -INFINITY ? 0.0f : ref[0]), (float)kOff + f - (ref[1] == -INFINITY ? 0.0f : ref[1])};
+    const float r[2] = {ref[0] == -INFINITY ? 0.0f : ref[0], ref[1] == -INFINITY ? 0.0f : ref[1]};
+    const float off[2] = {(float)kOff + f - rf[0], (float)kOff + f - rf[1]};
+    float up[2] = {off[0] - r[0], off[1] - r[1]};
+    if (__any_sync(0xffffffffu, fmaxf(fabsf(r[0]), fabsf(r[1])) > kFar)) {
+      // logits so large that the roundings of product and sum, up to 2^-24 of them, would show in the exponent: their difference
+      // from the reference, which is exact
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s.c[i][e] = __fadd_rn(__fmul_rn(s.c[i][e], sc[row_of(e)]), -r[row_of(e)]) + off[row_of(e)];
+      sc[0] = sc[1] = 1.0f, up[0] = up[1] = 0.0f;
+    }
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
@@ -431,11 +445,11 @@ struct Warp {
   // stat(row, reference, sum) once a row.
   template <class Put, class Stat>
   __device__ __forceinline__ void finish(int g, int qd, Put put, Stat stat) {
-    const float a = two_to(-kOff);
-    float s[2];
+    float a[2], s[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      s[n] = l[n] * a;
+      a[n] = two_to((int)rf[n] - kOff);
+      s[n] = l[n] * a[n];
 #pragma unroll
       for (int d = kCols ? 4 : 1; d < (kCols ? 32 : 4); d *= 2) s[n] += __shfl_xor_sync(0xffffffffu, s[n], d);
     }
@@ -448,13 +462,13 @@ struct Warp {
 #pragma unroll
           for (int m = 0; m < 4; m += 2)
             put(row, 64 * j + 8 * g + 2 * m, s[n],
-                make_float4(o[j][m][n] * a, o[j][m][2 + n] * a, o[j][m + 1][n] * a, o[j][m + 1][2 + n] * a));
+                make_float4(o[j][m][n] * a[n], o[j][m][2 + n] * a[n], o[j][m + 1][n] * a[n], o[j][m + 1][2 + n] * a[n]));
         } else {
 #pragma unroll
           for (int m = 0; m < 16; m += 4)
             put(row, 64 * j + 16 * qd + m, s[n],
-                make_float4(o[j][m % 8][2 * n + m / 8] * a, o[j][m % 8 + 1][2 * n + m / 8] * a, o[j][m % 8 + 2][2 * n + m / 8] * a,
-                            o[j][m % 8 + 3][2 * n + m / 8] * a));
+                make_float4(o[j][m % 8][2 * n + m / 8] * a[n], o[j][m % 8 + 1][2 * n + m / 8] * a[n], o[j][m % 8 + 2][2 * n + m / 8] * a[n],
+                            o[j][m % 8 + 3][2 * n + m / 8] * a[n]));
         }
       }
     if (kCols ? g == 0 : qd == 0) {

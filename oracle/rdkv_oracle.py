@@ -950,3 +950,72 @@ def q4_select(scores, n_keep, n_first, n_last):
     forced = set(range(n_first)) | set(range(P - n_last, P))
     rest = sorted((p for p in range(P) if p not in forced), key=lambda p: (-scores[p], p))
     return sorted(forced | set(rest[:n_keep - len(forced)]))
+
+
+# ---------------------------------------------------------------- 8-bit cache
+Q8_PAGE = 64
+Q8_LOW, Q8_HIGH = -24, 7
+Q8_MOST = 448.0 * 2.0 ** Q8_HIGH
+# the values of codes 0 .. 126: e4m3 magnitudes
+Q8_GRID = np.array([m * 2.0 ** -9 for m in range(8)] + [(8 + m) * 2.0 ** (f - 10) for f in range(1, 16) for m in range(8)][:-1])
+
+
+def q8_cut(x):
+    """Rows as the cache takes them: within +-Q8_MOST, a NaN as 0 (float64)."""
+    x = np.asarray(x, np.float64)
+    return np.where(np.isnan(x), 0.0, np.clip(x, -Q8_MOST, Q8_MOST))
+
+
+def q8_exponent(x):
+    """The smallest e in Q8_LOW .. Q8_HIGH with max |x| <= 448 2^e."""
+    top = np.abs(x).max(initial=0.0)
+    return next((e for e in range(Q8_LOW, Q8_HIGH) if top <= 448.0 * 2.0 ** e), Q8_HIGH)
+
+
+def q8_codes(x, e):
+    """Codes uint8 of values x in the scale 2^e: the nearest magnitude, halves to the even code."""
+    y = np.abs(np.asarray(x, np.float64)) / 2.0 ** e
+    up = np.clip(np.searchsorted(Q8_GRID, y), 1, len(Q8_GRID) - 1)
+    low = up - 1
+    gap_low, gap_up = y - Q8_GRID[low], Q8_GRID[up] - y
+    code = np.where((gap_up < gap_low) | ((gap_up == gap_low) & (up % 2 == 0)), up, low)
+    return (code + 128 * np.signbit(x)).astype(np.uint8)
+
+
+def q8_values(codes, e):
+    """The values of codes in the scale 2^e (float64)."""
+    c = np.asarray(codes, np.int64)
+    return np.where(c >= 128, -1.0, 1.0) * Q8_GRID[c % 128] * 2.0 ** e
+
+
+def q8_append(held, e, x):
+    """One page side of one head: rows x [n, D] written behind the rows `held` [m, D] (values; m = 0 begins the
+    page) whose scale is 2^e.  Returns all rows' values and the exponent of their scale."""
+    x = q8_cut(x)
+    now = q8_exponent(x) if len(held) == 0 else max(e, q8_exponent(x))
+    rows = np.concatenate([held, x]) if len(held) else x
+    return q8_values(q8_codes(rows, now), now), now
+
+
+def q8_page_bytes(k, ek, v, ev):
+    """Bytes uint8 [128 D] of one (page, head) of values k, v [64, D] in the scales 2^ek and 2^ev."""
+    D = k.shape[1]
+    out = np.zeros(128 * D, np.uint8)
+    kc, vc = q8_codes(k, ek), q8_codes(v, ev)
+    for t in range(Q8_PAGE):
+        for c in range(D):
+            out[(t // 2 * (D // 64) + c // 64) * 128 + t % 2 * 64 + c % 64] = kc[t, c]
+            at = (((t // 8 * (D // 64) + c // 64) * 8 + c % 64 // 8) * 4 + t % 8 // 2) * 16 + c % 8 * 2 + t % 2
+            out[64 * D + at] = vc[t, c]
+    return out
+
+
+def q8_evict(mass, n_keep, n_first, n_last):
+    """Kept positions, ascending: all when they fit, else the first, the last and the others with the most mass
+    (equal mass: the lower position; a NaN above any number)."""
+    n = len(mass)
+    if n <= n_keep:
+        return list(range(n))
+    forced = set(range(n_first)) | set(range(n - n_last, n))
+    rest = sorted((t for t in range(n) if t not in forced), key=lambda t: (0, 0.0, t) if np.isnan(mass[t]) else (1, -float(mass[t]), t))
+    return sorted(forced | set(rest[:n_keep - len(forced)]))

@@ -1,0 +1,834 @@
+"""GPU parity of the 8-bit cache (rdkv_q8_*) against the CPU oracle.
+
+Written pages, scales and rows read back: every bit.  Evicted: positions, rows, scales and weights, every bit.
+Attention: against float64 attention over the values the cache holds.  With S = sum_c |q_c k_c| / sqrt(D), the errors counted are
+
+  a logit   D / 16 products of 16 terms and an accumulator, each term cut below 2^-23 of the largest: 17 D / 16 2^-23 S; fp32
+            queries in two fp16 parts: 2^-22 S; the factors of the row, the page and the sum's rounding: 2^-21 of the logit;
+            the exponential: 2^-20.  A weight changes by as much relatively, an output by twice that times max|v|, the
+            log-sum-exp by that alone;
+  sums      four products of 16 terms a page: 68 2^-23, and n fp32 sums, n 2^-24, once for the weights and once for the
+            weighted values: 2 n 2^-24; a weight below fp16's normal range, 2^-25 of what is held 2^11 times: 2^-34 of
+            max|v| for each of n keys;
+  16 bits   a weight's rounding to fp16, 2^-11 (fp32 outputs: two parts, 2^-22), and the output's own, eps / 2 of it.
+
+An accumulated weight is a sum of weights p, each off by its logit's error and the log-sum-exp's, plus the rounding of the sums."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from mixed_bit_kv_gb300 import rdkv, synth
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0") if torch.cuda.is_available() else None
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if DEV is None:
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def _rows(n, h, D, dt, seed, mag=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(n, h, D, generator=g) * mag
+    x[:, :, 3] *= 10.0
+    return x.to(dt)
+
+
+def _cache(lens, h, D, stride=None, seed=0, extra=3, grow=0):
+    """A cache of shuffled pages whose every code is a NaN, and every scale, until it is written."""
+    B = len(lens)
+    stride = stride or max(1, max(-(-n // 64) for n in lens))
+    n = B * stride + extra
+    order = torch.randperm(n, generator=torch.Generator().manual_seed(seed))
+    table = order[:B * stride].to(torch.int32).view(B, stride)
+    for b, t in enumerate(lens):                  # entries that no token needs (yet) are not read
+        table[b, -(-t // 64) + grow:] = 1 << 30
+    return rdkv.Q8Cache(B, h, D, stride * 64, DEV, pages=torch.full((n, h, 128 * D), 0xFF, dtype=torch.uint8, device=DEV),
+                        scales=torch.full((n, h, 2), float("nan"), device=DEV), page_table=table.to(DEV), lens=_ints(lens))
+
+
+class Held:
+    """What one sequence's cache holds, by the oracle: values [n, h, D] and exponents [pages, h] of keys and values."""
+
+    def __init__(self, h, D):
+        self.h, self.D = h, D
+        self.x = [np.zeros((0, h, D)), np.zeros((0, h, D))]
+        self.e = [np.zeros((0, h), int), np.zeros((0, h), int)]
+
+    def write(self, k, v):
+        for s, new in enumerate((k, v)):
+            new = new.double().numpy()
+            while len(new):
+                n = len(self.x[s])
+                m = min(len(new), 64 - n % 64)
+                rows, es = [], []
+                for j in range(self.h):
+                    held = self.x[s][n - n % 64:, j]
+                    r, e = O.q8_append(held, self.e[s][-1, j] if n % 64 else 0, new[:m, j])
+                    rows.append(r)
+                    es.append(e)
+                self.x[s] = np.concatenate([self.x[s][:n - n % 64], np.stack(rows, 1)])
+                self.e[s] = np.concatenate([self.e[s][:n // 64], [es]]).astype(int)
+                new = new[m:]
+
+    def evict(self, kept):
+        """kept [h, n]: positions; a page whose rows all stay keeps its scale."""
+        n = kept.shape[1]
+        for s in (0, 1):
+            x = np.stack([self.x[s][kept[j], j] for j in range(self.h)], 1)
+            e = np.zeros((-(-n // 64), self.h), int)
+            for p in range(len(e)):
+                for j in range(self.h):
+                    rows = kept[j, 64 * p:64 * p + 64]
+                    if len(rows) == 64 and np.array_equal(rows, np.arange(64 * p, 64 * p + 64)):
+                        e[p, j] = self.e[s][p, j]
+                        continue
+                    y = x[64 * p:64 * p + 64, j]
+                    e[p, j] = O.q8_exponent(y)
+                    x[64 * p:64 * p + 64, j] = O.q8_values(O.q8_codes(y, e[p, j]), e[p, j])
+            self.x[s], self.e[s] = x, e
+
+    @property
+    def k(self):
+        return self.x[0]
+
+    @property
+    def v(self):
+        return self.x[1]
+
+
+def _write(c, held, k, v):
+    """Rows k, v [n, h, D] a sequence, behind what the sequences hold."""
+    n = [len(x) for x in k]
+    for b in range(c.batch):
+        held[b].write(k[b], v[b])
+    c.lens.copy_(_ints([len(x.k) for x in held]))
+    rdkv.rdkv_q8_write(c, torch.cat(k).to(DEV), torch.cat(v).to(DEV), row_start=_ints([0] + list(np.cumsum(n))), max_rows=max(max(n), 1))
+
+
+def _filled(lens, h, D, dt, seed=0, mag=1.0, **kw):
+    """A cache written in one call, and what it holds."""
+    c = _cache(lens, h, D, seed=seed, **kw)
+    held = [Held(h, D) for _ in lens]
+    _write(c, held, [_rows(n, h, D, dt, seed + 10 * i + 1, mag) for i, n in enumerate(lens)],
+           [_rows(n, h, D, dt, seed + 10 * i + 2, mag) for i, n in enumerate(lens)])
+    return c, held
+
+
+def _check_held(c, held):
+    """Pages (what the sequences hold of them), scales and rows read back: equal."""
+    D, h = c.head_dim, c.h_kv
+    pages, scales, table = c.pages.cpu().numpy(), c.scales.cpu().numpy(), c.page_table.cpu().numpy()
+    one = np.zeros((64, D))
+    for b, x in enumerate(held):
+        n = len(x.k)
+        for p in range(-(-n // 64)):
+            m = min(64, n - 64 * p)
+            for j in range(h):
+                e = [x.e[s][p, j] for s in (0, 1)]
+                assert scales[table[b, p], j].tolist() == [2.0 ** e[0], 2.0 ** e[1]], (b, p, j)
+                if p not in (0, n // 64) and (b + p + j) % 7:      # (the oracle's byte order is slow)
+                    continue
+                sides = []
+                for s in (0, 1):
+                    side = one.copy()
+                    side[:m] = x.x[s][64 * p:64 * p + m, j]
+                    sides.append(side)
+                full = O.q8_page_bytes(sides[0], e[0], sides[1], e[1])
+                live = O.q8_page_bytes(np.where(np.arange(64)[:, None] < m, 448.0, 0.0) + one, 0,
+                                       np.where(np.arange(64)[:, None] < m, 448.0, 0.0) + one, 0) != 0
+                got = pages[table[b, p], j]
+                # (0 and -0 stand for one value)
+                same = (got == full) | ((got & 0x7F) == 0) & ((full & 0x7F) == 0)
+                assert same[live].all(), (b, p, j)
+    lens = [len(x.k) for x in held]
+    k, v = rdkv.rdkv_q8_read(c, max(max(lens), 1), row_start=_ints([0] + list(np.cumsum(lens))), n_rows=sum(lens), dtype=torch.float32)
+    assert np.array_equal(k.double().cpu().numpy(), np.concatenate([x.k for x in held]))
+    assert np.array_equal(v.double().cpu().numpy(), np.concatenate([x.v for x in held]))
+    assert rdkv.rdkv_q8_status(c) == 0
+
+
+def _check_attention(q, held, out, lse, mass=None, before=None):
+    """q [B, T, Hq, D]; mass and what it held before [B, h, slots]."""
+    q64, out64, lse64 = q.double().numpy(), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    eps = torch.finfo(out.dtype).eps
+    B, T, Hq, D = q64.shape
+    for b in range(B):
+        n, h = held[b].k.shape[:2]
+        G = Hq // h
+        want = None if mass is None else before[b].double().cpu().numpy()
+        tol_m = None if mass is None else (T * G + 1) * 2.0 ** -24 * np.abs(want)
+        for t in range(T):
+            m = max(0, n - T + t + 1)
+            for j in range(Hq):
+                K, V = held[b].k[:m, j // G], held[b].v[:m, j // G]
+                if m == 0:
+                    assert (out64[b, t, j] == 0).all() and lse64[b, t, j] == -np.inf
+                    continue
+                ref, ref_lse = O.attention_lse(q64[b, t, j], K, V)
+                s = K @ q64[b, t, j] / math.sqrt(D)
+                mags = np.abs(K) @ np.abs(q64[b, t, j]) / math.sqrt(D)
+                logit = mags.max() * (17 * D / 16 * 2.0 ** -23 + 2.0 ** -22) + 2.0 ** -21 * np.abs(s).max() + 2.0 ** -20
+                big = np.abs(V).max()
+                tol = (2 * logit + 68 * 2.0 ** -23 + 2 * m * 2.0 ** -24 + m * 2.0 ** -34) * big
+                if out.dtype != torch.float32:
+                    tol = tol + 2.0 ** -11 * big + eps / 2 * np.abs(ref)
+                else:
+                    tol = tol + 2.0 ** -22 * big
+                assert (np.abs(out64[b, t, j] - ref) <= tol).all(), (b, t, j, np.abs(out64[b, t, j] - ref).max(), np.max(tol))
+                lse_tol = logit + 2.0 ** -22 * abs(ref_lse) + m * 2.0 ** -24
+                assert abs(lse64[b, t, j] - ref_lse) <= lse_tol, (b, t, j, abs(lse64[b, t, j] - ref_lse), lse_tol)
+                if mass is not None:
+                    p = np.exp(s - ref_lse)
+                    want[j // G, :m] += p
+                    tol_m[j // G, :m] += p * (logit + lse_tol + (T * G + 1) * 2.0 ** -24) + 2.0 ** -120
+        if mass is not None:
+            diff = np.abs(mass[b].double().cpu().numpy() - want)
+            assert (diff <= tol_m + 2.0 ** -24 * np.abs(want)).all(), (b, (diff - tol_m).max())
+
+
+# ---------------------------------------------------------------- write and read
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("D,h", [(64, 1), (64, 3), (128, 2)])
+def test_written_pages_scales_and_rows_read_back(D, h, dtype):
+    dt, lens, new = TYPES[dtype], [70, 0, 1, 200, 64, 129], [33, 0, 1, 195, 64, 1]
+    c = _cache([a - b for a, b in zip(lens, new)], h, D, stride=4, grow=4)
+    held = [Held(h, D) for _ in lens]
+    for lo, hi in (([0] * 6, [a - b for a, b in zip(lens, new)]), ([a - b for a, b in zip(lens, new)], lens)):
+        _write(c, held, [_rows(y - x, h, D, dt, 10 + i, 1.0 + 3.0 * (x > 0)) for i, (x, y) in enumerate(zip(lo, hi))],
+               [_rows(y - x, h, D, dt, 30 + i, 1.0 + 3.0 * (x > 0)) for i, (x, y) in enumerate(zip(lo, hi))])
+        _check_held(c, held)
+    # in other types, from inside, into given tensors that keep what no row fills
+    first = [3, 0, 0, 60, 63, 100]
+    k = torch.full((6, 50, h, D), 7.0, dtype=dt, device=DEV)
+    v = k.clone()
+    rdkv.rdkv_q8_read(c, 50, first=_ints(first), out=(k, v))
+    for got, name in ((k, "k"), (v, "v")):
+        for b in range(6):
+            x = getattr(held[b], name)[first[b]:first[b] + 50]
+            assert torch.equal(got[b, :len(x)].cpu(), torch.from_numpy(x).to(dt)) and (got[b, len(x):] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tokens_that_raise_the_scales_one_by_one(D, dtype):
+    """Each token larger than all before it: the earlier codes are taken in the new scale again and again, tokens at
+    even and odd slots, past a page's end; then small ones, which raise nothing."""
+    c = _cache([0], 2, D, stride=2, grow=2)
+    held = [Held(2, D)]
+    for i in range(70):
+        mag = 2.0 ** (min(i, 66) * 0.35 - 13)
+        _write(c, held, [_rows(1, 2, D, TYPES[dtype], i, mag)], [_rows(1, 2, D, TYPES[dtype], 100 + i, mag / 3)])
+    _check_held(c, held)
+    for n in (2, 3, 9, 17):
+        _write(c, held, [_rows(n, 2, D, TYPES[dtype], n, 4.0)], [_rows(n, 2, D, TYPES[dtype], 50 + n, 40.0)])
+    _check_held(c, held)
+
+
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 15, 63, 64, 65, 130])
+@pytest.mark.parametrize("at", [0, 1, 7, 8, 33, 63])
+def test_runs_of_any_length_at_any_slot(n, at):
+    """Every kind of launch (a token, some, whole pages) at even and odd starts and ends; [batch, n] rows of a strided
+    projection, an empty slot among them."""
+    h, D = 2, 128
+    c = _cache([at, at], h, D, stride=4, grow=4)
+    held = [Held(h, D), Held(h, D)]
+    if at:
+        _write(c, held, [_rows(at, h, D, torch.bfloat16, 1), _rows(0, h, D, torch.bfloat16, 1)],
+               [_rows(at, h, D, torch.bfloat16, 2), _rows(0, h, D, torch.bfloat16, 1)])
+    qkv = torch.zeros(2, n, 7, D, dtype=torch.bfloat16)
+    for i in range(7):
+        qkv[:, :, i] = _rows(2 * n, 1, D, torch.bfloat16, 20 + i, 1 + 5 * (i % 2)).view(2, n, D)
+    held[0].write(qkv[0, :, 3:5], qkv[0, :, 5:7])
+    c.lens.copy_(_ints([at + n, 0]))
+    x = qkv.to(DEV)
+    rdkv.rdkv_q8_write(c, x[:, :, 3:5], x[:, :, 5:7])
+    _check_held(c, held)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_flat_huge_tiny_and_non_finite_rows(dtype):
+    D, dt = 64, TYPES[dtype]
+    x = _rows(64 * 8, 1, D, torch.float32, 1)
+    x[:64] = 0.0
+    x[64:128] = -0.0
+    x[130, 0, :6] = torch.tensor([math.inf, -math.inf, math.nan, -math.nan, 6e4, -5.8e4])
+    x[192:256] = math.nan
+    x[256:320] *= 1e-6
+    x[320:384] *= 1e4 if dtype == "f16" else 1e30
+    x[384:448] *= 2.0 ** -24 if dtype == "f16" else 1e-38
+    x[448:512] = 448.0
+    c = _cache([len(x)], 1, D)
+    held = [Held(1, D)]
+    _write(c, held, [x.to(dt)], [x.flip(0).to(dt)])
+    _check_held(c, held)
+    e = held[0].e[0][:, 0].tolist()
+    assert [e[i] for i in (0, 1, 2, 3, 5, 6, 7)] == [-24, -24, 7, -24, 7, -24, 0]
+    k = rdkv.rdkv_q8_read(c, len(x), dtype=dt)[0]
+    assert k.isfinite().all() and (k[0, 192:256] == 0).all()
+
+
+def test_positions_past_two_to_the_thirty_first_bytes():
+    """Pages that lie beyond 2^31 (and 2^32) bytes of the pool; weights and logits beyond 2^31 elements."""
+    h, D, n = 8, 128, 34000  # 4.5 GB
+    c = rdkv.Q8Cache(1, h, D, 192, DEV, pages=torch.empty(n, h, 128 * D, dtype=torch.uint8, device=DEV),
+                     page_table=_ints([[n - 1, 17000, n - 2]]))
+    held = [Held(h, D)]
+    _write(c, held, [_rows(150, h, D, torch.float16, 1)], [_rows(150, h, D, torch.float16, 2)])
+    _check_held(c, held)
+    q = _rows(1, 2 * h, D, torch.float16, 3).view(1, 1, 2 * h, D)
+    mass = c.new_mass()
+    out, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+    _check_attention(q, held, out, lse, mass, torch.zeros_like(mass))
+    kept = rdkv.rdkv_q8_evict(c, mass, 100, n_last=10)
+    m = mass.clone()
+    held[0].evict(kept[0].cpu().numpy())
+    c.lens.clamp_(max=100)
+    _check_held(c, held)
+    assert (m[..., 100:] == 0).all()
+
+
+def test_weights_and_logits_past_two_to_the_thirty_first_elements():
+    B, h, G, D, stride = 300, 8, 8, 64, 1792     # logits: 300 x 64 x 114,688 = 2.2e9
+    lens = [0] * B
+    lens[-1] = 130
+    lens[3] = 1
+    table = torch.zeros(B, stride, dtype=torch.int32, device=DEV)
+    table[-1, :3] = _ints([1, 2, 3])
+    c = rdkv.Q8Cache(B, h, D, stride * 64, DEV, pages=torch.full((5, h, 128 * D), 0xFF, dtype=torch.uint8, device=DEV), page_table=table)
+    held = [Held(h, D) for _ in lens]
+    _write(c, held, [_rows(n, h, D, torch.float16, i) for i, n in enumerate(lens)], [_rows(n, h, D, torch.float16, 500 + i) for i, n in enumerate(lens)])
+    q = _rows(B, h * G, D, torch.float16, 3).view(B, 1, h * G, D)
+    mass = c.new_mass()
+    out, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+    pick = [3, B - 1]
+    m = mass[pick][..., :192]
+    _check_attention(q[pick], [held[i] for i in pick], out[pick], lse[pick], m, torch.zeros_like(m))
+    mass[pick] = 0
+    assert not mass.any() and not out[[0, 5, B - 2]].any()
+    mass[-1, :, :130] = torch.rand(h, 130, device=DEV)
+    before = mass[-1].cpu().numpy()
+    kept = rdkv.rdkv_q8_evict(c, mass, 70, n_last=5).cpu()
+    assert all(kept[-1, j].tolist() == O.q8_evict(before[j, :130], 70, 0, 5) for j in range(h))
+    assert (kept[3, :, 0] == 0).all() and (kept[3, :, 1:] == -1).all() and (kept[0] == -1).all()
+    assert rdkv.rdkv_q8_status(c) == 0
+
+
+# ---------------------------------------------------------------- attention
+CASES = [(64, 1, 4, 1, [513]), (128, 2, 3, 1, [1, 64, 65, 0, 300]), (64, 3, 8, 1, [640, 63]), (128, 1, 1, 1, [129]), (128, 2, 4, 4, [200, 3, 1, 0, 77]),
+         (64, 2, 5, 3, [70, 250]), (128, 1, 8, 2, [1000]), (64, 1, 2, 64, [100, 30]), (128, 8, 7, 5, [90]), (128, 1, 8, 64, [150])]
+
+
+@pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("bf16", "bf16"), ("f32", "f32"), ("f16", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("D,h,G,T,lens", CASES)
+def test_attention_and_the_weights_of_its_keys(D, h, G, T, lens, dtype, out):
+    c, held = _filled(lens, h, D, TYPES[dtype], seed=D + T)
+    q = _rows(len(lens) * T, h * G, D, TYPES[dtype], 9).view(len(lens), T, h * G, D)
+    o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), out_dtype=TYPES[out])
+    assert o.dtype == TYPES[out]
+    _check_attention(q, held, o, lse)
+    mass = torch.rand(c.batch, h, c.max_tokens, generator=torch.Generator().manual_seed(1)).to(DEV) * 3
+    before = mass.clone()
+    o2, lse2 = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass, out_dtype=TYPES[out])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    _check_attention(q, held, o2, lse2, mass, before)
+    for b, n in enumerate(lens):
+        assert torch.equal(mass[b, :, n:], before[b, :, n:])
+    again = before.clone()
+    rdkv.rdkv_q8_attn(c, q.to(DEV), mass=again, out_dtype=TYPES[out])
+    assert torch.equal(mass, again) and rdkv.rdkv_q8_status(c) == 0
+
+
+@pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("lens,h,G,T", [([20000], 2, 4, 1), ([64 * 40 + 9] * 40, 2, 3, 1), ([9000, 1, 0, 4000], 1, 8, 4), ([1] * 70, 1, 5, 1)])
+def test_attention_over_many_blocks(lens, h, G, T, dtype, out):
+    D = 128
+    c, held = _filled(lens, h, D, TYPES[dtype])
+    q = _rows(len(lens) * T, h * G, D, TYPES[dtype], 9).view(len(lens), T, h * G, D)
+    mass = c.new_mass()
+    o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass, out_dtype=TYPES[out])
+    _check_attention(q, held, o, lse, mass, torch.zeros_like(mass))
+    rest = torch.arange(c.max_tokens, device=DEV) >= c.lens[:, None, None]
+    assert not mass[rest.expand_as(mass)].any()
+    # a token's weights sum to one a head
+    assert torch.allclose(mass.sum(-1), torch.tensor([min(T, n) * float(G) for n in lens], device=DEV)[:, None].expand(-1, h), rtol=1e-4)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("T", [1, 4])
+def test_attention_over_values_whose_scales_differ_by_two_to_the_thirtieth(T, dtype):
+    """Pages of values from 2^-24 to 2^6, weights that favour each in turn: the sums keep the digits of whichever
+    contributes."""
+    D, h, G, n = 64, 1, 4, 64 * 8
+    for turn in range(4):
+        k, v = _rows(n, h, D, torch.float32, 1), _rows(n, h, D, torch.float32, 2)
+        for p in range(8):
+            v[64 * p:64 * p + 64] *= 2.0 ** (-24 + 30 * ((p * 3 + turn) % 8) / 7)
+        q = _rows(T, G, D, TYPES[dtype], 3)
+        k[64 * turn:64 * turn + 64] += q[0, 0].float() * (0, 0.05, 0.15, 0.4)[turn]
+        c = _cache([n], h, D)
+        held = [Held(h, D)]
+        _write(c, held, [k.to(TYPES[dtype])], [v.to(TYPES[dtype])])
+        q = q.view(1, T, G, D)
+        mass = c.new_mass()
+        o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+        _check_attention(q, held, o, lse, mass, torch.zeros_like(mass))
+
+
+@pytest.mark.parametrize("mag_q,mag", [(1e-4, 1.0), (30.0, 1.0), (1.0, 1e-3), (0.05, 300.0), (0.0, 1.0), (1.0, 0.0)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_attention_of_large_and_small_values(dtype, mag_q, mag):
+    c, held = _filled([300, 64], 2, 64, TYPES[dtype], mag=mag)
+    q = _rows(2, 6, 64, TYPES[dtype], 9, mag_q).view(2, 1, 6, 64)
+    mass = c.new_mass()
+    o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+    _check_attention(q, held, o, lse, mass, torch.zeros_like(mass))
+
+
+@pytest.mark.parametrize("exponent", [-126, -100, -84, 40, 100])
+def test_queries_from_the_smallest_to_large_numbers(exponent):
+    """fp32 and bf16 queries far outside fp16's range: rows are taken times a power of two."""
+    for dtype in ("f32", "bf16"):
+        c, held = _filled([130], 1, 64, TYPES[dtype], mag=2.0 ** max(-8, -exponent // 8))
+        q = (_rows(1, 3, 64, torch.float32, 9) * 2.0 ** exponent).to(TYPES[dtype]).view(1, 1, 3, 64)
+        o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV))
+        assert o.isfinite().all() and lse.isfinite().all()
+        _check_attention(q, held, o, lse)
+
+
+def test_a_nan_query_is_nan_alone_and_adds_no_weight():
+    D, h, G, T = 64, 2, 3, 2
+    c, held = _filled([200, 70], h, D, torch.float16)
+    for out in (torch.float16, torch.float32):
+        q = _rows(2 * T, h * G, D, torch.float16, 9).view(2, T, h * G, D)
+        clean_mass = c.new_mass()
+        ref, ref_lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=clean_mass, out_dtype=out)
+        q[1, 0, 4, 7] = math.nan
+        mass = c.new_mass()
+        o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass, out_dtype=out)
+        assert o[1, 0, 4].isnan().all() and lse[1, 0, 4].isnan()
+        o[1, 0, 4], lse[1, 0, 4] = ref[1, 0, 4], ref_lse[1, 0, 4]
+        assert torch.equal(o, ref) and torch.equal(lse, ref_lse)
+        assert torch.equal(mass[0], clean_mass[0]) and torch.equal(mass[1, 0], clean_mass[1, 0])
+        less = (clean_mass[1, 1].double() - mass[1, 1].double())
+        assert mass.isfinite().all() and (less >= -1e-6).all() and abs(float(less.sum()) - 1) < 1e-3
+
+
+def test_lse_of_a_few_keys():
+    """One key's lse is its logit: the sum's exponent and the reference do not round it twice."""
+    for D in (64, 128):
+        for out in ("f16", "f32"):
+            c, held = _filled([1, 2, 3], 1, D, torch.float16)
+            q = _rows(3, 5, D, torch.float16, 7).view(3, 1, 5, D)
+            _, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), out_dtype=TYPES[out])
+            for b in range(3):
+                for j in range(5):
+                    s = held[b].k[:, 0] @ q[b, 0, j].double().numpy() / math.sqrt(D)
+                    mags = (np.abs(held[b].k[:, 0]) @ np.abs(q[b, 0, j].double().numpy())).max() / math.sqrt(D)
+                    ref = np.log(np.exp(s - s.max()).sum()) + s.max()
+                    assert abs(float(lse[b, 0, j]) - ref) <= 17 * D / 16 * 2.0 ** -23 * mags + 4 * 2.0 ** -23 * (abs(ref) + np.abs(s).max()) + 2.0 ** -21
+
+
+def test_strided_queries_without_n_q_and_into_given_outputs():
+    B, h, G, D = 3, 2, 4, 64
+    c, held = _filled([100, 5, 64], h, D, torch.bfloat16)
+    qkv = _rows(B, h * G + 2 * h, D, torch.bfloat16, 4).to(DEV)
+    q = qkv[:, :h * G]
+    ref = rdkv.rdkv_q8_attn(c, q.contiguous())
+    out, lse = torch.full((B, h * G, D), 5.0, device=DEV), torch.full((B, h * G), 5.0, device=DEV)
+    got = rdkv.rdkv_q8_attn(c, q, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse
+    _check_attention(q.cpu()[:, None], held, out[:, None], lse[:, None])
+    assert torch.equal(rdkv.rdkv_q8_attn(c, q)[0], ref[0])
+
+
+# ---------------------------------------------------------------- eviction
+def _evicted(c, held, mass, keep, first, last):
+    """Evicts, checks kept, weights and rows; the cache and held are then at the new lengths."""
+    before = mass.cpu().numpy().copy()
+    kept = rdkv.rdkv_q8_evict(c, mass, keep, n_first=first, n_last=last)
+    got, now = kept.cpu().numpy(), mass.cpu().numpy()
+    for b, x in enumerate(held):
+        n = len(x.k)
+        rows = []
+        for j in range(c.h_kv):
+            want = O.q8_evict(before[b, j, :n], keep, first, last)
+            assert got[b, j].tolist() == want + [-1] * (keep - len(want)), (b, j)
+            m = before[b, j].copy()
+            if n > keep:
+                m[:keep] = before[b, j][want]
+                m[keep:n] = 0
+            assert np.array_equal(now[b, j].view(np.int32), m.view(np.int32)), (b, j)
+            rows.append(want)
+        if n > keep:
+            x.evict(np.array(rows))
+    c.lens.clamp_(max=keep)
+    _check_held(c, held)
+    return kept
+
+
+def _weights(c, seed, kind="spread"):
+    g = torch.Generator().manual_seed(seed)
+    m = torch.rand(c.batch, c.h_kv, c.max_tokens, generator=g)
+    if kind == "spread":
+        m = (6 * m - 8).exp2() * (torch.rand(m.shape, generator=g) > 0.2)
+    elif kind == "equal":
+        m[:] = 0.25
+    elif kind == "few":
+        m = (m * 3).floor()
+    elif kind == "near":
+        m = 1 + (m * 50).floor() * 2.0 ** -23
+    elif kind == "any":
+        m = (torch.randint(0, 2 ** 32, m.shape, generator=g, dtype=torch.int64) - 2 ** 31).int().view(torch.float32)
+        m[..., ::11], m[..., 1::11], m[..., 2::11], m[..., 3::11] = 0.0, -0.0, math.inf, -math.inf
+    return m.to(DEV)
+
+
+@pytest.mark.parametrize("kind", ["spread", "equal", "few", "near", "any"])
+@pytest.mark.parametrize("D,h,lens,keep,first,last", [
+    (64, 1, [513], 200, 4, 64), (128, 2, [300, 100, 0, 129, 1], 128, 0, 0), (64, 3, [200, 640, 201], 199, 1, 198), (128, 1, [65, 64, 63], 64, 0, 1),
+    (64, 2, [700, 90], 1, 0, 0), (64, 2, [700, 90], 1, 1, 0), (64, 1, [257], 256, 0, 256), (128, 1, [5, 2, 3], 2, 1, 1), (64, 1, [1200], 1137, 3, 100)])
+def test_eviction(D, h, lens, keep, first, last, kind):
+    c, held = _filled(lens, h, D, torch.float16, seed=3)
+    mass = _weights(c, 5, kind)
+    _evicted(c, held, mass, keep, first, last)
+
+
+@pytest.mark.parametrize("kind", ["spread", "few", "any"])
+@pytest.mark.parametrize("n,keep,last", [(64 * 65, 4096, 500), (64 * 300 + 7, 3000, 0), (64 * 1030, 64 * 1029, 1), (64 * 520, 17, 3)])
+def test_eviction_of_long_rows(n, keep, last, kind):
+    """Rows spread over clusters of two to eight blocks."""
+    D, h = 64, 2
+    c, held = _filled([n], h, D, torch.float16)
+    _evicted(c, held, _weights(c, 6, kind), keep, 4 if keep > 17 else 0, last)
+
+
+def test_eviction_moves_rows_between_pages_of_different_scales():
+    D, h, n = 128, 2, 64 * 9 + 30
+    k, v = _rows(n, h, D, torch.float32, 1), _rows(n, h, D, torch.float32, 2)
+    for p in range(10):
+        k[64 * p:64 * p + 64] *= 2.0 ** (5 * p - 30)
+        v[64 * p:64 * p + 64] *= 2.0 ** (15 - 5 * p)
+    c = _cache([n], h, D)
+    held = [Held(h, D)]
+    _write(c, held, [k], [v])
+    mass = _weights(c, 7)
+    for keep in (500, 431, 70, 3):
+        _evicted(c, held, mass, keep, 1, 2)
+
+
+def test_eviction_of_many_sequences_and_again_and_again():
+    """More pages than blocks at once; then tokens behind the rows that stayed, and the next eviction."""
+    D, h = 64, 2
+    lens = [64 * 20 + i for i in range(48)]
+    c, held = _filled(lens, h, D, torch.float16)
+    mass = _weights(c, 8)
+    for step in range(3):
+        _evicted(c, held, mass, 900 - 100 * step, 2, 64)
+        _write(c, held, [_rows(50 + step, h, D, torch.float16, 10 * step + i, 2.0) for i in range(48)],
+               [_rows(50 + step, h, D, torch.float16, 700 + 10 * step + i, 2.0) for i in range(48)])
+        mass += 0.01 * (torch.arange(c.max_tokens, device=DEV) < c.lens[:, None, None])
+    _check_held(c, held)
+
+
+def test_other_sequences_of_the_pool_keep_their_pages():
+    """Two caches in one pool: what one evicts touches no page of the other, and no page of no one."""
+    D, h = 64, 2
+    pool = torch.randint(0, 127, (40, h, 128 * D), dtype=torch.uint8, device=DEV)
+    scales = torch.rand(40, h, 2, device=DEV)
+    order = torch.randperm(40)[:20].int()
+    c = rdkv.Q8Cache(1, h, D, 20 * 64, DEV, pages=pool, scales=scales, page_table=order.view(1, 20).to(DEV), lens=_ints([20 * 64 - 3]))
+    before, sc = pool.clone(), scales.clone()
+    mass = torch.rand(1, h, 20 * 64 + 64, device=DEV)
+    rdkv.rdkv_q8_evict(c, mass, 300)
+    own = torch.zeros(40, dtype=torch.bool)
+    own[order[:5].long()] = True                 # pages that hold the 300 rows now
+    assert torch.equal(pool[~own], before[~own]) and torch.equal(scales[~own], sc[~own])
+    assert not torch.equal(pool[own], before[own]) and rdkv.rdkv_q8_status(c) == 0
+
+
+# ---------------------------------------------------------------- bad device data, workspaces, streams, graphs
+def test_bad_pages_and_lengths_are_left_out_and_reported():
+    lens = [200, 130]
+    c, held = _filled(lens, 1, 64, torch.float16, stride=4, grow=4)
+    q = _rows(2, 2, 64, torch.float16, 9).view(2, 1, 2, 64)
+    ok = c.page_table.clone()
+    for bad in (-1, c.pages.shape[0], 1 << 30):
+        c.page_table[0, 1] = bad
+        mass = c.new_mass()
+        o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+        assert rdkv.rdkv_q8_status(c) == rdkv.RDKV_ERR_INVALID_ARG and rdkv.rdkv_q8_status(c) == 0
+        keep = np.r_[0:64, 128:200]
+        part = [Held(1, 64), held[1]]
+        part[0].x = [x[keep] for x in held[0].x]
+        _check_attention(q, part, o, lse)
+        assert not mass[0, 0, 64:128].any() and abs(float(mass[0].sum()) - 2) < 1e-4
+        before, sc = c.pages.clone(), c.scales.clone()
+        mass = _weights(c, 3)
+        m0 = mass.clone()
+        kept = rdkv.rdkv_q8_evict(c, mass, 100)  # the first sequence stays as it is, the second is brought down
+        assert rdkv.rdkv_q8_status(c) == rdkv.RDKV_ERR_INVALID_ARG
+        assert (kept[0] == -1).all() and torch.equal(mass[0], m0[0])
+        assert kept[1, 0].tolist() == O.q8_evict(m0[1, 0, :130].cpu().numpy(), 100, 0, 0)
+        own = [int(p) for p in c.page_table[1, :2]]
+        rest = [p for p in range(c.pages.shape[0]) if p not in own]
+        assert torch.equal(c.pages[rest], before[rest]) and torch.equal(c.scales[rest].view(torch.int32), sc[rest].view(torch.int32))
+        c.pages.copy_(before)
+        c.scales.copy_(sc)
+        row = _rows(2 * 80, 1, 64, torch.float16, 3).view(2, 80, 1, 64).to(DEV)
+        c.lens.copy_(_ints([140, 130]))          # rows of positions 60 .. 139: pages 0, 1 and 2
+        rdkv.rdkv_q8_write(c, row, row)
+        assert rdkv.rdkv_q8_status(c) == rdkv.RDKV_ERR_INVALID_ARG
+        k = rdkv.rdkv_q8_read(c, 80, first=_ints([60, 50]), out=(torch.zeros_like(row), torch.zeros_like(row)))[0]
+        assert rdkv.rdkv_q8_status(c) == rdkv.RDKV_ERR_INVALID_ARG
+        assert (k[0, 4:68] == 0).all() and (k[0, :4] != 0).any() and (k[0, 68:] != 0).any()
+        c.pages.copy_(before)
+        c.scales.copy_(sc)
+        c.page_table.copy_(ok)
+        c.lens.copy_(_ints(lens))
+    row = _rows(2, 1, 64, torch.float16, 3).view(2, 1, 1, 64).to(DEV)
+    before = c.pages.clone()
+    for n, code in (([257, -3], rdkv.RDKV_ERR_CAPACITY), ([1 << 30, 0], rdkv.RDKV_ERR_CAPACITY), ([-5, -1], rdkv.RDKV_ERR_INVALID_ARG)):
+        c.lens.copy_(_ints(n))
+        rdkv.rdkv_q8_write(c, row, row)
+        assert rdkv.rdkv_q8_status(c) == code and torch.equal(c.pages, before)
+        if max(n) < 1:                           # (a length past the table: the table's tokens, which were not all written)
+            mass = c.new_mass()
+            out, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+            assert rdkv.rdkv_q8_status(c) == code and not out.any() and (lse == -math.inf).all() and not mass.any()
+            assert (rdkv.rdkv_q8_evict(c, mass, 3) == -1).all()
+            assert rdkv.rdkv_q8_status(c) == code and torch.equal(c.pages, before)
+    for lens_past in ([257, 130], [1 << 30, 130]):
+        c, held = _filled([256, 130], 1, 64, torch.float16, stride=4)
+        c.page_table[1, 3] = 0
+        c.lens.copy_(_ints(lens_past))
+        o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV))
+        assert rdkv.rdkv_q8_status(c) == rdkv.RDKV_ERR_CAPACITY
+        _check_attention(q, held, o, lse)
+        kept = rdkv.rdkv_q8_evict(c, _weights(c, 3), 200)
+        assert rdkv.rdkv_q8_status(c) == rdkv.RDKV_ERR_CAPACITY and int(kept[0].max()) < 256 and (kept[1, 0, 130:] == -1).all()
+
+
+@pytest.mark.parametrize("lens,h,G,T", [([64 * 47 - 3] * 25, 4, 5, 1), ([64 * 300], 1, 8, 3), ([70, 64 * 40, 0], 2, 3, 2), ([1], 1, 1, 64)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nothing_is_written_outside_workspaces_and_outputs(D, lens, h, G, T):
+    """Guard words behind every workspace, output and weight stay as they were; the counters are zero again."""
+    c, _ = _filled(lens, h, D, torch.bfloat16)
+    B = len(lens)
+    q = _rows(B * T, h * G, D, torch.bfloat16, 9).view(B, T, h * G, D).to(DEV)
+
+    def guarded(shape, dtype):
+        n = math.prod(shape)
+        big = torch.full((n + 4096,), 77, dtype=dtype, device=DEV)
+        return big, big[:n].view(shape)
+
+    for kind in ("attn", "attn f32", "mass", "mass f32", "evict"):
+        if kind == "evict":
+            nb = rdkv.lib().rdkv_q8_evict_workspace_bytes(ctypes.byref(c.c))
+        else:
+            nb = rdkv.lib().rdkv_q8_attn_workspace_bytes(ctypes.byref(c.c), h * G, T, "mass" in kind)
+        big = torch.full((nb + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+        if kind != "evict":
+            big[:rdkv.Q8_COUNTER_BYTES] = 0
+        ws = big[:nb]
+        for _ in range(2):
+            mass = guarded((B, h, c.max_tokens), torch.float32)
+            if kind == "evict":
+                guards = [mass, guarded((B, h, 100), torch.int32)]
+                rdkv.rdkv_q8_evict(c, mass[1], 100, n_first=1, n_last=2, out=guards[1][1], ws=ws)
+            else:
+                guards = [mass, guarded(q.shape, torch.float32 if "f32" in kind else q.dtype), guarded(q.shape[:-1], torch.float32)]
+                rdkv.rdkv_q8_attn(c, q, mass=mass[1] if "mass" in kind else None, out=guards[1][1], lse=guards[2][1], ws=ws)
+        assert (big[nb:] == 0xA5).all(), kind
+        for b, x in guards:
+            assert (b[x.numel():] == 77).all(), kind
+        if kind != "evict":
+            assert (ws[:rdkv.Q8_COUNTER_BYTES] == 0).all(), kind
+    assert rdkv.rdkv_q8_status(c) == 0
+
+
+def test_one_workspace_serves_calls_of_any_shape_in_turn():
+    caches = [_filled([64 * 50, 300], 2, 128, torch.float16), _filled([700], 1, 64, torch.float16)]
+    nb = max(rdkv.lib().rdkv_q8_attn_workspace_bytes(ctypes.byref(c.c), 8 * c.h_kv, 4, 1) for c, _ in caches)
+    ws = torch.zeros(nb, dtype=torch.uint8, device=DEV)
+    for turn in range(3):
+        for c, held in caches:
+            for G, T, out in ((3, 1, torch.float16), (8, 4, torch.float16), (5, 2, torch.float32)):
+                q = _rows(c.batch * T, c.h_kv * G, c.head_dim, torch.float16, turn).view(c.batch, T, -1, c.head_dim)
+                mass = c.new_mass()
+                o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass, out_dtype=out, ws=ws)
+                _check_attention(q, held, o, lse, mass, torch.zeros_like(mass))
+
+
+def test_a_side_stream_and_two_graphs_replayed_in_turn_and_at_once():
+    """Steps of write, attention with weights and eviction: eager on a side stream, then captured twice and replayed
+    with other rows; both graphs of two caches at once beside eager calls."""
+    B, h, G, D, budget = 3, 2, 4, 128, 64 * 8
+
+    def fresh(seed):
+        return _filled([64 * 8 - 1, 500, 64 * 8], h, D, torch.bfloat16, stride=10, grow=10, seed=seed)[0]
+
+    c = fresh(0)
+    mass = c.new_mass()
+    q = torch.zeros(B, 1, h * G, D, dtype=torch.bfloat16, device=DEV)
+    k, v = (torch.zeros(B, 1, h, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+
+    def step(c, mass):
+        c.lens.add_(1)
+        rdkv.rdkv_q8_write(c, k, v)
+        out, lse = rdkv.rdkv_q8_attn(c, q, mass=mass)
+        kept = rdkv.rdkv_q8_evict(c, mass, budget, n_first=2, n_last=100)
+        c.lens.clamp_(max=budget)
+        return out, lse, kept
+
+    def twin(c, mass):
+        return rdkv.Q8Cache(B, h, D, 640, DEV, pages=c.pages.clone(), scales=c.scales.clone(), page_table=c.page_table,
+                            lens=c.lens.clone()), mass.clone()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(c, mass)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = step(c, mass)
+        graphs.append((g, got))
+    ref, ref_mass = twin(c, mass)
+    torch.cuda.synchronize()
+    for i in range(6):
+        q.copy_(_rows(B, h * G, D, torch.bfloat16, 100 + i).view(q.shape))
+        k.copy_(_rows(B, h, D, torch.bfloat16, 200 + i).view(k.shape))
+        v.copy_(_rows(B, h, D, torch.bfloat16, 300 + i).view(k.shape))
+        g, got = graphs[i % 2]
+        g.replay()
+        want = step(ref, ref_mass)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(mass, ref_mass) and torch.equal(c.lens, ref.lens)
+        held = [rdkv.rdkv_q8_read(x, 512, dtype=torch.float32, out=tuple(torch.zeros(B, 512, h, D, device=DEV) for _ in "kv")) for x in (c, ref)]
+        assert all(torch.equal(a, b) for a, b in zip(*held))
+    # graphs of two caches at once, beside eager calls on a third stream
+    other, other_mass = twin(c, mass)
+    third, third_mass = twin(c, mass)
+    g2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g2):
+        got2 = step(other, other_mass)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(one):
+            graphs[0][0].replay()
+        with torch.cuda.stream(two):
+            g2.replay()
+        with torch.cuda.stream(side):
+            got3 = step(third, third_mass)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) and torch.equal(a, d) for a, b, d in zip(graphs[0][1], got2, got3))
+    assert torch.equal(mass, other_mass) and torch.equal(mass, third_mass)
+    assert rdkv.rdkv_q8_status(c) == rdkv.rdkv_q8_status(other) == rdkv.rdkv_q8_status(third) == 0
+
+
+@pytest.mark.parametrize("withhold", [1, 3])
+@pytest.mark.parametrize("dtype,out,D,G,T,lens", [("f16", "f16", 128, 3, 1, [64 * 30, 100, 0]), ("f16", "f16", 64, 4, 4, [64 * 200, 7]),
+                                                  ("f32", "f32", 128, 8, 1, [64 * 90 - 5] * 3)])
+def test_waits_that_run_out_are_reported_and_the_workspace_serves_on(withhold, dtype, out, D, G, T, lens):
+    import time
+    h = 2
+    c, held = _filled(lens, h, D, TYPES[dtype])
+    q = _rows(len(lens) * T, h * G, D, TYPES[dtype], 9).view(len(lens), T, h * G, D)
+    nb = rdkv.lib().rdkv_q8_attn_workspace_bytes(ctypes.byref(c.c), h * G, T, 0)
+    ws = torch.zeros(nb, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        o, lse = rdkv.rdkv_q8_timeout_selftest(c, q.to(DEV), out_dtype=TYPES[out], withhold=withhold, ws=ws)
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 5
+        with_status = rdkv.rdkv_q8_status(c)
+        assert with_status == rdkv.RDKV_ERR_TIMEOUT and rdkv.rdkv_q8_status(c) == 0
+        assert o.isfinite().all() and not lse.isnan().any()
+        assert (ws[:rdkv.Q8_COUNTER_BYTES] == 0).all()
+        o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), out_dtype=TYPES[out], ws=ws)
+        _check_attention(q, held, o, lse)
+    assert rdkv.rdkv_q8_status(c) == 0
+
+
+# ---------------------------------------------------------------- a run of them together
+def test_a_prompt_scored_evicted_and_decoded_at_a_budget():
+    """The prompt's weights from its scorer, its rows in the cache; brought down to a budget, then steps that write,
+    attend with weights and evict whenever a page more than the budget is held; merged with a TriZone cache's attention."""
+    w = synth.WORKLOADS["llama3b"].scaled(n_tokens=900, h_q=6, h_kv=2, window=64, batch=2)
+    q, k, v = (t.to(DEV) for t in synth.prefill_batch(w))
+    shape = rdkv.shape_of(q, k, w.window)
+    sc = rdkv.rdkv_score(shape, q, k, v)
+    c = rdkv.Q8Cache(w.batch, w.h_kv, w.head_dim, 960, DEV)
+    held = [Held(w.h_kv, w.head_dim) for _ in range(w.batch)]
+    _write(c, held, [x.cpu() for x in k], [x.cpu() for x in v])
+    mass = c.new_mass()
+    mass[..., :900] = sc["w_tok"]
+    budget = 400
+    _evicted(c, held, mass, budget, 4, 100)
+    for step in range(130):
+        qn, kn, vn = synth.decode_step(w, step)
+        for b in range(w.batch):
+            held[b].write(kn[b][None], vn[b][None])
+        c.lens.add_(1)
+        rdkv.rdkv_q8_write(c, kn[:, None].to(DEV), vn[:, None].to(DEV))
+        before = mass.clone()
+        out, lse = rdkv.rdkv_q8_attn(c, qn.to(DEV), mass=mass, out_dtype=torch.float32)
+        if step % 16 == 0:
+            _check_attention(qn[:, None], held, out[:, None], lse[:, None], mass, before)
+        if len(held[0].k) == budget + 64:
+            _evicted(c, held, mass, budget, 4, 100)
+    # joined with the attention over a compressed cache of the same prompt
+    al = rdkv.rdkv_allocate(shape, sc["g_tok"], sc["w_chan"], k, 2.5, 2.5)
+    zones = rdkv.rdkv_pack(shape, al["plan"], k, v, al["bits_tok"], al["bits_chan"], w.window)
+    outs, lses = torch.empty(2, *qn.shape, device=DEV), torch.empty(2, *qn.shape[:2], device=DEV)
+    rdkv.rdkv_decode_attn_lse(zones, qn.to(DEV), out=outs[0], lse=lses[0])
+    outs[1], lses[1] = out, lse
+    both, lse2 = rdkv.rdkv_merge_attn(outs, lses)
+    mo, ml = O.merge_attention(outs.cpu().numpy(), lses.cpu().numpy())
+    assert np.abs(both.cpu().numpy() - mo).max() <= 2e-3 and np.abs(lse2.cpu().numpy() - ml).max() <= 2e-3
+    assert rdkv.rdkv_q8_status(c) == 0
+
+
+@pytest.mark.parametrize("exponent", [20, 30, 60])
+@pytest.mark.parametrize("T", [1, 4])
+def test_equal_logits_of_any_size_share_the_weight_over_pages_of_different_scales(T, exponent):
+    """Every key the same: the mean of all values, however large the logit is beside the values' scales."""
+    D, n = 64, 64 * 5
+    for dtype in ("bf16", "f32"):
+        k = _rows(1, 1, D, torch.float32, 1).sign().expand(n, 1, D).to(TYPES[dtype])
+        v = _rows(n, 1, D, torch.float32, 2)
+        for p in range(5):
+            v[64 * p:64 * p + 64] *= 2.0 ** (3 - 4 * p)
+        c = _cache([n], 1, D)
+        held = [Held(1, D)]
+        _write(c, held, [k], [v.to(TYPES[dtype])])
+        q = (_rows(T, 3, D, torch.float32, 3).sign() * 2.0 ** exponent).to(TYPES[dtype]).view(1, T, 3, D)
+        mass = c.new_mass()
+        o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+        for t in range(T):
+            m = n - T + t + 1
+            mean = torch.from_numpy(held[0].v[:m, 0].mean(0))
+            # (weights are exactly equal: the roundings of the sums and of the output)
+            tol = (68 * 2.0 ** -23 + 2 * n * 2.0 ** -24) * held[0].v.max() + torch.finfo(o.dtype).eps / 2 * mean.abs()
+            assert ((o[0, t].double().cpu() - mean).abs() <= tol).all()
+        assert lse.isfinite().all() and abs(float(mass.double().sum()) / (3 * T) - 1) < 1e-4
