@@ -40,14 +40,14 @@ struct AttnArgs {
   const void* q;
   void* out;
   float* lse;
-  float* logits;     // or NULL; [units][64 page_stride][pad]: base 2, of every row of a unit
+  float* logits;     // or NULL; [units][page_stride][rows][64]: base 2
   float2* stats;     // (with logits) each query row's reference (base 2) and sum of weights
   float* heads;      // [grid * NW] partials: pieces of units that end inside a warp's run
   float* parts;      // [grid * 2] partials: a block's part of a unit that began before it, of one that goes on
   int32_t* tickets;  // [units] blocks that have written their part
   int64_t q_stride;
   int dtype, out_dtype, n_q, G, chunk, n_chunks;  // chunk: query tokens of a unit
-  int pad;                // rows of a unit, rounded up to an even number
+  int rows;               // of a unit at most
   int withhold;           // 0, or (the self-test) pages with (index + KV head) % withhold == 0 are waited for, not copied
   long long wait_cycles;  // limit of a wait for a page
 };
@@ -289,7 +289,7 @@ struct Warp {
     uint32_t hi[kPage / 16][kCols ? 2 : 4], low[PREC ? kPage / 16 : 1][2];
   };
   // cut (the same in all lanes): some tokens of the page are hidden from some rows: row n sees see[n] of them.
-  __device__ __forceinline__ void weigh(Logits& s, float2 page, int g, int qd, bool cut, const int (&see)[2], float* store, int pad,
+  __device__ __forceinline__ void weigh(Logits& s, float2 page, int g, int qd, bool cut, const int (&see)[2], float* store, int rows,
                                         Weights& p) {
     const float f = (float)exponent(page.y);
     float sc[2] = {scale[0] * page.x, scale[1] * page.x};
@@ -304,15 +304,15 @@ struct Warp {
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
         if constexpr (kCols) {
-          if (2 * qd < pad) {
-            float2* to = reinterpret_cast<float2*>(store + (16 * i + g) * pad + 2 * qd);
-            to[0] = make_float2(__fmul_rn(s.c[i][0], sc[0]), __fmul_rn(s.c[i][1], sc[1]));
-            to[4 * pad] = make_float2(__fmul_rn(s.c[i][2], sc[0]), __fmul_rn(s.c[i][3], sc[1]));
-          }
-        } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (g + 8 * (e >> 1) < pad) store[token_of(i, e, g, qd) * pad + g + 8 * (e >> 1)] = __fmul_rn(s.c[i][e], sc[e >> 1]);
+            if (2 * qd + (e & 1) < rows) store[(2 * qd + (e & 1)) * kPage + token_of(i, e, g, qd)] = __fmul_rn(s.c[i][e], sc[e & 1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+            if (g + 4 * e < rows)
+              *reinterpret_cast<float2*>(store + (g + 4 * e) * kPage + token_of(i, e, g, qd)) =
+                  make_float2(__fmul_rn(s.c[i][e], sc[e >> 1]), __fmul_rn(s.c[i][e + 1], sc[e >> 1]));
         }
       }
     }
@@ -478,6 +478,14 @@ struct Warp {
   }
 };
 
+// Adds a piece (its reference m, sum of weights l and four of its sums y) to those of a row, whose reference is top.  (A piece
+// without a reference may hold NaN, and keeps it.)
+__device__ __forceinline__ void add_piece(float4& o, float& sum, float top, float m, float l, float4 y) {
+  const float f = m == -INFINITY ? 0.0f : ex2(m - top);
+  sum = fmaf(f, l, sum);
+  o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+}
+
 // What a block knows of a piece it joins.
 struct Piece {
   int base, unit, items;  // the unit's first item, the unit, its items
@@ -504,7 +512,6 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   __shared__ uint32_t valid_s, start_s, end_s;
   __shared__ int total_s;
   __shared__ int last_s[2], first_s[2];
-  __shared__ uint8_t member_s[2 * NW];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, qd = lane % 4, H = a.c.h_kv;
   uint8_t* ring = smem + (size_t)warp * S::kRing;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * NS;
@@ -613,6 +620,11 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     }
     __syncwarp();
   };
+  // With logits to keep, pages leave the L2 first: the launch that follows reads the logits, and each page is read once (or, by
+  // several chunks of queries, at about the same time).
+  uint64_t policy;
+  if (a.logits) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
   // Copies half x of the run (the keys of item x / 2, or its values) into the stage that it falls in.
   auto issue = [&](int x, int stage) {
     const int i = x / 2;
@@ -626,9 +638,9 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       } else {
         const uint8_t* src = a.c.pages + (int64_t)e.x * L::kBytes + (x & 1) * L::kHalf;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(L::kHalf) : "memory");
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
                          smem_u32(ring + stage * L::kHalf)),
-                     "l"(src), "r"(L::kHalf), "r"(bar)
+                     "l"(src), "r"(L::kHalf), "r"(bar), "l"(policy)
                      : "memory");
       }
     }
@@ -700,8 +712,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       asm volatile("cp.async.wait_all;" ::: "memory");  // the scales
       __syncwarp();
       const float2 sc = scales[i % kInfo];
-      float* store = a.logits ? a.logits + ((int64_t)e.z * a.c.page_stride * kPage + (int64_t)e.y * kPage) * a.pad : nullptr;
-      w.weigh(s, sc, g, qd, cut, see, store, a.pad, pw);
+      float* store = a.logits ? a.logits + ((int64_t)e.z * a.c.page_stride + e.y) * a.rows * kPage : nullptr;
+      w.weigh(s, sc, g, qd, cut, see, store, un.rows, pw);
     }
     if (!__all_sync(0xffffffffu, wait_for(bars + stage, turn, a.wait_cycles))) {
       ok = false;
@@ -777,141 +789,173 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   __syncthreads();
 
   // ---- joining the block's pieces: runs of pieces of one unit, a run begins at a piece that holds its
-  // unit's first item, or at the block's first piece; a query row of a run a warp
+  // unit's first item, or at the block's first piece.  (Short loops: the code is fetched once a call, and what unrolling
+  // saves is less than the fetch of more of it.)
   const uint32_t valid = valid_s, ends = end_s, begins = start_s;
   const uint32_t starts = begins | (valid & (0u - valid));
-  if (tid < 2 * NW && (valid >> tid & 1)) member_s[__popc(valid & ((1u << tid) - 1u))] = (uint8_t)tid;
-  __syncthreads();
-  int open[2] = {-1, -1};  // pieces of runs that are a part of their unit: one that began before the block, one that goes on
-  auto block_of = [&](int64_t item) { return quotient((item + 1) * nb - 1, total); };
-  int task = 0;
+  int open0 = -1, open1 = -1;  // pieces of runs that are a part of their unit: one that began before the block, one that goes on
+#pragma unroll 1
   for (uint32_t left = starts; left; left &= left - 1) {
     const int s = __ffs(left) - 1;
     const uint32_t rest = left & (left - 1), members = valid & ~((1u << s) - 1u) & (rest ? (rest & (0u - rest)) - 1u : 0xffffffffu);
-    const bool whole = (begins >> s & 1) && (ends & members);
-    const Piece pc = piece_s[s];
-    const int slot = begins >> s & 1, n = __popc(members), first = __popc(valid & ((1u << s) - 1u));
-    const Unit ru = unit_at(a, pc.unit);
+    const int slot = begins >> s & 1;
+    const bool whole = slot && (ends & members);
+    const Unit ru = unit_at(a, piece_s[s].unit);
     float* part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * P::kFloats;
-    auto src = [&](int j) -> const float* {
-      const int e = member_s[first + j];
-      return e & 1 ? reinterpret_cast<const float*>(smem + (size_t)(e / 2) * S::kRing)
-                   : a.heads + ((int64_t)blockIdx.x * NW + e / 2) * P::kFloats;
-    };
-    for (int row = 0; row < ru.rows; ++row) {
-      if (task++ % NW != warp) continue;
-      float4 o;
-      float m, l;
-      const int ch = 4 * lane % D;
-      join_row<8>(
-          n, lane, [&](int j) { return src(j)[P::kRows * D + row]; }, [&](int j) { return src(j)[P::kRows * (D + 1) + row]; },
-          [&](int j) { return *reinterpret_cast<const float4*>(src(j) + row * D + ch); }, o, m, l);
+#pragma unroll 1
+    for (int i = tid; i < ru.rows * (D / 4); i += 32 * NW) {
+      const int row = i / (D / 4), ch = i % (D / 4) * 4;
+      auto src = [&](uint32_t m) -> const float* {
+        const int e = __ffs(m) - 1;
+        return e & 1 ? reinterpret_cast<const float*>(smem + (size_t)(e / 2) * S::kRing) : a.heads + ((int64_t)blockIdx.x * NW + e / 2) * P::kFloats;
+      };
+      float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+      for (uint32_t x = members; x; x &= x - 1) m = fmaxf(m, src(x)[P::kRows * D + row]);
+      float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+      for (uint32_t x = members; x; x &= x - 1) {
+        const float* y = src(x);
+        add_piece(o, l, m, y[P::kRows * D + row], y[P::kRows * (D + 1) + row], *reinterpret_cast<const float4*>(y + row * D + ch));
+      }
       if (whole) {
         const int64_t at = row_at(a, ru, row);
-        if (4 * lane < D) put4(a, at * D + ch, scaled(o, l));
-        if (lane == 0) put_lse(a, at, m, l);
+        put4(a, at * D + ch, scaled(o, l));
+        if (ch == 0) put_lse(a, at, m, l);
       } else {
-        if (4 * lane < D) *reinterpret_cast<float4*>(part + row * D + ch) = o;
-        if (lane == 0) part[P::kRows * D + row] = m, part[P::kRows * (D + 1) + row] = l;
+        *reinterpret_cast<float4*>(part + row * D + ch) = o;
+        if (ch == 0) part[P::kRows * D + row] = m, part[P::kRows * (D + 1) + row] = l;
       }
     }
-    if (!whole) open[slot] = s;
+    if (!whole) (slot ? open1 : open0) = s;
   }
   // ---- joining the blocks' parts: the last block of a unit to arrive does it
-  if (open[0] < 0 && open[1] < 0) return;
+  if (open0 < 0 && open1 < 0) return;
   __syncthreads();
-  if (tid < 2 && open[tid] >= 0) {
-    const Piece pc = piece_s[open[tid]];
-    const int first = block_of(pc.base), n = block_of(pc.base + pc.items - 1) - first + 1;
-    int32_t* t = a.tickets + pc.unit;
-    int before;
-    asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(t) : "memory");
-    const bool last = before == n - 1;
-    if (last) *t = 0;
-    last_s[tid] = last ? n : 0;
-    first_s[tid] = first;
+  auto block_of = [&](int64_t item) { return quotient((item + 1) * nb - 1, total); };
+  if (tid < 2) {
+    const int e = tid ? open1 : open0;
+    int n = 0;
+    if (e >= 0) {
+      const Piece pc = piece_s[e];
+      const int first = block_of(pc.base);
+      n = block_of(pc.base + pc.items - 1) - first + 1;
+      int32_t* t = a.tickets + pc.unit;
+      int before;
+      asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(t) : "memory");
+      if (before == n - 1) *t = 0;
+      else n = 0;
+      first_s[tid] = first;
+    }
+    last_s[tid] = n;
   }
   __syncthreads();
 #pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
-    const int e = slot ? open[1] : open[0];
-    if (e < 0 || last_s[slot] == 0) continue;
-    const int unit = piece_s[e].unit, n = last_s[slot], first = first_s[slot];
-    const Unit ru = unit_at(a, unit);
-    for (int row = warp; row < ru.rows; row += NW) {
-      // the unit's first block wrote it as the unit that goes on, the others as the one that began before
-      auto part = [&](int j) { return a.parts + ((int64_t)(first + j) * 2 + (j == 0 ? 1 : 0)) * P::kFloats; };
-      float4 o;
-      float m, l;
-      const int ch = 4 * lane % D;
-      join_row<16>(
-          n, lane, [&](int j) { return __ldcg(part(j) + P::kRows * D + row); },
-          [&](int j) { return __ldcg(part(j) + P::kRows * (D + 1) + row); },
-          [&](int j) { return __ldcg(reinterpret_cast<const float4*>(part(j) + row * D + ch)); }, o, m, l);
+    const int n = last_s[slot];
+    if (n == 0) continue;
+    const Unit ru = unit_at(a, piece_s[slot ? open1 : open0].unit);
+    // the unit's first block wrote it as the unit that goes on, the others as the one that began before
+    const float* parts = a.parts + (int64_t)first_s[slot] * 2 * P::kFloats;
+#pragma unroll 1
+    for (int i = tid; i < ru.rows * (D / 4); i += 32 * NW) {
+      const int row = i / (D / 4), ch = i % (D / 4) * 4;
+      constexpr int kAhead = 10;  // parts whose loads are under way together
+      float4 o = make_float4(0, 0, 0, 0);
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+      for (int j0 = 0; j0 < n; j0 += kAhead) {
+        float m[kAhead], l[kAhead];
+        float4 y[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const float* part = parts + (int64_t)(2 * (j0 + j) + (j0 + j == 0 ? 1 : 0)) * P::kFloats;
+          const bool real = j0 + j < n;
+          m[j] = real ? __ldcg(part + P::kRows * D + row) : -INFINITY;
+          l[j] = real ? __ldcg(part + P::kRows * (D + 1) + row) : 0.0f;
+          y[j] = real ? __ldcg(reinterpret_cast<const float4*>(part + row * D + ch)) : make_float4(0, 0, 0, 0);
+        }
+        float now = top;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) now = fmaxf(now, m[j]);
+        const float4 was = o;
+        const float had = sum, ref = top;
+        o = make_float4(0, 0, 0, 0), sum = 0.0f, top = now;
+        add_piece(o, sum, now, ref, had, was);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) add_piece(o, sum, now, m[j], l[j], y[j]);
+      }
       const int64_t at = row_at(a, ru, row);
-      if (4 * lane < D) put4(a, at * D + ch, scaled(o, l));
-      if (lane == 0) put_lse(a, at, m, l);
+      put4(a, at * D + ch, scaled(o, sum));
+      if (ch == 0) put_lse(a, at, top, sum);
     }
   }
 }
 
 // ---------------------------------------------------------------- the keys' weights
 // mass_t += sum over the query rows that see t of 2^(logit - reference) / sum, chunk after chunk and row after row.
-// A thread a position, kMassThreads positions of a (sequence, KV head) a block at a time.
-constexpr int kMassThreads = 128;
+// A thread two positions of a (sequence, KV head); the loads of eight rows under way together, the first with the rows'
+// statistics, the weights so far and the page table.
+constexpr int kMassThreads = 128, kMassKeys = 2 * kMassThreads;
 constexpr int kMassRows = kMaxQueries * 8;
 __global__ void __launch_bounds__(kMassThreads) mass_kernel(AttnArgs a, float* mass, int64_t mass_stride) {
   __shared__ float2 stat_s[kMassRows];
   after_previous();
-  const int H = a.c.h_kv, rows = a.n_q * a.G;
-  const int64_t tiles = ((int64_t)a.c.page_stride * kPage + kMassThreads - 1) / kMassThreads, total = tiles * a.c.batch * H;
-  for (int64_t n = blockIdx.x; n < total; n += gridDim.x) {
-    const int bh = (int)(n / tiles), b = bh / H, h = bh - b * H;
-    const int64_t t0 = n % tiles * kMassThreads;
-    const int held = held_tokens(a.c, b);
-    if (t0 >= held) continue;
-    // (a wait that ran out: the logits are not all there)
-    if (fetch(a.c.status) == RDKV_ERR_TIMEOUT) return;
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows; i += kMassThreads) {
-      const int t = i / a.G;
-      const uint2 w = fetch(reinterpret_cast<const uint2*>(a.stats + (((int64_t)b * a.n_q + t) * H + h) * a.G + i - t * a.G));
-      const float l = __uint_as_float(w.y);
-      stat_s[i] = make_float2(__uint_as_float(w.x), l > 0.0f && l < INFINITY ? 1.0f / l : 0.0f);
-    }
-    __syncthreads();
-    const int64_t t = t0 + threadIdx.x;
-    if (t >= held) continue;
-    const int page = fetch(a.c.page_table + (int64_t)b * a.c.page_stride + t / kPage);
-    if (page < 0 || page >= a.c.n_pages) continue;  // nothing was attended there
-    float sum = 0.0f;
-    for (int c = 0; c < a.n_chunks; ++c) {
-      if (t >= seen_by(a, b, c)) continue;
-      const float* u = a.logits + ((((int64_t)b * a.n_chunks + c) * H + h) * a.c.page_stride * kPage + t) * a.pad;
-      const float2* st = stat_s + c * a.chunk * a.G;
-      const int m = min(a.chunk, a.n_q - c * a.chunk) * a.G;
-      for (int r = 0; r < m; r += 2) {
-        const uint2 w = fetch(reinterpret_cast<const uint2*>(u + r));
-        const float2 s0 = st[r];
-        if (s0.y > 0.0f) sum = fmaf(ex2(__uint_as_float(w.x) - s0.x), s0.y, sum);
-        if (r + 1 < m) {
-          const float2 s1 = st[r + 1];
-          if (s1.y > 0.0f) sum = fmaf(ex2(__uint_as_float(w.y) - s1.x), s1.y, sum);
+  const int H = a.c.h_kv, rows = a.n_q * a.G, tid = threadIdx.x;
+  const int tiles = ceil_div(a.c.page_stride, kMassKeys / kPage), bh = blockIdx.x / tiles, b = bh / H, h = bh - b * H;
+  const int t = (int)(blockIdx.x % tiles) * kMassKeys + 2 * tid, held = held_tokens(a.c, b);
+  if (t - 2 * tid >= held) return;
+  const bool real = t < held;
+  float* to = mass + ((int64_t)b * H + h) * mass_stride + t;
+  // (a wait that ran out: the logits are not all there; a page outside the pool: nothing was attended there)
+  const int page = real ? fetch(a.c.page_table + (int64_t)b * a.c.page_stride + t / kPage) : -1, status = fetch(a.c.status);
+  const uint2 had = real ? fetch(reinterpret_cast<const uint2*>(to)) : make_uint2(0, 0);
+  constexpr int kAhead = 8;
+  uint2 w[kAhead];
+  auto load = [&](int c, int r0, int m, int seen) {
+    const float* u = a.logits + (((((int64_t)b * a.n_chunks + c) * H + h) * a.c.page_stride + t / kPage) * a.rows + r0) * kPage + t % kPage;
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r)
+      w[r] = t < seen && r0 + r < m ? fetch(reinterpret_cast<const uint2*>(u + r * kPage)) : make_uint2(0xff800000u, 0xff800000u);
+  };
+  auto rows_of = [&](int c) { return min(a.chunk, a.n_q - c * a.chunk) * a.G; };
+  load(0, 0, rows_of(0), seen_by(a, b, 0));
+  for (int i = tid; i < rows; i += kMassThreads) {
+    const int q = i / a.G;
+    const uint2 x = fetch(reinterpret_cast<const uint2*>(a.stats + (((int64_t)b * a.n_q + q) * H + h) * a.G + i - q * a.G));
+    const float l = __uint_as_float(x.y);
+    stat_s[i] = make_float2(__uint_as_float(x.x), l > 0.0f && l < INFINITY ? 1.0f / l : 0.0f);
+  }
+  __syncthreads();
+  float2 sum = make_float2(0.0f, 0.0f);
+  for (int c = 0; c < a.n_chunks; ++c) {
+    const int m = rows_of(c), seen = seen_by(a, b, c);
+    const float2* st = stat_s + c * a.chunk * a.G;
+#pragma unroll 1
+    for (int r0 = 0; r0 < m; r0 += kAhead) {
+      if (c || r0) load(c, r0, m, seen);
+#pragma unroll
+      for (int r = 0; r < kAhead; ++r) {
+        const float2 s = r0 + r < m ? st[r0 + r] : make_float2(0.0f, 0.0f);
+        if (s.y > 0.0f) {
+          sum.x = fmaf(ex2(__uint_as_float(w[r].x) - s.x), s.y, sum.x);
+          sum.y = fmaf(ex2(__uint_as_float(w[r].y) - s.x), s.y, sum.y);
         }
       }
     }
-    float* to = mass + ((int64_t)b * H + h) * mass_stride + t;
-    *to = __uint_as_float(fetch(reinterpret_cast<const uint32_t*>(to))) + sum;
   }
+  if (page < 0 || page >= a.c.n_pages || status == RDKV_ERR_TIMEOUT) return;
+  if (t + 1 < held) *reinterpret_cast<float2*>(to) = make_float2(__uint_as_float(had.x) + sum.x, __uint_as_float(had.y) + sum.y);
+  else *to = __uint_as_float(had.x) + sum.x;
 }
 
 // ---------------------------------------------------------------- launch
 // The workspace has the same places for every shape, so that calls of any shape may follow one another: the
 // tickets, then pieces of the largest variant; last, for calls with mass, the rows' statistics and the logits.
-constexpr int kMaxWarps = 12;
+constexpr int kMaxWarps = 8;
 
 struct Geometry {
-  int chunk, n_chunks, nt, grid, pad;
+  int chunk, n_chunks, nt, grid, rows;
   size_t heads_at, parts_at, stats_at, logits_at, bytes;
 };
 
@@ -922,15 +966,15 @@ static Geometry geometry(const rdkv_q8_cache* c, int h_q, int n_q, bool prec, bo
   // registers hold two parts of queries and weights)
   o.chunk = std::min(n_q, std::max(1, (prec ? 8 : 16) / G));
   o.n_chunks = ceil_div(n_q, o.chunk);
-  o.nt = o.chunk * G > 8 ? 2 : 1;
-  o.pad = (o.chunk * G + 1) / 2 * 2;
+  o.rows = o.chunk * G;
+  o.nt = o.rows > 8 ? 2 : 1;
   o.grid = num_sms();
   const int64_t part = 4LL * Partial<128, 2>::kFloats;
   o.heads_at = kCounterBytes;
   o.parts_at = o.heads_at + (size_t)align_up((int64_t)o.grid * kMaxWarps * part, 256);
   o.stats_at = o.parts_at + (size_t)align_up(2LL * o.grid * part, 256);
   o.logits_at = o.stats_at + (with_mass ? (size_t)align_up(8LL * c->batch * n_q * h_q, 256) : 0);
-  o.bytes = o.logits_at + (with_mass ? 4ull * c->batch * c->h_kv * o.n_chunks * o.pad * c->page_stride * kPage : 0);
+  o.bytes = o.logits_at + (with_mass ? 4ull * c->batch * c->h_kv * o.n_chunks * o.rows * c->page_stride * kPage : 0);
   return o;
 }
 
@@ -987,16 +1031,15 @@ static rdkv_status attn_impl(const rdkv_q8_cache* cache, int32_t dtype, const vo
   const AttnArgs a{q8::view_of(cache), q, out, lse, mass ? reinterpret_cast<float*>(w + geo.logits_at) : nullptr,
                    mass ? reinterpret_cast<float2*>(w + geo.stats_at) : nullptr, reinterpret_cast<float*>(w + geo.heads_at),
                    reinterpret_cast<float*>(w + geo.parts_at), reinterpret_cast<int32_t*>(w), q_stride, dtype, out_dtype, n_q,
-                   h_q / cache->h_kv, geo.chunk, geo.n_chunks, geo.pad, withhold, wait_cycles};
+                   h_q / cache->h_kv, geo.chunk, geo.n_chunks, geo.rows, withhold, wait_cycles};
   cudaStream_t cs = (cudaStream_t)stream;
   const bool wide = cache->head_dim == 128;
-  if (prec) st = (wide ? launch<128, 1, true, 12, 2> : launch<64, 1, true, 12, 4>)(a, geo.grid, cs);
+  if (prec) st = (wide ? launch<128, 1, true, 7, 3> : launch<64, 1, true, 7, 6>)(a, geo.grid, cs);
   else if (geo.nt == 2) st = (wide ? launch<128, 2, false, 8, 3> : launch<64, 2, false, 8, 6>)(a, geo.grid, cs);
-  else st = (wide ? launch<128, 1, false, 12, 2> : launch<64, 1, false, 12, 4>)(a, geo.grid, cs);
+  else st = (wide ? launch<128, 1, false, 7, 3> : launch<64, 1, false, 7, 6>)(a, geo.grid, cs);
   if (st != RDKV_OK || !mass) return st;
-  const int64_t tiles = ceil_div64((int64_t)cache->page_stride * kPage, kMassThreads) * cache->batch * cache->h_kv;
-  RDKV_TRY_CUDA(launch_after(mass_kernel, dim3((unsigned)std::min<int64_t>(tiles, (int64_t)num_sms() * 16)), kMassThreads, 0, cs, a, mass,
-                             mass_stride),
+  const int64_t tiles = (int64_t)ceil_div(cache->page_stride, kMassKeys / kPage) * cache->batch * cache->h_kv;  // (no more than items)
+  RDKV_TRY_CUDA(launch_after(mass_kernel, dim3((unsigned)tiles), kMassThreads, 0, cs, a, mass, mass_stride),
                 "8-bit cache weights");
   count_launch();
   return RDKV_OK;
