@@ -784,9 +784,9 @@ rdkv_status rdkv_q8_timeout_selftest(const rdkv_q8_cache* cache, int32_t dtype, 
  * 0 <= n_first, 0 <= n_last, n_first + n_last <= n_keep, 1 <= n_keep.  No page of
  * a sequence that is brought down may be shared with another sequence.  A
  * sequence with a page outside the pool (RDKV_ERR_INVALID_ARG in *status) is left as
- * it is, rows and mass, and its kept are -1.  ws: rdkv_q8_evict_workspace_bytes bytes,
- * 16-byte aligned, nothing in it needs to be zero; calls that may run at the
- * same time need one each.  Two launches. */
+ * it is, rows and mass, and its kept are -1.  ws as for rdkv_q8_attn, of
+ * rdkv_q8_evict_workspace_bytes bytes: calls of both may follow one another on it.
+ * Two launches. */
 size_t rdkv_q8_evict_workspace_bytes(const rdkv_q8_cache* cache);
 rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, int64_t mass_stride, int32_t n_keep, int32_t n_first,
                           int32_t n_last, int32_t* kept, void* ws, size_t ws_bytes, void* stream);

@@ -2,11 +2,11 @@
 //
 // Choice.  Of a (sequence, KV head) with more than n_keep tokens the n_keep - n_first - n_last largest weights
 // between the first and the last are found by their digits: a weight's bits, turned into a number of the same order, eight
-// bits a pass from the top, each pass counting the candidates by digit.  The row is spread over a cluster of blocks;
-// their counts meet through distributed shared memory, so that one launch does all passes without a trip
-// through global memory between them.  Counts lie in 32 columns, a lane its own, so that lanes that meet the same digit
-// (most do: weights share few exponents) do not wait for one another.  Of the weights equal to the last one kept, the
-// lowest positions are.
+// bits a pass from the top, each pass counting the candidates by digit.  The row is spread over a cluster of blocks, which
+// hold its weights in shared memory; their counts meet through distributed shared memory, so that one launch does all
+// passes without a trip through global memory.  Counts lie in 32 columns, a lane its own, so that lanes that meet the
+// same digit (most do: weights share few exponents) do not wait for one another.  Of the weights equal to the last one
+// kept, the lowest positions are.
 //
 // Move.  A kept row goes to a place at or below its own.  The pages of a row are taken in ascending order, each by one
 // block (a ticket says which: blocks that wait do so for lower tickets, which have started): it reads its
@@ -25,14 +25,16 @@ struct EvictArgs {
   int64_t mass_stride;
   int n_keep, n_first, n_last;
   int32_t* kept;
-  int32_t* ranks;   // [batch * h_kv][page_stride + 1]: rows kept before each page
+  int2* from;       // [batch * h_kv][n_keep]: the (page, head) that a kept row lies in, and its slot and scales (how_of)
   int32_t* flags;   // [batch * h_kv][page_stride]: 1: the page's rows have been read
-  int2* todo;       // [batch * h_kv * page_stride] (sequence * h_kv + head, page): the pages to move, ascending in a row
-  int32_t* ticket;  // [1] pages taken
+  int2* waits;      // [batch * h_kv][page_stride]: the first and last lower page that has rows of a page
+  int2* todo;       // [count] the pages to fill, (sequence, head) and page, ascending in a row
+  int32_t* count;   // pages to fill, pages taken, blocks done: zero between the calls
 };
 
+constexpr int kStay = -2;  // in a page's place: it stays
 constexpr int kPickThreads = 512;
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128, kMoveBlocks = 8;  // an SM
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -62,95 +64,107 @@ __device__ __forceinline__ uint32_t order_of(uint32_t w) {
   return w & 0x80000000u ? ~w : w | 0x80000000u;
 }
 
-// Pages that sequence b holds.
-__device__ __forceinline__ int pages_of(const PageView& v, int b) { return ceil_div(held_tokens(v, b), kPage); }
+// A row's slot and its page's scales' exponents, in a word.
+__device__ __forceinline__ int how_of(int slot, uint2 scales) {
+  auto e = [](uint32_t s) { return min(max(exponent(__uint_as_float(s)), kLowExp), kHighExp) - kLowExp; };
+  return slot | e(scales.x) << 8 | e(scales.y) << 16;
+}
+__device__ __forceinline__ int slot_of(int how) { return how & 63; }
+__device__ __forceinline__ float key_scale(int how) { return two_to((how >> 8 & 31) + kLowExp); }
+__device__ __forceinline__ float value_scale(int how) { return two_to((how >> 16 & 31) + kLowExp); }
+// The two words of a page's weights that are this lane's; past the row: not used.
+__device__ __forceinline__ uint2 weights_of(const float* mass, int p, int lane) {
+  return fetch(reinterpret_cast<const uint2*>(mass + (int64_t)p * kPage + 2 * lane));
+}
 
 // A cluster a (sequence, KV head); a warp has a run of the row's pages, a lane two positions of each.
-__global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a) {
+constexpr int kMaxBlocks = 8;  // of a cluster, everywhere
+constexpr int kHold = 16;      // pages of a warp whose weights shared memory holds; those of longer rows are loaded again
+// (Short loops: the code is fetched anew by every launch.  With the weights in registers and every loop unrolled, 30 KB of it, the
+// choice took 16 us for 32 rows of 3,000 tokens under the profiler.)
+__global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int hold) {
   constexpr int kWarps = kPickThreads / 32;
   __shared__ uint32_t count_s[256 * 32];  // by digit and lane
   __shared__ uint32_t block_s[256];       // this block's counts
   __shared__ uint32_t sum_s[256 / 32], digit_s, above_s, within_s;
   __shared__ uint2 warp_s[kWarps];        // a warp's rows kept for sure, and its candidates equal to the border
-  __shared__ uint32_t total_s[2];
+  __shared__ uint32_t total_s[2], first_s, base_s;
+  extern __shared__ uint2 held_s[];       // [warps][hold][32]
   after_previous();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const int row = blockIdx.x / size, H = a.c.h_kv, b = row / H, h = row - b * H;
   const int len = held_tokens(a.c, b), pages = ceil_div(len, kPage), stride = a.c.page_stride;
-  const float* mass = a.mass + (int64_t)row * a.mass_stride;
+  float* mass = a.mass + (int64_t)row * a.mass_stride;
+  const int32_t* table = a.c.page_table + (int64_t)b * stride;
   int32_t* kept = a.kept + (int64_t)row * a.n_keep;
-  int32_t* ranks = a.ranks + (int64_t)row * (stride + 1);
-  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
-  if (h == 0 && rank == 0 && tid == 0) check_length(a.c, b);
   const int part = rank * kWarps + warp, parts = size * kWarps;
   const int p0 = share(part, pages, parts), p1 = share(part + 1, pages, parts);
-  // where this row's pages are listed
-  int64_t base = 0;
-  for (int i = tid; i < b; i += kPickThreads) base += pages_of(a.c, i);
-  for (int d = 16; d; d >>= 1) base += __shfl_xor_sync(0xffffffffu, base, d);
+  uint2* held = held_s + (int64_t)warp * hold * 32 + lane;
+  if (len > a.n_keep) {
+#pragma unroll 4
+    for (int p = p0; p < min(p1, p0 + hold); ++p)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(held + (p - p0) * 32)), "l"(mass + (int64_t)p * kPage + 2 * lane) : "memory");
+  }
+  auto weights = [&](int p) { return p - p0 < hold ? held[(p - p0) * 32] : weights_of(mass, p, lane); };
+  if (h == 0 && rank == 0 && tid == 0) check_length(a.c, b);
   // a page outside the pool: the row stays
   bool bad = false;
   for (int p = tid; p < pages; p += kPickThreads) {
-    const int at = fetch(a.c.page_table + (int64_t)b * stride + p);
+    const int at = fetch(table + p);
     bad |= at < 0 || at >= a.c.n_pages;
   }
-  if (tid < 256) block_s[tid] = 0;
-  if (tid == 0) total_s[0] = total_s[1] = 0;
+  if (tid == 0) total_s[0] = total_s[1] = 0, first_s = 0x7fffffffu;
+  for (int i = tid; i < 256 * 32; i += kPickThreads) count_s[i] = 0;
   bad = __syncthreads_or(bad);
-  // (the lists' starts: over the warps)
-  if (lane == 0 && base) atomicAdd(&block_s[warp], (uint32_t)base);
-  __syncthreads();
-  base = 0;
-  for (int i = 0; i < kWarps; ++i) base += block_s[i];
-  base = base * H + (int64_t)h * pages;
-  __syncthreads();
-  int2* todo = a.todo + base;
-  const int part_of_all = rank * kPickThreads + tid, all = size * kPickThreads;
-  const bool stays = bad || len <= a.n_keep;  // (the same in the whole cluster)
-  if (stays) {
+  const int filled = ceil_div(a.n_keep, kPage), part_of_all = rank * kPickThreads + tid, all = size * kPickThreads;
+  if (bad || len <= a.n_keep) {  // (the same in the whole cluster)
     if (bad && part_of_all == 0) raise(a.c, RDKV_ERR_INVALID_ARG);
     for (int i = part_of_all; i < a.n_keep; i += all) kept[i] = !bad && i < len ? i : -1;
-    for (int p = part_of_all; p < pages; p += all) todo[p] = make_int2(-1, 0);
     return;
   }
-  for (int p = part_of_all; p < pages; p += all) a.flags[(int64_t)row * stride + p] = 0;
+  for (int p = part_of_all; p < filled; p += all) a.flags[(int64_t)row * stride + p] = 0;
+  asm volatile("cp.async.wait_all;" ::: "memory");  // (each thread reads what it asked for)
 
   // ---- the border: the need-th largest of the weights between the first and the last
   const int lo = a.n_first, hi = len - a.n_last;
   uint32_t need = a.n_keep - a.n_first - a.n_last, border = 0, mask = 0;
-  bool some = need > 0;
+  const bool some = need > 0;
 #pragma unroll 1
   for (int shift = 24; some && shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * 32; i += kPickThreads) count_s[i] = 0;
-    __syncthreads();
-    constexpr int kAhead = 4;
 #pragma unroll 1
-    for (int p = p0; p < p1; p += kAhead) {
-      uint2 w[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        w[i] = p + i < p1 ? fetch(reinterpret_cast<const uint2*>(mass + (int64_t)(p + i) * kPage + 2 * lane)) : make_uint2(0, 0);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int t = (p + i) * kPage + 2 * lane;
-        const uint32_t x = order_of(w[i].x), y = order_of(w[i].y);
-        if (p + i < p1 && t >= lo && t < hi && (x & mask) == border) atomicAdd(&count_s[(x >> shift & 255) * 32 + lane], 1u);
-        if (p + i < p1 && t + 1 >= lo && t + 1 < hi && (y & mask) == border) atomicAdd(&count_s[(y >> shift & 255) * 32 + lane], 1u);
-      }
+    for (int p = p0; p < p1; ++p) {
+      const uint2 w = weights(p);
+      const int t = p * kPage + 2 * lane;
+      const uint32_t x = order_of(w.x), y = order_of(w.y);
+      if (t >= lo && t < hi && (x & mask) == border) atomicAdd(&count_s[(x >> shift & 255) * 32 + lane], 1u);
+      if (t + 1 >= lo && t + 1 < hi && (y & mask) == border) atomicAdd(&count_s[(y >> shift & 255) * 32 + lane], 1u);
     }
     __syncthreads();
-    // a digit's count: its 32 columns, each thread from another one on (no bank conflicts)
-    for (int d = tid; d < 256; d += kPickThreads) {
+    // a digit's count: its 32 columns, each thread from another one on (no bank conflicts); cleared for the next pass
+    if (tid < 256) {
       uint32_t n = 0;
 #pragma unroll 8
-      for (int i = 0; i < 32; ++i) n += count_s[d * 32 + (i + tid) % 32];
-      block_s[d] = n;
+      for (int i = 0; i < 32; ++i) {
+        uint32_t* at = &count_s[tid * 32 + (i + tid) % 32];
+        n += *at;
+        *at = 0;
+      }
+      block_s[tid] = n;
     }
     cluster_sync();
     uint32_t n = 0;
-    if (tid < 256)  // digit 255 - tid: from the largest down
-      for (uint32_t r = 0; r < size; ++r) n += size > 1 ? remote(&block_s[255 - tid], r) : block_s[255 - tid];
+    if (tid < 256) {  // digit 255 - tid: from the largest down
+      if (size == 1) {
+        n = block_s[255 - tid];
+      } else {
+        uint32_t c[kMaxBlocks];
+#pragma unroll
+        for (int r = 0; r < kMaxBlocks; ++r) c[r] = r < size ? remote(&block_s[255 - tid], r) : 0;
+#pragma unroll
+        for (int r = 0; r < kMaxBlocks; ++r) n += c[r];
+      }
+    }
     uint32_t in = n;
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, in, o);
@@ -170,8 +184,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a) {
   }
   // kept are: the first, the last, what is above the border and, of what lies on it (under the mask), `need`
   // ---- how many of each before this warp's pages
-  auto classes = [&](int p, bool (&sure)[2], bool (&tie)[2]) {
-    const uint2 w = fetch(reinterpret_cast<const uint2*>(mass + (int64_t)p * kPage + 2 * lane));
+  auto classes = [&](int p, uint2 w, bool (&sure)[2], bool (&tie)[2]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = p * kPage + 2 * lane + i;
@@ -181,65 +194,74 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a) {
       tie[i] = open && some && x == border;
     }
   };
-  uint32_t n_sure = 0, n_tie = 0;
-#pragma unroll 4
+  uint32_t n_sure = 0, n_tie = 0, first = 0x7fffffffu;  // first: page of a row that may go
+#pragma unroll 1
   for (int p = p0; p < p1; ++p) {
     bool sure[2], tie[2];
-    classes(p, sure, tie);
+    classes(p, weights(p), sure, tie);
     n_sure += sure[0] + sure[1], n_tie += tie[0] + tie[1];
+    if (!(sure[0] && sure[1])) first = min(first, (uint32_t)p);
   }
+  first = __reduce_min_sync(0xffffffffu, first);
   n_sure = __reduce_add_sync(0xffffffffu, n_sure), n_tie = __reduce_add_sync(0xffffffffu, n_tie);
   if (lane == 0) {
     warp_s[warp] = make_uint2(n_sure, n_tie);
     atomicAdd(&total_s[0], n_sure), atomicAdd(&total_s[1], n_tie);
+    atomicMin(&first_s, first);
   }
   cluster_sync();
   uint32_t sure0 = 0, tie0 = 0;
-  for (uint32_t r = 0; r < rank; ++r) sure0 += remote(&total_s[0], r), tie0 += remote(&total_s[1], r);
+  {
+    uint32_t c[kMaxBlocks], d[kMaxBlocks], f[kMaxBlocks];
+#pragma unroll
+    for (int r = 0; r < kMaxBlocks; ++r) {
+      c[r] = r < rank ? remote(&total_s[0], r) : 0, d[r] = r < rank ? remote(&total_s[1], r) : 0;
+      f[r] = r < size ? remote(&first_s, r) : 0x7fffffffu;
+    }
+    first = f[0];
+#pragma unroll
+    for (int r = 0; r < kMaxBlocks; ++r) sure0 += c[r], tie0 += d[r], first = min(first, f[r]);
+  }
   for (int i = 0; i < warp; ++i) sure0 += warp_s[i].x, tie0 += warp_s[i].y;
-  cluster_sync();  // a block's shared memory outlives the others' reads
+  // (every row of a page before `first` stays where it is; some go, so there is one.  Behind it those of a page may still, where
+  // weights are equal to the border.)
+  if (rank == 0 && tid == 0) base_s = atomicAdd(a.count, max(0, filled - (int)first));
   // ---- their places
+  int2 *from = a.from + (int64_t)row * a.n_keep, *waits = a.waits + (int64_t)row * stride;
   uint32_t at = sure0 + min(tie0, need);
-#pragma unroll 2
+#pragma unroll 1
   for (int p = p0; p < p1; ++p) {
+    const int lies = fetch(table + p) * H + h;
+    const uint2 sc = fetch(reinterpret_cast<const uint2*>(a.c.scales + (int64_t)lies * 2));
     bool sure[2], tie[2];
-    classes(p, sure, tie);
-    const uint32_t before = (1u << lane) - 1u;
+    classes(p, weights(p), sure, tie);
+    const uint32_t below = (1u << lane) - 1u;
     const uint32_t t0 = __ballot_sync(0xffffffffu, tie[0]), t1 = __ballot_sync(0xffffffffu, tie[1]);
-    const uint32_t mine = tie0 + __popc(t0 & before) + __popc(t1 & before);
+    const uint32_t mine = tie0 + __popc(t0 & below) + __popc(t1 & below);
     const bool k0 = sure[0] || (tie[0] && mine < need), k1 = sure[1] || (tie[1] && mine + tie[0] < need);
     const uint32_t b0 = __ballot_sync(0xffffffffu, k0), b1 = __ballot_sync(0xffffffffu, k1);
-    const uint32_t to = at + __popc(b0 & before) + __popc(b1 & before);
-    const int t = p * kPage + 2 * lane;
-    if (k0) kept[to] = t;
-    if (k1) kept[to + k0] = t + 1;
+    const uint32_t to = at + __popc(b0 & below) + __popc(b1 & below);
+    const int t = p * kPage + 2 * lane, how = how_of(2 * lane, sc);
+    if (k0) kept[to] = t, from[to] = make_int2(lies, how);
+    if (k1) kept[to + k0] = t + 1, from[to + k0] = make_int2(lies, how + 1);
+    // a weight that goes and that no row's will take the place of (of the rows that stay the move sees to)
+    if (!k0 && t >= a.n_keep && t < len) mass[t] = 0.0f;
+    if (!k1 && t + 1 >= a.n_keep && t + 1 < len) mass[t + 1] = 0.0f;
     const uint32_t next = at + __popc(b0) + __popc(b1);
-    if (lane == 0) {
-      ranks[p] = at;
-      if (p == pages - 1) ranks[pages] = next;
-      // nothing to do where every row stays
-      todo[p] = at == (uint32_t)p * kPage && next == (uint32_t)min(len, (p + 1) * kPage) ? make_int2(-1, 0) : make_int2(row, p);
-    }
+    if (lane == 0 && p < filled)
+      waits[p] = at == (uint32_t)p * kPage && next == (uint32_t)(p + 1) * kPage
+                     ? make_int2(kStay, 0)  // nothing to do where every row stays
+                     : make_int2((int)(at / kPage), next > at ? min(p - 1, (int)((next - 1) / kPage)) : -1);
     at = next, tie0 += __popc(t0) + __popc(t1);
   }
+  // ---- the pages to fill
+  cluster_sync();
+  const uint32_t base = remote(&base_s, 0);
+  for (int p = max(p0, (int)first) + lane; p < min(p1, filled); p += 32)
+    a.todo[base + p - first] = make_int2(fetch(reinterpret_cast<const int32_t*>(waits + p)) == kStay ? kStay : row, p);
+  cluster_sync();  // a block's shared memory outlives the others' reads
 }
 
-// Loads past L1, in the order in which they stand: before the flag that says that they are done.
-__device__ __forceinline__ uint32_t fetch_l2(const float* p) {
-  uint32_t v;
-  asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 fetch_l2(const uint2* p) {
-  uint2 v;
-  asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 fetch_l2(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-  return v;
-}
 // The largest magnitude of four codes in a scale f, and top.
 __device__ __forceinline__ float largest(uint32_t w, float f, float top) {
   float x[4];
@@ -248,94 +270,124 @@ __device__ __forceinline__ float largest(uint32_t w, float f, float top) {
   for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(x[i]) * f);
   return top;
 }
+__device__ __forceinline__ void copy16(void* to, const uint8_t* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
 
+// A block takes a page in some 8 us, of which it waits for memory most, so what counts is how much is under way: the rows are
+// gathered into shared memory (24 KB a page at D = 128, the values' pairs with a half that is not used), eight pages an SM; and the
+// next page's ticket, place and rows are asked for while this one's codes are on their way.  With the codes in registers (four
+// pages an SM) 131,072 tokens of 8 heads brought down to a quarter took 75 us to move.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictArgs a) {
   using L = Layout<D>;
-  constexpr int kS = L::kSides, kKeys = kPage * D / 8 / kMoveThreads, kValues = kPage * D / 16 / kMoveThreads;
-  __shared__ int64_t from_s[kPage];   // a row's (page, head), -1: no row
-  __shared__ int slot_s[kPage];
-  __shared__ float2 scale_s[kPage];   // its scales
-  __shared__ uint32_t top_s[2][kMoveThreads / 32];
-  __shared__ int ticket_s, total_s;
+  constexpr int kS = L::kSides, kWarps = kMoveThreads / 32, kChunks = kPage * D / 16;  // of 16 bytes, in a page's half
+  __shared__ __align__(16) uint8_t keys_s[L::kHalf];
+  __shared__ __align__(16) uint8_t values_s[2][L::kHalf];  // the chunks that a pair's first and second token lie in
+  __shared__ int2 from_s[2][kPage];                        // a row's (page, head) and how it lies there; of this page and the next
+  __shared__ uint32_t top_s[2][kWarps], weight_s[kPage];
+  __shared__ int2 next_s;
   const int tid = threadIdx.x, H = a.c.h_kv, stride = a.c.page_stride;
   after_previous();
-  int total = 0;  // (the host has made sure that all rows' pages fit)
-  for (int i = tid; i < a.c.batch; i += kMoveThreads) total += pages_of(a.c, i) * H;
-  if (tid == 0) total_s = 0;
+  const int total = fetch(a.count);
+  constexpr int kNone = -1;
+  auto todo = [&](int ticket) { return ticket < total ? a.todo[ticket] : make_int2(kNone, 0); };
+  // this thread's row of a page: where it lies, and its position
+  auto look_up = [&](const int2& page, int2& lies, int& t) {
+    if (page.x >= 0 && tid < min(kPage, a.n_keep - page.y * kPage)) {
+      const int64_t at = (int64_t)page.x * a.n_keep + page.y * kPage + tid;
+      lies = a.from[at], t = a.kept[at];
+    }
+  };
+  if (tid == 0) next_s = todo(atomicAdd(a.count + 1, 1));
   __syncthreads();
-  if (total) atomicAdd(&total_s, total);
-  __syncthreads();
-  total = total_s;
+  int2 what = next_s, lies = make_int2(0, 0);
+  int t = 0;
+  look_up(what, lies, t);
+  bool ok = true;
 #pragma unroll 1
-  for (;;) {
-    if (tid == 0) ticket_s = atomicAdd(a.ticket, 1);
+  for (int turn = 0; what.x != kNone; turn ^= 1) {
+    const int2* from = from_s[turn];
+    const int row = what.x, p = what.y, n = row == kStay ? 0 : min(kPage, a.n_keep - p * kPage);  // rows that come here
+    if (tid < n) from_s[turn][tid] = lies;
     __syncthreads();
-    const int ticket = ticket_s;
-    if (ticket >= total) return;
-    const int2 what = *reinterpret_cast<const int2*>(a.todo + ticket);
-    if (what.x < 0) {
-      __syncthreads();  // (before the next ticket)
+    // The next ticket (no wait can run in a circle: of all pages taken the lowest whose rows have not been read belongs to a
+    // block whose present page is no higher, and whose wait is for lower ones).
+    int ticket = 0;
+    if (tid == 0) ticket = atomicAdd(a.count + 1, 1);
+    if (row == kStay) {
+      if (tid == 0) next_s = todo(ticket);
+      __syncthreads();
+      what = next_s;
+      look_up(what, lies, t);
       continue;
     }
-    const int row = what.x, p = what.y, b = row / H, h = row - b * H;
-    const int len = held_tokens(a.c, b);
-    const int32_t* kept = a.kept + (int64_t)row * a.n_keep;
-    const int32_t* ranks = a.ranks + (int64_t)row * (stride + 1);
-    const int32_t* table = a.c.page_table + (int64_t)b * stride;
     float* mass = a.mass + (int64_t)row * a.mass_stride;
-    const int n = max(0, min(kPage, a.n_keep - p * kPage));  // rows that come here
-    float m = 0.0f;
-    if (tid < kPage) {
-      int64_t from = -1;
-      if (tid < n) {
-        const int t = kept[p * kPage + tid];
-        from = (int64_t)table[t / kPage] * H + h;
-        slot_s[tid] = t % kPage;
-        const uint2 sc = fetch_l2(reinterpret_cast<const uint2*>(a.c.scales + from * 2));
-        scale_s[tid] = make_float2(__uint_as_float(sc.x), __uint_as_float(sc.y));
-        m = __uint_as_float(fetch_l2(mass + t));
-      }
-      from_s[tid] = from;
+    int32_t* flags = a.flags + (int64_t)row * stride;
+#pragma unroll 4
+    for (int u = tid; u < kChunks; u += kMoveThreads) {  // 16 channels of a token
+      const int t = u / (D / 16), j = u % (D / 16) / 4, c = u % 4 * 2;
+      const int2 f = from[t];
+      if (t < n) copy16(keys_s + L::key_at(t, j, c), a.c.pages + (int64_t)f.x * L::kBytes + L::key_at(slot_of(f.y), j, c));
     }
-    __syncthreads();
-    // the rows' codes: eight channels of a token of the keys, of a token pair of the values
-    uint2 kc[kKeys];
-    uint4 vc[kValues][2];
-    float top[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const int u = tid + i * kMoveThreads, t = u / (16 * kS) * 2 + u / 8 % 2;
-      kc[i] = t < n ? fetch_l2(reinterpret_cast<const uint2*>(a.c.pages + from_s[t] * L::kBytes + L::key_at(slot_s[t], u / 16 % kS, u % 8)))
-                    : make_uint2(0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kValues; ++i) {
-      const int u = tid + i * kMoveThreads, t = (u / (32 * kS) * 4 + u % 4) * 2, j = u / 32 % kS, g = u % 32 / 4;
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        vc[i][s] = t + s < n ? fetch_l2(reinterpret_cast<const uint4*>(a.c.pages + from_s[t + s] * L::kBytes + L::kHalf +
-                                                                     L::value_at(slot_s[t + s] / 2, j, g)))
-                             : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const int u = tid + i * kMoveThreads, t = u / (16 * kS) * 2 + u / 8 % 2;
-      const float f = t < n ? scale_s[t].x : 0.0f;
-      top[0] = largest(kc[i].x, f, largest(kc[i].y, f, top[0]));
-    }
-    uint2 vb[kValues][2];  // a token's eight codes
-#pragma unroll
-    for (int i = 0; i < kValues; ++i) {
-      const int u = tid + i * kMoveThreads, t = (u / (32 * kS) * 4 + u % 4) * 2;
+#pragma unroll 4
+    for (int u = tid; u < kChunks; u += kMoveThreads) {  // eight channels of a token pair
+      const int q = u / (32 * kS) * 4 + u % 4, j = u / 32 % kS, g = u % 32 / 4;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const bool real = t + s < n;
-        const uint32_t pick = real && (slot_s[t + s] & 1) ? 0x7531u : 0x6420u;
-        const uint4 w = vc[i][s];
-        vb[i][s] = make_uint2(__byte_perm(w.x, w.y, pick), __byte_perm(w.z, w.w, pick));
-        const float f = real ? scale_s[t + s].y : 0.0f;
-        top[1] = largest(vb[i][s].x, f, largest(vb[i][s].y, f, top[1]));
+        const int2 f = from[2 * q + s];
+        if (2 * q + s < n)
+          copy16(values_s[s] + 16 * u, a.c.pages + (int64_t)f.x * L::kBytes + L::kHalf + L::value_at(slot_of(f.y) / 2, j, g));
+      }
+    }
+    uint32_t m = 0;
+    if (tid < n) m = fetch(reinterpret_cast<const uint32_t*>(mass + t));
+    const int to = fetch(a.c.page_table + (int64_t)(row / H) * stride + p) * H + row % H;
+    const int2 wait = a.waits[(int64_t)row * stride + p];
+    // of the lower pages that have rows of theirs here: have they been read?
+    auto read = [&](int l) {
+      int seen;
+      asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(flags + l) : "memory");
+      return seen != 0;
+    };
+    bool seen = wait.x + tid > wait.y || read(wait.x + tid);
+    if (tid == 0) next_s = todo(ticket);
+    if (tid < n) {
+      weight_s[tid] = m;
+      if (t >= a.n_keep) mass[t] = 0.0f;  // (this row's alone)
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();  // every row and weight has been read
+    // (relaxed, here and above: what the flag tells are copies and loads that have ended; nothing that is written is read in
+    // this launch)
+    if (tid == 0) asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" ::"l"(flags + p), "r"(1) : "memory");
+    what = next_s;
+    look_up(what, lies, t);
+    float top[2] = {0.0f, 0.0f};
+#pragma unroll 2
+    for (int u = tid; u < kChunks; u += kMoveThreads) {
+      const int t = u / (2 * D / 16) * 2 + u / 4 % 2;  // (in the order of the page)
+      if (t >= n) continue;
+      const uint4 c = reinterpret_cast<const uint4*>(keys_s)[u];
+      const float f = key_scale(from[t].y);
+      top[0] = largest(c.x, f, largest(c.y, f, largest(c.z, f, largest(c.w, f, top[0]))));
+    }
+    // a token's eight codes of its chunk
+    auto codes_of = [&](int u, int s, int how) {
+      const uint32_t pick = how & 1 ? 0x7531u : 0x6420u;
+      const uint4 w = reinterpret_cast<const uint4*>(values_s[s])[u];
+      return make_uint2(__byte_perm(w.x, w.y, pick), __byte_perm(w.z, w.w, pick));
+    };
+#pragma unroll 2
+    for (int u = tid; u < kChunks; u += kMoveThreads) {
+      const int t = (u / (32 * kS) * 4 + u % 4) * 2;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (t + s >= n) continue;
+        const int how = from[t + s].y;
+        const uint2 c = codes_of(u, s, how);
+        const float f = value_scale(how);
+        top[1] = largest(c.x, f, largest(c.y, f, top[1]));
       }
     }
 #pragma unroll
@@ -343,70 +395,71 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a) {
       const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(top[s]));
       if (tid % 32 == 0) top_s[s][tid / 32] = w;
     }
-    __syncthreads();  // every row has been read
-    if (tid == 0) {
-      asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(a.flags + (int64_t)row * stride + p), "r"(1) : "memory");
-    }
-    // lower pages that have rows of theirs here
-    bool ok = true;
-    const int first = ranks[p] / kPage, last = min(p - 1, (ranks[p + 1] - 1) / kPage);
-    for (int l = first + tid; l <= last; l += kMoveThreads) {
-      const int32_t* f = a.flags + (int64_t)row * stride + l;
-      int seen;
+    for (int l = wait.x + tid; l <= wait.y; l += kMoveThreads) {
       const long long t0 = clock64();
-      do {
-        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(f) : "memory");
-      } while (!seen && clock64() - t0 < kWaitCycles);
-      ok &= seen != 0;
-    }
-    if (!__syncthreads_and(ok)) {
-      if (tid == 0) raise(a.c, RDKV_ERR_TIMEOUT);
-      return;
-    }
-    if (tid < kPage && p * kPage + tid < len) mass[p * kPage + tid] = m;
-    if (n > 0) {  // (what is left of the last page: zero)
-      uint32_t w[2] = {top_s[0][0], top_s[1][0]};
-#pragma unroll
-      for (int i = 1; i < kMoveThreads / 32; ++i) w[0] = max(w[0], top_s[0][i]), w[1] = max(w[1], top_s[1][i]);
-      const int ke = exponent_for(__uint_as_float(w[0])), ve = exponent_for(__uint_as_float(w[1]));
-      const int64_t to = (int64_t)table[p] * H + h;
-      uint8_t* page = a.c.pages + to * L::kBytes;
-      if (tid == 0) *reinterpret_cast<float2*>(a.c.scales + to * 2) = make_float2(two_to(ke), two_to(ve));
-      const float kf = two_to(-ke), vf = two_to(-ve);
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        const int u = tid + i * kMoveThreads, t = u / (16 * kS) * 2 + u / 8 % 2;
-        const float f = t < n ? scale_s[t].x * kf : 1.0f;
-        if (f != 1.0f) kc[i] = make_uint2(rescaled(kc[i].x, f), rescaled(kc[i].y, f));
-        *reinterpret_cast<uint2*>(page + L::key_at(t, u / 16 % kS, u % 8)) = kc[i];
+      while (!seen && ok) {
+        seen = read(l);
+        ok = seen || clock64() - t0 < kWaitCycles;
       }
-#pragma unroll
-      for (int i = 0; i < kValues; ++i) {
-        const int u = tid + i * kMoveThreads, q = u / (32 * kS) * 4 + u % 4, t = 2 * q;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const float f = t + s < n ? scale_s[t + s].y * vf : 1.0f;
-          if (f != 1.0f) vb[i][s] = make_uint2(rescaled(vb[i][s].x, f), rescaled(vb[i][s].y, f));
-        }
-        *reinterpret_cast<uint4*>(page + L::kHalf + L::value_at(q, u / 32 % kS, u % 32 / 4)) =
-            make_uint4(__byte_perm(vb[i][0].x, vb[i][1].x, 0x5140), __byte_perm(vb[i][0].x, vb[i][1].x, 0x7362),
-                       __byte_perm(vb[i][0].y, vb[i][1].y, 0x5140), __byte_perm(vb[i][0].y, vb[i][1].y, 0x7362));
-      }
+      seen = l + kMoveThreads > wait.y || read(l + kMoveThreads);
     }
-    __syncthreads();  // (before the next ticket and its rows)
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+    if (tid < n) mass[p * kPage + tid] = __uint_as_float(weight_s[tid]);
+    uint32_t w[2] = {top_s[0][0], top_s[1][0]};
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) w[0] = max(w[0], top_s[0][i]), w[1] = max(w[1], top_s[1][i]);
+    const int ke = exponent_for(__uint_as_float(w[0])), ve = exponent_for(__uint_as_float(w[1]));
+    uint8_t* page = a.c.pages + (int64_t)to * L::kBytes;
+    if (tid == 0) *reinterpret_cast<float2*>(a.c.scales + (int64_t)to * 2) = make_float2(two_to(ke), two_to(ve));
+    const float kf = two_to(-ke), vf = two_to(-ve);
+    // (what is left of the last page: zero)
+#pragma unroll 2
+    for (int u = tid; u < kChunks; u += kMoveThreads) {
+      const int t = u / (2 * D / 16) * 2 + u / 4 % 2;
+      uint4 c = t < n ? reinterpret_cast<const uint4*>(keys_s)[u] : make_uint4(0, 0, 0, 0);
+      const float f = t < n ? key_scale(from[t].y) * kf : 1.0f;
+      if (f != 1.0f) c = make_uint4(rescaled(c.x, f), rescaled(c.y, f), rescaled(c.z, f), rescaled(c.w, f));
+      reinterpret_cast<uint4*>(page)[u] = c;
+    }
+#pragma unroll 2
+    for (int u = tid; u < kChunks; u += kMoveThreads) {
+      const int t = (u / (32 * kS) * 4 + u % 4) * 2;
+      uint2 c[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int how = from[t + s].y;
+        c[s] = t + s < n ? codes_of(u, s, how) : make_uint2(0, 0);
+        const float f = t + s < n ? value_scale(how) * vf : 1.0f;
+        if (f != 1.0f) c[s] = make_uint2(rescaled(c[s].x, f), rescaled(c[s].y, f));
+      }
+      reinterpret_cast<uint4*>(page + L::kHalf)[u] =
+          make_uint4(__byte_perm(c[0].x, c[1].x, 0x5140), __byte_perm(c[0].x, c[1].x, 0x7362), __byte_perm(c[0].y, c[1].y, 0x5140),
+                     __byte_perm(c[0].y, c[1].y, 0x7362));
+    }
+  }
+  // the last block to end leaves the counters as it found them
+  __syncthreads();
+  if (tid == 0) {
+    if (!ok) raise(a.c, RDKV_ERR_TIMEOUT);
+    int done;
+    asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(done) : "l"(a.count + 2) : "memory");
+    if (done == (int)gridDim.x - 1) a.count[0] = a.count[1] = a.count[2] = 0;
   }
 }
 
 struct EvictLayout {
-  size_t ranks_at, flags_at, todo_at, bytes;
+  size_t flags_at, waits_at, todo_at, from_at, bytes;
 };
 static EvictLayout evict_layout(const rdkv_q8_cache* c) {
-  const int64_t rows = (int64_t)c->batch * c->h_kv;
+  const int64_t pages = (int64_t)c->batch * c->h_kv * c->page_stride;
   EvictLayout o;
-  o.ranks_at = 256;
-  o.flags_at = o.ranks_at + (size_t)align_up(4 * rows * (c->page_stride + 1), 256);
-  o.todo_at = o.flags_at + (size_t)align_up(4 * rows * c->page_stride, 256);
-  o.bytes = o.todo_at + (size_t)align_up(8 * rows * c->page_stride, 256);
+  o.flags_at = kCounterBytes;
+  o.waits_at = o.flags_at + (size_t)align_up(4 * pages, 256);
+  o.todo_at = o.waits_at + (size_t)align_up(8 * pages, 256);
+  o.from_at = o.todo_at + (size_t)align_up(8 * pages, 256);
+  // (rows are kept only of sequences that hold more: n_keep is then below what a table holds)
+  o.bytes = o.from_at + (size_t)align_up(8 * pages * kPage, 256);
   return o;
 }
 
@@ -437,25 +490,36 @@ extern "C" rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, in
   RDKV_REQUIRE(ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= lay.bytes, RDKV_ERR_WORKSPACE, "eviction workspace too small (%zu < %zu) or unaligned",
                ws_bytes, lay.bytes);
   char* w = static_cast<char*>(ws);
-  const EvictArgs a{q8::view_of(cache), mass, mass_stride, n_keep, n_first, n_last, kept, reinterpret_cast<int32_t*>(w + lay.ranks_at),
-                    reinterpret_cast<int32_t*>(w + lay.flags_at), reinterpret_cast<int2*>(w + lay.todo_at), reinterpret_cast<int32_t*>(w)};
+  const EvictArgs a{q8::view_of(cache), mass, mass_stride, n_keep, n_first, n_last, kept, reinterpret_cast<int2*>(w + lay.from_at),
+                    reinterpret_cast<int32_t*>(w + lay.flags_at), reinterpret_cast<int2*>(w + lay.waits_at), reinterpret_cast<int2*>(w + lay.todo_at),
+                    reinterpret_cast<int32_t*>(w)};
   cudaStream_t cs = (cudaStream_t)stream;
   const int rows = cache->batch * cache->h_kv;
-  // blocks of a row: 16 warps each; a warp takes four pages at least, and eight blocks are the most a cluster holds everywhere
+  // blocks of a row: a warp has eight pages before the row takes another block
+  constexpr int kWarps = kPickThreads / 32;
   int size = 1;
-  while (size < 8 && size * 64 < cache->page_stride) size *= 2;
+  while (size < kMaxBlocks && size * kWarps * 8 < cache->page_stride) size *= 2;
+  const int hold = std::min(kHold, ceil_div(cache->page_stride, size * kWarps));
+  static std::atomic<uint64_t> ready{0};  // once a device (of the first 64; the others pay for the call every time)
+  int dev = 0;
+  RDKV_TRY_CUDA(cudaGetDevice(&dev), "8-bit cache eviction");
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    RDKV_TRY_CUDA(cudaFuncSetAttribute(pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kHold * 256), "8-bit cache eviction");
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows * size), cfg.blockDim = dim3(kPickThreads), cfg.stream = cs;
+  cfg.gridDim = dim3((unsigned)rows * size), cfg.blockDim = dim3(kPickThreads), cfg.stream = cs, cfg.dynamicSmemBytes = kWarps * hold * 256;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = size, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr, cfg.numAttrs = 2;
-  RDKV_TRY_CUDA(cudaLaunchKernelEx(&cfg, pick_kernel, a), "8-bit cache eviction");
+  RDKV_TRY_CUDA(cudaLaunchKernelEx(&cfg, pick_kernel, a, hold), "8-bit cache eviction");
   count_launch();
-  const int64_t pages = (int64_t)rows * cache->page_stride;
-  const unsigned grid = (unsigned)std::min<int64_t>(pages, (int64_t)num_sms() * 6);
+  const int64_t pages = (int64_t)rows * std::min(cache->page_stride, ceil_div(n_keep, kPage));
+  const unsigned grid = (unsigned)std::min<int64_t>(pages, (int64_t)num_sms() * kMoveBlocks);
   auto move = cache->head_dim == 128 ? move_kernel<128> : move_kernel<64>;
   RDKV_TRY_CUDA(launch_after(move, dim3(grid), kMoveThreads, 0, cs, a), "8-bit cache eviction");
   count_launch();

@@ -1197,8 +1197,7 @@ class Q8Cache:
         ws = None if capturing else self._ws.get((kind, s))
         if ws is None or ws.numel() < nb:
             ws = torch.empty(nb, dtype=torch.uint8, device=self.device)
-            if kind != "evict":
-                ws[:Q8_COUNTER_BYTES].zero_()
+            ws[:Q8_COUNTER_BYTES].zero_()
             if not capturing:
                 self._ws[kind, s] = ws
         return ws

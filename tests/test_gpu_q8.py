@@ -642,8 +642,7 @@ def test_nothing_is_written_outside_workspaces_and_outputs(D, lens, h, G, T):
         else:
             nb = rdkv.lib().rdkv_q8_attn_workspace_bytes(ctypes.byref(c.c), h * G, T, "mass" in kind)
         big = torch.full((nb + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
-        if kind != "evict":
-            big[:rdkv.Q8_COUNTER_BYTES] = 0
+        big[:rdkv.Q8_COUNTER_BYTES] = 0
         ws = big[:nb]
         for _ in range(2):
             mass = guarded((B, h, c.max_tokens), torch.float32)
@@ -656,8 +655,7 @@ def test_nothing_is_written_outside_workspaces_and_outputs(D, lens, h, G, T):
         assert (big[nb:] == 0xA5).all(), kind
         for b, x in guards:
             assert (b[x.numel():] == 77).all(), kind
-        if kind != "evict":
-            assert (ws[:rdkv.Q8_COUNTER_BYTES] == 0).all(), kind
+        assert (ws[:rdkv.Q8_COUNTER_BYTES] == 0).all(), kind
     assert rdkv.rdkv_q8_status(c) == 0
 
 
