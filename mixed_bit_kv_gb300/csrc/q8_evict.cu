@@ -78,7 +78,8 @@ __device__ __forceinline__ uint2 weights_of(const float* mass, int p, int lane) 
 }
 
 // A cluster a (sequence, KV head); a warp has a run of the row's pages, a lane two positions of each.
-constexpr int kMaxBlocks = 8;  // of a cluster, everywhere
+constexpr int kMaxBlocks = 8;  // of a cluster (16, which have to be asked for: of eight such clusters one waits for another, 95 against 85 us)
+constexpr int kSplit = 8;
 constexpr int kHold = 16;      // pages of a warp whose weights shared memory holds; those of longer rows are loaded again
 // (Short loops: the code is fetched anew by every launch.  With the weights in registers and every loop unrolled, 30 KB of it, the
 // choice took 16 us for 32 rows of 3,000 tokens under the profiler.)
@@ -106,7 +107,12 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
     for (int p = p0; p < min(p1, p0 + hold); ++p)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(held + (p - p0) * 32)), "l"(mass + (int64_t)p * kPage + 2 * lane) : "memory");
   }
-  auto weights = [&](int p) { return p - p0 < hold ? held[(p - p0) * 32] : weights_of(mass, p, lane); };
+  // a page's two weights as numbers of their order
+  auto orders = [&](int p) {
+    if (p - p0 < hold) return held[(p - p0) * 32];
+    const uint2 w = weights_of(mass, p, lane);
+    return make_uint2(order_of(w.x), order_of(w.y));
+  };
   if (h == 0 && rank == 0 && tid == 0) check_length(a.c, b);
   // a page outside the pool: the row stays
   bool bad = false;
@@ -125,20 +131,25 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
   }
   for (int p = part_of_all; p < filled; p += all) a.flags[(int64_t)row * stride + p] = 0;
   asm volatile("cp.async.wait_all;" ::: "memory");  // (each thread reads what it asked for)
+#pragma unroll 2
+  for (int p = p0; p < min(p1, p0 + hold); ++p) {
+    const uint2 w = held[(p - p0) * 32];
+    held[(p - p0) * 32] = make_uint2(order_of(w.x), order_of(w.y));
+  }
 
   // ---- the border: the need-th largest of the weights between the first and the last
-  const int lo = a.n_first, hi = len - a.n_last;
+  const int lo = a.n_first;
+  const uint32_t range = len - a.n_last - a.n_first;  // positions that may go, from lo on
   uint32_t need = a.n_keep - a.n_first - a.n_last, border = 0, mask = 0;
   const bool some = need > 0;
 #pragma unroll 1
   for (int shift = 24; some && shift >= 0; shift -= 8) {
-#pragma unroll 1
+#pragma unroll 2
     for (int p = p0; p < p1; ++p) {
-      const uint2 w = weights(p);
-      const int t = p * kPage + 2 * lane;
-      const uint32_t x = order_of(w.x), y = order_of(w.y);
-      if (t >= lo && t < hi && (x & mask) == border) atomicAdd(&count_s[(x >> shift & 255) * 32 + lane], 1u);
-      if (t + 1 >= lo && t + 1 < hi && (y & mask) == border) atomicAdd(&count_s[(y >> shift & 255) * 32 + lane], 1u);
+      const uint2 w = orders(p);
+      const uint32_t t = (uint32_t)(p * kPage + 2 * lane - lo);
+      if (t < range && (w.x & mask) == border) atomicAdd(&count_s[(w.x >> shift & 255) * 32 + lane], 1u);
+      if (t + 1 < range && (w.y & mask) == border) atomicAdd(&count_s[(w.y >> shift & 255) * 32 + lane], 1u);
     }
     __syncthreads();
     // a digit's count: its 32 columns, each thread from another one on (no bank conflicts); cleared for the next pass
@@ -184,21 +195,22 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
   }
   // kept are: the first, the last, what is above the border and, of what lies on it (under the mask), `need`
   // ---- how many of each before this warp's pages
-  auto classes = [&](int p, uint2 w, bool (&sure)[2], bool (&tie)[2]) {
+  auto classes = [&](int p, bool (&sure)[2], bool (&tie)[2]) {
+    const uint2 w = orders(p);
+    const int t = p * kPage + 2 * lane;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int t = p * kPage + 2 * lane + i;
-      const uint32_t x = order_of(i ? w.y : w.x) & mask;
-      const bool open = t >= lo && t < hi;
-      sure[i] = t < len && (!open || (some && x > border));
+      const uint32_t x = (i ? w.y : w.x) & mask;
+      const bool open = (uint32_t)(t + i - lo) < range;
       tie[i] = open && some && x == border;
+      sure[i] = open ? some && x > border : t + i < len;
     }
   };
   uint32_t n_sure = 0, n_tie = 0, first = 0x7fffffffu;  // first: page of a row that may go
-#pragma unroll 1
+#pragma unroll 2
   for (int p = p0; p < p1; ++p) {
     bool sure[2], tie[2];
-    classes(p, weights(p), sure, tie);
+    classes(p, sure, tie);
     n_sure += sure[0] + sure[1], n_tie += tie[0] + tie[1];
     if (!(sure[0] && sure[1])) first = min(first, (uint32_t)p);
   }
@@ -229,19 +241,23 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
   // ---- their places
   int2 *from = a.from + (int64_t)row * a.n_keep, *waits = a.waits + (int64_t)row * stride;
   uint32_t at = sure0 + min(tie0, need);
+  int at_lane = 0, how_lane = 0;  // where the warp's pages lie and their scales, 32 at a time, a lane a page
 #pragma unroll 1
   for (int p = p0; p < p1; ++p) {
-    const int lies = fetch(table + p) * H + h;
-    const uint2 sc = fetch(reinterpret_cast<const uint2*>(a.c.scales + (int64_t)lies * 2));
+    if ((p - p0) % 32 == 0 && p + lane < p1) {
+      at_lane = fetch(table + p + lane) * H + h;
+      how_lane = how_of(0, fetch(reinterpret_cast<const uint2*>(a.c.scales + (int64_t)at_lane * 2)));
+    }
+    const int lies = __shfl_sync(0xffffffffu, at_lane, (p - p0) % 32);
     bool sure[2], tie[2];
-    classes(p, weights(p), sure, tie);
+    classes(p, sure, tie);
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t t0 = __ballot_sync(0xffffffffu, tie[0]), t1 = __ballot_sync(0xffffffffu, tie[1]);
     const uint32_t mine = tie0 + __popc(t0 & below) + __popc(t1 & below);
     const bool k0 = sure[0] || (tie[0] && mine < need), k1 = sure[1] || (tie[1] && mine + tie[0] < need);
     const uint32_t b0 = __ballot_sync(0xffffffffu, k0), b1 = __ballot_sync(0xffffffffu, k1);
     const uint32_t to = at + __popc(b0 & below) + __popc(b1 & below);
-    const int t = p * kPage + 2 * lane, how = how_of(2 * lane, sc);
+    const int t = p * kPage + 2 * lane, how = __shfl_sync(0xffffffffu, how_lane, (p - p0) % 32) + 2 * lane;
     if (k0) kept[to] = t, from[to] = make_int2(lies, how);
     if (k1) kept[to + k0] = t + 1, from[to + k0] = make_int2(lies, how + 1);
     // a weight that goes and that no row's will take the place of (of the rows that stay the move sees to)
@@ -495,10 +511,10 @@ extern "C" rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, in
                     reinterpret_cast<int32_t*>(w)};
   cudaStream_t cs = (cudaStream_t)stream;
   const int rows = cache->batch * cache->h_kv;
-  // blocks of a row: a warp has eight pages before the row takes another block
+  // blocks of a row: a warp has kSplit pages before the row takes another block
   constexpr int kWarps = kPickThreads / 32;
   int size = 1;
-  while (size < kMaxBlocks && size * kWarps * 8 < cache->page_stride) size *= 2;
+  while (size < kMaxBlocks && size * kWarps * kSplit < cache->page_stride) size *= 2;
   const int hold = std::min(kHold, ceil_div(cache->page_stride, size * kWarps));
   static std::atomic<uint64_t> ready{0};  // once a device (of the first 64; the others pay for the call every time)
   int dev = 0;
