@@ -1,5 +1,7 @@
 // The 8-bit paged cache: rows quantised as they are written (rdkv_q8_write) and read back (rdkv_q8_read), and the
 // host checks that every rdkv_q8_* call makes.
+#include <type_traits>
+
 #include "q8.cuh"
 
 namespace rdkv {
@@ -54,16 +56,92 @@ __device__ __forceinline__ void widen(const Raw<float>& r, float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
 }
-// The largest magnitude of eight channels and top; a NaN takes no part.
-template <typename T>
-__device__ __forceinline__ float largest(const Raw<T>& r, float top) {
+// The largest magnitude of eight channels and top (as the bits of a number that is no less than 0); kNan: a NaN, if there is one,
+// else it takes no part.
+template <bool kNan>
+__device__ __forceinline__ float larger(float a, float b) {
+  float d;
+  if constexpr (kNan) asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  else d = fmaxf(a, b);
+  return d;
+}
+template <bool kNan>
+__device__ __forceinline__ __half2 larger(__half2 a, __half2 b) {
+  return kNan ? __hmax2_nan(a, b) : __hmax2(a, b);
+}
+template <bool kNan>
+__device__ __forceinline__ __nv_bfloat162 larger(__nv_bfloat162 a, __nv_bfloat162 b) {
+  return kNan ? __hmax2_nan(a, b) : __hmax2(a, b);
+}
+template <bool kNan>
+__device__ __forceinline__ float largest(const Raw<float>& r, float top) {
   float x[8];
   widen(r, x);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+  for (int i = 0; i < 8; ++i) top = larger<kNan>(top, fabsf(x[i]));
   return top;
 }
+template <bool kNan, class T2>
+__device__ __forceinline__ float largest16(const uint4& w, float top) {
+  auto as = [](uint32_t v) { return __habs2(*reinterpret_cast<const T2*>(&v)); };
+  const T2 m = larger<kNan>(larger<kNan>(as(w.x), as(w.y)), larger<kNan>(as(w.z), as(w.w)));
+  return larger<kNan>(top, larger<kNan>((float)m.x, (float)m.y));
+}
+template <bool kNan>
+__device__ __forceinline__ float largest(const Raw<__half>& r, float top) {
+  return largest16<kNan, __half2>(r.w[0], top);
+}
+template <bool kNan>
+__device__ __forceinline__ float largest(const Raw<__nv_bfloat16>& r, float top) {
+  return largest16<kNan, __nv_bfloat162>(r.w[0], top);
+}
 
+// Eight channels' codes, and those of a token pair side by side, in the scale 2^e.  nan: there may be NaN among them, which become 0.
+__device__ __forceinline__ uint32_t clean(uint32_t w, bool nan) { return nan ? without_nan(w) : w; }
+template <typename T>
+struct Coder {
+  float f;
+  bool nan;
+  __device__ __forceinline__ Coder(int e, bool nan) : f(two_to(-e)), nan(nan) {}
+  __device__ __forceinline__ uint2 eight(const Raw<T>& r) const {
+    float x[8];
+    widen(r, x);
+    return make_uint2(clean(codes4(x[0] * f, x[1] * f, x[2] * f, x[3] * f), nan), clean(codes4(x[4] * f, x[5] * f, x[6] * f, x[7] * f), nan));
+  }
+  __device__ __forceinline__ uint4 pairs(const Raw<T>& a, const Raw<T>& b) const {
+    float x[8], y[8];
+    widen(a, x);
+    widen(b, y);
+    uint32_t c[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) c[m] = clean(codes4(x[2 * m] * f, y[2 * m] * f, x[2 * m + 1] * f, y[2 * m + 1] * f), nan);
+    return make_uint4(c[0], c[1], c[2], c[3]);
+  }
+};
+// fp16 rows stay fp16: times 2^-e, two at a time, is exact down to 2^-14 and within 2^-25 below, where every code's middle to the next
+// (2^-10 and up) is far.  2^-e past 2^15, of the smallest scales, in two factors.
+template <>
+struct Coder<__half> {
+  __half2 f, more;
+  bool twice, nan;
+  __device__ __forceinline__ Coder(int e, bool nan)
+      : f(__float2half2_rn(two_to(min(-e, 15)))), more(__float2half2_rn(two_to(max(-e - 15, 0)))), twice(e < -15), nan(nan) {}
+  __device__ __forceinline__ uint32_t two(uint32_t w) const {
+    __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w), f);
+    if (twice) x = __hmul2(x, more);
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+    return d;
+  }
+  __device__ __forceinline__ uint32_t four(uint32_t a, uint32_t b) const { return clean(two(a) | two(b) << 16, nan); }
+  __device__ __forceinline__ uint2 eight(const Raw<__half>& r) const { return make_uint2(four(r.w[0].x, r.w[0].y), four(r.w[0].z, r.w[0].w)); }
+  __device__ __forceinline__ uint4 pairs(const Raw<__half>& a, const Raw<__half>& b) const {
+    auto both = [&](uint32_t x, uint32_t y) { return four(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632)); };
+    return make_uint4(both(a.w[0].x, b.w[0].x), both(a.w[0].y, b.w[0].y), both(a.w[0].z, b.w[0].z), both(a.w[0].w, b.w[0].w));
+  }
+};
+
+constexpr int kWriteBlocks = 4;  // of 256 threads an SM, 16-bit rows
 // One block per (sequence, page that its rows touch, KV head), heads fastest.  A thread takes eight channels of a
 // token of the keys (8 bytes of codes) and eight channels of a token pair of the values (16 bytes), both in the
 // order of the page, so that a warp stores 256 and 512 bytes in a row; of the rows it then loads whole 128-byte
@@ -71,7 +149,7 @@ __device__ __forceinline__ float largest(const Raw<T>& r, float top) {
 // their codes.  Where the page was begun before and the new rows raise a scale, the block takes the earlier codes
 // in it too (one append in some dozens).
 template <typename T, int D, int kThreads, int kKeys, int kValues>
-__global__ void __launch_bounds__(kThreads) write_kernel(View v, Rows r, const T* k, const T* vv) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? (sizeof(T) == 2 ? kWriteBlocks : 2) : 1) write_kernel(View v, Rows r, const T* k, const T* vv) {
   using L = Layout<D>;
   constexpr int kS = L::kSides, kWarps = kThreads / 32;
   __shared__ uint32_t top_s[2][kWarps];
@@ -107,39 +185,51 @@ __global__ void __launch_bounds__(kThreads) write_kernel(View v, Rows r, const T
     vr[i][0] = load_raw(vv + row_at(2 * p) + 64 * j + 8 * g);
     vr[i][1] = load_raw(vv + row_at(2 * p + 1) + 64 * j + 8 * g);
   }
-  // (a token taken twice counts as once)
-  float top[2] = {0.0f, 0.0f};
+  // the largest magnitudes (a token taken twice counts as once), first as if there were no NaN: the bits of one are larger than any
+  // number's
+  uint32_t all[2];
+  auto find = [&](auto nan) {
+    constexpr bool kNan = decltype(nan)::value;
+    float top[2] = {0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < kKeys; ++i) top[0] = largest(kr[i], top[0]);
+    for (int i = 0; i < kKeys; ++i) top[0] = largest<kNan>(kr[i], top[0]);
 #pragma unroll
-  for (int i = 0; i < kValues; ++i) top[1] = largest(vr[i][1], largest(vr[i][0], top[1]));
+    for (int i = 0; i < kValues; ++i) top[1] = largest<kNan>(vr[i][1], largest<kNan>(vr[i][0], top[1]));
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top[s]));
+      if (lane == 0) top_s[s][tid / 32] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      all[s] = top_s[s][0];
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) all[s] = max(all[s], top_s[s][i]);
+    }
+  };
+  find(std::true_type());
+  const bool nan = max(all[0], all[1]) > 0x7f800000u;
+  if (nan) {
+    __syncthreads();
+    find(std::false_type());
+  }
   int e[2], old[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top[s]));
-    if (lane == 0) top_s[s][tid / 32] = m;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint32_t m = top_s[s][0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) m = max(m, top_s[s][i]);
-    e[s] = exponent_for(__uint_as_float(m));
+    e[s] = exponent_for(__uint_as_float(all[s]));
     old[s] = min(max(exponent(__uint_as_float(s ? was.y : was.x)), kLowExp), kHighExp);
     if (w.s0 > 0) e[s] = max(e[s], old[s]);
   }
   if (tid == 0) *reinterpret_cast<float2*>(v.scales + at * 2) = make_float2(two_to(e[0]), two_to(e[1]));
-  const float kf = two_to(-e[0]), vf = two_to(-e[1]), again = two_to(old[1] - e[1]);
+  const float again = two_to(old[1] - e[1]);
+  const Coder<T> key_codes(e[0], nan), value_codes(e[1], nan);
 #pragma unroll
   for (int i = 0; i < kKeys; ++i) {
     int t, j, c;
     key_unit(i, t, j, c);
     if (t < w.s0 || t >= w.s1) continue;
-    float x[8];
-    widen(kr[i], x);
-    *reinterpret_cast<uint2*>(page + L::key_at(t, j, c)) =
-        make_uint2(codes4(x[0] * kf, x[1] * kf, x[2] * kf, x[3] * kf), codes4(x[4] * kf, x[5] * kf, x[6] * kf, x[7] * kf));
+    *reinterpret_cast<uint2*>(page + L::key_at(t, j, c)) = key_codes.eight(kr[i]);
   }
 #pragma unroll
   for (int i = 0; i < kValues; ++i) {
@@ -147,24 +237,15 @@ __global__ void __launch_bounds__(kThreads) write_kernel(View v, Rows r, const T
     value_unit(i, p, j, g);
     const bool in0 = 2 * p >= w.s0 && 2 * p < w.s1, in1 = 2 * p + 1 >= w.s0 && 2 * p + 1 < w.s1;
     if (!in0 && !in1) continue;
-    float x[8], y[8];
-    widen(vr[i][0], x);
-    widen(vr[i][1], y);
     uint4* to = reinterpret_cast<uint4*>(page + L::kHalf + L::value_at(p, j, g));
-    uint32_t c[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) c[m] = codes4(x[2 * m] * vf, y[2 * m] * vf, x[2 * m + 1] * vf, y[2 * m + 1] * vf);
+    uint4 c = value_codes.pairs(vr[i][0], vr[i][1]);
     if (!(in0 && in1)) {  // the pair's other token: an earlier one, or one that holds nothing yet
-      const uint4 held = fetch(to);
-      uint32_t o[4] = {held.x, held.y, held.z, held.w};
+      uint4 o = fetch(to);
       const uint32_t mine = in0 ? 0x00ff00ffu : 0xff00ff00u;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (in1 && e[1] != old[1]) o[m] = rescaled(o[m], again);
-        c[m] = (c[m] & mine) | (o[m] & ~mine);
-      }
+      if (in1 && e[1] != old[1]) o = make_uint4(rescaled(o.x, again), rescaled(o.y, again), rescaled(o.z, again), rescaled(o.w, again));
+      c = make_uint4((c.x & mine) | (o.x & ~mine), (c.y & mine) | (o.y & ~mine), (c.z & mine) | (o.z & ~mine), (c.w & mine) | (o.w & ~mine));
     }
-    *to = make_uint4(c[0], c[1], c[2], c[3]);
+    *to = c;
   }
   // the earlier rows in the new scale
   if (w.s0 > 0 && e[0] != old[0]) {

@@ -51,9 +51,9 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
   return d;
 }
-// Four codes; what is no number has code 127, whatever its sign, and becomes 0.
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  const uint32_t w = codes2(a, b) | codes2(c, d) << 16;
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) { return codes2(a, b) | codes2(c, d) << 16; }
+// What is no number has code 127, whatever its sign: it becomes 0.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
   const uint32_t bad = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
   return w & ~((bad >> 7) * 255u);
 }
@@ -77,7 +77,7 @@ __device__ __forceinline__ void values4(uint32_t w, float (&x)[4]) {
 __device__ __forceinline__ uint32_t rescaled(uint32_t w, float f) {
   float x[4];
   values4(w, x);
-  return codes2(x[0] * f, x[1] * f) | codes2(x[2] * f, x[3] * f) << 16;
+  return codes4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
 }
 
 // ---------------------------------------------------------------- host checks
