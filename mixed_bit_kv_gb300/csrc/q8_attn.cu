@@ -107,6 +107,13 @@ __device__ __forceinline__ void put_lse(const AttnArgs& a, int64_t row, float m,
   if (a.stats) a.stats[row] = make_float2(m, l);
 }
 
+// A unit's rows, by one warp, where no key is seen.
+template <int D>
+__device__ __noinline__ void write_nothing(const AttnArgs& a, Unit un, int lane) {
+  for (int i = lane; i < un.rows * (D / 4); i += 32) put4(a, row_at(a, un, i / (D / 4)) * D + i % (D / 4) * 4, make_float4(0, 0, 0, 0));
+  if (lane < un.rows) put_lse(a, row_at(a, un, lane), 0.0f, 0.0f);
+}
+
 // One warp's running state over the pages of one unit.
 template <int D, int NT, bool PREC>
 struct Warp {
@@ -528,34 +535,30 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     for (int i = tid; i < a.c.batch; i += 32 * NW) check_length(a.c, i);
   const int c0 = lane < BC ? items_of(a, lane) : 0;  // of the first 32 (sequence, chunk) pairs
   int total;  // the host has made sure that all units' items fit
+  bool empty;  // some unit has no key
   if (BC <= 32) {
     total = __reduce_add_sync(0xffffffffu, c0);
+    empty = __any_sync(0xffffffffu, lane < BC && c0 == 0);
     __syncthreads();
   } else {
     int n = 0;
+    bool none = false;
     __syncthreads();
-    for (int i = tid; i < BC; i += 32 * NW) n += items_of(a, i);
+    for (int i = tid; i < BC; i += 32 * NW) {
+      const int c = items_of(a, i);
+      n += c, none |= c == 0;
+    }
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0 && n) atomicAdd(&total_s, n);
-    __syncthreads();
+    empty = __syncthreads_or(none);
     total = total_s;
   }
   total *= H;
-  // units without a key: nothing else writes their rows
-  for (int bc = blockIdx.x; bc < BC; bc += gridDim.x) {
-    if (items_of(a, bc) > 0) continue;
-    for (int h = 0; h < H; ++h) {
-      const Unit un = unit_at(a, bc * H + h);
-      for (int i = tid; i < un.rows * (D / 4); i += 32 * NW)
-        put4(a, row_at(a, un, i / (D / 4)) * D + i % (D / 4) * 4, make_float4(0, 0, 0, 0));
-      if (tid < un.rows) put_lse(a, row_at(a, un, tid), 0.0f, 0.0f);
-    }
-  }
   // a block for every kMinItems items: few items stay in few blocks
   const int nb = min((int)gridDim.x, ceil_div(total, kMinItems));
-  if ((int)blockIdx.x >= nb) return;
+  const bool idle = (int)blockIdx.x >= nb;
   const int nw = nb * NW, me = blockIdx.x * NW + warp;
-  const int w0 = share(me, total, nw), w1 = share(me + 1, total, nw), n_items = w1 - w0;
+  const int w0 = idle ? 0 : share(me, total, nw), w1 = idle ? 0 : share(me + 1, total, nw), n_items = w1 - w0;
   int bc = 0, h = 0, p = 0, cnt = 0;  // the next item to look up
   if (BC == 1) {
     cnt = __shfl_sync(0xffffffffu, c0, 0);
@@ -678,6 +681,12 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     w.begin(a.dtype, x, qd);
     in_unit = true;
   }
+  if (empty) {  // units without a key: nothing else writes their rows
+#pragma unroll 1
+    for (int u = warp * gridDim.x + blockIdx.x; u < BC * H; u += NW * gridDim.x)
+      if (items_of(a, u / H) == 0) write_nothing<D>(a, unit_at(a, u), lane);
+  }
+  if (idle) return;
 #pragma unroll 1
   for (; i < n_items; ++i) {
     const int4 e = info[i % kInfo];
@@ -773,10 +782,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       if (!(e.w & 2) && i < n_items - 1) continue;
       const bool ends = e.w & 2;
       if (began && ends) {
-        un = unit_at(a, e.z);
-        for (int x = lane; x < un.rows * (D / 4); x += 32)
-          put4(a, row_at(a, un, x / (D / 4)) * D + x % (D / 4) * 4, make_float4(0, 0, 0, 0));
-        if (lane < un.rows) put_lse(a, row_at(a, un, lane), 0.0f, 0.0f);
+        write_nothing<D>(a, unit_at(a, e.z), lane);
       } else {
         float* dst = ends ? a.heads + (int64_t)me * P::kFloats : reinterpret_cast<float*>(ring);
         for (int x = lane; x < P::kFloats; x += 32) dst[x] = x / P::kRows == D ? -INFINITY : 0.0f;
