@@ -503,8 +503,13 @@ struct Smem {
   static constexpr int kRing = NS * Layout<D>::kHalf;
   static_assert(Partial<D, NT>::kFloats * 4 <= kRing, "a warp's piece goes into its ring");
   static_assert(2 * NW <= 32, "a lane a piece");
+  // A piece of a unit that ends inside a warp's run, while copies into the ring are under way: beside the ring where there is
+  // room; else in global memory, from where the warp fetches it behind its other piece when its copies have ended.
+  static constexpr int kPiece = Partial<D, NT>::kFloats * 4;
+  static constexpr bool kRoom = NT == 1;
+  static_assert(kRoom || 2 * kPiece <= kRing, "both pieces in the ring");
   static constexpr size_t kBars = (size_t)NW * kRing, kInfoAt = kBars + 16 * ((NW * NS + 1) / 2), kScalesAt = kInfoAt + 16 * NW * kInfo,
-                          kBytes = kScalesAt + 8 * NW * kInfo;
+                          kHeads = kScalesAt + 8 * NW * kInfo, kBytes = kHeads + (kRoom ? NW * kPiece : 0);
   static_assert(kBytes <= 231 * 1024, "with the block's own variables at most 227 KB and 1 KB reserved");
 };
 
@@ -650,6 +655,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     __syncwarp();
   };
 
+  float* head = S::kRoom ? reinterpret_cast<float*>(smem + S::kHeads + (size_t)warp * S::kPiece) : a.heads + (int64_t)me * P::kFloats;
+  bool headed = false;  // there is such a piece
   // Enters the piece of a unit that this warp has written up to item i.
   auto leave_piece = [&](int i, int unit, bool began, bool ends) {
     const int at = 2 * warp + (ends ? 0 : 1), items = items_of(a, unit / H);
@@ -739,9 +746,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     next_stage();
     if ((e.w & 2) || i == n_items - 1) {  // the unit, or the run, ends
       const bool ends = e.w & 2;
-      // a unit that ends here without having begun lies first in the run: copies are under way, its piece
-      // goes to global memory
-      float* dst = ends ? a.heads + (int64_t)me * P::kFloats : reinterpret_cast<float*>(ring);
+      // a unit that ends here without having begun lies first in the run: copies are under way
+      float* dst = ends ? head : reinterpret_cast<float*>(ring);
       if (began && ends) {
         w.finish(
             g, qd,
@@ -756,6 +762,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
             g, qd, [&](int row, int ch, float, float4 o) { *reinterpret_cast<float4*>(dst + row * D + ch) = o; },
             [&](int row, float m, float l) { dst[P::kRows * D + row] = m, dst[P::kRows * (D + 1) + row] = l; });
         if (lane == 0) leave_piece(i, e.z, began, ends);
+        headed |= ends;
       }
       in_unit = false;
     }
@@ -784,13 +791,19 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       if (began && ends) {
         write_nothing<D>(a, unit_at(a, e.z), lane);
       } else {
-        float* dst = ends ? a.heads + (int64_t)me * P::kFloats : reinterpret_cast<float*>(ring);
+        float* dst = ends ? head : reinterpret_cast<float*>(ring);
         for (int x = lane; x < P::kFloats; x += 32) dst[x] = x / P::kRows == D ? -INFINITY : 0.0f;
         if (lane == 0) leave_piece(i, e.z, began, ends);
+        headed |= ends;
       }
       in_unit = false;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  if (!S::kRoom && headed) {
+    __syncwarp();
+#pragma unroll 8
+    for (int x = lane; x < P::kFloats / 4; x += 32) reinterpret_cast<float4*>(ring + S::kPiece)[x] = reinterpret_cast<const float4*>(head)[x];
   }
   __syncthreads();
 
@@ -813,7 +826,9 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       const int row = i / (D / 4), ch = i % (D / 4) * 4;
       auto src = [&](uint32_t m) -> const float* {
         const int e = __ffs(m) - 1;
-        return e & 1 ? reinterpret_cast<const float*>(smem + (size_t)(e / 2) * S::kRing) : a.heads + ((int64_t)blockIdx.x * NW + e / 2) * P::kFloats;
+        return reinterpret_cast<const float*>(smem + (e & 1         ? (size_t)(e / 2) * S::kRing
+                                                      : S::kRoom ? S::kHeads + (size_t)(e / 2) * S::kPiece
+                                                                 : (size_t)(e / 2) * S::kRing + S::kPiece));
       };
       float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
