@@ -915,29 +915,32 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
 
 // ---------------------------------------------------------------- the keys' weights
 // mass_t += sum over the query rows that see t of 2^(logit - reference) / sum, chunk after chunk and row after row.
-// A thread two positions of a (sequence, KV head); the loads of eight rows under way together, the first with the rows'
+// A thread four positions of a (sequence, KV head); the loads of eight rows under way together, the first with the rows'
 // statistics, the weights so far and the page table.
-constexpr int kMassThreads = 128, kMassKeys = 2 * kMassThreads;
+constexpr int kMassThreads = 128, kMassKeys = 4 * kMassThreads;
 constexpr int kMassRows = kMaxQueries * 8;
 __global__ void __launch_bounds__(kMassThreads) mass_kernel(AttnArgs a, float* mass, int64_t mass_stride) {
   __shared__ float2 stat_s[kMassRows];
   after_previous();
   const int H = a.c.h_kv, rows = a.n_q * a.G, tid = threadIdx.x;
   const int tiles = ceil_div(a.c.page_stride, kMassKeys / kPage), bh = blockIdx.x / tiles, b = bh / H, h = bh - b * H;
-  const int t = (int)(blockIdx.x % tiles) * kMassKeys + 2 * tid, held = held_tokens(a.c, b);
-  if (t - 2 * tid >= held) return;
+  const int t = (int)(blockIdx.x % tiles) * kMassKeys + 4 * tid, held = held_tokens(a.c, b);
+  if (t - 4 * tid >= held) return;
   const bool real = t < held;
   float* to = mass + ((int64_t)b * H + h) * mass_stride + t;
   // (a wait that ran out: the logits are not all there; a page outside the pool: nothing was attended there)
   const int page = real ? fetch(a.c.page_table + (int64_t)b * a.c.page_stride + t / kPage) : -1, status = fetch(a.c.status);
-  const uint2 had = real ? fetch(reinterpret_cast<const uint2*>(to)) : make_uint2(0, 0);
+  const uint2 had0 = real ? fetch(reinterpret_cast<const uint2*>(to)) : make_uint2(0, 0);
+  const uint2 had1 = real ? fetch(reinterpret_cast<const uint2*>(to + 2)) : make_uint2(0, 0);
   constexpr int kAhead = 8;
-  uint2 w[kAhead];
+  uint4 w[kAhead];
   auto load = [&](int c, int r0, int m, int seen) {
     const float* u = a.logits + (((((int64_t)b * a.n_chunks + c) * H + h) * a.c.page_stride + t / kPage) * a.rows + r0) * kPage + t % kPage;
 #pragma unroll
-    for (int r = 0; r < kAhead; ++r)
-      w[r] = t < seen && r0 + r < m ? fetch(reinterpret_cast<const uint2*>(u + r * kPage)) : make_uint2(0xff800000u, 0xff800000u);
+    for (int r = 0; r < kAhead; ++r) {
+      constexpr uint32_t kHidden = 0xff800000u;  // (a page's logits are all there as soon as one of its keys is seen)
+      w[r] = t < seen && r0 + r < m ? fetch(reinterpret_cast<const uint4*>(u + r * kPage)) : make_uint4(kHidden, kHidden, kHidden, kHidden);
+    }
   };
   auto rows_of = [&](int c) { return min(a.chunk, a.n_q - c * a.chunk) * a.G; };
   load(0, 0, rows_of(0), seen_by(a, b, 0));
@@ -948,7 +951,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(AttnArgs a, float* m
     stat_s[i] = make_float2(__uint_as_float(x.x), l > 0.0f && l < INFINITY ? 1.0f / l : 0.0f);
   }
   __syncthreads();
-  float2 sum = make_float2(0.0f, 0.0f);
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int c = 0; c < a.n_chunks; ++c) {
     const int m = rows_of(c), seen = seen_by(a, b, c);
     const float2* st = stat_s + c * a.chunk * a.G;
@@ -959,15 +962,24 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(AttnArgs a, float* m
       for (int r = 0; r < kAhead; ++r) {
         const float2 s = r0 + r < m ? st[r0 + r] : make_float2(0.0f, 0.0f);
         if (s.y > 0.0f) {
-          sum.x = fmaf(ex2(__uint_as_float(w[r].x) - s.x), s.y, sum.x);
-          sum.y = fmaf(ex2(__uint_as_float(w[r].y) - s.x), s.y, sum.y);
+          const uint32_t x[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum[k] = fmaf(ex2(__uint_as_float(x[k]) - s.x), s.y, sum[k]);
         }
       }
     }
   }
   if (page < 0 || page >= a.c.n_pages || status == RDKV_ERR_TIMEOUT) return;
-  if (t + 1 < held) *reinterpret_cast<float2*>(to) = make_float2(__uint_as_float(had.x) + sum.x, __uint_as_float(had.y) + sum.y);
-  else *to = __uint_as_float(had.x) + sum.x;
+  const uint32_t had[4] = {had0.x, had0.y, had1.x, had1.y};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum[k] += __uint_as_float(had[k]);
+  if (t + 3 < held) {
+    reinterpret_cast<float2*>(to)[0] = make_float2(sum[0], sum[1]), reinterpret_cast<float2*>(to)[1] = make_float2(sum[2], sum[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (t + k < held) to[k] = sum[k];
+  }
 }
 
 // ---------------------------------------------------------------- launch

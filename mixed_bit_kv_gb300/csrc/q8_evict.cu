@@ -123,12 +123,13 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
   if (tid == 0) total_s[0] = total_s[1] = 0, first_s = 0x7fffffffu;
   for (int i = tid; i < 256 * 32; i += kPickThreads) count_s[i] = 0;
   bad = __syncthreads_or(bad);
-  const int filled = ceil_div(a.n_keep, kPage), part_of_all = rank * kPickThreads + tid, all = size * kPickThreads;
+  const int part_of_all = rank * kPickThreads + tid, all = size * kPickThreads;
   if (bad || len <= a.n_keep) {  // (the same in the whole cluster)
     if (bad && part_of_all == 0) raise(a.c, RDKV_ERR_INVALID_ARG);
-    for (int i = part_of_all; i < a.n_keep; i += all) kept[i] = !bad && i < len ? i : -1;
+    for (int64_t i = part_of_all; i < a.n_keep; i += all) kept[i] = !bad && i < len ? (int)i : -1;
     return;
   }
+  const int filled = ceil_div(a.n_keep, kPage);
   for (int p = part_of_all; p < filled; p += all) a.flags[(int64_t)row * stride + p] = 0;
   asm volatile("cp.async.wait_all;" ::: "memory");  // (each thread reads what it asked for)
 #pragma unroll 2
@@ -534,7 +535,7 @@ extern "C" rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, in
   cfg.attrs = attr, cfg.numAttrs = 2;
   RDKV_TRY_CUDA(cudaLaunchKernelEx(&cfg, pick_kernel, a, hold), "8-bit cache eviction");
   count_launch();
-  const int64_t pages = (int64_t)rows * std::min(cache->page_stride, ceil_div(n_keep, kPage));
+  const int64_t pages = (int64_t)rows * std::min<int64_t>(cache->page_stride, ceil_div64(n_keep, kPage));
   const unsigned grid = (unsigned)std::min<int64_t>(pages, (int64_t)num_sms() * kMoveBlocks);
   auto move = cache->head_dim == 128 ? move_kernel<128> : move_kernel<64>;
   RDKV_TRY_CUDA(launch_after(move, dim3(grid), kMoveThreads, 0, cs, a), "8-bit cache eviction");

@@ -545,6 +545,20 @@ def test_eviction_of_many_sequences_and_again_and_again():
     _check_held(c, held)
 
 
+def test_a_budget_as_large_as_the_argument_allows():
+    """(The positions' loop, and the count of pages to fill, passed 2^31.)"""
+    c, held = _filled([130], 1, 64, torch.float16)
+    mass = _weights(c, 1)
+    before = mass.clone()
+    for keep in (2 ** 31 - 1, 2 ** 31 - 64, 131):
+        kept = rdkv.rdkv_q8_evict(c, mass, keep, n_first=keep)
+        assert torch.equal(kept[0, 0, :130].cpu(), torch.arange(130, dtype=torch.int32)) and int(kept[0, 0, 130:].max()) == -1
+        assert int(kept[0, 0, 130:].min()) == -1
+        del kept
+    assert torch.equal(mass, before) and rdkv.rdkv_q8_status(c) == 0
+    _check_held(c, held)
+
+
 def test_other_sequences_of_the_pool_keep_their_pages():
     """Two caches in one pool: what one evicts touches no page of the other, and no page of no one."""
     D, h = 64, 2
