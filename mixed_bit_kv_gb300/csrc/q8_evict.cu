@@ -46,8 +46,10 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+// All blocks of a cluster (of one: the block alone).
+__device__ __forceinline__ void cluster_sync(uint32_t size) {
+  if (size == 1) __syncthreads();
+  else asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // A word of another block's shared memory.
 __device__ __forceinline__ uint32_t remote(const uint32_t* p, uint32_t rank) {
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
       }
       block_s[tid] = n;
     }
-    cluster_sync();
+    cluster_sync(size);
     uint32_t n = 0;
     if (tid < 256) {  // digit 255 - tid: from the largest down
       if (size == 1) {
@@ -185,10 +187,11 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
     if (tid < 256 && lane == 31) sum_s[warp] = in;
     __syncthreads();
     if (tid < 256) {
-      for (int i = 0; i < warp; ++i) in += sum_s[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) in += i < warp ? sum_s[i] : 0;
       if (in >= need && in - n < need) digit_s = 255 - tid, above_s = in - n, within_s = n;
     }
-    cluster_sync();  // (also: every block has read the counts)
+    cluster_sync(size);  // (also: every block has read the counts)
     need -= above_s;
     border |= digit_s << shift;
     mask |= 0xffu << shift;
@@ -222,20 +225,21 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
     atomicAdd(&total_s[0], n_sure), atomicAdd(&total_s[1], n_tie);
     atomicMin(&first_s, first);
   }
-  cluster_sync();
+  cluster_sync(size);
   uint32_t sure0 = 0, tie0 = 0;
   {
     uint32_t c[kMaxBlocks], d[kMaxBlocks], f[kMaxBlocks];
 #pragma unroll
     for (int r = 0; r < kMaxBlocks; ++r) {
       c[r] = r < rank ? remote(&total_s[0], r) : 0, d[r] = r < rank ? remote(&total_s[1], r) : 0;
-      f[r] = r < size ? remote(&first_s, r) : 0x7fffffffu;
+      f[r] = size > 1 && r < size ? remote(&first_s, r) : 0x7fffffffu;
     }
-    first = f[0];
+    first = size > 1 ? f[0] : first_s;
 #pragma unroll
     for (int r = 0; r < kMaxBlocks; ++r) sure0 += c[r], tie0 += d[r], first = min(first, f[r]);
   }
-  for (int i = 0; i < warp; ++i) sure0 += warp_s[i].x, tie0 += warp_s[i].y;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) sure0 += i < warp ? warp_s[i].x : 0, tie0 += i < warp ? warp_s[i].y : 0;
   // (every row of a page before `first` stays where it is; some go, so there is one.  Behind it those of a page may still, where
   // weights are equal to the border.)
   if (rank == 0 && tid == 0) base_s = atomicAdd(a.count, max(0, filled - (int)first));
@@ -272,11 +276,11 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
     at = next, tie0 += __popc(t0) + __popc(t1);
   }
   // ---- the pages to fill
-  cluster_sync();
-  const uint32_t base = remote(&base_s, 0);
+  cluster_sync(size);
+  const uint32_t base = size == 1 ? base_s : remote(&base_s, 0);
   for (int p = max(p0, (int)first) + lane; p < min(p1, filled); p += 32)
     a.todo[base + p - first] = make_int2(fetch(reinterpret_cast<const int32_t*>(waits + p)) == kStay ? kStay : row, p);
-  cluster_sync();  // a block's shared memory outlives the others' reads
+  cluster_sync(size);  // a block's shared memory outlives the others' reads
 }
 
 // The largest magnitude of four codes in a scale f, and top.
