@@ -743,16 +743,16 @@ rdkv_status rdkv_q8_read(const rdkv_q8_cache* cache, int32_t dtype, void* k, voi
  * first use).  Sums are fp32; for 16-bit outputs the weights are rounded to
  * fp16, for fp32 outputs every operand is held in 22 bits or more.
  *
- * mass NULL, or fp32 [batch][h_kv][mass_stride] (mass_stride >= 64 * page_stride):
- * the weight that each held position p has received so far,
+ * mass NULL, or fp32 [batch][h_kv][mass_stride] (8-byte aligned, mass_stride an even
+ * number >= 64 * page_stride): the weight that each held position p has received so far,
  *   mass[b][j][p] += sum over query tokens i that see p and the G heads h of
  *                    KV head j of exp(q_i,h . k^_p / sqrt(head_dim) - lse_i,h),
  * summed in this order for every p, so that equal calls give equal bits.
  * rdkv_score's w_tok of a prompt is the same sum over the prompt's queries: copied in, it is
  * where the decode goes on.  A query head whose lse is not finite (it holds a NaN) adds
- * nothing.  Positions that are not held are not touched: rows that are written
- * over (rejected drafts) start with what mass holds at their positions, so
- * zero it there.  with_mass of the workspace query: 1 for calls with mass (it
+ * nothing, and so does a call that reports RDKV_ERR_TIMEOUT.  Positions that are not
+ * held are not touched: rows that are written over (rejected drafts) start with what mass
+ * holds at their positions, so zero it there.  with_mass of the workspace query: 1 for calls with mass (it
  * then holds the logits too), and such calls add one launch. */
 size_t rdkv_q8_attn_workspace_bytes(const rdkv_q8_cache* cache, int32_t h_q, int32_t n_q, int32_t with_mass);
 rdkv_status rdkv_q8_attn(const rdkv_q8_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,

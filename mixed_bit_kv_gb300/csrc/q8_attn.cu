@@ -28,6 +28,18 @@
 // accumulator (it does not round), so its accumulators start at zero for every page and the pages' sums are fp32 additions.
 //   16-bit outputs  queries as they are (a row times a power of two); weights rounded to fp16: 2^-12 of each.
 //   fp32 outputs    (PREC) queries and weights in two fp16 parts, 22 bits.
+//
+// Bound.  256 bytes a token and KV head at D = 128: 262,144 tokens of 8 heads (537 MB) in 87 us, 91 % of the measured copy
+// bandwidth, fp32 outputs as fast; eight sequences of 16,384 to 32,768 tokens (382 MB) in 65, 87 %.  A page of up to eight rows takes 64
+// products and some 550 instructions; issue slots are 26 % used, the tensor pipe 16 %.  Above the bytes stand some 3 us until
+// the first page is asked for, 4 us of joins, and that SMs do not get equal shares of the bandwidth: at 262,144 tokens 40 of
+// 152 take 9 % longer than the others for as many pages, always the same ones.  A dealing by who comes first would even that
+// out, but then the sums' order, and so their last bits, would change from call to call.  16 rows (four drafted tokens of 4 heads: 51 us, the
+// bytes 29) lose more to that and to changes of unit, 5 us each, because a warp has ten pages in all.
+//   Measured and not kept (us at 262,144 tokens, 16-bit and fp32 outputs; this is 90.8 and 89.5 on that day): warps x half
+// pages 12 x 2 92.4 and 117, 10 x 2 89.7 and 100, 8 x 3 89.7 and 90.6 (batched 68.8 and 70.9, here 67.9 and 68.1), 6 x 4 91.7 and 98.5, 5 x 5
+// 93.5 and 117, 4 x 6 91.1 and 107; the joins in a second launch, by a row a block or a row a group of warps: 104 and 96 against 94; the
+// next unit's queries asked for while the last page is multiplied, into registers (64 x 2,000 tokens: 55.6 against 55.0) or into L1 (55.8).
 #include <atomic>
 
 #include "q8.cuh"
@@ -917,6 +929,9 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
 // mass_t += sum over the query rows that see t of 2^(logit - reference) / sum, chunk after chunk and row after row.
 // A thread four positions of a (sequence, KV head); the loads of eight rows under way together, the first with the rows'
 // statistics, the weights so far and the page table.
+//   Bound: the logits.  With the stores of the launch before it 29 us beside the attention's 87 at 262,144 tokens of 64 heads
+// (67 MB of logits, 17 MB of weights), 7.4 beside 40 for sixteen sequences of 8,192 of 32 heads.  With the logits by key
+// instead of by row, and pages that pushed them out of the L2, 44 and 17; with two keys a thread 30.5 and 9.
 constexpr int kMassThreads = 128, kMassKeys = 4 * kMassThreads;
 constexpr int kMassRows = kMaxQueries * 8;
 __global__ void __launch_bounds__(kMassThreads) mass_kernel(AttnArgs a, float* mass, int64_t mass_stride) {

@@ -80,6 +80,9 @@ __device__ __forceinline__ uint2 weights_of(const float* mass, int p, int lane) 
 }
 
 // A cluster a (sequence, KV head); a warp has a run of the row's pages, a lane two positions of each.
+//   Bound: a chain of passes, each a count, a sum over lanes and blocks and a scan, some 1.2 us (0.5 of them counting at three
+// pages a warp), 3 at sixteen pages a warp, where the issue slots are half used.  8 us for 32 rows of 3,000 tokens, 11 for 128 rows of 4,160, 26 for 8
+// rows of 131,072 (8 blocks each).
 constexpr int kMaxBlocks = 8;  // of a cluster (16, which have to be asked for: of eight such clusters one waits for another, 95 against 85 us)
 constexpr int kSplit = 8;
 constexpr int kHold = 16;      // pages of a warp whose weights shared memory holds; those of longer rows are loaded again
@@ -295,7 +298,9 @@ __device__ __forceinline__ void copy16(void* to, const uint8_t* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 
-// A block takes a page in some 8 us, of which it waits for memory most, so what counts is how much is under way: the rows are
+// Bound: 131,072 tokens of 8 heads down to a quarter, some 47 us: 185 MB read, 62 written, 5.2 TB/s.  Of the values, whose bytes lie
+// by pairs of tokens (q8.cuh), a kept row brings its pair's and, by sectors, its neighbours' along: 2.8 times the rows' bytes.
+//   A block takes a page in some 8 us, of which it waits for memory most, so what counts is how much is under way: the rows are
 // gathered into shared memory (24 KB a page at D = 128, the values' pairs with a half that is not used), eight pages an SM.  With
 // the codes in registers (four pages an SM) 131,072 tokens of 8 heads brought down to a quarter took 75 us to move, now some 45.
 template <int D>
