@@ -750,7 +750,8 @@ rdkv_status rdkv_q8_read(const rdkv_q8_cache* cache, int32_t dtype, void* k, voi
  * summed in this order for every p, so that equal calls give equal bits.
  * rdkv_score's w_tok of a prompt is the same sum over the prompt's queries: copied in, it is
  * where the decode goes on.  A query head whose lse is not finite (it holds a NaN) adds
- * nothing, and so does a call that reports RDKV_ERR_TIMEOUT.  Positions that are not
+ * nothing, and neither does a call that reports RDKV_ERR_TIMEOUT, nor one after it before the
+ * status is read.  Positions that are not
  * held are not touched: rows that are written over (rejected drafts) start with what mass
  * holds at their positions, so zero it there.  with_mass of the workspace query: 1 for calls with mass (it
  * then holds the logits too), and such calls add one launch. */

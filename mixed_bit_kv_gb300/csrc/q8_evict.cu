@@ -260,23 +260,29 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
     bool sure[2], tie[2];
     classes(p, sure, tie);
     const uint32_t below = (1u << lane) - 1u;
-    const uint32_t t0 = __ballot_sync(0xffffffffu, tie[0]), t1 = __ballot_sync(0xffffffffu, tie[1]);
-    const uint32_t mine = tie0 + __popc(t0 & below) + __popc(t1 & below);
-    const bool k0 = sure[0] || (tie[0] && mine < need), k1 = sure[1] || (tie[1] && mine + tie[0] < need);
+    bool k0 = sure[0], k1 = sure[1];
+    if (__any_sync(0xffffffffu, tie[0] || tie[1])) {  // (of equal weights the lower positions)
+      const uint32_t t0 = __ballot_sync(0xffffffffu, tie[0]), t1 = __ballot_sync(0xffffffffu, tie[1]);
+      const uint32_t mine = tie0 + __popc(t0 & below) + __popc(t1 & below);
+      k0 |= tie[0] && mine < need, k1 |= tie[1] && mine + tie[0] < need;
+      tie0 += __popc(t0) + __popc(t1);
+    }
     const uint32_t b0 = __ballot_sync(0xffffffffu, k0), b1 = __ballot_sync(0xffffffffu, k1);
     const uint32_t to = at + __popc(b0 & below) + __popc(b1 & below);
     const int t = p * kPage + 2 * lane, how = __shfl_sync(0xffffffffu, how_lane, (p - p0) % 32) + 2 * lane;
     if (k0) kept[to] = t, from[to] = make_int2(lies, how);
     if (k1) kept[to + k0] = t + 1, from[to + k0] = make_int2(lies, how + 1);
     // a weight that goes and that no row's will take the place of (of the rows that stay the move sees to)
-    if (!k0 && t >= a.n_keep && t < len) mass[t] = 0.0f;
-    if (!k1 && t + 1 >= a.n_keep && t + 1 < len) mass[t + 1] = 0.0f;
+    if ((p + 1) * kPage > a.n_keep) {
+      if (!k0 && t >= a.n_keep && t < len) mass[t] = 0.0f;
+      if (!k1 && t + 1 >= a.n_keep && t + 1 < len) mass[t + 1] = 0.0f;
+    }
     const uint32_t next = at + __popc(b0) + __popc(b1);
     if (lane == 0 && p < filled)
       waits[p] = at == (uint32_t)p * kPage && next == (uint32_t)(p + 1) * kPage
                      ? make_int2(kStay, 0)  // nothing to do where every row stays
                      : make_int2((int)(at / kPage), next > at ? min(p - 1, (int)((next - 1) / kPage)) : -1);
-    at = next, tie0 += __popc(t0) + __popc(t1);
+    at = next;
   }
   // ---- the pages to fill
   cluster_sync(size);

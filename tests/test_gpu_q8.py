@@ -517,6 +517,28 @@ def test_eviction_of_long_rows(n, keep, last, kind):
     _evicted(c, held, _weights(c, 6, kind), keep, 4 if keep > 17 else 0, last)
 
 
+@pytest.mark.parametrize("kind", ["spread", "few", "any"])
+def test_eviction_of_rows_longer_than_shared_memory(kind):
+    """More than 131,072 tokens: a warp's last pages' weights are loaded again for every digit."""
+    D, n, keep = 64, 210_011, 70_001
+    c = rdkv.Q8Cache(1, 1, D, n, DEV)
+    c.lens += n
+    x = torch.randn(2, 1, n, 1, D, generator=torch.Generator().manual_seed(1)).half().to(DEV)
+    rdkv.rdkv_q8_write(c, x[0], x[1])
+    mass = _weights(c, 9, kind)
+    before, rows = mass[0, 0].cpu().numpy(), rdkv.rdkv_q8_read(c, n, dtype=torch.float32)
+    kept = rdkv.rdkv_q8_evict(c, mass, keep, n_first=3, n_last=1000)[0, 0]
+    want = O.q8_evict(before[:n], keep, 3, 1000)
+    assert kept.tolist() == want
+    now = mass[0, 0].cpu().numpy()
+    assert np.array_equal(now[:keep].view(np.int32), before[want].view(np.int32)) and not now[keep:n].any()
+    c.lens.clamp_(max=keep)
+    for a, b in zip(rdkv.rdkv_q8_read(c, keep, dtype=torch.float32), rows):
+        # (values below 2^-6 of a scale, 2^-5 at most here, are rounded once more: half of its 2^-9)
+        assert (a[0] - b[0][kept.long()]).abs().max() <= 2.0 ** -15
+    assert float(c.scales.max()) <= 2.0 ** -5 and rdkv.rdkv_q8_status(c) == 0
+
+
 def test_eviction_moves_rows_between_pages_of_different_scales():
     D, h, n = 128, 2, 64 * 9 + 30
     k, v = _rows(n, h, D, torch.float32, 1), _rows(n, h, D, torch.float32, 2)
@@ -676,9 +698,20 @@ def test_nothing_is_written_outside_workspaces_and_outputs(D, lens, h, G, T):
 def test_one_workspace_serves_calls_of_any_shape_in_turn():
     caches = [_filled([64 * 50, 300], 2, 128, torch.float16), _filled([700], 1, 64, torch.float16)]
     nb = max(rdkv.lib().rdkv_q8_attn_workspace_bytes(ctypes.byref(c.c), 8 * c.h_kv, 4, 1) for c, _ in caches)
+    nb = max(nb, *(rdkv.lib().rdkv_q8_evict_workspace_bytes(ctypes.byref(c.c)) for c, _ in caches))
     ws = torch.zeros(nb, dtype=torch.uint8, device=DEV)
     for turn in range(3):
         for c, held in caches:
+            mass = _weights(c, turn)
+            keep = len(held[0].k) - 150
+            before = mass.cpu().numpy()
+            kept = rdkv.rdkv_q8_evict(c, mass, keep, n_last=7, ws=ws).cpu().numpy()
+            for b, x in enumerate(held):
+                if len(x.k) > keep:
+                    assert all(kept[b, j].tolist() == O.q8_evict(before[b, j, :len(x.k)], keep, 0, 7) for j in range(c.h_kv))
+                    x.evict(kept[b])
+            c.lens.clamp_(max=keep)
+            _check_held(c, held)
             for G, T, out in ((3, 1, torch.float16), (8, 4, torch.float16), (5, 2, torch.float32)):
                 q = _rows(c.batch * T, c.h_kv * G, c.head_dim, torch.float16, turn).view(c.batch, T, -1, c.head_dim)
                 mass = c.new_mass()
@@ -780,6 +813,31 @@ def test_waits_that_run_out_are_reported_and_the_workspace_serves_on(withhold, d
         o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), out_dtype=TYPES[out], ws=ws)
         _check_attention(q, held, o, lse)
     assert rdkv.rdkv_q8_status(c) == 0
+
+
+def test_weights_without_a_log_sum_exp_and_behind_a_wait_that_ran_out():
+    """lse may be NULL; after a wait that ran out nothing is added until the status is read."""
+    c, held = _filled([300, 64], 2, 64, torch.float16)
+    q = _rows(2, 6, 64, torch.float16, 9).view(2, 1, 6, 64).to(DEV)
+    want = c.new_mass()
+    out, _ = rdkv.rdkv_q8_attn(c, q, mass=want)
+    nb = rdkv.lib().rdkv_q8_attn_workspace_bytes(ctypes.byref(c.c), 6, 1, 1)
+    ws, mass, got = torch.zeros(nb, dtype=torch.uint8, device=DEV), c.new_mass(), torch.empty_like(out)
+    s = torch.cuda.current_stream().cuda_stream
+
+    def call():
+        code = rdkv.lib().rdkv_q8_attn(ctypes.byref(c.c), rdkv.RDKV_F16, q.data_ptr(), 6 * 64, 6, 1, mass.data_ptr(), mass.shape[2],
+                                       got.data_ptr(), rdkv.RDKV_F16, None, ws.data_ptr(), nb, s)
+        assert code == rdkv.RDKV_OK
+
+    call()
+    assert torch.equal(got, out) and torch.equal(mass, want)
+    c.status.fill_(rdkv.RDKV_ERR_TIMEOUT)
+    call()
+    assert torch.equal(mass, want)
+    assert rdkv.rdkv_q8_status(c) == rdkv.RDKV_ERR_TIMEOUT
+    call()
+    assert torch.equal(mass, want + want) and rdkv.rdkv_q8_status(c) == 0
 
 
 # ---------------------------------------------------------------- a run of them together
