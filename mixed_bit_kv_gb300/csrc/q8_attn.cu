@@ -36,7 +36,7 @@
 // 152 take 9 % longer than the others for as many pages, always the same ones.  A dealing by who comes first would even that
 // out, but then the sums' order, and so their last bits, would change from call to call.  16 rows (four drafted tokens of 4 heads: 51 us, the
 // bytes 29) lose more to that and to changes of unit, 5 us each, because a warp has ten pages in all.
-//   Measured and not kept (us at 262,144 tokens, 16-bit and fp32 outputs; this is 90.8 and 89.5 on that day): warps x half
+//   Measured and not kept (us at 262,144 tokens, 16-bit and fp32 outputs; against 90.8 and 89.5): warps x half
 // pages 12 x 2 92.4 and 117, 10 x 2 89.7 and 100, 8 x 3 89.7 and 90.6 (batched 68.8 and 70.9, here 67.9 and 68.1), 6 x 4 91.7 and 98.5, 5 x 5
 // 93.5 and 117, 4 x 6 91.1 and 107; the joins in a second launch, by a row a block or a row a group of warps: 104 and 96 against 94; the
 // next unit's queries asked for while the last page is multiplied, into registers (64 x 2,000 tokens: 55.6 against 55.0) or into L1 (55.8).
