@@ -39,7 +39,8 @@
 //   Measured and not kept (us at 262,144 tokens, 16-bit and fp32 outputs; against 90.8 and 89.5): warps x half
 // pages 12 x 2 92.4 and 117, 10 x 2 89.7 and 100, 8 x 3 89.7 and 90.6 (batched 68.8 and 70.9, here 67.9 and 68.1), 6 x 4 91.7 and 98.5, 5 x 5
 // 93.5 and 117, 4 x 6 91.1 and 107; the joins in a second launch, by a row a block or a row a group of warps: 104 and 96 against 94; the
-// next unit's queries asked for while the last page is multiplied, into registers (64 x 2,000 tokens: 55.6 against 55.0) or into L1 (55.8).
+// next unit's queries asked for while the last page is multiplied, into registers (64 x 2,000 tokens: 55.6 against 55.0) or into L1
+// (55.8); items of 32 tokens instead of 64, in copies half as large, 101 against 87, and for 16 rows 51.6 against 51.2.
 #include <atomic>
 
 #include "q8.cuh"
