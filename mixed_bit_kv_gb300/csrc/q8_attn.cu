@@ -29,12 +29,12 @@
 //   16-bit outputs  queries as they are (a row times a power of two); weights rounded to fp16: 2^-12 of each.
 //   fp32 outputs    (PREC) queries and weights in two fp16 parts, 22 bits.
 //
-// Bound.  256 bytes a token and KV head at D = 128: 262,144 tokens of 8 heads (537 MB) in 87 us, 91 % of the measured copy
+// Bound.  256 bytes a token and KV head at D = 128: 262,144 tokens of 8 heads (537 MB) in 86 us, 92 % of the measured copy
 // bandwidth, fp32 outputs as fast; eight sequences of 16,384 to 32,768 tokens (382 MB) in 65, 87 %.  A page of up to eight rows takes 64
 // products and some 550 instructions; issue slots are 26 % used, the tensor pipe 16 %.  Above the bytes stand some 3 us until
 // the first page is asked for, 4 us of joins, and that SMs do not get equal shares of the bandwidth: at 262,144 tokens 40 of
 // 152 take 9 % longer than the others for as many pages, always the same ones.  A dealing by who comes first would even that
-// out, but then the sums' order, and so their last bits, would change from call to call.  16 rows (four drafted tokens of 4 heads: 51 us, the
+// out, but then the sums' order, and so their last bits, would change from call to call.  16 rows (four drafted tokens of 4 heads: 49 us, the
 // bytes 29) lose more to that and to changes of unit, 5 us each, because a warp has ten pages in all.
 //   Measured and not kept (us at 262,144 tokens, 16-bit and fp32 outputs; against 90.8 and 89.5): warps x half
 // pages 12 x 2 92.4 and 117, 10 x 2 89.7 and 100, 8 x 3 89.7 and 90.6 (batched 68.8 and 70.9, here 67.9 and 68.1), 6 x 4 91.7 and 98.5, 5 x 5
@@ -498,12 +498,20 @@ struct Warp {
   }
 };
 
-// Adds a piece (its reference m, sum of weights l and four of its sums y) to those of a row, whose reference is top.  (A piece
+// Eight sums of a row.
+struct Sums {
+  float4 x, y;
+};
+__device__ __forceinline__ Sums no_sums() { return Sums{make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)}; }
+__device__ __forceinline__ void add(float4& o, float f, float4 y) {
+  o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+}
+// Adds a piece (its reference m, sum of weights l and eight of its sums y) to those of a row, whose reference is top.  (A piece
 // without a reference may hold NaN, and keeps it.)
-__device__ __forceinline__ void add_piece(float4& o, float& sum, float top, float m, float l, float4 y) {
+__device__ __forceinline__ void add_piece(Sums& o, float& sum, float top, float m, float l, const Sums& y) {
   const float f = m == -INFINITY ? 0.0f : ex2(m - top);
   sum = fmaf(f, l, sum);
-  o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+  add(o.x, f, y.x), add(o.y, f, y.y);
 }
 
 // What a block knows of a piece it joins.
@@ -822,7 +830,9 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
 
   // ---- joining the block's pieces: runs of pieces of one unit, a run begins at a piece that holds its
   // unit's first item, or at the block's first piece.  (Short loops: the code is fetched once a call, and what unrolling
-  // saves is less than the fetch of more of it.)
+  // saves is less than the fetch of more of it.  A thread takes eight channels of a row, here and below, so that 8 or 16 rows take
+  // one turn: with four channels and two turns 87.9 us where it now takes 86.2 for 262,144 tokens of 8 rows, 51.3 for 48.8 with 16 rows; a
+  // few pages of 4 rows 9.9 for 10.2.)
   const uint32_t valid = valid_s, ends = end_s, begins = start_s;
   const uint32_t starts = begins | (valid & (0u - valid));
   int open0 = -1, open1 = -1;  // pieces of runs that are a part of their unit: one that began before the block, one that goes on
@@ -835,8 +845,8 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     const Unit ru = unit_at(a, piece_s[s].unit);
     float* part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * P::kFloats;
 #pragma unroll 1
-    for (int i = tid; i < ru.rows * (D / 4); i += 32 * NW) {
-      const int row = i / (D / 4), ch = i % (D / 4) * 4;
+    for (int i = tid; i < ru.rows * (D / 8); i += 32 * NW) {
+      const int row = i / (D / 8), ch = i % (D / 8) * 8;
       auto src = [&](uint32_t m) -> const float* {
         const int e = __ffs(m) - 1;
         return reinterpret_cast<const float*>(smem + (e & 1         ? (size_t)(e / 2) * S::kRing
@@ -846,18 +856,19 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
       for (uint32_t x = members; x; x &= x - 1) m = fmaxf(m, src(x)[P::kRows * D + row]);
-      float4 o = make_float4(0, 0, 0, 0);
+      Sums o = no_sums();
 #pragma unroll 2
       for (uint32_t x = members; x; x &= x - 1) {
         const float* y = src(x);
-        add_piece(o, l, m, y[P::kRows * D + row], y[P::kRows * (D + 1) + row], *reinterpret_cast<const float4*>(y + row * D + ch));
+        add_piece(o, l, m, y[P::kRows * D + row], y[P::kRows * (D + 1) + row], *reinterpret_cast<const Sums*>(y + row * D + ch));
       }
       if (whole) {
         const int64_t at = row_at(a, ru, row);
-        put4(a, at * D + ch, scaled(o, l));
+        put4(a, at * D + ch, scaled(o.x, l));
+        put4(a, at * D + ch + 4, scaled(o.y, l));
         if (ch == 0) put_lse(a, at, m, l);
       } else {
-        *reinterpret_cast<float4*>(part + row * D + ch) = o;
+        *reinterpret_cast<Sums*>(part + row * D + ch) = o;
         if (ch == 0) part[P::kRows * D + row] = m, part[P::kRows * (D + 1) + row] = l;
       }
     }
@@ -892,35 +903,37 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     // the unit's first block wrote it as the unit that goes on, the others as the one that began before
     const float* parts = a.parts + (int64_t)first_s[slot] * 2 * P::kFloats;
 #pragma unroll 1
-    for (int i = tid; i < ru.rows * (D / 4); i += 32 * NW) {
-      const int row = i / (D / 4), ch = i % (D / 4) * 4;
+    for (int i = tid; i < ru.rows * (D / 8); i += 32 * NW) {
+      const int row = i / (D / 8), ch = i % (D / 8) * 8;
       constexpr int kAhead = 10;  // parts whose loads are under way together
-      float4 o = make_float4(0, 0, 0, 0);
+      Sums o = no_sums();
       float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
       for (int j0 = 0; j0 < n; j0 += kAhead) {
         float m[kAhead], l[kAhead];
-        float4 y[kAhead];
+        Sums y[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           const float* part = parts + (int64_t)(2 * (j0 + j) + (j0 + j == 0 ? 1 : 0)) * P::kFloats;
           const bool real = j0 + j < n;
           m[j] = real ? __ldcg(part + P::kRows * D + row) : -INFINITY;
           l[j] = real ? __ldcg(part + P::kRows * (D + 1) + row) : 0.0f;
-          y[j] = real ? __ldcg(reinterpret_cast<const float4*>(part + row * D + ch)) : make_float4(0, 0, 0, 0);
+          y[j].x = real ? __ldcg(reinterpret_cast<const float4*>(part + row * D + ch)) : make_float4(0, 0, 0, 0);
+          y[j].y = real ? __ldcg(reinterpret_cast<const float4*>(part + row * D + ch) + 1) : make_float4(0, 0, 0, 0);
         }
         float now = top;
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) now = fmaxf(now, m[j]);
-        const float4 was = o;
+        const Sums was = o;
         const float had = sum, ref = top;
-        o = make_float4(0, 0, 0, 0), sum = 0.0f, top = now;
+        o = no_sums(), sum = 0.0f, top = now;
         add_piece(o, sum, now, ref, had, was);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) add_piece(o, sum, now, m[j], l[j], y[j]);
       }
       const int64_t at = row_at(a, ru, row);
-      put4(a, at * D + ch, scaled(o, sum));
+      put4(a, at * D + ch, scaled(o.x, sum));
+      put4(a, at * D + ch + 4, scaled(o.y, sum));
       if (ch == 0) put_lse(a, at, top, sum);
     }
   }
