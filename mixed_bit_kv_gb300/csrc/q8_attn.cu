@@ -34,7 +34,7 @@
 // products and some 550 instructions; issue slots are 26 % used, the tensor pipe 16 %.  Above the bytes stand some 3 us until
 // the first page is asked for, 4 us of joins, and that SMs do not get equal shares of the bandwidth: at 262,144 tokens 40 of
 // 152 take 9 % longer than the others for as many pages, always the same ones.  A dealing by who comes first would even that
-// out, but then the sums' order, and so their last bits, would change from call to call.  16 rows (four drafted tokens of 4 heads: 49 us, the
+// out, but then the sums' order, and so their last bits, would change from call to call.  16 rows (four drafted tokens of 4 heads: 47 us, the
 // bytes 29) lose more to that and to changes of unit, 5 us each, because a warp has ten pages in all.
 //   Measured and not kept (us at 262,144 tokens, 16-bit and fp32 outputs; against 90.8 and 89.5): warps x half
 // pages 12 x 2 92.4 and 117, 10 x 2 89.7 and 100, 8 x 3 89.7 and 90.6 (batched 68.8 and 70.9, here 67.9 and 68.1), 6 x 4 91.7 and 98.5, 5 x 5
@@ -525,13 +525,15 @@ struct Smem {
   static_assert(Partial<D, NT>::kFloats * 4 <= kRing, "a warp's piece goes into its ring");
   static_assert(2 * NW <= 32, "a lane a piece");
   // A piece of a unit that ends inside a warp's run, while copies into the ring are under way: beside the ring where there is
-  // room; else in global memory, from where the warp fetches it behind its other piece when its copies have ended.
+  // room for every warp's; else for the first kSlots that come, and of the others in global memory, from where a warp fetches
+  // its own behind its other piece when its copies have ended.  (Long units leave a block one or two; with all of them in global
+  // memory four drafted tokens of 16 sequences took 48.6 us, now 46.6.)
   static constexpr int kPiece = Partial<D, NT>::kFloats * 4;
-  static constexpr bool kRoom = NT == 1;
-  static_assert(kRoom || 2 * kPiece <= kRing, "both pieces in the ring");
+  static constexpr int kSlots = NT == 1 ? NW : 3;
+  static_assert(kSlots == NW || 2 * kPiece <= kRing, "both pieces in the ring");
   static constexpr size_t kBars = (size_t)NW * kRing, kInfoAt = kBars + 16 * ((NW * NS + 1) / 2), kScalesAt = kInfoAt + 16 * NW * kInfo,
-                          kHeads = kScalesAt + 8 * NW * kInfo, kBytes = kHeads + (kRoom ? NW * kPiece : 0);
-  static_assert(kBytes <= 231 * 1024, "with the block's own variables at most 227 KB and 1 KB reserved");
+                          kHeads = kScalesAt + 8 * NW * kInfo, kBytes = kHeads + (size_t)kSlots * kPiece;
+  static_assert(kBytes <= 226 * 1024, "with the block's own variables at most 227 KB");
 };
 
 template <int D, int NT, bool PREC, int NW, int NS>
@@ -544,14 +546,14 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   __shared__ Piece piece_s[2 * NW];
   __shared__ uint32_t valid_s, start_s, end_s;
   __shared__ int total_s;
-  __shared__ int last_s[2], first_s[2];
+  __shared__ int last_s[2], first_s[2], at_s[2 * NW], slots_s;  // at_s: where a piece lies; slots_s: slots taken
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, qd = lane % 4, H = a.c.h_kv;
   uint8_t* ring = smem + (size_t)warp * S::kRing;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * NS;
   int4* info = reinterpret_cast<int4*>(smem + S::kInfoAt) + warp * kInfo;
   float2* scales = reinterpret_cast<float2*>(smem + S::kScalesAt) + warp * kInfo;
   const int BC = a.c.batch * a.n_chunks;
-  if (tid == 0) total_s = 0, valid_s = start_s = end_s = 0;
+  if (tid == 0) total_s = 0, slots_s = 0, valid_s = start_s = end_s = 0;
   if (lane < NS) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bars + lane)) : "memory");
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   after_previous();
@@ -676,8 +678,22 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     __syncwarp();
   };
 
-  float* head = S::kRoom ? reinterpret_cast<float*>(smem + S::kHeads + (size_t)warp * S::kPiece) : a.heads + (int64_t)me * P::kFloats;
-  bool headed = false;  // there is such a piece
+  bool away = false;  // this warp's such piece lies in global memory
+  // Where the piece of a unit goes, one that ends inside the run or one that does not.
+  auto piece_at = [&](bool ends) {
+    int at = warp * S::kRing;
+    if (ends) {
+      int slot = warp;
+      if constexpr (S::kSlots < NW) {
+        if (lane == 0) slot = atomicAdd(&slots_s, 1);
+        slot = __shfl_sync(0xffffffffu, slot, 0);
+      }
+      away = slot >= S::kSlots;
+      at = away ? at + S::kPiece : (int)S::kHeads + slot * S::kPiece;
+    }
+    if (lane == 0) at_s[2 * warp + (ends ? 0 : 1)] = at;
+    return ends && away ? a.heads + (int64_t)me * P::kFloats : reinterpret_cast<float*>(smem + at);
+  };
   // Enters the piece of a unit that this warp has written up to item i.
   auto leave_piece = [&](int i, int unit, bool began, bool ends) {
     const int at = 2 * warp + (ends ? 0 : 1), items = items_of(a, unit / H);
@@ -767,8 +783,6 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     next_stage();
     if ((e.w & 2) || i == n_items - 1) {  // the unit, or the run, ends
       const bool ends = e.w & 2;
-      // a unit that ends here without having begun lies first in the run: copies are under way
-      float* dst = ends ? head : reinterpret_cast<float*>(ring);
       if (began && ends) {
         w.finish(
             g, qd,
@@ -779,11 +793,12 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
               if (row < un.rows) put_lse(a, row_at(a, un, row), m, l);
             });
       } else {
+        // a unit that ends here without having begun lies first in the run: copies are under way
+        float* dst = piece_at(ends);
         w.finish(
             g, qd, [&](int row, int ch, float, float4 o) { *reinterpret_cast<float4*>(dst + row * D + ch) = o; },
             [&](int row, float m, float l) { dst[P::kRows * D + row] = m, dst[P::kRows * (D + 1) + row] = l; });
         if (lane == 0) leave_piece(i, e.z, began, ends);
-        headed |= ends;
       }
       in_unit = false;
     }
@@ -812,17 +827,17 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
       if (began && ends) {
         write_nothing<D>(a, unit_at(a, e.z), lane);
       } else {
-        float* dst = ends ? head : reinterpret_cast<float*>(ring);
+        float* dst = piece_at(ends);
         for (int x = lane; x < P::kFloats; x += 32) dst[x] = x / P::kRows == D ? -INFINITY : 0.0f;
         if (lane == 0) leave_piece(i, e.z, began, ends);
-        headed |= ends;
       }
       in_unit = false;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
-  if (!S::kRoom && headed) {
+  if (S::kSlots < NW && away) {
     __syncwarp();
+    const float* head = a.heads + (int64_t)me * P::kFloats;
 #pragma unroll 8
     for (int x = lane; x < P::kFloats / 4; x += 32) reinterpret_cast<float4*>(ring + S::kPiece)[x] = reinterpret_cast<const float4*>(head)[x];
   }
@@ -848,10 +863,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
     for (int i = tid; i < ru.rows * (D / 8); i += 32 * NW) {
       const int row = i / (D / 8), ch = i % (D / 8) * 8;
       auto src = [&](uint32_t m) -> const float* {
-        const int e = __ffs(m) - 1;
-        return reinterpret_cast<const float*>(smem + (e & 1         ? (size_t)(e / 2) * S::kRing
-                                                      : S::kRoom ? S::kHeads + (size_t)(e / 2) * S::kPiece
-                                                                 : (size_t)(e / 2) * S::kRing + S::kPiece));
+        return reinterpret_cast<const float*>(smem + at_s[__ffs(m) - 1]);
       };
       float m = -INFINITY, l = 0.0f;
 #pragma unroll 1

@@ -368,6 +368,23 @@ def test_attention_over_many_blocks(lens, h, G, T, dtype, out):
     assert torch.allclose(mass.sum(-1), torch.tensor([min(T, n) * float(G) for n in lens], device=DEV)[:, None].expand(-1, h), rtol=1e-4)
 
 
+# Units of two to four pages, one to three pages a warp: in every block of eight warps four to six hold the end of a unit that another
+# one began, more than the block's shared memory has places for.
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,batch", [(130, 70), (190, 95), (256, 114)])
+def test_many_short_units_of_sixteen_rows(n, batch, D):
+    lens, h, G, T = [n - b % 3 for b in range(batch)], 8, 4, 4
+    c, held = _filled(lens, h, D, torch.bfloat16)
+    q = _rows(batch * T, h * G, D, torch.bfloat16, 9).view(batch, T, h * G, D)
+    mass = c.new_mass()
+    o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+    _check_attention(q, held, o, lse, mass, torch.zeros_like(mass))
+    for _ in range(3):
+        o2, lse2 = rdkv.rdkv_q8_attn(c, q.to(DEV))
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert rdkv.rdkv_q8_status(c) == 0
+
+
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("T", [1, 4])
 def test_attention_over_values_whose_scales_differ_by_two_to_the_thirtieth(T, dtype):
