@@ -83,7 +83,9 @@ __device__ __forceinline__ uint2 weights_of(const float* mass, int p, int lane) 
 //   Bound: a chain of passes, each a count, a sum over lanes and blocks and a scan, some 1.2 us (0.5 of them counting at three
 // pages a warp), 3 at sixteen pages a warp, where the issue slots are half used.  8 us for 32 rows of 3,000 tokens, 11 for 128 rows of 4,160, 26 for 8
 // rows of 131,072 (8 blocks each).
-constexpr int kMaxBlocks = 8;  // of a cluster (16, which have to be asked for: of eight such clusters one waits for another, 95 against 85 us)
+// of a cluster (16, which have to be asked for: of eight such clusters one waits for another, 95 against 85 us; with two blocks an SM, so
+// that none does, 81.2 against 80.3; eight blocks of 1,024 threads 80.6 against 79.5, and 23.4 against 20.9 for rows of 3,000 tokens)
+constexpr int kMaxBlocks = 8;
 constexpr int kSplit = 8;
 constexpr int kHold = 16;      // pages of a warp whose weights shared memory holds; those of longer rows are loaded again
 // (Short loops: the code is fetched anew by every launch.  With the weights in registers and every loop unrolled, 30 KB of it, the
