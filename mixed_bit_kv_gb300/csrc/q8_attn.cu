@@ -35,12 +35,14 @@
 // the first page is asked for, 4 us of joins, and that SMs do not get equal shares of the bandwidth: at 262,144 tokens 40 of
 // 152 take 9 % longer than the others for as many pages, always the same ones.  A dealing by who comes first would even that
 // out, but then the sums' order, and so their last bits, would change from call to call.  16 rows (four drafted tokens of 4 heads: 47 us, the
-// bytes 29) lose more to that and to changes of unit, 5 us each, because a warp has ten pages in all.
+// bytes 29) lose more to their own instructions, chains of which two warps a scheduler hide little: a page takes a warp 2.9 us, in a
+// sixth of which it waits for bytes (8 rows: 2.4, of which 0.9).  A change of unit costs a warp 1.3 us, with 16 rows some 3.
 //   Measured and not kept (us at 262,144 tokens, 16-bit and fp32 outputs; against 90.8 and 89.5): warps x half
 // pages 12 x 2 92.4 and 117, 10 x 2 89.7 and 100, 8 x 3 89.7 and 90.6 (batched 68.8 and 70.9, here 67.9 and 68.1), 6 x 4 91.7 and 98.5, 5 x 5
 // 93.5 and 117, 4 x 6 91.1 and 107; the joins in a second launch, by a row a block or a row a group of warps: 104 and 96 against 94; the
 // next unit's queries asked for while the last page is multiplied, into registers (64 x 2,000 tokens: 55.6 against 55.0) or into L1
-// (55.8); items of 32 tokens instead of 64, in copies half as large, 101 against 87, and for 16 rows 51.6 against 51.2.
+// (55.8); items of 32 tokens instead of 64, in copies half as large, 101 against 87, and for 16 rows 51.6 against 51.2; the code that begins a unit once instead
+// of twice, its first pages asked for inside: 16 rows 0.9 less, some others 0.4 more.
 #include <atomic>
 
 #include "q8.cuh"
@@ -659,7 +661,6 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   // Copies half x of the run (the keys of item x / 2, or its values) into the stage that it falls in.
   auto issue = [&](int x, int stage) {
     const int i = x / 2;
-    if (i >= known) look_up(kInfo / 2);
     if (lane == 0) {
       const int4 e = info[i % kInfo];
       const uint32_t bar = smem_u32(bars + stage);
@@ -733,6 +734,10 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   if (idle) return;
 #pragma unroll 1
   for (; i < n_items; ++i) {
+    // (once a turn and not where a copy is issued, twice in this loop: less code to fetch, 0.2 us of calls of a few pages)
+    constexpr int kReach = (1 + NS) / 2;  // the items that this turn issues are not further ahead
+    static_assert(kReach + kInfo / 2 < kInfo, "places that are still read");
+    if (known <= i + kReach && known < n_items) look_up(kInfo / 2);
     const int4 e = info[i % kInfo];
     if (!in_unit) {
       typename W::Rows x;
