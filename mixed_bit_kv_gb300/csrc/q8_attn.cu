@@ -35,14 +35,14 @@
 // the first page is asked for, 4 us of joins, and that SMs do not get equal shares of the bandwidth: at 262,144 tokens 40 of
 // 152 take 9 % longer than the others for as many pages, always the same ones.  A dealing by who comes first would even that
 // out, but then the sums' order, and so their last bits, would change from call to call.  16 rows (four drafted tokens of 4 heads: 47 us, the
-// bytes 29) lose more to their own instructions, chains of which two warps a scheduler hide little: a page takes a warp 2.9 us, in a
-// sixth of which it waits for bytes (8 rows: 2.4, of which 0.9).  A change of unit costs a warp 1.3 us, with 16 rows some 3.
+// bytes 29) lose more to their own instructions, chains of which two warps a scheduler hide little: by clocks read in the loop, which
+// slow it, a page takes a warp 3.7 us, of which it waits for bytes 0.7 (8 rows: 2.3, of which 0.9), and a change of unit 3 (1.3).
 //   Measured and not kept (us at 262,144 tokens, 16-bit and fp32 outputs; against 90.8 and 89.5): warps x half
 // pages 12 x 2 92.4 and 117, 10 x 2 89.7 and 100, 8 x 3 89.7 and 90.6 (batched 68.8 and 70.9, here 67.9 and 68.1), 6 x 4 91.7 and 98.5, 5 x 5
 // 93.5 and 117, 4 x 6 91.1 and 107; the joins in a second launch, by a row a block or a row a group of warps: 104 and 96 against 94; the
 // next unit's queries asked for while the last page is multiplied, into registers (64 x 2,000 tokens: 55.6 against 55.0) or into L1
-// (55.8); items of 32 tokens instead of 64, in copies half as large, 101 against 87, and for 16 rows 51.6 against 51.2; the code that begins a unit once instead
-// of twice, its first pages asked for inside: 16 rows 0.9 less, some others 0.4 more.
+// (55.8); items of 32 tokens instead of 64, in copies half as large, 101 against 87, and for 16 rows 51.6 against 51.2; the code that
+// begins a unit once instead of twice, its first pages asked for inside: 16 rows 0.9 less, others up to 0.4 more.
 #include <atomic>
 
 #include "q8.cuh"
@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
 // mass_t += sum over the query rows that see t of 2^(logit - reference) / sum, chunk after chunk and row after row.
 // A thread four positions of a (sequence, KV head); the loads of eight rows under way together, the first with the rows'
 // statistics, the weights so far and the page table.
-//   Bound: the logits.  With the stores of the launch before it 29 us beside the attention's 87 at 262,144 tokens of 64 heads
+//   Bound: the logits.  With the stores of the launch before it 29 us beside the attention's 86 at 262,144 tokens of 64 heads
 // (67 MB of logits, 17 MB of weights), 7.4 beside 40 for sixteen sequences of 8,192 of 32 heads.  With the logits by key
 // instead of by row, and pages that pushed them out of the L2, 44 and 17; with two keys a thread 30.5 and 9.
 constexpr int kMassThreads = 128, kMassKeys = 4 * kMassThreads;
