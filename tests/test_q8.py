@@ -233,3 +233,18 @@ def test_the_tensors_behind_the_struct_change_in_place_only():
         assert getattr(cache, name) is t
     cache.lens += 1
     assert cache.lens.tolist() == [1, 1, 1]
+
+
+# ---------------------------------------------------------------- order between blocks
+def _source(name):
+    import os
+    return open(os.path.join(os.path.dirname(os.path.abspath(rdkv.__file__)), "csrc", name)).read()
+
+
+def test_the_flags_of_the_pages_order_what_they_tell():
+    """A page is overwritten after other blocks have read their rows out of it: the flag that says so is stored with
+    release and polled with acquire at the GPU's scope, else the memory model orders neither side."""
+    import re
+    text = _source("q8_evict.cu")
+    accesses = re.findall(r'asm volatile\("([^;]*);"[^;]*"l"\(flags [^;]*;', text)
+    assert sorted(a.split(" ")[0] for a in accesses) == ["ld.acquire.gpu.global.s32", "st.release.gpu.global.s32"], accesses
