@@ -481,8 +481,10 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictAr
   __syncthreads();
   if (tid == 0) {
     if (!ok) raise(a.c, RDKV_ERR_TIMEOUT);
-    // (nothing but the counters hangs on this count, and a block has used its last ticket before it adds to it)
-    if (atomicAdd(a.count + 2, 1) == (int)gridDim.x - 1) a.count[0] = a.count[1] = a.count[2] = 0;
+    // (acquire and release: the counters are cleared behind what every other block has read of them and added to them)
+    int done;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(done) : "l"(a.count + 2) : "memory");
+    if (done == (int)gridDim.x - 1) a.count[0] = a.count[1] = a.count[2] = 0;
   }
 }
 

@@ -248,3 +248,12 @@ def test_the_flags_of_the_pages_order_what_they_tell():
     text = _source("q8_evict.cu")
     accesses = re.findall(r'asm volatile\("([^;]*);"[^;]*"l"\(flags [^;]*;', text)
     assert sorted(a.split(" ")[0] for a in accesses) == ["ld.acquire.gpu.global.s32", "st.release.gpu.global.s32"], accesses
+
+
+def test_the_last_block_clears_the_counters_behind_the_others():
+    """The block that counts itself last clears counters that the others have read and added to before they counted
+    themselves: that order needs acquire and release on the count."""
+    import re
+    text = _source("q8_evict.cu")
+    assert "atomicAdd(a.count + 2" not in text
+    assert re.findall(r'asm volatile\("([^ ]*) [^;]*;"[^;]*"l"\(a\.count \+ 2\)', text) == ["atom.add.acq_rel.gpu.global.s32"]
