@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int 
   if (bad || len <= a.n_keep) {  // (the same in the whole cluster)
     if (bad && part_of_all == 0) raise(a.c, RDKV_ERR_INVALID_ARG);
     for (int64_t i = part_of_all; i < a.n_keep; i += all) kept[i] = !bad && i < len ? (int)i : -1;
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (the weights of a row that would have been brought down)
     return;
   }
   const int filled = ceil_div(a.n_keep, kPage);

@@ -257,3 +257,14 @@ def test_the_last_block_clears_the_counters_behind_the_others():
     text = _source("q8_evict.cu")
     assert "atomicAdd(a.count + 2" not in text
     assert re.findall(r'asm volatile\("([^ ]*) [^;]*;"[^;]*"l"\(a\.count \+ 2\)', text) == ["atom.add.acq_rel.gpu.global.s32"]
+
+
+def test_the_choice_ends_with_no_copy_under_way():
+    """Every way out of the choice, whose weights arrive by cp.async, passes a wait behind the copies."""
+    import re
+    text = _source("q8_evict.cu")
+    kernel = text[text.index("pick_kernel"):]
+    kernel = kernel[:kernel.index("\n}\n")]
+    first = kernel.index("cp.async.ca")
+    ways_out = [m.start() for m in re.finditer(r"\breturn;", kernel) if m.start() > first]
+    assert ways_out and all("cp.async.wait_all" in kernel[first:at] for at in ways_out)
