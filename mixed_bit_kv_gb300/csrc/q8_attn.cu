@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   int bc = 0, h = 0, p = 0, cnt = 0;  // the next item to look up
   if (BC == 1) {
     cnt = __shfl_sync(0xffffffffu, c0, 0);
-    h = w0 / cnt, p = w0 - h * cnt;
+    if (!idle) h = w0 / cnt, p = w0 - h * cnt;  // (an empty sequence: 0)
   } else {
     int before = 0;
     for (int i0 = 0; i0 < BC && n_items > 0; i0 += 32) {

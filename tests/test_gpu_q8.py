@@ -353,6 +353,26 @@ def test_attention_and_the_weights_of_its_keys(D, h, G, T, lens, dtype, out):
     assert torch.equal(mass, again) and rdkv.rdkv_q8_status(c) == 0
 
 
+@pytest.mark.parametrize("D,h,G,T", [(64, 1, 1, 1), (128, 3, 8, 1), (64, 2, 3, 7), (128, 1, 8, 64)])
+@pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("bf16", "bf16"), ("f32", "f32")])
+def test_one_sequence_that_holds_nothing_or_less_than_the_queries(D, h, G, T, dtype, out):
+    """(An empty one alone has no items to divide its blocks by.)"""
+    for n in (0, 1, T // 2):
+        c, held = _filled([n], h, D, TYPES[dtype], stride=3, grow=3)
+        q = _rows(T, h * G, D, TYPES[dtype], 5).view(1, T, h * G, D)
+        mass = c.new_mass()
+        for _ in range(2):
+            before = mass.clone()
+            o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass, out_dtype=TYPES[out])
+            _check_attention(q, held, o, lse, mass, before)
+        assert not mass[..., n:].any()
+        assert torch.equal(rdkv.rdkv_q8_attn(c, q.to(DEV), out_dtype=TYPES[out])[0], o)
+        kept = rdkv.rdkv_q8_evict(c, mass, 5)
+        assert kept.tolist() == [[list(range(min(n, 5))) + [-1] * (5 - min(n, 5))] * h] or n > 5
+        c.lens.clamp_(max=5)
+        assert rdkv.rdkv_q8_status(c) == 0
+
+
 @pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("f32", "f32")])
 @pytest.mark.parametrize("lens,h,G,T", [([20000], 2, 4, 1), ([64 * 40 + 9] * 40, 2, 3, 1), ([9000, 1, 0, 4000], 1, 8, 4), ([1] * 70, 1, 5, 1)])
 def test_attention_over_many_blocks(lens, h, G, T, dtype, out):
