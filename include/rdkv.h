@@ -787,10 +787,29 @@ rdkv_status rdkv_q8_timeout_selftest(const rdkv_q8_cache* cache, int32_t dtype, 
  * sequence with a page outside the pool (RDKV_ERR_INVALID_ARG in *status) is left as
  * it is, rows and mass, and its kept are -1.  ws as for rdkv_q8_attn, of
  * rdkv_q8_evict_workspace_bytes bytes: calls of both may follow one another on it.
- * Two launches. */
+ * Two launches.
+ *
+ * Rows move in place, so a wait that ran out cannot be taken back: after
+ * RDKV_ERR_TIMEOUT from this call the rows, the scales, the mass and kept of the
+ * sequences that held more than n_keep tokens are undefined, at the old length and
+ * at the new one, and such a sequence has to be written anew.  Sequences of at
+ * most n_keep tokens and pages that hold no token of the others are as they were,
+ * and ws serves the next call.  (The wait is for another block of the same launch,
+ * of some microseconds; its limit is some two seconds.) */
 size_t rdkv_q8_evict_workspace_bytes(const rdkv_q8_cache* cache);
 rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, int64_t mass_stride, int32_t n_keep, int32_t n_first,
                           int32_t n_last, int32_t* kept, void* ws, size_t ws_bytes, void* stream);
+
+/* Failure-detection self-test of rdkv_q8_evict: its kernels on the same
+ * arguments, but a page of a sequence whose index plus KV head is a multiple of
+ * `withhold` (>= 1; 1: all) does not tell that its rows have been read, and a block
+ * that waits for it gives up after `wait_cycles` SM clock cycles (clamped to [1e5,
+ * 4e9]) and reports RDKV_ERR_TIMEOUT, as above: for a cache whose contents are not
+ * needed.  RDKV_ERR_INVALID_ARG for withhold or wait_cycles <= 0, else as
+ * rdkv_q8_evict. */
+rdkv_status rdkv_q8_evict_timeout_selftest(const rdkv_q8_cache* cache, float* mass, int64_t mass_stride, int32_t n_keep,
+                                           int32_t n_first, int32_t n_last, int32_t* kept, void* ws, size_t ws_bytes,
+                                           int32_t withhold, int64_t wait_cycles, void* stream);
 
 /* Reads *status and clears it.  SYNCHRONISES `stream`. */
 rdkv_status rdkv_q8_status(const rdkv_q8_cache* cache, void* stream);

@@ -30,6 +30,8 @@ struct EvictArgs {
   int2* waits;      // [batch * h_kv][page_stride]: the first and last lower page that has rows of a page
   int2* todo;       // [count] the pages to fill, (sequence, head) and page, ascending in a row
   int32_t* count;   // pages to fill, pages taken, blocks done: zero between the calls
+  int withhold;           // 0, or (the self-test) pages with (index + KV head) % withhold == 0 do not raise their flags
+  long long wait_cycles;  // limit of a wait for a flag
 };
 
 constexpr int kStay = -2;  // in a page's place: it stays
@@ -393,7 +395,8 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictAr
     // (release: with the barrier before it the reads of all threads come before the flag.  With relaxed accesses, which leave
     // that order to the hardware, 16 x 4,160 tokens take 39.5 us where they now take 40.9, 131,072 to a quarter 77.4 for 79.0,
     // small ragged rows 19.3 for 16.4)
-    if (tid == 0) asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(flags + p), "r"(1) : "memory");
+    const bool withheld = a.withhold && (p + row % H) % a.withhold == 0;
+    if (tid == 0 && !withheld) asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(flags + p), "r"(1) : "memory");
     float top[2] = {0.0f, 0.0f};
 #pragma unroll 2
     for (int u = tid; u < kChunks; u += kMoveThreads) {
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictAr
       const long long t0 = clock64();
       while (!seen && ok) {
         seen = read(l);
-        ok = seen || clock64() - t0 < kWaitCycles;
+        ok = seen || clock64() - t0 < a.wait_cycles;
       }
       seen = l + kMoveThreads > wait.y || read(l + kMoveThreads);
     }
@@ -515,8 +518,9 @@ extern "C" size_t rdkv_q8_evict_workspace_bytes(const rdkv_q8_cache* cache) {
   return evict_layout(cache).bytes;
 }
 
-extern "C" rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, int64_t mass_stride, int32_t n_keep, int32_t n_first,
-                                     int32_t n_last, int32_t* kept, void* ws, size_t ws_bytes, void* stream) {
+// withhold > 0: the self-test
+static rdkv_status evict_impl(const rdkv_q8_cache* cache, float* mass, int64_t mass_stride, int32_t n_keep, int32_t n_first, int32_t n_last,
+                              int32_t* kept, void* ws, size_t ws_bytes, void* stream, int withhold, long long wait_cycles) {
   rdkv_status st = check_cache(cache);
   if (st != RDKV_OK) return st;
   RDKV_REQUIRE(mass && kept, RDKV_ERR_INVALID_ARG, "NULL mass or kept");
@@ -533,7 +537,7 @@ extern "C" rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, in
   char* w = static_cast<char*>(ws);
   const EvictArgs a{q8::view_of(cache), mass, mass_stride, n_keep, n_first, n_last, kept, reinterpret_cast<int2*>(w + lay.from_at),
                     reinterpret_cast<int32_t*>(w + lay.flags_at), reinterpret_cast<int2*>(w + lay.waits_at), reinterpret_cast<int2*>(w + lay.todo_at),
-                    reinterpret_cast<int32_t*>(w)};
+                    reinterpret_cast<int32_t*>(w), withhold, wait_cycles};
   cudaStream_t cs = (cudaStream_t)stream;
   const int rows = cache->batch * cache->h_kv;
   // blocks of a row: a warp has kSplit pages before the row takes another block
@@ -565,4 +569,18 @@ extern "C" rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, in
   RDKV_TRY_CUDA(launch_after(move, dim3(grid), kMoveThreads, 0, cs, a), "8-bit cache eviction");
   count_launch();
   return RDKV_OK;
+}
+
+extern "C" rdkv_status rdkv_q8_evict(const rdkv_q8_cache* cache, float* mass, int64_t mass_stride, int32_t n_keep, int32_t n_first,
+                                     int32_t n_last, int32_t* kept, void* ws, size_t ws_bytes, void* stream) {
+  return evict_impl(cache, mass, mass_stride, n_keep, n_first, n_last, kept, ws, ws_bytes, stream, 0, kWaitCycles);
+}
+
+extern "C" rdkv_status rdkv_q8_evict_timeout_selftest(const rdkv_q8_cache* cache, float* mass, int64_t mass_stride, int32_t n_keep,
+                                                      int32_t n_first, int32_t n_last, int32_t* kept, void* ws, size_t ws_bytes,
+                                                      int32_t withhold, int64_t wait_cycles, void* stream) {
+  RDKV_REQUIRE(withhold >= 1, RDKV_ERR_INVALID_ARG, "withhold %d must be positive", withhold);
+  RDKV_REQUIRE(wait_cycles > 0, RDKV_ERR_INVALID_ARG, "wait_cycles %lld must be positive", (long long)wait_cycles);
+  return evict_impl(cache, mass, mass_stride, n_keep, n_first, n_last, kept, ws, ws_bytes, stream, withhold,
+                    std::min(kWaitCycles, std::max(kMinWaitCycles, (long long)wait_cycles)));
 }

@@ -36,6 +36,7 @@ EXPORTED = (
     "rdkv_q4_select_workspace_bytes", "rdkv_q4_select", "rdkv_q4_status", "rdkv_q4_timeout_selftest",
     "rdkv_q8_page_bytes", "rdkv_q8_write", "rdkv_q8_read", "rdkv_q8_attn_workspace_bytes", "rdkv_q8_attn",
     "rdkv_q8_evict_workspace_bytes", "rdkv_q8_evict", "rdkv_q8_status", "rdkv_q8_timeout_selftest",
+    "rdkv_q8_evict_timeout_selftest",
 )
 RDKV_CALL_SCORE, RDKV_CALL_ALLOCATE, RDKV_CALL_DECODE = 0, 1, 2
 
@@ -175,6 +176,8 @@ def lib():
             "rdkv_q8_evict_workspace_bytes": (ctypes.c_size_t, [_P]),
             "rdkv_q8_evict": (ctypes.c_int, [_P, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P,
                                              ctypes.c_size_t, _P]),
+            "rdkv_q8_evict_timeout_selftest": (ctypes.c_int, [_P, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                                              _P, _P, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, _P]),
             "rdkv_q8_status": (ctypes.c_int, [_P, _P]),
             "rdkv_q8_timeout_selftest": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P,
                                                         ctypes.c_int32, _P, _P, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, _P]),
@@ -1273,14 +1276,8 @@ def rdkv_q8_timeout_selftest(cache, q, out_dtype=None, withhold=1, wait_cycles=2
     return out, lse
 
 
-def rdkv_q8_evict(cache, mass, n_keep, n_first=0, n_last=0, out=None, ws=None, stream=None):
-    """Brings sequences of more than n_keep tokens down to n_keep, each KV head on its own: the first n_first, the
-    last n_last and the others with the most mass stay, in order, at the front; mass moves with them.
-    Returns the positions they came from: int32 [batch, h_kv, n_keep], ascending, -1 behind the last.  Lower
-    the lengths afterwards: cache.lens.clamp_(max=n_keep)."""
-    if stream is not None or cache._index != _current_device():
-        return _q4_elsewhere(cache, stream, rdkv_q8_evict, mass, n_keep, n_first, n_last, out, ws)
-    s = _raw_stream(cache._index)
+def _q8_eviction(cache, mass, n_keep, n_first, n_last, out, ws, s):
+    """(kept positions, the C arguments from mass to the workspace's size) of an eviction."""
     mass_ptr, mass_stride = _q8_mass(cache, mass)
     if not (1 <= n_keep < 2 ** 31 and 0 <= n_first <= n_keep and 0 <= n_last <= n_keep):  # (32-bit arguments wrap)
         raise RDKVError(RDKV_ERR_INVALID_ARG, f"n_keep {n_keep}, n_first {n_first}, n_last {n_last}")
@@ -1294,8 +1291,33 @@ def rdkv_q8_evict(cache, mass, n_keep, n_first=0, n_last=0, out=None, ws=None, s
         ws = cache.workspace("evict", 0, 0, s)
     else:
         _q4_check_ws(cache, ws)
-    _check(lib().rdkv_q8_evict(cache._ref, mass_ptr, mass_stride, n_keep, n_first, n_last, out.data_ptr(), ws.data_ptr(),
-                               ws.numel(), s))
+    return out, (mass_ptr, mass_stride, n_keep, n_first, n_last, out.data_ptr(), ws.data_ptr(), ws.numel())
+
+
+def rdkv_q8_evict(cache, mass, n_keep, n_first=0, n_last=0, out=None, ws=None, stream=None):
+    """Brings sequences of more than n_keep tokens down to n_keep, each KV head on its own: the first n_first, the
+    last n_last and the others with the most mass stay, in order, at the front; mass moves with them.
+    Returns the positions they came from: int32 [batch, h_kv, n_keep], ascending, -1 behind the last.  Lower
+    the lengths afterwards: cache.lens.clamp_(max=n_keep).  After RDKV_ERR_TIMEOUT (rdkv_q8_status) the sequences
+    that were to be brought down have to be written anew."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q8_evict, mass, n_keep, n_first, n_last, out, ws)
+    s = _raw_stream(cache._index)
+    out, args = _q8_eviction(cache, mass, n_keep, n_first, n_last, out, ws, s)
+    _check(lib().rdkv_q8_evict(cache._ref, *args, s))
+    return out
+
+
+def rdkv_q8_evict_timeout_selftest(cache, mass, n_keep, n_first=0, n_last=0, withhold=1, wait_cycles=2_000_000, out=None, ws=None,
+                                   stream=None):
+    """rdkv_q8_evict with the pages whose index plus KV head is a multiple of `withhold` not telling that their rows have
+    been read: blocks that wait for one give up after wait_cycles SM cycles and rdkv_q8_status reports
+    RDKV_ERR_TIMEOUT.  The sequences that hold more than n_keep tokens are lost."""
+    if stream is not None or cache._index != _current_device():
+        return _q4_elsewhere(cache, stream, rdkv_q8_evict_timeout_selftest, mass, n_keep, n_first, n_last, withhold, wait_cycles, out, ws)
+    s = _raw_stream(cache._index)
+    out, args = _q8_eviction(cache, mass, n_keep, n_first, n_last, out, ws, s)
+    _check(lib().rdkv_q8_evict_timeout_selftest(cache._ref, *args, int(withhold), int(wait_cycles), s))
     return out
 
 

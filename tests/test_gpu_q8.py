@@ -111,6 +111,12 @@ class Held:
         return self.x[1]
 
 
+def _copy(x):
+    y = Held(x.h, x.D)
+    y.x, y.e = list(x.x), list(x.e)
+    return y
+
+
 def _write(c, held, k, v):
     """Rows k, v [n, h, D] a sequence, behind what the sequences hold."""
     n = [len(x) for x in k]
@@ -850,6 +856,57 @@ def test_waits_that_run_out_are_reported_and_the_workspace_serves_on(withhold, d
         o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), out_dtype=TYPES[out], ws=ws)
         _check_attention(q, held, o, lse)
     assert rdkv.rdkv_q8_status(c) == 0
+
+
+@pytest.mark.parametrize("withhold", [1, 3])
+@pytest.mark.parametrize("D,h,n,keep,batch", [(128, 2, 64 * 30, 600, 3), (64, 3, 64 * 200 + 5, 3001, 1), (64, 2, 64 * 20 + 3, 900, 60)])
+def test_evictions_whose_waits_run_out_are_reported_and_the_workspace_serves_on(withhold, D, h, n, keep, batch):
+    """The sequences that were to be brought down are lost, and nothing else is: sequences within the budget, other pages,
+    scales and weights; written anew on the same workspace they are brought down as ever."""
+    import time
+    lens = [n] * batch + [keep, 70, 0]
+    c, held = _filled(lens, h, D, torch.float16)
+    whole = [_rows(n, h, D, torch.float16, 900 + i) for i in range(2)]
+    ws = torch.zeros(rdkv.lib().rdkv_q8_evict_workspace_bytes(ctypes.byref(c.c)), dtype=torch.uint8, device=DEV)
+    own = torch.zeros(c.pages.shape[0], dtype=torch.bool)
+    own[c.page_table[:batch, :-(-n // 64)].long().flatten().cpu()] = True
+    for _ in range(2):
+        mass = _weights(c, 4)
+        m0, pages, scales = mass.clone(), c.pages.clone(), c.scales.clone().view(torch.int32)
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        kept = rdkv.rdkv_q8_evict_timeout_selftest(c, mass, keep, n_first=2, n_last=60, withhold=withhold, wait_cycles=200_000, ws=ws)
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 5
+        assert rdkv.rdkv_q8_status(c) == rdkv.RDKV_ERR_TIMEOUT and rdkv.rdkv_q8_status(c) == 0
+        assert (ws[:rdkv.Q8_COUNTER_BYTES] == 0).all()
+        assert torch.equal(c.pages[~own], pages[~own]) and torch.equal(c.scales.view(torch.int32)[~own], scales[~own])
+        assert torch.equal(mass[batch:], m0[batch:]) and torch.equal(mass[:batch, :, n:], m0[:batch, :, n:])
+        for b in (batch, batch + 1, batch + 2):
+            want = list(range(lens[b])) + [-1] * (keep - lens[b])
+            assert kept[b].tolist() == [want] * h
+        # written anew
+        for b in range(batch):
+            held[b] = Held(h, D)
+            if b == 0:
+                held[0].write(*whole)
+            else:
+                held[b].x, held[b].e = held[0].x, held[0].e
+        rows = [x[None].expand(batch, -1, -1, -1).reshape(-1, h, D).to(DEV) for x in whole]
+        c.lens.copy_(_ints(lens))
+        rdkv.rdkv_q8_write(c, *rows, row_start=_ints([n * i for i in range(batch + 1)] + [n * batch] * 3), max_rows=n)
+        _check_held(c, held)
+    before = mass.copy_(m0).cpu().numpy()
+    kept = rdkv.rdkv_q8_evict(c, mass, keep, n_first=2, n_last=60, ws=ws).cpu().numpy()
+    for b in range(batch):
+        rows = np.array([O.q8_evict(before[b, j, :n], keep, 2, 60) for j in range(h)])
+        assert np.array_equal(kept[b], rows)
+        if b in (0, batch // 2, batch - 1):
+            assert np.array_equal(np.take_along_axis(before[b], rows, 1), mass[b, :, :keep].cpu().numpy())
+        held[b] = _copy(held[b])
+        held[b].evict(rows)
+    c.lens.clamp_(max=keep)
+    _check_held(c, held)
 
 
 def test_weights_without_a_log_sum_exp_and_behind_a_wait_that_ran_out():

@@ -235,6 +235,29 @@ def test_the_tensors_behind_the_struct_change_in_place_only():
     assert cache.lens.tolist() == [1, 1, 1]
 
 
+def _selftest(L, c, **kw):
+    a = dict(mass=4096, mass_stride=256, keep=8, first_n=1, last=1, kept=4096, ws=4096, ws_bytes=1 << 40, withhold=1, cycles=1000)
+    a.update(kw)
+    return L.rdkv_q8_evict_timeout_selftest(ctypes.byref(c), a["mass"], a["mass_stride"], a["keep"], a["first_n"], a["last"], a["kept"],
+                                            a["ws"], a["ws_bytes"], a["withhold"], a["cycles"], None)
+
+
+def test_the_evictions_selftest_refuses_what_the_eviction_does(L):
+    before = L.rdkv_launch_count()
+    for kw, code in BAD_CACHES:
+        assert _selftest(L, _struct(**kw)) == code, kw
+    for kw, code in ((dict(withhold=0), INVALID), (dict(withhold=-1), INVALID), (dict(cycles=0), INVALID), (dict(cycles=-5), INVALID),
+                     (dict(keep=0), INVALID), (dict(first_n=5, last=4), INVALID), (dict(mass=None), INVALID), (dict(kept=4098), INVALID),
+                     (dict(mass_stride=254), INVALID), (dict(ws_bytes=16), WORKSPACE), (dict(ws=None), WORKSPACE)):
+        assert _selftest(L, _struct(), **kw) == code, kw
+    assert L.rdkv_launch_count() == before
+    cache = _cache()
+    cache._index = 0
+    cache.device = torch.device("cuda", 0)
+    with pytest.raises(rdkv.RDKVError, match="cuda:1"):
+        rdkv.rdkv_q8_evict_timeout_selftest(cache, torch.zeros(2, 3, 256), 3, stream=types.SimpleNamespace(device=torch.device("cuda", 1)))
+
+
 # ---------------------------------------------------------------- order between blocks
 def _source(name):
     import os
