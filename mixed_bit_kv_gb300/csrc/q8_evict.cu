@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictAr
   constexpr int kS = L::kSides, kWarps = kMoveThreads / 32, kChunks = kPage * D / 16;  // of 16 bytes, in a page's half
   __shared__ __align__(16) uint8_t keys_s[L::kHalf];
   __shared__ __align__(16) uint8_t values_s[2][L::kHalf];  // the chunks that a pair's first and second token lie in
-  __shared__ int2 from_s[2][kPage];                        // a row's (page, head) and how it lies there; of this page and the next
+  __shared__ int2 from[kPage];                             // a row's (page, head) and how it lies there
   __shared__ uint32_t top_s[2][kWarps], weight_s[kPage];
   __shared__ int2 next_s;
   const int tid = threadIdx.x, H = a.c.h_kv, stride = a.c.page_stride;
@@ -343,10 +343,9 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictAr
   const bool one = total <= (int)gridDim.x;  // a page a block at most
   bool ok = true;
 #pragma unroll 1
-  for (int turn = 0; what.x != kNone; turn ^= 1) {
-    const int2* from = from_s[turn];
+  while (what.x != kNone) {
     const int row = what.x, p = what.y, n = row == kStay ? 0 : min(kPage, a.n_keep - p * kPage);  // rows that come here
-    if (tid < n) from_s[turn][tid] = lies;
+    if (tid < n) from[tid] = lies;  // (behind a barrier since the page before was written)
     __syncthreads();
     if (row == kStay) {
       if (one) break;
@@ -378,8 +377,8 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictAr
     if (tid < n) m = fetch(reinterpret_cast<const uint32_t*>(mass + t));
     const int to = fetch(a.c.page_table + (int64_t)(row / H) * stride + p) * H + row % H;
     const int2 wait = a.waits[(int64_t)row * stride + p];
-    // of the lower pages that have rows of theirs here: have they been read?  (acquire: what this block writes behind it comes after
-    // the reads that the flag tells of)
+    // of the lower pages that have rows of theirs here, two at most (a page's rows go to at most 64 places in a row), a thread each: have
+    // they been read?  (acquire: what this block writes behind it comes after the reads that the flag tells of)
     auto read = [&](int l) {
       int seen;
       asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(flags + l) : "memory");
@@ -392,9 +391,9 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictAr
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();  // every row and weight has been read
-    // (release: with the barrier before it the reads of all threads come before the flag.  With relaxed accesses, which leave
-    // that order to the hardware, 16 x 4,160 tokens take 39.5 us where they now take 40.9, 131,072 to a quarter 77.4 for 79.0,
-    // small ragged rows 19.3 for 16.4)
+    // (release: with the barrier before it the reads of all threads come before the flag.  With relaxed accesses, here and where
+    // blocks that are done are counted, which leave the order to the hardware, 16 x 4,160 tokens take 39.6 us where they now take
+    // 41.1, 131,072 to a quarter 77 for 79, small ragged rows 19.8 for 16.8)
     const bool withheld = a.withhold && (p + row % H) % a.withhold == 0;
     if (tid == 0 && !withheld) asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(flags + p), "r"(1) : "memory");
     float top[2] = {0.0f, 0.0f};
@@ -429,15 +428,12 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictAr
       const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(top[s]));
       if (tid % 32 == 0) top_s[s][tid / 32] = w;
     }
-    for (int l = wait.x + tid; l <= wait.y; l += kMoveThreads) {
+    if (!seen) {
       const long long t0 = clock64();
-      while (!seen && ok) {
-        seen = read(l);
-        ok = seen || clock64() - t0 < a.wait_cycles;
+      while (!(seen = read(wait.x + tid)) && clock64() - t0 < a.wait_cycles) {
       }
-      seen = l + kMoveThreads > wait.y || read(l + kMoveThreads);
     }
-    ok = __syncthreads_and(ok);
+    ok = __syncthreads_and(seen);
     if (!ok) break;
     // The next ticket, not before: a page that is taken and not yet read holds up the pages above it.  (With the ticket taken
     // while this page's rows were on their way 52.5 us where it now takes 40.7 for 16 x 4,160 tokens.)

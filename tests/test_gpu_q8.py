@@ -610,6 +610,52 @@ def test_eviction_of_many_sequences_and_again_and_again():
     _check_held(c, held)
 
 
+def _whole_rows(batch, n, h, D, seed):
+    """Rows fp16 [batch, n, h, D] that every scale a page of them can take holds exactly: codes of three digits, each page's
+    largest 448 2^0 .. 448 2^4, no value below 2^-6 of the largest scale."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = (8 + torch.randint(0, 8, (batch, n, h, D), generator=g, device=DEV)) * torch.randint(0, 6, (batch, n, h, D), generator=g, device=DEV).exp2()
+    x *= torch.randint(0, 2, x.shape, generator=g, device=DEV) * 2 - 1
+    x[..., 5] = 448.0
+    page = torch.arange(n, device=DEV) // 64 * 7 + torch.arange(batch, device=DEV)[:, None]
+    return (x * (page % 5).exp2()[..., None, None]).half()
+
+
+def _check_moved(c, mass, x, n, keep, first, last):
+    """Evicts sequences of n rows x (a pair, as _whole_rows makes them) and compares every position, weight and value."""
+    before = mass.clone()
+    kept = rdkv.rdkv_q8_evict(c, mass, keep, n_first=first, n_last=last)
+    host = before.cpu().numpy()
+    want = torch.tensor([[O.q8_evict(host[b, j, :n], keep, first, last) for j in range(c.h_kv)] for b in range(c.batch)], dtype=torch.int32)
+    assert torch.equal(kept.cpu(), want)
+    c.lens.clamp_(max=keep)
+    at = kept.long()
+    assert torch.equal(mass[..., :keep].view(torch.int32), before.gather(-1, at).view(torch.int32))
+    assert not mass[..., keep:n].any() and torch.equal(mass[..., n:].view(torch.int32), before[..., n:].view(torch.int32))
+    rows = [y.gather(1, at.transpose(1, 2)[..., None].expand(-1, -1, -1, c.head_dim)) for y in x]
+    got = rdkv.rdkv_q8_read(c, keep)
+    assert torch.equal(got[0], rows[0]) and torch.equal(got[1], rows[1])
+    assert rdkv.rdkv_q8_status(c) == 0
+    return rows
+
+
+@pytest.mark.parametrize("kind", ["spread", "few"])
+@pytest.mark.parametrize("D,h,batch", [(128, 2, 60), (64, 3, 50)])
+def test_evictions_of_more_pages_than_run_at_once(D, h, batch, kind):
+    """A block fills one page after another."""
+    n, keep = 64 * 17 + 5, 900
+    c = _cache([n] * batch, h, D)
+    x = [_whole_rows(batch, n, h, D, i) for i in (1, 2)]
+    rdkv.rdkv_q8_write(c, *x)
+    assert all(torch.equal(a, b) for a, b in zip(rdkv.rdkv_q8_read(c, n), x))
+    mass = _weights(c, 11, kind)
+    # of half of the sequences the first eight pages stay as they are: turns that fill nothing
+    mass[::2, :, :512] = 100.0
+    assert batch * h * -(-keep // 64) > 8 * torch.cuda.get_device_properties(DEV).multi_processor_count
+    x = _check_moved(c, mass, x, n, keep, 4, 64)
+    _check_moved(c, mass, x, keep, 511, 0, 100)
+
+
 def test_a_budget_as_large_as_the_argument_allows():
     """(The positions' loop, and the count of pages to fill, passed 2^31.)"""
     c, held = _filled([130], 1, 64, torch.float16)
