@@ -288,6 +288,36 @@ def test_flat_huge_tiny_and_non_finite_rows(dtype):
     assert k.isfinite().all() and (k[0, 192:256] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("D,h,lens", [(128, 8, [32768]), (128, 3, [9001, 64, 5000]), (64, 8, [20011, 1])])
+def test_long_prompts_of_every_type(D, h, lens, dtype):
+    """Whole prompts, against the definition in torch's casts: the smallest scale of each (page, head), the nearest code."""
+    c = _cache(lens, h, D)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rows = []
+    for i in (0, 1):
+        x = torch.randn(sum(lens), h, D, generator=g, device=DEV)
+        x *= (torch.randn(x.shape[:2], generator=g, device=DEV) * 4 - 3).exp2()[..., None]  # rows of many sizes
+        rows.append(x.to(TYPES[dtype]))
+    start = [0] + list(np.cumsum(lens))
+    rdkv.rdkv_q8_write(c, *rows, row_start=_ints(start), max_rows=max(lens))
+    got = rdkv.rdkv_q8_read(c, max(lens), row_start=_ints(start), n_rows=sum(lens), dtype=torch.float32)
+    table = c.page_table.long().cpu()
+    for s in (0, 1):
+        for b, n in enumerate(lens):
+            pages = -(-n // 64)
+            x = torch.zeros(pages * 64, h, D, dtype=torch.float64, device=DEV)
+            x[:n] = rows[s][start[b]:start[b + 1]].double().clamp(-O.Q8_MOST, O.Q8_MOST)  # (some are infinite in fp16)
+            x = x.view(pages, 64, h, D)
+            top = x.abs().amax((1, 3))
+            edges = torch.tensor([448.0 * 2.0 ** e for e in range(-24, 7)], dtype=torch.float64, device=DEV)
+            scale = (torch.searchsorted(edges, top) - 24).double().exp2()
+            assert torch.equal(c.scales[table[b, :pages].to(DEV), :, s].double(), scale)
+            y = (x / scale[:, None, :, None]).float().to(torch.float8_e4m3fn).double() * scale[:, None, :, None]
+            assert int((got[s][start[b]:start[b + 1]].double() != y.view(-1, h, D)[:n]).sum()) == 0
+    assert rdkv.rdkv_q8_status(c) == 0
+
+
 def test_positions_past_two_to_the_thirty_first_bytes():
     """Pages that lie beyond 2^31 (and 2^32) bytes of the pool; weights and logits beyond 2^31 elements."""
     h, D, n = 8, 128, 34000  # 4.5 GB
@@ -654,6 +684,41 @@ def test_evictions_of_more_pages_than_run_at_once(D, h, batch, kind):
     assert batch * h * -(-keep // 64) > 8 * torch.cuda.get_device_properties(DEV).multi_processor_count
     x = _check_moved(c, mass, x, n, keep, 4, 64)
     _check_moved(c, mass, x, keep, 511, 0, 100)
+
+
+@pytest.mark.parametrize("kind", ["spread", "few", "near"])
+def test_evictions_of_rows_whose_warps_look_up_more_pages_than_lanes(kind):
+    """More than 262,144 tokens: a warp of the choice has more than 32 pages, whose places it looks up 32 at a time."""
+    D, n, keep = 64, 300_011, 123_457
+    c = _cache([n], 1, D, seed=7)
+    x = [_whole_rows(1, n, 1, D, i) for i in (3, 4)]
+    rdkv.rdkv_q8_write(c, *x)
+    _check_moved(c, _weights(c, 12, kind), x, n, keep, 3, 1000)
+
+
+@pytest.mark.parametrize("D,h,G", [(128, 2, 4), (64, 1, 5)])
+def test_sequences_much_shorter_than_their_table(D, h, G):
+    """Tables of 131,072 tokens, whose entries behind the sequences may be anything: attended with weights, brought down and
+    attended again as in tables that are as long as the sequences."""
+    lens, stride, keep = [4160, 4096, 70, 4159, 0, 4100], 2048, 4096
+    short, held = _filled(lens, h, D, torch.float16)
+    pages = short.page_table.shape[1]
+    table = torch.full((len(lens), stride), -1 << 31, dtype=torch.int32, device=DEV)
+    table[:, :pages] = short.page_table
+    long = rdkv.Q8Cache(len(lens), h, D, stride * 64, DEV, pages=short.pages.clone(), scales=short.scales.clone(), page_table=table,
+                        lens=short.lens.clone())
+    q = _rows(len(lens) * 2, h * G, D, torch.float16, 5).view(len(lens), 2, h * G, D)
+    results = []
+    for c in (short, long):
+        mass = c.new_mass()
+        got = [*rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass), rdkv.rdkv_q8_evict(c, mass, keep, n_first=4, n_last=512)]
+        c.lens.clamp_(max=keep)
+        got += rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass, out_dtype=torch.float32)
+        assert not mass[..., max(lens):].any() and rdkv.rdkv_q8_status(c) == 0
+        results.append(got + [mass[..., :pages * 64].clone(), c.pages, c.scales.view(torch.int32)])
+    # (the items, and so the order of every sum, come from the lengths)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    _check_attention(q[:1], held[:1], results[0][0][:1], results[0][1][:1])
 
 
 def test_a_budget_as_large_as_the_argument_allows():
