@@ -1,6 +1,5 @@
 // Shared parts of the paged caches (rdkv_q4_* and rdkv_q8_* in include/rdkv.h): which pages and rows a call
-// touches, the rows' types, waits, products of 16-bit operands, joins of pieces of an attention, launches and the
-// host checks that both make.
+// touches, the rows' types, waits, products of 16-bit operands, launches and the host checks that both make.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -128,13 +127,6 @@ struct Eight<float> {
   }
 };
 
-// One value of a type that is named at run time.
-__device__ __forceinline__ float load_q(const void* p, int64_t i, int dtype) {
-  if (dtype == RDKV_F32) return static_cast<const float*>(p)[i];
-  if (dtype == RDKV_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
 // ---------------------------------------------------------------- rows and the pages they fall in
 struct Rows {
   int64_t n, stride;     // rows of k and v, elements between them
@@ -190,19 +182,6 @@ __device__ __forceinline__ Run find_run(const PageView& v, const Rows& r, int b,
 }
 
 // ---------------------------------------------------------------- arithmetic
-// two fp32 products and sums in one instruction
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)), "l"(*reinterpret_cast<const uint64_t*>(&c)));
-  return *reinterpret_cast<const float2*>(&d);
-}
-__device__ __forceinline__ float2 add2f(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
-  return *reinterpret_cast<const float2*>(&d);
-}
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -264,38 +243,7 @@ __device__ __forceinline__ int quotient(int64_t x, int y) {
 // The first of n items that part i of `parts` equal ones takes.
 __device__ __forceinline__ int share(int i, int n, int parts) { return quotient((int64_t)i * n, parts); }
 
-// ---------------------------------------------------------------- joins
-// Joins pieces of one query row: a lane's four channels of the sums and, in every lane, the row's reference
-// and sum.  n pieces, m_of(i), l_of(i) their statistics, y_of(i) this lane's channels: the loads of J
-// pieces are under way together.  Eight of a block's own (drafted tokens: 49.0 us; 51.1 with 16, 56.8 with 32, whose
-// code takes longer to fetch), 16 of other blocks' (32,777 tokens: 18.9 us; 19.3 with eight).
-template <int J, class M, class L, class Y>
-__device__ __forceinline__ void join_row(int n, int lane, M m_of, L l_of, Y y_of, float4& o, float& top, float& sum) {
-  o = make_float4(0, 0, 0, 0);
-  top = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += J) {
-    const bool mine = lane < J && i0 + lane < n;
-    const float m = mine ? m_of(i0 + lane) : -INFINITY, l = mine ? l_of(i0 + lane) : 0.0f;
-    float4 y[J];
-#pragma unroll
-    for (int i = 0; i < J; ++i) y[i] = i0 + i < n ? y_of(i0 + i) : make_float4(0, 0, 0, 0);
-    float now = m;
-    for (int d = J / 2; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
-    now = fmaxf(top, __shfl_sync(0xffffffffu, now, 0));
-    const float back = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
-    top = now;
-    o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
-    float part = f * l;
-    for (int d = J / 2; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-    sum = fmaf(sum, back, __shfl_sync(0xffffffffu, part, 0));
-#pragma unroll
-    for (int i = 0; i < J; ++i) {
-      const float w = __shfl_sync(0xffffffffu, f, i);
-      o.x = fmaf(w, y[i].x, o.x), o.y = fmaf(w, y[i].y, o.y), o.z = fmaf(w, y[i].z, o.z), o.w = fmaf(w, y[i].w, o.w);
-    }
-  }
-}
+// A row's sums by its sum of weights (0: zero).
 __device__ __forceinline__ float4 scaled(float4 o, float l) {
   const float f = l != 0.0f ? 1.0f / l : 0.0f;
   return make_float4(o.x * f, o.y * f, o.z * f, o.w * f);

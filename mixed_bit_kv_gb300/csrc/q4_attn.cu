@@ -680,6 +680,39 @@ struct Smem {
   static constexpr size_t kBytes = kRestAt + 8 * (size_t)NW * kRestLogits;
 };
 
+// ---------------------------------------------------------------- joins
+// Joins pieces of one query row: a lane's four channels of the sums and, in every lane, the row's reference
+// and sum.  n pieces, m_of(i), l_of(i) their statistics, y_of(i) this lane's channels: the loads of J
+// pieces are under way together.  Eight of a block's own (drafted tokens: 49.0 us; 51.1 with 16, 56.8 with 32, whose
+// code takes longer to fetch), 16 of other blocks' (32,777 tokens: 18.9 us; 19.3 with eight).
+template <int J, class M, class L, class Y>
+__device__ __forceinline__ void join_row(int n, int lane, M m_of, L l_of, Y y_of, float4& o, float& top, float& sum) {
+  o = make_float4(0, 0, 0, 0);
+  top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += J) {
+    const bool mine = lane < J && i0 + lane < n;
+    const float m = mine ? m_of(i0 + lane) : -INFINITY, l = mine ? l_of(i0 + lane) : 0.0f;
+    float4 y[J];
+#pragma unroll
+    for (int i = 0; i < J; ++i) y[i] = i0 + i < n ? y_of(i0 + i) : make_float4(0, 0, 0, 0);
+    float now = m;
+    for (int d = J / 2; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+    now = fmaxf(top, __shfl_sync(0xffffffffu, now, 0));
+    const float back = top == -INFINITY ? 0.0f : ex2(top - now), f = m == -INFINITY ? 0.0f : ex2(m - now);
+    top = now;
+    o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
+    float part = f * l;
+    for (int d = J / 2; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+    sum = fmaf(sum, back, __shfl_sync(0xffffffffu, part, 0));
+#pragma unroll
+    for (int i = 0; i < J; ++i) {
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      o.x = fmaf(w, y[i].x, o.x), o.y = fmaf(w, y[i].y, o.y), o.z = fmaf(w, y[i].z, o.z), o.w = fmaf(w, y[i].w, o.w);
+    }
+  }
+}
+
 template <int D, int NT, bool PREC, int NW, int NS>
 __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
   using L = Layout<D>;

@@ -31,6 +31,13 @@ struct SelectArgs {
   int dtype, n_q, G, keep, first, last, tiles, words;
 };
 
+// One value of a type that is named at run time.
+__device__ __forceinline__ float load_q(const void* p, int64_t i, int dtype) {
+  if (dtype == RDKV_F32) return static_cast<const float*>(p)[i];
+  if (dtype == RDKV_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
 constexpr int kTilePages = 16;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 
