@@ -267,6 +267,37 @@ def test_runs_of_any_length_at_any_slot(n, at):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("D,h,most", [(128, 2, 1), (64, 3, 20), (128, 1, 130), (64, 1, 64)])
+def test_rows_out_of_and_into_wider_ones_and_behind_the_last(D, h, most, dtype):
+    """Ragged rows inside wider ones: what lies beside them, between the sequences and behind the last one is neither taken
+    nor written."""
+    new = [most, 0, (most + 1) // 2, 1]
+    old = [63, 5, 0, 100]
+    c = _cache(old, h, D, stride=5, grow=5)
+    held = [Held(h, D) for _ in old]
+    _write(c, held, [_rows(n, h, D, TYPES[dtype], i) for i, n in enumerate(old)], [_rows(n, h, D, TYPES[dtype], 10 + i) for i, n in enumerate(old)])
+    rows = sum(new) + 9
+    wide = torch.full((rows, 2 * h + 1, D), float("nan"), dtype=TYPES[dtype])
+    start = [0] + list(np.cumsum(new))
+    for b, n in enumerate(new):
+        wide[start[b]:start[b + 1], :2 * h] = _rows(n, 2 * h, D, TYPES[dtype], 20 + b)
+        held[b].write(wide[start[b]:start[b + 1], :h], wide[start[b]:start[b + 1], h:2 * h])
+    c.lens.copy_(_ints([a + b for a, b in zip(old, new)]))
+    x = wide.to(DEV)
+    rdkv.rdkv_q8_write(c, x[:, :h], x[:, h:2 * h], row_start=_ints(start), max_rows=most)
+    _check_held(c, held)
+    back = torch.full_like(x, 7.0)
+    rdkv.rdkv_q8_read(c, most, row_start=_ints(start), first=_ints(old), out=(back[:, :h], back[:, h:2 * h]))
+    got = back.cpu()
+    assert (got[:, 2 * h:] == 7).all() and (got[start[-1]:] == 7).all()
+    for b, n in enumerate(new):
+        for s in (0, 1):
+            want = torch.from_numpy(held[b].x[s][old[b]:]).to(TYPES[dtype])
+            assert torch.equal(got[start[b]:start[b + 1], s * h:(s + 1) * h], want)
+    assert rdkv.rdkv_q8_status(c) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 def test_flat_huge_tiny_and_non_finite_rows(dtype):
     D, dt = 64, TYPES[dtype]
     x = _rows(64 * 8, 1, D, torch.float32, 1)
@@ -1082,6 +1113,31 @@ def test_a_prompt_scored_evicted_and_decoded_at_a_budget():
     mo, ml = O.merge_attention(outs.cpu().numpy(), lses.cpu().numpy())
     assert np.abs(both.cpu().numpy() - mo).max() <= 2e-3 and np.abs(lse2.cpu().numpy() - ml).max() <= 2e-3
     assert rdkv.rdkv_q8_status(c) == 0
+
+
+def test_a_prompt_in_a_long_table_goes_on_in_a_short_one():
+    """A second cache on the same pages and scales, with a table for the budget and what is written before the next
+    eviction; the weights stay where they are."""
+    h, G, D, n, budget = 2, 3, 64, 64 * 60 + 11, 64 * 6
+    long, held = _filled([n, 300], h, D, torch.float16)
+    mass = _weights(long, 4)
+    _evicted(long, held, mass, budget, 4, 50)
+    pages = budget // 64 + 1
+    c = rdkv.Q8Cache(2, h, D, pages * 64, DEV, pages=long.pages, scales=long.scales,
+                     page_table=long.page_table[:, :pages].contiguous(), lens=long.lens)
+    spare = sorted(set(range(c.pages.shape[0])) - set(c.page_table.flatten().tolist()))
+    c.page_table[1, -(-300 // 64):] = _ints(spare[:pages - -(-300 // 64)])
+    for step in range(70):
+        k, v = ([_rows(1, h, D, torch.float16, 1000 * i + 2 * step + b) for b in (0, 1)] for i in (1, 2))
+        _write(c, held, k, v)
+        q = _rows(2, h * G, D, torch.float16, 5000 + step).view(2, 1, h * G, D)
+        before = mass.clone()
+        out, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+        if step % 20 == 0:
+            _check_attention(q, held, out, lse, mass, before)
+        if len(held[0].k) == budget + 64:
+            _evicted(c, held, mass, budget, 4, 50)
+    assert rdkv.rdkv_q8_status(c) == rdkv.rdkv_q8_status(long) == 0
 
 
 @pytest.mark.parametrize("exponent", [20, 30, 60])
