@@ -753,8 +753,11 @@ rdkv_status rdkv_q8_read(const rdkv_q8_cache* cache, int32_t dtype, void* k, voi
  * nothing, and neither does a call that reports RDKV_ERR_TIMEOUT, nor one after it before the
  * status is read.  Positions that are not
  * held are not touched: rows that are written over (rejected drafts) start with what mass
- * holds at their positions, so zero it there.  with_mass of the workspace query: 1 for calls with mass (it
- * then holds the logits too), and such calls add one launch. */
+ * holds at their positions, so zero it there.  What a query token gave the positions before it stays
+ * when that token is rejected: mass keeps no account by query, so a caller who does not want it there
+ * copies mass before a call of drafts.  with_mass of the workspace query: 1 for calls with mass (it
+ * then holds the logits too, 4 bytes for every query row and position that the page TABLE has room
+ * for: some 256 * batch * n_q * h_q * page_stride), and such calls add one launch, which also grows with the table. */
 size_t rdkv_q8_attn_workspace_bytes(const rdkv_q8_cache* cache, int32_t h_q, int32_t n_q, int32_t with_mass);
 rdkv_status rdkv_q8_attn(const rdkv_q8_cache* cache, int32_t dtype, const void* q, int64_t q_stride, int32_t h_q,
                          int32_t n_q, float* mass, int64_t mass_stride, void* out, int32_t out_dtype, float* lse,

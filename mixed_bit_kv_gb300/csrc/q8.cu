@@ -150,7 +150,8 @@ constexpr int kWriteBlocks = 4;  // of 256 threads an SM, 16-bit rows
 // in it too (one append in some dozens).
 //   Bound: 34 us for 32,768 rows of 8 heads at D = 128 in fp16 (134 MB read, 67 MB written: 5.9 TB/s, 87 % of the measured copy);
 // 2.8 us for one row of 32 sequences.  With rows widened to fp32, a test for NaN of every code and two blocks an SM 45 us: the
-// ALU was half used and the registers held too little under way.
+// ALU was half used and the registers held too little under way.  The other types still are widened: 35.6 us in bf16 (the same bytes; 76
+// bytes a thread are spilled at four blocks an SM), 53.7 in fp32 (336 MB: 6.2 TB/s, two blocks an SM).
 template <typename T, int D, int kThreads, int kKeys, int kValues>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (sizeof(T) == 2 ? kWriteBlocks : 2) : 1) write_kernel(View v, Rows r, const T* k, const T* vv) {
   using L = Layout<D>;
@@ -268,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? (sizeof(T) == 2 ? 
   }
 }
 
-// The same units the other way.  Bound: HBM, 32 us for those rows back in fp16 (6.3 TB/s, 92 % of the measured copy).
+// The same units the other way.  Bound: HBM, 32 us for those rows back in fp16 or bf16 (6.3 TB/s, 92 % of the measured copy), 67.5 in fp32
+// (336 MB: 5.0 TB/s; the reason was not looked for).
 template <typename T, int D, int kThreads, int kKeys, int kValues>
 __global__ void __launch_bounds__(kThreads) read_kernel(View v, Rows r, T* k, T* vv) {
   using L = Layout<D>;

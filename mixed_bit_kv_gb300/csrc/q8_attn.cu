@@ -30,13 +30,17 @@
 //   fp32 outputs    (PREC) queries and weights in two fp16 parts, 22 bits.
 //
 // Bound.  256 bytes a token and KV head at D = 128: 262,144 tokens of 8 heads (537 MB) in 86 us, 92 % of the measured copy
-// bandwidth, fp32 outputs as fast; eight sequences of 16,384 to 32,768 tokens (382 MB) in 65, 87 %.  A page of up to eight rows takes 64
-// products and some 550 instructions; issue slots are 26 % used, the tensor pipe 16 %.  Above the bytes stand some 3 us until
+// bandwidth, fp32 outputs as fast; eight sequences of 16,384 to 32,768 tokens (382 MB) in 65, 86 %.  A page of up to eight rows takes 64
+// products and some 550 instructions; issue slots are 26 % used, the tensor pipe 14 %.  Above the bytes stand some 3 us until
 // the first page is asked for, 4 us of joins, and that SMs do not get equal shares of the bandwidth: at 262,144 tokens 40 of
 // 152 take 9 % longer than the others for as many pages, always the same ones.  A dealing by who comes first would even that
 // out, but then the sums' order, and so their last bits, would change from call to call.  16 rows (four drafted tokens of 4 heads: 47 us, the
 // bytes 29) lose more to their own instructions, chains of which two warps a scheduler hide little: by clocks read in the loop, which
 // slow it, a page takes a warp 3.7 us, of which it waits for bytes 0.7 (8 rows: 2.3, of which 0.9), and a change of unit 3 (1.3).
+// A warp's 16 rows by 128 channels of sums fill the 255 registers (56 bytes spilled at D = 128), so eight warps fit; a page shared by two
+// warps, half of the channels each, has not been built.  More query tokens than fit in 16 rows (fp32 outputs: 8) read the cache once for
+// every such chunk: 16 x up to 8,191 tokens of 4 heads a group take 68 us for 8 query tokens, 122 for 16 and 429 for 64 (fp32 outputs 126, 240
+// and 910; the bytes 30, the operations 7, 14 and 55).
 //   Measured and not kept (us at 262,144 tokens, 16-bit and fp32 outputs; against 90.8 and 89.5): warps x half
 // pages 12 x 2 92.4 and 117, 10 x 2 89.7 and 100, 8 x 3 89.7 and 90.6 (batched 68.8 and 70.9, here 67.9 and 68.1), 6 x 4 91.7 and 98.5, 5 x 5
 // 93.5 and 117, 4 x 6 91.1 and 107; the joins in a second launch, by a row a block or a row a group of warps: 104 and 96 against 94; the
@@ -961,7 +965,9 @@ __global__ void __launch_bounds__(32 * NW, 1) attn_kernel(AttnArgs a) {
 // A thread four positions of a (sequence, KV head); the loads of eight rows under way together, the first with the rows'
 // statistics, the weights so far and the page table.
 //   Bound: the logits.  With the stores of the launch before it 29 us beside the attention's 86 at 262,144 tokens of 64 heads
-// (67 MB of logits, 17 MB of weights), 7.4 beside 40 for sixteen sequences of 8,192 of 32 heads.  With the logits by key
+// (67 MB of logits, 17 MB of weights), 7.4 beside 40 for sixteen sequences of 8,192 of 32 heads.  The grid is the table's: blocks behind
+// a sequence's end fetch its length and return (16 x 4,160 tokens: 4.6 beside 31 in their own
+// tables, 34 in tables of 131,072).  With the logits by key
 // instead of by row, and pages that pushed them out of the L2, 44 and 17; with two keys a thread 30.5 and 9.
 constexpr int kMassThreads = 128, kMassKeys = 4 * kMassThreads;
 constexpr int kMassRows = kMaxQueries * 8;

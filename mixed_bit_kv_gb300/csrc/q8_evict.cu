@@ -37,6 +37,13 @@ struct EvictArgs {
 constexpr int kStay = -2;  // in a page's place: it stays
 constexpr int kPickThreads = 512;
 constexpr int kMoveThreads = 128, kMoveBlocks = 8;  // an SM
+// Blocks of a row's cluster at most.  (131,072 tokens of 8 heads to a quarter, in a build that took 85 us: with 16, which have to be asked
+// for, 95, as of eight such clusters one waits for another.  In one that took 80: with 16 and two blocks an SM, so that none waits, 1 more;
+// with eight blocks of 1,024 threads 1 more, and rows of 3,000 tokens 2.5 more.)
+constexpr int kMaxBlocks = 8;
+// Pages of the table a warp has before the row takes twice as many blocks: rows that a cluster shares pay for its barriers, some 0.5 us a pass.
+constexpr int kSplit = 8;
+constexpr int kHold = 16;  // pages of a warp whose weights shared memory holds; those of longer rows are loaded again
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -84,12 +91,8 @@ __device__ __forceinline__ uint2 weights_of(const float* mass, int p, int lane) 
 // A cluster a (sequence, KV head); a warp has a run of the row's pages, a lane two positions of each.
 //   Bound: a chain of passes, each a count, a sum over lanes and blocks and a scan, some 1.2 us (0.5 of them counting at three
 // pages a warp), 3 at sixteen pages a warp, where the issue slots are half used.  8 us for 32 rows of 3,000 tokens, 11 for 128 rows of 4,160, 26 for 8
-// rows of 131,072 (8 blocks each).
-// of a cluster (16, which have to be asked for: of eight such clusters one waits for another, 95 against 85 us; with two blocks an SM, so
-// that none does, 81.2 against 80.3; eight blocks of 1,024 threads 80.6 against 79.5, and 23.4 against 20.9 for rows of 3,000 tokens)
-constexpr int kMaxBlocks = 8;
-constexpr int kSplit = 8;
-constexpr int kHold = 16;      // pages of a warp whose weights shared memory holds; those of longer rows are loaded again
+// rows of 131,072 (8 blocks each).  Blocks and shared memory are those of the table: where sequences are much shorter than it the
+// rows pay for clusters that they do not need (16 x 4,160 tokens, all pages moving, in tables of 131,072: 149 us, in their own 75).
 // (Short loops: the code is fetched anew by every launch.  With the weights in registers and every loop unrolled, 30 KB of it, the
 // choice took 16 us for 32 rows of 3,000 tokens under the profiler.)
 __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(EvictArgs a, int hold) {
@@ -309,11 +312,12 @@ __device__ __forceinline__ void copy16(void* to, const uint8_t* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 
-// Bound: 131,072 tokens of 8 heads down to a quarter, some 47 us: 185 MB read, 62 written, 5.2 TB/s.  Of the values, whose bytes lie
-// by pairs of tokens (q8.cuh), a kept row brings its pair's and, by sectors, its neighbours' along: 2.8 times the rows' bytes.
+// Bound: 131,072 tokens of 8 heads down to a quarter, some 49 us: 185 MB read, 62 written, 5.0 TB/s.  The four pairs of a run of eight
+// tokens alternate every 16 bytes of the values (q8.cuh), so a kept row brings its pair's and, by sectors, the run's other pairs' along:
+// 2.8 times the rows' bytes.
 //   A block takes a page in some 8 us, of which it waits for memory most, so what counts is how much is under way: the rows are
 // gathered into shared memory (24 KB a page at D = 128, the values' pairs with a half that is not used), eight pages an SM.  With
-// the codes in registers (four pages an SM) 131,072 tokens of 8 heads brought down to a quarter took 75 us to move, now some 45.
+// the codes in registers (four pages an SM) 131,072 tokens of 8 heads brought down to a quarter took 75 us to move, now some 49.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) move_kernel(EvictArgs a) {
   using L = Layout<D>;

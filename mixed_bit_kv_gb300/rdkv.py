@@ -1242,7 +1242,7 @@ def rdkv_q8_attn(cache, q, mass=None, out=None, lse=None, out_dtype=None, ws=Non
     """Attention of the newest tokens' queries q [batch, n_q, h_q, D] (or [batch, h_q, D]) over the cache:
     (out in q's shape and out_dtype, lse fp32 without D).  out_dtype: q's type (default) or torch.float32.  mass
     (cache.new_mass()): takes the weight that each held position received, summed over the queries
-    that see it and the heads of its group."""
+    that see it and the heads of its group (those of drafts that are rejected later too)."""
     if stream is not None or cache._index != _current_device():
         return _q4_elsewhere(cache, stream, rdkv_q8_attn, q, mass, out, lse, out_dtype, ws)
     s = _raw_stream(cache._index)
