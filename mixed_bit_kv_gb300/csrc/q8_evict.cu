@@ -41,7 +41,9 @@ constexpr int kMoveThreads = 128, kMoveBlocks = 8;  // an SM
 // for, 95, as of eight such clusters one waits for another.  In one that took 80: with 16 and two blocks an SM, so that none waits, 1 more;
 // with eight blocks of 1,024 threads 1 more, and rows of 3,000 tokens 2.5 more.)
 constexpr int kMaxBlocks = 8;
-// Pages of the table a warp has before the row takes twice as many blocks: rows that a cluster shares pay for its barriers, some 0.5 us a pass.
+// Pages of the table a warp has before the row takes twice as many blocks.  A middle between few rows, which more blocks serve sooner, and
+// many, which fill the SMs by themselves (16,384 tokens, hardly a row moved: with 4, 8 and 16 pages a warp 8 rows take 15.0, 17.4 and
+// 20.4 us, 128 rows 48.2, 31.3 and 20.6).
 constexpr int kSplit = 8;
 constexpr int kHold = 16;  // pages of a warp whose weights shared memory holds; those of longer rows are loaded again
 
