@@ -514,6 +514,19 @@ def test_queries_from_the_smallest_to_large_numbers(exponent):
         _check_attention(q, held, o, lse)
 
 
+@pytest.mark.parametrize("T", [1, 4])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_queries_next_to_the_largest_numbers(dtype, T):
+    """Rows up to 2^127.4 over keys whose scales are the smallest: every logit is finite, and so is every result."""
+    c, held = _filled([130], 1, 128, TYPES[dtype], mag=2.0 ** -18)
+    q = _rows(T, 3, 128, torch.float32, 9)
+    q = (q / q.abs().max() * 1.3 * 2.0 ** 127).to(TYPES[dtype]).view(1, T, 3, 128)
+    mass = c.new_mass()
+    o, lse = rdkv.rdkv_q8_attn(c, q.to(DEV), mass=mass)
+    assert o.isfinite().all() and lse.isfinite().all() and mass.isfinite().all()
+    _check_attention(q, held, o, lse, mass, torch.zeros_like(mass))
+
+
 def test_a_nan_query_is_nan_alone_and_adds_no_weight():
     D, h, G, T = 64, 2, 3, 2
     c, held = _filled([200, 70], h, D, torch.float16)
